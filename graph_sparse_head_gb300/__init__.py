@@ -11,16 +11,22 @@ query token attends only to the key tokens along the live edges
 (source_index[e], target_index[e]); scores q_t . k_s / sqrt(d) are
 softmaxed over the edges into each target, weight the values, and the heads'
 mixes go through out_proj.
+
+Around it stands the rest of an encoder and of its training step: the norm of
+the residual sum (pmha_rms_norm), the gated feed-forward block (pmha_ffn_*),
+their gradients, clipping by the global norm (pmha_clip_grad_norm), and
+PackedEncoderLayer, which runs them together with the layer.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 
 import torch
 
 from . import _lib
-from ._lib import (PMHA_BF16, PMHA_F32, PMHA_WEIGHTS_AVG, PMHA_WEIGHTS_NONE, PMHA_WEIGHTS_PER_HEAD,
+from ._lib import (PMHA_ACT_GELU, PMHA_ACT_SILU, PMHA_BF16, PMHA_F32, PMHA_WEIGHTS_AVG, PMHA_WEIGHTS_NONE, PMHA_WEIGHTS_PER_HEAD,
                    PmhaError)
 
 __all__ = [
@@ -31,10 +37,16 @@ __all__ = [
     "pmha_device_status", "pmha_profile_enable", "pmha_profile_read", "pmha_launch_count",
     "pmha_backward", "pmha_backward_workspace_size", "pmha_graph_export_by_source",
     "WMODES",
+    "FfnParams", "FfnQuantizedParams", "PackedEncoderLayer", "quantize_rows",
+    "pmha_rms_norm", "pmha_rms_norm_quantized", "pmha_rms_norm_backward",
+    "pmha_ffn_forward", "pmha_ffn_forward_quantized", "pmha_ffn_backward",
+    "pmha_ffn_forward_workspace_size", "pmha_ffn_forward_quantized_workspace_size",
+    "pmha_ffn_backward_workspace_size", "pmha_clip_grad_norm",
 ]
 
 WMODES = {"none": PMHA_WEIGHTS_NONE, "avg": PMHA_WEIGHTS_AVG, "per_head": PMHA_WEIGHTS_PER_HEAD}
 _DTYPES = {torch.float32: PMHA_F32, torch.bfloat16: PMHA_BF16}
+ACTS = {"silu": PMHA_ACT_SILU, "gelu": PMHA_ACT_GELU}
 
 
 def _stream_ptr(stream) -> int:
@@ -472,3 +484,395 @@ class PackedMultiheadAttention:
             self._ws = torch.empty(need, dtype=torch.uint8, device=query.device)
         return pmha_forward(self.graph, self.params, query, key, value, wmode, workspace=self._ws,
                             key_padding_mask=key_padding_mask)
+
+
+# ---------------------------------------------------------------- the encoder around the layer
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Runs a call on `stream` of `device`: what is allocated inside belongs to
+    that stream, so that its memory is not handed out again before the stream
+    has passed the call."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the call runs on {device}")
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _check_rows(name, x, dtype=None):
+    """A contiguous CUDA tensor (..., width); returns (rows, width)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1 or not x.is_contiguous() \
+            or (x.dtype not in _DTYPES if dtype is None else x.dtype != dtype):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor (..., width) of "
+                         f"{'float32 or bfloat16' if dtype is None else dtype}")
+    width = x.shape[-1]
+    return (x.numel() // width if width else 0), width
+
+
+def _check_like(name, t, like):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype != like.dtype or t.device != like.device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(like.shape)} tensor of {like.dtype} on {like.device}")
+    return t.data_ptr()
+
+
+def _check_vector(name, t, n, dtype, device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n or t.dtype != dtype \
+            or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous ({n},) tensor of {dtype} on {device}")
+    return t.data_ptr()
+
+
+def pmha_rms_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, residual: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm over the last axis of s = x + residual:
+    s / sqrt(mean(s^2) + eps) * weight. Returns (out, s), s rounded to x's type
+    as the norm takes it, or (out, None) without a residual."""
+    rows, width = _check_rows("x", x)
+    w = _check_vector("weight", weight, width, x.dtype, x.device)
+    r = _check_like("residual", residual, x)
+    _check_like("out", out, x)
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        s = None if residual is None else torch.empty_like(x)
+        st = _lib.load().pmha_rms_norm(_DTYPES[x.dtype], rows, width, x.data_ptr(), r, w, eps, _ptr(s), out.data_ptr(),
+                                       None, None, _stream_ptr(stream))
+    _lib.check(st, "pmha_rms_norm")
+    return out, s
+
+
+def pmha_rms_norm_quantized(x: torch.Tensor, weight: torch.Tensor | None, eps: float,
+                            residual: torch.Tensor | None = None, stream=None):
+    """pmha_rms_norm with its output in 8 bits: (q, scale, s) with q in
+    float8_e4m3fn, scale (...,) float32, norm ~ q * scale[..., None]; every q is
+    the formula's value rounded once. What pmha_ffn_forward_quantized takes."""
+    rows, width = _check_rows("x", x)
+    w = _check_vector("weight", weight, width, x.dtype, x.device)
+    r = _check_like("residual", residual, x)
+    with _on(x.device, stream):
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        s = None if residual is None else torch.empty_like(x)
+        st = _lib.load().pmha_rms_norm(_DTYPES[x.dtype], rows, width, x.data_ptr(), r, w, eps, _ptr(s), None,
+                                       q.data_ptr(), scale.data_ptr(), _stream_ptr(stream))
+    _lib.check(st, "pmha_rms_norm")
+    return q, scale, s
+
+
+def pmha_rms_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, eps: float, dout: torch.Tensor,
+                           dsum: torch.Tensor | None = None, input_grad: bool = True, param_grad: bool = True,
+                           stream=None) -> dict:
+    """Gradients of the norm of x (with a residual: of the sum that pmha_rms_norm
+    returned): {"dx", "dweight"}; dx, in x's type, is the gradient of both
+    summands and includes dsum, the sum's gradient from its other uses; dweight
+    is float32 (None without a weight)."""
+    rows, width = _check_rows("x", x)
+    w = _check_vector("weight", weight, width, x.dtype, x.device)
+    dy = _check_like("dout", dout, x)
+    if dout is None:
+        raise ValueError("dout is missing")
+    ds = _check_like("dsum", dsum, x)
+    lib = _lib.load()
+    with _on(x.device, stream):
+        dx = torch.empty_like(x) if input_grad else None
+        dw = ws = None
+        need = 0
+        if param_grad and weight is not None:
+            dw = torch.empty(width, dtype=torch.float32, device=x.device)
+            need = lib.pmha_rms_norm_backward_workspace_size(_DTYPES[x.dtype], rows, width)
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        st = lib.pmha_rms_norm_backward(_DTYPES[x.dtype], rows, width, x.data_ptr(), w, eps, dy, ds, _ptr(dx),
+                                        _ptr(dw), _ptr(ws), need, _stream_ptr(stream))
+    _lib.check(st, "pmha_rms_norm_backward")
+    return {"dx": dx, "dweight": dw}
+
+
+def pmha_clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
+    """Scales the gradients (an iterable of contiguous float32 / bfloat16 CUDA
+    tensors of one device; None entries are skipped) by
+    min(1, max_norm / (norm + 1e-6)), norm the 2-norm of all their values, and
+    returns the norm before scaling as a float32 scalar on the device. In place,
+    or into the tensors of `out` (one for each gradient, same shape and type)."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError("out must have one tensor for each gradient")
+    if any(g is None for g in grads):
+        keep = [i for i, g in enumerate(grads) if g is not None]
+        grads, outs = [grads[i] for i in keep], [outs[i] for i in keep]
+    if not grads:
+        raise ValueError("no gradients: the call needs a tensor to know its device")
+    T = torch.Tensor
+    for ts in (grads,) if out is None else (grads, outs):
+        if not all(isinstance(t, T) for t in ts) or not all(map(T.is_contiguous, ts)) \
+                or not all(t.is_cuda for t in ts) or len({t.device for t in ts}) > 1:
+            raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
+    device = grads[0].device
+    types = [_DTYPES.get(t.dtype, -1) for t in grads]
+    if -1 in types:
+        raise TypeError("gradients must be float32 or bfloat16")
+    if out is not None and (outs[0].device != device or
+                            any(o.shape != g.shape or o.dtype != g.dtype for g, o in zip(grads, outs))):
+        raise ValueError("each output must have its gradient's shape, type and device")
+    n = len(grads)
+    gp = (ctypes.c_void_p * n)(*map(T.data_ptr, grads))
+    op = gp if out is None else (ctypes.c_void_p * n)(*map(T.data_ptr, outs))
+    sizes = (ctypes.c_int64 * n)(*map(T.numel, grads))
+    kinds = (ctypes.c_int * n)(*types)
+    lib = _lib.load()
+    need = lib.pmha_clip_grad_norm_workspace_size(n)
+    with _on(device, stream):
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        st = lib.pmha_clip_grad_norm(n, gp, op, sizes, kinds, max_norm, norm.data_ptr(), ws.data_ptr(), need,
+                                     _stream_ptr(stream))
+    _lib.check(st, "pmha_clip_grad_norm")
+    return norm
+
+
+def _ffn_struct(p, wg, wu, dtype) -> _lib.PmhaFfnParams:
+    """Checks a block's tensors and lists them for the library (wg, wu: None for
+    a quantized block)."""
+    wd = p.wd
+    if not isinstance(wd, torch.Tensor) or wd.dim() != 2 or wd.dtype not in _DTYPES or not wd.is_cuda \
+            or not wd.is_contiguous():
+        raise ValueError("wd must be a contiguous (E, F) CUDA tensor of float32 or bfloat16")
+    E, F = wd.shape
+    for n, w in (("wg", p.wg), ("wu", p.wu)):
+        want = wd.dtype if dtype is None else dtype
+        if not isinstance(w, torch.Tensor) or w.shape != (F, E) or w.dtype != want or w.device != wd.device \
+                or not w.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous ({F}, {E}) tensor of {want} on {wd.device}")
+    if p.act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    return _lib.PmhaFfnParams(E, F, _DTYPES[wd.dtype], ACTS[p.act], wg, wu, wd.data_ptr(),
+                              _check_vector("bg", p.bg, F, wd.dtype, wd.device),
+                              _check_vector("bu", p.bu, F, wd.dtype, wd.device),
+                              _check_vector("bd", p.bd, E, wd.dtype, wd.device))
+
+
+@dataclasses.dataclass
+class FfnParams:
+    """A gated feed-forward block, (act(x wg^T + bg) * (x wu^T + bu)) wd^T + bd:
+    wg, wu (F, E) and wd (E, F) stored (out, in), biases (F,), (F,), (E,) or None,
+    all float32 or all bfloat16 on one CUDA device; act "silu" or "gelu" (erf)."""
+    wg: torch.Tensor
+    wu: torch.Tensor
+    wd: torch.Tensor
+    bg: torch.Tensor | None = None
+    bu: torch.Tensor | None = None
+    bd: torch.Tensor | None = None
+    act: str = "silu"
+
+    def as_struct(self) -> _lib.PmhaFfnParams:
+        return _ffn_struct(self, _ptr(self.wg), _ptr(self.wu), None)
+
+
+@dataclasses.dataclass
+class FfnQuantizedParams:
+    """A bfloat16 block whose gate and up weights are float8_e4m3fn with one
+    float32 scale for each of their F rows (quantize_rows makes them)."""
+    wg: torch.Tensor
+    wg_scale: torch.Tensor
+    wu: torch.Tensor
+    wu_scale: torch.Tensor
+    wd: torch.Tensor
+    bg: torch.Tensor | None = None
+    bu: torch.Tensor | None = None
+    bd: torch.Tensor | None = None
+    act: str = "silu"
+
+    def as_struct(self) -> _lib.PmhaFfnParams:
+        return _ffn_struct(self, None, None, torch.float8_e4m3fn)
+
+    def quantized_struct(self) -> _lib.PmhaFfnQuantized:
+        F, dev = self.wg.shape[0], self.wd.device
+        for n in ("wg_scale", "wu_scale"):
+            if getattr(self, n) is None:
+                raise ValueError(f"{n} is missing")
+        return _lib.PmhaFfnQuantized(_ptr(self.wg), _ptr(self.wu),
+                                     _check_vector("wg_scale", self.wg_scale, F, torch.float32, dev),
+                                     _check_vector("wu_scale", self.wu_scale, F, torch.float32, dev))
+
+    @staticmethod
+    def from_params(params: FfnParams) -> "FfnQuantizedParams":
+        """The block with its gate and up weights quantized, once, when a model is loaded."""
+        return FfnQuantizedParams(*quantize_rows(params.wg), *quantize_rows(params.wu), params.wd, params.bg,
+                                  params.bu, params.bd, params.act)
+
+
+def quantize_rows(w: torch.Tensor):
+    """(q, scale) of a weight matrix: q float8_e4m3fn, scale float32 a row,
+    max|row| / 448 (at least 2^-64), w ~ q * scale[:, None]. A step of loading a
+    model, in torch operations; tokens are quantized by pmha_rms_norm_quantized."""
+    f = w.float()
+    scale = (f.abs().amax(-1) / 448.0).clamp_min(2.0 ** -64)
+    return (f / scale[..., None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn), scale
+
+
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
+def _ffn_size(fn, p, rows, where) -> int:
+    need = fn(ctypes.byref(p), rows)
+    if need == _NO_SIZE:
+        # the checks of the size functions are those of the calls: the message is there, and its kind follows it
+        raise PmhaError(1, where, (_lib.load().pmha_last_error() or b"").decode())
+    return need
+
+
+def pmha_ffn_forward_workspace_size(params: FfnParams, rows: int) -> int:
+    return _ffn_size(_lib.load().pmha_ffn_forward_workspace_size, params.as_struct(), int(rows), "pmha_ffn_forward")
+
+
+def pmha_ffn_forward_quantized_workspace_size(params: FfnQuantizedParams, rows: int) -> int:
+    return _ffn_size(_lib.load().pmha_ffn_forward_quantized_workspace_size, params.as_struct(), int(rows),
+                     "pmha_ffn_forward_quantized")
+
+
+def pmha_ffn_backward_workspace_size(params: FfnParams, rows: int) -> int:
+    return _ffn_size(_lib.load().pmha_ffn_backward_workspace_size, params.as_struct(), int(rows), "pmha_ffn_backward")
+
+
+def _ffn_tokens(name, x, params, dtype):
+    rows, width = _check_rows(name, x, dtype)
+    if width != params.wd.shape[0] or x.device != params.wd.device:
+        raise ValueError(f"{name} must be (..., {params.wd.shape[0]}) on {params.wd.device}")
+    return rows
+
+
+def pmha_ffn_forward(params: FfnParams, x: torch.Tensor, residual: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The gated feed-forward block on tokens x (..., E), plus the residual."""
+    p = params.as_struct()
+    rows = _ffn_tokens("x", x, params, params.wd.dtype)
+    r = _check_like("residual", residual, x)
+    _check_like("out", out, x)
+    lib = _lib.load()
+    need = _ffn_size(lib.pmha_ffn_forward_workspace_size, p, rows, "pmha_ffn_forward")
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        ws = _workspace(need, x.device, workspace)
+        st = lib.pmha_ffn_forward(ctypes.byref(p), x.data_ptr(), r, rows, out.data_ptr(), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _stream_ptr(stream))
+    _lib.check(st, "pmha_ffn_forward")
+    return out
+
+
+def pmha_ffn_forward_quantized(params: FfnQuantizedParams, x: torch.Tensor, x_scale: torch.Tensor,
+                               residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None, stream=None):
+    """pmha_ffn_forward for tokens in float8_e4m3fn with a float32 scale each (what
+    pmha_rms_norm_quantized returns) and a quantized block; residual and result
+    are bfloat16."""
+    p, q = params.as_struct(), params.quantized_struct()
+    rows = _ffn_tokens("x", x, params, torch.float8_e4m3fn)
+    if not isinstance(x_scale, torch.Tensor) or x_scale.shape != x.shape[:-1] or x_scale.dtype != torch.float32 \
+            or x_scale.device != x.device or not x_scale.is_contiguous():
+        raise ValueError(f"x_scale must be a contiguous {tuple(x.shape[:-1])} float32 tensor on {x.device}")
+    for n, t in (("residual", residual), ("out", out)):
+        if t is not None and (t.shape != x.shape or t.dtype != params.wd.dtype or t.device != x.device
+                              or not t.is_contiguous()):
+            raise ValueError(f"{n} must be a contiguous {tuple(x.shape)} tensor of {params.wd.dtype} on {x.device}")
+    lib = _lib.load()
+    need = _ffn_size(lib.pmha_ffn_forward_quantized_workspace_size, p, rows, "pmha_ffn_forward_quantized")
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty_like(x, dtype=params.wd.dtype)
+        ws = _workspace(need, x.device, workspace)
+        st = lib.pmha_ffn_forward_quantized(ctypes.byref(p), ctypes.byref(q), x.data_ptr(), x_scale.data_ptr(),
+                                            _ptr(residual), rows, out.data_ptr(), ws.data_ptr(),
+                                            ws.numel() * ws.element_size(), _stream_ptr(stream))
+    _lib.check(st, "pmha_ffn_forward_quantized")
+    return out
+
+
+def pmha_ffn_backward(params: FfnParams, x: torch.Tensor, dout: torch.Tensor, input_grads: bool = True,
+                      param_grads: bool = True, workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of the block for dout = dLoss/d(block(x)), the hidden rows
+    recomputed from x: {"dx", "dwg", "dwu", "dwd", "dbg", "dbu", "dbd"} in the
+    block's type (None for biases it does not have). A residual's gradient is
+    dout itself."""
+    p = params.as_struct()
+    rows = _ffn_tokens("x", x, params, params.wd.dtype)
+    if dout is None:
+        raise ValueError("dout is missing")
+    dy = _check_like("dout", dout, x)
+    lib = _lib.load()
+    need = _ffn_size(lib.pmha_ffn_backward_workspace_size, p, rows, "pmha_ffn_backward")
+    out = {}
+    g = _lib.PmhaFfnGrads()
+    with _on(x.device, stream):
+        dx = None
+        if input_grads:
+            out["dx"] = dx = torch.empty_like(x)
+        if param_grads:
+            for n in ("wg", "wu", "wd", "bg", "bu", "bd"):
+                t = getattr(params, n)
+                out["d" + n] = None if t is None else torch.empty_like(t)
+                setattr(g, n, _ptr(out["d" + n]))
+        ws = _workspace(need, x.device, workspace)
+        st = lib.pmha_ffn_backward(ctypes.byref(p), x.data_ptr(), dy, rows, _ptr(dx), ctypes.byref(g), ws.data_ptr(),
+                                   ws.numel() * ws.element_size(), _stream_ptr(stream))
+    _lib.check(st, "pmha_ffn_backward")
+    return out
+
+
+class PackedEncoderLayer:
+    """One pre-norm encoder layer around the packed attention, on tokens
+    x (B, n, E) of one graph with query_features == key_features:
+
+        a = attention(norm1(x));  s = x + a;  y = s + block(norm2(s))
+
+    ``layer(x)`` runs it (residual and norm2 in one pass over the tokens);
+    ``layer.backward(x, dy)`` returns the gradients of x and of every parameter
+    for dy = dLoss/dy, recomputing the forward pass; ``layer.clip_grads`` scales
+    them by their global norm."""
+
+    def __init__(self, graph: Graph, attention: Params, norm1: torch.Tensor, norm2: torch.Tensor, block: FfnParams,
+                 eps: float = 1e-6):
+        if graph.query_features != graph.key_features:
+            raise ValueError("an encoder layer needs a graph with query_features == key_features")
+        E = attention.embed_dim
+        for n, t in (("norm1", norm1), ("norm2", norm2)):
+            _check_vector(n, t, E, attention.dtype, attention.wq.device)
+        if block.wd.dtype != attention.dtype or block.wd.shape[0] != E:
+            raise ValueError(f"the block must have width {E} and type {attention.dtype}")
+        self.graph, self.attention, self.block = graph, attention, block
+        self.norm1, self.norm2, self.eps = norm1, norm2, float(eps)
+
+    def _attend(self, x, key_padding_mask):
+        n1, _ = pmha_rms_norm(x, self.norm1, self.eps)
+        a, _ = pmha_forward(self.graph, self.attention, n1, n1, n1, key_padding_mask=key_padding_mask)
+        n2, s = pmha_rms_norm(a, self.norm2, self.eps, residual=x)
+        return n1, s, n2
+
+    def __call__(self, x: torch.Tensor, key_padding_mask: torch.Tensor | None = None) -> torch.Tensor:
+        _, s, n2 = self._attend(x, key_padding_mask)
+        return pmha_ffn_forward(self.block, n2, residual=s)
+
+    def backward(self, x: torch.Tensor, dy: torch.Tensor, key_padding_mask: torch.Tensor | None = None) -> dict:
+        """{"dx", "dnorm1", "dnorm2", and the keys of pmha_backward's and
+        pmha_ffn_backward's parameter gradients}."""
+        n1, s, n2 = self._attend(x, key_padding_mask)
+        gb = pmha_ffn_backward(self.block, n2, dy)
+        g2 = pmha_rms_norm_backward(s, self.norm2, self.eps, gb.pop("dx"), dsum=dy)
+        ds = g2["dx"]  # of x and of the attention's output
+        ga = pmha_backward(self.graph, self.attention, n1, n1, n1, ds, key_padding_mask=key_padding_mask)
+        dn1 = ga.pop("dquery")  # one tensor: the sum over the three roles
+        del ga["dkey"], ga["dvalue"]
+        g1 = pmha_rms_norm_backward(x, self.norm1, self.eps, dn1, dsum=ds)
+        return {"dx": g1["dx"], "dnorm1": g1["dweight"], "dnorm2": g2["dweight"], **ga, **gb}
+
+    @staticmethod
+    def clip_grads(grads: dict, max_norm: float) -> torch.Tensor:
+        """Scales the parameter gradients of backward() in place; returns their norm."""
+        return pmha_clip_grad_norm([t for n, t in grads.items() if n != "dx"], max_norm)

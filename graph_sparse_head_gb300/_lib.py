@@ -16,6 +16,7 @@ STATUS_NAMES = {
 }
 PMHA_F32, PMHA_BF16 = 0, 1
 PMHA_WEIGHTS_NONE, PMHA_WEIGHTS_AVG, PMHA_WEIGHTS_PER_HEAD = 0, 1, 2
+PMHA_ACT_SILU, PMHA_ACT_GELU = 0, 1
 
 # Every function the header declares, with (restype, argtypes).
 _vp = ctypes.c_void_p
@@ -33,7 +34,23 @@ class PmhaGrads(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("wq", "wk", "wv", "wo", "bq", "bk", "bv", "bo")]
 
 
+class PmhaFfnParams(ctypes.Structure):
+    _fields_ = [("embed_dim", ctypes.c_int64), ("hidden_dim", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("wg", _vp), ("wu", _vp), ("wd", _vp), ("bg", _vp), ("bu", _vp), ("bd", _vp)]
+
+
+class PmhaFfnQuantized(ctypes.Structure):
+    _fields_ = [("wg", _vp), ("wu", _vp), ("wg_scale", _vp), ("wu_scale", _vp)]
+
+
+class PmhaFfnGrads(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("wg", "wu", "wd", "bg", "bu", "bd")]
+
+
 _P = ctypes.POINTER(PmhaParams)
+_F = ctypes.POINTER(PmhaFfnParams)
+_FQ = ctypes.POINTER(PmhaFfnQuantized)
+_FG = ctypes.POINTER(PmhaFfnGrads)
 _G = ctypes.POINTER(PmhaGrads)
 _I64P = ctypes.POINTER(ctypes.c_int64)
 
@@ -59,6 +76,18 @@ SIGNATURES = {
     "pmha_backward_workspace_size": (_sz, [_vp, _P, _i64]),
     "pmha_backward": (ctypes.c_int, [_vp, _P, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _G, _vp, _sz, _vp]),
     "pmha_graph_export_by_source": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+    "pmha_rms_norm": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp]),
+    "pmha_rms_norm_backward_workspace_size": (_sz, [ctypes.c_int, _i64, _i64]),
+    "pmha_rms_norm_backward": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                              _vp, _sz, _vp]),
+    "pmha_ffn_forward_workspace_size": (_sz, [_F, _i64]),
+    "pmha_ffn_forward": (ctypes.c_int, [_F, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "pmha_ffn_forward_quantized_workspace_size": (_sz, [_F, _i64]),
+    "pmha_ffn_forward_quantized": (ctypes.c_int, [_F, _FQ, _vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "pmha_ffn_backward_workspace_size": (_sz, [_F, _i64]),
+    "pmha_ffn_backward": (ctypes.c_int, [_F, _vp, _vp, _i64, _vp, _FG, _vp, _sz, _vp]),
+    "pmha_clip_grad_norm_workspace_size": (_sz, [_i64]),
+    "pmha_clip_grad_norm": (ctypes.c_int, [_i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }
 
 _lock = threading.Lock()

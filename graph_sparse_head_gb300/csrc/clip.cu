@@ -1,0 +1,322 @@
+// Clipping of many gradient tensors by their global norm:
+//   norm = sqrt(sum of g^2 over all tensors),  out = g * min(1, max_norm / (norm + 1e-6)).
+//
+// Two passes, bound by memory: a persistent grid sums squares over chunks of
+// kChunk values and leaves one partial sum a block; the scaling pass has every
+// block add the partial sums (a few KB from L2) in the same order, so all
+// blocks hold the same norm without a launch in between, and walks the chunks
+// backwards, because the last ones read are the ones still in L2. The table of
+// tensors travels in the kernel's parameters, so that nothing is copied, no
+// host array has to outlive the call, and a captured graph holds its own.
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "pmha_internal.h"
+
+namespace pmha {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kBatch = 512;       // tensors of one launch: a table of 12 KB of parameters
+constexpr int kChunk = 16384;     // values a block takes at a time
+constexpr int kBlocksPerSm = 4;
+constexpr int kMaxBlocks = 1024;  // partial sums of one launch
+constexpr unsigned kFull = 0xffffffffu;
+
+// Squares of float32 values span twice its exponents. Each value goes, by its
+// size, into one of three sums: as it is, scaled up by 2^80, or down by 2^-80
+// (powers of two: exact), each of which neither overflows nor loses small
+// squares; the three meet in double.
+constexpr float kSmall = 9.094947e-13f, kBig = 1.0995116e12f;  // 2^-40, 2^40
+constexpr float kUp = 1.2089258e24f, kDown = 8.2718061e-25f;   // 2^80, 2^-80
+
+struct Table {
+    const void *g[kBatch];
+    void *out[kBatch];
+    uint32_t first[kBatch + 1];  // first chunk of each tensor
+    uint32_t last_n[kBatch];     // values of its last chunk, 1 .. kChunk; top bit: bf16
+    int n;
+};
+
+struct Sums {
+    float mid, big, small;
+};
+
+__device__ __forceinline__ bool is_mid(float g)
+{
+    const float t = fabsf(g);
+    return (t >= kSmall || t == 0.f) && t <= kBig;
+}
+__device__ __forceinline__ void add_square(Sums &s, float g)
+{
+    const float t = fabsf(g);
+    if (t >= kSmall && t <= kBig) s.mid = fmaf(g, g, s.mid);
+    else if (t < kSmall) s.small = fmaf(g * kUp, g * kUp, s.small);
+    else s.big = fmaf(g * kDown, g * kDown, s.big);  // infinities and NaN too
+}
+
+// chunk -> tensor: the last i with first[i] <= c
+__device__ __forceinline__ int tensor_of(const Table &t, uint32_t c)
+{
+    int lo = 0, hi = t.n;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) / 2;
+        if (t.first[m] <= c) lo = m;
+        else hi = m;
+    }
+    return lo;
+}
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T>
+__device__ __forceinline__ void sum_chunk(const T *g, int n, Sums &s)
+{
+    constexpr int V = 16 / sizeof(T);
+    int i0 = 0;
+    if (((uintptr_t)g & 15) == 0) {
+        i0 = n / V * V;
+#pragma unroll 4
+        for (int i = threadIdx.x * V; i < i0; i += kThreads * V) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(g + i);
+            T v[V];
+            *reinterpret_cast<uint4 *>(v) = raw;
+            bool mid = true;
+#pragma unroll
+            for (int k = 0; k < V; ++k) mid &= is_mid(to_f<T>(v[k]));
+            if (mid) {  // the usual case, without a branch a value
+#pragma unroll
+                for (int k = 0; k < V; ++k) s.mid = fmaf(to_f<T>(v[k]), to_f<T>(v[k]), s.mid);
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k) add_square(s, to_f<T>(v[k]));
+            }
+        }
+    }
+    for (int i = i0 + threadIdx.x; i < n; i += kThreads) add_square(s, to_f<T>(g[i]));
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const T *g, T *out, int n, float c)
+{
+    constexpr int V = 16 / sizeof(T);
+    int i0 = 0;
+    if ((((uintptr_t)g | (uintptr_t)out) & 15) == 0) {
+        i0 = n / V * V;
+#pragma unroll 4
+        for (int i = threadIdx.x * V; i < i0; i += kThreads * V) {
+            uint4 raw = *reinterpret_cast<const uint4 *>(g + i);
+            T v[V];
+            *reinterpret_cast<uint4 *>(v) = raw;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = from_f<T>(to_f<T>(v[k]) * c);
+            *reinterpret_cast<uint4 *>(out + i) = *reinterpret_cast<uint4 *>(v);
+        }
+    }
+    for (int i = i0 + threadIdx.x; i < n; i += kThreads) out[i] = from_f<T>(to_f<T>(g[i]) * c);
+}
+
+// Sum over the block of a double, the same in every thread and in every block.
+__device__ __forceinline__ double block_sum(double v, double *sh)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
+    return v;
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_squares(const __grid_constant__ Table t, double *part)
+{
+    __shared__ double sh[kThreads / 32];
+    const uint32_t chunks = t.first[t.n];
+    Sums s = {0.f, 0.f, 0.f};
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int i = tensor_of(t, c);
+        const uint32_t at = c - t.first[i];
+        const bool bf16 = t.last_n[i] >> 31;
+        const int n = c + 1 < t.first[i + 1] ? kChunk : (int)(t.last_n[i] & 0x7fffffffu);
+        if (bf16) sum_chunk((const __nv_bfloat16 *)t.g[i] + (size_t)at * kChunk, n, s);
+        else sum_chunk((const float *)t.g[i] + (size_t)at * kChunk, n, s);
+    }
+    const double up = (double)kUp, down = (double)kDown;
+    const double v = (double)s.mid + (double)s.small / (up * up) + (double)s.big / (down * down);
+    const double sum = block_sum(v, sh);
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    k_grad_scale(const __grid_constant__ Table t, const double *__restrict__ part, int n_part, float max_norm,
+                 float *norm_out)
+{
+    __shared__ double sh[kThreads / 32];
+    double v = 0.0;
+    for (int i = threadIdx.x; i < n_part; i += kThreads) v += part[i];
+    const double norm = sqrt(block_sum(v, sh));
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+    const double ratio = (double)max_norm / (norm + 1e-6);
+    const float c = ratio > 1.0 ? 1.f : (float)ratio;  // a NaN stays
+    const uint32_t chunks = t.first[t.n];
+    for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
+        const uint32_t ch = chunks - 1 - b;
+        const int i = tensor_of(t, ch);
+        if (c == 1.f && t.out[i] == t.g[i]) continue;  // in place and nothing to scale
+        const size_t at = (size_t)(ch - t.first[i]) * kChunk;
+        const bool bf16 = t.last_n[i] >> 31;
+        const int n = ch + 1 < t.first[i + 1] ? kChunk : (int)(t.last_n[i] & 0x7fffffffu);
+        if (bf16) scale_chunk((const __nv_bfloat16 *)t.g[i] + at, (__nv_bfloat16 *)t.out[i] + at, n, c);
+        else scale_chunk((const float *)t.g[i] + at, (float *)t.out[i] + at, n, c);
+    }
+}
+
+size_t part_bytes(int64_t n_tensors)
+{
+    // batches are cut by tensors and by chunks (32-bit), so a call may take a few more than n / kBatch
+    return (size_t)((n_tensors + kBatch - 1) / kBatch + 1) * kMaxBlocks * sizeof(double);
+}
+
+struct Range {
+    uintptr_t at;
+    size_t n;
+    bool out;
+};
+
+}  // namespace
+}  // namespace pmha
+
+using namespace pmha;
+
+extern "C" {
+
+size_t pmha_clip_grad_norm_workspace_size(int64_t n_tensors)
+{
+    if (n_tensors < 0 || n_tensors > (int64_t)1 << 24) return 0;
+    return part_bytes(n_tensors);
+}
+
+pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, void *const *out, const int64_t *numel,
+                                const pmha_dtype *dtype, float max_norm, float *norm, void *workspace,
+                                size_t workspace_bytes, pmha_stream stream)
+{
+    if (n_tensors < 0 || n_tensors > (int64_t)1 << 24 || (n_tensors && (!grads || !numel || !dtype))) {
+        set_error("pmha_clip_grad_norm: %lld tensors, or a NULL table", (long long)n_tensors);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (!isfinite(max_norm) || max_norm < 0.f) {
+        set_error("pmha_clip_grad_norm: max_norm %g must be finite and at least 0", (double)max_norm);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (!norm || ((uintptr_t)norm & 3u)) {
+        set_error("pmha_clip_grad_norm: norm is NULL or not aligned");
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const size_t need = part_bytes(n_tensors);
+    if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) {
+        set_error("pmha_clip_grad_norm: workspace needs %zu bytes, 256-byte aligned (got %zu at %p)", need,
+                  workspace_bytes, workspace);
+        return PMHA_ERR_WORKSPACE;
+    }
+    cudaStream_t cs = (cudaStream_t)stream;
+    try {
+        std::vector<Range> ranges;
+        ranges.reserve((size_t)n_tensors * 2 + 1);
+        ranges.push_back({(uintptr_t)norm, 4, true});
+        int64_t total = 0;
+        for (int64_t i = 0; i < n_tensors; ++i) {
+            if (dtype[i] != PMHA_F32 && dtype[i] != PMHA_BF16) {
+                set_error("pmha_clip_grad_norm: tensor %lld: dtype %d is neither PMHA_F32 nor PMHA_BF16",
+                          (long long)i, (int)dtype[i]);
+                return PMHA_ERR_INVALID_ARG;
+            }
+            if (numel[i] < 0 || numel[i] > (int64_t)1 << 40 || (total += numel[i]) > (int64_t)1 << 44) {
+                set_error("pmha_clip_grad_norm: tensor %lld: %lld values", (long long)i, (long long)numel[i]);
+                return PMHA_ERR_INVALID_ARG;
+            }
+            if (numel[i] == 0) continue;
+            const size_t es = dtype[i] == PMHA_BF16 ? 2 : 4;
+            const void *o = out ? out[i] : grads[i];
+            if (!grads[i] || !o || ((uintptr_t)grads[i] % es) || ((uintptr_t)o % es)) {
+                set_error("pmha_clip_grad_norm: tensor %lld is NULL or not aligned to its values", (long long)i);
+                return PMHA_ERR_INVALID_ARG;
+            }
+            ranges.push_back({(uintptr_t)grads[i], (size_t)numel[i] * es, o == grads[i]});
+            if (o != grads[i]) ranges.push_back({(uintptr_t)o, (size_t)numel[i] * es, true});
+        }
+        // gradients counted twice are refused like outputs that touch anything
+        std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.at < b.at; });
+        uintptr_t end = 0;
+        for (const Range &r : ranges) {
+            if (r.at < end) {
+                set_error("pmha_clip_grad_norm: two of the tensors, outputs and norm overlap, or one is given twice");
+                return PMHA_ERR_INVALID_ARG;
+            }
+            end = r.at + r.n;
+        }
+        // launches of up to kBatch tensors and 2^31 chunks each
+        const int max_grid = std::min(num_sms() * kBlocksPerSm, kMaxBlocks);
+        auto fill = [&](Table &t, int64_t first) {
+            int64_t chunks = 0, i = first;
+            t.n = 0;
+            for (; i < n_tensors && t.n < kBatch; ++i) {
+                if (numel[i] == 0) continue;
+                const int64_t c = (numel[i] + kChunk - 1) / kChunk;
+                if (chunks + c > (int64_t)0x7fffffff) break;
+                t.g[t.n] = grads[i];
+                t.out[t.n] = out ? out[i] : const_cast<void *>(grads[i]);
+                t.first[t.n] = (uint32_t)chunks;
+                t.last_n[t.n] = (uint32_t)(numel[i] - (c - 1) * kChunk) | (dtype[i] == PMHA_BF16 ? 1u << 31 : 0u);
+                chunks += c;
+                ++t.n;
+            }
+            t.first[t.n] = (uint32_t)chunks;
+            return i;
+        };
+        Table t;
+        int n_part = 0, launches = 0;
+        double *part = (double *)workspace;
+        int64_t i = 0;
+        do {  // at least once: the norm of nothing is 0
+            i = fill(t, i);
+            const int grid = std::max(1, std::min<int>((int)t.first[t.n], max_grid));
+            if ((size_t)(n_part + grid) * sizeof(double) > need) {
+                set_error("pmha_clip_grad_norm: too many values for one call");
+                return PMHA_ERR_INVALID_ARG;
+            }
+            StageTimer timer("grad_squares", cs);
+            k_grad_squares<<<grid, kThreads, 0, cs>>>(t, part + n_part);
+            count_launch();
+            PMHA_CUDA_TRY(cudaGetLastError());
+            n_part += grid;
+            ++launches;
+        } while (i < n_tensors);
+        i = 0;
+        bool first = true;
+        do {
+            if (launches > 1) i = fill(t, i);
+            else i = n_tensors;  // the only table is still here
+            const int grid = std::max(1, std::min<int>((int)t.first[t.n], max_grid));
+            StageTimer timer("grad_scale", cs);
+            k_grad_scale<<<grid, kThreads, 0, cs>>>(t, part, n_part, max_norm, first ? norm : nullptr);
+            count_launch();
+            PMHA_CUDA_TRY(cudaGetLastError());
+            first = false;
+        } while (i < n_tensors);
+    } catch (const std::bad_alloc &) {
+        set_error("pmha_clip_grad_norm: out of host memory");
+        return PMHA_ERR_INVALID_ARG;
+    }
+    return PMHA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,739 @@
+// Gated feed-forward block: argument checks, workspace, the order of launches,
+// the float32 products on the CUDA cores, and the small kernels around the
+// tensor-core products (copies to padded widths, transposes, sums).
+//
+//   h = act(x Wg^T + bg) * (x Wu^T + bu),    y = h Wd^T + bd (+ residual)
+//   backward, from dy:  dh = dy Wd,  du = dh act(g),  dg = dh u act'(g),
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h, biases column sums.
+//
+// Rows are taken in blocks whose hidden values fit in L2 (kL2Block), so that
+// what one product writes the next reads without going to memory, and the
+// workspace stops growing with the rows.
+#include <math.h>
+
+#include <algorithm>
+
+#include "ffn_internal.h"
+#include "ffn_math.cuh"
+
+namespace pmha {
+namespace {
+
+constexpr int64_t kL2Block = 48 << 20;  // bytes of hidden values (h, or h, dg and du) of a block of rows
+constexpr int kSumParts = 32;           // row ranges of the bias sums
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// ---------------------------------------------------------------- float32 products
+// 64 x 64 outputs a block, 4 x 4 a thread, 16 values of K at a time from
+// shared memory; sums in ascending K with fused multiply-adds.
+constexpr int kT = 64, kK = 16;
+
+// acc[i][j] += sum_k A[m0 + 4 ty + i, k] B[n0 + 4 tx + j, k]. An operand's
+// element (row, k) lies at row * ld + k (K contiguous) or k * ld + row.
+template <bool AK, bool BK>
+__device__ void tile_product(const float *A, int64_t lda, int64_t M, const float *B, int64_t ldb, int64_t N, int64_t k0,
+                             int64_t k1, int64_t m0, int64_t n0, float (&acc)[4][4], float (*as)[kT + 4],
+                             float (*bs)[kT + 4])
+{
+    const int t = threadIdx.x, tx = t % 16, ty = t / 16;
+    for (int64_t k = k0; k < k1; k += kK) {
+#pragma unroll
+        for (int q = 0; q < kT * kK / 256; ++q) {
+            const int idx = t + q * 256;
+            const int ra = AK ? idx / kK : idx % kT, ka = AK ? idx % kK : idx / kT;
+            const int rb = BK ? idx / kK : idx % kT, kb = BK ? idx % kK : idx / kT;
+            as[ka][ra] = m0 + ra < M && k + ka < k1 ? A[AK ? (m0 + ra) * lda + k + ka : (k + ka) * lda + m0 + ra] : 0.f;
+            bs[kb][rb] = n0 + rb < N && k + kb < k1 ? B[BK ? (n0 + rb) * ldb + k + kb : (k + kb) * ldb + n0 + rb] : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kk = 0; kk < kK; ++kk) {
+            const float4 a = *reinterpret_cast<const float4 *>(&as[kk][ty * 4]);
+            const float4 b = *reinterpret_cast<const float4 *>(&bs[kk][tx * 4]);
+            const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(av[i], bv[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+}
+
+struct F32Args {
+    const float *x, *dy, *wg, *wu, *wd, *bg, *bu, *bd, *res;
+    float *h, *dg, *du, *out;
+    int64_t M, E, F;
+};
+
+#define PMHA_F32_TILE                                                 \
+    __shared__ __align__(16) float as[kK][kT + 4], bs[kK][kT + 4];    \
+    const int64_t m0 = (int64_t)blockIdx.x * kT, n0 = (int64_t)blockIdx.y * kT; \
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16
+
+template <int ACT, bool BWD>
+__global__ void __launch_bounds__(256) k_f32_hidden(F32Args a)
+{
+    PMHA_F32_TILE;
+    float g[4][4] = {}, u[4][4] = {}, d[4][4] = {};
+    tile_product<true, true>(a.x, a.E, a.M, a.wg, a.E, a.F, 0, a.E, m0, n0, g, as, bs);
+    tile_product<true, true>(a.x, a.E, a.M, a.wu, a.E, a.F, 0, a.E, m0, n0, u, as, bs);
+    if constexpr (BWD) tile_product<true, false>(a.dy, a.E, a.M, a.wd, a.F, a.F, 0, a.E, m0, n0, d, as, bs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
+            if (m >= a.M || n >= a.F) continue;
+            const float gv = g[i][j] + (a.bg ? a.bg[n] : 0.f), uv = u[i][j] + (a.bu ? a.bu[n] : 0.f);
+            if constexpr (BWD) {
+                float slope;
+                const float act = Act<ACT>::exact(gv, &slope);
+                a.h[m * a.F + n] = act * uv;
+                a.du[m * a.F + n] = d[i][j] * act;
+                a.dg[m * a.F + n] = d[i][j] * uv * slope;
+            } else {
+                a.h[m * a.F + n] = Act<ACT>::exact(gv) * uv;
+            }
+        }
+}
+
+// out = h Wd^T + bd + residual
+__global__ void __launch_bounds__(256) k_f32_down(F32Args a)
+{
+    PMHA_F32_TILE;
+    float c[4][4] = {};
+    tile_product<true, true>(a.h, a.F, a.M, a.wd, a.F, a.E, 0, a.F, m0, n0, c, as, bs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
+            if (m >= a.M || n >= a.E) continue;
+            float v = c[i][j] + (a.bd ? a.bd[n] : 0.f);
+            if (a.res) v += a.res[m * a.E + n];
+            a.out[m * a.E + n] = v;
+        }
+}
+
+// dx = dg Wg + du Wu
+__global__ void __launch_bounds__(256) k_f32_dx(F32Args a)
+{
+    PMHA_F32_TILE;
+    float c[4][4] = {};
+    tile_product<true, false>(a.dg, a.F, a.M, a.wg, a.E, a.E, 0, a.F, m0, n0, c, as, bs);
+    tile_product<true, false>(a.du, a.F, a.M, a.wu, a.E, a.E, 0, a.F, m0, n0, c, as, bs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
+            if (m < a.M && n < a.E) a.out[m * a.E + n] = c[i][j];
+        }
+}
+
+// part[split][what] (+)= {dg, du, h}^T {x, x, dy} over the split's rows; blockIdx.z = split * 3 + what
+__global__ void __launch_bounds__(256) k_f32_dw(F32Args a, float *part, int splits, bool accumulate)
+{
+    PMHA_F32_TILE;
+    const int what = blockIdx.z % 3, split = blockIdx.z / 3;
+    const int64_t per = (a.M + splits - 1) / splits, k0 = split * per, k1 = min(a.M, k0 + per);
+    const float *A = what == 0 ? a.dg : what == 1 ? a.du : a.h, *B = what == 2 ? a.dy : a.x;
+    float c[4][4] = {};
+    tile_product<false, false>(A, a.F, a.F, B, a.E, a.E, k0, k1, m0, n0, c, as, bs);
+    float *dst = part + (int64_t)blockIdx.z * a.F * a.E;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
+            if (m < a.F && n < a.E) dst[m * a.E + n] = accumulate ? dst[m * a.E + n] + c[i][j] : c[i][j];
+        }
+}
+
+// ---------------------------------------------------------------- small kernels
+
+// rows x cols bf16 of pitch `cols` -> pitch out_cols (padding zero, or cut)
+__global__ void __launch_bounds__(256) k_repitch(const uint16_t *in, int64_t rows, int cols, int64_t out_rows,
+                                                 int out_cols, uint16_t *out)
+{
+    const int64_t n = out_rows * out_cols;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / out_cols;
+        const int c = (int)(i - r * out_cols);
+        out[i] = r < rows && c < cols ? in[r * cols + c] : (uint16_t)0;
+    }
+}
+
+struct Transposes {
+    const uint16_t *in[3];
+    uint16_t *out[3];
+    int rows[3], cols[3];
+};
+// out[z] = in[z] transposed (bf16), 32 x 32 tiles
+__global__ void __launch_bounds__(256) k_transpose(Transposes t)
+{
+    __shared__ uint16_t sh[32][33];
+    const int z = blockIdx.z, rows = t.rows[z], cols = t.cols[z];
+    const int r0 = blockIdx.y * 32, c0 = blockIdx.x * 32, x = threadIdx.x % 32, y = threadIdx.x / 32;
+    if (r0 >= rows || c0 >= cols) return;
+    for (int i = y; i < 32; i += 8)
+        if (r0 + i < rows && c0 + x < cols) sh[i][x] = t.in[z][(int64_t)(r0 + i) * cols + c0 + x];
+    __syncthreads();
+    for (int i = y; i < 32; i += 8)
+        if (c0 + i < cols && r0 + x < rows) t.out[z][(int64_t)(c0 + i) * rows + r0 + x] = sh[x][i];
+}
+
+// Column sums of up to three matrices over this block of rows, by kSumParts
+// row ranges: out[z][range][col] (+)=
+struct Sums {
+    const void *in[3];
+    float *out[3];
+    int cols[3];
+    int64_t rows;
+    bool accumulate;
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_colsum(Sums s)
+{
+    __shared__ float sh[8][33];
+    const int z = blockIdx.z, cols = s.cols[z], c = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
+    if (!s.in[z] || blockIdx.x * 32 >= cols) return;
+    const int64_t per = (s.rows + kSumParts - 1) / kSumParts, r0 = blockIdx.y * per, r1 = min(s.rows, r0 + per);
+    const T *in = (const T *)s.in[z];
+    float v = 0.f;
+    if (c < cols)
+#pragma unroll 8
+        for (int64_t r = r0 + y; r < r1; r += 8) v += to_f<T>(in[r * cols + c]);
+    sh[y][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (y == 0 && c < cols) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += sh[i][threadIdx.x];
+        float *o = s.out[z] + (int64_t)blockIdx.y * cols + c;
+        *o = s.accumulate ? *o + v : v;
+    }
+}
+
+struct Finish {
+    const float *part;  // [splits][3][F2][E2]
+    void *w[3];         // (F, E), (F, E), (E, F) or null
+    const float *sums[3];
+    void *b[3];         // (F), (F), (E) or null
+    int splits;
+    int E, F, E2, F2;   // widths of the gradients and of the products
+};
+// Parameter gradients from the partial sums, each added in a fixed order.
+// 32 x 32 tiles of (F, E); the down weight's is written transposed.
+template <typename T>
+__global__ void __launch_bounds__(256) k_finish(Finish p)
+{
+    __shared__ float sh[32][33];
+    const int z = blockIdx.z, x = threadIdx.x % 32, y = threadIdx.x / 32;
+    if (z == 3) {  // biases: one column a thread
+        const int col = (blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int n = i == 2 ? p.E : p.F, n2 = i == 2 ? p.E2 : p.F2;
+            if (!p.b[i] || col >= n) continue;
+            float v = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < kSumParts; ++k) v += p.sums[i][(int64_t)k * n2 + col];
+            ((T *)p.b[i])[col] = from_f<T>(v);
+        }
+        return;
+    }
+    if (!p.w[z]) return;
+    const int f0 = blockIdx.y * 32, e0 = blockIdx.x * 32;
+    const int64_t step = (int64_t)3 * p.F2 * p.E2;
+    for (int i = y; i < 32; i += 8) {
+        const int f = f0 + i, e = e0 + x;
+        float v = 0.f;
+        if (f < p.F && e < p.E) {
+            const float *src = p.part + ((int64_t)z * p.F2 + f) * p.E2 + e;
+#pragma unroll 4
+            for (int k = 0; k < p.splits; ++k) v += src[k * step];
+            if (z < 2) ((T *)p.w[z])[(int64_t)f * p.E + e] = from_f<T>(v);
+        }
+        sh[i][x] = v;
+    }
+    if (z < 2) return;
+    __syncthreads();
+    for (int i = y; i < 32; i += 8)
+        if (e0 + i < p.E && f0 + x < p.F) ((T *)p.w[2])[(int64_t)(e0 + i) * p.F + f0 + x] = from_f<T>(sh[x][i]);
+}
+
+// ---------------------------------------------------------------- host side
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round8(int64_t n) { return (n + 7) & ~(int64_t)7; }
+bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool overlap(const void *a, size_t an, const void *b, size_t bn)
+{
+    if (!a || !b || !an || !bn) return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + bn && y < x + an;
+}
+
+pmha_status check_ffn(const char *who, const pmha_ffn_params *p, int64_t rows, bool quantized)
+{
+    if (!p) {
+        set_error("%s: params is NULL", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (p->dtype != PMHA_F32 && p->dtype != PMHA_BF16) {
+        set_error("%s: dtype %d is neither PMHA_F32 nor PMHA_BF16", who, (int)p->dtype);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (p->act != PMHA_ACT_SILU && p->act != PMHA_ACT_GELU) {
+        set_error("%s: act %d is neither PMHA_ACT_SILU nor PMHA_ACT_GELU", who, (int)p->act);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const int64_t most = 1 << 20;
+    if (p->embed_dim < 1 || p->hidden_dim < 1 || p->embed_dim > most || p->hidden_dim > most ||
+        p->embed_dim * p->hidden_dim > (int64_t)1 << 31) {
+        set_error("%s: embed_dim %lld and hidden_dim %lld must be 1 .. 2^20, their product at most 2^31", who,
+                  (long long)p->embed_dim, (long long)p->hidden_dim);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (rows < 0 || rows > ((int64_t)1 << 31) - 512 || rows * p->embed_dim > (int64_t)1 << 42) {
+        set_error("%s: rows %lld must be 0 .. 2^31 - 512, and rows * embed_dim at most 2^42", who, (long long)rows);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (quantized) {
+        if (p->dtype != PMHA_BF16) {
+            set_error("%s: the parameters must be PMHA_BF16", who);
+            return PMHA_ERR_INVALID_ARG;
+        }
+        if (p->embed_dim % 16 || p->hidden_dim % 8) {
+            set_error("%s: embed_dim %lld must be a multiple of 16 and hidden_dim %lld of 8", who,
+                      (long long)p->embed_dim, (long long)p->hidden_dim);
+            return PMHA_ERR_UNSUPPORTED;
+        }
+    }
+    return PMHA_OK;
+}
+
+pmha_status check_weights(const char *who, const pmha_ffn_params *p, bool quantized)
+{
+    const size_t es = p->dtype == PMHA_BF16 ? 2 : 4;
+    if ((!quantized && (!p->wg || !p->wu || !aligned(p->wg, 16) || !aligned(p->wu, 16))) || !p->wd ||
+        !aligned(p->wd, 16)) {
+        set_error("%s: a weight is NULL or not 16-byte aligned", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (!aligned(p->bg, es) || !aligned(p->bu, es) || !aligned(p->bd, es)) {
+        set_error("%s: a bias is not aligned to its elements", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    return PMHA_OK;
+}
+
+pmha_status check_workspace(const char *who, const void *ws, size_t got, size_t need)
+{
+    if (need && (!ws || got < need || !aligned(ws, 256))) {
+        set_error("%s: workspace needs %zu bytes, 256-byte aligned (got %zu at %p)", who, need, got, ws);
+        return PMHA_ERR_WORKSPACE;
+    }
+    return PMHA_OK;
+}
+
+// Offsets in the workspace and the block of rows, for widths E2, F2 of the
+// products (multiples of 8 for bf16; copies are made where that differs).
+struct Plan {
+    int64_t E2, F2, R;
+    bool padded;
+    size_t wg, wu, wd, bg, bu, bd;  // padded copies
+    size_t x, dy, out;              // padded rows of a block (dy: dy or the residual)
+    size_t wgt, wut, wdt;           // transposed weights (backward)
+    size_t h, dg, du, part, sums;
+    int splits;
+    size_t total;
+};
+
+int f32_splits(int64_t E, int64_t F, int64_t rows)
+{
+    const int64_t tiles = 3 * ceil_div(F, kT) * ceil_div(E, kT);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)num_sms() * 4 / tiles, ceil_div(rows, 128), 64}));
+}
+
+Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward)
+{
+    Plan l = {};
+    const bool bf16 = p->dtype == PMHA_BF16;
+    const size_t es = bf16 ? 2 : 4;
+    l.E2 = bf16 ? round8(p->embed_dim) : p->embed_dim;
+    l.F2 = bf16 ? round8(p->hidden_dim) : p->hidden_dim;
+    l.padded = l.E2 != p->embed_dim || l.F2 != p->hidden_dim;
+    const int64_t per_row = l.F2 * (int64_t)es * (backward ? 3 : 1);
+    l.R = std::max<int64_t>(256, kL2Block / per_row / 256 * 256);
+    l.R = std::min(l.R, ceil_div(std::max<int64_t>(rows, 1), 256) * 256);
+    size_t o = 0;
+    auto take = [&](int64_t n) {
+        const size_t at = o;
+        o += align256((size_t)n * es);
+        return at;
+    };
+    if (l.padded) {
+        l.wg = take(l.E2 * l.F2), l.wu = take(l.E2 * l.F2), l.wd = take(l.E2 * l.F2);
+        l.bg = take(l.F2), l.bu = take(l.F2), l.bd = take(l.E2);
+        l.x = take(l.R * l.E2), l.dy = take(l.R * l.E2), l.out = take(l.R * l.E2);
+    }
+    l.h = take(l.R * l.F2);
+    if (backward) {
+        l.dg = take(l.R * l.F2), l.du = take(l.R * l.F2);
+        if (bf16) l.wgt = take(l.E2 * l.F2), l.wut = take(l.E2 * l.F2), l.wdt = take(l.E2 * l.F2);
+        const int64_t block = std::min(l.R, std::max<int64_t>(rows, 1));
+        l.splits = bf16 ? ffn_dw_splits(l.E2, l.F2, block) : f32_splits(l.E2, l.F2, block);
+        l.part = o;
+        o += align256((size_t)l.splits * 3 * (size_t)(l.E2 * l.F2) * 4);
+        l.sums = o;
+        o += align256((size_t)kSumParts * (size_t)(2 * l.F2 + l.E2) * 4);
+    }
+    l.total = o;
+    return l;
+}
+
+unsigned grid_of(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 256), (int64_t)num_sms() * 16)); }
+
+pmha_status repitch(const void *in, int64_t rows, int64_t cols, int64_t out_rows, int64_t out_cols, void *out,
+                    cudaStream_t s)
+{
+    StageTimer timer("ffn_pad", s);
+    k_repitch<<<grid_of(out_rows * out_cols), 256, 0, s>>>((const uint16_t *)in, rows, (int)cols, out_rows,
+                                                            (int)out_cols, (uint16_t *)out);
+    count_launch();
+    PMHA_CUDA_TRY(cudaGetLastError());
+    return PMHA_OK;
+}
+
+#define PMHA_TRY(expr)                             \
+    do {                                           \
+        const pmha_status _s = (expr);             \
+        if (_s != PMHA_OK) return _s;              \
+    } while (0)
+
+// Weights and biases in the widths of the products.
+pmha_status pad_params(const pmha_ffn_params *p, const Plan &l, char *ws, pmha_ffn_params *q, cudaStream_t s)
+{
+    *q = *p;
+    if (!l.padded) return PMHA_OK;
+    const int64_t E = p->embed_dim, F = p->hidden_dim;
+    q->embed_dim = l.E2, q->hidden_dim = l.F2;
+    PMHA_TRY(repitch(p->wg, F, E, l.F2, l.E2, ws + l.wg, s));
+    PMHA_TRY(repitch(p->wu, F, E, l.F2, l.E2, ws + l.wu, s));
+    PMHA_TRY(repitch(p->wd, E, F, l.E2, l.F2, ws + l.wd, s));
+    q->wg = ws + l.wg, q->wu = ws + l.wu, q->wd = ws + l.wd;
+    if (p->bg) {
+        PMHA_TRY(repitch(p->bg, 1, F, 1, l.F2, ws + l.bg, s));
+        q->bg = ws + l.bg;
+    }
+    if (p->bu) {
+        PMHA_TRY(repitch(p->bu, 1, F, 1, l.F2, ws + l.bu, s));
+        q->bu = ws + l.bu;
+    }
+    if (p->bd) {
+        PMHA_TRY(repitch(p->bd, 1, E, 1, l.E2, ws + l.bd, s));
+        q->bd = ws + l.bd;
+    }
+    return PMHA_OK;
+}
+
+dim3 f32_grid(int64_t M, int64_t N, int64_t z = 1) { return dim3((unsigned)ceil_div(M, kT), (unsigned)ceil_div(N, kT), (unsigned)z); }
+
+pmha_status launched()
+{
+    count_launch();
+    PMHA_CUDA_TRY(cudaGetLastError());
+    return PMHA_OK;
+}
+
+pmha_status forward_f32(const pmha_ffn_params *p, const F32Args &a, cudaStream_t s)
+{
+    {
+        StageTimer timer("ffn_up", s);
+        if (p->act == PMHA_ACT_SILU) k_f32_hidden<PMHA_ACT_SILU, false><<<f32_grid(a.M, a.F), 256, 0, s>>>(a);
+        else k_f32_hidden<PMHA_ACT_GELU, false><<<f32_grid(a.M, a.F), 256, 0, s>>>(a);
+        PMHA_TRY(launched());
+    }
+    StageTimer timer("ffn_down", s);
+    k_f32_down<<<f32_grid(a.M, a.E), 256, 0, s>>>(a);
+    return launched();
+}
+
+// The forward pass, for tokens in the layer type or (q8) in E4M3.
+pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_quantized *q8, const void *x,
+                    const float *x_scale, const void *residual, int64_t rows, void *out, void *workspace,
+                    size_t ws_bytes, cudaStream_t s)
+{
+    const size_t es = p->dtype == PMHA_BF16 ? 2 : 4;
+    const int64_t E = p->embed_dim, F = p->hidden_dim;
+    if (rows == 0) return PMHA_OK;
+    PMHA_TRY(check_weights(who, p, q8 != nullptr));
+    if (!x || !out || !aligned(x, 16) || !aligned(out, 16) || !aligned(residual, 16)) {
+        set_error("%s: x or out is NULL, or a pointer is not 16-byte aligned", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const size_t ob = (size_t)(rows * E) * es, wb = (size_t)(E * F) * es;
+    bool bad = overlap(out, ob, x, q8 ? (size_t)(rows * E) : ob) || overlap(out, ob, residual, ob) ||
+               overlap(out, ob, p->wd, wb) || overlap(out, ob, p->bg, (size_t)F * es) ||
+               overlap(out, ob, p->bu, (size_t)F * es) || overlap(out, ob, p->bd, (size_t)E * es);
+    if (!q8) bad = bad || overlap(out, ob, p->wg, wb) || overlap(out, ob, p->wu, wb);
+    else
+        bad = bad || overlap(out, ob, q8->wg, wb / 2) || overlap(out, ob, q8->wu, wb / 2) ||
+              overlap(out, ob, q8->wg_scale, (size_t)F * 4) || overlap(out, ob, q8->wu_scale, (size_t)F * 4) ||
+              overlap(out, ob, x_scale, (size_t)rows * 4);
+    if (bad) {
+        set_error("%s: out overlaps an input", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const Plan l = plan_of(p, rows, false);
+    PMHA_TRY(check_workspace(who, workspace, ws_bytes, l.total));
+    char *ws = (char *)workspace;
+    pmha_ffn_params q;
+    PMHA_TRY(pad_params(p, l, ws, &q, s));
+    const FfnTc tc{l.E2, l.F2, q.act, q.bg, q.bu, q.bd};
+    for (int64_t r = 0; r < rows; r += l.R) {
+        const int64_t M = std::min(l.R, rows - r);
+        const char *xr = (const char *)x + (size_t)(r * E) * (q8 ? 1 : es);
+        const char *rr = residual ? (const char *)residual + (size_t)(r * E) * es : nullptr;
+        char *yr = (char *)out + (size_t)(r * E) * es;
+        if (p->dtype == PMHA_F32) {
+            F32Args a = {};
+            a.x = (const float *)xr, a.wg = (const float *)p->wg, a.wu = (const float *)p->wu;
+            a.wd = (const float *)p->wd, a.bg = (const float *)p->bg, a.bu = (const float *)p->bu;
+            a.bd = (const float *)p->bd, a.res = (const float *)rr, a.h = (float *)(ws + l.h), a.out = (float *)yr;
+            a.M = M, a.E = E, a.F = F;
+            PMHA_TRY(forward_f32(p, a, s));
+            continue;
+        }
+        const void *xp = xr, *rp = rr;
+        void *yp = yr;
+        if (l.padded) {
+            PMHA_TRY(repitch(xr, M, E, M, l.E2, ws + l.x, s));
+            xp = ws + l.x;
+            if (rr) {
+                PMHA_TRY(repitch(rr, M, E, M, l.E2, ws + l.dy, s));
+                rp = ws + l.dy;
+            }
+            yp = ws + l.out;
+        }
+        FfnUpArgs up = {};
+        up.x = xp, up.wg = q8 ? q8->wg : q.wg, up.wu = q8 ? q8->wu : q.wu;
+        if (q8) up.x_scale = x_scale + r, up.wg_scale = q8->wg_scale, up.wu_scale = q8->wu_scale;
+        up.M = M;
+        up.h = ws + l.h;
+        PMHA_TRY(ffn_tc_up(tc, up, s));
+        PMHA_TRY(ffn_tc_down(tc, ws + l.h, q.wd, rp, M, yp, s));
+        if (l.padded) PMHA_TRY(repitch(ws + l.out, M, l.E2, M, E, yr, s));
+    }
+    return PMHA_OK;
+}
+
+}  // namespace
+}  // namespace pmha
+
+using namespace pmha;
+
+extern "C" {
+
+size_t pmha_ffn_forward_workspace_size(const pmha_ffn_params *params, int64_t rows)
+{
+    if (check_ffn("pmha_ffn_forward", params, rows, false) != PMHA_OK) return SIZE_MAX;
+    return rows ? plan_of(params, rows, false).total : 0;
+}
+
+pmha_status pmha_ffn_forward(const pmha_ffn_params *params, const void *x, const void *residual, int64_t rows,
+                             void *out, void *workspace, size_t workspace_bytes, pmha_stream stream)
+{
+    PMHA_TRY(check_ffn("pmha_ffn_forward", params, rows, false));
+    return forward("pmha_ffn_forward", params, nullptr, x, nullptr, residual, rows, out, workspace, workspace_bytes,
+                   (cudaStream_t)stream);
+}
+
+size_t pmha_ffn_forward_quantized_workspace_size(const pmha_ffn_params *params, int64_t rows)
+{
+    if (check_ffn("pmha_ffn_forward_quantized", params, rows, true) != PMHA_OK) return SIZE_MAX;
+    return rows ? plan_of(params, rows, false).total : 0;
+}
+
+pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha_ffn_quantized *quantized,
+                                       const void *x, const float *x_scale, const void *residual, int64_t rows,
+                                       void *out, void *workspace, size_t workspace_bytes, pmha_stream stream)
+{
+    const char *who = "pmha_ffn_forward_quantized";
+    PMHA_TRY(check_ffn(who, params, rows, true));
+    if (!quantized || !quantized->wg || !quantized->wu || !quantized->wg_scale || !quantized->wu_scale ||
+        !aligned(quantized->wg, 16) || !aligned(quantized->wu, 16) || !aligned(quantized->wg_scale, 4) ||
+        !aligned(quantized->wu_scale, 4)) {
+        set_error("%s: a quantized weight or scale is NULL or not aligned", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (rows && (!x_scale || !aligned(x_scale, 4))) {
+        set_error("%s: x_scale is NULL or not aligned", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    return forward(who, params, quantized, x, x_scale, residual, rows, out, workspace, workspace_bytes,
+                   (cudaStream_t)stream);
+}
+
+size_t pmha_ffn_backward_workspace_size(const pmha_ffn_params *params, int64_t rows)
+{
+    if (check_ffn("pmha_ffn_backward", params, rows, false) != PMHA_OK) return SIZE_MAX;
+    return rows ? plan_of(params, rows, true).total : 0;
+}
+
+pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, const void *dout, int64_t rows, void *dx,
+                              const pmha_ffn_grads *grads, void *workspace, size_t workspace_bytes,
+                              pmha_stream stream)
+{
+    const char *who = "pmha_ffn_backward";
+    PMHA_TRY(check_ffn(who, params, rows, false));
+    const pmha_ffn_params *p = params;
+    const size_t es = p->dtype == PMHA_BF16 ? 2 : 4;
+    const int64_t E = p->embed_dim, F = p->hidden_dim;
+    cudaStream_t s = (cudaStream_t)stream;
+    void *gw[3] = {nullptr, nullptr, nullptr}, *gb[3] = {nullptr, nullptr, nullptr};
+    if (grads) {
+        gw[0] = grads->wg, gw[1] = grads->wu, gw[2] = grads->wd;
+        gb[0] = grads->bg, gb[1] = grads->bu, gb[2] = grads->bd;
+    }
+    const size_t nb[3] = {(size_t)F * es, (size_t)F * es, (size_t)E * es}, wb = (size_t)(E * F) * es,
+                 xb = (size_t)(rows * E) * es;
+    for (int i = 0; i < 3; ++i)
+        if (!aligned(gw[i], es) || !aligned(gb[i], es)) {
+            set_error("%s: a gradient is not aligned to its elements", who);
+            return PMHA_ERR_INVALID_ARG;
+        }
+    if (rows == 0) {
+        for (int i = 0; i < 3; ++i) {
+            if (gw[i]) PMHA_CUDA_TRY(cudaMemsetAsync(gw[i], 0, wb, s));
+            if (gb[i]) PMHA_CUDA_TRY(cudaMemsetAsync(gb[i], 0, nb[i], s));
+        }
+        return PMHA_OK;
+    }
+    PMHA_TRY(check_weights(who, p, false));
+    if (!x || !dout || !aligned(x, 16) || !aligned(dout, 16) || !aligned(dx, 16)) {
+        set_error("%s: x or dout is NULL, or a pointer is not 16-byte aligned", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    {
+        const void *in[8] = {x, dout, p->wg, p->wu, p->wd, p->bg, p->bu, p->bd};
+        const size_t in_n[8] = {xb, xb, wb, wb, wb, nb[0], nb[1], nb[2]};
+        const void *o[7] = {dx, gw[0], gw[1], gw[2], gb[0], gb[1], gb[2]};
+        const size_t o_n[7] = {xb, wb, wb, wb, nb[0], nb[1], nb[2]};
+        bool bad = false;
+        for (int i = 0; i < 7; ++i) {
+            for (int j = 0; j < 8; ++j) bad = bad || overlap(o[i], o_n[i], in[j], in_n[j]);
+            for (int j = 0; j < i; ++j) bad = bad || overlap(o[i], o_n[i], o[j], o_n[j]);
+        }
+        if (bad) {
+            set_error("%s: an output overlaps an input or another output", who);
+            return PMHA_ERR_INVALID_ARG;
+        }
+    }
+    const Plan l = plan_of(p, rows, true);
+    PMHA_TRY(check_workspace(who, workspace, workspace_bytes, l.total));
+    char *ws = (char *)workspace;
+    const bool bf16 = p->dtype == PMHA_BF16;
+    const bool any_w = gw[0] || gw[1] || gw[2], any_b = gb[0] || gb[1] || gb[2];
+    if (!dx && !any_w && !any_b) return PMHA_OK;
+    pmha_ffn_params q;
+    PMHA_TRY(pad_params(p, l, ws, &q, s));
+    const FfnTc tc{l.E2, l.F2, q.act, q.bg, q.bu, q.bd};
+    if (bf16) {
+        Transposes t = {};
+        const int E2 = (int)l.E2, F2 = (int)l.F2;
+        t.in[0] = (const uint16_t *)q.wg, t.out[0] = (uint16_t *)(ws + l.wgt), t.rows[0] = F2, t.cols[0] = E2;
+        t.in[1] = (const uint16_t *)q.wu, t.out[1] = (uint16_t *)(ws + l.wut), t.rows[1] = F2, t.cols[1] = E2;
+        t.in[2] = (const uint16_t *)q.wd, t.out[2] = (uint16_t *)(ws + l.wdt), t.rows[2] = E2, t.cols[2] = F2;
+        const unsigned side = (unsigned)ceil_div(std::max(E2, F2), 32);
+        StageTimer timer("ffn_transpose", s);
+        k_transpose<<<dim3(side, side, 3), 256, 0, s>>>(t);
+        PMHA_TRY(launched());
+    }
+    float *part = (float *)(ws + l.part), *sums = (float *)(ws + l.sums);
+    bool first = true;
+    for (int64_t r = 0; r < rows; r += l.R, first = false) {
+        const int64_t M = std::min(l.R, rows - r);
+        const void *xr = (const char *)x + (size_t)(r * E) * es, *dyr = (const char *)dout + (size_t)(r * E) * es;
+        void *dxr = dx ? (char *)dx + (size_t)(r * E) * es : nullptr;
+        if (bf16) {
+            const void *xp = xr, *dyp = dyr;
+            if (l.padded) {
+                PMHA_TRY(repitch(xr, M, E, M, l.E2, ws + l.x, s));
+                PMHA_TRY(repitch(dyr, M, E, M, l.E2, ws + l.dy, s));
+                xp = ws + l.x, dyp = ws + l.dy;
+            }
+            FfnHiddenArgs hid = {xp, dyp, q.wg, q.wu, ws + l.wdt, M, ws + l.h, ws + l.dg, ws + l.du};
+            PMHA_TRY(ffn_tc_hidden(tc, hid, s));
+            if (dx) {
+                PMHA_TRY(ffn_tc_dx(tc, ws + l.dg, ws + l.du, ws + l.wgt, ws + l.wut, M, l.padded ? ws + l.out : dxr, s));
+                if (l.padded) PMHA_TRY(repitch(ws + l.out, M, l.E2, M, E, dxr, s));
+            }
+            if (any_w) {
+                FfnDwArgs d = {ws + l.dg, ws + l.du, ws + l.h, xp, dyp, M, part, gw[0] || gw[1], gw[2] != nullptr, !first,
+                               l.splits};
+                PMHA_TRY(ffn_tc_dw(tc, d, s));
+            }
+            xr = xp, dyr = dyp;
+        } else {
+            F32Args a = {};
+            a.x = (const float *)xr, a.dy = (const float *)dyr, a.wg = (const float *)p->wg;
+            a.wu = (const float *)p->wu, a.wd = (const float *)p->wd, a.bg = (const float *)p->bg;
+            a.bu = (const float *)p->bu, a.h = (float *)(ws + l.h), a.dg = (float *)(ws + l.dg);
+            a.du = (float *)(ws + l.du), a.out = (float *)dxr, a.M = M, a.E = E, a.F = F;
+            {
+                StageTimer timer("ffn_hidden", s);
+                if (p->act == PMHA_ACT_SILU) k_f32_hidden<PMHA_ACT_SILU, true><<<f32_grid(M, F), 256, 0, s>>>(a);
+                else k_f32_hidden<PMHA_ACT_GELU, true><<<f32_grid(M, F), 256, 0, s>>>(a);
+                PMHA_TRY(launched());
+            }
+            if (dx) {
+                StageTimer timer("ffn_dx", s);
+                k_f32_dx<<<f32_grid(M, E), 256, 0, s>>>(a);
+                PMHA_TRY(launched());
+            }
+            if (any_w) {
+                StageTimer timer("ffn_dw", s);
+                k_f32_dw<<<f32_grid(F, E, 3 * l.splits), 256, 0, s>>>(a, part, l.splits, !first);
+                PMHA_TRY(launched());
+            }
+        }
+        if (any_b) {
+            Sums c = {};
+            c.in[0] = gb[0] ? ws + l.dg : nullptr, c.in[1] = gb[1] ? ws + l.du : nullptr, c.in[2] = gb[2] ? dyr : nullptr;
+            c.out[0] = sums, c.out[1] = sums + kSumParts * l.F2, c.out[2] = sums + 2 * kSumParts * l.F2;
+            c.cols[0] = c.cols[1] = (int)l.F2, c.cols[2] = (int)l.E2;
+            c.rows = M, c.accumulate = !first;
+            const dim3 grid((unsigned)ceil_div(std::max(l.E2, l.F2), 32), kSumParts, 3);
+            StageTimer timer("ffn_bias_sums", s);
+            if (bf16) k_colsum<__nv_bfloat16><<<grid, 256, 0, s>>>(c);
+            else k_colsum<float><<<grid, 256, 0, s>>>(c);
+            PMHA_TRY(launched());
+        }
+    }
+    if (any_w || any_b) {
+        Finish f = {};
+        f.part = part, f.splits = l.splits;
+        f.E = (int)E, f.F = (int)F, f.E2 = (int)l.E2, f.F2 = (int)l.F2;
+        for (int i = 0; i < 3; ++i) {
+            f.w[i] = gw[i], f.b[i] = gb[i];
+            f.sums[i] = sums + (i == 0 ? 0 : i == 1 ? kSumParts * l.F2 : 2 * kSumParts * l.F2);
+        }
+        const dim3 grid((unsigned)ceil_div(E, 32), (unsigned)ceil_div(F, 32), 4);
+        StageTimer timer("ffn_grads", s);
+        if (bf16) k_finish<__nv_bfloat16><<<grid, 256, 0, s>>>(f);
+        else k_finish<float><<<grid, 256, 0, s>>>(f);
+        PMHA_TRY(launched());
+    }
+    return PMHA_OK;
+}
+
+}  // extern "C"

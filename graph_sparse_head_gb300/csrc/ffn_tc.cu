@@ -1,0 +1,722 @@
+// Tensor-core products of the gated feed-forward block (sm_103a), one kernel
+// shape for all five:
+//
+//   up      h = act(x Wg^T + bg) * (x Wu^T + bu)      tile 256 tokens x 128 hidden, gate and up side by side
+//   down    y = h Wd^T + bd + residual                tile 256 tokens x 128 or 256 outputs
+//   hidden  h, dg, du of the backward pass            tile 256 tokens x 64 hidden, three products
+//   dx      dg Wg + du Wu                             the down kernel with two pairs of operands
+//   dw      dg^T x, du^T x, h^T dy                    tile 256 hidden x 128 or 256 columns, operands as they lie
+//
+// Two CTAs form a pair (tc_pair.cuh). Each has 10 warps: warp 0 copies
+// 128-byte-wide operand tiles by TMA into a ring of stages, warp 1 of the even
+// CTA issues tcgen05.mma into accumulators in tensor memory (two, so that the
+// products of one tile run under the epilogue of the last), and two groups of
+// four warps turn accumulators into outputs: each thread reads its row's
+// columns, applies the tile's arithmetic, writes the result to a swizzled
+// tile in shared memory, and one thread stores that by TMA. Pairs are
+// persistent and take tiles in order, the column tiles of one row block side
+// by side, so that the rows come from L2 after their first read.
+//
+// Ragged sizes need no code of their own: TMA fills rows and columns past a
+// tensor's end with zeros and does not store them.
+//
+// Every mbarrier wait is bounded (tc_util.cuh); on expiry the pair gives up,
+// waits for its copies and products, frees its tensor memory and returns, and
+// pmha_device_status reports PMHA_ERR_TIMEOUT.
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "ffn_internal.h"
+#include "ffn_math.cuh"
+#include "tc_pair.cuh"
+
+namespace pmha {
+namespace {
+using namespace tcu;
+
+constexpr int kThreads = 320;
+constexpr int kBox = 128 * 128;  // bytes of a tile of 128 rows of 128 bytes
+enum Kind { kUp, kUpQ8, kDown, kHidden, kDw };
+
+// Bytes of a stage and its parts for one CTA, per kind and column tile BN.
+template <int KIND, int BN>
+struct Cfg {
+    static constexpr bool kQ8 = KIND == kUpQ8;
+    static constexpr bool kIsUp = KIND == kUp || KIND == kUpQ8;
+    static constexpr int kA = KIND == kHidden ? 2 * kBox : kBox;        // x (and dy), or 128 columns of an M-major A
+    static constexpr int kB = KIND == kHidden ? kBox / 2 + kBox / 4     // 64 rows of Wg or Wu, 32 of Wd^T
+                              : kIsUp ? kBox                            // 128 rows of Wg or Wu
+                                      : BN / 2 * 128;                   // half of the columns
+    static constexpr int kStage = kA + kB;
+    static constexpr int kOut = KIND == kHidden ? 3 * kBox : KIND == kDw ? 0 : kIsUp ? 2 * kBox : BN / 64 * kBox;
+    static constexpr int kAccCols = KIND == kHidden ? 192 : kIsUp ? 256 : BN;
+    static constexpr int kAccStride = kAccCols > 128 ? 256 : 128;
+    static constexpr int kTmemCols = 2 * kAccStride;
+    static constexpr int kVec = 4 * 256 * 4;  // bias and scale columns, float32
+    static constexpr int kBars = 512;
+    static constexpr int kFit = (232448 - 1024 - kOut - kVec - kBars) / kStage;
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kSmem = 1024 + kStages * kStage + kOut + kVec + kBars;
+    static_assert(kStages >= 3, "a ring of at least three stages");
+    static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+struct Params {
+    CUtensorMap a0, a1, a2, b0, b1, b2, o0, o1, o2, res;
+    int M, E, F;            // tokens, outer and hidden width
+    int n_tiles, tiles_n;   // pair tiles, column tiles of one row block
+    int kb;                 // K blocks of one operand pair
+    int segs;               // operand pairs (down: 1; dx: 2)
+    const __nv_bfloat16 *bias0, *bias1;
+    const float *xs, *gs, *us;
+    int has_res;
+    // dw: row blocks [split * kb_per, ...) of 64 tokens; products `what`
+    int splits, kb_per, tiles_m, first_what, accumulate;
+    float *part;
+    int *err;
+};
+
+// accumulator columns c .. c + 31 of this warp's 32 rows
+__device__ __forceinline__ uint32_t tmem_at(uint32_t base, int quarter, int col)
+{
+    return base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
+}
+// two such reads in flight before one wait
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Keeps the uses of r behind the wait above.
+__device__ __forceinline__ void pin(uint32_t (&r)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// named barrier 3 over both epilogue groups
+__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool both_sync_or(bool pred)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 3, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred)
+        : "memory");
+    return r != 0;
+}
+
+template <int KIND, int BN, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(const __grid_constant__ Params p)
+{
+    using C = Cfg<KIND, BN>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *out_s = smem + kStages * C::kStage;
+    float *vec_s = (float *)(out_s + C::kOut);  // [4][256]
+    uint64_t *full = (uint64_t *)((uint8_t *)vec_s + C::kVec);  // [kStages], counted in the even CTA
+    uint64_t *empty = full + kStages;                           // [kStages], in each CTA
+    uint64_t *acc_full = empty + kStages;                       // [2], in each CTA
+    uint64_t *acc_empty = acc_full + 2;                         // [2], counted in the even CTA
+    uint64_t *mma_done = acc_empty + 2;
+    uint64_t *res_full = mma_done + 1;                          // [2]: the residual's tile of each group
+    uint32_t *tmem_holder = (uint32_t *)(res_full + 2);
+    volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
+    int *issued = (int *)(tmem_holder + 2);  // [kStages]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+            issued[s] = 0;
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&acc_full[i]), 1);
+            mbar_init(smem_u32(&acc_empty[i]), 4);  // two groups in each CTA
+            mbar_init(smem_u32(&res_full[i]), 1);
+        }
+        mbar_init(smem_u32(mma_done), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), C::kTmemCols);
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    // tile -> (row block of 256, column tile, K blocks, product of dw)
+    auto decode = [&](int tile, int &m, int &n, int &kb0, int &kb1, int &what) {
+        kb0 = 0;
+        kb1 = p.kb;
+        what = 0;
+        if constexpr (KIND == kDw) {
+            const int per = p.tiles_m * p.tiles_n;
+            const int split = tile % p.splits;
+            tile /= p.splits;
+            what = p.first_what + tile / per;
+            tile %= per;
+            kb0 = min(p.kb, split * p.kb_per);
+            kb1 = min(p.kb, kb0 + p.kb_per);
+        }
+        m = tile / p.tiles_n;
+        n = tile % p.tiles_n;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer of this CTA
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int tile = pair; tile < p.n_tiles && !*abort_flag; tile += n_pairs) {
+                int m, n, kb0, kb1, what;
+                decode(tile, m, n, kb0, kb1, what);
+                const int row = m * 256 + (int)rank * 128;
+                const int n_kb = KIND == kDown ? p.segs * p.kb : kb1;
+                for (int kb = kb0; kb < n_kb; ++kb) {
+                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p.err)) break;
+                    const uint32_t fb = map_rank(smem_u32(&full[stage]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * C::kStage);
+                    issued[stage] += 1;
+                    const uint32_t sa = smem_u32(smem + stage * C::kStage), sb = sa + C::kA;
+                    if constexpr (C::kIsUp) {
+                        constexpr int kElems = C::kQ8 ? 128 : 64;
+                        tma_load_2d_pair(sa, &p.a0, kb * kElems, row, fb);
+                        tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * kElems, n * 128, fb);
+                    } else if constexpr (KIND == kHidden) {
+                        tma_load_2d_pair(sa, &p.a0, kb * 64, row, fb);
+                        tma_load_2d_pair(sa + kBox, &p.a1, kb * 64, row, fb);
+                        tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * 64, n * 64, fb);
+                        tma_load_2d_pair(sb + kBox / 2, &p.b2, kb * 64, n * 64 + (int)rank * 32, fb);
+                    } else if constexpr (KIND == kDown) {
+                        const bool second = kb >= p.kb;
+                        const int k = (second ? kb - p.kb : kb) * 64;
+                        tma_load_2d_pair(sa, second ? &p.a1 : &p.a0, k, row, fb);
+                        tma_load_2d_pair(sb, second ? &p.b1 : &p.b0, k, n * BN + (int)rank * (BN / 2), fb);
+                    } else {
+                        const CUtensorMap *ma = what == 0 ? &p.a0 : what == 1 ? &p.a1 : &p.a2;
+                        const CUtensorMap *mb = what == 2 ? &p.b1 : &p.b0;
+                        tma_load_2d_pair(sa, ma, row, kb * 64, fb);
+                        tma_load_2d_pair(sa + kBox / 2, ma, row + 64, kb * 64, fb);
+#pragma unroll
+                        for (int j = 0; j < BN / 128; ++j)
+                            tma_load_2d_pair(sb + j * (kBox / 2), mb, n * BN + (int)rank * (BN / 2) + j * 64, kb * 64,
+                                             fb);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer of the pair
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            for (int tile = pair; tile < p.n_tiles && !*abort_flag; tile += n_pairs) {
+                int m, n, kb0, kb1, what;
+                decode(tile, m, n, kb0, kb1, what);
+                const int n_kb = KIND == kDown ? p.segs * p.kb : kb1;
+                if (!mbar_wait_cluster(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, abort_flag, p.err)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * C::kAccStride);
+                bool ok = true;
+                for (int kb = kb0; kb < n_kb; ++kb) {
+                    if (!mbar_wait_cluster(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * C::kStage), sb = sa + C::kA;
+                    const uint32_t more = kb > kb0 ? 1u : 0u;
+                    if constexpr (KIND == kDw) {
+                        const uint64_t da = smem_desc_mn(sa, kBox / 2), db = smem_desc_mn(sb, kBox / 2);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // 16 tokens = 2048 bytes
+                            mma_pair<false>(d, da + (uint64_t)(128 * k), db + (uint64_t)(128 * k),
+                                            idesc_of(false, true, 256, BN), more | (k > 0));
+                    } else {
+                        const uint64_t da = smem_desc(sa), db = smem_desc(sb);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // 32 bytes along K = 2 in the address field
+                            mma_pair<C::kQ8>(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k),
+                                             idesc_of(C::kQ8, false, 256, KIND == kHidden ? 128 : C::kAccCols),
+                                             more | (k > 0));
+                        if constexpr (KIND == kHidden) {
+                            const uint64_t da1 = smem_desc(sa + kBox), db1 = smem_desc(sb + kBox / 2);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_pair<false>(d + 128, da1 + (uint64_t)(2 * k), db1 + (uint64_t)(2 * k),
+                                                idesc_of(false, false, 256, 64), more | (k > 0));
+                        }
+                    }
+                    mma_commit_pair(smem_u32(&empty[stage]));
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit_pair(smem_u32(&acc_full[acc]));
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            mma_commit_pair(smem_u32(mma_done));
+            int dummy = 0;
+            mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
+        }
+    } else {
+        // ---------------- epilogue: group g takes its share of the columns of every tile
+        const int quarter = warp & 3, g = (warp - 2) >> 2, et = threadIdx.x - 64 - 128 * g;
+        const int r = quarter * 32 + lane;  // row within this CTA's 128
+        float *v0 = vec_s + g * 128, *v1 = vec_s + 256 + g * 128;        // the group's bias columns
+        float *s0 = vec_s + 512 + g * 128, *s1 = vec_s + 768 + g * 128;  // and scales
+        uint32_t res_phase = 0;
+        bool res_armed = false;  // the residual's barrier holds a phase that was not waited out
+        int i = 0;
+        for (int tile = pair; tile < p.n_tiles; tile += n_pairs, ++i) {
+            const int acc = i & 1;
+            const uint32_t acc_phase = (uint32_t)(i >> 1) & 1u;
+            int m, n, kb0, kb1, what;
+            decode(tile, m, n, kb0, kb1, what);
+            const int row0 = m * 256 + (int)rank * 128;
+            const bool live = row0 + r < p.M;
+            // columns, bias and scales of the tile, fetched under the products
+            constexpr int kCols = C::kIsUp ? 64 : KIND == kHidden ? 32 : BN / 2;  // of this group
+            const int c0 = (C::kIsUp ? n * 128 : KIND == kHidden ? n * 64 : n * BN) + g * kCols;
+            float xs = 1.f;
+            if (et == 0) store_wait_read();  // the last store has read the tile in shared memory
+            if constexpr (KIND == kDown) {
+                if (p.has_res) {
+                    res_armed = true;
+                    if (et == 0 && row0 < p.M) {
+                        const uint32_t rb = smem_u32(&res_full[g]);
+                        uint32_t bytes = 0;
+                        for (int j = 0; j < kCols / 64; ++j) bytes += c0 + j * 64 < p.E ? kBox : 0;
+                        if (bytes) {
+                            mbar_arrive_expect_tx(rb, bytes);
+                            for (int j = 0; j < kCols / 64; ++j)
+                                if (c0 + j * 64 < p.E)
+                                    tma_load_2d(smem_u32(out_s + (g * (kCols / 64) + j) * kBox), &p.res, c0 + j * 64,
+                                                row0, rb);
+                        } else {
+                            mbar_arrive(rb);
+                        }
+                    } else if (et == 0) {
+                        mbar_arrive(smem_u32(&res_full[g]));
+                    }
+                }
+            }
+            if constexpr (KIND != kDw) {
+                const int limit = KIND == kDown ? p.E : p.F;
+                if (et < kCols) {
+                    const bool in = c0 + et < limit;
+                    v0[et] = p.bias0 && in ? __bfloat162float(p.bias0[c0 + et]) : 0.f;
+                    if constexpr (KIND != kDown) v1[et] = p.bias1 && in ? __bfloat162float(p.bias1[c0 + et]) : 0.f;
+                    if constexpr (C::kQ8) {
+                        s0[et] = in ? p.gs[c0 + et] : 0.f;
+                        s1[et] = in ? p.us[c0 + et] : 0.f;
+                    }
+                }
+                if constexpr (C::kQ8) xs = live ? p.xs[row0 + r] : 0.f;
+            }
+            bool ok = mbar_wait(smem_u32(&acc_full[acc]), acc_phase, abort_flag, p.err);
+            if constexpr (KIND == kDown) {
+                if (p.has_res) {
+                    if (!ok || !mbar_wait(smem_u32(&res_full[g]), res_phase, abort_flag, p.err)) {
+                        ok = false;
+                    } else {
+                        res_armed = false;
+                        res_phase ^= 1u;
+                    }
+                }
+            }
+            // one decision for all threads that meet in this tile's barriers; the vectors are written
+            if (KIND == kHidden ? both_sync_or(!ok) : group_sync_or(g, !ok)) break;
+            tc_fence_after();
+            const uint32_t t0 = tmem_at(tmem, quarter, acc * C::kAccStride);
+            if constexpr (KIND == kDw) {
+                float *dst = p.part + ((size_t)(tile % p.splits) * 3 + what) * (size_t)p.F * p.E;
+                const int f = row0 + r;
+                const bool some = kb1 > kb0;
+                // the accumulator's rows are hidden columns here
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(t0 + (uint32_t)(g * kCols + c), v);
+                    tmem_wait();
+                    pin(v);
+                    if (f < p.F && c0 + c < p.E) {
+                        float4 *d4 = (float4 *)(dst + (size_t)f * p.E + c0 + c);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (c0 + c + 4 * q >= p.E) break;
+                            float4 o = some ? make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                                          __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (p.accumulate) {
+                                const float4 b = d4[q];
+                                o.x += b.x;
+                                o.y += b.y;
+                                o.z += b.z;
+                                o.w += b.w;
+                            }
+                            d4[q] = o;
+                        }
+                    }
+                }
+            } else if constexpr (C::kIsUp) {
+                uint8_t *sb = out_s + g * kBox;
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) {
+                    uint32_t vg[16], vu[16], w[8];
+                    tmem_ld16(t0 + (uint32_t)(g * 64 + c), vg);
+                    tmem_ld16(t0 + (uint32_t)(128 + g * 64 + c), vu);
+                    tmem_wait();
+                    pin(vg);
+                    pin(vu);
+                    float h[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a = __uint_as_float(vg[j]), b = __uint_as_float(vu[j]);
+                        if constexpr (C::kQ8) {
+                            a = fmaf(a, xs * s0[c + j], v0[c + j]);
+                            b = fmaf(b, xs * s1[c + j], v1[c + j]);
+                        } else {
+                            a += v0[c + j];
+                            b += v1[c + j];
+                        }
+                        h[j] = Act<ACT>::fast(a) * b;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = pack_bf16(h[2 * j], h[2 * j + 1]);
+                    *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            } else if constexpr (KIND == kHidden) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t vg[16], vu[16], vd[16], w[8];
+                    tmem_ld16(t0 + (uint32_t)(g * 32 + c), vg);
+                    tmem_ld16(t0 + (uint32_t)(64 + g * 32 + c), vu);
+                    tmem_ld16(t0 + (uint32_t)(128 + g * 32 + c), vd);
+                    tmem_wait();
+                    pin(vg);
+                    pin(vu);
+                    pin(vd);
+                    float h[16], dg[16], du[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = __uint_as_float(vg[j]) + v0[c + j], b = __uint_as_float(vu[j]) + v1[c + j];
+                        const float dh = __uint_as_float(vd[j]);
+                        float slope;
+                        const float act = Act<ACT>::fast(a, &slope);
+                        h[j] = act * b;
+                        du[j] = dh * act;
+                        dg[j] = dh * b * slope;
+                    }
+                    const int u = (g * 32 + c) / 8;
+#pragma unroll
+                    for (int o = 0; o < 3; ++o) {
+                        const float *src = o == 0 ? h : o == 1 ? dg : du;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[j] = pack_bf16(src[2 * j], src[2 * j + 1]);
+                        uint8_t *sb = out_s + o * kBox;
+                        *reinterpret_cast<uint4 *>(sb + swizzled(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(sb + swizzled(r, u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+            } else {
+                uint8_t *sb0 = out_s + g * (kCols / 64) * kBox;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t v[16], w[8];
+                    tmem_ld16(t0 + (uint32_t)(g * kCols + c), v);
+                    tmem_wait();
+                    pin(v);
+                    uint8_t *sb = sb0 + (c / 64) * kBox;
+                    uint4 *p0 = reinterpret_cast<uint4 *>(sb + swizzled(r, (c % 64) / 8));
+                    uint4 *p1 = reinterpret_cast<uint4 *>(sb + swizzled(r, (c % 64) / 8 + 1));
+                    uint32_t rw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (p.has_res) {
+                        const uint4 a = *p0, b = *p1;
+                        rw[0] = a.x, rw[1] = a.y, rw[2] = a.z, rw[3] = a.w;
+                        rw[4] = b.x, rw[5] = b.y, rw[6] = b.z, rw[7] = b.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 e = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&rw[j]));
+                        w[j] = pack_bf16(__uint_as_float(v[2 * j]) + v0[c + 2 * j] + e.x,
+                                         __uint_as_float(v[2 * j + 1]) + v0[c + 2 * j + 1] + e.y);
+                    }
+                    *p0 = make_uint4(w[0], w[1], w[2], w[3]);
+                    *p1 = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+            // the accumulator is read: back to the issuer, once per group and CTA
+            tc_fence_before();
+            if constexpr (KIND != kDw) fence_async_shared();
+            group_sync(g);
+            if (et == 0) {
+                mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
+                if (row0 < p.M) {
+                    if constexpr (C::kIsUp) {
+                        if (c0 < p.F) tma_store_tile(&p.o0, smem_u32(out_s + g * kBox), c0, row0);
+                    } else if constexpr (KIND == kDown) {
+                        for (int j = 0; j < kCols / 64; ++j)
+                            if (c0 + j * 64 < p.E)
+                                tma_store_tile(&p.o0, smem_u32(out_s + (g * (kCols / 64) + j) * kBox), c0 + j * 64,
+                                               row0);
+                    }
+                }
+                if constexpr (C::kIsUp || KIND == kDown) store_commit();
+            }
+            if constexpr (KIND == kHidden) {
+                // both groups have written their halves of the three tiles
+                both_sync();
+                if (g == 0 && et == 0) {
+                    if (row0 < p.M) {
+                        tma_store_tile(&p.o0, smem_u32(out_s), n * 64, row0);
+                        tma_store_tile(&p.o1, smem_u32(out_s + kBox), n * 64, row0);
+                        tma_store_tile(&p.o2, smem_u32(out_s + 2 * kBox), n * 64, row0);
+                    }
+                    store_commit();
+                    store_wait_read();
+                }
+                both_sync();
+            }
+        }
+        if (et == 0) {
+            store_wait_all();  // shared memory outlives its stores, and the residual's copies
+            if (res_armed) {  // left early: the armed copy lands, or was counted without bytes
+                int dummy = 0;
+                mbar_wait(smem_u32(&res_full[g]), res_phase, (volatile int *)&dummy, p.err);
+            }
+        }
+    }
+
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // every product has run before either CTA frees what it reads; after an
+        // expired wait, let the copies this CTA counted land first
+        int dummy = 0;
+        mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
+        if (*abort_flag && rank == 0)
+            for (int s = 0; s < kStages; ++s)
+                if (issued[s] > 0)
+                    mbar_wait(smem_u32(&full[s]), (uint32_t)((issued[s] - 1) & 1), (volatile int *)&dummy, p.err);
+    }
+    __syncthreads();
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free_pair(tmem, C::kTmemCols);
+}
+
+// ---------------------------------------------------------------- host side
+
+// Pairs that run at once on the current device for this kernel.
+template <typename K>
+pmha_status configure(K kern, int smem, int *pairs)
+{
+    static std::mutex mu;
+    static std::map<std::pair<int, void *>, int> known;
+    int dev = 0;
+    PMHA_CUDA_TRY(cudaGetDevice(&dev));
+    std::lock_guard<std::mutex> lk(mu);
+    const auto it = known.find({dev, (void *)kern});
+    if (it != known.end()) {
+        *pairs = it->second;
+        return PMHA_OK;
+    }
+    PMHA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    PMHA_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
+    n = std::max(1, std::min(n, num_sms() / 2));
+    known[{dev, (void *)kern}] = n;
+    *pairs = n;
+    return PMHA_OK;
+}
+
+template <int KIND, int BN, int ACT>
+pmha_status launch(Params &p, const char *stage, cudaStream_t s)
+{
+    using C = Cfg<KIND, BN>;
+    p.err = device_error_word();
+    if (!p.err) return PMHA_ERR_CUDA;
+    int pairs = 0;
+    auto kern = k_ffn<KIND, BN, ACT>;
+    const pmha_status st = configure(kern, C::kSmem, &pairs);
+    if (st != PMHA_OK) return st;
+    const int grid = 2 * std::min(pairs, p.n_tiles);
+    StageTimer timer(stage, s);
+    kern<<<grid, kThreads, C::kSmem, s>>>(p);
+    count_launch();
+    PMHA_CUDA_TRY(cudaGetLastError());
+    return PMHA_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+pmha_status map_failed(const char *what)
+{
+    set_error("%s: cuTensorMapEncodeTiled failed", what);
+    return PMHA_ERR_CUDA;
+}
+
+pmha_status too_large(const char *what, int64_t tiles)
+{
+    set_error("%s: %lld tiles exceed the 32-bit tile index", what, (long long)tiles);
+    return PMHA_ERR_INVALID_ARG;
+}
+
+// 256 outputs a tile where there are that many; else 128 (less waste)
+bool wide_tiles(int64_t n) { return n % 256 == 0 || n > 512; }
+
+pmha_status down_like(const FfnTc &f, const void *a0, const void *a1, const void *b0, const void *b1, const void *bias,
+                      const void *residual, int64_t M, void *out, const char *stage, cudaStream_t s)
+{
+    Params p = {};
+    const bool wide = wide_tiles(f.E);
+    const int bn = wide ? 256 : 128;
+    p.M = (int)M, p.E = (int)f.E, p.F = (int)f.F;
+    p.tiles_n = (int)ceil_div(f.E, bn);
+    const int64_t tiles = ceil_div(M, 256) * p.tiles_n;
+    if (tiles > 0x3fffffff) return too_large(stage, tiles);
+    p.n_tiles = (int)tiles;
+    p.kb = (int)ceil_div(f.F, 64);
+    p.segs = a1 ? 2 : 1;
+    p.bias0 = (const __nv_bfloat16 *)bias;
+    p.has_res = residual != nullptr;
+    bool ok = make_tile_map(&p.a0, a0, M, f.F, f.F, 2, 128) && make_tile_map(&p.b0, b0, f.E, f.F, f.F, 2, bn / 2) &&
+              make_tile_map(&p.o0, out, M, f.E, f.E, 2, 128);
+    if (a1) ok = ok && make_tile_map(&p.a1, a1, M, f.F, f.F, 2, 128) && make_tile_map(&p.b1, b1, f.E, f.F, f.F, 2, bn / 2);
+    if (residual) ok = ok && make_tile_map(&p.res, residual, M, f.E, f.E, 2, 128);
+    if (!ok) return map_failed(stage);
+    return wide ? launch<kDown, 256, 0>(p, stage, s) : launch<kDown, 128, 0>(p, stage, s);
+}
+
+}  // namespace
+
+pmha_status ffn_tc_up(const FfnTc &f, const FfnUpArgs &a, cudaStream_t s)
+{
+    Params p = {};
+    const bool q8 = a.x_scale != nullptr;
+    p.M = (int)a.M, p.E = (int)f.E, p.F = (int)f.F;
+    p.tiles_n = (int)ceil_div(f.F, 128);
+    const int64_t tiles = ceil_div(a.M, 256) * p.tiles_n;
+    if (tiles > 0x3fffffff) return too_large("ffn_up", tiles);
+    p.n_tiles = (int)tiles;
+    p.kb = (int)ceil_div(f.E, q8 ? 128 : 64);
+    p.bias0 = (const __nv_bfloat16 *)f.bg;
+    p.bias1 = (const __nv_bfloat16 *)f.bu;
+    p.xs = a.x_scale, p.gs = a.wg_scale, p.us = a.wu_scale;
+    const int es = q8 ? 1 : 2;
+    if (!make_tile_map(&p.a0, a.x, a.M, f.E, f.E, es, 128) || !make_tile_map(&p.b0, a.wg, f.F, f.E, f.E, es, 128) ||
+        !make_tile_map(&p.b1, a.wu, f.F, f.E, f.E, es, 128) || !make_tile_map(&p.o0, a.h, a.M, f.F, f.F, 2, 128))
+        return map_failed("ffn_up");
+    if (q8)
+        return f.act == PMHA_ACT_SILU ? launch<kUpQ8, 128, PMHA_ACT_SILU>(p, "ffn_up_quantized", s)
+                                      : launch<kUpQ8, 128, PMHA_ACT_GELU>(p, "ffn_up_quantized", s);
+    return f.act == PMHA_ACT_SILU ? launch<kUp, 128, PMHA_ACT_SILU>(p, "ffn_up", s)
+                                  : launch<kUp, 128, PMHA_ACT_GELU>(p, "ffn_up", s);
+}
+
+pmha_status ffn_tc_down(const FfnTc &f, const void *h, const void *wd, const void *residual, int64_t M, void *out,
+                        cudaStream_t s)
+{
+    return down_like(f, h, nullptr, wd, nullptr, f.bd, residual, M, out, "ffn_down", s);
+}
+
+pmha_status ffn_tc_dx(const FfnTc &f, const void *dg, const void *du, const void *wg_t, const void *wu_t, int64_t M,
+                      void *dx, cudaStream_t s)
+{
+    return down_like(f, dg, du, wg_t, wu_t, nullptr, nullptr, M, dx, "ffn_dx", s);
+}
+
+pmha_status ffn_tc_hidden(const FfnTc &f, const FfnHiddenArgs &a, cudaStream_t s)
+{
+    Params p = {};
+    p.M = (int)a.M, p.E = (int)f.E, p.F = (int)f.F;
+    p.tiles_n = (int)ceil_div(f.F, 64);
+    const int64_t tiles = ceil_div(a.M, 256) * p.tiles_n;
+    if (tiles > 0x3fffffff) return too_large("ffn_hidden", tiles);
+    p.n_tiles = (int)tiles;
+    p.kb = (int)ceil_div(f.E, 64);
+    p.bias0 = (const __nv_bfloat16 *)f.bg;
+    p.bias1 = (const __nv_bfloat16 *)f.bu;
+    if (!make_tile_map(&p.a0, a.x, a.M, f.E, f.E, 2, 128) || !make_tile_map(&p.a1, a.dy, a.M, f.E, f.E, 2, 128) ||
+        !make_tile_map(&p.b0, a.wg, f.F, f.E, f.E, 2, 64) || !make_tile_map(&p.b1, a.wu, f.F, f.E, f.E, 2, 64) ||
+        !make_tile_map(&p.b2, a.wd_t, f.F, f.E, f.E, 2, 32) || !make_tile_map(&p.o0, a.h, a.M, f.F, f.F, 2, 128) ||
+        !make_tile_map(&p.o1, a.dg, a.M, f.F, f.F, 2, 128) || !make_tile_map(&p.o2, a.du, a.M, f.F, f.F, 2, 128))
+        return map_failed("ffn_hidden");
+    return f.act == PMHA_ACT_SILU ? launch<kHidden, 64, PMHA_ACT_SILU>(p, "ffn_hidden", s)
+                                  : launch<kHidden, 64, PMHA_ACT_GELU>(p, "ffn_hidden", s);
+}
+
+int ffn_dw_splits(int64_t E, int64_t F, int64_t rows)
+{
+    // as many pieces of the row range as fill the pairs, each of at least 4 blocks of 64 rows
+    const int64_t tiles = 3 * ceil_div(F, 256) * ceil_div(E, wide_tiles(E) ? 256 : 128);
+    const int64_t pairs = num_sms() / 2;
+    return (int)std::max<int64_t>(1, std::min(pairs / tiles, ceil_div(rows, 256)));
+}
+
+pmha_status ffn_tc_dw(const FfnTc &f, const FfnDwArgs &a, cudaStream_t s)
+{
+    Params p = {};
+    const bool wide = wide_tiles(f.E);
+    p.M = (int)f.F;  // rows of the result
+    p.E = (int)f.E, p.F = (int)f.F;
+    p.tiles_m = (int)ceil_div(f.F, 256);
+    p.tiles_n = (int)ceil_div(f.E, wide ? 256 : 128);
+    p.splits = a.splits;
+    p.first_what = a.gate_up ? 0 : 2;
+    const int n_what = (a.gate_up ? 2 : 0) + (a.down ? 1 : 0);
+    if (!n_what) return PMHA_OK;
+    const int64_t tiles = (int64_t)n_what * p.tiles_m * p.tiles_n * p.splits;
+    if (tiles > 0x3fffffff) return too_large("ffn_dw", tiles);
+    p.n_tiles = (int)tiles;
+    p.kb = (int)ceil_div(a.M, 64);
+    p.kb_per = (int)ceil_div(p.kb, p.splits);
+    p.part = a.part;
+    p.accumulate = a.accumulate;
+    if (!make_tile_map(&p.a0, a.dg, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.a1, a.du, a.M, f.F, f.F, 2, 64) ||
+        !make_tile_map(&p.a2, a.h, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.b0, a.x, a.M, f.E, f.E, 2, 64) ||
+        !make_tile_map(&p.b1, a.dy, a.M, f.E, f.E, 2, 64))
+        return map_failed("ffn_dw");
+    return wide ? launch<kDw, 256, 0>(p, "ffn_dw", s) : launch<kDw, 128, 0>(p, "ffn_dw", s);
+}
+
+}  // namespace pmha

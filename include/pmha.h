@@ -315,6 +315,161 @@ pmha_status pmha_backward(const pmha_graph *graph, const pmha_params *params, co
 pmha_status pmha_graph_export_by_source(const pmha_graph *graph, int32_t *src_row_ptr, int32_t *target,
                                         pmha_stream stream);
 
+/* ------------------------------------------------------------------------
+ * The encoder around the layer (kpnn2 leaves it to the user: "norm, residual,
+ * FFN"): root-mean-square norm with the residual's addition, gated
+ * feed-forward block, and clipping of all gradients by their global norm.
+ * Tokens are `rows` rows of one width, dense row-major: a (B, L, E) tensor is
+ * B * L rows. rows may be 0: such a call writes no rows, and zeros to its
+ * parameter gradients. Unless a call says otherwise its outputs overlap
+ * neither its inputs nor one another (PMHA_ERR_INVALID_ARG).
+ */
+
+/*
+ * pmha_rms_norm - out = s / sqrt(mean(s^2) + eps) * weight for each row, where
+ * s = x + residual, rounded to `dtype` (the sum as it is kept), or x itself
+ * without a residual.
+ *  x, residual  device (rows, width) in dtype; residual NULL: no addition.
+ *  weight  device (width) in dtype, or NULL for ones.
+ *  eps     finite, at least 1e-30.
+ *  sum     device (rows, width) in dtype: receives s; NULL: not kept.
+ *  out     device (rows, width) in dtype, or NULL when out_q is given.
+ *  out_q, scale  both or neither: device (rows, width) bytes in the 8-bit
+ *          float format E4M3 and device (rows) float32. A row's scale is
+ *          max|y| / 448, at least 2^-64, with y the row of the norm in exact
+ *          arithmetic, and out_q is y / scale rounded to the nearest E4M3
+ *          value (ties to even): y ~ out_q * scale. The values are those of
+ *          the formula in exact arithmetic (scale and eps rounded to
+ *          float32), whatever the order of its sums, for rows whose
+ *          squares are not below float32's normal numbers. A row with an
+ *          infinity or a NaN gets a NaN scale and NaN bytes.
+ * Statistics are float32; a row whose squares leave float32 is scaled first. Asynchronous; needs no workspace.
+ * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_CUDA.
+ */
+pmha_status pmha_rms_norm(pmha_dtype dtype, int64_t rows, int64_t width, const void *x, const void *residual,
+                          const void *weight, float eps, void *sum, void *out, void *out_q, float *scale,
+                          pmha_stream stream);
+
+/*
+ * pmha_rms_norm_backward - gradients of pmha_rms_norm's `out` for the row
+ * that was normalised:
+ *  x     device (rows, width): the kept sum (or x without a residual).
+ *  dout  device (rows, width), dLoss/d(out).
+ *  dsum  device (rows, width) or NULL: dLoss/d(sum) from its other uses (the
+ *        residual stream), added to dx.
+ *  dx    device (rows, width) or NULL: the gradient of x, and of the residual.
+ *  dweight  device float32 (width) or NULL: summed over the rows in a fixed
+ *        order (deterministic).
+ *  workspace  pmha_rms_norm_backward_workspace_size() bytes, 256-byte aligned
+ *        (0 when the arguments are invalid).
+ * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
+ */
+size_t pmha_rms_norm_backward_workspace_size(pmha_dtype dtype, int64_t rows, int64_t width);
+pmha_status pmha_rms_norm_backward(pmha_dtype dtype, int64_t rows, int64_t width, const void *x, const void *weight,
+                                   float eps, const void *dout, const void *dsum, void *dx, float *dweight,
+                                   void *workspace, size_t workspace_bytes, pmha_stream stream);
+
+/* Activation of the gate: g * sigmoid(g), or g * Phi(g) with Phi the normal
+ * distribution function (the erf form of GELU). */
+typedef enum { PMHA_ACT_SILU = 0, PMHA_ACT_GELU = 1 } pmha_act;
+
+/* A gated feed-forward block y = (act(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd,
+ * weights stored (out, in) like nn.Linear. Device pointers in `dtype`;
+ * weights 16-byte aligned, biases to their elements; NULL bias: none. */
+typedef struct {
+    int64_t embed_dim;       /* E >= 1 */
+    int64_t hidden_dim;      /* F >= 1 */
+    pmha_dtype dtype;
+    pmha_act act;
+    const void *wg, *wu;     /* (F, E) */
+    const void *wd;          /* (E, F) */
+    const void *bg, *bu;     /* (F) or NULL */
+    const void *bd;          /* (E) or NULL */
+} pmha_ffn_params;
+
+/*
+ * pmha_ffn_forward - out = block(x) (+ residual) for `rows` tokens.
+ *  x, residual  device (rows, E); residual NULL: none.
+ *  out          device (rows, E).
+ *  workspace    pmha_ffn_forward_workspace_size() bytes, 256-byte aligned
+ *               (0 bytes, and workspace may be NULL, for some sizes; the
+ *               size function returns SIZE_MAX for invalid arguments).
+ * Sums are float32. A bf16 block rounds the hidden row act(.) * (.) to bf16
+ * between its products, a float32 block keeps float32.
+ * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
+ */
+size_t pmha_ffn_forward_workspace_size(const pmha_ffn_params *params, int64_t rows);
+pmha_status pmha_ffn_forward(const pmha_ffn_params *params, const void *x, const void *residual, int64_t rows,
+                             void *out, void *workspace, size_t workspace_bytes, pmha_stream stream);
+
+/* Gate and up weights of a block in E4M3 with one float32 scale for each
+ * output row: W ~ w * scale[:, None] (the form in which a served model
+ * keeps them). */
+typedef struct {
+    const void *wg, *wu;             /* (F, E) E4M3 bytes, 16-byte aligned */
+    const float *wg_scale, *wu_scale; /* (F) */
+} pmha_ffn_quantized;
+
+/*
+ * pmha_ffn_forward_quantized - pmha_ffn_forward for tokens in E4M3 with a scale
+ * each (pmha_rms_norm's out_q and scale) and E4M3 gate and up weights; the
+ * down product, biases, residual and out are bf16 (params->dtype must be
+ * PMHA_BF16; params->wg and wu are not read). Needs E a multiple of 16 and F
+ * a multiple of 8 (PMHA_ERR_UNSUPPORTED otherwise, SIZE_MAX from the size
+ * function).
+ */
+size_t pmha_ffn_forward_quantized_workspace_size(const pmha_ffn_params *params, int64_t rows);
+pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha_ffn_quantized *quantized,
+                                       const void *x, const float *x_scale, const void *residual, int64_t rows,
+                                       void *out, void *workspace, size_t workspace_bytes, pmha_stream stream);
+
+/*
+ * pmha_ffn_backward - gradients of block(x) for dout = dLoss/d(block(x)); the
+ * residual's gradient is dout itself. Recomputes the hidden rows from x.
+ *  dx      device (rows, E) in dtype, or NULL.
+ *  grads   parameter gradients in dtype, any member NULL to skip it, NULL
+ *          skips all; written, not accumulated. The sums are float32, in a
+ *          fixed order (deterministic), and rounded to dtype once: a bf16
+ *          block's products take the hidden gradients rounded to bf16, so
+ *          float32 results would carry no more.
+ *  workspace  pmha_ffn_backward_workspace_size() bytes, 256-byte aligned
+ *          (SIZE_MAX when the arguments are invalid). Its size does not grow
+ *          with rows past some tens of MB: rows are taken in blocks whose
+ *          hidden gradients stay in L2.
+ * Errors as pmha_ffn_forward.
+ */
+typedef struct {
+    void *wg, *wu, *wd;
+    void *bg, *bu, *bd;
+} pmha_ffn_grads;
+size_t pmha_ffn_backward_workspace_size(const pmha_ffn_params *params, int64_t rows);
+pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, const void *dout, int64_t rows, void *dx,
+                              const pmha_ffn_grads *grads, void *workspace, size_t workspace_bytes,
+                              pmha_stream stream);
+
+/*
+ * pmha_clip_grad_norm - the 2-norm of all values of n_tensors gradient tensors
+ * and the tensors scaled by min(1, max_norm / (norm + 1e-6)).
+ *  grads, out, numel, dtype  HOST arrays of n_tensors entries, read during
+ *        the call: device pointers (aligned to their elements), numbers of
+ *        values (0 allowed) and types. out[i] == grads[i] scales in place;
+ *        otherwise out[i] must not overlap any gradient, nor another output,
+ *        and the gradients are left as they were. out NULL: all in place. A
+ *        tensor given twice is refused.
+ *  max_norm  finite and >= 0.
+ *  norm  device float32: receives the norm before scaling.
+ *  workspace  pmha_clip_grad_norm_workspace_size() bytes, 256-byte aligned.
+ * Squares of any size count: the sum neither overflows nor underflows for
+ * finite gradients whose norm float32 holds. With an infinite gradient the
+ * factor is 0 (the infinite values become NaN), with a NaN every value
+ * becomes NaN; the norm tells. The sums' order is fixed (deterministic).
+ * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
+ */
+size_t pmha_clip_grad_norm_workspace_size(int64_t n_tensors);
+pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, void *const *out, const int64_t *numel,
+                                const pmha_dtype *dtype, float max_norm, float *norm, void *workspace,
+                                size_t workspace_bytes, pmha_stream stream);
+
 /* Message describing the last failure of a call made by this thread ("" if none). */
 const char *pmha_last_error(void);
 
