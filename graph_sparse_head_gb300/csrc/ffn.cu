@@ -19,7 +19,9 @@
 namespace pmha {
 namespace {
 
-constexpr int64_t kL2Block = 48 << 20;  // bytes of hidden values (h, or h, dg and du) of a block of rows
+constexpr int64_t kL2Block = 64 << 20;  // bytes of hidden values (h, or h, dg and du) of a block of rows
+constexpr int64_t kMostBlock = 256 << 20;
+constexpr int64_t kFusedRows = 2048;    // rows from which the forward pass runs as one kernel
 constexpr int kSumParts = 32;           // row ranges of the bias sums
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
@@ -348,7 +350,7 @@ pmha_status check_workspace(const char *who, const void *ws, size_t got, size_t 
 // products (multiples of 8 for bf16; copies are made where that differs).
 struct Plan {
     int64_t E2, F2, R;
-    bool padded;
+    bool padded, fused;
     size_t wg, wu, wd, bg, bu, bd;  // padded copies
     size_t x, dy, out;              // padded rows of a block (dy: dy or the residual)
     size_t wgt, wut, wdt;           // transposed weights (backward)
@@ -371,8 +373,15 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward)
     l.E2 = bf16 ? round8(p->embed_dim) : p->embed_dim;
     l.F2 = bf16 ? round8(p->hidden_dim) : p->hidden_dim;
     l.padded = l.E2 != p->embed_dim || l.F2 != p->hidden_dim;
+    l.fused = bf16 && ffn_fused_supported(l.E2, l.F2) && (backward || rows >= kFusedRows);
     const int64_t per_row = l.F2 * (int64_t)es * (backward ? 3 : 1);
+    // a block of rows fills the pairs of SMs a whole number of times where L2 holds that many, else
+    // once where that is not too much memory
+    const int64_t wave = 256 * (int64_t)(num_sms() / 2);
     l.R = std::max<int64_t>(256, kL2Block / per_row / 256 * 256);
+    if (l.R >= wave) l.R = l.R / wave * wave;
+    else if (l.fused && wave * per_row <= kMostBlock) l.R = wave;
+    if (l.fused && !backward && !l.padded) l.R = rows;
     l.R = std::min(l.R, ceil_div(std::max<int64_t>(rows, 1), 256) * 256);
     size_t o = 0;
     auto take = [&](int64_t n) {
@@ -385,7 +394,7 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward)
         l.bg = take(l.F2), l.bu = take(l.F2), l.bd = take(l.E2);
         l.x = take(l.R * l.E2), l.dy = take(l.R * l.E2), l.out = take(l.R * l.E2);
     }
-    l.h = take(l.R * l.F2);
+    if (backward || !l.fused) l.h = take(l.R * l.F2);
     if (backward) {
         l.dg = take(l.R * l.F2), l.du = take(l.R * l.F2);
         if (bf16) l.wgt = take(l.E2 * l.F2), l.wut = take(l.E2 * l.F2), l.wdt = take(l.E2 * l.F2);
@@ -529,8 +538,12 @@ pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_qu
         if (q8) up.x_scale = x_scale + r, up.wg_scale = q8->wg_scale, up.wu_scale = q8->wu_scale;
         up.M = M;
         up.h = ws + l.h;
-        PMHA_TRY(ffn_tc_up(tc, up, s));
-        PMHA_TRY(ffn_tc_down(tc, ws + l.h, q.wd, rp, M, yp, s));
+        if (l.fused) {
+            PMHA_TRY(ffn_fused_forward(tc, up, q.wd, rp, yp, s));
+        } else {
+            PMHA_TRY(ffn_tc_up(tc, up, s));
+            PMHA_TRY(ffn_tc_down(tc, ws + l.h, q.wd, rp, M, yp, s));
+        }
         if (l.padded) PMHA_TRY(repitch(ws + l.out, M, l.E2, M, E, yr, s));
     }
     return PMHA_OK;
@@ -672,9 +685,12 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 xp = ws + l.x, dyp = ws + l.dy;
             }
             FfnHiddenArgs hid = {xp, dyp, q.wg, q.wu, ws + l.wdt, M, ws + l.h, ws + l.dg, ws + l.du};
-            PMHA_TRY(ffn_tc_hidden(tc, hid, s));
+            void *dxp = !dx ? nullptr : l.padded ? ws + l.out : dxr;
+            if (l.fused) PMHA_TRY(ffn_fused_backward(tc, hid, ws + l.wgt, ws + l.wut, dxp, s));
+            else PMHA_TRY(ffn_tc_hidden(tc, hid, s));
             if (dx) {
-                PMHA_TRY(ffn_tc_dx(tc, ws + l.dg, ws + l.du, ws + l.wgt, ws + l.wut, M, l.padded ? ws + l.out : dxr, s));
+                if (!l.fused || !ffn_fused_dx(l.E2))
+                    PMHA_TRY(ffn_tc_dx(tc, ws + l.dg, ws + l.du, ws + l.wgt, ws + l.wut, M, dxp, s));
                 if (l.padded) PMHA_TRY(repitch(ws + l.out, M, l.E2, M, E, dxr, s));
             }
             if (any_w) {

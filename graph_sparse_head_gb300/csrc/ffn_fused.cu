@@ -1,0 +1,656 @@
+// The gated block with its hidden rows kept on the chip (sm_103a), for
+// embed_dim up to 256. A pair of CTAs (tc_pair.cuh) owns 256 rows, 128 a CTA:
+// its tokens stay in shared memory while the hidden width passes in chunks of
+// 64 columns, whose weights stream through two rings of TMA stages.
+//
+//   forward, chunk c:   S = x [Wg_c | Wu_c]^T           tensor memory, two buffers
+//                       h = act(S_g + bg) * (S_u + bu)   -> shared memory, bf16
+//                       Y += h Wd_c^T                    tensor memory
+//   after the last:     y = Y + bd + residual
+//
+//   backward, chunk c:  S as above, D = dy Wd_c
+//                       h, dg, du -> global memory (the weight gradients read them)
+//                       X += dg Wg_c + du Wu_c           (embed_dim up to 128)
+//   after the last:     dx = X
+//
+// The hidden values never go to memory in the forward pass, and the tokens are
+// read once; what bounds it is the tensor pipe and, near it, the epilogue's
+// arithmetic (two special-function results for each hidden value). So the
+// warps are specialised: warp 0 copies, warp 1 of the even CTA issues the
+// products, two groups of four warps take the chunks in turn (each has two
+// chunks' time, so that one group's tensor-memory reads and barriers run under
+// the other's arithmetic), and a fourth group drains the row block's result
+// while the next block's chunks go on. The issuer runs S two chunks ahead:
+// S(0) S(1) | Y(0) S(2) | Y(1) S(3) ... across row blocks.
+//
+// Every wait is bounded; after an expired one the waits return at once, the
+// loops run out, and pmha_device_status reports PMHA_ERR_TIMEOUT.
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "ffn_internal.h"
+#include "ffn_math.cuh"
+#include "tc_pair.cuh"
+
+namespace pmha {
+namespace {
+using namespace tcu;
+
+constexpr int kThreads = 448;       // 2 + 4 + 4 + 4 warps
+constexpr int kBox = 128 * 128;     // 128 rows of 128 bytes
+constexpr int kMaxHidden = 4096;    // bias (and scale) columns held in shared memory
+constexpr int kSmemMost = 232448;
+
+// EB: blocks of 64 output columns; KB: blocks of 128 bytes of a token.
+template <int EB, bool BWD, bool Q8>
+struct Cfg {
+    static constexpr int KB = Q8 ? (EB + 1) / 2 : EB;
+    static constexpr bool kOut = !BWD || EB <= 2;               // the kernel forms y, or dx
+    static constexpr int kX = (BWD ? 2 : 1) * KB * kBox;        // x (and dy) of a row block
+    static constexpr int kSSlot = BWD ? 12288 : 8192;           // 64 rows of Wg or Wu (and 32 of Wd^T), one K block
+    static constexpr int kYSlot = kOut ? EB * (BWD ? 8192 : 4096) : 0;  // half of the output columns of a chunk
+    static constexpr int kStaged = kOut ? (BWD ? 2 : 1) * kBox : 0;     // h, or dg and du
+    static constexpr int kSCols = BWD ? 192 : 128;
+    static constexpr int kNY = kOut ? (BWD ? 2 : 3) : 0;
+    static constexpr int kVec = 2048 * 8 + 1024;                // biases of 4096 columns, output bias
+    static constexpr int kScales = Q8 ? kMaxHidden * 8 : 0;
+    static constexpr int kBars = 512;
+    static constexpr int kFixed = 1024 + kNY * kYSlot + 2 * kStaged + kVec + kScales + kBars;
+    static constexpr int kXB = kFixed + 2 * kX + 2 * KB * kSSlot <= kSmemMost ? 2 : 1;  // token buffers
+    static constexpr int kNSFit = (kSmemMost - kFixed - kXB * kX) / kSSlot;
+    static constexpr int kNS = kNSFit > 8 ? 8 : kNSFit;
+    static constexpr int kOB = 2 * kSCols + 2 * EB * 64 <= 512 ? 2 : 1;  // output accumulators
+    static constexpr int kSmem = kFixed + kXB * kX + kNS * kSSlot;
+    static_assert(kNS >= KB, "a chunk's weights fit in the ring");
+    static_assert(!kOut || 2 * kSCols + kOB * EB * 64 <= 512, "tensor memory");
+};
+
+struct Params {
+    CUtensorMap x, dy, wg, wu, wd;  // wd: Wd (E, F), or Wd^T (F, E) in the backward pass
+    CUtensorMap wgt, wut;           // (E, F): Wg^T, Wu^T
+    int M, E, F;
+    int items, parts;               // row blocks x parts of the hidden width
+    int chunks, per_part;           // chunks of 64 hidden columns, and of one part
+    const __nv_bfloat16 *bg, *bu, *bd, *res;
+    const float *xs, *gs, *us;
+    __nv_bfloat16 *out, *h, *dg, *du;
+    int wide_e, wide_f;             // rows of out and residual / of h, dg, du allow 32-byte accesses
+    int *err;
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's tensor-memory reads; the values' uses stay behind it.
+template <typename... R>
+__device__ __forceinline__ void tmem_wait(R &...regs)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    auto pin = [](uint32_t(&r)[16]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+    };
+    (pin(regs), ...);
+}
+
+// 16 bf16 values of a row: one 32-byte access where the rows allow it, else two
+// of 16 bytes, each only if its 8 columns exist.
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const uint32_t (&w)[8], int left, bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        if (left > 0) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (left > 8) *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, uint32_t (&w)[8], int left, bool wide)
+{
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (left > 0) a = *reinterpret_cast<const uint4 *>(p);
+        if (left > 8) b = *reinterpret_cast<const uint4 *>(p + 8);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+}
+
+template <int EB, bool BWD, bool Q8, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block(const __grid_constant__ Params p)
+{
+    using C = Cfg<EB, BWD, Q8>;
+    constexpr int KB = C::KB, NS = C::kNS, NY = C::kNY > 0 ? C::kNY : 1, XB = C::kXB, OB = C::kOB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *x_s = smem;                              // [XB][x blocks, dy blocks]
+    uint8_t *s_ring = x_s + XB * C::kX;               // [NS]
+    uint8_t *y_ring = s_ring + NS * C::kSSlot;        // [kNY]
+    uint8_t *staged = y_ring + C::kNY * C::kYSlot;    // [2]
+    uint32_t *bias_s = (uint32_t *)(staged + 2 * C::kStaged);  // (bg, bu) bf16 pairs
+    float *bd_s = (float *)((uint8_t *)bias_s + kMaxHidden * 4);
+    float2 *scale_s = (float2 *)((uint8_t *)bias_s + C::kVec);
+    uint64_t *bar = (uint64_t *)((uint8_t *)scale_s + C::kScales);
+    uint64_t *x_full = bar, *x_empty = x_full + 2, *s_full = x_empty + 2, *s_empty = s_full + 8, *y_full = s_empty + 8,
+             *y_empty = y_full + 4, *acc_full = y_empty + 4, *h_full = acc_full + 2, *h_empty = h_full + 2,
+             *out_full = h_empty + 2, *out_empty = out_full + 2, *mma_done = out_empty + 2;
+    uint32_t *tmem_holder = (uint32_t *)(mma_done + 1);
+    volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
+    volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted: x, S slots, Y slots
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&x_full[i]), 1);
+            mbar_init(smem_u32(&x_empty[i]), 1);
+            mbar_init(smem_u32(&acc_full[i]), 1);
+            mbar_init(smem_u32(&h_full[i]), 2);  // the group in either CTA
+            mbar_init(smem_u32(&h_empty[i]), 1);
+            mbar_init(smem_u32(&out_full[i]), 1);
+            mbar_init(smem_u32(&out_empty[i]), 2);
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(smem_u32(&s_full[i]), 1);
+            mbar_init(smem_u32(&s_empty[i]), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&y_full[i]), 1);
+            mbar_init(smem_u32(&y_empty[i]), 1);
+        }
+        mbar_init(smem_u32(mma_done), 1);
+        *abort_flag = 0;
+        armed[0] = armed[1] = armed[2] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
+    for (int i = threadIdx.x; i < p.chunks * 64; i += kThreads) {
+        const bool in = i < p.F;
+        const float g = in && p.bg ? __bfloat162float(p.bg[i]) : 0.f, u = in && p.bu ? __bfloat162float(p.bu[i]) : 0.f;
+        bias_s[i] = pack_bf16(g, u);
+        if constexpr (Q8) scale_s[i] = in ? make_float2(p.gs[i], p.us[i]) : make_float2(0.f, 0.f);
+    }
+    for (int i = threadIdx.x; i < EB * 64; i += kThreads) bd_s[i] = p.bd && i < p.E ? __bfloat162float(p.bd[i]) : 0.f;
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    // item -> row block, first chunk; every item has the chunks of one part (the last part may have fewer)
+    auto chunks_of = [&](int item) { return min(p.per_part, p.chunks - (item % p.parts) * p.per_part); };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer of this CTA, in the issuer's order
+            uint32_t ns = 0, ny = 0, nx = 0;  // copies made into each ring
+            auto load_s = [&](int f0) {
+                for (int j = 0; j < KB; ++j, ++ns) {
+                    const int slot = (int)(ns % NS);
+                    if (!mbar_wait(smem_u32(&s_empty[slot]), ((ns / NS) & 1u) ^ 1u, abort_flag, p.err)) return;
+                    const uint32_t fb = map_rank(smem_u32(&s_full[slot]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s_full[slot]), 2 * C::kSSlot);
+                    armed[1] = ns + 1;
+                    const uint32_t a = smem_u32(s_ring + slot * C::kSSlot);
+                    const int k = j * (Q8 ? 128 : 64);
+                    tma_load_2d_pair(a, rank ? &p.wu : &p.wg, k, f0, fb);
+                    if constexpr (BWD) tma_load_2d_pair(a + 8192, &p.wd, k, f0 + (int)rank * 32, fb);
+                }
+            };
+            auto load_y = [&](int f0) {
+                const int slot = (int)(ny % NY);
+                if (!mbar_wait(smem_u32(&y_empty[slot]), ((ny / NY) & 1u) ^ 1u, abort_flag, p.err)) return;
+                const uint32_t fb = map_rank(smem_u32(&y_full[slot]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&y_full[slot]), 2 * C::kYSlot);
+                armed[2] = ++ny;
+                const uint32_t a = smem_u32(y_ring + slot * C::kYSlot);
+                if constexpr (BWD) {
+                    tma_load_2d_pair(a, &p.wgt, f0, (int)rank * EB * 32, fb);
+                    tma_load_2d_pair(a + EB * 4096, &p.wut, f0, (int)rank * EB * 32, fb);
+                } else {
+                    tma_load_2d_pair(a, &p.wd, f0, (int)rank * EB * 32, fb);
+                }
+            };
+            auto load_x = [&](int row) {
+                const int b = (int)(nx % XB);
+                if (!mbar_wait(smem_u32(&x_empty[b]), ((nx / XB) & 1u) ^ 1u, abort_flag, p.err)) return;
+                const uint32_t fb = map_rank(smem_u32(&x_full[b]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&x_full[b]), 2 * C::kX);
+                armed[0] = ++nx;
+                const uint32_t a = smem_u32(x_s + b * C::kX);
+                for (int j = 0; j < KB; ++j) {
+                    tma_load_2d_pair(a + j * kBox, &p.x, j * (Q8 ? 128 : 64), row, fb);
+                    if constexpr (BWD) tma_load_2d_pair(a + (KB + j) * kBox, &p.dy, j * 64, row, fb);
+                }
+            };
+            int y1 = -1, y2 = -1;  // hidden columns of the chunks one and two steps back
+            for (int item = pair; item < p.items && !*abort_flag; item += n_pairs) {
+                const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
+                const int row = (item / p.parts) * 256 + (int)rank * 128;
+                for (int c = 0; c < n && !*abort_flag; ++c) {
+                    if (C::kOut && y2 >= 0) load_y(y2);
+                    if (c == 0) load_x(row);
+                    load_s(f_first + c * 64);
+                    y2 = y1;
+                    y1 = f_first + c * 64;
+                }
+            }
+            if (C::kOut && !*abort_flag) {
+                if (y2 >= 0) load_y(y2);
+                if (y1 >= 0) load_y(y1);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer of the pair
+            uint32_t ns = 0, ny = 0, nx = 0, k = 0, ky = 0, n_out = 0;
+            bool ok = true;
+            auto wait_for = [&](uint64_t *b, uint32_t parity) {
+                if (ok) ok = mbar_wait_cluster(smem_u32(b), parity, abort_flag, p.err);
+                return ok;
+            };
+            auto issue_s = [&](bool first, bool last) {
+                const int xb = (int)(nx % XB);
+                if (first && !wait_for(&x_full[xb], (nx / XB) & 1u)) return;
+                const uint32_t d = tmem + (k & 1u) * C::kSCols;
+                const uint32_t xa = smem_u32(x_s + xb * C::kX);
+                for (int j = 0; j < KB; ++j, ++ns) {
+                    const int slot = (int)(ns % NS);
+                    if (!wait_for(&s_full[slot], (ns / NS) & 1u)) return;
+                    tc_fence_after();
+                    const uint32_t b = smem_u32(s_ring + slot * C::kSSlot);
+                    const uint64_t da = smem_desc(xa + j * kBox), db = smem_desc(b);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mma_pair<Q8>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q), idesc_of(Q8, false, 256, 128),
+                                     (uint32_t)(j > 0 || q > 0));
+                    if constexpr (BWD) {
+                        const uint64_t da1 = smem_desc(xa + (KB + j) * kBox), db1 = smem_desc(b + 8192);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mma_pair<false>(d + 128, da1 + (uint64_t)(2 * q), db1 + (uint64_t)(2 * q),
+                                            idesc_of(false, false, 256, 64), (uint32_t)(j > 0 || q > 0));
+                    }
+                    mma_commit_pair(smem_u32(&s_empty[slot]));
+                }
+                mma_commit_pair(smem_u32(&acc_full[k & 1u]));
+                if (last) {
+                    mma_commit_pair(smem_u32(&x_empty[xb]));
+                    ++nx;
+                }
+                ++k;
+            };
+            // the product that takes chunk ky's hidden values (without one: only the hand-back of its S buffer)
+            auto issue_y = [&](bool first, bool last) {
+                const int hb = (int)(ky & 1u);
+                if (!wait_for(&h_full[hb], (ky >> 1) & 1u)) return;
+                tc_fence_after();
+                if constexpr (C::kOut) {
+                    const int ob = (int)(n_out % OB);
+                    if (first && !wait_for(&out_empty[ob], ((n_out / OB) & 1u) ^ 1u)) return;
+                    const int slot = (int)(ny % NY);
+                    if (!wait_for(&y_full[slot], (ny / NY) & 1u)) return;
+                    tc_fence_after();
+                    const uint32_t d = tmem + 2 * C::kSCols + (uint32_t)(ob * EB * 64);
+                    const uint32_t a = smem_u32(staged + hb * C::kStaged), b = smem_u32(y_ring + slot * C::kYSlot);
+#pragma unroll
+                    for (int z = 0; z < (BWD ? 2 : 1); ++z) {
+                        const uint64_t da = smem_desc(a + z * kBox), db = smem_desc(b + z * EB * 4096);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mma_pair<false>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q),
+                                            idesc_of(false, false, 256, EB * 64), (uint32_t)(!first || z > 0 || q > 0));
+                    }
+                    mma_commit_pair(smem_u32(&y_empty[slot]));
+                    mma_commit_pair(smem_u32(&h_empty[hb]));
+                    ++ny;
+                    if (last) {
+                        mma_commit_pair(smem_u32(&out_full[ob]));
+                        ++n_out;
+                    }
+                }
+                ++ky;
+            };
+            uint32_t f1 = 0, f2 = 0;  // (first | last << 1 | 4) of the chunks one and two steps back
+            for (int item = pair; item < p.items && ok; item += n_pairs) {
+                const int n = chunks_of(item);
+                for (int c = 0; c < n && ok; ++c) {
+                    if (f2) issue_y(f2 & 1u, f2 & 2u);
+                    if (ok) issue_s(c == 0, c == n - 1);
+                    f2 = f1;
+                    f1 = (uint32_t)(c == 0) | (uint32_t)(c == n - 1) << 1 | 4u;
+                }
+            }
+            if (ok && f2) issue_y(f2 & 1u, f2 & 2u);
+            if (ok && f1) issue_y(f1 & 1u, f1 & 2u);
+            mma_commit_pair(smem_u32(mma_done));
+            int dummy = 0;
+            mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
+        }
+    } else if (warp < 10) {
+        // ---------------- chunk epilogue: group g takes chunks g, g + 2, ...
+        const int quarter = warp & 3, g = (warp - 2) >> 2;
+        const int r = quarter * 32 + lane;
+        const bool lead = threadIdx.x == 64 + 128 * g;
+        const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(g * C::kSCols);
+        uint8_t *st = staged + g * C::kStaged;
+        const uint32_t h_bar = map_rank(smem_u32(&h_full[g]), 0);
+        uint32_t k = 0, mine = 0;  // chunks so far, and those of this group
+        for (int item = pair; item < p.items; item += n_pairs) {
+            const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
+            const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
+            const bool live = row < p.M;
+            float xs = 1.f;
+            if constexpr (Q8) xs = live ? p.xs[row] : 0.f;
+            for (int c = 0; c < n; ++c, ++k) {
+                if ((k & 1u) != (uint32_t)g) continue;
+                const int f0 = f_first + c * 64;
+                mbar_wait(smem_u32(&acc_full[g]), mine & 1u, abort_flag, p.err);
+                tc_fence_after();
+                if constexpr (C::kOut) mbar_wait(smem_u32(&h_empty[g]), (mine & 1u) ^ 1u, abort_flag, p.err);
+#pragma unroll
+                for (int s = 0; s < 64; s += 16) {
+                    uint32_t vg[16], vu[16], vd[16], bias[16];
+                    tmem_ld16(t0 + (uint32_t)s, vg);
+                    tmem_ld16(t0 + (uint32_t)(64 + s), vu);
+                    if constexpr (BWD) tmem_ld16(t0 + (uint32_t)(128 + s), vd);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<uint4 *>(bias + j) = *reinterpret_cast<const uint4 *>(bias_s + f0 + s + j);
+                    if constexpr (BWD) tmem_wait(vg, vu, vd);
+                    else tmem_wait(vg, vu);
+                    uint32_t wh[8], wg[8], wu[8];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        float h[2], dg[2], du[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float bg = __uint_as_float(bias[j + e] << 16);
+                            const float bu = __uint_as_float(bias[j + e] & 0xffff0000u);
+                            float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
+                            if constexpr (Q8) {
+                                const float2 sc = scale_s[f0 + s + j + e];
+                                a = fmaf(a, xs * sc.x, bg);
+                                b = fmaf(b, xs * sc.y, bu);
+                            } else {
+                                a += bg;
+                                b += bu;
+                            }
+                            if constexpr (BWD) {
+                                const float d = __uint_as_float(vd[j + e]);
+                                float slope;
+                                const float act = Act<ACT>::fast(a, &slope);
+                                h[e] = act * b;
+                                du[e] = d * act;
+                                dg[e] = d * b * slope;
+                            } else {
+                                h[e] = Act<ACT>::fast(a) * b;
+                            }
+                        }
+                        wh[j / 2] = pack_bf16(h[0], h[1]);
+                        if constexpr (BWD) {
+                            wg[j / 2] = pack_bf16(dg[0], dg[1]);
+                            wu[j / 2] = pack_bf16(du[0], du[1]);
+                        }
+                    }
+                    if constexpr (C::kOut) {
+                        const uint32_t o0 = swizzled(r, s / 8), o1 = swizzled(r, s / 8 + 1);
+                        const uint32_t *a = BWD ? wg : wh;
+                        *reinterpret_cast<uint4 *>(st + o0) = make_uint4(a[0], a[1], a[2], a[3]);
+                        *reinterpret_cast<uint4 *>(st + o1) = make_uint4(a[4], a[5], a[6], a[7]);
+                        if constexpr (BWD) {
+                            *reinterpret_cast<uint4 *>(st + kBox + o0) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+                            *reinterpret_cast<uint4 *>(st + kBox + o1) = make_uint4(wu[4], wu[5], wu[6], wu[7]);
+                        }
+                    }
+                    if constexpr (BWD) {
+                        const int left = p.F - (f0 + s);
+                        if (live && left > 0) {
+                            const size_t at = (size_t)row * p.F + f0 + s;
+                            const bool wide = p.wide_f && left >= 16;
+                            store16(p.h + at, wh, left, wide);
+                            store16(p.dg + at, wg, left, wide);
+                            store16(p.du + at, wu, left, wide);
+                        }
+                    }
+                }
+                tc_fence_before();
+                if constexpr (C::kOut) fence_async_shared();
+                group_sync(g);
+                if (lead) mbar_arrive_cluster(h_bar);
+                ++mine;
+            }
+        }
+    } else if constexpr (C::kOut) {
+        // ---------------- the row block's result
+        const int quarter = warp & 3, r = quarter * 32 + lane;
+        const bool lead = threadIdx.x == 64 + 256;
+        uint32_t i = 0;
+        for (int item = pair; item < p.items; item += n_pairs, ++i) {
+            const int ob = (int)(i % OB);
+            const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
+            const bool live = row < p.M;
+            mbar_wait(smem_u32(&out_full[ob]), (i / OB) & 1u, abort_flag, p.err);
+            tc_fence_after();
+            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(2 * C::kSCols + ob * EB * 64);
+#pragma unroll
+            for (int s0 = 0; s0 < EB * 64; s0 += 64) {
+                uint32_t e[4][8];
+                const bool with_res = !BWD && p.res && live;
+                if (with_res)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int c = s0 + 16 * q, left = p.E - c;
+                        if (left > 0) load16(p.res + (size_t)row * p.E + c, e[q], left, p.wide_e && left >= 16);
+                    }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int c = s0 + 16 * q, left = p.E - c;
+                    uint32_t v[16], w[8];
+                    tmem_ld16(t0 + (uint32_t)c, v);
+                    tmem_wait(v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
+                        if constexpr (!BWD) {
+                            const float2 bb = *reinterpret_cast<const float2 *>(bd_s + c + 2 * j);
+                            a += bb.x;
+                            b += bb.y;
+                            if (with_res) {
+                                a += __uint_as_float(e[q][j] << 16);
+                                b += __uint_as_float(e[q][j] & 0xffff0000u);
+                            }
+                        }
+                        w[j] = pack_bf16(a, b);
+                    }
+                    if (live && left > 0 && p.out) store16(p.out + (size_t)row * p.E + c, w, left, p.wide_e && left >= 16);
+                }
+            }
+            tc_fence_before();
+            group_sync(2);
+            if (lead) mbar_arrive_cluster(map_rank(smem_u32(&out_empty[ob]), 0));
+        }
+    }
+
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // every product has run before either CTA goes; after an expired wait the counted copies land first
+        int dummy = 0;
+        mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
+        if (*abort_flag && rank == 0) {
+            auto drain = [&](uint64_t *full, uint32_t made, uint32_t slots) {
+                for (uint32_t i = made > slots ? made - slots : 0; i < made; ++i)
+                    mbar_wait(smem_u32(&full[i % slots]), (i / slots) & 1u, (volatile int *)&dummy, p.err);
+            };
+            drain(x_full, armed[0], XB);
+            drain(s_full, armed[1], NS);
+            drain(y_full, armed[2], NY);
+        }
+    }
+    __syncthreads();
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free_pair(tmem, 512);
+}
+
+// ---------------------------------------------------------------- host side
+
+template <typename K>
+pmha_status configure(K kern, int smem, int *pairs)
+{
+    static std::mutex mu;
+    static std::map<std::pair<int, void *>, int> known;
+    int dev = 0;
+    PMHA_CUDA_TRY(cudaGetDevice(&dev));
+    std::lock_guard<std::mutex> lk(mu);
+    const auto it = known.find({dev, (void *)kern});
+    if (it != known.end()) {
+        *pairs = it->second;
+        return PMHA_OK;
+    }
+    PMHA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    PMHA_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
+    n = std::max(1, std::min(n, num_sms() / 2));
+    known[{dev, (void *)kern}] = n;
+    *pairs = n;
+    return PMHA_OK;
+}
+
+template <int EB, bool BWD, bool Q8, int ACT>
+pmha_status launch(Params &p, const char *stage, cudaStream_t s)
+{
+    using C = Cfg<EB, BWD, Q8>;
+    static_assert(C::kSmem <= kSmemMost, "shared memory of one CTA");
+    p.err = device_error_word();
+    if (!p.err) return PMHA_ERR_CUDA;
+    int pairs = 0;
+    auto kern = k_block<EB, BWD, Q8, ACT>;
+    const pmha_status st = configure(kern, C::kSmem, &pairs);
+    if (st != PMHA_OK) return st;
+    if (C::kOut) p.parts = 1;
+    else {
+        // parts of the hidden width even out the last wave of row blocks
+        int best = 1;
+        double best_cost = 1e30;
+        for (int parts = 1; parts <= std::min(p.chunks, 8); ++parts) {
+            const int per = (p.chunks + parts - 1) / parts;
+            const int64_t waves = ((int64_t)p.items * ((p.chunks + per - 1) / per) + pairs - 1) / pairs;
+            const double cost = (double)waves * (per + 1);  // a part costs about a chunk more for its tokens
+            if (cost < best_cost) best_cost = cost, best = parts;
+        }
+        p.parts = best;
+    }
+    p.per_part = (p.chunks + p.parts - 1) / p.parts;
+    p.parts = (p.chunks + p.per_part - 1) / p.per_part;
+    p.items *= p.parts;
+    const int grid = 2 * std::min(pairs, p.items);
+    StageTimer timer(stage, s);
+    kern<<<grid, kThreads, C::kSmem, s>>>(p);
+    count_launch();
+    PMHA_CUDA_TRY(cudaGetLastError());
+    return PMHA_OK;
+}
+
+template <int EB, bool BWD, bool Q8>
+pmha_status launch_act(pmha_act act, Params &p, const char *stage, cudaStream_t s)
+{
+    return act == PMHA_ACT_SILU ? launch<EB, BWD, Q8, PMHA_ACT_SILU>(p, stage, s)
+                                : launch<EB, BWD, Q8, PMHA_ACT_GELU>(p, stage, s);
+}
+
+template <bool BWD, bool Q8>
+pmha_status launch_width(pmha_act act, Params &p, const char *stage, cudaStream_t s)
+{
+    switch ((p.E + 63) / 64) {
+    case 1: return launch_act<1, BWD, Q8>(act, p, stage, s);
+    case 2: return launch_act<2, BWD, Q8>(act, p, stage, s);
+    case 3: return launch_act<3, BWD, Q8>(act, p, stage, s);
+    default: return launch_act<4, BWD, Q8>(act, p, stage, s);
+    }
+}
+
+bool aligned32(const void *p) { return ((uintptr_t)p & 31u) == 0; }
+
+}  // namespace
+
+bool ffn_fused_supported(int64_t E, int64_t F) { return E <= 256 && F <= kMaxHidden; }
+bool ffn_fused_dx(int64_t E) { return E <= 128; }
+
+pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
+                              cudaStream_t s)
+{
+    Params p = {};
+    const bool q8 = a.x_scale != nullptr;
+    const int es = q8 ? 1 : 2;
+    const int eb = (int)((f.E + 63) / 64);
+    p.M = (int)a.M, p.E = (int)f.E, p.F = (int)f.F;
+    p.items = (int)((a.M + 255) / 256);
+    p.chunks = (int)((f.F + 63) / 64);
+    p.bg = (const __nv_bfloat16 *)f.bg, p.bu = (const __nv_bfloat16 *)f.bu, p.bd = (const __nv_bfloat16 *)f.bd;
+    p.res = (const __nv_bfloat16 *)residual;
+    p.xs = a.x_scale, p.gs = a.wg_scale, p.us = a.wu_scale;
+    p.out = (__nv_bfloat16 *)out;
+    p.wide_e = f.E % 16 == 0 && aligned32(out) && aligned32(residual);
+    if (!make_tile_map(&p.x, a.x, a.M, f.E, f.E, es, 128) || !make_tile_map(&p.wg, a.wg, f.F, f.E, f.E, es, 64) ||
+        !make_tile_map(&p.wu, a.wu, f.F, f.E, f.E, es, 64) ||
+        !make_tile_map(&p.wd, wd, f.E, f.F, f.F, 2, (uint32_t)(eb * 32))) {
+        set_error("ffn_block: cuTensorMapEncodeTiled failed");
+        return PMHA_ERR_CUDA;
+    }
+    return q8 ? launch_width<false, true>(f.act, p, "ffn_block_quantized", s)
+              : launch_width<false, false>(f.act, p, "ffn_block", s);
+}
+
+pmha_status ffn_fused_backward(const FfnTc &f, const FfnHiddenArgs &a, const void *wg_t, const void *wu_t, void *dx,
+                               cudaStream_t s)
+{
+    Params p = {};
+    const int eb = (int)((f.E + 63) / 64);
+    p.M = (int)a.M, p.E = (int)f.E, p.F = (int)f.F;
+    p.items = (int)((a.M + 255) / 256);
+    p.chunks = (int)((f.F + 63) / 64);
+    p.bg = (const __nv_bfloat16 *)f.bg, p.bu = (const __nv_bfloat16 *)f.bu;
+    p.out = (__nv_bfloat16 *)dx;
+    p.h = (__nv_bfloat16 *)a.h, p.dg = (__nv_bfloat16 *)a.dg, p.du = (__nv_bfloat16 *)a.du;
+    p.wide_e = f.E % 16 == 0 && aligned32(dx);
+    p.wide_f = f.F % 16 == 0;
+    if (!make_tile_map(&p.x, a.x, a.M, f.E, f.E, 2, 128) || !make_tile_map(&p.dy, a.dy, a.M, f.E, f.E, 2, 128) ||
+        !make_tile_map(&p.wg, a.wg, f.F, f.E, f.E, 2, 64) || !make_tile_map(&p.wu, a.wu, f.F, f.E, f.E, 2, 64) ||
+        !make_tile_map(&p.wd, a.wd_t, f.F, f.E, f.E, 2, 32) ||
+        !make_tile_map(&p.wgt, wg_t, f.E, f.F, f.F, 2, (uint32_t)(eb * 32)) ||
+        !make_tile_map(&p.wut, wu_t, f.E, f.F, f.F, 2, (uint32_t)(eb * 32))) {
+        set_error("ffn_block_backward: cuTensorMapEncodeTiled failed");
+        return PMHA_ERR_CUDA;
+    }
+    return launch_width<true, false>(f.act, p, "ffn_block_backward", s);
+}
+
+}  // namespace pmha

@@ -24,6 +24,10 @@ pmha_status ffn_tc_up(const FfnTc &f, const FfnUpArgs &a, cudaStream_t s);
 // out (M, E) = h Wd^T + bd + residual
 pmha_status ffn_tc_down(const FfnTc &f, const void *h, const void *wd, const void *residual, int64_t M, void *out,
                         cudaStream_t s);
+// The whole forward in one kernel, the hidden rows on the chip (ffn_fused.cu).
+bool ffn_fused_supported(int64_t E, int64_t F);
+pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
+                              cudaStream_t s);
 // h, dg, du (M, F): the hidden row and the gradients of gate and up, from x,
 // dout and wd_t (F, E) = Wd transposed
 struct FfnHiddenArgs {
@@ -32,6 +36,11 @@ struct FfnHiddenArgs {
     void *h, *dg, *du;
 };
 pmha_status ffn_tc_hidden(const FfnTc &f, const FfnHiddenArgs &a, cudaStream_t s);
+// The same from one kernel that keeps the tokens on the chip and, where
+// ffn_fused_dx(E), forms dx (M, E) too.
+bool ffn_fused_dx(int64_t E);
+pmha_status ffn_fused_backward(const FfnTc &f, const FfnHiddenArgs &a, const void *wg_t, const void *wu_t, void *dx,
+                               cudaStream_t s);
 // dx (M, E) = dg Wg + du Wu from the transposed weights (E, F)
 pmha_status ffn_tc_dx(const FfnTc &f, const void *dg, const void *du, const void *wg_t, const void *wu_t, int64_t M,
                       void *dx, cudaStream_t s);

@@ -49,10 +49,13 @@ def check_backward(rows, E, F, dtype, bias=True, act="silu"):
 # one tile, ragged tiles, several tiles, both column-tile widths, K past one block, padded widths
 SHAPES = [(256, 128, 128), (1, 64, 64), (128, 64, 128), (129, 64, 64), (255, 8, 8), (257, 72, 200), (300, 256, 136),
           (1000, 128, 512), (513, 320, 264), (700, 576, 128), (1, 256, 1024), (33, 512, 2048), (2, 1024, 96)]
+# rows enough for the kernel that keeps the hidden rows on the chip, every width it has, ragged ends
+LONG = [(2048, 64, 64), (2300, 8, 72), (2500, 128, 512), (3001, 192, 264), (2049, 256, 1024), (40000, 128, 136),
+        (2200, 72, 4096), (2600, 248, 8)]
 ODD = [(5, 1, 1), (3, 7, 9), (130, 33, 65), (257, 100, 171), (64, 130, 514)]
 
 
-@pytest.mark.parametrize("rows,E,F", SHAPES + ODD)
+@pytest.mark.parametrize("rows,E,F", SHAPES + LONG + ODD + [(2055, 100, 171)])
 def test_forward_bf16(rows, E, F):
     check_forward(rows, E, F, BF16, bias=(rows + E) % 2 == 0, residual=F % 16 != 0 or rows % 2 == 1)
     check_forward(rows, E, F, BF16, bias=True, act="gelu", residual=True)
@@ -64,7 +67,7 @@ def test_forward_f32(rows, E, F):
     check_forward(rows, E, F, F32, act="gelu")
 
 
-@pytest.mark.parametrize("rows,E,F", SHAPES + ODD)
+@pytest.mark.parametrize("rows,E,F", SHAPES + LONG + ODD)
 def test_backward_bf16(rows, E, F):
     check_backward(rows, E, F, BF16)
     check_backward(rows, E, F, BF16, bias=False, act="gelu")
@@ -83,7 +86,8 @@ def test_more_rows_than_a_block(dtype):
     check_backward(4500, 32, 4096, dtype)
 
 
-@pytest.mark.parametrize("rows,E,F", [(256, 128, 128), (1, 16, 8), (100, 48, 72), (300, 256, 264), (1000, 512, 1024)])
+@pytest.mark.parametrize("rows,E,F", [(256, 128, 128), (1, 16, 8), (100, 48, 72), (300, 256, 264), (1000, 512, 1024),
+                                      (2048, 128, 512), (2111, 48, 72), (2300, 192, 200), (2500, 256, 4096)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_forward_quantized(rows, E, F, act):
     p, x, r = make(rows, E, F, BF16, act=act)
