@@ -49,7 +49,9 @@ struct Cfg {
     static constexpr int KB = Q8 ? (EB + 1) / 2 : EB;
     static constexpr bool kOut = !BWD || EB <= 2;               // the kernel forms y, or dx
     static constexpr int kX = (BWD ? 2 : 1) * KB * kBox;        // x (and dy) of a row block
-    static constexpr int kSSlot = BWD ? 12288 : 8192;           // 64 rows of Wg or Wu (and 32 of Wd^T), one K block
+    static constexpr int kSBlock = BWD ? 12288 : 8192;          // 64 rows of Wg or Wu (and 32 of Wd^T), one K block
+    static constexpr int SG = BWD && EB == 4 ? 2 : KB;          // K blocks of a stage: a chunk's where they fit
+    static constexpr int kSSlot = SG * kSBlock;
     static constexpr int kYSlot = kOut ? EB * (BWD ? 8192 : 4096) : 0;  // half of the output columns of a chunk
     static constexpr int kStaged = kOut ? (BWD ? 2 : 1) * kBox : 0;     // h, or dg and du
     static constexpr int kSCols = BWD ? 192 : 128;
@@ -58,12 +60,12 @@ struct Cfg {
     static constexpr int kScales = Q8 ? kMaxHidden * 8 : 0;
     static constexpr int kBars = 512;
     static constexpr int kFixed = 1024 + kNY * kYSlot + 2 * kStaged + kVec + kScales + kBars;
-    static constexpr int kXB = kFixed + 2 * kX + 2 * KB * kSSlot <= kSmemMost ? 2 : 1;  // token buffers
+    static constexpr int kXB = kFixed + 2 * kX + 2 * kSSlot <= kSmemMost ? 2 : 1;  // token buffers
     static constexpr int kNSFit = (kSmemMost - kFixed - kXB * kX) / kSSlot;
-    static constexpr int kNS = kNSFit > 8 ? 8 : kNSFit;
+    static constexpr int kNS = kNSFit > 4 ? 4 : kNSFit;
     static constexpr int kOB = 2 * kSCols + 2 * EB * 64 <= 512 ? 2 : 1;  // output accumulators
     static constexpr int kSmem = kFixed + kXB * kX + kNS * kSSlot;
-    static_assert(kNS >= KB, "a chunk's weights fit in the ring");
+    static_assert(kNS >= 2 && kNS * SG >= KB, "a chunk's weights fit in the ring");
     static_assert(!kOut || 2 * kSCols + kOB * EB * 64 <= 512, "tensor memory");
 };
 
@@ -145,9 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     float *bd_s = (float *)((uint8_t *)bias_s + kMaxHidden * 4);
     float2 *scale_s = (float2 *)((uint8_t *)bias_s + C::kVec);
     uint64_t *bar = (uint64_t *)((uint8_t *)scale_s + C::kScales);
-    uint64_t *x_full = bar, *x_empty = x_full + 2, *s_full = x_empty + 2, *s_empty = s_full + 8, *y_full = s_empty + 8,
-             *y_empty = y_full + 4, *acc_full = y_empty + 4, *h_full = acc_full + 2, *h_empty = h_full + 2,
-             *out_full = h_empty + 2, *out_empty = out_full + 2, *mma_done = out_empty + 2;
+    uint64_t *x_full = bar, *s_full = x_full + 2, *s_empty = s_full + 4, *y_full = s_empty + 4, *step = y_full + 4,
+             *h_full = step + 4, *out_full = h_full + 2, *out_empty = out_full + 2, *mma_done = out_empty + 2;
     uint32_t *tmem_holder = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
     volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted: x, S slots, Y slots
@@ -159,20 +160,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&x_full[i]), 1);
-            mbar_init(smem_u32(&x_empty[i]), 1);
-            mbar_init(smem_u32(&acc_full[i]), 1);
             mbar_init(smem_u32(&h_full[i]), 2);  // the group in either CTA
-            mbar_init(smem_u32(&h_empty[i]), 1);
             mbar_init(smem_u32(&out_full[i]), 1);
             mbar_init(smem_u32(&out_empty[i]), 2);
         }
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&s_empty[i]), 1);
-        }
-        for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&y_full[i]), 1);
-            mbar_init(smem_u32(&y_empty[i]), 1);
+            mbar_init(smem_u32(&step[i]), 1);
         }
         mbar_init(smem_u32(mma_done), 1);
         *abort_flag = 0;
@@ -195,29 +191,42 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     // item -> row block, first chunk; every item has the chunks of one part (the last part may have fewer)
     auto chunks_of = [&](int item) { return min(p.per_part, p.chunks - (item % p.parts) * p.per_part); };
 
+    // Step k: the product Y of chunk k - 2, then S of chunk k, committed together: S(k) can be read, and the
+    // staged values and weights of Y(k - 2) and the weights of S(k) are free. Four barriers in turn.
+    auto wait_step = [&](uint32_t k) { return wait_bar(smem_u32(&step[k & 3u]), (k >> 2) & 1u, abort_flag, p.err); };
+
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- TMA producer of this CTA, in the issuer's order
-            uint32_t ns = 0, ny = 0, nx = 0;  // copies made into each ring
-            auto load_s = [&](int f0) {
-                for (int j = 0; j < KB; ++j, ++ns) {
-                    const int slot = (int)(ns % NS);
-                    if (!mbar_wait(smem_u32(&s_empty[slot]), ((ns / NS) & 1u) ^ 1u, abort_flag, p.err)) return;
+        // ---------------- TMA producer of this CTA, in the issuer's order
+        const bool one = elect_one();
+        uint32_t ns = 0, ny = 0, nx = 0, k = 0;  // copies made into each ring; steps
+        uint32_t last1 = 0, last2 = 0;           // 1 + the last step of the row blocks one and two back
+        auto load_s = [&](int f0) {
+            for (int j = 0; j < KB; j += C::SG, ++ns) {
+                const int slot = (int)(ns % NS);
+                if constexpr (C::SG < KB) {
+                    if (!wait_bar(smem_u32(&s_empty[slot]), ((ns / NS) & 1u) ^ 1u, abort_flag, p.err)) return;
+                } else if (k >= (uint32_t)NS && !wait_step(k - NS)) return;
+                if (one) {
                     const uint32_t fb = map_rank(smem_u32(&s_full[slot]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s_full[slot]), 2 * C::kSSlot);
                     armed[1] = ns + 1;
-                    const uint32_t a = smem_u32(s_ring + slot * C::kSSlot);
-                    const int k = j * (Q8 ? 128 : 64);
-                    tma_load_2d_pair(a, rank ? &p.wu : &p.wg, k, f0, fb);
-                    if constexpr (BWD) tma_load_2d_pair(a + 8192, &p.wd, k, f0 + (int)rank * 32, fb);
+#pragma unroll
+                    for (int i = 0; i < C::SG; ++i) {
+                        const uint32_t a = smem_u32(s_ring + slot * C::kSSlot + i * C::kSBlock);
+                        const int c = (j + i) * (Q8 ? 128 : 64);
+                        tma_load_2d_pair(a, rank ? &p.wu : &p.wg, c, f0, fb);
+                        if constexpr (BWD) tma_load_2d_pair(a + 8192, &p.wd, c, f0 + (int)rank * 32, fb);
+                    }
                 }
-            };
-            auto load_y = [&](int f0) {
-                const int slot = (int)(ny % NY);
-                if (!mbar_wait(smem_u32(&y_empty[slot]), ((ny / NY) & 1u) ^ 1u, abort_flag, p.err)) return;
+            }
+        };
+        auto load_y = [&](int f0) {  // of chunk ny; its slot was read by step ny - NY + 2
+            const int slot = (int)(ny % NY);
+            if (ny >= (uint32_t)NY && !wait_step(ny - NY + 2)) return;
+            if (one) {
                 const uint32_t fb = map_rank(smem_u32(&y_full[slot]), 0);
                 if (rank == 0) mbar_arrive_expect_tx(smem_u32(&y_full[slot]), 2 * C::kYSlot);
-                armed[2] = ++ny;
+                armed[2] = ny + 1;
                 const uint32_t a = smem_u32(y_ring + slot * C::kYSlot);
                 if constexpr (BWD) {
                     tma_load_2d_pair(a, &p.wgt, f0, (int)rank * EB * 32, fb);
@@ -225,120 +234,143 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 } else {
                     tma_load_2d_pair(a, &p.wd, f0, (int)rank * EB * 32, fb);
                 }
-            };
-            auto load_x = [&](int row) {
-                const int b = (int)(nx % XB);
-                if (!mbar_wait(smem_u32(&x_empty[b]), ((nx / XB) & 1u) ^ 1u, abort_flag, p.err)) return;
+            }
+            ++ny;
+        };
+        auto load_x = [&](int row) {
+            const int b = (int)(nx % XB);
+            const uint32_t before = XB == 1 ? last1 : last2;
+            // a step more than NS back is known to be over (load_s of this step waited for a later one)
+            if (before && before + NS > k && !wait_step(before - 1)) return;
+            if (one) {
                 const uint32_t fb = map_rank(smem_u32(&x_full[b]), 0);
                 if (rank == 0) mbar_arrive_expect_tx(smem_u32(&x_full[b]), 2 * C::kX);
-                armed[0] = ++nx;
+                armed[0] = nx + 1;
                 const uint32_t a = smem_u32(x_s + b * C::kX);
+#pragma unroll
                 for (int j = 0; j < KB; ++j) {
                     tma_load_2d_pair(a + j * kBox, &p.x, j * (Q8 ? 128 : 64), row, fb);
                     if constexpr (BWD) tma_load_2d_pair(a + (KB + j) * kBox, &p.dy, j * 64, row, fb);
                 }
-            };
-            int y1 = -1, y2 = -1;  // hidden columns of the chunks one and two steps back
-            for (int item = pair; item < p.items && !*abort_flag; item += n_pairs) {
-                const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
-                const int row = (item / p.parts) * 256 + (int)rank * 128;
-                for (int c = 0; c < n && !*abort_flag; ++c) {
-                    if (C::kOut && y2 >= 0) load_y(y2);
-                    if (c == 0) load_x(row);
-                    load_s(f_first + c * 64);
-                    y2 = y1;
-                    y1 = f_first + c * 64;
-                }
             }
-            if (C::kOut && !*abort_flag) {
-                if (y2 >= 0) load_y(y2);
-                if (y1 >= 0) load_y(y1);
+            ++nx;
+        };
+        int y1 = -1, y2 = -1;  // hidden columns of the chunks one and two steps back
+        for (int item = pair; item < p.items && !*abort_flag; item += n_pairs) {
+            const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
+            const int row = (item / p.parts) * 256 + (int)rank * 128;
+            for (int c = 0; c < n && !*abort_flag; ++c, ++k) {
+                load_s(f_first + c * 64);
+                // a second token buffer is filled as early as can be; a single one waits for the last step
+                if (XB == 2 && c == 0) load_x(row);
+                if (C::kOut && y2 >= 0) load_y(y2);
+                if (XB == 1 && c == 0) load_x(row);
+                y2 = y1;
+                y1 = f_first + c * 64;
             }
+            last2 = last1;
+            last1 = k;
+        }
+        if (C::kOut && !*abort_flag) {
+            if (y2 >= 0) load_y(y2);
+            if (y1 >= 0) load_y(y1);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // ---------------- MMA issuer of the pair
-            uint32_t ns = 0, ny = 0, nx = 0, k = 0, ky = 0, n_out = 0;
+        if (rank == 0) {
+            // ---------------- MMA issuer of the pair: the whole warp walks the steps, so that addresses stay in
+            // uniform registers; one lane issues
+            const bool one = elect_one();
+            uint32_t ns = 0, nx = 0, k = 0, n_out = 0;
             bool ok = true;
             auto wait_for = [&](uint64_t *b, uint32_t parity) {
-                if (ok) ok = mbar_wait_cluster(smem_u32(b), parity, abort_flag, p.err);
-                return ok;
+                if (ok) ok = wait_bar(smem_u32(b), parity, abort_flag, p.err);
             };
-            auto issue_s = [&](bool first, bool last) {
-                const int xb = (int)(nx % XB);
-                if (first && !wait_for(&x_full[xb], (nx / XB) & 1u)) return;
-                const uint32_t d = tmem + (k & 1u) * C::kSCols;
-                const uint32_t xa = smem_u32(x_s + xb * C::kX);
-                for (int j = 0; j < KB; ++j, ++ns) {
-                    const int slot = (int)(ns % NS);
-                    if (!wait_for(&s_full[slot], (ns / NS) & 1u)) return;
-                    tc_fence_after();
-                    const uint32_t b = smem_u32(s_ring + slot * C::kSSlot);
-                    const uint64_t da = smem_desc(xa + j * kBox), db = smem_desc(b);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mma_pair<Q8>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q), idesc_of(Q8, false, 256, 128),
-                                     (uint32_t)(j > 0 || q > 0));
-                    if constexpr (BWD) {
-                        const uint64_t da1 = smem_desc(xa + (KB + j) * kBox), db1 = smem_desc(b + 8192);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mma_pair<false>(d + 128, da1 + (uint64_t)(2 * q), db1 + (uint64_t)(2 * q),
-                                            idesc_of(false, false, 256, 64), (uint32_t)(j > 0 || q > 0));
-                    }
-                    mma_commit_pair(smem_u32(&s_empty[slot]));
+            // (first | last << 1 | 4) of the chunks one and two steps back
+            auto run_step = [&](uint32_t y, bool has_s, bool first, bool last) {
+                const uint32_t ky = k - 2;  // the chunk of Y
+                const int ys = (int)(ky % NY), xb = (int)(nx % XB), ob = (int)(n_out % OB);
+                // what is loaded long before comes first: only the hidden values are waited for in earnest
+                if (C::kOut && y) {
+                    wait_for(&y_full[ys], (ky / NY) & 1u);
+                    if (y & 1u) wait_for(&out_empty[ob], ((n_out / OB) & 1u) ^ 1u);
                 }
-                mma_commit_pair(smem_u32(&acc_full[k & 1u]));
-                if (last) {
-                    mma_commit_pair(smem_u32(&x_empty[xb]));
-                    ++nx;
+                if (has_s) {
+                    if (first) wait_for(&x_full[xb], (nx / XB) & 1u);
+                    if constexpr (C::SG == KB) wait_for(&s_full[ns % NS], (ns / NS) & 1u);
                 }
-                ++k;
-            };
-            // the product that takes chunk ky's hidden values (without one: only the hand-back of its S buffer)
-            auto issue_y = [&](bool first, bool last) {
-                const int hb = (int)(ky & 1u);
-                if (!wait_for(&h_full[hb], (ky >> 1) & 1u)) return;
+                if (y) wait_for(&h_full[ky & 1u], (ky >> 1) & 1u);
+                if (!ok) return;
                 tc_fence_after();
                 if constexpr (C::kOut) {
-                    const int ob = (int)(n_out % OB);
-                    if (first && !wait_for(&out_empty[ob], ((n_out / OB) & 1u) ^ 1u)) return;
-                    const int slot = (int)(ny % NY);
-                    if (!wait_for(&y_full[slot], (ny / NY) & 1u)) return;
-                    tc_fence_after();
-                    const uint32_t d = tmem + 2 * C::kSCols + (uint32_t)(ob * EB * 64);
-                    const uint32_t a = smem_u32(staged + hb * C::kStaged), b = smem_u32(y_ring + slot * C::kYSlot);
+                    if (y && one) {
+                        const uint32_t d = tmem + 2 * C::kSCols + (uint32_t)(ob * EB * 64);
+                        const uint32_t a = smem_u32(staged + (ky & 1u) * C::kStaged), b = smem_u32(y_ring + ys * C::kYSlot);
 #pragma unroll
-                    for (int z = 0; z < (BWD ? 2 : 1); ++z) {
-                        const uint64_t da = smem_desc(a + z * kBox), db = smem_desc(b + z * EB * 4096);
+                        for (int z = 0; z < (BWD ? 2 : 1); ++z) {
+                            const uint64_t da = smem_desc(a + z * kBox), db = smem_desc(b + z * EB * 4096);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mma_pair<false>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q),
-                                            idesc_of(false, false, 256, EB * 64), (uint32_t)(!first || z > 0 || q > 0));
+                            for (int q = 0; q < 4; ++q)
+                                mma_pair<false>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q),
+                                                idesc_of(false, false, 256, EB * 64), z + q ? 1u : (y & 1u) ^ 1u);
+                        }
+                        if (y & 2u) mma_commit_pair(smem_u32(&out_full[ob]));
                     }
-                    mma_commit_pair(smem_u32(&y_empty[slot]));
-                    mma_commit_pair(smem_u32(&h_empty[hb]));
-                    ++ny;
-                    if (last) {
-                        mma_commit_pair(smem_u32(&out_full[ob]));
-                        ++n_out;
-                    }
+                    if (y & 2u) ++n_out;
                 }
-                ++ky;
+                if (has_s) {
+                    const uint32_t d = tmem + (k & 1u) * C::kSCols;
+                    const uint32_t xa = smem_u32(x_s + xb * C::kX);
+#pragma unroll
+                    for (int j0 = 0; j0 < KB; j0 += C::SG, ++ns) {
+                        const int slot = (int)(ns % NS);
+                        if constexpr (C::SG < KB) {
+                            wait_for(&s_full[slot], (ns / NS) & 1u);
+                            if (!ok) return;
+                            tc_fence_after();
+                        }
+                        if (one) {
+#pragma unroll
+                            for (int i = 0; i < C::SG; ++i) {
+                                const int j = j0 + i;
+                                const uint32_t b = smem_u32(s_ring + slot * C::kSSlot + i * C::kSBlock);
+                                const uint64_t da = smem_desc(xa + j * kBox), db = smem_desc(b);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    mma_pair<Q8>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q),
+                                                 idesc_of(Q8, false, 256, 128), (uint32_t)(j > 0 || q > 0));
+                                if constexpr (BWD) {
+                                    const uint64_t da1 = smem_desc(xa + (KB + j) * kBox), db1 = smem_desc(b + 8192);
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        mma_pair<false>(d + 128, da1 + (uint64_t)(2 * q), db1 + (uint64_t)(2 * q),
+                                                        idesc_of(false, false, 256, 64), (uint32_t)(j > 0 || q > 0));
+                                }
+                            }
+                            if constexpr (C::SG < KB) mma_commit_pair(smem_u32(&s_empty[slot]));
+                        }
+                    }
+                    if (last) ++nx;
+                }
+                if (one) mma_commit_pair(smem_u32(&step[k & 3u]));
+                __syncwarp();
+                ++k;
             };
-            uint32_t f1 = 0, f2 = 0;  // (first | last << 1 | 4) of the chunks one and two steps back
+            uint32_t f1 = 0, f2 = 0;
             for (int item = pair; item < p.items && ok; item += n_pairs) {
                 const int n = chunks_of(item);
                 for (int c = 0; c < n && ok; ++c) {
-                    if (f2) issue_y(f2 & 1u, f2 & 2u);
-                    if (ok) issue_s(c == 0, c == n - 1);
+                    run_step(f2, true, c == 0, c == n - 1);
                     f2 = f1;
                     f1 = (uint32_t)(c == 0) | (uint32_t)(c == n - 1) << 1 | 4u;
                 }
             }
-            if (ok && f2) issue_y(f2 & 1u, f2 & 2u);
-            if (ok && f1) issue_y(f1 & 1u, f1 & 2u);
-            mma_commit_pair(smem_u32(mma_done));
+            for (int z = 0; z < 2 && ok; ++z) {
+                if (f2 || k < 2) run_step(f2, false, false, false);
+                f2 = f1;
+                f1 = 0;
+            }
+            if (one) mma_commit_pair(smem_u32(mma_done));
+            __syncwarp();
             int dummy = 0;
             mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
@@ -350,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(g * C::kSCols);
         uint8_t *st = staged + g * C::kStaged;
         const uint32_t h_bar = map_rank(smem_u32(&h_full[g]), 0);
-        uint32_t k = 0, mine = 0;  // chunks so far, and those of this group
+        uint32_t k = 0;
         for (int item = pair; item < p.items; item += n_pairs) {
             const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
             const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
@@ -360,11 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             for (int c = 0; c < n; ++c, ++k) {
                 if ((k & 1u) != (uint32_t)g) continue;
                 const int f0 = f_first + c * 64;
-                mbar_wait(smem_u32(&acc_full[g]), mine & 1u, abort_flag, p.err);
+                wait_step(k);  // and the staged values of chunk k - 2 are read
                 tc_fence_after();
-                if constexpr (C::kOut) mbar_wait(smem_u32(&h_empty[g]), (mine & 1u) ^ 1u, abort_flag, p.err);
-#pragma unroll
-                for (int s = 0; s < 64; s += 16) {
+#pragma unroll 1
+                for (int s = 0; s < 64; s += 16) {  // rolled: the warps of an SM share its instruction cache
                     uint32_t vg[16], vu[16], vd[16], bias[16];
                     tmem_ld16(t0 + (uint32_t)s, vg);
                     tmem_ld16(t0 + (uint32_t)(64 + s), vu);
@@ -433,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 if constexpr (C::kOut) fence_async_shared();
                 group_sync(g);
                 if (lead) mbar_arrive_cluster(h_bar);
-                ++mine;
             }
         }
     } else if constexpr (C::kOut) {
@@ -445,10 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             const int ob = (int)(i % OB);
             const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
             const bool live = row < p.M;
-            mbar_wait(smem_u32(&out_full[ob]), (i / OB) & 1u, abort_flag, p.err);
+            wait_bar(smem_u32(&out_full[ob]), (i / OB) & 1u, abort_flag, p.err);
             tc_fence_after();
             const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(2 * C::kSCols + ob * EB * 64);
-#pragma unroll
+#pragma unroll 1
             for (int s0 = 0; s0 < EB * 64; s0 += 64) {
                 uint32_t e[4][8];
                 const bool with_res = !BWD && p.res && live;
@@ -491,11 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     if (threadIdx.x == 0) {
         // every product has run before either CTA goes; after an expired wait the counted copies land first
         int dummy = 0;
-        mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
+        wait_bar(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         if (*abort_flag && rank == 0) {
             auto drain = [&](uint64_t *full, uint32_t made, uint32_t slots) {
                 for (uint32_t i = made > slots ? made - slots : 0; i < made; ++i)
-                    mbar_wait(smem_u32(&full[i % slots]), (i / slots) & 1u, (volatile int *)&dummy, p.err);
+                    wait_bar(smem_u32(&full[i % slots]), (i / slots) & 1u, (volatile int *)&dummy, p.err);
             };
             drain(x_full, armed[0], XB);
             drain(s_full, armed[1], NS);

@@ -236,12 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                 int m, n, kb0, kb1, what;
                 decode(tile, m, n, kb0, kb1, what);
                 const int n_kb = KIND == kDown ? p.segs * p.kb : kb1;
-                if (!mbar_wait_cluster(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, abort_flag, p.err)) break;
+                if (!mbar_wait(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, abort_flag, p.err)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * C::kAccStride);
                 bool ok = true;
                 for (int kb = kb0; kb < n_kb; ++kb) {
-                    if (!mbar_wait_cluster(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }

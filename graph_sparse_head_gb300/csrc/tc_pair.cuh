@@ -28,37 +28,27 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// arrival on a barrier of either CTA (a shared::cluster address)
+// Arrival on a barrier of either CTA (a shared::cluster address). What the
+// barriers of a pair hand over is read and written by the tensor core and the
+// copy engine, ordered by fence.proxy.async and tcgen05.fence; the arrivals
+// and waits keep CTA scope. (An acquire or release of cluster scope
+// costs 400 to 600 cycles each: a chunk of the fused block took 3,100 cycles
+// with them, most of it in waits on barriers already complete.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+// mbar_wait with the usual case, a phase already complete, in line.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err)
 {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
+    return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort_flag, err);
 }
-// mbar_wait for barriers that the other CTA arrives on; bounded alike.
-__device__ __noinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err)
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
 {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            atomicOr(err, kErrTimeoutBit);
-            return false;
-        }
-    }
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 // A tile into this CTA's shared memory, its bytes counted by a barrier of either CTA.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
