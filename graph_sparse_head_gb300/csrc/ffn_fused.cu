@@ -17,10 +17,12 @@
 // read once; what bounds it is the tensor pipe and, near it, the epilogue's
 // arithmetic (two special-function results for each hidden value). So the
 // warps are specialised: warp 0 copies, warp 1 of the even CTA issues the
-// products, two groups of four warps take the chunks in turn (each has two
+// products, two groups of eight warps take the chunks in turn (each has two
 // chunks' time, so that one group's tensor-memory reads and barriers run under
-// the other's arithmetic), and a fourth group drains the row block's result
-// while the next block's chunks go on. The issuer runs S two chunks ahead:
+// the other's arithmetic; eight warps, because a chunk's time is a loop from S
+// through the epilogue to Y and the next S of its buffer, and half the columns
+// a warp halve the longest part of it), and four more drain the row block's
+// result while the next block's chunks go on. The issuer runs S two chunks ahead:
 // S(0) S(1) | Y(0) S(2) | Y(1) S(3) ... across row blocks.
 //
 // Every wait is bounded; after an expired one the waits return at once, the
@@ -38,9 +40,9 @@ namespace pmha {
 namespace {
 using namespace tcu;
 
-constexpr int kThreads = 448;       // 2 + 4 + 4 + 4 warps
+constexpr int kThreads = 704;       // 2 + 8 + 8 + 4 warps
 constexpr int kBox = 128 * 128;     // 128 rows of 128 bytes
-constexpr int kMaxHidden = 4096;    // bias (and scale) columns held in shared memory
+constexpr int kMaxHidden = 2048;    // bias (and scale) columns held in shared memory
 constexpr int kSmemMost = 232448;
 
 // EB: blocks of 64 output columns; KB: blocks of 128 bytes of a token.
@@ -56,7 +58,7 @@ struct Cfg {
     static constexpr int kStaged = kOut ? (BWD ? 2 : 1) * kBox : 0;     // h, or dg and du
     static constexpr int kSCols = BWD ? 192 : 128;
     static constexpr int kNY = kOut ? (BWD ? 2 : 3) : 0;
-    static constexpr int kVec = 2048 * 8 + 1024;                // biases of 4096 columns, output bias
+    static constexpr int kVec = kMaxHidden * 8 + 1024;          // gate, up and output biases, float32
     static constexpr int kScales = Q8 ? kMaxHidden * 8 : 0;
     static constexpr int kBars = 512;
     static constexpr int kFixed = 1024 + kNY * kYSlot + 2 * kStaged + kVec + kScales + kBars;
@@ -72,6 +74,7 @@ struct Cfg {
 struct Params {
     CUtensorMap x, dy, wg, wu, wd;  // wd: Wd (E, F), or Wd^T (F, E) in the backward pass
     CUtensorMap wgt, wut;           // (E, F): Wg^T, Wu^T
+    CUtensorMap dg_map, du_map;     // (M, F)
     int M, E, F;
     int items, parts;               // row blocks x parts of the hidden width
     int chunks, per_part;           // chunks of 64 hidden columns, and of one part
@@ -92,15 +95,25 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 // Waits for this thread's tensor-memory reads; the values' uses stay behind it.
 template <typename... R>
 __device__ __forceinline__ void tmem_wait(R &...regs)
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-    auto pin = [](uint32_t(&r)[16]) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
-    };
     (pin(regs), ...);
 }
 
@@ -143,10 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     uint8_t *s_ring = x_s + XB * C::kX;               // [NS]
     uint8_t *y_ring = s_ring + NS * C::kSSlot;        // [kNY]
     uint8_t *staged = y_ring + C::kNY * C::kYSlot;    // [2]
-    uint32_t *bias_s = (uint32_t *)(staged + 2 * C::kStaged);  // (bg, bu) bf16 pairs
-    float *bd_s = (float *)((uint8_t *)bias_s + kMaxHidden * 4);
-    float2 *scale_s = (float2 *)((uint8_t *)bias_s + C::kVec);
-    uint64_t *bar = (uint64_t *)((uint8_t *)scale_s + C::kScales);
+    float *bg_s = (float *)(staged + 2 * C::kStaged), *bu_s = bg_s + kMaxHidden, *bd_s = bu_s + kMaxHidden;
+    float *gs_s = (float *)((uint8_t *)bg_s + C::kVec), *us_s = gs_s + kMaxHidden;
+    uint64_t *bar = (uint64_t *)((uint8_t *)gs_s + C::kScales);
     uint64_t *x_full = bar, *s_full = x_full + 2, *s_empty = s_full + 4, *y_full = s_empty + 4, *step = y_full + 4,
              *h_full = step + 4, *out_full = h_full + 2, *out_empty = out_full + 2, *mma_done = out_empty + 2;
     uint32_t *tmem_holder = (uint32_t *)(mma_done + 1);
@@ -178,9 +190,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
     for (int i = threadIdx.x; i < p.chunks * 64; i += kThreads) {
         const bool in = i < p.F;
-        const float g = in && p.bg ? __bfloat162float(p.bg[i]) : 0.f, u = in && p.bu ? __bfloat162float(p.bu[i]) : 0.f;
-        bias_s[i] = pack_bf16(g, u);
-        if constexpr (Q8) scale_s[i] = in ? make_float2(p.gs[i], p.us[i]) : make_float2(0.f, 0.f);
+        bg_s[i] = in && p.bg ? __bfloat162float(p.bg[i]) : 0.f;
+        bu_s[i] = in && p.bu ? __bfloat162float(p.bu[i]) : 0.f;
+        if constexpr (Q8) {
+            gs_s[i] = in ? p.gs[i] : 0.f;
+            us_s[i] = in ? p.us[i] : 0.f;
+        }
     }
     for (int i = threadIdx.x; i < EB * 64; i += kThreads) bd_s[i] = p.bd && i < p.E ? __bfloat162float(p.bd[i]) : 0.f;
     tc_fence_before();
@@ -374,12 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             int dummy = 0;
             mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
-    } else if (warp < 10) {
-        // ---------------- chunk epilogue: group g takes chunks g, g + 2, ...
-        const int quarter = warp & 3, g = (warp - 2) >> 2;
+    } else if (warp < 18) {
+        // ---------------- chunk epilogue: group g takes chunks g, g + 2, ..., each of its halves 32 columns
+        constexpr int kW = BWD ? 8 : 16;  // columns at a time: what 80 registers hold
+        const int quarter = warp & 3, g = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1;
         const int r = quarter * 32 + lane;
-        const bool lead = threadIdx.x == 64 + 128 * g;
+        const bool lead = threadIdx.x == 64 + 256 * g;
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(g * C::kSCols);
+        auto chunk_sync = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory"); };
         uint8_t *st = staged + g * C::kStaged;
         const uint32_t h_bar = map_rank(smem_u32(&h_full[g]), 0);
         uint32_t k = 0;
@@ -392,84 +409,113 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             for (int c = 0; c < n; ++c, ++k) {
                 if ((k & 1u) != (uint32_t)g) continue;
                 const int f0 = f_first + c * 64;
-                wait_step(k);  // and the staged values of chunk k - 2 are read
+                if constexpr (BWD && C::kOut) {
+                    if (lead) store_wait_read();  // the copies out of chunk k - 2's staged values
+                    chunk_sync();
+                }
+                wait_step(k);  // and the products with them are over
                 tc_fence_after();
 #pragma unroll 1
-                for (int s = 0; s < 64; s += 16) {  // rolled: the warps of an SM share its instruction cache
-                    uint32_t vg[16], vu[16], vd[16], bias[16];
-                    tmem_ld16(t0 + (uint32_t)s, vg);
-                    tmem_ld16(t0 + (uint32_t)(64 + s), vu);
-                    if constexpr (BWD) tmem_ld16(t0 + (uint32_t)(128 + s), vd);
+                for (int s = half * 32; s < half * 32 + 32; s += 16) {  // rolled: the warps of an SM share its instruction cache
+                    uint32_t wh[8];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<uint4 *>(bias + j) = *reinterpret_cast<const uint4 *>(bias_s + f0 + s + j);
-                    if constexpr (BWD) tmem_wait(vg, vu, vd);
-                    else tmem_wait(vg, vu);
-                    uint32_t wh[8], wg[8], wu[8];
+                    for (int q = 0; q < 16; q += kW) {
+                        uint32_t vg[kW], vu[kW], vd[kW], w0[kW / 2], w1[kW / 2];
+                        tmem_read(t0 + (uint32_t)(s + q), vg);
+                        tmem_read(t0 + (uint32_t)(64 + s + q), vu);
+                        if constexpr (BWD) {
+                            tmem_read(t0 + (uint32_t)(128 + s + q), vd);
+                            tmem_wait(vg, vu, vd);
+                        } else {
+                            tmem_wait(vg, vu);
+                        }
+                        const float *bg = bg_s + f0 + s + q, *bu = bu_s + f0 + s + q;
+                        const float *gs = gs_s + f0 + s + q, *us = us_s + f0 + s + q;
+                        auto pair_of = [](const uint32_t (&v)[kW], int j) {
+                            return f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                        };
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        float h[2], dg[2], du[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float bg = __uint_as_float(bias[j + e] << 16);
-                            const float bu = __uint_as_float(bias[j + e] & 0xffff0000u);
-                            float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
+                        for (int j = 0; j < kW; j += 4) {
+                            const float4 b4 = *reinterpret_cast<const float4 *>(bg + j);
+                            const float4 c4 = *reinterpret_cast<const float4 *>(bu + j);
+                            float4 m4 = {}, n4 = {};
                             if constexpr (Q8) {
-                                const float2 sc = scale_s[f0 + s + j + e];
-                                a = fmaf(a, xs * sc.x, bg);
-                                b = fmaf(b, xs * sc.y, bu);
-                            } else {
-                                a += bg;
-                                b += bu;
+                                m4 = *reinterpret_cast<const float4 *>(gs + j);
+                                n4 = *reinterpret_cast<const float4 *>(us + j);
                             }
-                            if constexpr (BWD) {
-                                const float d = __uint_as_float(vd[j + e]);
-                                float slope;
-                                const float act = Act<ACT>::fast(a, &slope);
-                                h[e] = act * b;
-                                du[e] = d * act;
-                                dg[e] = d * b * slope;
-                            } else {
-                                h[e] = Act<ACT>::fast(a) * b;
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                const F2 bj = e ? f2(b4.z, b4.w) : f2(b4.x, b4.y), cj = e ? f2(c4.z, c4.w) : f2(c4.x, c4.y);
+                                F2 a = pair_of(vg, j + e), b = pair_of(vu, j + e);
+                                if constexpr (Q8) {
+                                    const F2 mj = e ? f2(m4.z, m4.w) : f2(m4.x, m4.y);
+                                    const F2 nj = e ? f2(n4.z, n4.w) : f2(n4.x, n4.y);
+                                    a = fma2(a, mj * f2(xs), bj);
+                                    b = fma2(b, nj * f2(xs), cj);
+                                } else {
+                                    a = a + bj;
+                                    b = b + cj;
+                                }
+                                const int w = (j + e) / 2;
+                                if constexpr (BWD) {
+                                    const F2 d = pair_of(vd, j + e);
+                                    F2 slope;
+                                    const F2 act = Act<ACT>::fast(a, &slope);
+                                    wh[q / 2 + w] = to_bf16x2(act * b);
+                                    w1[w] = to_bf16x2(d * act);
+                                    w0[w] = to_bf16x2(d * b * slope);
+                                } else {
+                                    wh[q / 2 + w] = to_bf16x2(Act<ACT>::fast(a) * b);
+                                }
                             }
                         }
-                        wh[j / 2] = pack_bf16(h[0], h[1]);
                         if constexpr (BWD) {
-                            wg[j / 2] = pack_bf16(dg[0], dg[1]);
-                            wu[j / 2] = pack_bf16(du[0], du[1]);
+                            if constexpr (C::kOut) {
+                                const uint32_t o = swizzled(r, (s + q) / 8);
+                                *reinterpret_cast<uint4 *>(st + o) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                                *reinterpret_cast<uint4 *>(st + kBox + o) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                            } else if (live && f0 + s + q < p.F) {
+                                const size_t at = (size_t)row * p.F + f0 + s + q;
+                                *reinterpret_cast<uint4 *>(p.dg + at) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                                *reinterpret_cast<uint4 *>(p.du + at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                            }
                         }
                     }
-                    if constexpr (C::kOut) {
-                        const uint32_t o0 = swizzled(r, s / 8), o1 = swizzled(r, s / 8 + 1);
-                        const uint32_t *a = BWD ? wg : wh;
-                        *reinterpret_cast<uint4 *>(st + o0) = make_uint4(a[0], a[1], a[2], a[3]);
-                        *reinterpret_cast<uint4 *>(st + o1) = make_uint4(a[4], a[5], a[6], a[7]);
-                        if constexpr (BWD) {
-                            *reinterpret_cast<uint4 *>(st + kBox + o0) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-                            *reinterpret_cast<uint4 *>(st + kBox + o1) = make_uint4(wu[4], wu[5], wu[6], wu[7]);
-                        }
+                    if constexpr (!BWD) {
+                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8 + 1)) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
                     }
                     if constexpr (BWD) {
                         const int left = p.F - (f0 + s);
                         if (live && left > 0) {
                             const size_t at = (size_t)row * p.F + f0 + s;
-                            const bool wide = p.wide_f && left >= 16;
-                            store16(p.h + at, wh, left, wide);
-                            store16(p.dg + at, wg, left, wide);
-                            store16(p.du + at, wu, left, wide);
+                            store16(p.h + at, wh, left, p.wide_f && left >= 16);
                         }
                     }
                 }
                 tc_fence_before();
                 if constexpr (C::kOut) fence_async_shared();
-                group_sync(g);
-                if (lead) mbar_arrive_cluster(h_bar);
+                chunk_sync();
+                if (lead) {
+                    mbar_arrive_cluster(h_bar);
+                    if constexpr (BWD && C::kOut) {
+                        // the staged tiles are also what the weight gradients read: whole lines by TMA (stored
+                        // from registers, a warp's 32 rows cost the memory pipe 32 cycles an instruction)
+                        const int row0 = row - r;
+                        if (row0 < p.M && f0 < p.F) {
+                            tma_store_tile(&p.dg_map, smem_u32(st), f0, row0);
+                            tma_store_tile(&p.du_map, smem_u32(st + kBox), f0, row0);
+                        }
+                        store_commit();
+                    }
+                }
             }
         }
+        if (lead) store_wait_all();
     } else if constexpr (C::kOut) {
         // ---------------- the row block's result
         const int quarter = warp & 3, r = quarter * 32 + lane;
-        const bool lead = threadIdx.x == 64 + 256;
+        const bool lead = threadIdx.x == 64 + 512;
         uint32_t i = 0;
         for (int item = pair; item < p.items; item += n_pairs, ++i) {
             const int ob = (int)(i % OB);
@@ -675,6 +721,8 @@ pmha_status ffn_fused_backward(const FfnTc &f, const FfnHiddenArgs &a, const voi
     if (!make_tile_map(&p.x, a.x, a.M, f.E, f.E, 2, 128) || !make_tile_map(&p.dy, a.dy, a.M, f.E, f.E, 2, 128) ||
         !make_tile_map(&p.wg, a.wg, f.F, f.E, f.E, 2, 64) || !make_tile_map(&p.wu, a.wu, f.F, f.E, f.E, 2, 64) ||
         !make_tile_map(&p.wd, a.wd_t, f.F, f.E, f.E, 2, 32) ||
+        !make_tile_map(&p.dg_map, a.dg, a.M, f.F, f.F, 2, 128) ||
+        !make_tile_map(&p.du_map, a.du, a.M, f.F, f.F, 2, 128) ||
         !make_tile_map(&p.wgt, wg_t, f.E, f.F, f.F, 2, (uint32_t)(eb * 32)) ||
         !make_tile_map(&p.wut, wu_t, f.E, f.F, f.F, 2, (uint32_t)(eb * 32))) {
         set_error("ffn_block_backward: cuTensorMapEncodeTiled failed");

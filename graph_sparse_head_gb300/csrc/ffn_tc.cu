@@ -395,28 +395,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     tmem_wait();
                     pin(vg);
                     pin(vu);
-                    float h[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float a = __uint_as_float(vg[j]), b = __uint_as_float(vu[j]);
+                    for (int j = 0; j < 16; j += 2) {
+                        F2 a = f2(__uint_as_float(vg[j]), __uint_as_float(vg[j + 1]));
+                        F2 b = f2(__uint_as_float(vu[j]), __uint_as_float(vu[j + 1]));
+                        const float2 ba = *reinterpret_cast<const float2 *>(v0 + c + j);
+                        const float2 bb = *reinterpret_cast<const float2 *>(v1 + c + j);
                         if constexpr (C::kQ8) {
-                            a = fmaf(a, xs * s0[c + j], v0[c + j]);
-                            b = fmaf(b, xs * s1[c + j], v1[c + j]);
+                            const float2 sa = *reinterpret_cast<const float2 *>(s0 + c + j);
+                            const float2 su = *reinterpret_cast<const float2 *>(s1 + c + j);
+                            a = fma2(a, f2(sa.x, sa.y) * f2(xs), f2(ba.x, ba.y));
+                            b = fma2(b, f2(su.x, su.y) * f2(xs), f2(bb.x, bb.y));
                         } else {
-                            a += v0[c + j];
-                            b += v1[c + j];
+                            a = a + f2(ba.x, ba.y);
+                            b = b + f2(bb.x, bb.y);
                         }
-                        h[j] = Act<ACT>::fast(a) * b;
+                        w[j / 2] = to_bf16x2(Act<ACT>::fast(a) * b);
                     }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = pack_bf16(h[2 * j], h[2 * j + 1]);
                     *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
                     *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             } else if constexpr (KIND == kHidden) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 16) {
-                    uint32_t vg[16], vu[16], vd[16], w[8];
+                    uint32_t vg[16], vu[16], vd[16];
                     tmem_ld16(t0 + (uint32_t)(g * 32 + c), vg);
                     tmem_ld16(t0 + (uint32_t)(64 + g * 32 + c), vu);
                     tmem_ld16(t0 + (uint32_t)(128 + g * 32 + c), vd);
@@ -424,23 +426,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     pin(vg);
                     pin(vu);
                     pin(vd);
-                    float h[16], dg[16], du[16];
+                    uint32_t wo[3][8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float a = __uint_as_float(vg[j]) + v0[c + j], b = __uint_as_float(vu[j]) + v1[c + j];
-                        const float dh = __uint_as_float(vd[j]);
-                        float slope;
-                        const float act = Act<ACT>::fast(a, &slope);
-                        h[j] = act * b;
-                        du[j] = dh * act;
-                        dg[j] = dh * b * slope;
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 ba = *reinterpret_cast<const float2 *>(v0 + c + j);
+                        const float2 bb = *reinterpret_cast<const float2 *>(v1 + c + j);
+                        const F2 a = f2(__uint_as_float(vg[j]), __uint_as_float(vg[j + 1])) + f2(ba.x, ba.y);
+                        const F2 b = f2(__uint_as_float(vu[j]), __uint_as_float(vu[j + 1])) + f2(bb.x, bb.y);
+                        const F2 dh = f2(__uint_as_float(vd[j]), __uint_as_float(vd[j + 1]));
+                        F2 slope;
+                        const F2 act = Act<ACT>::fast(a, &slope);
+                        wo[0][j / 2] = to_bf16x2(act * b);
+                        wo[1][j / 2] = to_bf16x2(dh * b * slope);
+                        wo[2][j / 2] = to_bf16x2(dh * act);
                     }
                     const int u = (g * 32 + c) / 8;
 #pragma unroll
                     for (int o = 0; o < 3; ++o) {
-                        const float *src = o == 0 ? h : o == 1 ? dg : du;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) w[j] = pack_bf16(src[2 * j], src[2 * j + 1]);
+                        const uint32_t(&w)[8] = wo[o];
                         uint8_t *sb = out_s + o * kBox;
                         *reinterpret_cast<uint4 *>(sb + swizzled(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
                         *reinterpret_cast<uint4 *>(sb + swizzled(r, u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
