@@ -190,11 +190,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
     for (int i = threadIdx.x; i < p.chunks * 64; i += kThreads) {
         const bool in = i < p.F;
-        bg_s[i] = in && p.bg ? __bfloat162float(p.bg[i]) : 0.f;
-        bu_s[i] = in && p.bu ? __bfloat162float(p.bu[i]) : 0.f;
+        constexpr float kg = BWD ? 1.f : Act<ACT>::kGate, ku = BWD ? 1.f : Act<ACT>::kUp;
+        bg_s[i] = in && p.bg ? kg * __bfloat162float(p.bg[i]) : 0.f;
+        bu_s[i] = in && p.bu ? ku * __bfloat162float(p.bu[i]) : 0.f;
         if constexpr (Q8) {
-            gs_s[i] = in ? p.gs[i] : 0.f;
-            us_s[i] = in ? p.us[i] : 0.f;
+            gs_s[i] = in ? kg * p.gs[i] : 0.f;
+            us_s[i] = in ? ku * p.us[i] : 0.f;
         }
     }
     for (int i = threadIdx.x; i < EB * 64; i += kThreads) bd_s[i] = p.bd && i < p.E ? __bfloat162float(p.bd[i]) : 0.f;
@@ -431,41 +432,42 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                         }
                         const float *bg = bg_s + f0 + s + q, *bu = bu_s + f0 + s + q;
                         const float *gs = gs_s + f0 + s + q, *us = us_s + f0 + s + q;
-                        auto pair_of = [](const uint32_t (&v)[kW], int j) {
-                            return f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                        };
 #pragma unroll
                         for (int j = 0; j < kW; j += 4) {
                             const float4 b4 = *reinterpret_cast<const float4 *>(bg + j);
                             const float4 c4 = *reinterpret_cast<const float4 *>(bu + j);
-                            float4 m4 = {}, n4 = {};
+                            const float bj[4] = {b4.x, b4.y, b4.z, b4.w}, cj[4] = {c4.x, c4.y, c4.z, c4.w};
+                            float mj[4] = {}, nj[4] = {};
                             if constexpr (Q8) {
-                                m4 = *reinterpret_cast<const float4 *>(gs + j);
-                                n4 = *reinterpret_cast<const float4 *>(us + j);
+                                const float4 m4 = *reinterpret_cast<const float4 *>(gs + j);
+                                const float4 n4 = *reinterpret_cast<const float4 *>(us + j);
+                                mj[0] = m4.x, mj[1] = m4.y, mj[2] = m4.z, mj[3] = m4.w;
+                                nj[0] = n4.x, nj[1] = n4.y, nj[2] = n4.z, nj[3] = n4.w;
+                            }
+                            float h[4], dg[4], du[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
+                                if constexpr (BWD) {
+                                    const float d = __uint_as_float(vd[j + e]), u = b + cj[e];
+                                    float slope;
+                                    const float act = Act<ACT>::fast(a + bj[e], &slope);
+                                    h[e] = act * u;
+                                    du[e] = d * act;
+                                    dg[e] = d * u * slope;
+                                } else if constexpr (Q8) {
+                                    h[e] = Act<ACT>::hidden(fmaf(a, xs * mj[e], bj[e]), fmaf(b, xs * nj[e], cj[e]));
+                                } else {
+                                    h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, bj[e]),
+                                                            fmaf(b, Act<ACT>::kUp, cj[e]));
+                                }
                             }
 #pragma unroll
                             for (int e = 0; e < 4; e += 2) {
-                                const F2 bj = e ? f2(b4.z, b4.w) : f2(b4.x, b4.y), cj = e ? f2(c4.z, c4.w) : f2(c4.x, c4.y);
-                                F2 a = pair_of(vg, j + e), b = pair_of(vu, j + e);
-                                if constexpr (Q8) {
-                                    const F2 mj = e ? f2(m4.z, m4.w) : f2(m4.x, m4.y);
-                                    const F2 nj = e ? f2(n4.z, n4.w) : f2(n4.x, n4.y);
-                                    a = fma2(a, mj * f2(xs), bj);
-                                    b = fma2(b, nj * f2(xs), cj);
-                                } else {
-                                    a = a + bj;
-                                    b = b + cj;
-                                }
-                                const int w = (j + e) / 2;
+                                wh[(q + j + e) / 2] = pack_bf16(h[e], h[e + 1]);
                                 if constexpr (BWD) {
-                                    const F2 d = pair_of(vd, j + e);
-                                    F2 slope;
-                                    const F2 act = Act<ACT>::fast(a, &slope);
-                                    wh[q / 2 + w] = to_bf16x2(act * b);
-                                    w1[w] = to_bf16x2(d * act);
-                                    w0[w] = to_bf16x2(d * b * slope);
-                                } else {
-                                    wh[q / 2 + w] = to_bf16x2(Act<ACT>::fast(a) * b);
+                                    w0[(j + e) / 2] = pack_bf16(dg[e], dg[e + 1]);
+                                    w1[(j + e) / 2] = pack_bf16(du[e], du[e + 1]);
                                 }
                             }
                         }

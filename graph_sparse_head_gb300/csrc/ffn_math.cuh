@@ -1,5 +1,5 @@
 // The gate's activation and its derivative, shared by the feed-forward
-// kernels. `fast` forms serve the bf16 block, whose hidden values are rounded
+// kernels. `hidden` and `fast` serve the bf16 block, whose hidden values are rounded
 // to 8 bits of mantissa (2^-9 relative) right after; float32 blocks take the
 // library's expf, erff and division.
 #pragma once
@@ -11,47 +11,6 @@
 namespace pmha {
 namespace {
 
-// Two float32 values in one 64-bit register: one instruction for both on this
-// architecture's packed adders and multipliers.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float a, float b)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
-__device__ __forceinline__ void split(F2 x, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b)
-{
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ uint32_t to_bf16x2(F2 x)
-{
-    float a, b;
-    split(x, a, b);
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&h);
-}
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -64,24 +23,14 @@ __device__ __forceinline__ float rcp(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// the larger, NaN if either is
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-// 1 / a and 1 / b from one reciprocal of their product, for 1 <= a, b <= 2^59.
-// The special-function unit gives 16 results a clock and SM, and the tensor
-// pipe passes 128 x 64 hidden values in 770 clocks: four of them for a pair of
-// values would take longer than the products, three do not.
-__device__ __forceinline__ F2 rcp2(F2 d)
-{
-    float a, b;
-    split(d, a, b);
-    return f2(b, a) * f2(rcp(a * b));
-}
 
+// The fast forms take the gate and the other factor times constants (kGate,
+// kUp) that the caller folds into scales and biases: with the gate times
+// -log2(e) the exponential needs no product of its own, and -ln(2) on the other
+// side undoes it. Two special-function results a value (16 a clock and SM: 128 x
+// 64 values take 1,024 clocks) and seven other instructions, which is what
+// decides a chunk's time; packed float32 pairs and one reciprocal for two
+// values were measured slower (register moves: 15 instructions a value).
 template <int ACT>
 struct Act;
 
@@ -94,25 +43,17 @@ struct Act<PMHA_ACT_SILU> {
         return g * p;
     }
     static __device__ __forceinline__ float exact(float g) { return g / (1.f + expf(-g)); }
-    // sigmoid(g) with g held at -40 (where g sigmoid(g) is -2e-16, and a NaN stays):
-    // a product of two denominators is then at most 2^116
-    static __device__ __forceinline__ F2 sigmoid(F2 &g)
+    static constexpr float kGate = -1.44269504f, kUp = -0.69314718f;
+    // g sigmoid(g) u; a gate far below 0 gives 1 / infinity = 0
+    static __device__ __forceinline__ float hidden(float gate, float up)
     {
-        float a, b;
-        split(g, a, b);
-        g = f2(max_nan(a, -40.f), max_nan(b, -40.f));
-        split(g * f2(-1.44269504f), a, b);
-        return rcp2(f2(fminf(ex2(a), 2.9e17f), fminf(ex2(b), 2.9e17f)) + f2(1.f));
+        return gate * up * rcp(1.f + ex2(gate));
     }
-    static __device__ __forceinline__ F2 fast(F2 g)
+    // act(g) and its slope, from the plain gate
+    static __device__ __forceinline__ float fast(float g, float *slope)
     {
-        const F2 p = sigmoid(g);
-        return g * p;
-    }
-    static __device__ __forceinline__ F2 fast(F2 g, F2 *slope)
-    {
-        const F2 p = sigmoid(g), a = g * p;
-        *slope = fma2(a, fma2(p, f2(-1.f), f2(1.f)), p);
+        const float p = rcp(1.f + ex2(kGate * g)), a = g * p;
+        *slope = fmaf(a, 1.f - p, p);
         return a;
     }
 };
@@ -126,40 +67,33 @@ struct Act<PMHA_ACT_GELU> {
         return g * p;
     }
     static __device__ __forceinline__ float exact(float g) { return g * (0.5f * erfcf(-0.70710678f * g)); }
-    // Phi(g), from Phi(-|g|) = erfc(z) / 2, z = |g| / sqrt(2), by the rational form 7.1.26
-    // of Abramowitz and Stegun (error below 1.5e-7): a polynomial in t = 1 / (1 + p z)
-    // times e^(-z^2), which also gives the density that the slope needs.
-    static __device__ __forceinline__ F2 phi(F2 g, F2 *e)
+    static constexpr float kGate = 1.f, kUp = 1.f;
+    // Phi(-z) for z = min(|g|, 64) (0 from 14 on), by the rational form 7.1.26 of Abramowitz
+    // and Stegun for erfc(z / sqrt(2)) (error below 1.5e-7): a polynomial in
+    // t = 1 / (1 + p z) times e = exp(-g^2 / 2), which the slope needs as well.
+    static __device__ __forceinline__ float lower(float g, float z, float *e)
     {
-        float a, b;
-        split(g, a, b);
-        // past |g| = 64 the exponential is 0 whatever t is
-        const F2 t = rcp2(fma2(f2(fminf(fabsf(a), 64.f), fminf(fabsf(b), 64.f)), f2(0.3275911f * 0.70710678f), f2(1.f)));
-        float u, v;
-        split(g * g * f2(-0.72134752f), u, v);
-        *e = f2(ex2(u), ex2(v));
-        F2 q = fma2(t, f2(0.5f * 1.061405429f), f2(-0.5f * 1.453152027f));
-        q = fma2(t, q, f2(0.5f * 1.421413741f));
-        q = fma2(t, q, f2(-0.5f * 0.284496736f));
-        q = fma2(t, q, f2(0.5f * 0.254829592f));
-        q = q * t * *e;
-        const F2 r = fma2(q, f2(-1.f), f2(1.f));
-        float q0, q1, r0, r1;
-        split(q, q0, q1);
-        split(r, r0, r1);
-        return f2(a < 0.f ? q0 : r0, b < 0.f ? q1 : r1);
+        const float t = rcp(fmaf(z, 0.3275911f * 0.70710678f, 1.f));
+        *e = ex2(g * g * -0.72134752f);
+        float q = fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f);
+        q = fmaf(t, q, 0.5f * 1.421413741f);
+        q = fmaf(t, q, -0.5f * 0.284496736f);
+        q = fmaf(t, q, 0.5f * 0.254829592f);
+        return q * t * *e;
     }
-    static __device__ __forceinline__ F2 fast(F2 g)
+    // g Phi(g) = max(g, 0) - |g| Phi(-|g|)
+    static __device__ __forceinline__ float hidden(float gate, float up)
     {
-        F2 e;
-        return g * phi(g, &e);
+        float e;
+        const float z = fminf(fabsf(gate), 64.f);
+        return fmaf(-z, lower(gate, z, &e), fmaxf(gate, 0.f)) * up;
     }
-    static __device__ __forceinline__ F2 fast(F2 g, F2 *slope)
+    static __device__ __forceinline__ float fast(float g, float *slope)
     {
-        F2 e;
-        const F2 p = phi(g, &e);
-        *slope = fma2(g * f2(0.39894228f), e, p);
-        return g * p;
+        float e;
+        const float z = fminf(fabsf(g), 64.f), q = lower(g, z, &e);
+        *slope = fmaf(g * 0.39894228f, e, 0.5f + copysignf(0.5f - q, g));
+        return fmaf(-z, q, fmaxf(g, 0.f));
     }
 };
 

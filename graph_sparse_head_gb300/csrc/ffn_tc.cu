@@ -332,11 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                 const int limit = KIND == kDown ? p.E : p.F;
                 if (et < kCols) {
                     const bool in = c0 + et < limit;
-                    v0[et] = p.bias0 && in ? __bfloat162float(p.bias0[c0 + et]) : 0.f;
-                    if constexpr (KIND != kDown) v1[et] = p.bias1 && in ? __bfloat162float(p.bias1[c0 + et]) : 0.f;
+                    constexpr float kg = C::kIsUp ? Act<ACT>::kGate : 1.f, ku = C::kIsUp ? Act<ACT>::kUp : 1.f;
+                    v0[et] = p.bias0 && in ? kg * __bfloat162float(p.bias0[c0 + et]) : 0.f;
+                    if constexpr (KIND != kDown) v1[et] = p.bias1 && in ? ku * __bfloat162float(p.bias1[c0 + et]) : 0.f;
                     if constexpr (C::kQ8) {
-                        s0[et] = in ? p.gs[c0 + et] : 0.f;
-                        s1[et] = in ? p.us[c0 + et] : 0.f;
+                        s0[et] = in ? kg * p.gs[c0 + et] : 0.f;
+                        s1[et] = in ? ku * p.us[c0 + et] : 0.f;
                     }
                 }
                 if constexpr (C::kQ8) xs = live ? p.xs[row0 + r] : 0.f;
@@ -397,20 +398,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     pin(vu);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        F2 a = f2(__uint_as_float(vg[j]), __uint_as_float(vg[j + 1]));
-                        F2 b = f2(__uint_as_float(vu[j]), __uint_as_float(vu[j + 1]));
-                        const float2 ba = *reinterpret_cast<const float2 *>(v0 + c + j);
-                        const float2 bb = *reinterpret_cast<const float2 *>(v1 + c + j);
-                        if constexpr (C::kQ8) {
-                            const float2 sa = *reinterpret_cast<const float2 *>(s0 + c + j);
-                            const float2 su = *reinterpret_cast<const float2 *>(s1 + c + j);
-                            a = fma2(a, f2(sa.x, sa.y) * f2(xs), f2(ba.x, ba.y));
-                            b = fma2(b, f2(su.x, su.y) * f2(xs), f2(bb.x, bb.y));
-                        } else {
-                            a = a + f2(ba.x, ba.y);
-                            b = b + f2(bb.x, bb.y);
+                        float h[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
+                            const int q = c + j + e;
+                            if constexpr (C::kQ8)
+                                h[e] = Act<ACT>::hidden(fmaf(a, xs * s0[q], v0[q]), fmaf(b, xs * s1[q], v1[q]));
+                            else
+                                h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, v0[q]), fmaf(b, Act<ACT>::kUp, v1[q]));
                         }
-                        w[j / 2] = to_bf16x2(Act<ACT>::fast(a) * b);
+                        w[j / 2] = pack_bf16(h[0], h[1]);
                     }
                     *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
                     *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -429,16 +427,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     uint32_t wo[3][8];
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        const float2 ba = *reinterpret_cast<const float2 *>(v0 + c + j);
-                        const float2 bb = *reinterpret_cast<const float2 *>(v1 + c + j);
-                        const F2 a = f2(__uint_as_float(vg[j]), __uint_as_float(vg[j + 1])) + f2(ba.x, ba.y);
-                        const F2 b = f2(__uint_as_float(vu[j]), __uint_as_float(vu[j + 1])) + f2(bb.x, bb.y);
-                        const F2 dh = f2(__uint_as_float(vd[j]), __uint_as_float(vd[j + 1]));
-                        F2 slope;
-                        const F2 act = Act<ACT>::fast(a, &slope);
-                        wo[0][j / 2] = to_bf16x2(act * b);
-                        wo[1][j / 2] = to_bf16x2(dh * b * slope);
-                        wo[2][j / 2] = to_bf16x2(dh * act);
+                        float h[2], dg[2], du[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float b = __uint_as_float(vu[j + e]) + v1[c + j + e], dh = __uint_as_float(vd[j + e]);
+                            float slope;
+                            const float act = Act<ACT>::fast(__uint_as_float(vg[j + e]) + v0[c + j + e], &slope);
+                            h[e] = act * b;
+                            dg[e] = dh * b * slope;
+                            du[e] = dh * act;
+                        }
+                        wo[0][j / 2] = pack_bf16(h[0], h[1]);
+                        wo[1][j / 2] = pack_bf16(dg[0], dg[1]);
+                        wo[2][j / 2] = pack_bf16(du[0], du[1]);
                     }
                     const int u = (g * 32 + c) / 8;
 #pragma unroll
