@@ -22,7 +22,7 @@ namespace {
 constexpr int64_t kL2Block = 64 << 20;  // bytes of hidden values (h, or h, dg and du) of a block of rows
 constexpr int64_t kMostBlock = 256 << 20;
 constexpr int64_t kFusedRows = 2048;    // rows from which the forward pass runs as one kernel
-constexpr int kSumParts = 32;           // row ranges of the bias sums
+constexpr int kSumParts = 32;           // row ranges of a float32 block's bias sums
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
@@ -192,33 +192,32 @@ __global__ void __launch_bounds__(256) k_transpose(Transposes t)
         if (c0 + i < cols && r0 + x < rows) t.out[z][(int64_t)(c0 + i) * rows + r0 + x] = sh[x][i];
 }
 
-// Column sums of up to three matrices over this block of rows, by kSumParts
-// row ranges: out[z][range][col] (+)=
+// Column sums of a float32 block's dg, du and dy over this block of rows, by kSumParts
+// row ranges: out[range][2 F + E] (+)=
 struct Sums {
-    const void *in[3];
-    float *out[3];
-    int cols[3];
+    const float *in[3];
+    float *out;
+    int cols[3], at[3], width;
     int64_t rows;
     bool accumulate;
 };
-template <typename T>
 __global__ void __launch_bounds__(256) k_colsum(Sums s)
 {
     __shared__ float sh[8][33];
     const int z = blockIdx.z, cols = s.cols[z], c = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
     if (!s.in[z] || blockIdx.x * 32 >= cols) return;
     const int64_t per = (s.rows + kSumParts - 1) / kSumParts, r0 = blockIdx.y * per, r1 = min(s.rows, r0 + per);
-    const T *in = (const T *)s.in[z];
+    const float *in = s.in[z];
     float v = 0.f;
     if (c < cols)
 #pragma unroll 8
-        for (int64_t r = r0 + y; r < r1; r += 8) v += to_f<T>(in[r * cols + c]);
+        for (int64_t r = r0 + y; r < r1; r += 8) v += in[r * cols + c];
     sh[y][threadIdx.x % 32] = v;
     __syncthreads();
     if (y == 0 && c < cols) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) v += sh[i][threadIdx.x];
-        float *o = s.out[z] + (int64_t)blockIdx.y * cols + c;
+        float *o = s.out + (int64_t)blockIdx.y * s.width + s.at[z] + c;
         *o = s.accumulate ? *o + v : v;
     }
 }
@@ -226,9 +225,9 @@ __global__ void __launch_bounds__(256) k_colsum(Sums s)
 struct Finish {
     const float *part;  // [splits][3][F2][E2]
     void *w[3];         // (F, E), (F, E), (E, F) or null
-    const float *sums[3];
+    const float *sums;  // [sum_parts][2 F2 + E2]
     void *b[3];         // (F), (F), (E) or null
-    int splits;
+    int splits, sum_parts;
     int E, F, E2, F2;   // widths of the gradients and of the products
 };
 // Parameter gradients from the partial sums, each added in a fixed order.
@@ -242,11 +241,10 @@ __global__ void __launch_bounds__(256) k_finish(Finish p)
         const int col = (blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const int n = i == 2 ? p.E : p.F, n2 = i == 2 ? p.E2 : p.F2;
-            if (!p.b[i] || col >= n) continue;
+            if (!p.b[i] || col >= (i == 2 ? p.E : p.F)) continue;
             float v = 0.f;
 #pragma unroll 8
-            for (int k = 0; k < kSumParts; ++k) v += p.sums[i][(int64_t)k * n2 + col];
+            for (int k = 0; k < p.sum_parts; ++k) v += p.sums[(int64_t)k * (2 * p.F2 + p.E2) + i * p.F2 + col];
             ((T *)p.b[i])[col] = from_f<T>(v);
         }
         return;
@@ -355,7 +353,7 @@ struct Plan {
     size_t x, dy, out;              // padded rows of a block (dy: dy or the residual)
     size_t wgt, wut, wdt;           // transposed weights (backward)
     size_t h, dg, du, part, sums;
-    int splits;
+    int splits, sum_parts;
     size_t total;
 };
 
@@ -403,7 +401,8 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward)
         l.part = o;
         o += align256((size_t)l.splits * 3 * (size_t)(l.E2 * l.F2) * 4);
         l.sums = o;
-        o += align256((size_t)kSumParts * (size_t)(2 * l.F2 + l.E2) * 4);
+        l.sum_parts = bf16 ? l.splits : kSumParts;
+        o += align256((size_t)l.sum_parts * (size_t)(2 * l.F2 + l.E2) * 4);
     }
     l.total = o;
     return l;
@@ -693,12 +692,11 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                     PMHA_TRY(ffn_tc_dx(tc, ws + l.dg, ws + l.du, ws + l.wgt, ws + l.wut, M, dxp, s));
                 if (l.padded) PMHA_TRY(repitch(ws + l.out, M, l.E2, M, E, dxr, s));
             }
-            if (any_w) {
-                FfnDwArgs d = {ws + l.dg, ws + l.du, ws + l.h, xp, dyp, M, part, gw[0] || gw[1], gw[2] != nullptr, !first,
-                               l.splits};
+            if (any_w || any_b) {
+                FfnDwArgs d = {ws + l.dg, ws + l.du, ws + l.h, xp, dyp, M, part, any_b ? sums : nullptr,
+                               gw[0] || gw[1] || gb[0] || gb[1], gw[2] || gb[2], !first, l.splits};
                 PMHA_TRY(ffn_tc_dw(tc, d, s));
             }
-            xr = xp, dyr = dyp;
         } else {
             F32Args a = {};
             a.x = (const float *)xr, a.dy = (const float *)dyr, a.wg = (const float *)p->wg;
@@ -721,28 +719,24 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 k_f32_dw<<<f32_grid(F, E, 3 * l.splits), 256, 0, s>>>(a, part, l.splits, !first);
                 PMHA_TRY(launched());
             }
-        }
-        if (any_b) {
-            Sums c = {};
-            c.in[0] = gb[0] ? ws + l.dg : nullptr, c.in[1] = gb[1] ? ws + l.du : nullptr, c.in[2] = gb[2] ? dyr : nullptr;
-            c.out[0] = sums, c.out[1] = sums + kSumParts * l.F2, c.out[2] = sums + 2 * kSumParts * l.F2;
-            c.cols[0] = c.cols[1] = (int)l.F2, c.cols[2] = (int)l.E2;
-            c.rows = M, c.accumulate = !first;
-            const dim3 grid((unsigned)ceil_div(std::max(l.E2, l.F2), 32), kSumParts, 3);
-            StageTimer timer("ffn_bias_sums", s);
-            if (bf16) k_colsum<__nv_bfloat16><<<grid, 256, 0, s>>>(c);
-            else k_colsum<float><<<grid, 256, 0, s>>>(c);
-            PMHA_TRY(launched());
+            if (any_b) {
+                Sums c = {};
+                c.in[0] = a.dg, c.in[1] = a.du, c.in[2] = a.dy;
+                c.out = sums;
+                c.cols[0] = c.cols[1] = (int)F, c.cols[2] = (int)E;
+                c.at[1] = (int)F, c.at[2] = (int)(2 * F), c.width = (int)(2 * F + E);
+                c.rows = M, c.accumulate = !first;
+                StageTimer timer("ffn_bias_sums", s);
+                k_colsum<<<dim3((unsigned)ceil_div(std::max(E, F), 32), kSumParts, 3), 256, 0, s>>>(c);
+                PMHA_TRY(launched());
+            }
         }
     }
     if (any_w || any_b) {
         Finish f = {};
-        f.part = part, f.splits = l.splits;
+        f.part = part, f.splits = l.splits, f.sums = sums, f.sum_parts = l.sum_parts;
         f.E = (int)E, f.F = (int)F, f.E2 = (int)l.E2, f.F2 = (int)l.F2;
-        for (int i = 0; i < 3; ++i) {
-            f.w[i] = gw[i], f.b[i] = gb[i];
-            f.sums[i] = sums + (i == 0 ? 0 : i == 1 ? kSumParts * l.F2 : 2 * kSumParts * l.F2);
-        }
+        for (int i = 0; i < 3; ++i) f.w[i] = gw[i], f.b[i] = gb[i];
         const dim3 grid((unsigned)ceil_div(E, 32), (unsigned)ceil_div(F, 32), 4);
         StageTimer timer("ffn_grads", s);
         if (bf16) k_finish<__nv_bfloat16><<<grid, 256, 0, s>>>(f);

@@ -188,21 +188,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
-    for (int i = threadIdx.x; i < p.chunks * 64; i += kThreads) {
-        const bool in = i < p.F;
-        constexpr float kg = BWD ? 1.f : Act<ACT>::kGate, ku = BWD ? 1.f : Act<ACT>::kUp;
-        bg_s[i] = in && p.bg ? kg * __bfloat162float(p.bg[i]) : 0.f;
-        bu_s[i] = in && p.bu ? ku * __bfloat162float(p.bu[i]) : 0.f;
-        if constexpr (Q8) {
-            gs_s[i] = in ? kg * p.gs[i] : 0.f;
-            us_s[i] = in ? ku * p.us[i] : 0.f;
-        }
-    }
-    for (int i = threadIdx.x; i < EB * 64; i += kThreads) bd_s[i] = p.bd && i < p.E ? __bfloat162float(p.bd[i]) : 0.f;
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+    grid_dependency_wait();
 
     // item -> row block, first chunk; every item has the chunks of one part (the last part may have fewer)
     auto chunks_of = [&](int item) { return min(p.per_part, p.chunks - (item % p.parts) * p.per_part); };
@@ -400,6 +390,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
         auto chunk_sync = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory"); };
         uint8_t *st = staged + g * C::kStaged;
         const uint32_t h_bar = map_rank(smem_u32(&h_full[g]), 0);
+        for (int i = threadIdx.x - 64; i < p.chunks * 64; i += 512) {
+            const bool in = i < p.F;
+            constexpr float kg = BWD ? 1.f : Act<ACT>::kGate, ku = BWD ? 1.f : Act<ACT>::kUp;
+            bg_s[i] = in && p.bg ? kg * __bfloat162float(p.bg[i]) : 0.f;
+            bu_s[i] = in && p.bu ? ku * __bfloat162float(p.bu[i]) : 0.f;
+            if constexpr (Q8) {
+                gs_s[i] = in ? kg * p.gs[i] : 0.f;
+                us_s[i] = in ? ku * p.us[i] : 0.f;
+            }
+        }
+        asm volatile("bar.sync 4, 512;" ::: "memory");  // both groups: the vectors are there
         uint32_t k = 0;
         for (int item = pair; item < p.items; item += n_pairs) {
             const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
@@ -518,6 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
         // ---------------- the row block's result
         const int quarter = warp & 3, r = quarter * 32 + lane;
         const bool lead = threadIdx.x == 64 + 512;
+        for (int i = threadIdx.x - 576; i < EB * 64; i += 128)
+            bd_s[i] = p.bd && i < p.E ? __bfloat162float(p.bd[i]) : 0.f;
+        group_sync(2);
         uint32_t i = 0;
         for (int item = pair; item < p.items; item += n_pairs, ++i) {
             const int ob = (int)(i % OB);
@@ -649,12 +653,8 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     p.per_part = (p.chunks + p.parts - 1) / p.parts;
     p.parts = (p.chunks + p.per_part - 1) / p.per_part;
     p.items *= p.parts;
-    const int grid = 2 * std::min(pairs, p.items);
     StageTimer timer(stage, s);
-    kern<<<grid, kThreads, C::kSmem, s>>>(p);
-    count_launch();
-    PMHA_CUDA_TRY(cudaGetLastError());
-    return PMHA_OK;
+    return launch_pairs(kern, 2 * std::min(pairs, p.items), kThreads, C::kSmem, s, p);
 }
 
 template <int EB, bool BWD, bool Q8>

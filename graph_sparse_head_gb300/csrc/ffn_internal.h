@@ -46,11 +46,12 @@ pmha_status ffn_tc_dx(const FfnTc &f, const void *dg, const void *du, const void
                       void *dx, cudaStream_t s);
 // Partial weight gradients over the M rows, all three as (F, E) float32:
 // part[split][0..2] (+)= dg^T x, du^T x, h^T dy; the row range is cut into
-// ffn_dw_splits() pieces. `accumulate` adds to what part holds.
+// ffn_dw_splits() pieces. `accumulate` adds to what part holds. sums, where not
+// null, takes the column sums of dg, du and dy: (split, 2 F + E).
 struct FfnDwArgs {
     const void *dg, *du, *h, *x, *dy;
     int64_t M;
-    float *part;
+    float *part, *sums;
     bool gate_up, down;  // which of the products are wanted
     bool accumulate;
     int splits;

@@ -7,13 +7,13 @@
 //   dx      dg Wg + du Wu                             the down kernel with two pairs of operands
 //   dw      dg^T x, du^T x, h^T dy                    tile 256 hidden x 128 or 256 columns, operands as they lie
 //
-// Two CTAs form a pair (tc_pair.cuh). Each has 10 warps: warp 0 copies
+// Two CTAs form a pair (tc_pair.cuh). Each has 18 warps: warp 0 copies
 // 128-byte-wide operand tiles by TMA into a ring of stages, warp 1 of the even
 // CTA issues tcgen05.mma into accumulators in tensor memory (two, so that the
-// products of one tile run under the epilogue of the last), and two groups of
-// four warps turn accumulators into outputs: each thread reads its row's
-// columns, applies the tile's arithmetic, writes the result to a swizzled
-// tile in shared memory, and one thread stores that by TMA. Pairs are
+// products of one tile run under the epilogue of the last), and four groups of
+// four warps turn accumulators into outputs: each thread reads a quarter of
+// its row's columns, applies the tile's arithmetic, writes the result to a
+// swizzled tile in shared memory, and one thread stores that by TMA. Pairs are
 // persistent and take tiles in order, the column tiles of one row block side
 // by side, so that the rows come from L2 after their first read.
 //
@@ -36,7 +36,7 @@ namespace pmha {
 namespace {
 using namespace tcu;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 64 + 512;
 constexpr int kBox = 128 * 128;  // bytes of a tile of 128 rows of 128 bytes
 enum Kind { kUp, kUpQ8, kDown, kHidden, kDw };
 
@@ -50,40 +50,43 @@ struct Cfg {
                               : kIsUp ? kBox                            // 128 rows of Wg or Wu
                                       : BN / 2 * 128;                   // half of the columns
     static constexpr int kStage = kA + kB;
-    static constexpr int kOut = KIND == kHidden ? 3 * kBox : KIND == kDw ? 0 : kIsUp ? 2 * kBox : BN / 64 * kBox;
-    static constexpr int kAccCols = KIND == kHidden ? 192 : kIsUp ? 256 : BN;
-    static constexpr int kAccStride = kAccCols > 128 ? 256 : 128;
-    static constexpr int kTmemCols = 2 * kAccStride;
-    static constexpr int kVec = 4 * 256 * 4;  // bias and scale columns, float32
+    static constexpr int kCols = kIsUp ? 128 : KIND == kHidden ? 64 : BN;  // output columns of a tile
+    static constexpr int kPart = kCols / 4;                                // of one of the four warp groups
+    static constexpr int kTile = KIND == kHidden ? 3 * kBox : KIND == kDw ? 0 : kCols / 64 * kBox;  // output tile
+    static constexpr int kTiles = kTile <= 2 * kBox ? 2 : 1;  // output tiles in shared memory
+    static constexpr int kAccCols = KIND == kHidden ? 192 : kIsUp ? 256 : KIND == kDw ? 2 * BN : BN;
+    static constexpr int kAccStride = kAccCols > 256 ? 512 : kAccCols > 128 ? 256 : 128;
+    static constexpr int kAccs = kAccStride == 512 || KIND == kDw ? 1 : 2;
+    static constexpr int kTmemCols = kAccs * kAccStride;
+    static constexpr int kVec = KIND == kDw ? 4096 : 2 * 4 * 128 * 4;  // bias and scale columns of two tiles, or ones
     static constexpr int kBars = 512;
-    static constexpr int kFit = (232448 - 1024 - kOut - kVec - kBars) / kStage;
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static constexpr int kSmem = 1024 + kStages * kStage + kOut + kVec + kBars;
+    static constexpr int kFit = (232448 - 1024 - kTiles * kTile - kVec - kBars) / kStage;
+    static constexpr int kStages = kFit > 7 ? 7 : kFit;
+    static constexpr int kSmem = 1024 + kStages * kStage + kTiles * kTile + kVec + kBars;
     static_assert(kStages >= 3, "a ring of at least three stages");
     static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
 struct Params {
     CUtensorMap a0, a1, a2, b0, b1, b2, o0, o1, o2, res;
-    int M, E, F;            // tokens, outer and hidden width
+    int M, E, F;            // tokens (dw: hidden rows of the result), outer and hidden width
     int n_tiles, tiles_n;   // pair tiles, column tiles of one row block
     int kb;                 // K blocks of one operand pair
     int segs;               // operand pairs (down: 1; dx: 2)
     const __nv_bfloat16 *bias0, *bias1;
     const float *xs, *gs, *us;
     int has_res;
-    // dw: row blocks [split * kb_per, ...) of 64 tokens; products `what`
+    // dw: row blocks [split * kb_per, ...) of 64 tokens; products from first_what on
     int splits, kb_per, tiles_m, first_what, accumulate;
-    float *part;
+    float *part, *sums;     // dw: partial products; column sums (split, 2 F + E) or null
     int *err;
 };
 
-// accumulator columns c .. c + 31 of this warp's 32 rows
+// accumulator columns of this warp's 32 rows
 __device__ __forceinline__ uint32_t tmem_at(uint32_t base, int quarter, int col)
 {
     return base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
 }
-// two such reads in flight before one wait
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
@@ -101,21 +104,23 @@ __device__ __forceinline__ void pin(uint32_t (&r)[16])
 #pragma unroll
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
+// named barrier 1 over the epilogue's 512 threads
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
-// named barrier 3 over both epilogue groups
-__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
-__device__ __forceinline__ bool both_sync_or(bool pred)
+// Partial sums: one CTA owns each value and the launches that add to it follow
+// one another, so the additions' order is fixed; they need no read of their own.
+__device__ __forceinline__ void put4(float *p, float a, float b, float c, float d, bool add)
 {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 3, 256, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)pred)
-        : "memory");
-    return r != 0;
+    if (add)
+        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+    else
+        *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void put1(float *p, float a, bool add)
+{
+    if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(a) : "memory");
+    else *p = a;
 }
 
 template <int KIND, int BN, int ACT>
@@ -126,16 +131,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *out_s = smem + kStages * C::kStage;
-    float *vec_s = (float *)(out_s + C::kOut);  // [4][256]
+    float *vec_s = (float *)(out_s + C::kTiles * C::kTile);     // [2][4][128]; dw: 4 KB of bf16 ones
     uint64_t *full = (uint64_t *)((uint8_t *)vec_s + C::kVec);  // [kStages], counted in the even CTA
     uint64_t *empty = full + kStages;                           // [kStages], in each CTA
     uint64_t *acc_full = empty + kStages;                       // [2], in each CTA
     uint64_t *acc_empty = acc_full + 2;                         // [2], counted in the even CTA
     uint64_t *mma_done = acc_empty + 2;
-    uint64_t *res_full = mma_done + 1;                          // [2]: the residual's tile of each group
-    uint32_t *tmem_holder = (uint32_t *)(res_full + 2);
+    uint64_t *res_full = mma_done + 1;                          // the residual's tile
+    uint32_t *tmem_holder = (uint32_t *)(res_full + 1);
     volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
-    int *issued = (int *)(tmem_holder + 2);  // [kStages]
+    volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -145,27 +150,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
-            issued[s] = 0;
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), 4);  // two groups in each CTA
-            mbar_init(smem_u32(&res_full[i]), 1);
+            mbar_init(smem_u32(&acc_empty[i]), 2);  // the epilogue of either CTA
         }
         mbar_init(smem_u32(mma_done), 1);
+        mbar_init(smem_u32(res_full), 1);
         *abort_flag = 0;
+        *armed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), C::kTmemCols);
+    if constexpr (KIND == kDw) {
+        for (int i = threadIdx.x; i < 1024; i += kThreads) ((uint32_t *)vec_s)[i] = 0x3f803f80u;
+        fence_async_shared();
+    }
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
+    grid_dependency_wait();
     const uint32_t tmem = *tmem_holder;
 
     // tile -> (row block of 256, column tile, K blocks, product of dw)
     auto decode = [&](int tile, int &m, int &n, int &kb0, int &kb1, int &what) {
         kb0 = 0;
-        kb1 = p.kb;
+        kb1 = KIND == kDown ? p.segs * p.kb : p.kb;
         what = 0;
         if constexpr (KIND == kDw) {
             const int per = p.tiles_m * p.tiles_n;
@@ -181,218 +191,221 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- TMA producer of this CTA
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int tile = pair; tile < p.n_tiles && !*abort_flag; tile += n_pairs) {
-                int m, n, kb0, kb1, what;
-                decode(tile, m, n, kb0, kb1, what);
-                const int row = m * 256 + (int)rank * 128;
-                const int n_kb = KIND == kDown ? p.segs * p.kb : kb1;
-                for (int kb = kb0; kb < n_kb; ++kb) {
-                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p.err)) break;
-                    const uint32_t fb = map_rank(smem_u32(&full[stage]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * C::kStage);
-                    issued[stage] += 1;
-                    const uint32_t sa = smem_u32(smem + stage * C::kStage), sb = sa + C::kA;
-                    if constexpr (C::kIsUp) {
-                        constexpr int kElems = C::kQ8 ? 128 : 64;
-                        tma_load_2d_pair(sa, &p.a0, kb * kElems, row, fb);
-                        tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * kElems, n * 128, fb);
-                    } else if constexpr (KIND == kHidden) {
-                        tma_load_2d_pair(sa, &p.a0, kb * 64, row, fb);
-                        tma_load_2d_pair(sa + kBox, &p.a1, kb * 64, row, fb);
-                        tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * 64, n * 64, fb);
-                        tma_load_2d_pair(sb + kBox / 2, &p.b2, kb * 64, n * 64 + (int)rank * 32, fb);
-                    } else if constexpr (KIND == kDown) {
-                        const bool second = kb >= p.kb;
-                        const int k = (second ? kb - p.kb : kb) * 64;
-                        tma_load_2d_pair(sa, second ? &p.a1 : &p.a0, k, row, fb);
-                        tma_load_2d_pair(sb, second ? &p.b1 : &p.b0, k, n * BN + (int)rank * (BN / 2), fb);
-                    } else {
-                        const CUtensorMap *ma = what == 0 ? &p.a0 : what == 1 ? &p.a1 : &p.a2;
-                        const CUtensorMap *mb = what == 2 ? &p.b1 : &p.b0;
-                        tma_load_2d_pair(sa, ma, row, kb * 64, fb);
-                        tma_load_2d_pair(sa + kBox / 2, ma, row + 64, kb * 64, fb);
+        // ---------------- TMA producer of this CTA
+        const bool one = elect_one();
+        uint32_t made = 0;
+        for (int tile = pair; tile < p.n_tiles && !*abort_flag; tile += n_pairs) {
+            int m, n, kb0, kb1, what;
+            decode(tile, m, n, kb0, kb1, what);
+            const int row = m * 256 + (int)rank * 128;
+            for (int kb = kb0; kb < kb1; ++kb, ++made) {
+                const int stage = (int)(made % kStages);
+                if (!wait_bar(smem_u32(&empty[stage]), ((made / kStages) & 1u) ^ 1u, abort_flag, p.err)) break;
+                if (!one) continue;
+                const uint32_t fb = map_rank(smem_u32(&full[stage]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * C::kStage);
+                *armed = made + 1;
+                const uint32_t sa = smem_u32(smem + stage * C::kStage), sb = sa + C::kA;
+                if constexpr (C::kIsUp) {
+                    constexpr int kElems = C::kQ8 ? 128 : 64;
+                    tma_load_2d_pair(sa, &p.a0, kb * kElems, row, fb);
+                    tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * kElems, n * 128, fb);
+                } else if constexpr (KIND == kHidden) {
+                    tma_load_2d_pair(sa, &p.a0, kb * 64, row, fb);
+                    tma_load_2d_pair(sa + kBox, &p.a1, kb * 64, row, fb);
+                    tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * 64, n * 64, fb);
+                    tma_load_2d_pair(sb + kBox / 2, &p.b2, kb * 64, n * 64 + (int)rank * 32, fb);
+                } else if constexpr (KIND == kDown) {
+                    const bool second = kb >= p.kb;
+                    const int k = (second ? kb - p.kb : kb) * 64;
+                    tma_load_2d_pair(sa, second ? &p.a1 : &p.a0, k, row, fb);
+                    tma_load_2d_pair(sb, second ? &p.b1 : &p.b0, k, n * BN + (int)rank * (BN / 2), fb);
+                } else {
+                    const CUtensorMap *ma = what == 0 ? &p.a0 : what == 1 ? &p.a1 : &p.a2;
+                    const CUtensorMap *mb = what == 2 ? &p.b1 : &p.b0;
+                    tma_load_2d_pair(sa, ma, row, kb * 64, fb);
+                    tma_load_2d_pair(sa + kBox / 2, ma, row + 64, kb * 64, fb);
 #pragma unroll
-                        for (int j = 0; j < BN / 128; ++j)
-                            tma_load_2d_pair(sb + j * (kBox / 2), mb, n * BN + (int)rank * (BN / 2) + j * 64, kb * 64,
-                                             fb);
-                    }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    for (int j = 0; j < BN / 128; ++j)
+                        tma_load_2d_pair(sb + j * (kBox / 2), mb, n * BN + (int)rank * (BN / 2) + j * 64, kb * 64, fb);
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // ---------------- MMA issuer of the pair
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            for (int tile = pair; tile < p.n_tiles && !*abort_flag; tile += n_pairs) {
+        if (rank == 0) {
+            // ---------------- MMA issuer of the pair: the whole warp walks, so that addresses stay in uniform
+            // registers; one lane issues
+            const bool one = elect_one();
+            uint32_t used = 0, i = 0;
+            bool ok = true;
+            for (int tile = pair; tile < p.n_tiles && ok; tile += n_pairs, ++i) {
                 int m, n, kb0, kb1, what;
                 decode(tile, m, n, kb0, kb1, what);
-                const int n_kb = KIND == kDown ? p.segs * p.kb : kb1;
-                if (!mbar_wait(smem_u32(&acc_empty[acc]), acc_phase ^ 1u, abort_flag, p.err)) break;
+                const int acc = (int)(i % C::kAccs);
+                if (!wait_bar(smem_u32(&acc_empty[acc]), ((i / C::kAccs) & 1u) ^ 1u, abort_flag, p.err)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * C::kAccStride);
-                bool ok = true;
-                for (int kb = kb0; kb < n_kb; ++kb) {
-                    if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
+                for (int kb = kb0; kb < kb1; ++kb, ++used) {
+                    const int stage = (int)(used % kStages);
+                    ok = wait_bar(smem_u32(&full[stage]), (used / kStages) & 1u, abort_flag, p.err);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * C::kStage), sb = sa + C::kA;
                     const uint32_t more = kb > kb0 ? 1u : 0u;
-                    if constexpr (KIND == kDw) {
-                        const uint64_t da = smem_desc_mn(sa, kBox / 2), db = smem_desc_mn(sb, kBox / 2);
+                    if (one) {
+                        if constexpr (KIND == kDw) {
+                            const uint64_t da = smem_desc_mn(sa, kBox / 2), db = smem_desc_mn(sb, kBox / 2);
+                            // a tile of ones takes the place of an operand for the column sums: of dg and du
+                            // beside the first column tile, of dy beside the first row block of h^T dy
+                            const uint64_t ones = smem_desc_mn(smem_u32(vec_s), 2048);
+                            const bool rows = p.sums && what < 2 && n == 0, cols = p.sums && what == 2 && m == 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 16 tokens = 2048 bytes
-                            mma_pair<false>(d, da + (uint64_t)(128 * k), db + (uint64_t)(128 * k),
-                                            idesc_of(false, true, 256, BN), more | (k > 0));
-                    } else {
-                        const uint64_t da = smem_desc(sa), db = smem_desc(sb);
+                            for (int k = 0; k < 4; ++k) {  // 16 tokens = 2048 bytes
+                                const uint64_t ak = da + (uint64_t)(128 * k), bk = db + (uint64_t)(128 * k);
+                                mma_pair<false>(d, ak, bk, idesc_of(false, true, 256, BN), more | (k > 0));
+                                if (rows) mma_pair<false>(d + BN, ak, ones, idesc_of(false, true, 256, 32), more | (k > 0));
+                                if (cols) mma_pair<false>(d + BN, ones, bk, idesc_of(false, true, 256, BN), more | (k > 0));
+                            }
+                        } else {
+                            const uint64_t da = smem_desc(sa), db = smem_desc(sb);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 32 bytes along K = 2 in the address field
-                            mma_pair<C::kQ8>(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k),
-                                             idesc_of(C::kQ8, false, 256, KIND == kHidden ? 128 : C::kAccCols),
-                                             more | (k > 0));
-                        if constexpr (KIND == kHidden) {
-                            const uint64_t da1 = smem_desc(sa + kBox), db1 = smem_desc(sb + kBox / 2);
+                            for (int k = 0; k < 4; ++k)  // 32 bytes along K = 2 in the address field
+                                mma_pair<C::kQ8>(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k),
+                                                 idesc_of(C::kQ8, false, 256, KIND == kHidden ? 128 : C::kAccCols),
+                                                 more | (k > 0));
+                            if constexpr (KIND == kHidden) {
+                                const uint64_t da1 = smem_desc(sa + kBox), db1 = smem_desc(sb + kBox / 2);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_pair<false>(d + 128, da1 + (uint64_t)(2 * k), db1 + (uint64_t)(2 * k),
-                                                idesc_of(false, false, 256, 64), more | (k > 0));
+                                for (int k = 0; k < 4; ++k)
+                                    mma_pair<false>(d + 128, da1 + (uint64_t)(2 * k), db1 + (uint64_t)(2 * k),
+                                                    idesc_of(false, false, 256, 64), more | (k > 0));
+                            }
                         }
+                        mma_commit_pair(smem_u32(&empty[stage]));
                     }
-                    mma_commit_pair(smem_u32(&empty[stage]));
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    __syncwarp();
                 }
-                if (!ok) break;
-                mma_commit_pair(smem_u32(&acc_full[acc]));
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1u;
-                }
+                if (one && ok) mma_commit_pair(smem_u32(&acc_full[acc]));
+                __syncwarp();
             }
-            mma_commit_pair(smem_u32(mma_done));
+            if (one) mma_commit_pair(smem_u32(mma_done));
+            __syncwarp();
             int dummy = 0;
             mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
     } else {
-        // ---------------- epilogue: group g takes its share of the columns of every tile
-        const int quarter = warp & 3, g = (warp - 2) >> 2, et = threadIdx.x - 64 - 128 * g;
+        // ---------------- epilogue: four groups of four warps, each a quarter of the columns of every tile
+        const int quarter = warp & 3, part = (warp - 2) >> 2, et = threadIdx.x - 64;
+        const bool lead = et == 0;
         const int r = quarter * 32 + lane;  // row within this CTA's 128
-        float *v0 = vec_s + g * 128, *v1 = vec_s + 256 + g * 128;        // the group's bias columns
-        float *s0 = vec_s + 512 + g * 128, *s1 = vec_s + 768 + g * 128;  // and scales
-        uint32_t res_phase = 0;
-        bool res_armed = false;  // the residual's barrier holds a phase that was not waited out
-        int i = 0;
+        const int cp = part * C::kPart;     // first column within the tile
+        uint32_t i = 0;
         for (int tile = pair; tile < p.n_tiles; tile += n_pairs, ++i) {
-            const int acc = i & 1;
-            const uint32_t acc_phase = (uint32_t)(i >> 1) & 1u;
+            const int acc = (int)(i % C::kAccs);
             int m, n, kb0, kb1, what;
             decode(tile, m, n, kb0, kb1, what);
-            const int row0 = m * 256 + (int)rank * 128;
+            const int row0 = m * 256 + (int)rank * 128, c0 = n * C::kCols;
             const bool live = row0 + r < p.M;
-            // columns, bias and scales of the tile, fetched under the products
-            constexpr int kCols = C::kIsUp ? 64 : KIND == kHidden ? 32 : BN / 2;  // of this group
-            const int c0 = (C::kIsUp ? n * 128 : KIND == kHidden ? n * 64 : n * BN) + g * kCols;
+            uint8_t *tile_s = out_s + (i % C::kTiles) * C::kTile;
+            float *v0 = vec_s + (i & 1u) * 512, *v1 = v0 + 128, *s0 = v0 + 256, *s1 = v0 + 384;
             float xs = 1.f;
-            if (et == 0) store_wait_read();  // the last store has read the tile in shared memory
-            if constexpr (KIND == kDown) {
-                if (p.has_res) {
-                    res_armed = true;
-                    if (et == 0 && row0 < p.M) {
-                        const uint32_t rb = smem_u32(&res_full[g]);
-                        uint32_t bytes = 0;
-                        for (int j = 0; j < kCols / 64; ++j) bytes += c0 + j * 64 < p.E ? kBox : 0;
-                        if (bytes) {
-                            mbar_arrive_expect_tx(rb, bytes);
-                            for (int j = 0; j < kCols / 64; ++j)
-                                if (c0 + j * 64 < p.E)
-                                    tma_load_2d(smem_u32(out_s + (g * (kCols / 64) + j) * kBox), &p.res, c0 + j * 64,
-                                                row0, rb);
-                        } else {
-                            mbar_arrive(rb);
-                        }
-                    } else if (et == 0) {
-                        mbar_arrive(smem_u32(&res_full[g]));
-                    }
-                }
-            }
             if constexpr (KIND != kDw) {
+                // bias and scales of the tile's columns, and the residual's tile, under the products
+                constexpr float kg = C::kIsUp ? Act<ACT>::kGate : 1.f, ku = C::kIsUp ? Act<ACT>::kUp : 1.f;
                 const int limit = KIND == kDown ? p.E : p.F;
-                if (et < kCols) {
-                    const bool in = c0 + et < limit;
-                    constexpr float kg = C::kIsUp ? Act<ACT>::kGate : 1.f, ku = C::kIsUp ? Act<ACT>::kUp : 1.f;
-                    v0[et] = p.bias0 && in ? kg * __bfloat162float(p.bias0[c0 + et]) : 0.f;
-                    if constexpr (KIND != kDown) v1[et] = p.bias1 && in ? ku * __bfloat162float(p.bias1[c0 + et]) : 0.f;
+                const bool in = et < C::kCols && c0 + et < limit;
+                const float b0 = p.bias0 && in ? kg * __bfloat162float(p.bias0[c0 + et]) : 0.f;
+                float b1 = 0.f, g0 = 0.f, g1 = 0.f;
+                if constexpr (KIND != kDown) b1 = p.bias1 && in ? ku * __bfloat162float(p.bias1[c0 + et]) : 0.f;
+                if constexpr (C::kQ8) {
+                    g0 = in ? kg * p.gs[c0 + et] : 0.f;
+                    g1 = in ? ku * p.us[c0 + et] : 0.f;
+                    xs = live ? p.xs[row0 + r] : 0.f;
+                }
+                if (lead) {
+                    if constexpr (C::kTiles == 2) store_wait_read1();  // the store before the last has read this tile
+                    else store_wait_read();
+                    if constexpr (KIND == kDown)
+                        if (p.has_res) {
+                            uint32_t bytes = 0;
+                            for (int j = 0; j < C::kCols / 64; ++j)
+                                bytes += row0 < p.M && c0 + j * 64 < p.E ? kBox : 0;
+                            if (bytes) mbar_arrive_expect_tx(smem_u32(res_full), bytes);
+                            else mbar_arrive(smem_u32(res_full));
+                            for (int j = 0; j < C::kCols / 64; ++j)
+                                if (row0 < p.M && c0 + j * 64 < p.E)
+                                    tma_load_2d(smem_u32(tile_s + j * kBox), &p.res, c0 + j * 64, row0,
+                                                smem_u32(res_full));
+                        }
+                }
+                if constexpr (KIND == kDown) {
+                    // BN columns of one vector: [256] across v0 and v1
+                    if (et < C::kCols) v0[et] = b0;
+                } else if (et < C::kCols) {
+                    v0[et] = b0;
+                    v1[et] = b1;
                     if constexpr (C::kQ8) {
-                        s0[et] = in ? kg * p.gs[c0 + et] : 0.f;
-                        s1[et] = in ? ku * p.us[c0 + et] : 0.f;
+                        s0[et] = g0;
+                        s1[et] = g1;
                     }
                 }
-                if constexpr (C::kQ8) xs = live ? p.xs[row0 + r] : 0.f;
+                epi_sync();
             }
-            bool ok = mbar_wait(smem_u32(&acc_full[acc]), acc_phase, abort_flag, p.err);
-            if constexpr (KIND == kDown) {
-                if (p.has_res) {
-                    if (!ok || !mbar_wait(smem_u32(&res_full[g]), res_phase, abort_flag, p.err)) {
-                        ok = false;
-                    } else {
-                        res_armed = false;
-                        res_phase ^= 1u;
-                    }
-                }
-            }
-            // one decision for all threads that meet in this tile's barriers; the vectors are written
-            if (KIND == kHidden ? both_sync_or(!ok) : group_sync_or(g, !ok)) break;
+            // after an expired wait the waits return at once and the loop runs out
+            wait_bar(smem_u32(&acc_full[acc]), (i / C::kAccs) & 1u, abort_flag, p.err);
+            if constexpr (KIND == kDown)
+                if (p.has_res) wait_bar(smem_u32(res_full), i & 1u, abort_flag, p.err);
             tc_fence_after();
             const uint32_t t0 = tmem_at(tmem, quarter, acc * C::kAccStride);
             if constexpr (KIND == kDw) {
-                float *dst = p.part + ((size_t)(tile % p.splits) * 3 + what) * (size_t)p.F * p.E;
-                const int f = row0 + r;
-                const bool some = kb1 > kb0;
-                // the accumulator's rows are hidden columns here
-                for (int c = 0; c < kCols; c += 16) {
+                const int split = tile % p.splits, f = row0 + r;
+                float *dst = p.part + ((size_t)split * 3 + what) * (size_t)p.F * p.E;
+                float *sums = p.sums ? p.sums + (size_t)split * (2 * p.F + p.E) + what * p.F : nullptr;
+                const bool some = kb1 > kb0, add = p.accumulate;  // without tokens: zeros
+#pragma unroll 1
+                for (int c = cp; c < cp + C::kPart; c += 16) {
                     uint32_t v[16];
-                    tmem_ld16(t0 + (uint32_t)(g * kCols + c), v);
+                    tmem_ld16(t0 + (uint32_t)c, v);
                     tmem_wait();
                     pin(v);
-                    if (f < p.F && c0 + c < p.E) {
-                        float4 *d4 = (float4 *)(dst + (size_t)f * p.E + c0 + c);
+                    if (f >= p.F || c0 + c >= p.E) continue;
+                    float *d = dst + (size_t)f * p.E + c0 + c;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (c0 + c + 4 * q >= p.E) break;
-                            float4 o = some ? make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                                          __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]))
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (p.accumulate) {
-                                const float4 b = d4[q];
-                                o.x += b.x;
-                                o.y += b.y;
-                                o.z += b.z;
-                                o.w += b.w;
-                            }
-                            d4[q] = o;
+                    for (int q = 0; q < 16; q += 4)
+                        if (c0 + c + q < p.E) {
+                            if (some)
+                                put4(d + q, __uint_as_float(v[q]), __uint_as_float(v[q + 1]), __uint_as_float(v[q + 2]),
+                                     __uint_as_float(v[q + 3]), add);
+                            else if (!add)
+                                put4(d + q, 0.f, 0.f, 0.f, 0.f, false);
                         }
+                }
+                if (sums && what < 2 && n == 0 && part == 0) {
+                    uint32_t v[16];
+                    tmem_ld16(t0 + (uint32_t)BN, v);
+                    tmem_wait();
+                    pin(v);
+                    if (f < p.F && (some || !add)) put1(sums + f, some ? __uint_as_float(v[0]) : 0.f, add);
+                }
+                if (sums && what == 2 && m == 0 && quarter == 0) {  // every row holds the sums: lane 0 writes
+#pragma unroll 1
+                    for (int c = cp; c < cp + C::kPart; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(t0 + (uint32_t)(BN + c), v);
+                        tmem_wait();
+                        pin(v);
+                        if (lane == 0 && rank == 0 && (some || !add))
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                if (c0 + c + q < p.E) put1(sums + c0 + c + q, some ? __uint_as_float(v[q]) : 0.f, add);
                     }
                 }
             } else if constexpr (C::kIsUp) {
-                uint8_t *sb = out_s + g * kBox;
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) {
+#pragma unroll 1
+                for (int c = cp; c < cp + C::kPart; c += 16) {
                     uint32_t vg[16], vu[16], w[8];
-                    tmem_ld16(t0 + (uint32_t)(g * 64 + c), vg);
-                    tmem_ld16(t0 + (uint32_t)(128 + g * 64 + c), vu);
+                    tmem_ld16(t0 + (uint32_t)c, vg);
+                    tmem_ld16(t0 + (uint32_t)(128 + c), vu);
                     tmem_wait();
                     pin(vg);
                     pin(vu);
@@ -410,55 +423,52 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                         }
                         w[j / 2] = pack_bf16(h[0], h[1]);
                     }
-                    *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(sb + swizzled(r, c / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    uint8_t *sb = tile_s + (c / 64) * kBox;
+                    const int u = (c % 64) / 8;
+                    *reinterpret_cast<uint4 *>(sb + swizzled(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(sb + swizzled(r, u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             } else if constexpr (KIND == kHidden) {
+                uint32_t vg[16], vu[16], vd[16];
+                tmem_ld16(t0 + (uint32_t)cp, vg);
+                tmem_ld16(t0 + (uint32_t)(64 + cp), vu);
+                tmem_ld16(t0 + (uint32_t)(128 + cp), vd);
+                tmem_wait();
+                pin(vg);
+                pin(vu);
+                pin(vd);
+                uint32_t wo[3][8];
 #pragma unroll
-                for (int c = 0; c < 32; c += 16) {
-                    uint32_t vg[16], vu[16], vd[16];
-                    tmem_ld16(t0 + (uint32_t)(g * 32 + c), vg);
-                    tmem_ld16(t0 + (uint32_t)(64 + g * 32 + c), vu);
-                    tmem_ld16(t0 + (uint32_t)(128 + g * 32 + c), vd);
-                    tmem_wait();
-                    pin(vg);
-                    pin(vu);
-                    pin(vd);
-                    uint32_t wo[3][8];
+                for (int j = 0; j < 16; j += 2) {
+                    float h[2], dg[2], du[2];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        float h[2], dg[2], du[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float b = __uint_as_float(vu[j + e]) + v1[c + j + e], dh = __uint_as_float(vd[j + e]);
-                            float slope;
-                            const float act = Act<ACT>::fast(__uint_as_float(vg[j + e]) + v0[c + j + e], &slope);
-                            h[e] = act * b;
-                            dg[e] = dh * b * slope;
-                            du[e] = dh * act;
-                        }
-                        wo[0][j / 2] = pack_bf16(h[0], h[1]);
-                        wo[1][j / 2] = pack_bf16(dg[0], dg[1]);
-                        wo[2][j / 2] = pack_bf16(du[0], du[1]);
+                    for (int e = 0; e < 2; ++e) {
+                        const float b = __uint_as_float(vu[j + e]) + v1[cp + j + e], dh = __uint_as_float(vd[j + e]);
+                        float slope;
+                        const float act = Act<ACT>::fast(__uint_as_float(vg[j + e]) + v0[cp + j + e], &slope);
+                        h[e] = act * b;
+                        dg[e] = dh * b * slope;
+                        du[e] = dh * act;
                     }
-                    const int u = (g * 32 + c) / 8;
+                    wo[0][j / 2] = pack_bf16(h[0], h[1]);
+                    wo[1][j / 2] = pack_bf16(dg[0], dg[1]);
+                    wo[2][j / 2] = pack_bf16(du[0], du[1]);
+                }
 #pragma unroll
-                    for (int o = 0; o < 3; ++o) {
-                        const uint32_t(&w)[8] = wo[o];
-                        uint8_t *sb = out_s + o * kBox;
-                        *reinterpret_cast<uint4 *>(sb + swizzled(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4 *>(sb + swizzled(r, u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
+                for (int o = 0; o < 3; ++o) {
+                    const uint32_t(&w)[8] = wo[o];
+                    uint8_t *sb = tile_s + o * kBox;
+                    *reinterpret_cast<uint4 *>(sb + swizzled(r, cp / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(sb + swizzled(r, cp / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             } else {
-                uint8_t *sb0 = out_s + g * (kCols / 64) * kBox;
-#pragma unroll
-                for (int c = 0; c < kCols; c += 16) {
+#pragma unroll 1
+                for (int c = cp; c < cp + C::kPart; c += 16) {
                     uint32_t v[16], w[8];
-                    tmem_ld16(t0 + (uint32_t)(g * kCols + c), v);
+                    tmem_ld16(t0 + (uint32_t)c, v);
                     tmem_wait();
                     pin(v);
-                    uint8_t *sb = sb0 + (c / 64) * kBox;
+                    uint8_t *sb = tile_s + (c / 64) * kBox;
                     uint4 *p0 = reinterpret_cast<uint4 *>(sb + swizzled(r, (c % 64) / 8));
                     uint4 *p1 = reinterpret_cast<uint4 *>(sb + swizzled(r, (c % 64) / 8 + 1));
                     uint32_t rw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -468,67 +478,51 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                         rw[4] = b.x, rw[5] = b.y, rw[6] = b.z, rw[7] = b.w;
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 e = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&rw[j]));
-                        w[j] = pack_bf16(__uint_as_float(v[2 * j]) + v0[c + 2 * j] + e.x,
-                                         __uint_as_float(v[2 * j + 1]) + v0[c + 2 * j + 1] + e.y);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = pack_bf16(__uint_as_float(v[2 * j]) + v0[c + 2 * j] + __uint_as_float(rw[j] << 16),
+                                         __uint_as_float(v[2 * j + 1]) + v0[c + 2 * j + 1] +
+                                             __uint_as_float(rw[j] & 0xffff0000u));
                     *p0 = make_uint4(w[0], w[1], w[2], w[3]);
                     *p1 = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             }
-            // the accumulator is read: back to the issuer, once per group and CTA
+            // the accumulator is read: back to the issuer, once in each CTA; the tile goes out
             tc_fence_before();
             if constexpr (KIND != kDw) fence_async_shared();
-            group_sync(g);
-            if (et == 0) {
+            epi_sync();
+            if (lead) {
                 mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
-                if (row0 < p.M) {
-                    if constexpr (C::kIsUp) {
-                        if (c0 < p.F) tma_store_tile(&p.o0, smem_u32(out_s + g * kBox), c0, row0);
-                    } else if constexpr (KIND == kDown) {
-                        for (int j = 0; j < kCols / 64; ++j)
-                            if (c0 + j * 64 < p.E)
-                                tma_store_tile(&p.o0, smem_u32(out_s + (g * (kCols / 64) + j) * kBox), c0 + j * 64,
-                                               row0);
-                    }
-                }
-                if constexpr (C::kIsUp || KIND == kDown) store_commit();
-            }
-            if constexpr (KIND == kHidden) {
-                // both groups have written their halves of the three tiles
-                both_sync();
-                if (g == 0 && et == 0) {
+                if constexpr (KIND == kHidden) {
                     if (row0 < p.M) {
-                        tma_store_tile(&p.o0, smem_u32(out_s), n * 64, row0);
-                        tma_store_tile(&p.o1, smem_u32(out_s + kBox), n * 64, row0);
-                        tma_store_tile(&p.o2, smem_u32(out_s + 2 * kBox), n * 64, row0);
+                        tma_store_tile(&p.o0, smem_u32(tile_s), c0, row0);
+                        tma_store_tile(&p.o1, smem_u32(tile_s + kBox), c0, row0);
+                        tma_store_tile(&p.o2, smem_u32(tile_s + 2 * kBox), c0, row0);
                     }
-                    store_commit();
-                    store_wait_read();
+                } else if constexpr (KIND != kDw) {
+                    const int limit = KIND == kDown ? p.E : p.F;
+                    for (int j = 0; j < C::kCols / 64; ++j)
+                        if (row0 < p.M && c0 + j * 64 < limit)
+                            tma_store_tile(&p.o0, smem_u32(tile_s + j * kBox), c0 + j * 64, row0);
                 }
-                both_sync();
+                if constexpr (KIND != kDw) store_commit();
             }
         }
-        if (et == 0) {
-            store_wait_all();  // shared memory outlives its stores, and the residual's copies
-            if (res_armed) {  // left early: the armed copy lands, or was counted without bytes
-                int dummy = 0;
-                mbar_wait(smem_u32(&res_full[g]), res_phase, (volatile int *)&dummy, p.err);
-            }
+        if (lead && KIND != kDw) {
+            store_wait_all();  // shared memory outlives its stores, and after an expired wait the residual's copy
+            int dummy = 0;
+            if (KIND == kDown && *abort_flag && p.has_res && i)
+                mbar_wait(smem_u32(res_full), (i - 1) & 1u, (volatile int *)&dummy, p.err);
         }
     }
 
     __syncthreads();
     if (threadIdx.x == 0) {
-        // every product has run before either CTA frees what it reads; after an
-        // expired wait, let the copies this CTA counted land first
+        // every product has run before either CTA goes; after an expired wait the counted copies land first
         int dummy = 0;
         mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         if (*abort_flag && rank == 0)
-            for (int s = 0; s < kStages; ++s)
-                if (issued[s] > 0)
-                    mbar_wait(smem_u32(&full[s]), (uint32_t)((issued[s] - 1) & 1), (volatile int *)&dummy, p.err);
+            for (uint32_t i = *armed > kStages ? *armed - kStages : 0; i < *armed; ++i)
+                mbar_wait(smem_u32(&full[i % kStages]), (i / kStages) & 1u, (volatile int *)&dummy, p.err);
     }
     __syncthreads();
     __syncwarp();
@@ -583,12 +577,8 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     auto kern = k_ffn<KIND, BN, ACT>;
     const pmha_status st = configure(kern, C::kSmem, &pairs);
     if (st != PMHA_OK) return st;
-    const int grid = 2 * std::min(pairs, p.n_tiles);
     StageTimer timer(stage, s);
-    kern<<<grid, kThreads, C::kSmem, s>>>(p);
-    count_launch();
-    PMHA_CUDA_TRY(cudaGetLastError());
-    return PMHA_OK;
+    return launch_pairs(kern, 2 * std::min(pairs, p.n_tiles), kThreads, C::kSmem, s, p);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -715,6 +705,7 @@ pmha_status ffn_tc_dw(const FfnTc &f, const FfnDwArgs &a, cudaStream_t s)
     p.kb = (int)ceil_div(a.M, 64);
     p.kb_per = (int)ceil_div(p.kb, p.splits);
     p.part = a.part;
+    p.sums = a.sums;
     p.accumulate = a.accumulate;
     if (!make_tile_map(&p.a0, a.dg, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.a1, a.du, a.M, f.F, f.F, 2, 64) ||
         !make_tile_map(&p.a2, a.h, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.b0, a.x, a.M, f.E, f.E, 2, 64) ||

@@ -43,6 +43,14 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 {
     return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort_flag, err);
 }
+// Waits for the launches this one was allowed to start before the end of; lets
+// the next one start likewise (its blocks come up as this one's leave, which
+// hides the launch). Everything that touches global memory comes after.
+__device__ __forceinline__ void grid_dependency_wait()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -151,6 +159,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 }
 // 16-byte unit u (0..7) of row r of a 128-byte-wide tile with 128-byte swizzle
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4)); }
+
+// A launch of `grid` CTAs in pairs that may come up before the launch before it
+// has ended (the kernel calls grid_dependency_wait).
+template <typename P>
+pmha_status launch_pairs(void (*kern)(P), int grid, int threads, int smem, cudaStream_t s, const P &p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    PMHA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p));
+    count_launch();
+    return PMHA_OK;
+}
 
 // 2-D map of rows x cols elements of es bytes (1: bytes, 2: bf16), row pitch
 // in elements, box of 128 bytes x box_rows, 128-byte swizzle.
