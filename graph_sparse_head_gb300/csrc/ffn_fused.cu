@@ -3,27 +3,31 @@
 // its tokens stay in shared memory while the hidden width passes in chunks of
 // 64 columns, whose weights stream through two rings of TMA stages.
 //
-//   forward, chunk c:   S = x [Wg_c | Wu_c]^T           tensor memory, two buffers
+//   forward, chunk c:   S = x [Wg_c | Wu_c]^T           tensor memory, two or three buffers
 //                       h = act(S_g + bg) * (S_u + bu)   -> shared memory, bf16
 //                       Y += h Wd_c^T                    tensor memory
 //   after the last:     y = Y + bd + residual
 //
 //   backward, chunk c:  S as above, D = dy Wd_c
-//                       h, dg, du -> global memory (the weight gradients read them)
+//                       h, dg, du -> shared memory, and by TMA to memory (the weight gradients read them)
 //                       X += dg Wg_c + du Wu_c           (embed_dim up to 128)
 //   after the last:     dx = X
 //
 // The hidden values never go to memory in the forward pass, and the tokens are
-// read once; what bounds it is the tensor pipe and, near it, the epilogue's
-// arithmetic (two special-function results for each hidden value). So the
-// warps are specialised: warp 0 copies, warp 1 of the even CTA issues the
-// products, two groups of eight warps take the chunks in turn (each has two
-// chunks' time, so that one group's tensor-memory reads and barriers run under
-// the other's arithmetic; eight warps, because a chunk's time is a loop from S
-// through the epilogue to Y and the next S of its buffer, and half the columns
-// a warp halve the longest part of it), and four more drain the row block's
-// result while the next block's chunks go on. The issuer runs S two chunks ahead:
-// S(0) S(1) | Y(0) S(2) | Y(1) S(3) ... across row blocks.
+// read once. The warps are specialised: warp 0 copies, warp 1 of the even CTA
+// issues the products, sixteen warps turn S into hidden values, and four drain
+// the row block's result while the next block's chunks go on. The issuer runs S
+// as many chunks ahead as there are buffers, across row blocks: S(0) S(1) S(2) |
+// Y(0) S(3) | Y(1) S(4) ... A chunk's time is that of a loop, S -> epilogue -> Y
+// and the next S of the buffer, over the buffers; what was measured on the way
+// (cycles a chunk of 64 columns, embed_dim 128, where the products take 770):
+// waits with cluster-scope acquires and one wait and commit for each stage
+// 3,100; one commit a step, waits for what is long loaded taken first, the
+// issuing warp converged (uniform addresses) and the epilogue rolled, so that
+// the warps share the instruction cache, 2,000; sixteen epilogue warps instead
+// of eight 1,440 to 1,640; the result through TMA instead of 32-byte accesses (a
+// warp's 32 rows cost the memory pipe 32 cycles an instruction) and a third
+// S buffer: see the forward rate beside ffn_fused_forward.
 //
 // Every wait is bounded; after an expired one the waits return at once, the
 // loops run out, and pmha_device_status reports PMHA_ERR_TIMEOUT.
@@ -40,7 +44,7 @@ namespace pmha {
 namespace {
 using namespace tcu;
 
-constexpr int kThreads = 704;       // 2 + 8 + 8 + 4 warps
+constexpr int kThreads = 704;       // 2 + 16 + 4 warps
 constexpr int kBox = 128 * 128;     // 128 rows of 128 bytes
 constexpr int kMaxHidden = 2048;    // bias (and scale) columns held in shared memory
 constexpr int kSmemMost = 232448;
@@ -50,38 +54,43 @@ template <int EB, bool BWD, bool Q8>
 struct Cfg {
     static constexpr int KB = Q8 ? (EB + 1) / 2 : EB;
     static constexpr bool kOut = !BWD || EB <= 2;               // the kernel forms y, or dx
+    static constexpr int SB = !BWD && EB <= 2 ? 3 : 2;          // S buffers in tensor memory
     static constexpr int kX = (BWD ? 2 : 1) * KB * kBox;        // x (and dy) of a row block
     static constexpr int kSBlock = BWD ? 12288 : 8192;          // 64 rows of Wg or Wu (and 32 of Wd^T), one K block
-    static constexpr int SG = BWD && EB == 4 ? 2 : KB;          // K blocks of a stage: a chunk's where they fit
+    static constexpr int SG = BWD ? 1 : !Q8 && EB == 4 ? 2 : KB;        // K blocks of a stage of the S ring
     static constexpr int kSSlot = SG * kSBlock;
     static constexpr int kYSlot = kOut ? EB * (BWD ? 8192 : 4096) : 0;  // half of the output columns of a chunk
-    static constexpr int kStaged = kOut ? (BWD ? 2 : 1) * kBox : 0;     // h, or dg and du
+    static constexpr int kNY = kOut ? 2 : 0;
+    static constexpr int kStaged = BWD ? 3 * kBox : kBox;       // dg, du and h, or h
+    static constexpr int kStages = BWD ? 1 : SB;
+    static constexpr int kOutTiles = kOut ? 2 * kBox : 0;       // two tiles of 64 result columns
     static constexpr int kSCols = BWD ? 192 : 128;
-    static constexpr int kNY = kOut ? (BWD ? 2 : 3) : 0;
-    static constexpr int kVec = kMaxHidden * 8 + 1024;          // gate, up and output biases, float32
+    static constexpr int kVec = kMaxHidden * (BWD ? 4 : 8) + 1024;      // gate and up biases; output bias
     static constexpr int kScales = Q8 ? kMaxHidden * 8 : 0;
     static constexpr int kBars = 512;
-    static constexpr int kFixed = 1024 + kNY * kYSlot + 2 * kStaged + kVec + kScales + kBars;
-    static constexpr int kXB = kFixed + 2 * kX + 2 * kSSlot <= kSmemMost ? 2 : 1;  // token buffers
+    static constexpr int kFixed = 1024 + kNY * kYSlot + kStages * kStaged + kOutTiles + kVec + kScales + kBars;
+    static constexpr int kXB = kFixed + 2 * kX + 3 * kSSlot <= kSmemMost ? 2 : 1;  // token buffers
     static constexpr int kNSFit = (kSmemMost - kFixed - kXB * kX) / kSSlot;
     static constexpr int kNS = kNSFit > 4 ? 4 : kNSFit;
-    static constexpr int kOB = 2 * kSCols + 2 * EB * 64 <= 512 ? 2 : 1;  // output accumulators
+    static constexpr int kOB = SB * kSCols + 2 * EB * 64 <= 512 ? 2 : 1;  // output accumulators
     static constexpr int kSmem = kFixed + kXB * kX + kNS * kSSlot;
-    static_assert(kNS >= 2 && kNS * SG >= KB, "a chunk's weights fit in the ring");
-    static_assert(!kOut || 2 * kSCols + kOB * EB * 64 <= 512, "tensor memory");
+    static_assert(kNS >= 3, "a ring of at least three stages");
+    static_assert(KB <= kNS * SG || !kOut, "the down product's weights come after the tokens");
+    static_assert(SG == KB || kXB == 1, "the reuse of a second token buffer is known from the S ring");
+    static_assert(!kOut || SB * kSCols + kOB * EB * 64 <= 512, "tensor memory");
 };
 
 struct Params {
     CUtensorMap x, dy, wg, wu, wd;  // wd: Wd (E, F), or Wd^T (F, E) in the backward pass
     CUtensorMap wgt, wut;           // (E, F): Wg^T, Wu^T
-    CUtensorMap dg_map, du_map;     // (M, F)
+    CUtensorMap h, dg, du;          // (M, F)
+    CUtensorMap out, res;           // (M, E)
     int M, E, F;
     int items, parts;               // row blocks x parts of the hidden width
     int chunks, per_part;           // chunks of 64 hidden columns, and of one part
-    const __nv_bfloat16 *bg, *bu, *bd, *res;
+    const __nv_bfloat16 *bg, *bu, *bd;
     const float *xs, *gs, *us;
-    __nv_bfloat16 *out, *h, *dg, *du;
-    int wide_e, wide_f;             // rows of out and residual / of h, dg, du allow 32-byte accesses
+    int has_res, has_out;
     int *err;
 };
 
@@ -117,53 +126,33 @@ __device__ __forceinline__ void tmem_wait(R &...regs)
     (pin(regs), ...);
 }
 
-// 16 bf16 values of a row: one 32-byte access where the rows allow it, else two
-// of 16 bytes, each only if its 8 columns exist.
-__device__ __forceinline__ void store16(__nv_bfloat16 *p, const uint32_t (&w)[8], int left, bool wide)
-{
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        if (left > 0) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (left > 8) *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16 *p, uint32_t (&w)[8], int left, bool wide)
-{
-    if (wide) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p));
-    } else {
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (left > 0) a = *reinterpret_cast<const uint4 *>(p);
-        if (left > 8) b = *reinterpret_cast<const uint4 *>(p + 8);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    }
-}
+// named barrier 4 over the chunk epilogue's 512 threads
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 4, 512;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 template <int EB, bool BWD, bool Q8, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block(const __grid_constant__ Params p)
 {
     using C = Cfg<EB, BWD, Q8>;
-    constexpr int KB = C::KB, NS = C::kNS, NY = C::kNY > 0 ? C::kNY : 1, XB = C::kXB, OB = C::kOB;
+    constexpr int KB = C::KB, NS = C::kNS, NY = C::kNY > 0 ? C::kNY : 1, XB = C::kXB, OB = C::kOB, SB = C::SB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *x_s = smem;                              // [XB][x blocks, dy blocks]
     uint8_t *s_ring = x_s + XB * C::kX;               // [NS]
     uint8_t *y_ring = s_ring + NS * C::kSSlot;        // [kNY]
-    uint8_t *staged = y_ring + C::kNY * C::kYSlot;    // [2]
-    float *bg_s = (float *)(staged + 2 * C::kStaged), *bu_s = bg_s + kMaxHidden, *bd_s = bu_s + kMaxHidden;
-    float *gs_s = (float *)((uint8_t *)bg_s + C::kVec), *us_s = gs_s + kMaxHidden;
+    uint8_t *staged = y_ring + C::kNY * C::kYSlot;    // [kStages]
+    uint8_t *out_s = staged + C::kStages * C::kStaged;  // [2] tiles of 64 result columns
+    float *bd_s = (float *)(out_s + C::kOutTiles);      // [256]
+    float *bg_s = bd_s + 256, *bu_s = bg_s + kMaxHidden;  // forward: float32, times the activation's constants
+    uint32_t *bias_s = (uint32_t *)bg_s;                  // backward: (bg, bu) as bf16
+    float *gs_s = (float *)((uint8_t *)bd_s + C::kVec), *us_s = gs_s + kMaxHidden;
     uint64_t *bar = (uint64_t *)((uint8_t *)gs_s + C::kScales);
     uint64_t *x_full = bar, *s_full = x_full + 2, *s_empty = s_full + 4, *y_full = s_empty + 4, *step = y_full + 4,
-             *h_full = step + 4, *out_full = h_full + 2, *out_empty = out_full + 2, *mma_done = out_empty + 2;
+             *h_full = step + 4, *out_full = h_full + 3, *out_empty = out_full + 2, *res_full = out_empty + 2,
+             *y_done = res_full + 2, *mma_done = y_done + 1;
     uint32_t *tmem_holder = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
-    volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted: x, S slots, Y slots
+    volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted: x, S and Y slots, residual
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -172,19 +161,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&x_full[i]), 1);
-            mbar_init(smem_u32(&h_full[i]), 2);  // the group in either CTA
             mbar_init(smem_u32(&out_full[i]), 1);
-            mbar_init(smem_u32(&out_empty[i]), 2);
+            mbar_init(smem_u32(&out_empty[i]), 2);  // the group in either CTA
+            mbar_init(smem_u32(&res_full[i]), 1);
         }
+        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&h_full[i]), 2);  // the group in either CTA
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&s_empty[i]), 1);
             mbar_init(smem_u32(&y_full[i]), 1);
             mbar_init(smem_u32(&step[i]), 1);
         }
+        mbar_init(smem_u32(y_done), 1);
         mbar_init(smem_u32(mma_done), 1);
         *abort_flag = 0;
-        armed[0] = armed[1] = armed[2] = 0;
+        armed[0] = armed[1] = armed[2] = armed[3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
@@ -197,8 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     // item -> row block, first chunk; every item has the chunks of one part (the last part may have fewer)
     auto chunks_of = [&](int item) { return min(p.per_part, p.chunks - (item % p.parts) * p.per_part); };
 
-    // Step k: the product Y of chunk k - 2, then S of chunk k, committed together: S(k) can be read, and the
-    // staged values and weights of Y(k - 2) and the weights of S(k) are free. Four barriers in turn.
+    // Step k: the product Y of chunk k - SB, then S of chunk k, committed together: S(k) can be read, and the
+    // staged values and weights of Y(k - SB) and the weights of S(k) are free. Four barriers in turn: a step is
+    // over before the one four later can be issued, whoever waits for it.
     auto wait_step = [&](uint32_t k) { return wait_bar(smem_u32(&step[k & 3u]), (k >> 2) & 1u, abort_flag, p.err); };
 
     if (warp == 0) {
@@ -206,9 +198,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
         const bool one = elect_one();
         uint32_t ns = 0, ny = 0, nx = 0, k = 0;  // copies made into each ring; steps
         uint32_t last1 = 0, last2 = 0;           // 1 + the last step of the row blocks one and two back
-        auto load_s = [&](int f0) {
+        auto load_x = [&](int row) {
+            const int b = (int)(nx % XB);
+            const uint32_t before = XB == 1 ? last1 : last2;
+            // a step more than NS back is known to be over (load_s of this step waited for a later one)
+            if (before && (C::SG < KB || before + NS > k) && !wait_step(before - 1)) return;
+            if (one) {
+                const uint32_t fb = map_rank(smem_u32(&x_full[b]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&x_full[b]), 2 * C::kX);
+                armed[0] = nx + 1;
+                const uint32_t a = smem_u32(x_s + b * C::kX);
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+                    tma_load_2d_pair(a + j * kBox, &p.x, j * (Q8 ? 128 : 64), row, fb);
+                    if constexpr (BWD) tma_load_2d_pair(a + (KB + j) * kBox, &p.dy, j * 64, row, fb);
+                }
+            }
+            ++nx;
+        };
+        // where a chunk has more stages than the ring, the tokens of a new row block (row >= 0) come before those
+        // that wait for its first products
+        auto load_s = [&](int f0, int row) {
             for (int j = 0; j < KB; j += C::SG, ++ns) {
                 const int slot = (int)(ns % NS);
+                if (j == NS * C::SG && row >= 0) load_x(row);
                 if constexpr (C::SG < KB) {
                     if (!wait_bar(smem_u32(&s_empty[slot]), ((ns / NS) & 1u) ^ 1u, abort_flag, p.err)) return;
                 } else if (k >= (uint32_t)NS && !wait_step(k - NS)) return;
@@ -226,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 }
             }
         };
-        auto load_y = [&](int f0) {  // of chunk ny; its slot was read by step ny - NY + 2
+        auto load_y = [&](int f0) {  // of chunk ny; its slot was read by step ny - NY + SB
             const int slot = (int)(ny % NY);
-            if (ny >= (uint32_t)NY && !wait_step(ny - NY + 2)) return;
+            if (ny >= (uint32_t)NY && !wait_step(ny - NY + SB)) return;
             if (one) {
                 const uint32_t fb = map_rank(smem_u32(&y_full[slot]), 0);
                 if (rank == 0) mbar_arrive_expect_tx(smem_u32(&y_full[slot]), 2 * C::kYSlot);
@@ -243,44 +256,28 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             }
             ++ny;
         };
-        auto load_x = [&](int row) {
-            const int b = (int)(nx % XB);
-            const uint32_t before = XB == 1 ? last1 : last2;
-            // a step more than NS back is known to be over (load_s of this step waited for a later one)
-            if (before && before + NS > k && !wait_step(before - 1)) return;
-            if (one) {
-                const uint32_t fb = map_rank(smem_u32(&x_full[b]), 0);
-                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&x_full[b]), 2 * C::kX);
-                armed[0] = nx + 1;
-                const uint32_t a = smem_u32(x_s + b * C::kX);
-#pragma unroll
-                for (int j = 0; j < KB; ++j) {
-                    tma_load_2d_pair(a + j * kBox, &p.x, j * (Q8 ? 128 : 64), row, fb);
-                    if constexpr (BWD) tma_load_2d_pair(a + (KB + j) * kBox, &p.dy, j * 64, row, fb);
-                }
-            }
-            ++nx;
-        };
-        int y1 = -1, y2 = -1;  // hidden columns of the chunks one and two steps back
+        int yf[3] = {-1, -1, -1};  // hidden columns of the chunks one, two and three steps back
         for (int item = pair; item < p.items && !*abort_flag; item += n_pairs) {
             const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
             const int row = (item / p.parts) * 256 + (int)rank * 128;
             for (int c = 0; c < n && !*abort_flag; ++c, ++k) {
-                load_s(f_first + c * 64);
+                constexpr bool kInside = KB > NS * C::SG;
+                load_s(f_first + c * 64, kInside && c == 0 ? row : -1);
                 // a second token buffer is filled as early as can be; a single one waits for the last step
                 if (XB == 2 && c == 0) load_x(row);
-                if (C::kOut && y2 >= 0) load_y(y2);
-                if (XB == 1 && c == 0) load_x(row);
-                y2 = y1;
-                y1 = f_first + c * 64;
+                if (C::kOut && yf[SB - 1] >= 0) load_y(yf[SB - 1]);
+                if (XB == 1 && !kInside && c == 0) load_x(row);
+                yf[2] = yf[1];
+                yf[1] = yf[0];
+                yf[0] = f_first + c * 64;
             }
             last2 = last1;
             last1 = k;
         }
-        if (C::kOut && !*abort_flag) {
-            if (y2 >= 0) load_y(y2);
-            if (y1 >= 0) load_y(y1);
-        }
+        if constexpr (C::kOut)
+#pragma unroll
+            for (int z = SB - 1; z >= 0; --z)
+                if (!*abort_flag && yf[z] >= 0) load_y(yf[z]);
     } else if (warp == 1) {
         if (rank == 0) {
             // ---------------- MMA issuer of the pair: the whole warp walks the steps, so that addresses stay in
@@ -291,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             auto wait_for = [&](uint64_t *b, uint32_t parity) {
                 if (ok) ok = wait_bar(smem_u32(b), parity, abort_flag, p.err);
             };
-            // (first | last << 1 | 4) of the chunks one and two steps back
+            // y: (first | last << 1 | 4) of the chunk SB steps back, 0: none
             auto run_step = [&](uint32_t y, bool has_s, bool first, bool last) {
-                const uint32_t ky = k - 2;  // the chunk of Y
-                const int ys = (int)(ky % NY), xb = (int)(nx % XB), ob = (int)(n_out % OB);
+                const uint32_t ky = k - SB;  // the chunk of Y
+                const int ys = (int)(ky % NY), yb = (int)(ky % SB), xb = (int)(nx % XB), ob = (int)(n_out % OB);
                 // what is loaded long before comes first: only the hidden values are waited for in earnest
                 if (C::kOut && y) {
                     wait_for(&y_full[ys], (ky / NY) & 1u);
@@ -304,13 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                     if (first) wait_for(&x_full[xb], (nx / XB) & 1u);
                     if constexpr (C::SG == KB) wait_for(&s_full[ns % NS], (ns / NS) & 1u);
                 }
-                if (y) wait_for(&h_full[ky & 1u], (ky >> 1) & 1u);
+                if (y) wait_for(&h_full[yb], (ky / SB) & 1u);
                 if (!ok) return;
                 tc_fence_after();
                 if constexpr (C::kOut) {
                     if (y && one) {
-                        const uint32_t d = tmem + 2 * C::kSCols + (uint32_t)(ob * EB * 64);
-                        const uint32_t a = smem_u32(staged + (ky & 1u) * C::kStaged), b = smem_u32(y_ring + ys * C::kYSlot);
+                        const uint32_t d = tmem + SB * C::kSCols + (uint32_t)(ob * EB * 64);
+                        const uint32_t a = smem_u32(staged + (BWD ? 0 : yb) * C::kStaged);
+                        const uint32_t b = smem_u32(y_ring + ys * C::kYSlot);
 #pragma unroll
                         for (int z = 0; z < (BWD ? 2 : 1); ++z) {
                             const uint64_t da = smem_desc(a + z * kBox), db = smem_desc(b + z * EB * 4096);
@@ -319,12 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                                 mma_pair<false>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q),
                                                 idesc_of(false, false, 256, EB * 64), z + q ? 1u : (y & 1u) ^ 1u);
                         }
+                        if constexpr (BWD) mma_commit_pair(smem_u32(y_done));
                         if (y & 2u) mma_commit_pair(smem_u32(&out_full[ob]));
                     }
                     if (y & 2u) ++n_out;
                 }
                 if (has_s) {
-                    const uint32_t d = tmem + (k & 1u) * C::kSCols;
+                    const uint32_t d = tmem + (k % SB) * C::kSCols;
                     const uint32_t xa = smem_u32(x_s + xb * C::kX);
 #pragma unroll
                     for (int j0 = 0; j0 < KB; j0 += C::SG, ++ns) {
@@ -361,19 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 __syncwarp();
                 ++k;
             };
-            uint32_t f1 = 0, f2 = 0;
+            uint32_t back = 0;  // three bits for each of the last SB chunks
             for (int item = pair; item < p.items && ok; item += n_pairs) {
                 const int n = chunks_of(item);
                 for (int c = 0; c < n && ok; ++c) {
-                    run_step(f2, true, c == 0, c == n - 1);
-                    f2 = f1;
-                    f1 = (uint32_t)(c == 0) | (uint32_t)(c == n - 1) << 1 | 4u;
+                    run_step((back >> (3 * SB - 3)) & 7u, true, c == 0, c == n - 1);
+                    back = back << 3 | (uint32_t)(c == 0) | (uint32_t)(c == n - 1) << 1 | 4u;
                 }
             }
-            for (int z = 0; z < 2 && ok; ++z) {
-                if (f2 || k < 2) run_step(f2, false, false, false);
-                f2 = f1;
-                f1 = 0;
+            for (int z = 0; z < SB && ok; ++z) {
+                run_step((back >> (3 * SB - 3)) & 7u, false, false, false);
+                back <<= 3;
             }
             if (one) mma_commit_pair(smem_u32(mma_done));
             __syncwarp();
@@ -381,192 +378,233 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
     } else if (warp < 18) {
-        // ---------------- chunk epilogue: group g takes chunks g, g + 2, ..., each of its halves 32 columns
-        constexpr int kW = BWD ? 8 : 16;  // columns at a time: what 80 registers hold
-        const int quarter = warp & 3, g = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1;
-        const int r = quarter * 32 + lane;
-        const bool lead = threadIdx.x == 64 + 256 * g;
-        const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(g * C::kSCols);
-        auto chunk_sync = [&]() { asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory"); };
-        uint8_t *st = staged + g * C::kStaged;
-        const uint32_t h_bar = map_rank(smem_u32(&h_full[g]), 0);
+        // ---------------- chunk epilogue, 16 warps
+        const int quarter = warp & 3, r = quarter * 32 + lane;
         for (int i = threadIdx.x - 64; i < p.chunks * 64; i += 512) {
             const bool in = i < p.F;
-            constexpr float kg = BWD ? 1.f : Act<ACT>::kGate, ku = BWD ? 1.f : Act<ACT>::kUp;
-            bg_s[i] = in && p.bg ? kg * __bfloat162float(p.bg[i]) : 0.f;
-            bu_s[i] = in && p.bu ? ku * __bfloat162float(p.bu[i]) : 0.f;
-            if constexpr (Q8) {
-                gs_s[i] = in ? kg * p.gs[i] : 0.f;
-                us_s[i] = in ? ku * p.us[i] : 0.f;
+            const float g = in && p.bg ? __bfloat162float(p.bg[i]) : 0.f, u = in && p.bu ? __bfloat162float(p.bu[i]) : 0.f;
+            if constexpr (BWD) {
+                bias_s[i] = pack_bf16(g, u);
+            } else {
+                bg_s[i] = Act<ACT>::kGate * g;
+                bu_s[i] = Act<ACT>::kUp * u;
+                if constexpr (Q8) {
+                    gs_s[i] = in ? Act<ACT>::kGate * p.gs[i] : 0.f;
+                    us_s[i] = in ? Act<ACT>::kUp * p.us[i] : 0.f;
+                }
             }
         }
-        asm volatile("bar.sync 4, 512;" ::: "memory");  // both groups: the vectors are there
+        epi_sync();  // the vectors are there
         uint32_t k = 0;
-        for (int item = pair; item < p.items; item += n_pairs) {
-            const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
-            const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
-            const bool live = row < p.M;
-            float xs = 1.f;
-            if constexpr (Q8) xs = live ? p.xs[row] : 0.f;
-            for (int c = 0; c < n; ++c, ++k) {
-                if ((k & 1u) != (uint32_t)g) continue;
-                const int f0 = f_first + c * 64;
-                if constexpr (BWD && C::kOut) {
-                    if (lead) store_wait_read();  // the copies out of chunk k - 2's staged values
-                    chunk_sync();
+        if constexpr (!BWD) {
+            // two groups of eight warps take the chunks in turn, a warp 32 of the columns
+            const int g = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1;
+            const bool lead = threadIdx.x == 64 + 256 * g;
+            for (int item = pair; item < p.items; item += n_pairs) {
+                const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
+                float xs = 1.f;
+                if constexpr (Q8) {
+                    const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
+                    xs = row < p.M ? p.xs[row] : 0.f;
                 }
-                wait_step(k);  // and the products with them are over
-                tc_fence_after();
+                for (int c = 0; c < n; ++c, ++k) {
+                    if ((k & 1u) != (uint32_t)g) continue;
+                    const int f0 = f_first + c * 64, sb = (int)(k % SB);
+                    const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(sb * C::kSCols);
+                    uint8_t *st = staged + sb * C::kStaged;
+                    wait_step(k);  // and the product with the values that were staged here is over
+                    tc_fence_after();
 #pragma unroll 1
-                for (int s = half * 32; s < half * 32 + 32; s += 16) {  // rolled: the warps of an SM share its instruction cache
-                    uint32_t wh[8];
+                    for (int s = half * 32; s < half * 32 + 32; s += 16) {  // rolled: the SM's warps share its instruction cache
+                        uint32_t vg[16], vu[16], w[8];
+                        tmem_read(t0 + (uint32_t)s, vg);
+                        tmem_read(t0 + (uint32_t)(64 + s), vu);
+                        tmem_wait(vg, vu);
+                        const float *bg = bg_s + f0 + s, *bu = bu_s + f0 + s, *gs = gs_s + f0 + s, *us = us_s + f0 + s;
 #pragma unroll
-                    for (int q = 0; q < 16; q += kW) {
-                        uint32_t vg[kW], vu[kW], vd[kW], w0[kW / 2], w1[kW / 2];
-                        tmem_read(t0 + (uint32_t)(s + q), vg);
-                        tmem_read(t0 + (uint32_t)(64 + s + q), vu);
-                        if constexpr (BWD) {
-                            tmem_read(t0 + (uint32_t)(128 + s + q), vd);
-                            tmem_wait(vg, vu, vd);
-                        } else {
-                            tmem_wait(vg, vu);
-                        }
-                        const float *bg = bg_s + f0 + s + q, *bu = bu_s + f0 + s + q;
-                        const float *gs = gs_s + f0 + s + q, *us = us_s + f0 + s + q;
-#pragma unroll
-                        for (int j = 0; j < kW; j += 4) {
+                        for (int j = 0; j < 16; j += 4) {
                             const float4 b4 = *reinterpret_cast<const float4 *>(bg + j);
                             const float4 c4 = *reinterpret_cast<const float4 *>(bu + j);
                             const float bj[4] = {b4.x, b4.y, b4.z, b4.w}, cj[4] = {c4.x, c4.y, c4.z, c4.w};
-                            float mj[4] = {}, nj[4] = {};
+                            float mj[4] = {}, nj[4] = {}, h[4];
                             if constexpr (Q8) {
                                 const float4 m4 = *reinterpret_cast<const float4 *>(gs + j);
                                 const float4 n4 = *reinterpret_cast<const float4 *>(us + j);
                                 mj[0] = m4.x, mj[1] = m4.y, mj[2] = m4.z, mj[3] = m4.w;
                                 nj[0] = n4.x, nj[1] = n4.y, nj[2] = n4.z, nj[3] = n4.w;
                             }
-                            float h[4], dg[4], du[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
-                                if constexpr (BWD) {
-                                    const float d = __uint_as_float(vd[j + e]), u = b + cj[e];
-                                    float slope;
-                                    const float act = Act<ACT>::fast(a + bj[e], &slope);
-                                    h[e] = act * u;
-                                    du[e] = d * act;
-                                    dg[e] = d * u * slope;
-                                } else if constexpr (Q8) {
+                                if constexpr (Q8)
                                     h[e] = Act<ACT>::hidden(fmaf(a, xs * mj[e], bj[e]), fmaf(b, xs * nj[e], cj[e]));
-                                } else {
+                                else
                                     h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, bj[e]),
                                                             fmaf(b, Act<ACT>::kUp, cj[e]));
-                                }
                             }
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                wh[(q + j + e) / 2] = pack_bf16(h[e], h[e + 1]);
-                                if constexpr (BWD) {
-                                    w0[(j + e) / 2] = pack_bf16(dg[e], dg[e + 1]);
-                                    w1[(j + e) / 2] = pack_bf16(du[e], du[e + 1]);
-                                }
-                            }
+                            w[j / 2] = pack_bf16(h[0], h[1]);
+                            w[j / 2 + 1] = pack_bf16(h[2], h[3]);
                         }
-                        if constexpr (BWD) {
-                            if constexpr (C::kOut) {
-                                const uint32_t o = swizzled(r, (s + q) / 8);
-                                *reinterpret_cast<uint4 *>(st + o) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-                                *reinterpret_cast<uint4 *>(st + kBox + o) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                            } else if (live && f0 + s + q < p.F) {
-                                const size_t at = (size_t)row * p.F + f0 + s + q;
-                                *reinterpret_cast<uint4 *>(p.dg + at) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-                                *reinterpret_cast<uint4 *>(p.du + at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                            }
-                        }
+                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
-                    if constexpr (!BWD) {
-                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8 + 1)) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
-                    }
-                    if constexpr (BWD) {
-                        const int left = p.F - (f0 + s);
-                        if (live && left > 0) {
-                            const size_t at = (size_t)row * p.F + f0 + s;
-                            store16(p.h + at, wh, left, p.wide_f && left >= 16);
-                        }
-                    }
+                    tc_fence_before();
+                    fence_async_shared();
+                    asm volatile("bar.sync %0, 256;" ::"r"(1 + g) : "memory");
+                    if (lead) mbar_arrive_cluster(map_rank(smem_u32(&h_full[sb]), 0));
                 }
-                tc_fence_before();
-                if constexpr (C::kOut) fence_async_shared();
-                chunk_sync();
-                if (lead) {
-                    mbar_arrive_cluster(h_bar);
-                    if constexpr (BWD && C::kOut) {
-                        // the staged tiles are also what the weight gradients read: whole lines by TMA (stored
-                        // from registers, a warp's 32 rows cost the memory pipe 32 cycles an instruction)
-                        const int row0 = row - r;
+            }
+        } else {
+            // all warps on every chunk, a warp 16 of the columns: the three tiles that go out fit in shared
+            // memory once, and a chunk's values wait in registers until the last chunk's have left it
+            const int s = ((warp - 2) >> 2) * 16;
+            const bool lead = threadIdx.x == 64;
+            for (int item = pair; item < p.items; item += n_pairs) {
+                const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
+                const int row0 = (item / p.parts) * 256 + (int)rank * 128;
+                for (int c = 0; c < n; ++c, ++k) {
+                    const int f0 = f_first + c * 64, sb = (int)(k % SB);
+                    const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(sb * C::kSCols + s);
+                    wait_step(k);
+                    tc_fence_after();
+                    uint32_t wg[8], wu[8], wh[8];
+#pragma unroll
+                    for (int q = 0; q < 16; q += 8) {
+                        uint32_t vg[8], vu[8], vd[8], bias[8];
+                        tmem_read(t0 + (uint32_t)q, vg);
+                        tmem_read(t0 + (uint32_t)(64 + q), vu);
+                        tmem_read(t0 + (uint32_t)(128 + q), vd);
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4)
+                            *reinterpret_cast<uint4 *>(bias + j) = *reinterpret_cast<const uint4 *>(bias_s + f0 + s + q + j);
+                        tmem_wait(vg, vu, vd);
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            float h[2], dg[2], du[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float u = __uint_as_float(vu[j + e]) + __uint_as_float(bias[j + e] & 0xffff0000u);
+                                const float d = __uint_as_float(vd[j + e]);
+                                float slope;
+                                const float act =
+                                    Act<ACT>::fast(__uint_as_float(vg[j + e]) + __uint_as_float(bias[j + e] << 16), &slope);
+                                h[e] = act * u;
+                                du[e] = d * act;
+                                dg[e] = d * u * slope;
+                            }
+                            wg[(q + j) / 2] = pack_bf16(dg[0], dg[1]);
+                            wu[(q + j) / 2] = pack_bf16(du[0], du[1]);
+                            wh[(q + j) / 2] = pack_bf16(h[0], h[1]);
+                        }
+                    }
+                    tc_fence_before();
+                    if (lead) store_wait_read();  // the last chunk's tiles have been copied out
+                    epi_sync();
+                    if (C::kOut && k) wait_bar(smem_u32(y_done), (k - 1) & 1u, abort_flag, p.err);  // and multiplied
+                    const uint32_t o0 = swizzled(r, s / 8), o1 = swizzled(r, s / 8 + 1);
+                    *reinterpret_cast<uint4 *>(staged + o0) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+                    *reinterpret_cast<uint4 *>(staged + o1) = make_uint4(wg[4], wg[5], wg[6], wg[7]);
+                    *reinterpret_cast<uint4 *>(staged + kBox + o0) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+                    *reinterpret_cast<uint4 *>(staged + kBox + o1) = make_uint4(wu[4], wu[5], wu[6], wu[7]);
+                    *reinterpret_cast<uint4 *>(staged + 2 * kBox + o0) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                    *reinterpret_cast<uint4 *>(staged + 2 * kBox + o1) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
+                    fence_async_shared();
+                    epi_sync();
+                    if (lead) {
+                        mbar_arrive_cluster(map_rank(smem_u32(&h_full[sb]), 0));
+                        // whole lines by TMA: stored from registers, a warp's 32 rows cost the memory pipe 32
+                        // cycles an instruction (the n=20k chunk 2,460 -> 3,700 cycles)
                         if (row0 < p.M && f0 < p.F) {
-                            tma_store_tile(&p.dg_map, smem_u32(st), f0, row0);
-                            tma_store_tile(&p.du_map, smem_u32(st + kBox), f0, row0);
+                            tma_store_tile(&p.dg, smem_u32(staged), f0, row0);
+                            tma_store_tile(&p.du, smem_u32(staged + kBox), f0, row0);
+                            tma_store_tile(&p.h, smem_u32(staged + 2 * kBox), f0, row0);
                         }
                         store_commit();
                     }
                 }
             }
+            if (lead) store_wait_all();
         }
-        if (lead) store_wait_all();
     } else if constexpr (C::kOut) {
-        // ---------------- the row block's result
+        // ---------------- the row block's result, 64 columns at a time through two tiles in shared memory: the
+        // residual comes in by TMA long before, the sum goes out by TMA
         const int quarter = warp & 3, r = quarter * 32 + lane;
-        const bool lead = threadIdx.x == 64 + 512;
+        const bool lead = threadIdx.x == 64 + 512, with_res = !BWD && p.has_res;
         for (int i = threadIdx.x - 576; i < EB * 64; i += 128)
             bd_s[i] = p.bd && i < p.E ? __bfloat162float(p.bd[i]) : 0.f;
+        // residual of pass q (row block q / EB of this pair, columns 64 (q % EB)) into tile q % 2
+        auto load_res = [&](uint32_t q) {
+            const int item = pair + (int)(q / EB) * n_pairs;
+            if (!with_res || item >= p.items) return;
+            const int row0 = (item / p.parts) * 256 + (int)rank * 128;
+            const uint32_t rb = smem_u32(&res_full[q & 1u]);
+            armed[3] = q + 1;
+            if (row0 < p.M) {
+                mbar_arrive_expect_tx(rb, kBox);
+                tma_load_2d(smem_u32(out_s + (q & 1u) * kBox), &p.res, (int)(q % EB) * 64, row0, rb);
+            } else {
+                mbar_arrive(rb);
+            }
+        };
+        if (lead) {
+            load_res(0);
+            load_res(1);
+        }
         group_sync(2);
-        uint32_t i = 0;
+        uint32_t i = 0, q = 0;
         for (int item = pair; item < p.items; item += n_pairs, ++i) {
             const int ob = (int)(i % OB);
-            const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
-            const bool live = row < p.M;
-            wait_bar(smem_u32(&out_full[ob]), (i / OB) & 1u, abort_flag, p.err);
-            tc_fence_after();
-            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(2 * C::kSCols + ob * EB * 64);
+            const int row0 = (item / p.parts) * 256 + (int)rank * 128;
+            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(SB * C::kSCols + ob * EB * 64);
 #pragma unroll 1
-            for (int s0 = 0; s0 < EB * 64; s0 += 64) {
-                uint32_t e[4][8];
-                const bool with_res = !BWD && p.res && live;
-                if (with_res)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int c = s0 + 16 * q, left = p.E - c;
-                        if (left > 0) load16(p.res + (size_t)row * p.E + c, e[q], left, p.wide_e && left >= 16);
+            for (int cb = 0; cb < EB; ++cb, ++q) {
+                uint8_t *st = out_s + (q & 1u) * kBox;
+                if (cb == 0) {
+                    wait_bar(smem_u32(&out_full[ob]), (i / OB) & 1u, abort_flag, p.err);
+                    tc_fence_after();
+                }
+                if (with_res) {
+                    wait_bar(smem_u32(&res_full[q & 1u]), (q >> 1) & 1u, abort_flag, p.err);
+                } else {
+                    if (lead) store_wait_read1();  // the tile of two passes back has been copied out
+                    group_sync(2);
+                }
+#pragma unroll 1
+                for (int s = 0; s < 64; s += 16) {
+                    uint32_t v[16], w[8], e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    tmem_read(t0 + (uint32_t)(cb * 64 + s), v);
+                    uint4 *p0 = reinterpret_cast<uint4 *>(st + swizzled(r, s / 8));
+                    uint4 *p1 = reinterpret_cast<uint4 *>(st + swizzled(r, s / 8 + 1));
+                    if (with_res) {
+                        const uint4 a = *p0, b = *p1;
+                        e[0] = a.x, e[1] = a.y, e[2] = a.z, e[3] = a.w;
+                        e[4] = b.x, e[5] = b.y, e[6] = b.z, e[7] = b.w;
                     }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int c = s0 + 16 * q, left = p.E - c;
-                    uint32_t v[16], w[8];
-                    tmem_ld16(t0 + (uint32_t)c, v);
                     tmem_wait(v);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
-                        if constexpr (!BWD) {
-                            const float2 bb = *reinterpret_cast<const float2 *>(bd_s + c + 2 * j);
-                            a += bb.x;
-                            b += bb.y;
-                            if (with_res) {
-                                a += __uint_as_float(e[q][j] << 16);
-                                b += __uint_as_float(e[q][j] & 0xffff0000u);
-                            }
-                        }
-                        w[j] = pack_bf16(a, b);
+                        const float2 bb = *reinterpret_cast<const float2 *>(bd_s + cb * 64 + s + 2 * j);
+                        w[j] = pack_bf16(__uint_as_float(v[2 * j]) + bb.x + __uint_as_float(e[j] << 16),
+                                         __uint_as_float(v[2 * j + 1]) + bb.y + __uint_as_float(e[j] & 0xffff0000u));
                     }
-                    if (live && left > 0 && p.out) store16(p.out + (size_t)row * p.E + c, w, left, p.wide_e && left >= 16);
+                    *p0 = make_uint4(w[0], w[1], w[2], w[3]);
+                    *p1 = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+                if (cb == EB - 1) tc_fence_before();
+                fence_async_shared();
+                group_sync(2);
+                if (lead) {
+                    if (cb == EB - 1) mbar_arrive_cluster(map_rank(smem_u32(&out_empty[ob]), 0));
+                    if (p.has_out && row0 < p.M) tma_store_tile(&p.out, smem_u32(st), cb * 64, row0);
+                    store_commit();
+                    if (with_res) {
+                        store_wait_read();
+                        load_res(q + 2);
+                    }
                 }
             }
-            tc_fence_before();
-            group_sync(2);
-            if (lead) mbar_arrive_cluster(map_rank(smem_u32(&out_empty[ob]), 0));
         }
+        if (lead) store_wait_all();
     }
 
     __syncthreads();
@@ -583,6 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             drain(s_full, armed[1], NS);
             drain(y_full, armed[2], NY);
         }
+        if (*abort_flag && armed[3])
+            for (uint32_t i = armed[3] > 2 ? armed[3] - 2 : 0; i < armed[3]; ++i)
+                mbar_wait(smem_u32(&res_full[i & 1u]), (i >> 1) & 1u, (volatile int *)&dummy, p.err);
     }
     __syncthreads();
     __syncwarp();
@@ -675,8 +716,6 @@ pmha_status launch_width(pmha_act act, Params &p, const char *stage, cudaStream_
     }
 }
 
-bool aligned32(const void *p) { return ((uintptr_t)p & 31u) == 0; }
-
 }  // namespace
 
 bool ffn_fused_supported(int64_t E, int64_t F) { return E <= 256 && F <= kMaxHidden; }
@@ -693,13 +732,14 @@ pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd
     p.items = (int)((a.M + 255) / 256);
     p.chunks = (int)((f.F + 63) / 64);
     p.bg = (const __nv_bfloat16 *)f.bg, p.bu = (const __nv_bfloat16 *)f.bu, p.bd = (const __nv_bfloat16 *)f.bd;
-    p.res = (const __nv_bfloat16 *)residual;
     p.xs = a.x_scale, p.gs = a.wg_scale, p.us = a.wu_scale;
-    p.out = (__nv_bfloat16 *)out;
-    p.wide_e = f.E % 16 == 0 && aligned32(out) && aligned32(residual);
+    p.has_out = 1;
+    p.has_res = residual != nullptr;
     if (!make_tile_map(&p.x, a.x, a.M, f.E, f.E, es, 128) || !make_tile_map(&p.wg, a.wg, f.F, f.E, f.E, es, 64) ||
         !make_tile_map(&p.wu, a.wu, f.F, f.E, f.E, es, 64) ||
-        !make_tile_map(&p.wd, wd, f.E, f.F, f.F, 2, (uint32_t)(eb * 32))) {
+        !make_tile_map(&p.wd, wd, f.E, f.F, f.F, 2, (uint32_t)(eb * 32)) ||
+        !make_tile_map(&p.out, out, a.M, f.E, f.E, 2, 128) ||
+        (residual && !make_tile_map(&p.res, residual, a.M, f.E, f.E, 2, 128))) {
         set_error("ffn_block: cuTensorMapEncodeTiled failed");
         return PMHA_ERR_CUDA;
     }
@@ -716,15 +756,13 @@ pmha_status ffn_fused_backward(const FfnTc &f, const FfnHiddenArgs &a, const voi
     p.items = (int)((a.M + 255) / 256);
     p.chunks = (int)((f.F + 63) / 64);
     p.bg = (const __nv_bfloat16 *)f.bg, p.bu = (const __nv_bfloat16 *)f.bu;
-    p.out = (__nv_bfloat16 *)dx;
-    p.h = (__nv_bfloat16 *)a.h, p.dg = (__nv_bfloat16 *)a.dg, p.du = (__nv_bfloat16 *)a.du;
-    p.wide_e = f.E % 16 == 0 && aligned32(dx);
-    p.wide_f = f.F % 16 == 0;
+    p.has_out = dx != nullptr;
     if (!make_tile_map(&p.x, a.x, a.M, f.E, f.E, 2, 128) || !make_tile_map(&p.dy, a.dy, a.M, f.E, f.E, 2, 128) ||
         !make_tile_map(&p.wg, a.wg, f.F, f.E, f.E, 2, 64) || !make_tile_map(&p.wu, a.wu, f.F, f.E, f.E, 2, 64) ||
         !make_tile_map(&p.wd, a.wd_t, f.F, f.E, f.E, 2, 32) ||
-        !make_tile_map(&p.dg_map, a.dg, a.M, f.F, f.F, 2, 128) ||
-        !make_tile_map(&p.du_map, a.du, a.M, f.F, f.F, 2, 128) ||
+        !make_tile_map(&p.h, a.h, a.M, f.F, f.F, 2, 128) || !make_tile_map(&p.dg, a.dg, a.M, f.F, f.F, 2, 128) ||
+        !make_tile_map(&p.du, a.du, a.M, f.F, f.F, 2, 128) ||
+        (dx && !make_tile_map(&p.out, dx, a.M, f.E, f.E, 2, 128)) ||
         !make_tile_map(&p.wgt, wg_t, f.E, f.F, f.F, 2, (uint32_t)(eb * 32)) ||
         !make_tile_map(&p.wut, wu_t, f.E, f.F, f.F, 2, (uint32_t)(eb * 32))) {
         set_error("ffn_block_backward: cuTensorMapEncodeTiled failed");
