@@ -363,7 +363,7 @@ int f32_splits(int64_t E, int64_t F, int64_t rows)
     return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)num_sms() * 4 / tiles, ceil_div(rows, 128), 64}));
 }
 
-Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward)
+Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
 {
     Plan l = {};
     const bool bf16 = p->dtype == PMHA_BF16;
@@ -371,7 +371,7 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward)
     l.E2 = bf16 ? round8(p->embed_dim) : p->embed_dim;
     l.F2 = bf16 ? round8(p->hidden_dim) : p->hidden_dim;
     l.padded = l.E2 != p->embed_dim || l.F2 != p->hidden_dim;
-    l.fused = bf16 && ffn_fused_supported(l.E2, l.F2) && (backward || rows >= kFusedRows);
+    l.fused = bf16 && ffn_fused_supported(l.E2, l.F2, backward, q8) && (backward || rows >= kFusedRows);
     const int64_t per_row = l.F2 * (int64_t)es * (backward ? 3 : 1);
     // a block of rows fills the pairs of SMs a whole number of times where L2 holds that many, else
     // once where that is not too much memory
@@ -501,7 +501,7 @@ pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_qu
         set_error("%s: out overlaps an input", who);
         return PMHA_ERR_INVALID_ARG;
     }
-    const Plan l = plan_of(p, rows, false);
+    const Plan l = plan_of(p, rows, false, q8 != nullptr);
     PMHA_TRY(check_workspace(who, workspace, ws_bytes, l.total));
     char *ws = (char *)workspace;
     pmha_ffn_params q;
@@ -558,7 +558,7 @@ extern "C" {
 size_t pmha_ffn_forward_workspace_size(const pmha_ffn_params *params, int64_t rows)
 {
     if (check_ffn("pmha_ffn_forward", params, rows, false) != PMHA_OK) return SIZE_MAX;
-    return rows ? plan_of(params, rows, false).total : 0;
+    return rows ? plan_of(params, rows, false, false).total : 0;
 }
 
 pmha_status pmha_ffn_forward(const pmha_ffn_params *params, const void *x, const void *residual, int64_t rows,
@@ -572,7 +572,7 @@ pmha_status pmha_ffn_forward(const pmha_ffn_params *params, const void *x, const
 size_t pmha_ffn_forward_quantized_workspace_size(const pmha_ffn_params *params, int64_t rows)
 {
     if (check_ffn("pmha_ffn_forward_quantized", params, rows, true) != PMHA_OK) return SIZE_MAX;
-    return rows ? plan_of(params, rows, false).total : 0;
+    return rows ? plan_of(params, rows, false, true).total : 0;
 }
 
 pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha_ffn_quantized *quantized,
@@ -598,7 +598,7 @@ pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha
 size_t pmha_ffn_backward_workspace_size(const pmha_ffn_params *params, int64_t rows)
 {
     if (check_ffn("pmha_ffn_backward", params, rows, false) != PMHA_OK) return SIZE_MAX;
-    return rows ? plan_of(params, rows, true).total : 0;
+    return rows ? plan_of(params, rows, true, false).total : 0;
 }
 
 pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, const void *dout, int64_t rows, void *dx,
@@ -650,7 +650,7 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
             return PMHA_ERR_INVALID_ARG;
         }
     }
-    const Plan l = plan_of(p, rows, true);
+    const Plan l = plan_of(p, rows, true, false);
     PMHA_TRY(check_workspace(who, workspace, workspace_bytes, l.total));
     char *ws = (char *)workspace;
     const bool bf16 = p->dtype == PMHA_BF16;

@@ -46,7 +46,6 @@ using namespace tcu;
 
 constexpr int kThreads = 704;       // 2 + 16 + 4 warps
 constexpr int kBox = 128 * 128;     // 128 rows of 128 bytes
-constexpr int kMaxHidden = 2048;    // bias (and scale) columns held in shared memory
 constexpr int kSmemMost = 232448;
 
 // EB: blocks of 64 output columns; KB: blocks of 128 bytes of a token.
@@ -60,10 +59,12 @@ struct Cfg {
     static constexpr int SG = BWD ? 1 : !Q8 && EB == 4 ? 2 : KB;        // K blocks of a stage of the S ring
     static constexpr int kSSlot = SG * kSBlock;
     static constexpr int kYSlot = kOut ? EB * (BWD ? 8192 : 4096) : 0;  // half of the output columns of a chunk
-    static constexpr int kNY = kOut ? 2 : 0;
+    static constexpr int kNY = !kOut ? 0 : SB == 3 ? 3 : 2;
+    static constexpr int kMaxHidden = !BWD && !Q8 && EB == 2 ? 1024 : 2048;  // bias (and scale) columns held
     static constexpr int kStaged = BWD ? 3 * kBox : kBox;       // dg, du and h, or h
     static constexpr int kStages = BWD ? 1 : SB;
-    static constexpr int kOutTiles = kOut ? 2 * kBox : 0;       // two tiles of 64 result columns
+    static constexpr int kOT = BWD ? 1 : 2;                     // tiles of 64 result columns
+    static constexpr int kOutTiles = kOut ? kOT * kBox : 0;
     static constexpr int kSCols = BWD ? 192 : 128;
     static constexpr int kVec = kMaxHidden * (BWD ? 4 : 8) + 1024;      // gate and up biases; output bias
     static constexpr int kScales = Q8 ? kMaxHidden * 8 : 0;
@@ -141,15 +142,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     uint8_t *s_ring = x_s + XB * C::kX;               // [NS]
     uint8_t *y_ring = s_ring + NS * C::kSSlot;        // [kNY]
     uint8_t *staged = y_ring + C::kNY * C::kYSlot;    // [kStages]
-    uint8_t *out_s = staged + C::kStages * C::kStaged;  // [2] tiles of 64 result columns
+    uint8_t *out_s = staged + C::kStages * C::kStaged;  // [kOT] tiles of 64 result columns
     float *bd_s = (float *)(out_s + C::kOutTiles);      // [256]
-    float *bg_s = bd_s + 256, *bu_s = bg_s + kMaxHidden;  // forward: float32, times the activation's constants
+    float *bg_s = bd_s + 256, *bu_s = bg_s + C::kMaxHidden;  // forward: float32, times the activation's constants
     uint32_t *bias_s = (uint32_t *)bg_s;                  // backward: (bg, bu) as bf16
-    float *gs_s = (float *)((uint8_t *)bd_s + C::kVec), *us_s = gs_s + kMaxHidden;
+    float *gs_s = (float *)((uint8_t *)bd_s + C::kVec), *us_s = gs_s + C::kMaxHidden;
     uint64_t *bar = (uint64_t *)((uint8_t *)gs_s + C::kScales);
     uint64_t *x_full = bar, *s_full = x_full + 2, *s_empty = s_full + 4, *y_full = s_empty + 4, *step = y_full + 4,
              *h_full = step + 4, *out_full = h_full + 3, *out_empty = out_full + 2, *res_full = out_empty + 2,
-             *y_done = res_full + 2, *mma_done = y_done + 1;
+             *y_done = res_full + 2, *mma_done = y_done + 4;
     uint32_t *tmem_holder = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
     volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted: x, S and Y slots, residual
@@ -171,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             mbar_init(smem_u32(&s_empty[i]), 1);
             mbar_init(smem_u32(&y_full[i]), 1);
             mbar_init(smem_u32(&step[i]), 1);
+            mbar_init(smem_u32(&y_done[i]), 1);
         }
-        mbar_init(smem_u32(y_done), 1);
         mbar_init(smem_u32(mma_done), 1);
         *abort_flag = 0;
         armed[0] = armed[1] = armed[2] = armed[3] = 0;
@@ -188,10 +189,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
     // item -> row block, first chunk; every item has the chunks of one part (the last part may have fewer)
     auto chunks_of = [&](int item) { return min(p.per_part, p.chunks - (item % p.parts) * p.per_part); };
 
-    // Step k: the product Y of chunk k - SB, then S of chunk k, committed together: S(k) can be read, and the
-    // staged values and weights of Y(k - SB) and the weights of S(k) are free. Four barriers in turn: a step is
-    // over before the one four later can be issued, whoever waits for it.
-    auto wait_step = [&](uint32_t k) { return wait_bar(smem_u32(&step[k & 3u]), (k >> 2) & 1u, abort_flag, p.err); };
+    // Step k: S of chunk k into the buffer that chunk k - SB's epilogue has read, then Y of chunk k - SB. Four
+    // barriers each in turn tell that S(k) can be read, and that Y(k) is over: its staged values and weights are
+    // free. Either is over before the one four later can be issued, whoever waits for it.
+    auto wait_s = [&](uint32_t k) { return wait_bar(smem_u32(&step[k & 3u]), (k >> 2) & 1u, abort_flag, p.err); };
+    auto wait_y = [&](uint32_t k) { return wait_bar(smem_u32(&y_done[k & 3u]), (k >> 2) & 1u, abort_flag, p.err); };
 
     if (warp == 0) {
         // ---------------- TMA producer of this CTA, in the issuer's order
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             const int b = (int)(nx % XB);
             const uint32_t before = XB == 1 ? last1 : last2;
             // a step more than NS back is known to be over (load_s of this step waited for a later one)
-            if (before && (C::SG < KB || before + NS > k) && !wait_step(before - 1)) return;
+            if (before && (C::SG < KB || before + NS > k) && !wait_s(before - 1)) return;
             if (one) {
                 const uint32_t fb = map_rank(smem_u32(&x_full[b]), 0);
                 if (rank == 0) mbar_arrive_expect_tx(smem_u32(&x_full[b]), 2 * C::kX);
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 if (j == NS * C::SG && row >= 0) load_x(row);
                 if constexpr (C::SG < KB) {
                     if (!wait_bar(smem_u32(&s_empty[slot]), ((ns / NS) & 1u) ^ 1u, abort_flag, p.err)) return;
-                } else if (k >= (uint32_t)NS && !wait_step(k - NS)) return;
+                } else if (k >= (uint32_t)NS && !wait_s(k - NS)) return;
                 if (one) {
                     const uint32_t fb = map_rank(smem_u32(&s_full[slot]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s_full[slot]), 2 * C::kSSlot);
@@ -239,9 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 }
             }
         };
-        auto load_y = [&](int f0) {  // of chunk ny; its slot was read by step ny - NY + SB
+        auto load_y = [&](int f0) {
             const int slot = (int)(ny % NY);
-            if (ny >= (uint32_t)NY && !wait_step(ny - NY + SB)) return;
+            if (ny >= (uint32_t)NY && !wait_y(ny - NY)) return;
             if (one) {
                 const uint32_t fb = map_rank(smem_u32(&y_full[slot]), 0);
                 if (rank == 0) mbar_arrive_expect_tx(smem_u32(&y_full[slot]), 2 * C::kYSlot);
@@ -292,11 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             auto run_step = [&](uint32_t y, bool has_s, bool first, bool last) {
                 const uint32_t ky = k - SB;  // the chunk of Y
                 const int ys = (int)(ky % NY), yb = (int)(ky % SB), xb = (int)(nx % XB), ob = (int)(n_out % OB);
-                // what is loaded long before comes first: only the hidden values are waited for in earnest
-                if (C::kOut && y) {
-                    wait_for(&y_full[ys], (ky / NY) & 1u);
-                    if (y & 1u) wait_for(&out_empty[ob], ((n_out / OB) & 1u) ^ 1u);
-                }
                 if (has_s) {
                     if (first) wait_for(&x_full[xb], (nx / XB) & 1u);
                     if constexpr (C::SG == KB) wait_for(&s_full[ns % NS], (ns / NS) & 1u);
@@ -304,24 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 if (y) wait_for(&h_full[yb], (ky / SB) & 1u);
                 if (!ok) return;
                 tc_fence_after();
-                if constexpr (C::kOut) {
-                    if (y && one) {
-                        const uint32_t d = tmem + SB * C::kSCols + (uint32_t)(ob * EB * 64);
-                        const uint32_t a = smem_u32(staged + (BWD ? 0 : yb) * C::kStaged);
-                        const uint32_t b = smem_u32(y_ring + ys * C::kYSlot);
-#pragma unroll
-                        for (int z = 0; z < (BWD ? 2 : 1); ++z) {
-                            const uint64_t da = smem_desc(a + z * kBox), db = smem_desc(b + z * EB * 4096);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                mma_pair<false>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q),
-                                                idesc_of(false, false, 256, EB * 64), z + q ? 1u : (y & 1u) ^ 1u);
-                        }
-                        if constexpr (BWD) mma_commit_pair(smem_u32(y_done));
-                        if (y & 2u) mma_commit_pair(smem_u32(&out_full[ob]));
-                    }
-                    if (y & 2u) ++n_out;
-                }
                 if (has_s) {
                     const uint32_t d = tmem + (k % SB) * C::kSCols;
                     const uint32_t xa = smem_u32(x_s + xb * C::kX);
@@ -355,8 +334,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                         }
                     }
                     if (last) ++nx;
+                    if (one) mma_commit_pair(smem_u32(&step[k & 3u]));
                 }
-                if (one) mma_commit_pair(smem_u32(&step[k & 3u]));
+                if constexpr (C::kOut) {
+                    if (y) {
+                        wait_for(&y_full[ys], (ky / NY) & 1u);
+                        if (y & 1u) wait_for(&out_empty[ob], ((n_out / OB) & 1u) ^ 1u);
+                        if (!ok) return;
+                        tc_fence_after();
+                        if (one) {
+                            const uint32_t d = tmem + SB * C::kSCols + (uint32_t)(ob * EB * 64);
+                            const uint32_t a = smem_u32(staged + (BWD ? 0 : yb) * C::kStaged);
+                            const uint32_t b = smem_u32(y_ring + ys * C::kYSlot);
+#pragma unroll
+                            for (int z = 0; z < (BWD ? 2 : 1); ++z) {
+                                const uint64_t da = smem_desc(a + z * kBox), db = smem_desc(b + z * EB * 4096);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    mma_pair<false>(d, da + (uint64_t)(2 * q), db + (uint64_t)(2 * q),
+                                                    idesc_of(false, false, 256, EB * 64), z + q ? 1u : (y & 1u) ^ 1u);
+                            }
+                            mma_commit_pair(smem_u32(&y_done[ky & 3u]));
+                            if (y & 2u) mma_commit_pair(smem_u32(&out_full[ob]));
+                        }
+                        if (y & 2u) ++n_out;
+                    }
+                }
                 __syncwarp();
                 ++k;
             };
@@ -412,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                     const int f0 = f_first + c * 64, sb = (int)(k % SB);
                     const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(sb * C::kSCols);
                     uint8_t *st = staged + sb * C::kStaged;
-                    wait_step(k);  // and the product with the values that were staged here is over
+                    wait_s(k);
+                    if (k >= (uint32_t)SB) wait_y(k - SB);  // of the values that were staged here
                     tc_fence_after();
 #pragma unroll 1
                     for (int s = half * 32; s < half * 32 + 32; s += 16) {  // rolled: the SM's warps share its instruction cache
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                 for (int c = 0; c < n; ++c, ++k) {
                     const int f0 = f_first + c * 64, sb = (int)(k % SB);
                     const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(sb * C::kSCols + s);
-                    wait_step(k);
+                    wait_s(k);
                     tc_fence_after();
                     uint32_t wg[8], wu[8], wh[8];
 #pragma unroll
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                     tc_fence_before();
                     if (lead) store_wait_read();  // the last chunk's tiles have been copied out
                     epi_sync();
-                    if (C::kOut && k) wait_bar(smem_u32(y_done), (k - 1) & 1u, abort_flag, p.err);  // and multiplied
+                    if (C::kOut && k) wait_y(k - 1);  // and multiplied
                     const uint32_t o0 = swizzled(r, s / 8), o1 = swizzled(r, s / 8 + 1);
                     *reinterpret_cast<uint4 *>(staged + o0) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
                     *reinterpret_cast<uint4 *>(staged + o1) = make_uint4(wg[4], wg[5], wg[6], wg[7]);
@@ -532,24 +536,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
         const bool lead = threadIdx.x == 64 + 512, with_res = !BWD && p.has_res;
         for (int i = threadIdx.x - 576; i < EB * 64; i += 128)
             bd_s[i] = p.bd && i < p.E ? __bfloat162float(p.bd[i]) : 0.f;
-        // residual of pass q (row block q / EB of this pair, columns 64 (q % EB)) into tile q % 2
-        auto load_res = [&](uint32_t q) {
-            const int item = pair + (int)(q / EB) * n_pairs;
-            if (!with_res || item >= p.items) return;
+        // residual of pass n (row block n / EB of this pair, columns 64 (n % EB)) into tile n % kOT
+        uint32_t loaded = 0;
+        auto load_res = [&]() {
+            const uint32_t n = loaded++;
+            const int item = pair + (int)(n / EB) * n_pairs;
+            if (item >= p.items) return;
             const int row0 = (item / p.parts) * 256 + (int)rank * 128;
-            const uint32_t rb = smem_u32(&res_full[q & 1u]);
-            armed[3] = q + 1;
+            const uint32_t rb = smem_u32(&res_full[n % C::kOT]);
+            armed[3] = n + 1;
             if (row0 < p.M) {
                 mbar_arrive_expect_tx(rb, kBox);
-                tma_load_2d(smem_u32(out_s + (q & 1u) * kBox), &p.res, (int)(q % EB) * 64, row0, rb);
+                tma_load_2d(smem_u32(out_s + (n % C::kOT) * kBox), &p.res, (int)(n % EB) * 64, row0, rb);
             } else {
                 mbar_arrive(rb);
             }
         };
-        if (lead) {
-            load_res(0);
-            load_res(1);
-        }
+        if (lead && with_res)
+            while (loaded < (uint32_t)C::kOT) load_res();
         group_sync(2);
         uint32_t i = 0, q = 0;
         for (int item = pair; item < p.items; item += n_pairs, ++i) {
@@ -558,37 +562,44 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(SB * C::kSCols + ob * EB * 64);
 #pragma unroll 1
             for (int cb = 0; cb < EB; ++cb, ++q) {
-                uint8_t *st = out_s + (q & 1u) * kBox;
+                uint8_t *st = out_s + (q % C::kOT) * kBox;
                 if (cb == 0) {
                     wait_bar(smem_u32(&out_full[ob]), (i / OB) & 1u, abort_flag, p.err);
                     tc_fence_after();
                 }
                 if (with_res) {
-                    wait_bar(smem_u32(&res_full[q & 1u]), (q >> 1) & 1u, abort_flag, p.err);
+                    wait_bar(smem_u32(&res_full[q % C::kOT]), (q / C::kOT) & 1u, abort_flag, p.err);
                 } else {
-                    if (lead) store_wait_read1();  // the tile of two passes back has been copied out
+                    if (lead) {  // the tile's last columns have been copied out
+                        if constexpr (C::kOT == 2) store_wait_read1();
+                        else store_wait_read();
+                    }
                     group_sync(2);
                 }
 #pragma unroll 1
-                for (int s = 0; s < 64; s += 16) {
-                    uint32_t v[16], w[8], e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    tmem_read(t0 + (uint32_t)(cb * 64 + s), v);
-                    uint4 *p0 = reinterpret_cast<uint4 *>(st + swizzled(r, s / 8));
-                    uint4 *p1 = reinterpret_cast<uint4 *>(st + swizzled(r, s / 8 + 1));
-                    if (with_res) {
-                        const uint4 a = *p0, b = *p1;
-                        e[0] = a.x, e[1] = a.y, e[2] = a.z, e[3] = a.w;
-                        e[4] = b.x, e[5] = b.y, e[6] = b.z, e[7] = b.w;
-                    }
-                    tmem_wait(v);
+                for (int s = 0; s < 64; s += 32) {
+                    uint32_t v0[16], v1[16];
+                    tmem_read(t0 + (uint32_t)(cb * 64 + s), v0);
+                    tmem_read(t0 + (uint32_t)(cb * 64 + s + 16), v1);
+                    tmem_wait(v0, v1);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 bb = *reinterpret_cast<const float2 *>(bd_s + cb * 64 + s + 2 * j);
-                        w[j] = pack_bf16(__uint_as_float(v[2 * j]) + bb.x + __uint_as_float(e[j] << 16),
-                                         __uint_as_float(v[2 * j + 1]) + bb.y + __uint_as_float(e[j] & 0xffff0000u));
+                    for (int u = 0; u < 4; ++u) {
+                        uint4 *at = reinterpret_cast<uint4 *>(st + swizzled(r, s / 8 + u));
+                        const uint4 a = with_res ? *at : make_uint4(0, 0, 0, 0);
+                        const float4 b0 = *reinterpret_cast<const float4 *>(bd_s + cb * 64 + s + 8 * u);
+                        const float4 b1 = *reinterpret_cast<const float4 *>(bd_s + cb * 64 + s + 8 * u + 4);
+                        const uint32_t e[4] = {a.x, a.y, a.z, a.w};
+                        const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t *v = u < 2 ? v0 + 8 * u : v1 + 8 * (u - 2);
+                            w[j] = pack_bf16(__uint_as_float(v[2 * j]) + bb[2 * j] + __uint_as_float(e[j] << 16),
+                                             __uint_as_float(v[2 * j + 1]) + bb[2 * j + 1] +
+                                                 __uint_as_float(e[j] & 0xffff0000u));
+                        }
+                        *at = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *p0 = make_uint4(w[0], w[1], w[2], w[3]);
-                    *p1 = make_uint4(w[4], w[5], w[6], w[7]);
                 }
                 if (cb == EB - 1) tc_fence_before();
                 fence_async_shared();
@@ -597,9 +608,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                     if (cb == EB - 1) mbar_arrive_cluster(map_rank(smem_u32(&out_empty[ob]), 0));
                     if (p.has_out && row0 < p.M) tma_store_tile(&p.out, smem_u32(st), cb * 64, row0);
                     store_commit();
-                    if (with_res) {
-                        store_wait_read();
-                        load_res(q + 2);
+                    // a tile takes its next residual when its store has read it: within a row block only the one
+                    // that is needed next (the store before this one is long read), at its end all
+                    if (with_res && (cb == EB - 1 || loaded <= q + 1)) {
+                        if (cb == EB - 1) store_wait_read();
+                        else store_wait_read1();
+                        while (loaded <= (cb == EB - 1 ? q + C::kOT : q + 1)) load_res();
                     }
                 }
             }
@@ -622,8 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             drain(y_full, armed[2], NY);
         }
         if (*abort_flag && armed[3])
-            for (uint32_t i = armed[3] > 2 ? armed[3] - 2 : 0; i < armed[3]; ++i)
-                mbar_wait(smem_u32(&res_full[i & 1u]), (i >> 1) & 1u, (volatile int *)&dummy, p.err);
+            for (uint32_t i = armed[3] > C::kOT ? armed[3] - C::kOT : 0; i < armed[3]; ++i)
+                mbar_wait(smem_u32(&res_full[i % C::kOT]), (i / C::kOT) & 1u, (volatile int *)&dummy, p.err);
     }
     __syncthreads();
     __syncwarp();
@@ -718,7 +732,11 @@ pmha_status launch_width(pmha_act act, Params &p, const char *stage, cudaStream_
 
 }  // namespace
 
-bool ffn_fused_supported(int64_t E, int64_t F) { return E <= 256 && F <= kMaxHidden; }
+bool ffn_fused_supported(int64_t E, int64_t F, bool backward, bool q8)
+{
+    const bool two = E > 64 && E <= 128 && !backward && !q8;
+    return E <= 256 && F <= (two ? Cfg<2, false, false>::kMaxHidden : Cfg<1, false, false>::kMaxHidden);
+}
 bool ffn_fused_dx(int64_t E) { return E <= 128; }
 
 pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
