@@ -19,9 +19,12 @@ PackedEncoderLayer, which runs them together with the layer.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import dataclasses
+import itertools
+import operator
 
 import torch
 
@@ -487,45 +490,52 @@ class PackedMultiheadAttention:
 
 
 # ---------------------------------------------------------------- the encoder around the layer
+# These calls are short on the GPU (a norm of a small batch takes 4 us), so the
+# checks in front of them are written for few Python operations.
 _HERE = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the pointer alone, without a Stream object
+_T = torch.Tensor
 
 
-def _on(device, stream):
-    """Runs a call on `stream` of `device`: what is allocated inside belongs to
-    that stream, so that its memory is not handed out again before the stream
-    has passed the call."""
+def _on(index, stream):
+    """Runs a call on `stream` of device `index`: what is allocated inside
+    belongs to that stream, so that its memory is not handed out again before
+    the stream has passed the call."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the call runs on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"the stream belongs to {stream.device}, the call runs on cuda:{index}")
         return torch.cuda.stream(stream)
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _check_rows(name, x, dtype=None):
-    """A contiguous CUDA tensor (..., width); returns (rows, width)."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1 or not x.is_contiguous() \
-            or (x.dtype not in _DTYPES if dtype is None else x.dtype != dtype):
+def _stream_of(index, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _library():
+    return _lib._lib if _lib._lib is not None else _lib.load()
+
+
+def _rows_of(name, x, dtype=None):
+    """(shape, rows, width, device index) of a contiguous CUDA tensor (..., width)."""
+    if not isinstance(x, _T) or not x.is_cuda or not x.is_contiguous() or not x.dim() \
+            or (x.dtype not in _DTYPES if dtype is None else x.dtype is not dtype):
         raise ValueError(f"{name} must be a contiguous CUDA tensor (..., width) of "
                          f"{'float32 or bfloat16' if dtype is None else dtype}")
-    width = x.shape[-1]
-    return (x.numel() // width if width else 0), width
+    shape = x.shape
+    width = shape[-1]
+    return shape, x.numel() // width if width else 0, width, x.get_device()
 
 
-def _check_like(name, t, like):
+def _like(name, t, shape, dtype, index):
+    """Pointer of a contiguous tensor of this shape, type and device (None: none)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype != like.dtype or t.device != like.device \
+    if not isinstance(t, _T) or t.shape != shape or t.dtype is not dtype or t.get_device() != index \
             or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(like.shape)} tensor of {like.dtype} on {like.device}")
-    return t.data_ptr()
-
-
-def _check_vector(name, t, n, dtype, device):
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n or t.dtype != dtype \
-            or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous ({n},) tensor of {dtype} on {device}")
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -534,17 +544,20 @@ def pmha_rms_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, resi
     """Root-mean-square norm over the last axis of s = x + residual:
     s / sqrt(mean(s^2) + eps) * weight. Returns (out, s), s rounded to x's type
     as the norm takes it, or (out, None) without a residual."""
-    rows, width = _check_rows("x", x)
-    w = _check_vector("weight", weight, width, x.dtype, x.device)
-    r = _check_like("residual", residual, x)
-    _check_like("out", out, x)
-    with _on(x.device, stream):
+    shape, rows, width, dev = _rows_of("x", x)
+    dtype = x.dtype
+    w = _like("weight", weight, (width,), dtype, dev)
+    r = _like("residual", residual, shape, dtype, dev)
+    o = _like("out", out, shape, dtype, dev)
+    with _on(dev, stream):
         if out is None:
             out = torch.empty_like(x)
+            o = out.data_ptr()
         s = None if residual is None else torch.empty_like(x)
-        st = _lib.load().pmha_rms_norm(_DTYPES[x.dtype], rows, width, x.data_ptr(), r, w, eps, _ptr(s), out.data_ptr(),
-                                       None, None, _stream_ptr(stream))
-    _lib.check(st, "pmha_rms_norm")
+        st = _library().pmha_rms_norm(_DTYPES[dtype], rows, width, x.data_ptr(), r, w, eps,
+                                      None if s is None else s.data_ptr(), o, None, None, _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_rms_norm")
     return out, s
 
 
@@ -553,16 +566,19 @@ def pmha_rms_norm_quantized(x: torch.Tensor, weight: torch.Tensor | None, eps: f
     """pmha_rms_norm with its output in 8 bits: (q, scale, s) with q in
     float8_e4m3fn, scale (...,) float32, norm ~ q * scale[..., None]; every q is
     the formula's value rounded once. What pmha_ffn_forward_quantized takes."""
-    rows, width = _check_rows("x", x)
-    w = _check_vector("weight", weight, width, x.dtype, x.device)
-    r = _check_like("residual", residual, x)
-    with _on(x.device, stream):
+    shape, rows, width, dev = _rows_of("x", x)
+    dtype = x.dtype
+    w = _like("weight", weight, (width,), dtype, dev)
+    r = _like("residual", residual, shape, dtype, dev)
+    with _on(dev, stream):
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale = x.new_empty(shape[:-1], dtype=torch.float32)
         s = None if residual is None else torch.empty_like(x)
-        st = _lib.load().pmha_rms_norm(_DTYPES[x.dtype], rows, width, x.data_ptr(), r, w, eps, _ptr(s), None,
-                                       q.data_ptr(), scale.data_ptr(), _stream_ptr(stream))
-    _lib.check(st, "pmha_rms_norm")
+        st = _library().pmha_rms_norm(_DTYPES[dtype], rows, width, x.data_ptr(), r, w, eps,
+                                      None if s is None else s.data_ptr(), None, q.data_ptr(), scale.data_ptr(),
+                                      _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_rms_norm")
     return q, scale, s
 
 
@@ -573,25 +589,34 @@ def pmha_rms_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, eps: fl
     returned): {"dx", "dweight"}; dx, in x's type, is the gradient of both
     summands and includes dsum, the sum's gradient from its other uses; dweight
     is float32 (None without a weight)."""
-    rows, width = _check_rows("x", x)
-    w = _check_vector("weight", weight, width, x.dtype, x.device)
-    dy = _check_like("dout", dout, x)
+    shape, rows, width, dev = _rows_of("x", x)
+    dtype = x.dtype
+    w = _like("weight", weight, (width,), dtype, dev)
+    dy = _like("dout", dout, shape, dtype, dev)
     if dout is None:
         raise ValueError("dout is missing")
-    ds = _check_like("dsum", dsum, x)
-    lib = _lib.load()
-    with _on(x.device, stream):
+    ds = _like("dsum", dsum, shape, dtype, dev)
+    lib = _library()
+    with _on(dev, stream):
         dx = torch.empty_like(x) if input_grad else None
         dw = ws = None
         need = 0
         if param_grad and weight is not None:
-            dw = torch.empty(width, dtype=torch.float32, device=x.device)
-            need = lib.pmha_rms_norm_backward_workspace_size(_DTYPES[x.dtype], rows, width)
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-        st = lib.pmha_rms_norm_backward(_DTYPES[x.dtype], rows, width, x.data_ptr(), w, eps, dy, ds, _ptr(dx),
-                                        _ptr(dw), _ptr(ws), need, _stream_ptr(stream))
-    _lib.check(st, "pmha_rms_norm_backward")
+            dw = x.new_empty(width, dtype=torch.float32)
+            need = lib.pmha_rms_norm_backward_workspace_size(_DTYPES[dtype], rows, width)
+            ws = x.new_empty(need, dtype=torch.uint8)
+        st = lib.pmha_rms_norm_backward(_DTYPES[dtype], rows, width, x.data_ptr(), w, eps, dy, ds, _ptr(dx), _ptr(dw),
+                                        _ptr(ws), need, _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_rms_norm_backward")
     return {"dx": dx, "dweight": dw}
+
+
+def _pointers(ts):
+    return array.array("q", map(_T.data_ptr, ts))
+
+
+_dtype_of = operator.attrgetter("dtype")
 
 
 def pmha_clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
@@ -599,63 +624,69 @@ def pmha_clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.
     tensors of one device; None entries are skipped) by
     min(1, max_norm / (norm + 1e-6)), norm the 2-norm of all their values, and
     returns the norm before scaling as a float32 scalar on the device. In place,
-    or into the tensors of `out` (one for each gradient, same shape and type)."""
+    or into the tensors of `out` (one for each gradient, same type and number of
+    values)."""
     grads = list(grads)
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError("out must have one tensor for each gradient")
-    if any(g is None for g in grads):
+    if any(map(operator.is_, grads, itertools.repeat(None))):
         keep = [i for i, g in enumerate(grads) if g is not None]
-        grads, outs = [grads[i] for i in keep], [outs[i] for i in keep]
+        grads, outs = [grads[i] for i in keep], outs if out is None else [outs[i] for i in keep]
+        if out is None:
+            outs = grads
     if not grads:
         raise ValueError("no gradients: the call needs a tensor to know its device")
-    T = torch.Tensor
-    for ts in (grads,) if out is None else (grads, outs):
-        if not all(isinstance(t, T) for t in ts) or not all(map(T.is_contiguous, ts)) \
-                or not all(t.is_cuda for t in ts) or len({t.device for t in ts}) > 1:
-            raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
-    device = grads[0].device
-    types = [_DTYPES.get(t.dtype, -1) for t in grads]
-    if -1 in types:
-        raise TypeError("gradients must be float32 or bfloat16")
-    if out is not None and (outs[0].device != device or
-                            any(o.shape != g.shape or o.dtype != g.dtype for g, o in zip(grads, outs))):
-        raise ValueError("each output must have its gradient's shape, type and device")
     n = len(grads)
-    gp = (ctypes.c_void_p * n)(*map(T.data_ptr, grads))
-    op = gp if out is None else (ctypes.c_void_p * n)(*map(T.data_ptr, outs))
-    sizes = (ctypes.c_int64 * n)(*map(T.numel, grads))
-    kinds = (ctypes.c_int * n)(*types)
-    lib = _lib.load()
+    # each step is one pass of a C-level map over the tensors: a stack of layers has hundreds
+    gp = _pointers(grads)  # TypeError for what is no tensor
+    sizes = array.array("q", map(_T.numel, grads))
+    devices = set(map(_T.get_device, grads))
+    kinds = array.array("i", map(_DTYPES.get, map(_dtype_of, grads), itertools.repeat(-1)))
+    dense = all(map(_T.is_contiguous, grads))
+    op = gp
+    if out is not None:
+        op = _pointers(outs)
+        devices |= set(map(_T.get_device, outs))
+        dense = dense and all(map(_T.is_contiguous, outs))
+        if array.array("q", map(_T.numel, outs)) != sizes or \
+                not all(map(operator.is_, map(_dtype_of, outs), map(_dtype_of, grads))):
+            raise ValueError("each output must have its gradient's type and number of values")
+    if not dense or len(devices) > 1 or -1 in devices:
+        raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
+    if -1 in kinds:
+        raise TypeError("gradients must be float32 or bfloat16")
+    dev = devices.pop()
+    lib = _library()
     need = lib.pmha_clip_grad_norm_workspace_size(n)
-    with _on(device, stream):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        st = lib.pmha_clip_grad_norm(n, gp, op, sizes, kinds, max_norm, norm.data_ptr(), ws.data_ptr(), need,
-                                     _stream_ptr(stream))
-    _lib.check(st, "pmha_clip_grad_norm")
+    with _on(dev, stream):
+        norm = grads[0].new_empty((), dtype=torch.float32)
+        ws = grads[0].new_empty(need, dtype=torch.uint8)
+        st = lib.pmha_clip_grad_norm(n, gp.buffer_info()[0], op.buffer_info()[0], sizes.buffer_info()[0],
+                                     kinds.buffer_info()[0], max_norm, norm.data_ptr(), ws.data_ptr(), need,
+                                     _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_clip_grad_norm")
     return norm
 
 
-def _ffn_struct(p, wg, wu, dtype) -> _lib.PmhaFfnParams:
-    """Checks a block's tensors and lists them for the library (wg, wu: None for
-    a quantized block)."""
+def _ffn_struct(p, dtype):
+    """Checks a block's tensors and lists them for the library; dtype: of its gate and up weights (None: wd's)."""
     wd = p.wd
-    if not isinstance(wd, torch.Tensor) or wd.dim() != 2 or wd.dtype not in _DTYPES or not wd.is_cuda \
-            or not wd.is_contiguous():
+    if not isinstance(wd, _T) or wd.dim() != 2 or wd.dtype not in _DTYPES or not wd.is_cuda or not wd.is_contiguous():
         raise ValueError("wd must be a contiguous (E, F) CUDA tensor of float32 or bfloat16")
     E, F = wd.shape
-    for n, w in (("wg", p.wg), ("wu", p.wu)):
-        want = wd.dtype if dtype is None else dtype
-        if not isinstance(w, torch.Tensor) or w.shape != (F, E) or w.dtype != want or w.device != wd.device \
-                or not w.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous ({F}, {E}) tensor of {want} on {wd.device}")
-    if p.act not in ACTS:
+    t, dev = wd.dtype, wd.get_device()
+    act = ACTS.get(p.act)
+    if act is None:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    return _lib.PmhaFfnParams(E, F, _DTYPES[wd.dtype], ACTS[p.act], wg, wu, wd.data_ptr(),
-                              _check_vector("bg", p.bg, F, wd.dtype, wd.device),
-                              _check_vector("bu", p.bu, F, wd.dtype, wd.device),
-                              _check_vector("bd", p.bd, E, wd.dtype, wd.device))
+    g = _like("wg", p.wg, (F, E), dtype or t, dev)
+    u = _like("wu", p.wu, (F, E), dtype or t, dev)
+    if g is None or u is None:
+        raise ValueError("wg and wu are missing")
+    return _lib.PmhaFfnParams(E, F, _DTYPES[t], act, None if dtype else g, None if dtype else u, wd.data_ptr(),
+                              _like("bg", p.bg, (F,), t, dev), _like("bu", p.bu, (F,), t, dev),
+                              _like("bd", p.bd, (E,), t, dev))
 
 
 @dataclasses.dataclass
@@ -672,7 +703,7 @@ class FfnParams:
     act: str = "silu"
 
     def as_struct(self) -> _lib.PmhaFfnParams:
-        return _ffn_struct(self, _ptr(self.wg), _ptr(self.wu), None)
+        return _ffn_struct(self, None)
 
 
 @dataclasses.dataclass
@@ -690,16 +721,15 @@ class FfnQuantizedParams:
     act: str = "silu"
 
     def as_struct(self) -> _lib.PmhaFfnParams:
-        return _ffn_struct(self, None, None, torch.float8_e4m3fn)
+        return _ffn_struct(self, torch.float8_e4m3fn)
 
     def quantized_struct(self) -> _lib.PmhaFfnQuantized:
-        F, dev = self.wg.shape[0], self.wd.device
-        for n in ("wg_scale", "wu_scale"):
-            if getattr(self, n) is None:
-                raise ValueError(f"{n} is missing")
-        return _lib.PmhaFfnQuantized(_ptr(self.wg), _ptr(self.wu),
-                                     _check_vector("wg_scale", self.wg_scale, F, torch.float32, dev),
-                                     _check_vector("wu_scale", self.wu_scale, F, torch.float32, dev))
+        F, dev = self.wg.shape[0], self.wd.get_device()
+        gs = _like("wg_scale", self.wg_scale, (F,), torch.float32, dev)
+        us = _like("wu_scale", self.wu_scale, (F,), torch.float32, dev)
+        if gs is None or us is None:
+            raise ValueError("wg_scale and wu_scale are missing")
+        return _lib.PmhaFfnQuantized(self.wg.data_ptr(), self.wu.data_ptr(), gs, us)
 
     @staticmethod
     def from_params(params: FfnParams) -> "FfnQuantizedParams":
@@ -722,48 +752,61 @@ _NO_SIZE = ctypes.c_size_t(-1).value
 
 def _ffn_size(fn, p, rows, where) -> int:
     need = fn(ctypes.byref(p), rows)
-    if need == _NO_SIZE:
-        # the checks of the size functions are those of the calls: the message is there, and its kind follows it
-        raise PmhaError(1, where, (_lib.load().pmha_last_error() or b"").decode())
+    if need == _NO_SIZE:  # the size functions make the checks of their calls
+        message = (_lib.load().pmha_last_error() or b"").decode()
+        raise PmhaError(5 if "must be a multiple" in message else 1, where, message)
     return need
 
 
 def pmha_ffn_forward_workspace_size(params: FfnParams, rows: int) -> int:
-    return _ffn_size(_lib.load().pmha_ffn_forward_workspace_size, params.as_struct(), int(rows), "pmha_ffn_forward")
+    return _ffn_size(_library().pmha_ffn_forward_workspace_size, params.as_struct(), int(rows), "pmha_ffn_forward")
 
 
 def pmha_ffn_forward_quantized_workspace_size(params: FfnQuantizedParams, rows: int) -> int:
-    return _ffn_size(_lib.load().pmha_ffn_forward_quantized_workspace_size, params.as_struct(), int(rows),
+    return _ffn_size(_library().pmha_ffn_forward_quantized_workspace_size, params.as_struct(), int(rows),
                      "pmha_ffn_forward_quantized")
 
 
 def pmha_ffn_backward_workspace_size(params: FfnParams, rows: int) -> int:
-    return _ffn_size(_lib.load().pmha_ffn_backward_workspace_size, params.as_struct(), int(rows), "pmha_ffn_backward")
+    return _ffn_size(_library().pmha_ffn_backward_workspace_size, params.as_struct(), int(rows), "pmha_ffn_backward")
 
 
-def _ffn_tokens(name, x, params, dtype):
-    rows, width = _check_rows(name, x, dtype)
-    if width != params.wd.shape[0] or x.device != params.wd.device:
-        raise ValueError(f"{name} must be (..., {params.wd.shape[0]}) on {params.wd.device}")
-    return rows
+def _ffn_tokens(name, x, p, wd, dtype):
+    shape, rows, width, dev = _rows_of(name, x, dtype)
+    if width != p.embed_dim or dev != wd.get_device():
+        raise ValueError(f"{name} must be (..., {p.embed_dim}) on {wd.device}")
+    return shape, rows, dev
+
+
+def _scratch(x, need, workspace):
+    """(pointer, bytes, the tensor to keep) of the workspace, the caller's or a new one."""
+    if workspace is not None:
+        ws = _workspace(need, x.device, workspace)
+        return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+    if not need:
+        return None, 0, None
+    ws = x.new_empty(need, dtype=torch.uint8)
+    return ws.data_ptr(), need, ws
 
 
 def pmha_ffn_forward(params: FfnParams, x: torch.Tensor, residual: torch.Tensor | None = None,
                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """The gated feed-forward block on tokens x (..., E), plus the residual."""
     p = params.as_struct()
-    rows = _ffn_tokens("x", x, params, params.wd.dtype)
-    r = _check_like("residual", residual, x)
-    _check_like("out", out, x)
-    lib = _lib.load()
+    dtype = params.wd.dtype
+    shape, rows, dev = _ffn_tokens("x", x, p, params.wd, dtype)
+    r = _like("residual", residual, shape, dtype, dev)
+    o = _like("out", out, shape, dtype, dev)
+    lib = _library()
     need = _ffn_size(lib.pmha_ffn_forward_workspace_size, p, rows, "pmha_ffn_forward")
-    with _on(x.device, stream):
+    with _on(dev, stream):
         if out is None:
             out = torch.empty_like(x)
-        ws = _workspace(need, x.device, workspace)
-        st = lib.pmha_ffn_forward(ctypes.byref(p), x.data_ptr(), r, rows, out.data_ptr(), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), _stream_ptr(stream))
-    _lib.check(st, "pmha_ffn_forward")
+            o = out.data_ptr()
+        wp, wn, keep = _scratch(x, need, workspace)
+        st = lib.pmha_ffn_forward(ctypes.byref(p), x.data_ptr(), r, rows, o, wp, wn, _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_ffn_forward")
     return out
 
 
@@ -774,24 +817,24 @@ def pmha_ffn_forward_quantized(params: FfnQuantizedParams, x: torch.Tensor, x_sc
     pmha_rms_norm_quantized returns) and a quantized block; residual and result
     are bfloat16."""
     p, q = params.as_struct(), params.quantized_struct()
-    rows = _ffn_tokens("x", x, params, torch.float8_e4m3fn)
-    if not isinstance(x_scale, torch.Tensor) or x_scale.shape != x.shape[:-1] or x_scale.dtype != torch.float32 \
-            or x_scale.device != x.device or not x_scale.is_contiguous():
-        raise ValueError(f"x_scale must be a contiguous {tuple(x.shape[:-1])} float32 tensor on {x.device}")
-    for n, t in (("residual", residual), ("out", out)):
-        if t is not None and (t.shape != x.shape or t.dtype != params.wd.dtype or t.device != x.device
-                              or not t.is_contiguous()):
-            raise ValueError(f"{n} must be a contiguous {tuple(x.shape)} tensor of {params.wd.dtype} on {x.device}")
-    lib = _lib.load()
+    dtype = params.wd.dtype
+    shape, rows, dev = _ffn_tokens("x", x, p, params.wd, torch.float8_e4m3fn)
+    xs = _like("x_scale", x_scale, shape[:-1], torch.float32, dev)
+    if xs is None:
+        raise ValueError("x_scale is missing")
+    r = _like("residual", residual, shape, dtype, dev)
+    o = _like("out", out, shape, dtype, dev)
+    lib = _library()
     need = _ffn_size(lib.pmha_ffn_forward_quantized_workspace_size, p, rows, "pmha_ffn_forward_quantized")
-    with _on(x.device, stream):
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty_like(x, dtype=params.wd.dtype)
-        ws = _workspace(need, x.device, workspace)
-        st = lib.pmha_ffn_forward_quantized(ctypes.byref(p), ctypes.byref(q), x.data_ptr(), x_scale.data_ptr(),
-                                            _ptr(residual), rows, out.data_ptr(), ws.data_ptr(),
-                                            ws.numel() * ws.element_size(), _stream_ptr(stream))
-    _lib.check(st, "pmha_ffn_forward_quantized")
+            out = torch.empty_like(x, dtype=dtype)
+            o = out.data_ptr()
+        wp, wn, keep = _scratch(x, need, workspace)
+        st = lib.pmha_ffn_forward_quantized(ctypes.byref(p), ctypes.byref(q), x.data_ptr(), xs, r, rows, o, wp, wn,
+                                            _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_ffn_forward_quantized")
     return out
 
 
@@ -802,27 +845,30 @@ def pmha_ffn_backward(params: FfnParams, x: torch.Tensor, dout: torch.Tensor, in
     block's type (None for biases it does not have). A residual's gradient is
     dout itself."""
     p = params.as_struct()
-    rows = _ffn_tokens("x", x, params, params.wd.dtype)
+    dtype = params.wd.dtype
+    shape, rows, dev = _ffn_tokens("x", x, p, params.wd, dtype)
+    dy = _like("dout", dout, shape, dtype, dev)
     if dout is None:
         raise ValueError("dout is missing")
-    dy = _check_like("dout", dout, x)
-    lib = _lib.load()
+    lib = _library()
     need = _ffn_size(lib.pmha_ffn_backward_workspace_size, p, rows, "pmha_ffn_backward")
     out = {}
     g = _lib.PmhaFfnGrads()
-    with _on(x.device, stream):
+    with _on(dev, stream):
         dx = None
         if input_grads:
             out["dx"] = dx = torch.empty_like(x)
         if param_grads:
             for n in ("wg", "wu", "wd", "bg", "bu", "bd"):
                 t = getattr(params, n)
-                out["d" + n] = None if t is None else torch.empty_like(t)
-                setattr(g, n, _ptr(out["d" + n]))
-        ws = _workspace(need, x.device, workspace)
-        st = lib.pmha_ffn_backward(ctypes.byref(p), x.data_ptr(), dy, rows, _ptr(dx), ctypes.byref(g), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), _stream_ptr(stream))
-    _lib.check(st, "pmha_ffn_backward")
+                out["d" + n] = d = None if t is None else torch.empty_like(t)
+                if d is not None:
+                    setattr(g, n, d.data_ptr())
+        wp, wn, keep = _scratch(x, need, workspace)
+        st = lib.pmha_ffn_backward(ctypes.byref(p), x.data_ptr(), dy, rows, _ptr(dx), ctypes.byref(g), wp, wn,
+                                   _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_ffn_backward")
     return out
 
 
@@ -843,9 +889,10 @@ class PackedEncoderLayer:
             raise ValueError("an encoder layer needs a graph with query_features == key_features")
         E = attention.embed_dim
         for n, t in (("norm1", norm1), ("norm2", norm2)):
-            _check_vector(n, t, E, attention.dtype, attention.wq.device)
+            _like(n, t, (E,), attention.dtype, attention.wq.get_device())
         if block.wd.dtype != attention.dtype or block.wd.shape[0] != E:
             raise ValueError(f"the block must have width {E} and type {attention.dtype}")
+        block.as_struct()  # checks its tensors
         self.graph, self.attention, self.block = graph, attention, block
         self.norm1, self.norm2, self.eps = norm1, norm2, float(eps)
 

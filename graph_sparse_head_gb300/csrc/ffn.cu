@@ -6,9 +6,11 @@
 //   backward, from dy:  dh = dy Wd,  du = dh act(g),  dg = dh u act'(g),
 //   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h, biases column sums.
 //
-// Rows are taken in blocks whose hidden values fit in L2 (kL2Block), so that
-// what one product writes the next reads without going to memory, and the
-// workspace stops growing with the rows.
+// Rows are taken in blocks of at most kBlock bytes of hidden values, so that
+// the workspace stops growing with the rows. Blocks that stay in L2 were
+// measured slower: a launch costs some 8 us of start and drain, and at embed_dim
+// 128, 512 hidden, 320,000 rows the backward pass took 624 us with blocks of
+// 60 MB, 556 with 120, 521 with 240 and 488 with 480.
 #include <math.h>
 
 #include <algorithm>
@@ -19,8 +21,7 @@
 namespace pmha {
 namespace {
 
-constexpr int64_t kL2Block = 64 << 20;  // bytes of hidden values (h, or h, dg and du) of a block of rows
-constexpr int64_t kMostBlock = 256 << 20;
+constexpr int64_t kBlock = 512 << 20;   // bytes of hidden values (h, or h, dg and du) of a block of rows
 constexpr int64_t kFusedRows = 2048;    // rows from which the forward pass runs as one kernel
 constexpr int kSumParts = 32;           // row ranges of a float32 block's bias sums
 
@@ -373,12 +374,10 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
     l.padded = l.E2 != p->embed_dim || l.F2 != p->hidden_dim;
     l.fused = bf16 && ffn_fused_supported(l.E2, l.F2, backward, q8) && (backward || rows >= kFusedRows);
     const int64_t per_row = l.F2 * (int64_t)es * (backward ? 3 : 1);
-    // a block of rows fills the pairs of SMs a whole number of times where L2 holds that many, else
-    // once where that is not too much memory
+    // a whole number of times 256 rows for each pair of SMs, where there are that many
     const int64_t wave = 256 * (int64_t)(num_sms() / 2);
-    l.R = std::max<int64_t>(256, kL2Block / per_row / 256 * 256);
+    l.R = std::max<int64_t>(256, kBlock / per_row / 256 * 256);
     if (l.R >= wave) l.R = l.R / wave * wave;
-    else if (l.fused && wave * per_row <= kMostBlock) l.R = wave;
     if (l.fused && !backward && !l.padded) l.R = rows;
     l.R = std::min(l.R, ceil_div(std::max<int64_t>(rows, 1), 256) * 256);
     size_t o = 0;
