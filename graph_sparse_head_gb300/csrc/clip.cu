@@ -77,27 +77,34 @@ template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+constexpr int kInFlight = 4;  // 16-byte loads of a thread before their values are used
+
 template <typename T>
 __device__ __forceinline__ void sum_chunk(const T *g, int n, Sums &s)
 {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), kStep = kThreads * V;
     int i0 = 0;
     if (((uintptr_t)g & 15) == 0) {
         i0 = n / V * V;
-#pragma unroll 4
-        for (int i = threadIdx.x * V; i < i0; i += kThreads * V) {
-            const uint4 raw = *reinterpret_cast<const uint4 *>(g + i);
-            T v[V];
-            *reinterpret_cast<uint4 *>(v) = raw;
-            bool mid = true;
+        for (int i = threadIdx.x * V; i < i0; i += kInFlight * kStep) {
+            uint4 raw[kInFlight];
 #pragma unroll
-            for (int k = 0; k < V; ++k) mid &= is_mid(to_f<T>(v[k]));
-            if (mid) {  // the usual case, without a branch a value
+            for (int u = 0; u < kInFlight; ++u)
+                raw[u] = i + u * kStep < i0 ? *reinterpret_cast<const uint4 *>(g + i + u * kStep) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int k = 0; k < V; ++k) s.mid = fmaf(to_f<T>(v[k]), to_f<T>(v[k]), s.mid);
-            } else {
+            for (int u = 0; u < kInFlight; ++u) {
+                T v[V];
+                *reinterpret_cast<uint4 *>(v) = raw[u];
+                bool mid = true;
 #pragma unroll
-                for (int k = 0; k < V; ++k) add_square(s, to_f<T>(v[k]));
+                for (int k = 0; k < V; ++k) mid &= is_mid(to_f<T>(v[k]));
+                if (mid) {  // the usual case, without a branch a value
+#pragma unroll
+                    for (int k = 0; k < V; ++k) s.mid = fmaf(to_f<T>(v[k]), to_f<T>(v[k]), s.mid);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) add_square(s, to_f<T>(v[k]));
+                }
             }
         }
     }
@@ -107,18 +114,24 @@ __device__ __forceinline__ void sum_chunk(const T *g, int n, Sums &s)
 template <typename T>
 __device__ __forceinline__ void scale_chunk(const T *g, T *out, int n, float c)
 {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), kStep = kThreads * V;
     int i0 = 0;
     if ((((uintptr_t)g | (uintptr_t)out) & 15) == 0) {
         i0 = n / V * V;
-#pragma unroll 4
-        for (int i = threadIdx.x * V; i < i0; i += kThreads * V) {
-            uint4 raw = *reinterpret_cast<const uint4 *>(g + i);
-            T v[V];
-            *reinterpret_cast<uint4 *>(v) = raw;
+        for (int i = threadIdx.x * V; i < i0; i += kInFlight * kStep) {
+            uint4 raw[kInFlight];
 #pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = from_f<T>(to_f<T>(v[k]) * c);
-            *reinterpret_cast<uint4 *>(out + i) = *reinterpret_cast<uint4 *>(v);
+            for (int u = 0; u < kInFlight; ++u)
+                if (i + u * kStep < i0) raw[u] = *reinterpret_cast<const uint4 *>(g + i + u * kStep);
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u) {
+                if (i + u * kStep >= i0) break;
+                T v[V];
+                *reinterpret_cast<uint4 *>(v) = raw[u];
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[k] = from_f<T>(to_f<T>(v[k]) * c);
+                *reinterpret_cast<uint4 *>(out + i + u * kStep) = *reinterpret_cast<uint4 *>(v);
+            }
         }
     }
     for (int i = i0 + threadIdx.x; i < n; i += kThreads) out[i] = from_f<T>(to_f<T>(g[i]) * c);
@@ -189,7 +202,6 @@ size_t part_bytes(int64_t n_tensors)
 struct Range {
     uintptr_t at;
     size_t n;
-    bool out;
 };
 
 }  // namespace
@@ -230,8 +242,10 @@ pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, voi
     cudaStream_t cs = (cudaStream_t)stream;
     try {
         std::vector<Range> ranges;
+        std::vector<Range> outs;
         ranges.reserve((size_t)n_tensors * 2 + 1);
-        ranges.push_back({(uintptr_t)norm, 4, true});
+        if (out) outs.reserve((size_t)n_tensors + 1);
+        outs.push_back({(uintptr_t)norm, 4});
         int64_t total = 0;
         for (int64_t i = 0; i < n_tensors; ++i) {
             if (dtype[i] != PMHA_F32 && dtype[i] != PMHA_BF16) {
@@ -250,11 +264,15 @@ pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, voi
                 set_error("pmha_clip_grad_norm: tensor %lld is NULL or not aligned to its values", (long long)i);
                 return PMHA_ERR_INVALID_ARG;
             }
-            ranges.push_back({(uintptr_t)grads[i], (size_t)numel[i] * es, o == grads[i]});
-            if (o != grads[i]) ranges.push_back({(uintptr_t)o, (size_t)numel[i] * es, true});
+            ranges.push_back({(uintptr_t)grads[i], (size_t)numel[i] * es});
+            if (o != grads[i]) outs.push_back({(uintptr_t)o, (size_t)numel[i] * es});
         }
         // gradients counted twice are refused like outputs that touch anything
-        std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.at < b.at; });
+        const auto before = [](const Range &a, const Range &b) { return a.at < b.at; };
+        for (std::vector<Range> *v : {&ranges, &outs})  // usually in order already: each laid out in one buffer
+            if (!std::is_sorted(v->begin(), v->end(), before)) std::sort(v->begin(), v->end(), before);
+        const auto middle = ranges.insert(ranges.end(), outs.begin(), outs.end());
+        std::inplace_merge(ranges.begin(), middle, ranges.end(), before);
         uintptr_t end = 0;
         for (const Range &r : ranges) {
             if (r.at < end) {

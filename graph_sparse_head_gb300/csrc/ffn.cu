@@ -1,6 +1,6 @@
 // Gated feed-forward block: argument checks, workspace, the order of launches,
-// the float32 products on the CUDA cores, and the small kernels around the
-// tensor-core products (copies to padded widths, transposes, sums).
+// and the small kernels around the products (copies to padded widths,
+// transposes, sums).
 //
 //   h = act(x Wg^T + bg) * (x Wu^T + bu),    y = h Wd^T + bd (+ residual)
 //   backward, from dy:  dh = dy Wd,  du = dh act(g),  dg = dh u act'(g),
@@ -31,134 +31,6 @@ template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v
 template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-// ---------------------------------------------------------------- float32 products
-// 64 x 64 outputs a block, 4 x 4 a thread, 16 values of K at a time from
-// shared memory; sums in ascending K with fused multiply-adds.
-constexpr int kT = 64, kK = 16;
-
-// acc[i][j] += sum_k A[m0 + 4 ty + i, k] B[n0 + 4 tx + j, k]. An operand's
-// element (row, k) lies at row * ld + k (K contiguous) or k * ld + row.
-template <bool AK, bool BK>
-__device__ void tile_product(const float *A, int64_t lda, int64_t M, const float *B, int64_t ldb, int64_t N, int64_t k0,
-                             int64_t k1, int64_t m0, int64_t n0, float (&acc)[4][4], float (*as)[kT + 4],
-                             float (*bs)[kT + 4])
-{
-    const int t = threadIdx.x, tx = t % 16, ty = t / 16;
-    for (int64_t k = k0; k < k1; k += kK) {
-#pragma unroll
-        for (int q = 0; q < kT * kK / 256; ++q) {
-            const int idx = t + q * 256;
-            const int ra = AK ? idx / kK : idx % kT, ka = AK ? idx % kK : idx / kT;
-            const int rb = BK ? idx / kK : idx % kT, kb = BK ? idx % kK : idx / kT;
-            as[ka][ra] = m0 + ra < M && k + ka < k1 ? A[AK ? (m0 + ra) * lda + k + ka : (k + ka) * lda + m0 + ra] : 0.f;
-            bs[kb][rb] = n0 + rb < N && k + kb < k1 ? B[BK ? (n0 + rb) * ldb + k + kb : (k + kb) * ldb + n0 + rb] : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kK; ++kk) {
-            const float4 a = *reinterpret_cast<const float4 *>(&as[kk][ty * 4]);
-            const float4 b = *reinterpret_cast<const float4 *>(&bs[kk][tx * 4]);
-            const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(av[i], bv[j], acc[i][j]);
-        }
-        __syncthreads();
-    }
-}
-
-struct F32Args {
-    const float *x, *dy, *wg, *wu, *wd, *bg, *bu, *bd, *res;
-    float *h, *dg, *du, *out;
-    int64_t M, E, F;
-};
-
-#define PMHA_F32_TILE                                                 \
-    __shared__ __align__(16) float as[kK][kT + 4], bs[kK][kT + 4];    \
-    const int64_t m0 = (int64_t)blockIdx.x * kT, n0 = (int64_t)blockIdx.y * kT; \
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16
-
-template <int ACT, bool BWD>
-__global__ void __launch_bounds__(256) k_f32_hidden(F32Args a)
-{
-    PMHA_F32_TILE;
-    float g[4][4] = {}, u[4][4] = {}, d[4][4] = {};
-    tile_product<true, true>(a.x, a.E, a.M, a.wg, a.E, a.F, 0, a.E, m0, n0, g, as, bs);
-    tile_product<true, true>(a.x, a.E, a.M, a.wu, a.E, a.F, 0, a.E, m0, n0, u, as, bs);
-    if constexpr (BWD) tile_product<true, false>(a.dy, a.E, a.M, a.wd, a.F, a.F, 0, a.E, m0, n0, d, as, bs);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= a.M || n >= a.F) continue;
-            const float gv = g[i][j] + (a.bg ? a.bg[n] : 0.f), uv = u[i][j] + (a.bu ? a.bu[n] : 0.f);
-            if constexpr (BWD) {
-                float slope;
-                const float act = Act<ACT>::exact(gv, &slope);
-                a.h[m * a.F + n] = act * uv;
-                a.du[m * a.F + n] = d[i][j] * act;
-                a.dg[m * a.F + n] = d[i][j] * uv * slope;
-            } else {
-                a.h[m * a.F + n] = Act<ACT>::exact(gv) * uv;
-            }
-        }
-}
-
-// out = h Wd^T + bd + residual
-__global__ void __launch_bounds__(256) k_f32_down(F32Args a)
-{
-    PMHA_F32_TILE;
-    float c[4][4] = {};
-    tile_product<true, true>(a.h, a.F, a.M, a.wd, a.F, a.E, 0, a.F, m0, n0, c, as, bs);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= a.M || n >= a.E) continue;
-            float v = c[i][j] + (a.bd ? a.bd[n] : 0.f);
-            if (a.res) v += a.res[m * a.E + n];
-            a.out[m * a.E + n] = v;
-        }
-}
-
-// dx = dg Wg + du Wu
-__global__ void __launch_bounds__(256) k_f32_dx(F32Args a)
-{
-    PMHA_F32_TILE;
-    float c[4][4] = {};
-    tile_product<true, false>(a.dg, a.F, a.M, a.wg, a.E, a.E, 0, a.F, m0, n0, c, as, bs);
-    tile_product<true, false>(a.du, a.F, a.M, a.wu, a.E, a.E, 0, a.F, m0, n0, c, as, bs);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m < a.M && n < a.E) a.out[m * a.E + n] = c[i][j];
-        }
-}
-
-// part[split][what] (+)= {dg, du, h}^T {x, x, dy} over the split's rows; blockIdx.z = split * 3 + what
-__global__ void __launch_bounds__(256) k_f32_dw(F32Args a, float *part, int splits, bool accumulate)
-{
-    PMHA_F32_TILE;
-    const int what = blockIdx.z % 3, split = blockIdx.z / 3;
-    const int64_t per = (a.M + splits - 1) / splits, k0 = split * per, k1 = min(a.M, k0 + per);
-    const float *A = what == 0 ? a.dg : what == 1 ? a.du : a.h, *B = what == 2 ? a.dy : a.x;
-    float c[4][4] = {};
-    tile_product<false, false>(A, a.F, a.F, B, a.E, a.E, k0, k1, m0, n0, c, as, bs);
-    float *dst = part + (int64_t)blockIdx.z * a.F * a.E;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m < a.F && n < a.E) dst[m * a.E + n] = accumulate ? dst[m * a.E + n] + c[i][j] : c[i][j];
-        }
-}
 
 // ---------------------------------------------------------------- small kernels
 
@@ -349,7 +221,7 @@ pmha_status check_workspace(const char *who, const void *ws, size_t got, size_t 
 // products (multiples of 8 for bf16; copies are made where that differs).
 struct Plan {
     int64_t E2, F2, R;
-    bool padded, fused;
+    bool padded, fused, small;
     size_t wg, wu, wd, bg, bu, bd;  // padded copies
     size_t x, dy, out;              // padded rows of a block (dy: dy or the residual)
     size_t wgt, wut, wdt;           // transposed weights (backward)
@@ -358,12 +230,6 @@ struct Plan {
     size_t total;
 };
 
-int f32_splits(int64_t E, int64_t F, int64_t rows)
-{
-    const int64_t tiles = 3 * ceil_div(F, kT) * ceil_div(E, kT);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)num_sms() * 4 / tiles, ceil_div(rows, 128), 64}));
-}
-
 Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
 {
     Plan l = {};
@@ -371,6 +237,8 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
     const size_t es = bf16 ? 2 : 4;
     l.E2 = bf16 ? round8(p->embed_dim) : p->embed_dim;
     l.F2 = bf16 ? round8(p->hidden_dim) : p->hidden_dim;
+    l.small = bf16 && !backward && ffn_small_supported(p->embed_dim, rows, q8);
+    if (l.small) l.E2 = p->embed_dim, l.F2 = p->hidden_dim;
     l.padded = l.E2 != p->embed_dim || l.F2 != p->hidden_dim;
     l.fused = bf16 && ffn_fused_supported(l.E2, l.F2, backward, q8) && (backward || rows >= kFusedRows);
     const int64_t per_row = l.F2 * (int64_t)es * (backward ? 3 : 1);
@@ -396,7 +264,7 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
         l.dg = take(l.R * l.F2), l.du = take(l.R * l.F2);
         if (bf16) l.wgt = take(l.E2 * l.F2), l.wut = take(l.E2 * l.F2), l.wdt = take(l.E2 * l.F2);
         const int64_t block = std::min(l.R, std::max<int64_t>(rows, 1));
-        l.splits = bf16 ? ffn_dw_splits(l.E2, l.F2, block) : f32_splits(l.E2, l.F2, block);
+        l.splits = bf16 ? ffn_dw_splits(l.E2, l.F2, block) : ffn_f32_splits(l.E2, l.F2, block);
         l.part = o;
         o += align256((size_t)l.splits * 3 * (size_t)(l.E2 * l.F2) * 4);
         l.sums = o;
@@ -452,26 +320,11 @@ pmha_status pad_params(const pmha_ffn_params *p, const Plan &l, char *ws, pmha_f
     return PMHA_OK;
 }
 
-dim3 f32_grid(int64_t M, int64_t N, int64_t z = 1) { return dim3((unsigned)ceil_div(M, kT), (unsigned)ceil_div(N, kT), (unsigned)z); }
-
 pmha_status launched()
 {
     count_launch();
     PMHA_CUDA_TRY(cudaGetLastError());
     return PMHA_OK;
-}
-
-pmha_status forward_f32(const pmha_ffn_params *p, const F32Args &a, cudaStream_t s)
-{
-    {
-        StageTimer timer("ffn_up", s);
-        if (p->act == PMHA_ACT_SILU) k_f32_hidden<PMHA_ACT_SILU, false><<<f32_grid(a.M, a.F), 256, 0, s>>>(a);
-        else k_f32_hidden<PMHA_ACT_GELU, false><<<f32_grid(a.M, a.F), 256, 0, s>>>(a);
-        PMHA_TRY(launched());
-    }
-    StageTimer timer("ffn_down", s);
-    k_f32_down<<<f32_grid(a.M, a.E), 256, 0, s>>>(a);
-    return launched();
 }
 
 // The forward pass, for tokens in the layer type or (q8) in E4M3.
@@ -512,12 +365,13 @@ pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_qu
         const char *rr = residual ? (const char *)residual + (size_t)(r * E) * es : nullptr;
         char *yr = (char *)out + (size_t)(r * E) * es;
         if (p->dtype == PMHA_F32) {
-            F32Args a = {};
+            FfnF32Args a = {};
             a.x = (const float *)xr, a.wg = (const float *)p->wg, a.wu = (const float *)p->wu;
             a.wd = (const float *)p->wd, a.bg = (const float *)p->bg, a.bu = (const float *)p->bu;
             a.bd = (const float *)p->bd, a.res = (const float *)rr, a.h = (float *)(ws + l.h), a.out = (float *)yr;
             a.M = M, a.E = E, a.F = F;
-            PMHA_TRY(forward_f32(p, a, s));
+            PMHA_TRY(ffn_f32_hidden(p->act, a, false, s));
+            PMHA_TRY(ffn_f32_down(a, s));
             continue;
         }
         const void *xp = xr, *rp = rr;
@@ -536,7 +390,9 @@ pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_qu
         if (q8) up.x_scale = x_scale + r, up.wg_scale = q8->wg_scale, up.wu_scale = q8->wu_scale;
         up.M = M;
         up.h = ws + l.h;
-        if (l.fused) {
+        if (l.small) {
+            PMHA_TRY(ffn_small_forward(tc, up, q.wd, rp, yp, s));
+        } else if (l.fused) {
             PMHA_TRY(ffn_fused_forward(tc, up, q.wd, rp, yp, s));
         } else {
             PMHA_TRY(ffn_tc_up(tc, up, s));
@@ -697,27 +553,14 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 PMHA_TRY(ffn_tc_dw(tc, d, s));
             }
         } else {
-            F32Args a = {};
+            FfnF32Args a = {};
             a.x = (const float *)xr, a.dy = (const float *)dyr, a.wg = (const float *)p->wg;
             a.wu = (const float *)p->wu, a.wd = (const float *)p->wd, a.bg = (const float *)p->bg;
             a.bu = (const float *)p->bu, a.h = (float *)(ws + l.h), a.dg = (float *)(ws + l.dg);
             a.du = (float *)(ws + l.du), a.out = (float *)dxr, a.M = M, a.E = E, a.F = F;
-            {
-                StageTimer timer("ffn_hidden", s);
-                if (p->act == PMHA_ACT_SILU) k_f32_hidden<PMHA_ACT_SILU, true><<<f32_grid(M, F), 256, 0, s>>>(a);
-                else k_f32_hidden<PMHA_ACT_GELU, true><<<f32_grid(M, F), 256, 0, s>>>(a);
-                PMHA_TRY(launched());
-            }
-            if (dx) {
-                StageTimer timer("ffn_dx", s);
-                k_f32_dx<<<f32_grid(M, E), 256, 0, s>>>(a);
-                PMHA_TRY(launched());
-            }
-            if (any_w) {
-                StageTimer timer("ffn_dw", s);
-                k_f32_dw<<<f32_grid(F, E, 3 * l.splits), 256, 0, s>>>(a, part, l.splits, !first);
-                PMHA_TRY(launched());
-            }
+            PMHA_TRY(ffn_f32_hidden(p->act, a, true, s));
+            if (dx) PMHA_TRY(ffn_f32_dx(a, s));
+            if (any_w) PMHA_TRY(ffn_f32_dw(a, part, l.splits, !first, s));
             if (any_b) {
                 Sums c = {};
                 c.in[0] = a.dg, c.in[1] = a.du, c.in[2] = a.dy;

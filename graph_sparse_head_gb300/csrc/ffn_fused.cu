@@ -709,7 +709,7 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     p.parts = (p.chunks + p.per_part - 1) / p.per_part;
     p.items *= p.parts;
     StageTimer timer(stage, s);
-    return launch_pairs(kern, 2 * std::min(pairs, p.items), kThreads, C::kSmem, s, p);
+    return launch_overlapping(kern, 2 * std::min(pairs, p.items), kThreads, C::kSmem, s, p);
 }
 
 template <int EB, bool BWD, bool Q8>

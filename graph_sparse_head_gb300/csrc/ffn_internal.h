@@ -1,6 +1,8 @@
 // Declarations shared by the feed-forward block's translation units.
 #pragma once
 
+#include <algorithm>
+
 #include "pmha_internal.h"
 
 namespace pmha {
@@ -27,6 +29,10 @@ pmha_status ffn_tc_down(const FfnTc &f, const void *h, const void *wd, const voi
 // The whole forward in one kernel, the hidden rows on the chip (ffn_fused.cu).
 bool ffn_fused_supported(int64_t E, int64_t F, bool backward, bool q8);
 pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
+                              cudaStream_t s);
+// The same for a few tokens, on the CUDA cores (ffn_small.cu); any widths.
+bool ffn_small_supported(int64_t E, int64_t M, bool q8);
+pmha_status ffn_small_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
                               cudaStream_t s);
 // h, dg, du (M, F): the hidden row and the gradients of gate and up, from x,
 // dout and wd_t (F, E) = Wd transposed
@@ -58,5 +64,17 @@ struct FfnDwArgs {
 };
 int ffn_dw_splits(int64_t E, int64_t F, int64_t rows_per_block);
 pmha_status ffn_tc_dw(const FfnTc &f, const FfnDwArgs &a, cudaStream_t s);
+
+// Products of a float32 block (ffn_f32.cu), over M rows.
+struct FfnF32Args {
+    const float *x, *dy, *wg, *wu, *wd, *bg, *bu, *bd, *res;
+    float *h, *dg, *du, *out;
+    int64_t M, E, F;
+};
+pmha_status ffn_f32_hidden(pmha_act act, const FfnF32Args &a, bool backward, cudaStream_t s);
+pmha_status ffn_f32_down(const FfnF32Args &a, cudaStream_t s);
+pmha_status ffn_f32_dx(const FfnF32Args &a, cudaStream_t s);
+int ffn_f32_splits(int64_t E, int64_t F, int64_t rows);
+pmha_status ffn_f32_dw(const FfnF32Args &a, float *part, int splits, bool accumulate, cudaStream_t s);
 
 }  // namespace pmha

@@ -578,7 +578,7 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     const pmha_status st = configure(kern, C::kSmem, &pairs);
     if (st != PMHA_OK) return st;
     StageTimer timer(stage, s);
-    return launch_pairs(kern, 2 * std::min(pairs, p.n_tiles), kThreads, C::kSmem, s, p);
+    return launch_overlapping(kern, 2 * std::min(pairs, p.n_tiles), kThreads, C::kSmem, s, p);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

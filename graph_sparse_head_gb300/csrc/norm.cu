@@ -141,28 +141,45 @@ __device__ __forceinline__ Quant quant(Two ss, Two amax, int width, float eps)
     z.c = div(r, z.scale);
     return z;
 }
+// The product of two bf16 values, and a bf16 value's square, have at most 16
+// significant bits: one float holds them (EXACT), which leaves some 30
+// instructions a value instead of 120.
+template <bool EXACT>
+__device__ __forceinline__ Two product(float a, float b)
+{
+    if constexpr (EXACT) return {__fmul_rn(a, b), 0.f};
+    else return two_mul(a, b);
+}
+template <bool EXACT>
 __device__ __forceinline__ float quant_value(float f, float w, Two c)
 {
-    const Two p = two_mul(f, w);  // exact in one float for bf16 operands
+    const Two p = product<EXACT>(f, w);
     Two v = two_mul(p.hi, c.hi);
-    v.lo = __fadd_rn(v.lo, __fmaf_rn(p.hi, c.lo, __fmul_rn(p.lo, c.hi)));
+    if constexpr (EXACT) v.lo = __fmaf_rn(p.hi, c.lo, v.lo);
+    else v.lo = __fadd_rn(v.lo, __fmaf_rn(p.hi, c.lo, __fmul_rn(p.lo, c.hi)));
     return to_odd(v);
 }
+template <bool EXACT>
 __device__ __forceinline__ void take_max(Two &m, Two o)
 {
-    if (o.hi > m.hi || (o.hi == m.hi && o.lo > m.lo)) m = o;
+    if constexpr (EXACT) m.hi = fmaxf(m.hi, o.hi);
+    else if (o.hi > m.hi || (o.hi == m.hi && o.lo > m.lo)) m = o;
 }
+template <bool EXACT>
 __device__ __forceinline__ Two abs_mul(float f, float w)
 {
-    Two p = two_mul(f, w);
-    if (p.hi < 0.f) p = {-p.hi, -p.lo};
+    Two p = product<EXACT>(f, w);
+    if constexpr (EXACT) p.hi = fabsf(p.hi);
+    else if (p.hi < 0.f) p = {-p.hi, -p.lo};
     return p;
 }
+template <bool EXACT>
 __device__ __forceinline__ void square_into(Two &ss, float f)
 {
-    const Two p = two_mul(f, f);
+    const Two p = product<EXACT>(f, f);
     const Two t = two_sum(ss.hi, p.hi);
-    ss = {t.hi, __fadd_rn(ss.lo, __fadd_rn(t.lo, p.lo))};
+    if constexpr (EXACT) ss = {t.hi, __fadd_rn(ss.lo, t.lo)};
+    else ss = {t.hi, __fadd_rn(ss.lo, __fadd_rn(t.lo, p.lo))};
 }
 __device__ __forceinline__ uint8_t to_e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
 
@@ -172,6 +189,7 @@ template <typename T, int VEC, int NV, int LPR, bool Q8>
 __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
 {
     constexpr int kRows = 32 / LPR;  // rows of a warp
+    constexpr bool kExact = sizeof(T) == 2;
     const int lane = threadIdx.x & 31, l = lane % LPR;
     const long long row = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kRows + lane / LPR;
     const bool live = row < a.rows;
@@ -252,13 +270,13 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const float f = to_f<T>(v[j].v[i]) * sc;
-                    square_into(ss, f);
-                    take_max(am, abs_mul(f, to_f<T>(wv[j].v[i])));
+                    square_into<kExact>(ss, f);
+                    take_max<kExact>(am, abs_mul<kExact>(f, to_f<T>(wv[j].v[i])));
                 }
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) {
                 ss = add(ss, Two{__shfl_xor_sync(kFull, ss.hi, o), __shfl_xor_sync(kFull, ss.lo, o)});
-                take_max(am, Two{__shfl_xor_sync(kFull, am.hi, o), __shfl_xor_sync(kFull, am.lo, o)});
+                take_max<kExact>(am, Two{__shfl_xor_sync(kFull, am.hi, o), __shfl_xor_sync(kFull, am.lo, o)});
             }
         };
         stats();
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
             alignas(8) uint8_t b[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                b[i] = to_e4m3(quant_value(to_f<T>(v[j].v[i]) * sc, to_f<T>(wv[j].v[i]), z.c));
+                b[i] = to_e4m3(quant_value<kExact>(to_f<T>(v[j].v[i]) * sc, to_f<T>(wv[j].v[i]), z.c));
             *reinterpret_cast<typename Bytes<VEC>::type *>(a.q + base + c) =
                 *reinterpret_cast<typename Bytes<VEC>::type *>(b);
         }
@@ -301,6 +319,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
 {
     __shared__ float sh[kThreads / 32];
     __shared__ Two sh2[kThreads / 32], shm[kThreads / 32];
+    constexpr bool kExact = sizeof(T) == 2;
     const long long row = blockIdx.x, base = row * a.width;
     const T *x = (const T *)a.x, *res = (const T *)a.res, *w = (const T *)a.w;
     auto kept = [&](int c, Vals<T, VEC> &v) {
@@ -334,8 +353,8 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
                 const float f = to_f<T>(v.v[i]) * sc;
                 ss = fmaf(f, f, ss);
                 if constexpr (Q8) {
-                    square_into(s2, f);
-                    take_max(am, abs_mul(f, to_f<T>(wv.v[i])));
+                    square_into<kExact>(s2, f);
+                    take_max<kExact>(am, abs_mul<kExact>(f, to_f<T>(wv.v[i])));
                 }
             }
         }
@@ -351,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             s2 = add(s2, Two{__shfl_xor_sync(kFull, s2.hi, o), __shfl_xor_sync(kFull, s2.lo, o)});
-            take_max(am, Two{__shfl_xor_sync(kFull, am.hi, o), __shfl_xor_sync(kFull, am.lo, o)});
+            take_max<kExact>(am, Two{__shfl_xor_sync(kFull, am.hi, o), __shfl_xor_sync(kFull, am.lo, o)});
         }
         if ((threadIdx.x & 31) == 0) {
             sh2[threadIdx.x >> 5] = s2;
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
         s2 = am = Two{0.f, 0.f};
         for (int i = 0; i < kThreads / 32; ++i) {
             s2 = add(s2, sh2[i]);
-            take_max(am, shm[i]);
+            take_max<kExact>(am, shm[i]);
         }
         z = quant(s2, am, a.width, a.eps * sc * sc);
         if (threadIdx.x == 0) a.scale[row] = z.scale;
@@ -379,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
         if constexpr (Q8) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                a.q[base + c + i] = to_e4m3(quant_value(to_f<T>(v.v[i]) * sc, to_f<T>(wv.v[i]), z.c));
+                a.q[base + c + i] = to_e4m3(quant_value<kExact>(to_f<T>(v.v[i]) * sc, to_f<T>(wv.v[i]), z.c));
         }
     }
 }
@@ -418,22 +437,34 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
     }
     const long long step = (long long)gridDim.x * (kThreads / 32) * kRows;
     const float inv_width = 1.f / (float)a.width;
-    for (long long row0 = ((long long)blockIdx.x * (kThreads / 32) + warp) * kRows; row0 < a.rows; row0 += step) {
+    // up to 16 values a lane the next rows' loads are under way while these are
+    // worked on (more would not fit in the registers)
+    constexpr bool kAhead = NV * VEC <= 16;
+    Vals<T, VEC> v[NV], g[NV], s[NV], vn[NV], gn[NV], sn[NV];
+    auto fetch = [&](long long row0) {
         const long long row = row0 + lane / LPR, base = row * a.width;
-        const bool live = row < a.rows;
-        Vals<T, VEC> v[NV], g[NV], s[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + l) * VEC;
-            if (live && c < a.width) {
-                load<T, VEC>(x + base + c, v[j].v);
-                load<T, VEC>(dy + base + c, g[j].v);
-                if (ds) load<T, VEC>(ds + base + c, s[j].v);
+            if (row < a.rows && c < a.width) {
+                load<T, VEC>(x + base + c, vn[j].v);
+                load<T, VEC>(dy + base + c, gn[j].v);
+                if (ds) load<T, VEC>(ds + base + c, sn[j].v);
             } else {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[j].v[i] = g[j].v[i] = s[j].v[i] = from_f<T>(0.f);
+                for (int i = 0; i < VEC; ++i) vn[j].v[i] = gn[j].v[i] = sn[j].v[i] = from_f<T>(0.f);
             }
         }
+    };
+    const long long row_first = ((long long)blockIdx.x * (kThreads / 32) + warp) * kRows;
+    if constexpr (kAhead) fetch(row_first);
+    for (long long row0 = row_first; row0 < a.rows; row0 += step) {
+        const long long row = row0 + lane / LPR, base = row * a.width;
+        const bool live = row < a.rows;
+        if constexpr (!kAhead) fetch(row0);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = vn[j], g[j] = gn[j], s[j] = sn[j];
+        if constexpr (kAhead) fetch(row0 + step);
         float ss, as, sc = 1.f;
         auto stats = [&]() {
             ss = as = 0.f;

@@ -46,10 +46,12 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 // Waits for the launches this one was allowed to start before the end of; lets
 // the next one start likewise (its blocks come up as this one's leave, which
 // hides the launch). Everything that touches global memory comes after.
+__device__ __forceinline__ void grid_dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait()
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_dependents_may_start();
+    grid_wait();
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
@@ -160,10 +162,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 // 16-byte unit u (0..7) of row r of a 128-byte-wide tile with 128-byte swizzle
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4)); }
 
-// A launch of `grid` CTAs in pairs that may come up before the launch before it
-// has ended (the kernel calls grid_dependency_wait).
+// A launch of `grid` CTAs that may come up before the launch before it has
+// ended (the kernel calls grid_wait before it reads what that one writes).
 template <typename P>
-pmha_status launch_pairs(void (*kern)(P), int grid, int threads, int smem, cudaStream_t s, const P &p)
+pmha_status launch_overlapping(void (*kern)(P), int grid, int threads, int smem, cudaStream_t s, const P &p)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);

@@ -52,16 +52,22 @@ SHAPES = [(256, 128, 128), (1, 64, 64), (128, 64, 128), (129, 64, 64), (255, 8, 
 # rows enough for the kernel that keeps the hidden rows on the chip, every width it has, ragged ends
 LONG = [(2048, 64, 64), (2300, 8, 72), (2500, 128, 512), (3001, 192, 264), (2049, 256, 1024), (40000, 128, 136),
         (2200, 72, 4096), (2600, 248, 8)]
+# a few tokens: the kernels that read each weight once on the CUDA cores
+FEW = [(1, 8, 8), (1, 128, 512), (3, 256, 1000), (4, 100, 171), (5, 64, 72), (16, 512, 2048), (16, 33, 65), (2, 4096, 264),
+       (7, 1024, 4097)]
 ODD = [(5, 1, 1), (3, 7, 9), (130, 33, 65), (257, 100, 171), (64, 130, 514)]
 
 
-@pytest.mark.parametrize("rows,E,F", SHAPES + LONG + ODD + [(2055, 100, 171)])
+@pytest.mark.parametrize("rows,E,F", SHAPES + LONG + FEW + ODD + [(2055, 100, 171)])
 def test_forward_bf16(rows, E, F):
     check_forward(rows, E, F, BF16, bias=(rows + E) % 2 == 0, residual=F % 16 != 0 or rows % 2 == 1)
     check_forward(rows, E, F, BF16, bias=True, act="gelu", residual=True)
 
 
-@pytest.mark.parametrize("rows,E,F", SHAPES[:9] + ODD)
+F32_LONG = [(5000, 130, 260), (20000, 33, 65)]
+
+
+@pytest.mark.parametrize("rows,E,F", SHAPES[:9] + ODD + F32_LONG)
 def test_forward_f32(rows, E, F):
     check_forward(rows, E, F, F32, bias=(rows + E) % 2 == 0, residual=rows % 2 == 1)
     check_forward(rows, E, F, F32, act="gelu")
@@ -73,7 +79,7 @@ def test_backward_bf16(rows, E, F):
     check_backward(rows, E, F, BF16, bias=False, act="gelu")
 
 
-@pytest.mark.parametrize("rows,E,F", SHAPES[:9] + ODD)
+@pytest.mark.parametrize("rows,E,F", SHAPES[:9] + ODD + F32_LONG)
 def test_backward_f32(rows, E, F):
     check_backward(rows, E, F, F32)
     check_backward(rows, E, F, F32, bias=False, act="gelu")
@@ -87,7 +93,7 @@ def test_more_rows_than_a_block(dtype):
 
 
 @pytest.mark.parametrize("rows,E,F", [(256, 128, 128), (1, 16, 8), (100, 48, 72), (300, 256, 264), (1000, 512, 1024),
-                                      (2048, 128, 512), (2111, 48, 72), (2300, 192, 200), (2500, 256, 4096)])
+                                      (4, 128, 512), (16, 80, 136), (2048, 128, 512), (2111, 48, 72), (2300, 192, 200), (2500, 256, 4096)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_forward_quantized(rows, E, F, act):
     p, x, r = make(rows, E, F, BF16, act=act)
