@@ -1,11 +1,11 @@
 // Clipping of many gradient tensors by their global norm:
 //   norm = sqrt(sum of g^2 over all tensors),  out = g * min(1, max_norm / (norm + 1e-6)).
 //
-// Two passes, bound by memory: a persistent grid sums squares over chunks of
-// kChunk values and leaves one partial sum a block; the scaling pass has every
-// block add the partial sums (a few KB from L2) in the same order, so all
-// blocks hold the same norm without a launch in between, and walks the chunks
-// backwards, because the last ones read are the ones still in L2. The table of
+// Two passes, bound by memory: each block sums the squares of its run of chunks
+// (64 KB each) and leaves one partial sum; the scaling pass has every block add
+// the partial sums (a few KB from L2) in the same order, so all blocks hold the
+// same norm without a launch in between, and walks its run backwards, because
+// the last chunks read are the ones still in L2. The table of
 // tensors travels in the kernel's parameters, so that nothing is copied, no
 // host array has to outlive the call, and a captured graph holds its own.
 #include <math.h>
@@ -21,8 +21,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kBatch = 512;       // tensors of one launch: a table of 12 KB of parameters
-constexpr int kChunk = 16384;     // values a block takes at a time
-constexpr int kBlocksPerSm = 4;
+constexpr int kChunkBytes = 65536;  // what a block takes at a time
+constexpr int kBlocksPerSm = 3;   // all resident at 42 registers a thread
 constexpr int kMaxBlocks = 1024;  // partial sums of one launch
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -37,7 +37,7 @@ struct Table {
     const void *g[kBatch];
     void *out[kBatch];
     uint32_t first[kBatch + 1];  // first chunk of each tensor
-    uint32_t last_n[kBatch];     // values of its last chunk, 1 .. kChunk; top bit: bf16
+    uint32_t last_n[kBatch];     // values of its last chunk; top bit: bf16
     int n;
 };
 
@@ -80,13 +80,13 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 constexpr int kInFlight = 4;  // 16-byte loads of a thread before their values are used
 
 template <typename T>
-__device__ __forceinline__ void sum_chunk(const T *g, int n, Sums &s)
+__device__ __forceinline__ void sum_run(const T *g, size_t n, Sums &s)
 {
     constexpr int V = 16 / sizeof(T), kStep = kThreads * V;
-    int i0 = 0;
+    size_t i0 = 0;
     if (((uintptr_t)g & 15) == 0) {
         i0 = n / V * V;
-        for (int i = threadIdx.x * V; i < i0; i += kInFlight * kStep) {
+        for (size_t i = threadIdx.x * V; i < i0; i += kInFlight * kStep) {
             uint4 raw[kInFlight];
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u)
@@ -108,7 +108,7 @@ __device__ __forceinline__ void sum_chunk(const T *g, int n, Sums &s)
             }
         }
     }
-    for (int i = i0 + threadIdx.x; i < n; i += kThreads) add_square(s, to_f<T>(g[i]));
+    for (size_t i = i0 + threadIdx.x; i < n; i += kThreads) add_square(s, to_f<T>(g[i]));
 }
 
 template <typename T>
@@ -150,26 +150,36 @@ __device__ __forceinline__ double block_sum(double v, double *sh)
     return v;
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_squares(const __grid_constant__ Table t, double *part)
+// This block's run of chunks: [first, last) of `chunks`, in equal parts.
+__device__ __forceinline__ uint32_t run_start(uint32_t chunks, uint32_t block)
+{
+    return (uint32_t)((uint64_t)chunks * block / gridDim.x);
+}
+
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_grad_squares(const __grid_constant__ Table t, double *part)
 {
     __shared__ double sh[kThreads / 32];
-    const uint32_t chunks = t.first[t.n];
+    const uint32_t chunks = t.first[t.n], last = run_start(chunks, blockIdx.x + 1);
+    uint32_t c = run_start(chunks, blockIdx.x);
     Sums s = {0.f, 0.f, 0.f};
-    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int i = tensor_of(t, c);
-        const uint32_t at = c - t.first[i];
-        const bool bf16 = t.last_n[i] >> 31;
-        const int n = c + 1 < t.first[i + 1] ? kChunk : (int)(t.last_n[i] & 0x7fffffffu);
-        if (bf16) sum_chunk((const __nv_bfloat16 *)t.g[i] + (size_t)at * kChunk, n, s);
-        else sum_chunk((const float *)t.g[i] + (size_t)at * kChunk, n, s);
-    }
+    if (c < last)
+        for (int i = tensor_of(t, c); c < last; ++i) {
+            const uint32_t first = t.first[i], end = min(last, t.first[i + 1]);
+            const bool bf16 = t.last_n[i] >> 31, whole = end < t.first[i + 1];  // its last chunk is not in this run
+            const int es = bf16 ? 2 : 4, per = kChunkBytes / es;
+            const size_t n = (size_t)(end - c - 1) * per + (whole ? per : (int)(t.last_n[i] & 0x7fffffffu));
+            const char *g = (const char *)t.g[i] + (size_t)(c - first) * kChunkBytes;
+            if (bf16) sum_run((const __nv_bfloat16 *)g, n, s);
+            else sum_run((const float *)g, n, s);
+            c = end;
+        }
     const double up = (double)kUp, down = (double)kDown;
     const double v = (double)s.mid + (double)s.small / (up * up) + (double)s.big / (down * down);
     const double sum = block_sum(v, sh);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     k_grad_scale(const __grid_constant__ Table t, const double *__restrict__ part, int n_part, float max_norm,
                  float *norm_out)
 {
@@ -180,17 +190,26 @@ __global__ void __launch_bounds__(kThreads)
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
     const double ratio = (double)max_norm / (norm + 1e-6);
     const float c = ratio > 1.0 ? 1.f : (float)ratio;  // a NaN stays
-    const uint32_t chunks = t.first[t.n];
-    for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
-        const uint32_t ch = chunks - 1 - b;
-        const int i = tensor_of(t, ch);
-        if (c == 1.f && t.out[i] == t.g[i]) continue;  // in place and nothing to scale
-        const size_t at = (size_t)(ch - t.first[i]) * kChunk;
-        const bool bf16 = t.last_n[i] >> 31;
-        const int n = ch + 1 < t.first[i + 1] ? kChunk : (int)(t.last_n[i] & 0x7fffffffu);
-        if (bf16) scale_chunk((const __nv_bfloat16 *)t.g[i] + at, (__nv_bfloat16 *)t.out[i] + at, n, c);
-        else scale_chunk((const float *)t.g[i] + at, (float *)t.out[i] + at, n, c);
-    }
+    const uint32_t chunks = t.first[t.n], first = run_start(chunks, blockIdx.x);
+    uint32_t end = run_start(chunks, blockIdx.x + 1);
+    if (first < end)
+        for (int i = tensor_of(t, end - 1); end > first; --i) {
+            // chunks [from, end) of tensor i, from the last one down
+            const uint32_t from = max(first, t.first[i]);
+            if (!(c == 1.f && t.out[i] == t.g[i])) {  // else in place and nothing to scale
+                const bool bf16 = t.last_n[i] >> 31;
+                const int per = kChunkBytes / (bf16 ? 2 : 4);
+                for (uint32_t ch = end; ch-- > from;) {
+                    const size_t at = (size_t)(ch - t.first[i]) * kChunkBytes;
+                    const int n = ch + 1 < t.first[i + 1] ? per : (int)(t.last_n[i] & 0x7fffffffu);
+                    const char *g = (const char *)t.g[i] + at;
+                    char *o = (char *)t.out[i] + at;
+                    if (bf16) scale_chunk((const __nv_bfloat16 *)g, (__nv_bfloat16 *)o, n, c);
+                    else scale_chunk((const float *)g, (float *)o, n, c);
+                }
+            }
+            end = from;
+        }
 }
 
 size_t part_bytes(int64_t n_tensors)
@@ -288,12 +307,12 @@ pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, voi
             t.n = 0;
             for (; i < n_tensors && t.n < kBatch; ++i) {
                 if (numel[i] == 0) continue;
-                const int64_t c = (numel[i] + kChunk - 1) / kChunk;
+                const int64_t per = kChunkBytes / (dtype[i] == PMHA_BF16 ? 2 : 4), c = (numel[i] + per - 1) / per;
                 if (chunks + c > (int64_t)0x7fffffff) break;
                 t.g[t.n] = grads[i];
                 t.out[t.n] = out ? out[i] : const_cast<void *>(grads[i]);
                 t.first[t.n] = (uint32_t)chunks;
-                t.last_n[t.n] = (uint32_t)(numel[i] - (c - 1) * kChunk) | (dtype[i] == PMHA_BF16 ? 1u << 31 : 0u);
+                t.last_n[t.n] = (uint32_t)(numel[i] - (c - 1) * per) | (dtype[i] == PMHA_BF16 ? 1u << 31 : 0u);
                 chunks += c;
                 ++t.n;
             }

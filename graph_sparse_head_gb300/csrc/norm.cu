@@ -84,10 +84,24 @@ __device__ __forceinline__ Two add(Two a, Two b)
     const Two s = two_sum(a.hi, b.hi);
     return {s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
 }
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// a / b for normal b: an approximate quotient (some 22 bits) and its exact
+// remainder's quotient; hi and lo may overlap in two bits.
 __device__ __forceinline__ Two div(Two a, float b)
 {
-    const float q = __fdiv_rn(a.hi, b);
-    return {q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, b, a.hi), a.lo), b)};
+    const float r = rcp(b), q = __fmul_rn(a.hi, r);
+    return {q, __fmul_rn(__fadd_rn(__fmaf_rn(-q, b, a.hi), a.lo), r)};
+}
+__device__ __forceinline__ Two mul(Two a, Two b)
+{
+    Two p = two_mul(a.hi, b.hi);
+    p.lo = __fadd_rn(p.lo, __fmaf_rn(a.hi, b.lo, __fmul_rn(a.lo, b.hi)));
+    return p;
 }
 // 1 / sqrt(m): one Newton step with its second-order term from the library's root
 __device__ __forceinline__ Two inv_sqrt(Two m)
@@ -98,18 +112,8 @@ __device__ __forceinline__ Two inv_sqrt(Two m)
     e = __fsub_rn(e, __fmaf_rn(m.hi, p.lo, __fmul_rn(m.lo, p.hi)));
     return {y, __fmul_rn(y, __fmaf_rn(__fmul_rn(0.375f, e), e, __fmul_rn(0.5f, e)))};
 }
-// The float next to hi + lo that a later rounding to fewer bits takes as it
-// would take the exact sum: the last bit of a cut result is set ("to odd").
-__device__ __forceinline__ float to_odd(Two v)
-{
-    const float s = __fadd_rn(v.hi, v.lo);
-    const float d = __fsub_rn(v.lo, __fsub_rn(s, v.hi));  // exact: |hi| >= |lo|
-    int b = __float_as_int(s);
-    if (d != 0.f && !(b & 1) && s != 0.f) b += ((d > 0.f) == (s > 0.f)) ? 1 : -1;
-    return __int_as_float(b);
-}
-
 struct NormArgs {
+    Two inv_width;
     const void *x, *res, *w;
     void *sum, *out;
     uint8_t *q;
@@ -124,16 +128,13 @@ struct Quant {
     float scale;
     Two c;
 };
-__device__ __forceinline__ Quant quant(Two ss, Two amax, int width, float eps)
+__device__ __forceinline__ Quant quant(Two ss, Two amax, Two inv_width, float eps)
 {
-    Two m = div(ss, (float)width);
-    m = add(m, Two{eps, 0.f});
+    Two m = add(mul(ss, inv_width), Two{eps, 0.f});
     const float mh = __fadd_rn(m.hi, m.lo);
     m = {mh, __fsub_rn(m.lo, __fsub_rn(mh, m.hi))};
     const Two r = inv_sqrt(m);
-    Two y = two_mul(amax.hi, r.hi);
-    y.lo = __fadd_rn(y.lo, __fmaf_rn(amax.hi, r.lo, __fmul_rn(amax.lo, r.hi)));
-    const Two s = div(y, 448.f);
+    const Two s = mul(mul(amax, r), Two{1.f / 448.f, (float)(1.0 / 448.0 - (double)(1.f / 448.f))});
     Quant z;
     z.scale = __fadd_rn(s.hi, s.lo);
     if (z.scale < kScaleMin) z.scale = kScaleMin;  // a NaN stays
@@ -150,14 +151,16 @@ __device__ __forceinline__ Two product(float a, float b)
     if constexpr (EXACT) return {__fmul_rn(a, b), 0.f};
     else return two_mul(a, b);
 }
+// f w c, cut to a float whose last bit is set where anything was cut ("to
+// odd"): a later rounding to fewer bits then falls as that of the exact product.
 template <bool EXACT>
 __device__ __forceinline__ float quant_value(float f, float w, Two c)
 {
     const Two p = product<EXACT>(f, w);
-    Two v = two_mul(p.hi, c.hi);
-    if constexpr (EXACT) v.lo = __fmaf_rn(p.hi, c.lo, v.lo);
-    else v.lo = __fadd_rn(v.lo, __fmaf_rn(p.hi, c.lo, __fmul_rn(p.lo, c.hi)));
-    return to_odd(v);
+    const float e = EXACT ? __fmul_rn(p.hi, c.lo) : __fmaf_rn(p.hi, c.lo, __fmul_rn(p.lo, c.hi));
+    const float s = __fmaf_rz(p.hi, c.hi, e);
+    const float cut = __fadd_rn(__fmaf_rn(p.hi, c.hi, -s), e);
+    return __int_as_float(__float_as_int(s) | (cut != 0.f ? 1 : 0));
 }
 template <bool EXACT>
 __device__ __forceinline__ void take_max(Two &m, Two o)
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
             sc = ss.hi <= kMostSquares ? 1.f : kDown;
             stats();
         }
-        const Quant z = quant(ss, am, a.width, a.eps * sc * sc);
+        const Quant z = quant(ss, am, a.inv_width, a.eps * sc * sc);
         if (live && l == 0) a.scale[row] = z.scale;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
             s2 = add(s2, sh2[i]);
             take_max<kExact>(am, shm[i]);
         }
-        z = quant(s2, am, a.width, a.eps * sc * sc);
+        z = quant(s2, am, a.inv_width, a.eps * sc * sc);
         if (threadIdx.x == 0) a.scale[row] = z.scale;
     }
     const float r = rsqrtf(ss / (float)a.width + a.eps * sc * sc) * sc;
@@ -413,6 +416,16 @@ struct NormBwdArgs {
     float eps;
 };
 
+// 16 bytes from global to shared memory, or zeros
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+template <typename T, int VEC, int NV>
+constexpr int kRingOf = VEC * sizeof(T) == 16 && NV <= 2 ? 4 / NV : 0;
+
 // Persistent: a warp walks its rows and keeps its columns' weight gradient in
 // registers (chains of at most a few hundred terms); a block sums its warps'
 // through shared memory and writes one partial row.
@@ -423,58 +436,82 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
     constexpr int kRows = 32 / LPR;
     const int lane = threadIdx.x & 31, l = lane % LPR, warp = threadIdx.x >> 5;
     const T *x = (const T *)a.x, *w = (const T *)a.w, *dy = (const T *)a.dy, *ds = (const T *)a.ds;
-    Vals<T, VEC> wv[NV];
-    float dw[NV][VEC];
+    float dw[NV][VEC], wf[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * LPR + l) * VEC;
+        Vals<T, VEC> wv;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) wv.v[i] = from_f<T>(1.f);
+        if (w && c < a.width) load<T, VEC>(w + c, wv.v);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             dw[j][i] = 0.f;
-            wv[j].v[i] = from_f<T>(1.f);
+            wf[j][i] = to_f<T>(wv.v[i]);
         }
-        if (w && c < a.width) load<T, VEC>(w + c, wv[j].v);
     }
     const long long step = (long long)gridDim.x * (kThreads / 32) * kRows;
     const float inv_width = 1.f / (float)a.width;
-    // up to 16 values a lane the next rows' loads are under way while these are
-    // worked on (more would not fit in the registers)
-    constexpr bool kAhead = NV * VEC <= 16;
-    Vals<T, VEC> v[NV], g[NV], s[NV], vn[NV], gn[NV], sn[NV];
-    auto fetch = [&](long long row0) {
+    Vals<T, VEC> v[NV], g[NV], s[NV];
+    // Rows of 16-byte pieces come through a ring of kRing rows a warp, each lane
+    // copying and reading its own pieces (no barrier): what is in flight does
+    // not take registers, and 200 KB an SM of it keep memory busy. Others are
+    // loaded when they are needed.
+    constexpr int kRing = kRingOf<T, VEC, NV>;
+    uint8_t *ring = (uint8_t *)shw + ((a.width * 4 + 15) & ~15) + threadIdx.x * 16;
+    auto fetch = [&](long long row0, int slot) {
         const long long row = row0 + lane / LPR, base = row * a.width;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + l) * VEC;
-            if (row < a.rows && c < a.width) {
-                load<T, VEC>(x + base + c, vn[j].v);
-                load<T, VEC>(dy + base + c, gn[j].v);
-                if (ds) load<T, VEC>(ds + base + c, sn[j].v);
+            const bool in = row < a.rows && c < a.width;
+            if constexpr (kRing > 0) {
+                uint8_t *p = ring + (slot * NV + j) * 3 * kThreads * 16;
+                const size_t at = in ? base + c : 0;
+                copy16(p, x + at, in);
+                copy16(p + kThreads * 16, dy + at, in);
+                if (ds) copy16(p + 2 * kThreads * 16, ds + at, in);
+            } else if (in) {
+                load<T, VEC>(x + base + c, v[j].v);
+                load<T, VEC>(dy + base + c, g[j].v);
+                if (ds) load<T, VEC>(ds + base + c, s[j].v);
             } else {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) vn[j].v[i] = gn[j].v[i] = sn[j].v[i] = from_f<T>(0.f);
+                for (int i = 0; i < VEC; ++i) v[j].v[i] = g[j].v[i] = s[j].v[i] = from_f<T>(0.f);
             }
         }
+        if constexpr (kRing > 0) asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const long long row_first = ((long long)blockIdx.x * (kThreads / 32) + warp) * kRows;
-    if constexpr (kAhead) fetch(row_first);
+    if constexpr (kRing > 0)
+        for (int i = 0; i < kRing - 1; ++i) fetch(row_first + i * step, i);
+    int slot = 0;
     for (long long row0 = row_first; row0 < a.rows; row0 += step) {
         const long long row = row0 + lane / LPR, base = row * a.width;
         const bool live = row < a.rows;
-        if constexpr (!kAhead) fetch(row0);
+        if constexpr (kRing > 0) {
+            fetch(row0 + (kRing - 1) * step, slot ? slot - 1 : kRing - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
 #pragma unroll
-        for (int j = 0; j < NV; ++j) v[j] = vn[j], g[j] = gn[j], s[j] = sn[j];
-        if constexpr (kAhead) fetch(row0 + step);
-        float ss, as, sc = 1.f;
+            for (int j = 0; j < NV; ++j) {
+                const uint8_t *p = ring + (slot * NV + j) * 3 * kThreads * 16;
+                load<T, VEC>((const T *)p, v[j].v);
+                load<T, VEC>((const T *)(p + kThreads * 16), g[j].v);
+                if (ds) load<T, VEC>((const T *)(p + 2 * kThreads * 16), s[j].v);
+            }
+            slot = slot + 1 == kRing ? 0 : slot + 1;
+        } else {
+            fetch(row0, 0);
+        }
+        float f[NV][VEC], da[NV][VEC], ss, as;
         auto stats = [&]() {
             ss = as = 0.f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float f = to_f<T>(v[j].v[i]) * sc;
-                    ss = fmaf(f, f, ss);
-                    as = fmaf(to_f<T>(g[j].v[i]) * to_f<T>(wv[j].v[i]), f, as);
+                    ss = fmaf(f[j][i], f[j][i], ss);
+                    as = fmaf(da[j][i], f[j][i], as);
                 }
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) {
@@ -482,9 +519,21 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
                 as += __shfl_xor_sync(kFull, as, o);
             }
         };
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                f[j][i] = to_f<T>(v[j].v[i]);
+                da[j][i] = to_f<T>(g[j].v[i]) * wf[j][i];
+            }
         stats();
+        float sc = 1.f;
         if (__any_sync(kFull, ss > kMostSquares)) {
             sc = ss > kMostSquares ? kDown : 1.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) f[j][i] *= sc;
             stats();
         }
         const float r = rsqrtf(ss / (float)a.width + a.eps * sc * sc);  // of s sc
@@ -496,11 +545,9 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
             Vals<T, VEC> o;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float f = to_f<T>(v[j].v[i]) * sc, gi = to_f<T>(g[j].v[i]);
-                dw[j][i] = fmaf(gi, f * r, dw[j][i]);
-                float d = rd * fmaf(-f, k, gi * to_f<T>(wv[j].v[i]));
-                if (ds) d += to_f<T>(s[j].v[i]);
-                o.v[i] = from_f<T>(d);
+                dw[j][i] = fmaf(to_f<T>(g[j].v[i]), f[j][i] * r, dw[j][i]);
+                const float d = fmaf(-f[j][i], k, da[j][i]);
+                o.v[i] = from_f<T>(ds ? fmaf(rd, d, to_f<T>(s[j].v[i])) : rd * d);
             }
             if (a.dx && live && c < a.width) store<T, VEC>((T *)a.dx + base + c, o.v);
         }
@@ -740,7 +787,8 @@ pmha_status pmha_rms_norm(pmha_dtype dtype, int64_t rows, int64_t width, const v
             return PMHA_ERR_INVALID_ARG;
         }
     }
-    NormArgs a{x, residual, weight, sum, out, (uint8_t *)out_q, scale, rows, (int)width, eps};
+    const double inv = 1.0 / (double)width;
+    NormArgs a{Two{(float)inv, (float)(inv - (double)(float)inv)}, x, residual, weight, sum, out, (uint8_t *)out_q, scale, rows, (int)width, eps};
     const Shape s = shape_of(dtype, width);
     cudaStream_t cs = (cudaStream_t)stream;
     {
@@ -816,13 +864,20 @@ pmha_status pmha_rms_norm_backward(pmha_dtype dtype, int64_t rows, int64_t width
     const int64_t grid = bwd_blocks(dtype, rows, width);
     NormBwdArgs a{x, weight, dout, dsum, dx, dweight ? (float *)workspace : nullptr, rows, (int)width, eps};
     const Shape s = shape_of(dtype, width);
+    cudaError_t attr = cudaSuccess;
     {
         StageTimer timer("rms_norm_backward", cs);
         if (s.lpr)
             dispatch(dtype, s, [&](auto t) {
                 using G = decltype(t);
-                k_rms_norm_bwd<typename G::type, G::vec, G::nv, G::lpr>
-                    <<<(unsigned)grid, kThreads, (size_t)width * 4, cs>>>(a);
+                using T = typename G::type;
+                // the block's weight gradient, then the ring: below 48 KB + 4 KB
+                const size_t smem = (((size_t)width * 4 + 15) & ~(size_t)15) +
+                                    (size_t)kRingOf<T, G::vec, G::nv> * G::nv * 3 * kThreads * 16;
+                auto kern = k_rms_norm_bwd<T, G::vec, G::nv, G::lpr>;
+                attr = smem > 48 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                        : cudaSuccess;
+                if (attr == cudaSuccess) kern<<<(unsigned)grid, kThreads, smem, cs>>>(a);
             });
         else
             dispatch_wide(dtype, s.vec, [&](auto t) {
@@ -830,6 +885,7 @@ pmha_status pmha_rms_norm_backward(pmha_dtype dtype, int64_t rows, int64_t width
                 k_rms_norm_bwd_wide<typename G::type, G::vec><<<(unsigned)grid, kThreads, 0, cs>>>(a);
             });
     }
+    PMHA_CUDA_TRY(attr);
     count_launch();
     PMHA_CUDA_TRY(cudaGetLastError());
     if (dweight) {
