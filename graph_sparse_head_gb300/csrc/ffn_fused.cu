@@ -264,10 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             const int row = (item / p.parts) * 256 + (int)rank * 128;
             for (int c = 0; c < n && !*abort_flag; ++c, ++k) {
                 constexpr bool kInside = KB > NS * C::SG;
+                if (BWD && C::kOut && yf[SB - 1] >= 0) load_y(yf[SB - 1]);
                 load_s(f_first + c * 64, kInside && c == 0 ? row : -1);
                 // a second token buffer is filled as early as can be; a single one waits for the last step
                 if (XB == 2 && c == 0) load_x(row);
-                if (C::kOut && yf[SB - 1] >= 0) load_y(yf[SB - 1]);
+                if (!BWD && C::kOut && yf[SB - 1] >= 0) load_y(yf[SB - 1]);
                 if (XB == 1 && !kInside && c == 0) load_x(row);
                 yf[2] = yf[1];
                 yf[1] = yf[0];
@@ -294,14 +295,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             auto run_step = [&](uint32_t y, bool has_s, bool first, bool last) {
                 const uint32_t ky = k - SB;  // the chunk of Y
                 const int ys = (int)(ky % NY), yb = (int)(ky % SB), xb = (int)(nx % XB), ob = (int)(n_out % OB);
-                if (has_s) {
+                auto wait_inputs = [&]() {
                     if (first) wait_for(&x_full[xb], (nx / XB) & 1u);
                     if constexpr (C::SG == KB) wait_for(&s_full[ns % NS], (ns / NS) & 1u);
-                }
+                };
+                if (has_s && !BWD) wait_inputs();  // long there: before the wait that counts
                 if (y) wait_for(&h_full[yb], (ky / SB) & 1u);
                 if (!ok) return;
                 tc_fence_after();
-                if (has_s) {
+                auto issue_s = [&]() {
+                    if constexpr (BWD) {
+                        wait_inputs();
+                        if (!ok) return;
+                        tc_fence_after();
+                    }
                     const uint32_t d = tmem + (k % SB) * C::kSCols;
                     const uint32_t xa = smem_u32(x_s + xb * C::kX);
 #pragma unroll
@@ -335,9 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                     }
                     if (last) ++nx;
                     if (one) mma_commit_pair(smem_u32(&step[k & 3u]));
-                }
-                if constexpr (C::kOut) {
-                    if (y) {
+                };
+                auto issue_y = [&]() {
+                    if constexpr (C::kOut) {
                         wait_for(&y_full[ys], (ky / NY) & 1u);
                         if (y & 1u) wait_for(&out_empty[ob], ((n_out / OB) & 1u) ^ 1u);
                         if (!ok) return;
@@ -359,7 +366,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                         }
                         if (y & 2u) ++n_out;
                     }
-                }
+                };
+                // Forward, S comes first: the next chunks' hidden values can be worked on while Y waits for the last
+                // row block to be drained. Backward, where the next chunk's epilogue waits for Y to have read the
+                // staged tiles, Y does, but for that first one.
+                const bool y_first = BWD && C::kOut && !(y & 1u);
+                if (y && y_first) issue_y();
+                if (has_s && ok) issue_s();
+                if (y && !y_first && ok) issue_y();
                 __syncwarp();
                 ++k;
             };
