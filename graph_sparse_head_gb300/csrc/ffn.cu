@@ -7,10 +7,10 @@
 //   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h, biases column sums.
 //
 // Rows are taken in blocks of at most kBlock bytes of hidden values, so that
-// the workspace stops growing with the rows. Blocks that stay in L2 were
-// measured slower: a launch costs some 8 us of start and drain, and at embed_dim
-// 128, 512 hidden, 320,000 rows the backward pass took 624 us with blocks of
-// 60 MB, 556 with 120, 521 with 240 and 488 with 480.
+// the workspace stops growing with the rows. Smaller blocks, which stay in L2,
+// were measured slower: every launch has its start and drain, and at embed_dim
+// 128, 512 hidden, 320,000 rows the backward pass took 638 us with blocks of
+// 60 MB, 575 with 120, 532 with 240, 497 with 480 and 456 with one of 980 MB.
 #include <math.h>
 
 #include <algorithm>
@@ -21,7 +21,7 @@
 namespace pmha {
 namespace {
 
-constexpr int64_t kBlock = 512 << 20;   // bytes of hidden values (h, or h, dg and du) of a block of rows
+constexpr int64_t kBlock = (int64_t)2 << 30;   // bytes of hidden values (h, or h, dg and du) of a block of rows
 constexpr int64_t kFusedRows = 2048;    // rows from which the forward pass runs as one kernel
 constexpr int kSumParts = 32;           // row ranges of a float32 block's bias sums
 

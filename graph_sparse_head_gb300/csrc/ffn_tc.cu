@@ -10,9 +10,9 @@
 // Two CTAs form a pair (tc_pair.cuh). Each has 18 warps: warp 0 copies
 // 128-byte-wide operand tiles by TMA into a ring of stages, warp 1 of the even
 // CTA issues tcgen05.mma into accumulators in tensor memory (two, so that the
-// products of one tile run under the epilogue of the last), and four groups of
-// four warps turn accumulators into outputs: each thread reads a quarter of
-// its row's columns, applies the tile's arithmetic, writes the result to a
+// products of one tile run under the epilogue of the last), and sixteen
+// warps turn accumulators into outputs: each thread reads its part of its
+// row's columns, applies the tile's arithmetic, writes the result to a
 // swizzled tile in shared memory, and one thread stores that by TMA. Pairs are
 // persistent and take tiles in order, the column tiles of one row block side
 // by side, so that the rows come from L2 after their first read.
@@ -51,7 +51,10 @@ struct Cfg {
                                       : BN / 2 * 128;                   // half of the columns
     static constexpr int kStage = kA + kB;
     static constexpr int kCols = kIsUp ? 128 : KIND == kHidden ? 64 : BN;  // output columns of a tile
-    static constexpr int kPart = kCols / 4;                                // of one of the four warp groups
+    // The up product's arithmetic outweighs its products: two teams of eight warps take the tiles in turn, so that
+    // one team's waits run under the other's arithmetic. Elsewhere one team of sixteen shares every tile.
+    static constexpr int kTeams = kIsUp ? 2 : 1;
+    static constexpr int kPart = kCols * kTeams / 4;  // columns of one of a team's groups of four warps
     static constexpr int kTile = KIND == kHidden ? 3 * kBox : KIND == kDw ? 0 : kCols / 64 * kBox;  // output tile
     static constexpr int kTiles = kTile <= 2 * kBox ? 2 : 1;  // output tiles in shared memory
     static constexpr int kAccCols = KIND == kHidden ? 192 : kIsUp ? 256 : KIND == kDw ? 2 * BN : BN;
@@ -76,8 +79,8 @@ struct Params {
     const __nv_bfloat16 *bias0, *bias1;
     const float *xs, *gs, *us;
     int has_res;
-    // dw: row blocks [split * kb_per, ...) of 64 tokens; products from first_what on
-    int splits, kb_per, tiles_m, first_what, accumulate;
+    // dw: row blocks of 64 tokens dealt to the splits; products from first_what on
+    int splits, tiles_m, first_what, accumulate;
     float *part, *sums;     // dw: partial products; column sums (split, 2 F + E) or null
     int *err;
 };
@@ -104,9 +107,19 @@ __device__ __forceinline__ void pin(uint32_t (&r)[16])
 #pragma unroll
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
-// named barrier 1 over the epilogue's 512 threads
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// named barrier 1 + team over its threads
+template <int THREADS>
+__device__ __forceinline__ void team_sync(int team)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(THREADS) : "memory");
+}
 __device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+
+__device__ __forceinline__ void four(float (&f)[4], const float *p)
+{
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
 
 // Partial sums: one CTA owns each value and the launches that add to it follow
 // one another, so the additions' order is fixed; they need no read of their own.
@@ -183,8 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
             tile /= p.splits;
             what = p.first_what + tile / per;
             tile %= per;
-            kb0 = min(p.kb, split * p.kb_per);
-            kb1 = min(p.kb, kb0 + p.kb_per);
+            kb1 = (p.kb - split + p.splits - 1) / p.splits;  // row blocks split, split + splits, ... from the end
         }
         m = tile / p.tiles_n;
         n = tile % p.tiles_n;
@@ -221,13 +233,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     tma_load_2d_pair(sa, second ? &p.a1 : &p.a0, k, row, fb);
                     tma_load_2d_pair(sb, second ? &p.b1 : &p.b0, k, n * BN + (int)rank * (BN / 2), fb);
                 } else {
+                    // the last rows first: they were written last and are still in L2
+                    const int k0 = (p.kb - 1 - (tile % p.splits) - kb * p.splits) * 64;
                     const CUtensorMap *ma = what == 0 ? &p.a0 : what == 1 ? &p.a1 : &p.a2;
                     const CUtensorMap *mb = what == 2 ? &p.b1 : &p.b0;
-                    tma_load_2d_pair(sa, ma, row, kb * 64, fb);
-                    tma_load_2d_pair(sa + kBox / 2, ma, row + 64, kb * 64, fb);
+                    tma_load_2d_pair(sa, ma, row, k0, fb);
+                    tma_load_2d_pair(sa + kBox / 2, ma, row + 64, k0, fb);
 #pragma unroll
                     for (int j = 0; j < BN / 128; ++j)
-                        tma_load_2d_pair(sb + j * (kBox / 2), mb, n * BN + (int)rank * (BN / 2) + j * 64, kb * 64, fb);
+                        tma_load_2d_pair(sb + j * (kBox / 2), mb, n * BN + (int)rank * (BN / 2) + j * 64, k0, fb);
                 }
             }
         }
@@ -294,13 +308,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
             mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
     } else {
-        // ---------------- epilogue: four groups of four warps, each a quarter of the columns of every tile
-        const int quarter = warp & 3, part = (warp - 2) >> 2, et = threadIdx.x - 64;
+        // ---------------- epilogue: teams of warps in groups of four, each group its part of a tile's columns
+        constexpr int kTeam = 512 / C::kTeams;
+        const int team = (threadIdx.x - 64) / kTeam, et = (threadIdx.x - 64) % kTeam;
+        const int quarter = warp & 3, part = et >> 7;
+        auto epi_sync = [&]() { team_sync<kTeam>(team); };
         const bool lead = et == 0;
         const int r = quarter * 32 + lane;  // row within this CTA's 128
         const int cp = part * C::kPart;     // first column within the tile
-        uint32_t i = 0;
-        for (int tile = pair; tile < p.n_tiles; tile += n_pairs, ++i) {
+        uint32_t i = (uint32_t)team;
+        for (int tile = pair + team * n_pairs; tile < p.n_tiles; tile += C::kTeams * n_pairs, i += C::kTeams) {
             const int acc = (int)(i % C::kAccs);
             int m, n, kb0, kb1, what;
             decode(tile, m, n, kb0, kb1, what);
@@ -323,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     xs = live ? p.xs[row0 + r] : 0.f;
                 }
                 if (lead) {
-                    if constexpr (C::kTiles == 2) store_wait_read1();  // the store before the last has read this tile
+                    // this thread's last store that used the tile has read it
+                    if constexpr (C::kTiles == 2 && C::kTeams == 1) store_wait_read1();
                     else store_wait_read();
                     if constexpr (KIND == kDown)
                         if (p.has_res) {
@@ -410,18 +428,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     pin(vg);
                     pin(vu);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        float h[2];
+                    for (int j = 0; j < 16; j += 4) {
+                        float bg[4], bu[4], sg[4], su[4], h[4];
+                        four(bg, v0 + c + j);
+                        four(bu, v1 + c + j);
+                        if constexpr (C::kQ8) {
+                            four(sg, s0 + c + j);
+                            four(su, s1 + c + j);
+                        }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int e = 0; e < 4; ++e) {
                             const float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
-                            const int q = c + j + e;
                             if constexpr (C::kQ8)
-                                h[e] = Act<ACT>::hidden(fmaf(a, xs * s0[q], v0[q]), fmaf(b, xs * s1[q], v1[q]));
+                                h[e] = Act<ACT>::hidden(fmaf(a, xs * sg[e], bg[e]), fmaf(b, xs * su[e], bu[e]));
                             else
-                                h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, v0[q]), fmaf(b, Act<ACT>::kUp, v1[q]));
+                                h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, bg[e]), fmaf(b, Act<ACT>::kUp, bu[e]));
                         }
                         w[j / 2] = pack_bf16(h[0], h[1]);
+                        w[j / 2 + 1] = pack_bf16(h[2], h[3]);
                     }
                     uint8_t *sb = tile_s + (c / 64) * kBox;
                     const int u = (c % 64) / 8;
@@ -439,20 +463,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                 pin(vd);
                 uint32_t wo[3][8];
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    float h[2], dg[2], du[2];
+                for (int j = 0; j < 16; j += 4) {
+                    float bg[4], bu[4], h[4], dg[4], du[4];
+                    four(bg, v0 + cp + j);
+                    four(bu, v1 + cp + j);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float b = __uint_as_float(vu[j + e]) + v1[cp + j + e], dh = __uint_as_float(vd[j + e]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float b = __uint_as_float(vu[j + e]) + bu[e], dh = __uint_as_float(vd[j + e]);
                         float slope;
-                        const float act = Act<ACT>::fast(__uint_as_float(vg[j + e]) + v0[cp + j + e], &slope);
+                        const float act = Act<ACT>::fast(__uint_as_float(vg[j + e]) + bg[e], &slope);
                         h[e] = act * b;
                         dg[e] = dh * b * slope;
                         du[e] = dh * act;
                     }
-                    wo[0][j / 2] = pack_bf16(h[0], h[1]);
-                    wo[1][j / 2] = pack_bf16(dg[0], dg[1]);
-                    wo[2][j / 2] = pack_bf16(du[0], du[1]);
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        wo[0][(j + e) / 2] = pack_bf16(h[e], h[e + 1]);
+                        wo[1][(j + e) / 2] = pack_bf16(dg[e], dg[e + 1]);
+                        wo[2][(j + e) / 2] = pack_bf16(du[e], du[e + 1]);
+                    }
                 }
 #pragma unroll
                 for (int o = 0; o < 3; ++o) {
@@ -478,10 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                         rw[4] = b.x, rw[5] = b.y, rw[6] = b.z, rw[7] = b.w;
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = pack_bf16(__uint_as_float(v[2 * j]) + v0[c + 2 * j] + __uint_as_float(rw[j] << 16),
-                                         __uint_as_float(v[2 * j + 1]) + v0[c + 2 * j + 1] +
-                                             __uint_as_float(rw[j] & 0xffff0000u));
+                    for (int j = 0; j < 8; j += 2) {
+                        float b[4];
+                        four(b, v0 + c + 2 * j);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            w[j + e] = pack_bf16(__uint_as_float(v[2 * (j + e)]) + b[2 * e] + __uint_as_float(rw[j + e] << 16),
+                                                 __uint_as_float(v[2 * (j + e) + 1]) + b[2 * e + 1] +
+                                                     __uint_as_float(rw[j + e] & 0xffff0000u));
+                    }
                     *p0 = make_uint4(w[0], w[1], w[2], w[3]);
                     *p1 = make_uint4(w[4], w[5], w[6], w[7]);
                 }
@@ -703,7 +737,6 @@ pmha_status ffn_tc_dw(const FfnTc &f, const FfnDwArgs &a, cudaStream_t s)
     if (tiles > 0x3fffffff) return too_large("ffn_dw", tiles);
     p.n_tiles = (int)tiles;
     p.kb = (int)ceil_div(a.M, 64);
-    p.kb_per = (int)ceil_div(p.kb, p.splits);
     p.part = a.part;
     p.sums = a.sums;
     p.accumulate = a.accumulate;
