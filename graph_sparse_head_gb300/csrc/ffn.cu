@@ -23,6 +23,18 @@ namespace {
 
 constexpr int64_t kBlock = (int64_t)2 << 30;   // bytes of hidden values (h, or h, dg and du) of a block of rows
 constexpr int64_t kFusedRows = 2048;    // rows from which the forward pass runs as one kernel
+// rows * E * F up to which a bf16 block's backward pass runs on float32 copies
+// and the CUDA cores: as fast there (both wait for launches), and without the
+// rounding of the hidden gradients to bf16, which few values do not average out
+constexpr int64_t kFewWork = (int64_t)1 << 26;
+// Hidden widths from which the gate and up biases' gradients are sums of the
+// bf16 values that the weights' gradients take (a tile of ones beside the
+// products, which wait for memory there), instead of the float32 ones (sums over
+// the lanes of the hidden kernel's epilogue: 259 -> 309 us at embed_dim 128,
+// 512 hidden, 320,000 rows). Either way the result is rounded to bf16; the
+// rounded terms make the error of the whole vector 1.4 times that rounding, and
+// below some 500 elements the chance of a vector far above that is not small.
+constexpr int64_t kRoundedSums = 512;
 constexpr int kSumParts = 32;           // row ranges of a float32 block's bias sums
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
@@ -44,6 +56,24 @@ __global__ void __launch_bounds__(256) k_repitch(const uint16_t *in, int64_t row
         const int c = (int)(i - r * out_cols);
         out[i] = r < rows && c < cols ? in[r * cols + c] : (uint16_t)0;
     }
+}
+
+// Up to eight bf16 arrays as float32, end to end
+struct Widen {
+    const __nv_bfloat16 *in[8];
+    float *out[8];
+    int64_t n[8];
+};
+__global__ void __launch_bounds__(256) k_widen(Widen w)
+{
+    for (int a = 0; a < 8; ++a)
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < w.n[a]; i += (int64_t)gridDim.x * 256)
+            w.out[a][i] = __bfloat162float(w.in[a][i]);
+}
+__global__ void __launch_bounds__(256) k_narrow(const float *in, int64_t n, __nv_bfloat16 *out)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        out[i] = __float2bfloat16_rn(in[i]);
 }
 
 struct Transposes {
@@ -98,9 +128,12 @@ __global__ void __launch_bounds__(256) k_colsum(Sums s)
 struct Finish {
     const float *part;  // [splits][3][F2][E2]
     void *w[3];         // (F, E), (F, E), (E, F) or null
-    const float *sums;  // [sum_parts][2 F2 + E2]
+    struct {
+        const float *p;  // n rows of partial column sums, ld apart
+        int n, ld;
+    } sums[3];
     void *b[3];         // (F), (F), (E) or null
-    int splits, sum_parts;
+    int splits;
     int E, F, E2, F2;   // widths of the gradients and of the products
 };
 // Parameter gradients from the partial sums, each added in a fixed order.
@@ -110,15 +143,22 @@ __global__ void __launch_bounds__(256) k_finish(Finish p)
 {
     __shared__ float sh[32][33];
     const int z = blockIdx.z, x = threadIdx.x % 32, y = threadIdx.x / 32;
-    if (z == 3) {  // biases: one column a thread
-        const int col = (blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            if (!p.b[i] || col >= (i == 2 ? p.E : p.F)) continue;
+    if (z == 3) {  // biases: 8 columns at a time, 32 threads a column in a fixed order
+        const int nf = (p.F + 7) / 8, ne = (p.E + 7) / 8, c8 = threadIdx.x % 8, row = threadIdx.x / 8;
+        for (int t = blockIdx.y * gridDim.x + blockIdx.x; t < 2 * nf + ne; t += gridDim.x * gridDim.y) {
+            const int i = t < nf ? 0 : t < 2 * nf ? 1 : 2, col = (t - i * nf) * 8 + c8;
+            const bool in = p.b[i] && col < (i == 2 ? p.E : p.F);
             float v = 0.f;
+            if (in)
 #pragma unroll 8
-            for (int k = 0; k < p.sum_parts; ++k) v += p.sums[(int64_t)k * (2 * p.F2 + p.E2) + i * p.F2 + col];
-            ((T *)p.b[i])[col] = from_f<T>(v);
+                for (int k = row; k < p.sums[i].n; k += 32) v += p.sums[i].p[(int64_t)k * p.sums[i].ld + col];
+            sh[row][c8] = v;
+            __syncthreads();
+            if (row == 0 && in) {
+                for (int k = 1; k < 32; ++k) v += sh[k][c8];
+                ((T *)p.b[i])[col] = from_f<T>(v);
+            }
+            __syncthreads();
         }
         return;
     }
@@ -225,15 +265,20 @@ struct Plan {
     size_t wg, wu, wd, bg, bu, bd;  // padded copies
     size_t x, dy, out;              // padded rows of a block (dy: dy or the residual)
     size_t wgt, wut, wdt;           // transposed weights (backward)
-    size_t h, dg, du, part, sums;
-    int splits, sum_parts;
+    size_t h, dg, du, part, sums, dy_sums;
+    int splits;
+    int64_t sum_rows;
+    bool exact_sums;                // gate and up bias sums from float32 values: see kRoundedSums
+    bool few;                       // a bf16 block's backward pass in float32: see kFewWork
+    size_t f_x, f_dy, f_w[3], f_b[2], f_dx;  // its float32 copies
     size_t total;
 };
 
 Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
 {
     Plan l = {};
-    const bool bf16 = p->dtype == PMHA_BF16;
+    l.few = p->dtype == PMHA_BF16 && backward && rows * p->embed_dim <= kFewWork / p->hidden_dim;
+    const bool bf16 = p->dtype == PMHA_BF16 && !l.few;  // products on the tensor cores
     const size_t es = bf16 ? 2 : 4;
     l.E2 = bf16 ? round8(p->embed_dim) : p->embed_dim;
     l.F2 = bf16 ? round8(p->hidden_dim) : p->hidden_dim;
@@ -259,7 +304,7 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
         l.bg = take(l.F2), l.bu = take(l.F2), l.bd = take(l.E2);
         l.x = take(l.R * l.E2), l.dy = take(l.R * l.E2), l.out = take(l.R * l.E2);
     }
-    if (backward || !l.fused) l.h = take(l.R * l.F2);
+    if (backward || !l.fused) l.h = take(l.R * l.F2 * (l.small ? 2 : 1));  // float32 for a few tokens
     if (backward) {
         l.dg = take(l.R * l.F2), l.du = take(l.R * l.F2);
         if (bf16) l.wgt = take(l.E2 * l.F2), l.wut = take(l.E2 * l.F2), l.wdt = take(l.E2 * l.F2);
@@ -267,9 +312,19 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
         l.splits = bf16 ? ffn_dw_splits(l.E2, l.F2, block) : ffn_f32_splits(l.E2, l.F2, block);
         l.part = o;
         o += align256((size_t)l.splits * 3 * (size_t)(l.E2 * l.F2) * 4);
+        // column sums: of a float32 block kSumParts rows of [2 F + E], of a bf16 block a row a split; and with
+        // exact_sums the hidden kernel's rows of [2][F]
+        l.exact_sums = bf16 && l.F2 < kRoundedSums;
+        l.dy_sums = o;
+        o += align256((size_t)(bf16 ? l.splits : kSumParts) * (size_t)(2 * l.F2 + l.E2) * 4);
         l.sums = o;
-        l.sum_parts = bf16 ? l.splits : kSumParts;
-        o += align256((size_t)l.sum_parts * (size_t)(2 * l.F2 + l.E2) * 4);
+        l.sum_rows = l.exact_sums ? ffn_hidden_parts(block, l.F2) : 0;
+        o += align256((size_t)l.sum_rows * (size_t)(2 * l.F2) * 4);
+        if (l.few) {
+            l.f_x = take(rows * l.E2), l.f_dy = take(rows * l.E2), l.f_dx = take(rows * l.E2);
+            for (size_t &w : l.f_w) w = take(l.E2 * l.F2);
+            for (size_t &w : l.f_b) w = take(l.F2);
+        }
     }
     l.total = o;
     return l;
@@ -508,7 +563,7 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
     const Plan l = plan_of(p, rows, true, false);
     PMHA_TRY(check_workspace(who, workspace, workspace_bytes, l.total));
     char *ws = (char *)workspace;
-    const bool bf16 = p->dtype == PMHA_BF16;
+    const bool bf16 = p->dtype == PMHA_BF16 && !l.few;
     const bool any_w = gw[0] || gw[1] || gw[2], any_b = gb[0] || gb[1] || gb[2];
     if (!dx && !any_w && !any_b) return PMHA_OK;
     pmha_ffn_params q;
@@ -525,12 +580,32 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
         k_transpose<<<dim3(side, side, 3), 256, 0, s>>>(t);
         PMHA_TRY(launched());
     }
-    float *part = (float *)(ws + l.part), *sums = (float *)(ws + l.sums);
+    float *part = (float *)(ws + l.part), *sums = (float *)(ws + l.sums), *dy_sums = (float *)(ws + l.dy_sums);
+    void *const dx_out = dx;
+    if (l.few) {
+        const void *in[7] = {x, dout, p->wg, p->wu, p->wd, p->bg, p->bu};
+        const size_t at[7] = {l.f_x, l.f_dy, l.f_w[0], l.f_w[1], l.f_w[2], l.f_b[0], l.f_b[1]};
+        const int64_t n[7] = {rows * E, rows * E, E * F, E * F, E * F, F, F};
+        Widen w = {};
+        for (int i = 0; i < 7; ++i)
+            if (in[i]) w.in[i] = (const __nv_bfloat16 *)in[i], w.out[i] = (float *)(ws + at[i]), w.n[i] = n[i];
+        q.wg = ws + l.f_w[0], q.wu = ws + l.f_w[1], q.wd = ws + l.f_w[2];
+        if (q.bg) q.bg = ws + l.f_b[0];
+        if (q.bu) q.bu = ws + l.f_b[1];
+        x = ws + l.f_x, dout = ws + l.f_dy;
+        if (dx) dx = ws + l.f_dx;
+        StageTimer timer("ffn_widen", s);
+        k_widen<<<grid_of(std::max(E * F, rows * E)), 256, 0, s>>>(w);
+        PMHA_TRY(launched());
+    }
+    if (l.exact_sums && (gb[0] || gb[1]))
+        PMHA_CUDA_TRY(cudaMemsetAsync(sums, 0, (size_t)l.sum_rows * 2 * (size_t)l.F2 * 4, s));
+    const size_t rs = bf16 ? 2 : 4;  // bytes of a token's value from here on
     bool first = true;
     for (int64_t r = 0; r < rows; r += l.R, first = false) {
         const int64_t M = std::min(l.R, rows - r);
-        const void *xr = (const char *)x + (size_t)(r * E) * es, *dyr = (const char *)dout + (size_t)(r * E) * es;
-        void *dxr = dx ? (char *)dx + (size_t)(r * E) * es : nullptr;
+        const void *xr = (const char *)x + (size_t)(r * E) * rs, *dyr = (const char *)dout + (size_t)(r * E) * rs;
+        void *dxr = dx ? (char *)dx + (size_t)(r * E) * rs : nullptr;
         if (bf16) {
             const void *xp = xr, *dyp = dyr;
             if (l.padded) {
@@ -538,7 +613,8 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 PMHA_TRY(repitch(dyr, M, E, M, l.E2, ws + l.dy, s));
                 xp = ws + l.x, dyp = ws + l.dy;
             }
-            FfnHiddenArgs hid = {xp, dyp, q.wg, q.wu, ws + l.wdt, M, ws + l.h, ws + l.dg, ws + l.du};
+            FfnHiddenArgs hid = {xp, dyp, q.wg, q.wu, ws + l.wdt, M, ws + l.h, ws + l.dg, ws + l.du,
+                                 l.exact_sums && (gb[0] || gb[1]) ? sums : nullptr};
             void *dxp = !dx ? nullptr : l.padded ? ws + l.out : dxr;
             if (l.fused) PMHA_TRY(ffn_fused_backward(tc, hid, ws + l.wgt, ws + l.wut, dxp, s));
             else PMHA_TRY(ffn_tc_hidden(tc, hid, s));
@@ -547,16 +623,17 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                     PMHA_TRY(ffn_tc_dx(tc, ws + l.dg, ws + l.du, ws + l.wgt, ws + l.wut, M, dxp, s));
                 if (l.padded) PMHA_TRY(repitch(ws + l.out, M, l.E2, M, E, dxr, s));
             }
-            if (any_w || any_b) {
-                FfnDwArgs d = {ws + l.dg, ws + l.du, ws + l.h, xp, dyp, M, part, any_b ? sums : nullptr,
-                               gw[0] || gw[1] || gb[0] || gb[1], gw[2] || gb[2], !first, l.splits};
+            const bool row_sums = !l.exact_sums && (gb[0] || gb[1]);
+            if (any_w || gb[2] || row_sums) {
+                FfnDwArgs d = {ws + l.dg, ws + l.du, ws + l.h, xp, dyp, M, part, gb[2] || row_sums ? dy_sums : nullptr,
+                               row_sums, gw[0] || gw[1] || row_sums, gw[2] || gb[2], !first, l.splits};
                 PMHA_TRY(ffn_tc_dw(tc, d, s));
             }
         } else {
             FfnF32Args a = {};
-            a.x = (const float *)xr, a.dy = (const float *)dyr, a.wg = (const float *)p->wg;
-            a.wu = (const float *)p->wu, a.wd = (const float *)p->wd, a.bg = (const float *)p->bg;
-            a.bu = (const float *)p->bu, a.h = (float *)(ws + l.h), a.dg = (float *)(ws + l.dg);
+            a.x = (const float *)xr, a.dy = (const float *)dyr, a.wg = (const float *)q.wg;
+            a.wu = (const float *)q.wu, a.wd = (const float *)q.wd, a.bg = (const float *)q.bg;
+            a.bu = (const float *)q.bu, a.h = (float *)(ws + l.h), a.dg = (float *)(ws + l.dg);
             a.du = (float *)(ws + l.du), a.out = (float *)dxr, a.M = M, a.E = E, a.F = F;
             PMHA_TRY(ffn_f32_hidden(p->act, a, true, s));
             if (dx) PMHA_TRY(ffn_f32_dx(a, s));
@@ -564,7 +641,7 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
             if (any_b) {
                 Sums c = {};
                 c.in[0] = a.dg, c.in[1] = a.du, c.in[2] = a.dy;
-                c.out = sums;
+                c.out = dy_sums;
                 c.cols[0] = c.cols[1] = (int)F, c.cols[2] = (int)E;
                 c.at[1] = (int)F, c.at[2] = (int)(2 * F), c.width = (int)(2 * F + E);
                 c.rows = M, c.accumulate = !first;
@@ -574,14 +651,25 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
             }
         }
     }
+    if (l.few && dx) {
+        StageTimer timer("ffn_narrow", s);
+        k_narrow<<<grid_of(rows * E), 256, 0, s>>>((const float *)dx, rows * E, (__nv_bfloat16 *)dx_out);
+        PMHA_TRY(launched());
+    }
     if (any_w || any_b) {
         Finish f = {};
-        f.part = part, f.splits = l.splits, f.sums = sums, f.sum_parts = l.sum_parts;
+        f.part = part, f.splits = l.splits;
+        for (int i = 0; i < 3; ++i) {
+            const bool hidden = l.exact_sums && i < 2;
+            f.sums[i].p = (hidden ? sums : dy_sums) + i * l.F2;
+            f.sums[i].n = hidden ? (int)l.sum_rows : bf16 ? l.splits : kSumParts;
+            f.sums[i].ld = (int)(2 * l.F2 + (hidden ? 0 : l.E2));
+        }
         f.E = (int)E, f.F = (int)F, f.E2 = (int)l.E2, f.F2 = (int)l.F2;
         for (int i = 0; i < 3; ++i) f.w[i] = gw[i], f.b[i] = gb[i];
         const dim3 grid((unsigned)ceil_div(E, 32), (unsigned)ceil_div(F, 32), 4);
         StageTimer timer("ffn_grads", s);
-        if (bf16) k_finish<__nv_bfloat16><<<grid, 256, 0, s>>>(f);
+        if (p->dtype == PMHA_BF16) k_finish<__nv_bfloat16><<<grid, 256, 0, s>>>(f);
         else k_finish<float><<<grid, 256, 0, s>>>(f);
         PMHA_TRY(launched());
     }

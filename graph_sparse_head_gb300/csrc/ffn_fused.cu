@@ -92,6 +92,7 @@ struct Params {
     const __nv_bfloat16 *bg, *bu, *bd;
     const float *xs, *gs, *us;
     int has_res, has_out;
+    float *sums;                    // (CTA, quarter of its rows, 2, F) column sums of dg and du, or null
     int *err;
 };
 
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             // memory once, and a chunk's values wait in registers until the last chunk's have left it
             const int s = ((warp - 2) >> 2) * 16;
             const bool lead = threadIdx.x == 64;
+            float *sums = p.sums + (size_t)(blockIdx.x * 4 + quarter) * 2 * p.F;
             for (int item = pair; item < p.items; item += n_pairs) {
                 const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
                 const int row0 = (item / p.parts) * 256 + (int)rank * 128;
@@ -497,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                             *reinterpret_cast<uint4 *>(bias + j) = *reinterpret_cast<const uint4 *>(bias_s + f0 + s + q + j);
                         tmem_wait(vg, vu, vd);
 #pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            float h[2], dg[2], du[2];
+                        for (int j = 0; j < 8; j += 4) {
+                            float h[4], dg[4], du[4];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
+                            for (int e = 0; e < 4; ++e) {
                                 const float u = __uint_as_float(vu[j + e]) + __uint_as_float(bias[j + e] & 0xffff0000u);
                                 const float d = __uint_as_float(vd[j + e]);
                                 float slope;
@@ -510,9 +512,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                                 du[e] = d * act;
                                 dg[e] = d * u * slope;
                             }
-                            wg[(q + j) / 2] = pack_bf16(dg[0], dg[1]);
-                            wu[(q + j) / 2] = pack_bf16(du[0], du[1]);
-                            wh[(q + j) / 2] = pack_bf16(h[0], h[1]);
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                wg[(q + j + e) / 2] = pack_bf16(dg[e], dg[e + 1]);
+                                wu[(q + j + e) / 2] = pack_bf16(du[e], du[e + 1]);
+                                wh[(q + j + e) / 2] = pack_bf16(h[e], h[e + 1]);
+                            }
+                            if (p.sums) add_column_sums(sums, dg, du, f0 + s + q + j, p.F, lane);
                         }
                     }
                     tc_fence_before();
@@ -723,7 +729,7 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     p.parts = (p.chunks + p.per_part - 1) / p.per_part;
     p.items *= p.parts;
     StageTimer timer(stage, s);
-    return launch_overlapping(kern, 2 * std::min(pairs, p.items), kThreads, C::kSmem, s, p);
+    return launch_overlapping(kern, dim3(2u * (unsigned)std::min(pairs, p.items)), kThreads, C::kSmem, s, p);
 }
 
 template <int EB, bool BWD, bool Q8>
@@ -789,6 +795,7 @@ pmha_status ffn_fused_backward(const FfnTc &f, const FfnHiddenArgs &a, const voi
     p.chunks = (int)((f.F + 63) / 64);
     p.bg = (const __nv_bfloat16 *)f.bg, p.bu = (const __nv_bfloat16 *)f.bu;
     p.has_out = dx != nullptr;
+    p.sums = a.sums;
     if (!make_tile_map(&p.x, a.x, a.M, f.E, f.E, 2, 128) || !make_tile_map(&p.dy, a.dy, a.M, f.E, f.E, 2, 128) ||
         !make_tile_map(&p.wg, a.wg, f.F, f.E, f.E, 2, 64) || !make_tile_map(&p.wu, a.wu, f.F, f.E, f.E, 2, 64) ||
         !make_tile_map(&p.wd, a.wd_t, f.F, f.E, f.E, 2, 32) ||

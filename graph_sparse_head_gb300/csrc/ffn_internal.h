@@ -40,7 +40,10 @@ struct FfnHiddenArgs {
     const void *x, *dy, *wg, *wu, *wd_t;
     int64_t M;
     void *h, *dg, *du;
+    // null, or ffn_hidden_parts() rows of [2][F] partial column sums of dg and du, added to (zero before the first)
+    float *sums;
 };
+int64_t ffn_hidden_parts(int64_t M, int64_t F);
 pmha_status ffn_tc_hidden(const FfnTc &f, const FfnHiddenArgs &a, cudaStream_t s);
 // The same from one kernel that keeps the tokens on the chip and, where
 // ffn_fused_dx(E), forms dx (M, E) too.
@@ -53,11 +56,12 @@ pmha_status ffn_tc_dx(const FfnTc &f, const void *dg, const void *du, const void
 // Partial weight gradients over the M rows, all three as (F, E) float32:
 // part[split][0..2] (+)= dg^T x, du^T x, h^T dy; the row range is cut into
 // ffn_dw_splits() pieces. `accumulate` adds to what part holds. sums, where not
-// null, takes the column sums of dg, du and dy: (split, 2 F + E).
+// null, takes column sums: (split, 2 F + E) of dg and du (where row_sums) and dy.
 struct FfnDwArgs {
     const void *dg, *du, *h, *x, *dy;
     int64_t M;
     float *part, *sums;
+    bool row_sums;
     bool gate_up, down;  // which of the products are wanted
     bool accumulate;
     int splits;

@@ -1,8 +1,8 @@
 // The gated block for a few tokens (single-token decoding, small graphs): the
 // weights are read once, by every SM, and multiplied on the CUDA cores. A warp
 // takes one hidden column (its gate and up rows, 16 bytes a lane), then one
-// output column; the tokens lie in shared memory, the hidden rows go through L2
-// in bf16 as everywhere. What bounds it is latency: two launches, of which the
+// output column, for 16 tokens, which lie in shared memory; the hidden rows go
+// through L2 in float32. What bounds it is latency: two launches, of which the
 // second comes up and loads its weights while the first one runs.
 #include <cuda_fp8.h>
 
@@ -21,9 +21,24 @@ struct SmallArgs {
     const void *x, *wg, *wu;
     const float *xs, *gs, *us;
     const __nv_bfloat16 *wd, *bg, *bu, *bd, *res;
-    __nv_bfloat16 *h, *out;
+    float *h;
+    __nv_bfloat16 *out;
     int M, E, F;
 };
+constexpr int kTokens = 16;  // of a block; blockIdx.y counts the blocks of tokens
+
+// This block's tokens of the arguments.
+__device__ __forceinline__ SmallArgs tokens_of(SmallArgs a, int bytes)
+{
+    const int m0 = blockIdx.y * kTokens;
+    a.x = (const uint8_t *)a.x + (size_t)m0 * a.E * bytes;
+    if (a.xs) a.xs += m0;
+    if (a.res) a.res += (size_t)m0 * a.E;
+    a.h += (size_t)m0 * a.F;
+    a.out += (size_t)m0 * a.E;
+    a.M = min(kTokens, a.M - m0);
+    return a;
+}
 
 // V consecutive values as float: 16 bytes of bf16 (V = 8) or E4M3 (V = 16), or one value
 template <bool Q8, int V>
@@ -60,9 +75,10 @@ __device__ __forceinline__ float warp_sum(float v)
 }
 
 template <bool Q8, int V, int MB, int ACT>
-__global__ void __launch_bounds__(kThreads) k_small_up(SmallArgs a)
+__global__ void __launch_bounds__(kThreads) k_small_up(SmallArgs all)
 {
     constexpr int kBytes = Q8 ? 1 : 2;
+    const SmallArgs a = tokens_of(all, kBytes);
     extern __shared__ __align__(16) uint8_t x_s[];  // M rows
     tcu::grid_dependents_may_start();
     const int lane = threadIdx.x & 31, f = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -108,12 +124,13 @@ __global__ void __launch_bounds__(kThreads) k_small_up(SmallArgs a)
     }
     if (a.bg) mg += __bfloat162float(a.bg[f]);
     if (a.bu) mu += __bfloat162float(a.bu[f]);
-    a.h[(size_t)lane * a.F + f] = __float2bfloat16_rn(Act<ACT>::hidden(mg * Act<ACT>::kGate, mu * Act<ACT>::kUp));
+    a.h[(size_t)lane * a.F + f] = Act<ACT>::hidden(mg * Act<ACT>::kGate, mu * Act<ACT>::kUp);
 }
 
 template <int V, int MB>
-__global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs a)
+__global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs all)
 {
+    const SmallArgs a = tokens_of(all, 2);
     constexpr int kAhead = 4;  // weight pieces loaded before the hidden rows are there
     const int lane = threadIdx.x & 31, e = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const __nv_bfloat16 *wd = a.wd + (size_t)min(e, a.E - 1) * a.F;
@@ -132,10 +149,16 @@ __global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs a)
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             if (m >= a.M) break;
-            float h[V];
-            widen<false, V>(a.h + (size_t)m * a.F + c, h);
+            const float *h = a.h + (size_t)m * a.F + c;
+            float hv[V];
+            if constexpr (V == 8) {
+                *reinterpret_cast<float4 *>(hv) = *reinterpret_cast<const float4 *>(h);
+                *reinterpret_cast<float4 *>(hv + 4) = *reinterpret_cast<const float4 *>(h + 4);
+            } else {
+                hv[0] = h[0];
+            }
 #pragma unroll
-            for (int i = 0; i < V; ++i) y[m] = fmaf(wv[i], h[i], y[m]);
+            for (int i = 0; i < V; ++i) y[m] = fmaf(wv[i], hv[i], y[m]);
         }
     };
 #pragma unroll
@@ -162,8 +185,8 @@ __global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs a)
 template <bool Q8, int V, int MB>
 pmha_status launch_up(pmha_act act, const SmallArgs &a, cudaStream_t s)
 {
-    const int grid = (a.F + kWarps - 1) / kWarps;
-    const size_t smem = (size_t)a.M * a.E * (Q8 ? 1 : 2);
+    const dim3 grid((unsigned)((a.F + kWarps - 1) / kWarps), (unsigned)((a.M + kTokens - 1) / kTokens));
+    const size_t smem = (size_t)std::min(a.M, kTokens) * a.E * (Q8 ? 1 : 2);
     StageTimer timer(Q8 ? "ffn_up_quantized" : "ffn_up", s);
     if (act == PMHA_ACT_SILU) k_small_up<Q8, V, MB, PMHA_ACT_SILU><<<grid, kThreads, smem, s>>>(a);
     else k_small_up<Q8, V, MB, PMHA_ACT_GELU><<<grid, kThreads, smem, s>>>(a);
@@ -181,17 +204,20 @@ pmha_status launch(pmha_act act, const SmallArgs &a, cudaStream_t s)
     else st = launch_up<false, 1, MB>(act, a, s);
     if (st != PMHA_OK) return st;
     StageTimer timer("ffn_down", s);
-    const int grid = (a.E + kWarps - 1) / kWarps;
+    const dim3 grid((unsigned)((a.E + kWarps - 1) / kWarps), (unsigned)((a.M + kTokens - 1) / kTokens));
     return a.F % 8 == 0 ? tcu::launch_overlapping(k_small_down<8, MB>, grid, kThreads, 0, s, a)
                         : tcu::launch_overlapping(k_small_down<1, MB>, grid, kThreads, 0, s, a);
 }
 
 }  // namespace
 
-// Up to 16 tokens whose rows fit in 48 KB of shared memory. One token through
-// width 256, hidden 1,024: 5.6 us against 17 of the tensor-core kernels, whose
-// tiles hold 256 tokens.
-bool ffn_small_supported(int64_t E, int64_t M, bool q8) { return M <= 16 && M * E * (q8 ? 1 : 2) <= 48 * 1024; }
+// Up to 64 tokens, 16 of whose rows fit in 48 KB of shared memory. One token
+// through width 256, hidden 1,024: 6.2 us against 17 of the tensor-core kernels,
+// whose tiles hold 256 tokens.
+bool ffn_small_supported(int64_t E, int64_t M, bool q8)
+{
+    return M <= 64 && std::min<int64_t>(M, kTokens) * E * (q8 ? 1 : 2) <= 48 * 1024;
+}
 
 pmha_status ffn_small_forward(const FfnTc &f, const FfnUpArgs &u, const void *wd, const void *residual, void *out,
                               cudaStream_t s)
@@ -200,7 +226,7 @@ pmha_status ffn_small_forward(const FfnTc &f, const FfnUpArgs &u, const void *wd
     a.x = u.x, a.wg = u.wg, a.wu = u.wu, a.xs = u.x_scale, a.gs = u.wg_scale, a.us = u.wu_scale;
     a.wd = (const __nv_bfloat16 *)wd, a.res = (const __nv_bfloat16 *)residual;
     a.bg = (const __nv_bfloat16 *)f.bg, a.bu = (const __nv_bfloat16 *)f.bu, a.bd = (const __nv_bfloat16 *)f.bd;
-    a.h = (__nv_bfloat16 *)u.h, a.out = (__nv_bfloat16 *)out;
+    a.h = (float *)u.h, a.out = (__nv_bfloat16 *)out;
     a.M = (int)u.M, a.E = (int)f.E, a.F = (int)f.F;
     if (a.M == 1) return launch<1>(f.act, a, s);
     return a.M <= 4 ? launch<4>(f.act, a, s) : launch<16>(f.act, a, s);

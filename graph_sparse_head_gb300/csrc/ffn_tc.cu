@@ -81,7 +81,8 @@ struct Params {
     int has_res;
     // dw: row blocks of 64 tokens dealt to the splits; products from first_what on
     int splits, tiles_m, first_what, accumulate;
-    float *part, *sums;     // dw: partial products; column sums (split, 2 F + E) or null
+    float *part, *sums;     // dw: partial products; column sums (split, 2 F + E) or null. hidden: see FfnHiddenArgs
+    int row_sums;           // dw: sums of dg and du too
     int *err;
 };
 
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                             // a tile of ones takes the place of an operand for the column sums: of dg and du
                             // beside the first column tile, of dy beside the first row block of h^T dy
                             const uint64_t ones = smem_desc_mn(smem_u32(vec_s), 2048);
-                            const bool rows = p.sums && what < 2 && n == 0, cols = p.sums && what == 2 && m == 0;
+                            const bool rows = p.row_sums && what < 2 && n == 0, cols = p.sums && what == 2 && m == 0;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {  // 16 tokens = 2048 bytes
                                 const uint64_t ak = da + (uint64_t)(128 * k), bk = db + (uint64_t)(128 * k);
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                                 put4(d + q, 0.f, 0.f, 0.f, 0.f, false);
                         }
                 }
-                if (sums && what < 2 && n == 0 && part == 0) {
+                if (p.row_sums && what < 2 && n == 0 && part == 0) {
                     uint32_t v[16];
                     tmem_ld16(t0 + (uint32_t)BN, v);
                     tmem_wait();
@@ -476,6 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                         dg[e] = dh * b * slope;
                         du[e] = dh * act;
                     }
+                    if (p.sums)
+                        add_column_sums(p.sums + (size_t)(blockIdx.x * 4 + quarter) * 2 * p.F, dg, du, c0 + cp + j, p.F, lane);
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         wo[0][(j + e) / 2] = pack_bf16(h[e], h[e + 1]);
@@ -612,7 +615,7 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     const pmha_status st = configure(kern, C::kSmem, &pairs);
     if (st != PMHA_OK) return st;
     StageTimer timer(stage, s);
-    return launch_overlapping(kern, 2 * std::min(pairs, p.n_tiles), kThreads, C::kSmem, s, p);
+    return launch_overlapping(kern, dim3(2u * (unsigned)std::min(pairs, p.n_tiles)), kThreads, C::kSmem, s, p);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -704,6 +707,7 @@ pmha_status ffn_tc_hidden(const FfnTc &f, const FfnHiddenArgs &a, cudaStream_t s
     p.kb = (int)ceil_div(f.E, 64);
     p.bias0 = (const __nv_bfloat16 *)f.bg;
     p.bias1 = (const __nv_bfloat16 *)f.bu;
+    p.sums = a.sums;
     if (!make_tile_map(&p.a0, a.x, a.M, f.E, f.E, 2, 128) || !make_tile_map(&p.a1, a.dy, a.M, f.E, f.E, 2, 128) ||
         !make_tile_map(&p.b0, a.wg, f.F, f.E, f.E, 2, 64) || !make_tile_map(&p.b1, a.wu, f.F, f.E, f.E, 2, 64) ||
         !make_tile_map(&p.b2, a.wd_t, f.F, f.E, f.E, 2, 32) || !make_tile_map(&p.o0, a.h, a.M, f.F, f.F, 2, 128) ||
@@ -711,6 +715,12 @@ pmha_status ffn_tc_hidden(const FfnTc &f, const FfnHiddenArgs &a, cudaStream_t s
         return map_failed("ffn_hidden");
     return f.act == PMHA_ACT_SILU ? launch<kHidden, 64, PMHA_ACT_SILU>(p, "ffn_hidden", s)
                                   : launch<kHidden, 64, PMHA_ACT_GELU>(p, "ffn_hidden", s);
+}
+
+int64_t ffn_hidden_parts(int64_t M, int64_t F)
+{
+    // four warps' rows in each CTA of the pairs, of which there are at most as many as tiles
+    return 8 * std::min<int64_t>(num_sms() / 2, ceil_div(M, 256) * ceil_div(F, 64));
 }
 
 int ffn_dw_splits(int64_t E, int64_t F, int64_t rows)
@@ -739,6 +749,7 @@ pmha_status ffn_tc_dw(const FfnTc &f, const FfnDwArgs &a, cudaStream_t s)
     p.kb = (int)ceil_div(a.M, 64);
     p.part = a.part;
     p.sums = a.sums;
+    p.row_sums = a.sums && a.row_sums;
     p.accumulate = a.accumulate;
     if (!make_tile_map(&p.a0, a.dg, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.a1, a.du, a.M, f.F, f.F, 2, 64) ||
         !make_tile_map(&p.a2, a.h, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.b0, a.x, a.M, f.E, f.E, 2, 64) ||

@@ -159,16 +159,43 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&h);
 }
+// Sums of eight values over the warp's 32 lanes; lane l returns that of value
+// (l / 4) % 8.
+__device__ __forceinline__ float sum8_over_lanes(float (&v)[8], int lane)
+{
+#pragma unroll
+    for (int h = 4, o = 16; h > 0; h >>= 1, o >>= 1)
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const bool up = lane & o;
+            const float keep = up ? v[i + h] : v[i], send = up ? v[i] : v[i + h];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    float s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 2);
+    return s + __shfl_xor_sync(0xffffffffu, s, 1);
+}
+// Adds the column sums over a warp's 32 rows of four columns' dg and du (float32, before their rounding: the bias
+// gradients) to this warp's row of partial sums, [2][F] from `sums`. One warp owns each value, so the additions' order
+// is fixed, and they need no read.
+__device__ __forceinline__ void add_column_sums(float *sums, const float (&dg)[4], const float (&du)[4], int col, int F, int lane)
+{
+    float v[8] = {dg[0], dg[1], dg[2], dg[3], du[0], du[1], du[2], du[3]};
+    const float s = sum8_over_lanes(v, lane);
+    const int i = (lane >> 2) & 7, c = col + (i & 3);
+    if ((lane & 3) == 0 && c < F)
+        asm volatile("red.global.add.f32 [%0], %1;" ::"l"(sums + (size_t)(i >> 2) * F + c), "f"(s) : "memory");
+}
+
 // 16-byte unit u (0..7) of row r of a 128-byte-wide tile with 128-byte swizzle
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4)); }
 
 // A launch of `grid` CTAs that may come up before the launch before it has
 // ended (the kernel calls grid_wait before it reads what that one writes).
 template <typename P>
-pmha_status launch_overlapping(void (*kern)(P), int grid, int threads, int smem, cudaStream_t s, const P &p)
+pmha_status launch_overlapping(void (*kern)(P), dim3 grid, int threads, int smem, cudaStream_t s, const P &p)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
