@@ -19,12 +19,12 @@ PackedEncoderLayer, which runs them together with the layer.
 """
 from __future__ import annotations
 
-import array
 import contextlib
 import ctypes
 import dataclasses
 import itertools
 import operator
+import struct
 
 import torch
 
@@ -572,7 +572,7 @@ def pmha_rms_norm_quantized(x: torch.Tensor, weight: torch.Tensor | None, eps: f
     r = _like("residual", residual, shape, dtype, dev)
     with _on(dev, stream):
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        scale = x.new_empty(shape[:-1], dtype=torch.float32)
+        scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
         s = None if residual is None else torch.empty_like(x)
         st = _library().pmha_rms_norm(_DTYPES[dtype], rows, width, x.data_ptr(), r, w, eps,
                                       None if s is None else s.data_ptr(), None, q.data_ptr(), scale.data_ptr(),
@@ -602,9 +602,9 @@ def pmha_rms_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, eps: fl
         dw = ws = None
         need = 0
         if param_grad and weight is not None:
-            dw = x.new_empty(width, dtype=torch.float32)
+            dw = torch.empty(width, dtype=torch.float32, device=x.device)
             need = lib.pmha_rms_norm_backward_workspace_size(_DTYPES[dtype], rows, width)
-            ws = x.new_empty(need, dtype=torch.uint8)
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
         st = lib.pmha_rms_norm_backward(_DTYPES[dtype], rows, width, x.data_ptr(), w, eps, dy, ds, _ptr(dx), _ptr(dw),
                                         _ptr(ws), need, _stream_of(dev, stream))
     if st:
@@ -612,8 +612,9 @@ def pmha_rms_norm_backward(x: torch.Tensor, weight: torch.Tensor | None, eps: fl
     return {"dx": dx, "dweight": dw}
 
 
-def _pointers(ts):
-    return array.array("q", map(_T.data_ptr, ts))
+def _table(code, values):
+    """A host array for the library (the format's C type, one of each value)."""
+    return struct.pack(f"{len(values)}{code}", *values)
 
 
 _dtype_of = operator.attrgetter("dtype")
@@ -639,32 +640,33 @@ def pmha_clip_grad_norm(grads, max_norm: float, out=None, stream=None) -> torch.
         raise ValueError("no gradients: the call needs a tensor to know its device")
     n = len(grads)
     # each step is one pass of a C-level map over the tensors: a stack of layers has hundreds
-    gp = _pointers(grads)  # TypeError for what is no tensor
-    sizes = array.array("q", map(_T.numel, grads))
+    gp = op = list(map(_T.data_ptr, grads))  # TypeError for what is no tensor
+    sizes = list(map(_T.numel, grads))
+    types = list(map(_dtype_of, grads))
     devices = set(map(_T.get_device, grads))
-    kinds = array.array("i", map(_DTYPES.get, map(_dtype_of, grads), itertools.repeat(-1)))
     dense = all(map(_T.is_contiguous, grads))
-    op = gp
     if out is not None:
-        op = _pointers(outs)
-        devices |= set(map(_T.get_device, outs))
+        op = list(map(_T.data_ptr, outs))
+        devices.update(map(_T.get_device, outs))
         dense = dense and all(map(_T.is_contiguous, outs))
-        if array.array("q", map(_T.numel, outs)) != sizes or \
-                not all(map(operator.is_, map(_dtype_of, outs), map(_dtype_of, grads))):
+        if list(map(_T.numel, outs)) != sizes or list(map(_dtype_of, outs)) != types:
             raise ValueError("each output must have its gradient's type and number of values")
     if not dense or len(devices) > 1 or -1 in devices:
         raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
-    if -1 in kinds:
+    bf16 = torch.bfloat16
+    if types.count(torch.float32) + types.count(bf16) != n:
         raise TypeError("gradients must be float32 or bfloat16")
+    kinds = _table("i", [PMHA_BF16 if t is bf16 else PMHA_F32 for t in types])
+    gt = _table("q", gp)
     dev = devices.pop()
     lib = _library()
     need = lib.pmha_clip_grad_norm_workspace_size(n)
     with _on(dev, stream):
-        norm = grads[0].new_empty((), dtype=torch.float32)
-        ws = grads[0].new_empty(need, dtype=torch.uint8)
-        st = lib.pmha_clip_grad_norm(n, gp.buffer_info()[0], op.buffer_info()[0], sizes.buffer_info()[0],
-                                     kinds.buffer_info()[0], max_norm, norm.data_ptr(), ws.data_ptr(), need,
-                                     _stream_of(dev, stream))
+        device = grads[0].device
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        st = lib.pmha_clip_grad_norm(n, gt, gt if op is gp else _table("q", op), _table("q", sizes), kinds, max_norm,
+                                     norm.data_ptr(), ws.data_ptr(), need, _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_clip_grad_norm")
     return norm
@@ -785,7 +787,7 @@ def _scratch(x, need, workspace):
         return ws.data_ptr(), ws.numel() * ws.element_size(), ws
     if not need:
         return None, 0, None
-    ws = x.new_empty(need, dtype=torch.uint8)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)  # half of new_empty's host time
     return ws.data_ptr(), need, ws
 
 

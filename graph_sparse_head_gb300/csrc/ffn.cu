@@ -17,6 +17,7 @@
 
 #include "ffn_internal.h"
 #include "ffn_math.cuh"
+#include "tc_pair.cuh"
 
 namespace pmha {
 namespace {
@@ -24,18 +25,14 @@ namespace {
 constexpr int64_t kBlock = (int64_t)2 << 30;   // bytes of hidden values (h, or h, dg and du) of a block of rows
 constexpr int64_t kFusedRows = 2048;    // rows from which the forward pass runs as one kernel
 // rows * E * F up to which a bf16 block's backward pass runs on float32 copies
-// and the CUDA cores: as fast there (both wait for launches), and without the
-// rounding of the hidden gradients to bf16, which few values do not average out
-constexpr int64_t kFewWork = (int64_t)1 << 26;
-// Hidden widths from which the gate and up biases' gradients are sums of the
-// bf16 values that the weights' gradients take (a tile of ones beside the
-// products, which wait for memory there), instead of the float32 ones (sums over
-// the lanes of the hidden kernel's epilogue: 259 -> 309 us at embed_dim 128,
-// 512 hidden, 320,000 rows). Either way the result is rounded to bf16; the
-// rounded terms make the error of the whole vector 1.4 times that rounding, and
-// below some 500 elements the chance of a vector far above that is not small.
-constexpr int64_t kRoundedSums = 512;
-constexpr int kSumParts = 32;           // row ranges of a float32 block's bias sums
+// and the CUDA cores, without the rounding of the hidden gradients to bf16,
+// which few values do not average out. Both wait for launches there: 64 x 128 at
+// 1,000 rows 62 us against 55 of the tensor cores, 16 x 16 at 8,192 rows 67
+// against 56, and at 32,000 rows 99 against 58.
+constexpr int64_t kFewWork = (int64_t)1 << 21;
+// The same up to so many values of dx, the array on which the rounding shows most: 128 x 512 at 16 rows costs the
+// same, 512 x 1,024 at 2 rows 84 us against 56.
+constexpr int64_t kFewOut = 2048;
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
@@ -58,22 +55,27 @@ __global__ void __launch_bounds__(256) k_repitch(const uint16_t *in, int64_t row
     }
 }
 
-// Up to eight bf16 arrays as float32, end to end
+// Up to seven bf16 arrays as float32
 struct Widen {
-    const __nv_bfloat16 *in[8];
-    float *out[8];
-    int64_t n[8];
+    const __nv_bfloat16 *in[7];
+    float *out[7];
+    int64_t n[7];
 };
 __global__ void __launch_bounds__(256) k_widen(Widen w)
 {
-    for (int a = 0; a < 8; ++a)
+    for (int a = 0; a < 7; ++a)
         for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < w.n[a]; i += (int64_t)gridDim.x * 256)
             w.out[a][i] = __bfloat162float(w.in[a][i]);
 }
-__global__ void __launch_bounds__(256) k_narrow(const float *in, int64_t n, __nv_bfloat16 *out)
+// out = the sum of `parts` float32 arrays, n apart, as bf16
+__global__ void __launch_bounds__(256) k_narrow(const float *in, int64_t n, int parts, __nv_bfloat16 *out)
 {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
-        out[i] = __float2bfloat16_rn(in[i]);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) v += in[k * n + i];
+        out[i] = __float2bfloat16_rn(v);
+    }
 }
 
 struct Transposes {
@@ -81,21 +83,37 @@ struct Transposes {
     uint16_t *out[3];
     int rows[3], cols[3];
 };
-// out[z] = in[z] transposed (bf16), 32 x 32 tiles
+// out[z] = in[z] transposed (bf16; rows and columns multiples of 8), 64 x 64
+// tiles, 16 bytes a load and store. Three 4,096 x 1,024 weights: 21 us
+// (115 with 32 x 32 tiles and 2-byte accesses).
 __global__ void __launch_bounds__(256) k_transpose(Transposes t)
 {
-    __shared__ uint16_t sh[32][33];
-    const int z = blockIdx.z, rows = t.rows[z], cols = t.cols[z];
-    const int r0 = blockIdx.y * 32, c0 = blockIdx.x * 32, x = threadIdx.x % 32, y = threadIdx.x / 32;
-    if (r0 >= rows || c0 >= cols) return;
-    for (int i = y; i < 32; i += 8)
-        if (r0 + i < rows && c0 + x < cols) sh[i][x] = t.in[z][(int64_t)(r0 + i) * cols + c0 + x];
+    __shared__ uint32_t sh[64][33];
+    const int z = blockIdx.y, rows = t.rows[z], cols = t.cols[z], across = (cols + 63) / 64;
+    const int r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int idx = threadIdx.x + i * 256, r = idx / 8, u = idx % 8;
+        if (r0 + r < rows && c0 + 8 * u < cols) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(t.in[z] + (int64_t)(r0 + r) * cols + c0 + 8 * u);
+            sh[r][4 * u] = v.x, sh[r][4 * u + 1] = v.y, sh[r][4 * u + 2] = v.z, sh[r][4 * u + 3] = v.w;
+        }
+    }
     __syncthreads();
-    for (int i = y; i < 32; i += 8)
-        if (c0 + i < cols && r0 + x < rows) t.out[z][(int64_t)(c0 + i) * rows + r0 + x] = sh[x][i];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int idx = threadIdx.x + i * 256, c = idx / 8, u = idx % 8;
+        if (c0 + c < cols && r0 + 8 * u < rows) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = __byte_perm(sh[8 * u + 2 * k][c / 2], sh[8 * u + 2 * k + 1][c / 2], c & 1 ? 0x7632 : 0x5410);
+            *reinterpret_cast<uint4 *>(t.out[z] + (int64_t)(c0 + c) * rows + r0 + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
 }
 
-// Column sums of a float32 block's dg, du and dy over this block of rows, by kSumParts
+// Column sums of a float32 block's dg, du and dy over this block of rows, by gridDim.y
 // row ranges: out[range][2 F + E] (+)=
 struct Sums {
     const float *in[3];
@@ -109,12 +127,16 @@ __global__ void __launch_bounds__(256) k_colsum(Sums s)
     __shared__ float sh[8][33];
     const int z = blockIdx.z, cols = s.cols[z], c = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
     if (!s.in[z] || blockIdx.x * 32 >= cols) return;
-    const int64_t per = (s.rows + kSumParts - 1) / kSumParts, r0 = blockIdx.y * per, r1 = min(s.rows, r0 + per);
+    const int64_t per = (s.rows + gridDim.y - 1) / gridDim.y, r0 = blockIdx.y * per, r1 = min(s.rows, r0 + per);
     const float *in = s.in[z];
-    float v = 0.f;
+    float v = 0.f, w[8] = {};  // eight chains of additions, each an eighth as long
     if (c < cols)
-#pragma unroll 8
-        for (int64_t r = r0 + y; r < r1; r += 8) v += in[r * cols + c];
+        for (int64_t r = r0 + y; r < r1; r += 64)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r + 8 * i < r1) w[i] += in[(r + 8 * i) * cols + c];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += w[i];
     sh[y][threadIdx.x % 32] = v;
     __syncthreads();
     if (y == 0 && c < cols) {
@@ -134,18 +156,20 @@ struct Finish {
     } sums[3];
     void *b[3];         // (F), (F), (E) or null
     int splits;
+    int vec;            // four consecutive gate or up gradients are one aligned piece
     int E, F, E2, F2;   // widths of the gradients and of the products
 };
 // Parameter gradients from the partial sums, each added in a fixed order.
-// 32 x 32 tiles of (F, E); the down weight's is written transposed.
+// 64 x 64 tiles of (F, E), four columns a load; the down weight's is written transposed.
 template <typename T>
 __global__ void __launch_bounds__(256) k_finish(Finish p)
 {
-    __shared__ float sh[32][33];
-    const int z = blockIdx.z, x = threadIdx.x % 32, y = threadIdx.x / 32;
-    if (z == 3) {  // biases: 8 columns at a time, 32 threads a column in a fixed order
+    __shared__ float sh[64][65];
+    const int z = blockIdx.z;
+    if (z >= 3) {  // biases: 8 columns at a time, 32 threads a column in a fixed order
         const int nf = (p.F + 7) / 8, ne = (p.E + 7) / 8, c8 = threadIdx.x % 8, row = threadIdx.x / 8;
-        for (int t = blockIdx.y * gridDim.x + blockIdx.x; t < 2 * nf + ne; t += gridDim.x * gridDim.y) {
+        const int blocks = gridDim.x * gridDim.y;
+        for (int t = (z - 3) * blocks + blockIdx.y * gridDim.x + blockIdx.x; t < 2 * nf + ne; t += (gridDim.z - 3) * blocks) {
             const int i = t < nf ? 0 : t < 2 * nf ? 1 : 2, col = (t - i * nf) * 8 + c8;
             const bool in = p.b[i] && col < (i == 2 ? p.E : p.F);
             float v = 0.f;
@@ -163,23 +187,54 @@ __global__ void __launch_bounds__(256) k_finish(Finish p)
         return;
     }
     if (!p.w[z]) return;
-    const int f0 = blockIdx.y * 32, e0 = blockIdx.x * 32;
+    const int f0 = blockIdx.y * 64, e0 = blockIdx.x * 64, x = threadIdx.x % 16 * 4, y = threadIdx.x / 16, e = e0 + x;
     const int64_t step = (int64_t)3 * p.F2 * p.E2;
-    for (int i = y; i < 32; i += 8) {
-        const int f = f0 + i, e = e0 + x;
-        float v = 0.f;
-        if (f < p.F && e < p.E) {
-            const float *src = p.part + ((int64_t)z * p.F2 + f) * p.E2 + e;
+    const float *src = p.part + ((int64_t)z * p.F2 + f0 + y) * p.E2 + e;
+    float v[4][4] = {};  // rows y, y + 16, y + 32, y + 48 of the tile
+    if (p.E2 % 4 == 0) {
 #pragma unroll 4
-            for (int k = 0; k < p.splits; ++k) v += src[k * step];
-            if (z < 2) ((T *)p.w[z])[(int64_t)f * p.E + e] = from_f<T>(v);
-        }
-        sh[i][x] = v;
+        for (int k = 0; k < p.splits; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (f0 + y + 16 * i < p.F && e < p.E) {
+                    const float4 a = *reinterpret_cast<const float4 *>(src + k * step + (int64_t)(16 * i) * p.E2);
+                    v[i][0] += a.x, v[i][1] += a.y, v[i][2] += a.z, v[i][3] += a.w;
+                }
+    } else {
+        for (int k = 0; k < p.splits; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (f0 + y + 16 * i < p.F && e + j < p.E) v[i][j] += src[k * step + (int64_t)(16 * i) * p.E2 + j];
     }
-    if (z < 2) return;
+    if (z < 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int f = f0 + y + 16 * i;
+            if (f >= p.F) break;
+            T *o = (T *)p.w[z] + (int64_t)f * p.E + e;
+            if (p.vec && e < p.E) {
+                if constexpr (sizeof(T) == 2)
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(tcu::pack_bf16(v[i][0], v[i][1]), tcu::pack_bf16(v[i][2], v[i][3]));
+                else
+                    *reinterpret_cast<float4 *>(o) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (e + j < p.E) o[j] = from_f<T>(v[i][j]);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sh[y + 16 * i][x + j] = v[i][j];
     __syncthreads();
-    for (int i = y; i < 32; i += 8)
-        if (e0 + i < p.E && f0 + x < p.F) ((T *)p.w[2])[(int64_t)(e0 + i) * p.F + f0 + x] = from_f<T>(sh[x][i]);
+    const int f = threadIdx.x % 64;
+    for (int i = threadIdx.x / 64; i < 64; i += 4)
+        if (e0 + i < p.E && f0 + f < p.F) ((T *)p.w[2])[(int64_t)(e0 + i) * p.F + f0 + f] = from_f<T>(sh[f][i]);
 }
 
 // ---------------------------------------------------------------- host side
@@ -268,8 +323,9 @@ struct Plan {
     size_t h, dg, du, part, sums, dy_sums;
     int splits;
     int64_t sum_rows;
-    bool exact_sums;                // gate and up bias sums from float32 values: see kRoundedSums
+    int sum_parts;                  // row ranges of a float32 block's column sums
     bool few;                       // a bf16 block's backward pass in float32: see kFewWork
+    int dx_parts;
     size_t f_x, f_dy, f_w[3], f_b[2], f_dx;  // its float32 copies
     size_t total;
 };
@@ -277,7 +333,8 @@ struct Plan {
 Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
 {
     Plan l = {};
-    l.few = p->dtype == PMHA_BF16 && backward && rows * p->embed_dim <= kFewWork / p->hidden_dim;
+    l.few = p->dtype == PMHA_BF16 && backward &&
+            (rows * p->embed_dim <= kFewWork / p->hidden_dim || rows * p->embed_dim <= kFewOut);
     const bool bf16 = p->dtype == PMHA_BF16 && !l.few;  // products on the tensor cores
     const size_t es = bf16 ? 2 : 4;
     l.E2 = bf16 ? round8(p->embed_dim) : p->embed_dim;
@@ -312,22 +369,42 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
         l.splits = bf16 ? ffn_dw_splits(l.E2, l.F2, block) : ffn_f32_splits(l.E2, l.F2, block);
         l.part = o;
         o += align256((size_t)l.splits * 3 * (size_t)(l.E2 * l.F2) * 4);
-        // column sums: of a float32 block kSumParts rows of [2 F + E], of a bf16 block a row a split; and with
-        // exact_sums the hidden kernel's rows of [2][F]
-        l.exact_sums = bf16 && l.F2 < kRoundedSums;
+        // blocks of 32 columns and some 256 rows or more, enough for every SM
+        l.sum_parts = (int)std::max<int64_t>(
+            1, std::min(ceil_div(block, 256), ceil_div((int64_t)num_sms() * 4, ceil_div(2 * l.F2 + l.E2, 32))));
+        // column sums: of a float32 block sum_parts rows of [2 F + E]; of a bf16 block a row of [E] a split, and the
+        // hidden kernel's rows of [2][F]
         l.dy_sums = o;
-        o += align256((size_t)(bf16 ? l.splits : kSumParts) * (size_t)(2 * l.F2 + l.E2) * 4);
+        o += align256((bf16 ? (size_t)l.splits * (size_t)l.E2 : (size_t)l.sum_parts * (size_t)(2 * l.F2 + l.E2)) * 4);
         l.sums = o;
-        l.sum_rows = l.exact_sums ? ffn_hidden_parts(block, l.F2) : 0;
+        l.sum_rows = bf16 ? ffn_hidden_parts(block, l.F2) : 0;
         o += align256((size_t)l.sum_rows * (size_t)(2 * l.F2) * 4);
         if (l.few) {
-            l.f_x = take(rows * l.E2), l.f_dy = take(rows * l.E2), l.f_dx = take(rows * l.E2);
+            l.f_x = take(l.R * l.E2), l.f_dy = take(l.R * l.E2);
+            // dx in parts, of at most a tile of 64 x 32 for each SM
+            l.dx_parts = ffn_f32_dx_parts(l.E2, l.F2, block);
+            l.f_dx = take(std::max<int64_t>(l.R * l.E2, (int64_t)num_sms() * 64 * 32));
             for (size_t &w : l.f_w) w = take(l.E2 * l.F2);
             for (size_t &w : l.f_b) w = take(l.F2);
         }
     }
     l.total = o;
     return l;
+}
+
+// Workspace of the most expensive number of rows up to `rows`: a program that
+// sizes its workspace once can run every smaller batch in it. The paths for
+// fewer rows may take more than the one for many (float32 hidden rows of a few
+// tokens, the float32 backward pass of small problems, hidden rows in memory
+// below kFusedRows); within a path the size grows with the rows.
+size_t most_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
+{
+    if (!rows) return 0;
+    const int64_t few = std::max(kFewWork / p->hidden_dim, kFewOut) / p->embed_dim;
+    size_t n = 0;
+    for (const int64_t r : {rows, backward ? few : kSmallRows, kFusedRows - 1})
+        if (r > 0 && r <= rows) n = std::max(n, plan_of(p, r, backward, q8).total);
+    return n;
 }
 
 unsigned grid_of(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 256), (int64_t)num_sms() * 16)); }
@@ -409,7 +486,7 @@ pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_qu
         return PMHA_ERR_INVALID_ARG;
     }
     const Plan l = plan_of(p, rows, false, q8 != nullptr);
-    PMHA_TRY(check_workspace(who, workspace, ws_bytes, l.total));
+    PMHA_TRY(check_workspace(who, workspace, ws_bytes, most_of(p, rows, false, q8 != nullptr)));
     char *ws = (char *)workspace;
     pmha_ffn_params q;
     PMHA_TRY(pad_params(p, l, ws, &q, s));
@@ -468,7 +545,7 @@ extern "C" {
 size_t pmha_ffn_forward_workspace_size(const pmha_ffn_params *params, int64_t rows)
 {
     if (check_ffn("pmha_ffn_forward", params, rows, false) != PMHA_OK) return SIZE_MAX;
-    return rows ? plan_of(params, rows, false, false).total : 0;
+    return most_of(params, rows, false, false);
 }
 
 pmha_status pmha_ffn_forward(const pmha_ffn_params *params, const void *x, const void *residual, int64_t rows,
@@ -482,7 +559,7 @@ pmha_status pmha_ffn_forward(const pmha_ffn_params *params, const void *x, const
 size_t pmha_ffn_forward_quantized_workspace_size(const pmha_ffn_params *params, int64_t rows)
 {
     if (check_ffn("pmha_ffn_forward_quantized", params, rows, true) != PMHA_OK) return SIZE_MAX;
-    return rows ? plan_of(params, rows, false, true).total : 0;
+    return most_of(params, rows, false, true);
 }
 
 pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha_ffn_quantized *quantized,
@@ -508,7 +585,7 @@ pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha
 size_t pmha_ffn_backward_workspace_size(const pmha_ffn_params *params, int64_t rows)
 {
     if (check_ffn("pmha_ffn_backward", params, rows, false) != PMHA_OK) return SIZE_MAX;
-    return rows ? plan_of(params, rows, true, false).total : 0;
+    return most_of(params, rows, true, false);
 }
 
 pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, const void *dout, int64_t rows, void *dx,
@@ -561,7 +638,7 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
         }
     }
     const Plan l = plan_of(p, rows, true, false);
-    PMHA_TRY(check_workspace(who, workspace, workspace_bytes, l.total));
+    PMHA_TRY(check_workspace(who, workspace, workspace_bytes, most_of(p, rows, true, false)));
     char *ws = (char *)workspace;
     const bool bf16 = p->dtype == PMHA_BF16 && !l.few;
     const bool any_w = gw[0] || gw[1] || gw[2], any_b = gb[0] || gb[1] || gb[2];
@@ -575,37 +652,38 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
         t.in[0] = (const uint16_t *)q.wg, t.out[0] = (uint16_t *)(ws + l.wgt), t.rows[0] = F2, t.cols[0] = E2;
         t.in[1] = (const uint16_t *)q.wu, t.out[1] = (uint16_t *)(ws + l.wut), t.rows[1] = F2, t.cols[1] = E2;
         t.in[2] = (const uint16_t *)q.wd, t.out[2] = (uint16_t *)(ws + l.wdt), t.rows[2] = E2, t.cols[2] = F2;
-        const unsigned side = (unsigned)ceil_div(std::max(E2, F2), 32);
+        const unsigned tiles = (unsigned)(ceil_div(E2, 64) * ceil_div(F2, 64));
         StageTimer timer("ffn_transpose", s);
-        k_transpose<<<dim3(side, side, 3), 256, 0, s>>>(t);
+        k_transpose<<<dim3(tiles, 3), 256, 0, s>>>(t);
         PMHA_TRY(launched());
     }
     float *part = (float *)(ws + l.part), *sums = (float *)(ws + l.sums), *dy_sums = (float *)(ws + l.dy_sums);
-    void *const dx_out = dx;
     if (l.few) {
-        const void *in[7] = {x, dout, p->wg, p->wu, p->wd, p->bg, p->bu};
-        const size_t at[7] = {l.f_x, l.f_dy, l.f_w[0], l.f_w[1], l.f_w[2], l.f_b[0], l.f_b[1]};
-        const int64_t n[7] = {rows * E, rows * E, E * F, E * F, E * F, F, F};
-        Widen w = {};
-        for (int i = 0; i < 7; ++i)
-            if (in[i]) w.in[i] = (const __nv_bfloat16 *)in[i], w.out[i] = (float *)(ws + at[i]), w.n[i] = n[i];
         q.wg = ws + l.f_w[0], q.wu = ws + l.f_w[1], q.wd = ws + l.f_w[2];
         if (q.bg) q.bg = ws + l.f_b[0];
         if (q.bu) q.bu = ws + l.f_b[1];
-        x = ws + l.f_x, dout = ws + l.f_dy;
-        if (dx) dx = ws + l.f_dx;
-        StageTimer timer("ffn_widen", s);
-        k_widen<<<grid_of(std::max(E * F, rows * E)), 256, 0, s>>>(w);
-        PMHA_TRY(launched());
     }
-    if (l.exact_sums && (gb[0] || gb[1]))
+    const bool hidden_sums = bf16 && (gb[0] || gb[1]);
+    if (hidden_sums)
         PMHA_CUDA_TRY(cudaMemsetAsync(sums, 0, (size_t)l.sum_rows * 2 * (size_t)l.F2 * 4, s));
-    const size_t rs = bf16 ? 2 : 4;  // bytes of a token's value from here on
     bool first = true;
     for (int64_t r = 0; r < rows; r += l.R, first = false) {
         const int64_t M = std::min(l.R, rows - r);
-        const void *xr = (const char *)x + (size_t)(r * E) * rs, *dyr = (const char *)dout + (size_t)(r * E) * rs;
-        void *dxr = dx ? (char *)dx + (size_t)(r * E) * rs : nullptr;
+        const void *xr = (const char *)x + (size_t)(r * E) * es, *dyr = (const char *)dout + (size_t)(r * E) * es;
+        void *dxr = dx ? (char *)dx + (size_t)(r * E) * es : nullptr, *const dx_out = dxr;
+        if (l.few) {  // float32 copies of the rows, and once of the weights
+            const void *in[7] = {xr, dyr, p->wg, p->wu, p->wd, p->bg, p->bu};
+            const size_t at[7] = {l.f_x, l.f_dy, l.f_w[0], l.f_w[1], l.f_w[2], l.f_b[0], l.f_b[1]};
+            const int64_t n[7] = {M * E, M * E, E * F, E * F, E * F, F, F};
+            Widen w = {};
+            for (int i = 0; i < (first ? 7 : 2); ++i)
+                if (in[i]) w.in[i] = (const __nv_bfloat16 *)in[i], w.out[i] = (float *)(ws + at[i]), w.n[i] = n[i];
+            xr = ws + l.f_x, dyr = ws + l.f_dy;
+            if (dx) dxr = ws + l.f_dx;
+            StageTimer timer("ffn_widen", s);
+            k_widen<<<grid_of(std::max(E * F, M * E)), 256, 0, s>>>(w);
+            PMHA_TRY(launched());
+        }
         if (bf16) {
             const void *xp = xr, *dyp = dyr;
             if (l.padded) {
@@ -614,7 +692,7 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 xp = ws + l.x, dyp = ws + l.dy;
             }
             FfnHiddenArgs hid = {xp, dyp, q.wg, q.wu, ws + l.wdt, M, ws + l.h, ws + l.dg, ws + l.du,
-                                 l.exact_sums && (gb[0] || gb[1]) ? sums : nullptr};
+                                 hidden_sums ? sums : nullptr};
             void *dxp = !dx ? nullptr : l.padded ? ws + l.out : dxr;
             if (l.fused) PMHA_TRY(ffn_fused_backward(tc, hid, ws + l.wgt, ws + l.wut, dxp, s));
             else PMHA_TRY(ffn_tc_hidden(tc, hid, s));
@@ -623,10 +701,9 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                     PMHA_TRY(ffn_tc_dx(tc, ws + l.dg, ws + l.du, ws + l.wgt, ws + l.wut, M, dxp, s));
                 if (l.padded) PMHA_TRY(repitch(ws + l.out, M, l.E2, M, E, dxr, s));
             }
-            const bool row_sums = !l.exact_sums && (gb[0] || gb[1]);
-            if (any_w || gb[2] || row_sums) {
-                FfnDwArgs d = {ws + l.dg, ws + l.du, ws + l.h, xp, dyp, M, part, gb[2] || row_sums ? dy_sums : nullptr,
-                               row_sums, gw[0] || gw[1] || row_sums, gw[2] || gb[2], !first, l.splits};
+            if (any_w || gb[2]) {
+                FfnDwArgs d = {ws + l.dg, ws + l.du, ws + l.h, xp, dyp, M, part, gb[2] ? dy_sums : nullptr,
+                               gw[0] || gw[1], gw[2] || gb[2], !first, l.splits};
                 PMHA_TRY(ffn_tc_dw(tc, d, s));
             }
         } else {
@@ -636,7 +713,7 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
             a.bu = (const float *)q.bu, a.h = (float *)(ws + l.h), a.dg = (float *)(ws + l.dg);
             a.du = (float *)(ws + l.du), a.out = (float *)dxr, a.M = M, a.E = E, a.F = F;
             PMHA_TRY(ffn_f32_hidden(p->act, a, true, s));
-            if (dx) PMHA_TRY(ffn_f32_dx(a, s));
+            if (dx) PMHA_TRY(ffn_f32_dx(a, l.few ? l.dx_parts : 1, s));
             if (any_w) PMHA_TRY(ffn_f32_dw(a, part, l.splits, !first, s));
             if (any_b) {
                 Sums c = {};
@@ -646,28 +723,31 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 c.at[1] = (int)F, c.at[2] = (int)(2 * F), c.width = (int)(2 * F + E);
                 c.rows = M, c.accumulate = !first;
                 StageTimer timer("ffn_bias_sums", s);
-                k_colsum<<<dim3((unsigned)ceil_div(std::max(E, F), 32), kSumParts, 3), 256, 0, s>>>(c);
+                k_colsum<<<dim3((unsigned)ceil_div(std::max(E, F), 32), (unsigned)l.sum_parts, 3), 256, 0, s>>>(c);
+                PMHA_TRY(launched());
+            }
+            if (l.few && dx) {
+                StageTimer timer("ffn_narrow", s);
+                k_narrow<<<grid_of(M * E), 256, 0, s>>>((const float *)dxr, M * E, l.dx_parts, (__nv_bfloat16 *)dx_out);
                 PMHA_TRY(launched());
             }
         }
-    }
-    if (l.few && dx) {
-        StageTimer timer("ffn_narrow", s);
-        k_narrow<<<grid_of(rows * E), 256, 0, s>>>((const float *)dx, rows * E, (__nv_bfloat16 *)dx_out);
-        PMHA_TRY(launched());
     }
     if (any_w || any_b) {
         Finish f = {};
         f.part = part, f.splits = l.splits;
         for (int i = 0; i < 3; ++i) {
-            const bool hidden = l.exact_sums && i < 2;
-            f.sums[i].p = (hidden ? sums : dy_sums) + i * l.F2;
-            f.sums[i].n = hidden ? (int)l.sum_rows : bf16 ? l.splits : kSumParts;
-            f.sums[i].ld = (int)(2 * l.F2 + (hidden ? 0 : l.E2));
+            const bool hidden = bf16 && i < 2;
+            f.sums[i].p = hidden ? sums + i * l.F2 : bf16 ? dy_sums : dy_sums + i * l.F2;
+            f.sums[i].n = hidden ? (int)l.sum_rows : bf16 ? l.splits : l.sum_parts;
+            f.sums[i].ld = (int)(hidden ? 2 * l.F2 : bf16 ? l.E2 : 2 * l.F2 + l.E2);
         }
         f.E = (int)E, f.F = (int)F, f.E2 = (int)l.E2, f.F2 = (int)l.F2;
         for (int i = 0; i < 3; ++i) f.w[i] = gw[i], f.b[i] = gb[i];
-        const dim3 grid((unsigned)ceil_div(E, 32), (unsigned)ceil_div(F, 32), 4);
+        f.vec = E % 4 == 0 && aligned(gw[0], 4 * es) && aligned(gw[1], 4 * es);
+        const int64_t tiles = ceil_div(E, 64) * ceil_div(F, 64), columns8 = 2 * ceil_div(F, 8) + ceil_div(E, 8);
+        const dim3 grid((unsigned)ceil_div(E, 64), (unsigned)ceil_div(F, 64),
+                        3 + (unsigned)std::min<int64_t>(ceil_div(columns8, tiles), 64));
         StageTimer timer("ffn_grads", s);
         if (p->dtype == PMHA_BF16) k_finish<__nv_bfloat16><<<grid, 256, 0, s>>>(f);
         else k_finish<float><<<grid, 256, 0, s>>>(f);

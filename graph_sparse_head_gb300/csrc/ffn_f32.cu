@@ -2,7 +2,7 @@
 // the operands): 64 x 32 to 128 x 128 outputs a block of 256 threads (the
 // largest tiles that leave no SM idle), 16 values of K at a time through two shared-memory buffers,
 // the next ones' loads under way while these are multiplied. Sums run in
-// ascending K with fused multiply-adds. The gate and up products share their
+// ascending K with fused multiply-adds, by pieces of 256 where registers allow. The gate and up products share their
 // tokens' tile, and the epilogues apply the activation, the residual or the
 // gradients' arithmetic.
 #include "ffn_internal.h"
@@ -76,9 +76,41 @@ struct Tile {
         return ((uintptr_t)o.p & 15) == 0 && o.ld % 4 == 0;
     }
 
+    template <typename S>
+    static __device__ __forceinline__ float (&sums_of(S &folded, float (&acc)[NB][TM][TN]))[NB][TM][TN]
+    {
+        if constexpr (kFolds) return folded;
+        else return acc;
+    }
+    // A sum in ascending order is off by some sqrt(K) roundings of its running value: where there are registers for
+    // a second set of sums, `c` takes kFold values of K and is folded into `acc`. The larger tiles take K at once.
+    static constexpr bool kFolds = NB == 1 ? TM * TN < 64 : TN == 2;
+    static constexpr int64_t kFold = 256;
     __device__ void run(const Operand &A, const Operand (&B)[NB], int64_t m0, int64_t n0, int64_t k0, int64_t k1,
                         float (&acc)[NB][TM][TN])
     {
+        float folded[kFolds ? NB : 1][kFolds ? TM : 1][kFolds ? TN : 1];
+        float(&c)[NB][TM][TN] = sums_of(folded, acc);
+        auto clear = [&]() {
+#pragma unroll
+            for (auto &operand : folded)
+#pragma unroll
+                for (auto &row : operand)
+#pragma unroll
+                    for (float &v : row) v = 0.f;
+        };
+        auto fold = [&]() {
+            if constexpr (kFolds) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) acc[b][i][j] += folded[b][i][j];
+                clear();
+            }
+        };
+        clear();
         const bool va = vectors(A) && k0 % 4 == 0;
         bool vb[NB];
 #pragma unroll
@@ -123,14 +155,16 @@ struct Tile {
 #pragma unroll
                     for (int i = 0; i < TM; ++i)
 #pragma unroll
-                        for (int j = 0; j < TN; ++j) acc[b][i][j] = __fmaf_rn(a[i], e[j], acc[b][i][j]);
+                        for (int j = 0; j < TN; ++j) c[b][i][j] = __fmaf_rn(a[i], e[j], c[b][i][j]);
                 }
             }
             if (k + kK < k1) {
                 store(t ^ 1);
                 __syncthreads();
             }
+            if ((k - k0) % kFold == kFold - kK) fold();
         }
+        fold();
     }
 };
 
@@ -197,23 +231,27 @@ __global__ void __launch_bounds__(kThreads) k_down(FfnF32Args a)
         }
 }
 
-// dx = dg Wg + du Wu
+// dx = dg Wg + du Wu, over the hidden columns of part blockIdx.z of `parts`
 template <int TM, int TN>
-__global__ void __launch_bounds__(kThreads) k_dx(FfnF32Args a)
+__global__ void __launch_bounds__(kThreads) k_dx(FfnF32Args a, int parts)
 {
     using T = Tile<1, TM, TN, true, false>;
     __shared__ T sh;
     PMHA_TILE_ORIGIN(T);
     float c[1][TM][TN] = {};
     const Operand G[1] = {{a.wg, a.E, a.E}}, U[1] = {{a.wu, a.E, a.E}};
-    sh.run({a.dg, a.F, a.M}, G, m0, n0, 0, a.F, c);
-    sh.run({a.du, a.F, a.M}, U, m0, n0, 0, a.F, c);
+    const int64_t per = ((a.F + parts - 1) / parts + 3) / 4 * 4, k0 = min(a.F, blockIdx.z * per), k1 = min(a.F, k0 + per);
+    if (k0 < k1) {
+        sh.run({a.dg, a.F, a.M}, G, m0, n0, k0, k1, c);
+        sh.run({a.du, a.F, a.M}, U, m0, n0, k0, k1, c);
+    }
+    float *out = a.out + blockIdx.z * a.M * a.E;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t m = m0 + T::mrow(i), n = n0 + T::ncol(j);
-            if (m < a.M && n < a.E) a.out[m * a.E + n] = c[0][i][j];
+            if (m < a.M && n < a.E) out[m * a.E + n] = c[0][i][j];
         }
 }
 
@@ -291,12 +329,18 @@ pmha_status ffn_f32_down(const FfnF32Args &a, cudaStream_t s)
     return launched();
 }
 
-pmha_status ffn_f32_dx(const FfnF32Args &a, cudaStream_t s)
+int ffn_f32_dx_parts(int64_t E, int64_t F, int64_t rows)
+{
+    // pieces of 64 hidden columns or more, until every SM has a tile of 64 x 32
+    return (int)std::max<int64_t>(1, std::min(ceil_div(F, 64), num_sms() / (ceil_div(rows, 64) * ceil_div(E, 32))));
+}
+
+pmha_status ffn_f32_dx(const FfnF32Args &a, int parts, cudaStream_t s)
 {
     StageTimer timer("ffn_dx", s);
-    with_tile<8>(a.M, a.E, 1, [&](auto t, dim3 g) {
+    with_tile<8>(a.M, a.E, parts, [&](auto t, dim3 g) {
         using S = decltype(t);
-        k_dx<S::TM, S::TN><<<g, kThreads, 0, s>>>(a);
+        k_dx<S::TM, S::TN><<<g, kThreads, 0, s>>>(a, parts);
     });
     return launched();
 }

@@ -27,14 +27,13 @@
 // the warps share the instruction cache, 2,000; sixteen epilogue warps instead
 // of eight 1,440 to 1,640; the result through TMA instead of 32-byte accesses (a
 // warp's 32 rows cost the memory pipe 32 cycles an instruction) and a third
-// S buffer: see the forward rate beside ffn_fused_forward.
+// S buffer about 1,350, of which two special-function results a value take 1,024.
+// 320,000 rows of embed_dim 128, 512 hidden: forward 125 us (126 GFLOP: 1.01
+// PFLOP/s, 53 % of cuBLAS bf16), backward 246 of the 443 us of its pass.
 //
 // Every wait is bounded; after an expired one the waits return at once, the
 // loops run out, and pmha_device_status reports PMHA_ERR_TIMEOUT.
 #include <algorithm>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "ffn_internal.h"
 #include "ffn_math.cuh"
@@ -96,24 +95,7 @@ struct Params {
     int *err;
 };
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
-__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
 template <int N>
 __device__ __forceinline__ void pin(uint32_t (&r)[N])
 {
@@ -130,7 +112,6 @@ __device__ __forceinline__ void tmem_wait(R &...regs)
 
 // named barrier 4 over the chunk epilogue's 512 threads
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 4, 512;" ::: "memory"); }
-__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 template <int EB, bool BWD, bool Q8, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block(const __grid_constant__ Params p)
@@ -397,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
         }
     } else if (warp < 18) {
         // ---------------- chunk epilogue, 16 warps
-        const int quarter = warp & 3, r = quarter * 32 + lane;
+        const int quarter = warp & 3;
         for (int i = threadIdx.x - 64; i < p.chunks * 64; i += 512) {
             const bool in = i < p.F;
             const float g = in && p.bg ? __bfloat162float(p.bg[i]) : 0.f, u = in && p.bu ? __bfloat162float(p.bu[i]) : 0.f;
@@ -420,11 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             const bool lead = threadIdx.x == 64 + 256 * g;
             for (int item = pair; item < p.items; item += n_pairs) {
                 const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
-                float xs = 1.f;
-                if constexpr (Q8) {
-                    const int row = (item / p.parts) * 256 + (int)rank * 128 + r;
-                    xs = row < p.M ? p.xs[row] : 0.f;
-                }
+                float xs[4] = {};  // of rows g + 8 i of the warp's
+                if constexpr (Q8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = (item / p.parts) * 256 + (int)rank * 128 + quarter * 32 + 8 * i + (lane >> 2);
+                        xs[i] = row < p.M ? p.xs[row] : 0.f;
+                    }
                 for (int c = 0; c < n; ++c, ++k) {
                     if ((k & 1u) != (uint32_t)g) continue;
                     const int f0 = f_first + c * 64, sb = (int)(k % SB);
@@ -435,37 +418,44 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                     tc_fence_after();
 #pragma unroll 1
                     for (int s = half * 32; s < half * 32 + 32; s += 16) {  // rolled: the SM's warps share its instruction cache
-                        uint32_t vg[16], vu[16], w[8];
-                        tmem_read(t0 + (uint32_t)s, vg);
-                        tmem_read(t0 + (uint32_t)(64 + s), vu);
-                        tmem_wait(vg, vu);
-                        const float *bg = bg_s + f0 + s, *bu = bu_s + f0 + s, *gs = gs_s + f0 + s, *us = us_s + f0 + s;
+                        uint32_t vg[2][8], vu[2][8];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 b4 = *reinterpret_cast<const float4 *>(bg + j);
-                            const float4 c4 = *reinterpret_cast<const float4 *>(bu + j);
-                            const float bj[4] = {b4.x, b4.y, b4.z, b4.w}, cj[4] = {c4.x, c4.y, c4.z, c4.w};
-                            float mj[4] = {}, nj[4] = {}, h[4];
-                            if constexpr (Q8) {
-                                const float4 m4 = *reinterpret_cast<const float4 *>(gs + j);
-                                const float4 n4 = *reinterpret_cast<const float4 *>(us + j);
-                                mj[0] = m4.x, mj[1] = m4.y, mj[2] = m4.z, mj[3] = m4.w;
-                                nj[0] = n4.x, nj[1] = n4.y, nj[2] = n4.z, nj[3] = n4.w;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
-                                if constexpr (Q8)
-                                    h[e] = Act<ACT>::hidden(fmaf(a, xs * mj[e], bj[e]), fmaf(b, xs * nj[e], cj[e]));
-                                else
-                                    h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, bj[e]),
-                                                            fmaf(b, Act<ACT>::kUp, cj[e]));
-                            }
-                            w[j / 2] = pack_bf16(h[0], h[1]);
-                            w[j / 2 + 1] = pack_bf16(h[2], h[3]);
+                        for (int q = 0; q < 2; ++q) {
+                            tmem_ld_frag(t0 + ((uint32_t)(q * 16) << 16) + (uint32_t)s, vg[q]);
+                            tmem_ld_frag(t0 + ((uint32_t)(q * 16) << 16) + (uint32_t)(64 + s), vu[q]);
                         }
-                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4 *>(st + swizzled(r, s / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        const int c2 = f0 + s + 2 * (lane & 3);
+                        float bg[4], bu[4], mg[4] = {}, mu[4] = {};
+                        two_pairs(bg, bg_s + c2);
+                        two_pairs(bu, bu_s + c2);
+                        if constexpr (Q8) {
+                            two_pairs(mg, gs_s + c2);
+                            two_pairs(mu, us_s + c2);
+                        }
+                        tmem_wait(vg[0], vu[0], vg[1], vu[1]);
+                        const uint32_t at = smem_u32(st) + swizzled(quarter * 32 + (lane & 15), s / 8 + (lane >> 4));
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) {
+                                float h[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int i = (j >> 2) * 2 + e;
+                                    const float a = __uint_as_float(vg[q][j + e]), b = __uint_as_float(vu[q][j + e]);
+                                    if constexpr (Q8) {
+                                        const float x = xs[2 * q + ((j >> 1) & 1)];
+                                        h[e] = Act<ACT>::hidden(fmaf(a, x * mg[i], bg[i]), fmaf(b, x * mu[i], bu[i]));
+                                    } else {
+                                        h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, bg[i]),
+                                                                fmaf(b, Act<ACT>::kUp, bu[i]));
+                                    }
+                                }
+                                w[j / 2] = pack_bf16(h[0], h[1]);
+                            }
+                            store_frags(at + (uint32_t)(q * 16 * 128), w[0], w[1], w[2], w[3]);
+                        }
                     }
                     tc_fence_before();
                     fence_async_shared();
@@ -479,6 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
             const int s = ((warp - 2) >> 2) * 16;
             const bool lead = threadIdx.x == 64;
             float *sums = p.sums + (size_t)(blockIdx.x * 4 + quarter) * 2 * p.F;
+            // this lane's row of the four 8 x 8 matrices of 16 rows x 16 columns
+            const uint32_t staged_at =
+                smem_u32(staged) + swizzled(quarter * 32 + (lane & 15), s / 8 + (lane >> 4));
             for (int item = pair; item < p.items; item += n_pairs) {
                 const int n = chunks_of(item), f_first = (item % p.parts) * p.per_part * 64;
                 const int row0 = (item / p.parts) * 256 + (int)rank * 128;
@@ -488,50 +481,52 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
                     wait_s(k);
                     tc_fence_after();
                     uint32_t wg[8], wu[8], wh[8];
+                    float cs[8] = {};
+                    uint32_t bias[4];
+                    *reinterpret_cast<uint2 *>(bias) = *reinterpret_cast<const uint2 *>(bias_s + f0 + s + 2 * (lane & 3));
+                    *reinterpret_cast<uint2 *>(bias + 2) = *reinterpret_cast<const uint2 *>(bias_s + f0 + s + 8 + 2 * (lane & 3));
 #pragma unroll
-                    for (int q = 0; q < 16; q += 8) {
-                        uint32_t vg[8], vu[8], vd[8], bias[8];
-                        tmem_read(t0 + (uint32_t)q, vg);
-                        tmem_read(t0 + (uint32_t)(64 + q), vu);
-                        tmem_read(t0 + (uint32_t)(128 + q), vd);
-#pragma unroll
-                        for (int j = 0; j < 8; j += 4)
-                            *reinterpret_cast<uint4 *>(bias + j) = *reinterpret_cast<const uint4 *>(bias_s + f0 + s + q + j);
+                    for (int q = 0; q < 2; ++q) {  // 16 of the warp's rows
+                        uint32_t vg[8], vu[8], vd[8];
+                        const uint32_t tq = t0 + ((uint32_t)(q * 16) << 16);
+                        tmem_ld_frag(tq, vg);
+                        tmem_ld_frag(tq + 64, vu);
+                        tmem_ld_frag(tq + 128, vd);
                         tmem_wait(vg, vu, vd);
 #pragma unroll
-                        for (int j = 0; j < 8; j += 4) {
-                            float h[4], dg[4], du[4];
+                        for (int j = 0; j < 8; j += 2) {
+                            float h[2], dg[2], du[2];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float u = __uint_as_float(vu[j + e]) + __uint_as_float(bias[j + e] & 0xffff0000u);
+                            for (int e = 0; e < 2; ++e) {
+                                const int c = (j >> 2) * 2 + e;
+                                const float u = __uint_as_float(vu[j + e]) + __uint_as_float(bias[c] & 0xffff0000u);
                                 const float d = __uint_as_float(vd[j + e]);
                                 float slope;
                                 const float act =
-                                    Act<ACT>::fast(__uint_as_float(vg[j + e]) + __uint_as_float(bias[j + e] << 16), &slope);
+                                    Act<ACT>::fast(__uint_as_float(vg[j + e]) + __uint_as_float(bias[c] << 16), &slope);
                                 h[e] = act * u;
                                 du[e] = d * act;
                                 dg[e] = d * u * slope;
+                                cs[c] += dg[e];
+                                cs[4 + c] += du[e];
                             }
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                wg[(q + j + e) / 2] = pack_bf16(dg[e], dg[e + 1]);
-                                wu[(q + j + e) / 2] = pack_bf16(du[e], du[e + 1]);
-                                wh[(q + j + e) / 2] = pack_bf16(h[e], h[e + 1]);
-                            }
-                            if (p.sums) add_column_sums(sums, dg, du, f0 + s + q + j, p.F, lane);
+                            wg[(8 * q + j) / 2] = pack_bf16(dg[0], dg[1]);
+                            wu[(8 * q + j) / 2] = pack_bf16(du[0], du[1]);
+                            wh[(8 * q + j) / 2] = pack_bf16(h[0], h[1]);
                         }
                     }
+                    if (p.sums) add_column_sums(sums, cs, f0 + s, p.F, lane);
                     tc_fence_before();
                     if (lead) store_wait_read();  // the last chunk's tiles have been copied out
                     epi_sync();
                     if (C::kOut && k) wait_y(k - 1);  // and multiplied
-                    const uint32_t o0 = swizzled(r, s / 8), o1 = swizzled(r, s / 8 + 1);
-                    *reinterpret_cast<uint4 *>(staged + o0) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-                    *reinterpret_cast<uint4 *>(staged + o1) = make_uint4(wg[4], wg[5], wg[6], wg[7]);
-                    *reinterpret_cast<uint4 *>(staged + kBox + o0) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-                    *reinterpret_cast<uint4 *>(staged + kBox + o1) = make_uint4(wu[4], wu[5], wu[6], wu[7]);
-                    *reinterpret_cast<uint4 *>(staged + 2 * kBox + o0) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-                    *reinterpret_cast<uint4 *>(staged + 2 * kBox + o1) = make_uint4(wh[4], wh[5], wh[6], wh[7]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t at = staged_at + (uint32_t)(q * 16 * 128);
+                        store_frags(at, wg[4 * q], wg[4 * q + 1], wg[4 * q + 2], wg[4 * q + 3]);
+                        store_frags(at + kBox, wu[4 * q], wu[4 * q + 1], wu[4 * q + 2], wu[4 * q + 3]);
+                        store_frags(at + 2 * kBox, wh[4 * q], wh[4 * q + 1], wh[4 * q + 2], wh[4 * q + 3]);
+                    }
                     fence_async_shared();
                     epi_sync();
                     if (lead) {
@@ -669,38 +664,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_block
 
 // ---------------------------------------------------------------- host side
 
-template <typename K>
-pmha_status configure(K kern, int smem, int *pairs)
-{
-    static std::mutex mu;
-    static std::map<std::pair<int, void *>, int> known;
-    int dev = 0;
-    PMHA_CUDA_TRY(cudaGetDevice(&dev));
-    std::lock_guard<std::mutex> lk(mu);
-    const auto it = known.find({dev, (void *)kern});
-    if (it != known.end()) {
-        *pairs = it->second;
-        return PMHA_OK;
-    }
-    PMHA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 2;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    PMHA_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
-    n = std::max(1, std::min(n, num_sms() / 2));
-    known[{dev, (void *)kern}] = n;
-    *pairs = n;
-    return PMHA_OK;
-}
-
 template <int EB, bool BWD, bool Q8, int ACT>
 pmha_status launch(Params &p, const char *stage, cudaStream_t s)
 {
@@ -710,7 +673,8 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     if (!p.err) return PMHA_ERR_CUDA;
     int pairs = 0;
     auto kern = k_block<EB, BWD, Q8, ACT>;
-    const pmha_status st = configure(kern, C::kSmem, &pairs);
+    static std::atomic<int> known[kKnownDevices];
+    const pmha_status st = pairs_at_once(kern, kThreads, C::kSmem, known, &pairs);
     if (st != PMHA_OK) return st;
     if (C::kOut) p.parts = 1;
     else {

@@ -31,6 +31,7 @@ bool ffn_fused_supported(int64_t E, int64_t F, bool backward, bool q8);
 pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
                               cudaStream_t s);
 // The same for a few tokens, on the CUDA cores (ffn_small.cu); any widths.
+constexpr int64_t kSmallRows = 64;
 bool ffn_small_supported(int64_t E, int64_t M, bool q8);
 pmha_status ffn_small_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
                               cudaStream_t s);
@@ -56,12 +57,11 @@ pmha_status ffn_tc_dx(const FfnTc &f, const void *dg, const void *du, const void
 // Partial weight gradients over the M rows, all three as (F, E) float32:
 // part[split][0..2] (+)= dg^T x, du^T x, h^T dy; the row range is cut into
 // ffn_dw_splits() pieces. `accumulate` adds to what part holds. sums, where not
-// null, takes column sums: (split, 2 F + E) of dg and du (where row_sums) and dy.
+// null, takes column sums of dy, (split, E).
 struct FfnDwArgs {
     const void *dg, *du, *h, *x, *dy;
     int64_t M;
     float *part, *sums;
-    bool row_sums;
     bool gate_up, down;  // which of the products are wanted
     bool accumulate;
     int splits;
@@ -77,7 +77,9 @@ struct FfnF32Args {
 };
 pmha_status ffn_f32_hidden(pmha_act act, const FfnF32Args &a, bool backward, cudaStream_t s);
 pmha_status ffn_f32_down(const FfnF32Args &a, cudaStream_t s);
-pmha_status ffn_f32_dx(const FfnF32Args &a, cudaStream_t s);
+// dx, or with parts > 1 as many arrays (M, E), one after the other, that add up to it
+int ffn_f32_dx_parts(int64_t E, int64_t F, int64_t rows);
+pmha_status ffn_f32_dx(const FfnF32Args &a, int parts, cudaStream_t s);
 int ffn_f32_splits(int64_t E, int64_t F, int64_t rows);
 pmha_status ffn_f32_dw(const FfnF32Args &a, float *part, int splits, bool accumulate, cudaStream_t s);
 

@@ -44,10 +44,10 @@ struct Act<PMHA_ACT_SILU> {
     }
     static __device__ __forceinline__ float exact(float g) { return g / (1.f + expf(-g)); }
     static constexpr float kGate = -1.44269504f, kUp = -0.69314718f;
-    // g sigmoid(g) u; a gate far below 0 gives 1 / infinity = 0
+    // g sigmoid(g) u; a gate far below 0 gives 1 / infinity = 0, also where gate times up would overflow
     static __device__ __forceinline__ float hidden(float gate, float up)
     {
-        return gate * up * rcp(1.f + ex2(gate));
+        return gate * rcp(1.f + ex2(gate)) * up;
     }
     // act(g) and its slope, from the plain gate
     static __device__ __forceinline__ float fast(float g, float *slope)

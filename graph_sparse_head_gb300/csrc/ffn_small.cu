@@ -216,7 +216,7 @@ pmha_status launch(pmha_act act, const SmallArgs &a, cudaStream_t s)
 // whose tiles hold 256 tokens.
 bool ffn_small_supported(int64_t E, int64_t M, bool q8)
 {
-    return M <= 64 && std::min<int64_t>(M, kTokens) * E * (q8 ? 1 : 2) <= 48 * 1024;
+    return M <= kSmallRows && std::min<int64_t>(M, kTokens) * E * (q8 ? 1 : 2) <= 48 * 1024;
 }
 
 pmha_status ffn_small_forward(const FfnTc &f, const FfnUpArgs &u, const void *wd, const void *residual, void *out,

@@ -24,9 +24,6 @@
 // waits for its copies and products, frees its tensor memory and returns, and
 // pmha_device_status reports PMHA_ERR_TIMEOUT.
 #include <algorithm>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "ffn_internal.h"
 #include "ffn_math.cuh"
@@ -81,8 +78,7 @@ struct Params {
     int has_res;
     // dw: row blocks of 64 tokens dealt to the splits; products from first_what on
     int splits, tiles_m, first_what, accumulate;
-    float *part, *sums;     // dw: partial products; column sums (split, 2 F + E) or null. hidden: see FfnHiddenArgs
-    int row_sums;           // dw: sums of dg and du too
+    float *part, *sums;     // dw: partial products; column sums of dy (split, E) or null. hidden: see FfnHiddenArgs
     int *err;
 };
 
@@ -91,22 +87,13 @@ __device__ __forceinline__ uint32_t tmem_at(uint32_t base, int quarter, int col)
 {
     return base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // Keeps the uses of r behind the wait above.
-__device__ __forceinline__ void pin(uint32_t (&r)[16])
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N])
 {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 // named barrier 1 + team over its threads
 template <int THREADS>
@@ -114,7 +101,6 @@ __device__ __forceinline__ void team_sync(int team)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(THREADS) : "memory");
 }
-__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 __device__ __forceinline__ void four(float (&f)[4], const float *p)
 {
@@ -270,15 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                     if (one) {
                         if constexpr (KIND == kDw) {
                             const uint64_t da = smem_desc_mn(sa, kBox / 2), db = smem_desc_mn(sb, kBox / 2);
-                            // a tile of ones takes the place of an operand for the column sums: of dg and du
-                            // beside the first column tile, of dy beside the first row block of h^T dy
+                            // a tile of ones takes the place of an operand for the column sums of dy, beside the
+                            // first row block of h^T dy
                             const uint64_t ones = smem_desc_mn(smem_u32(vec_s), 2048);
-                            const bool rows = p.row_sums && what < 2 && n == 0, cols = p.sums && what == 2 && m == 0;
+                            const bool cols = p.sums && what == 2 && m == 0;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {  // 16 tokens = 2048 bytes
                                 const uint64_t ak = da + (uint64_t)(128 * k), bk = db + (uint64_t)(128 * k);
                                 mma_pair<false>(d, ak, bk, idesc_of(false, true, 256, BN), more | (k > 0));
-                                if (rows) mma_pair<false>(d + BN, ak, ones, idesc_of(false, true, 256, 32), more | (k > 0));
                                 if (cols) mma_pair<false>(d + BN, ones, bk, idesc_of(false, true, 256, BN), more | (k > 0));
                             }
                         } else {
@@ -323,10 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
             int m, n, kb0, kb1, what;
             decode(tile, m, n, kb0, kb1, what);
             const int row0 = m * 256 + (int)rank * 128, c0 = n * C::kCols;
-            const bool live = row0 + r < p.M;
             uint8_t *tile_s = out_s + (i % C::kTiles) * C::kTile;
             float *v0 = vec_s + (i & 1u) * 512, *v1 = v0 + 128, *s0 = v0 + 256, *s1 = v0 + 384;
-            float xs = 1.f;
+            float xs[4] = {};  // of rows g + 8 i of the warp's
             if constexpr (KIND != kDw) {
                 // bias and scales of the tile's columns, and the residual's tile, under the products
                 constexpr float kg = C::kIsUp ? Act<ACT>::kGate : 1.f, ku = C::kIsUp ? Act<ACT>::kUp : 1.f;
@@ -338,7 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                 if constexpr (C::kQ8) {
                     g0 = in ? kg * p.gs[c0 + et] : 0.f;
                     g1 = in ? ku * p.us[c0 + et] : 0.f;
-                    xs = live ? p.xs[row0 + r] : 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = row0 + quarter * 32 + 8 * k + (lane >> 2);
+                        xs[k] = row < p.M ? p.xs[row] : 0.f;
+                    }
                 }
                 if (lead) {
                     // this thread's last store that used the tile has read it
@@ -379,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
             if constexpr (KIND == kDw) {
                 const int split = tile % p.splits, f = row0 + r;
                 float *dst = p.part + ((size_t)split * 3 + what) * (size_t)p.F * p.E;
-                float *sums = p.sums ? p.sums + (size_t)split * (2 * p.F + p.E) + what * p.F : nullptr;
+                float *sums = p.sums ? p.sums + (size_t)split * p.E : nullptr;
                 const bool some = kb1 > kb0, add = p.accumulate;  // without tokens: zeros
 #pragma unroll 1
                 for (int c = cp; c < cp + C::kPart; c += 16) {
@@ -399,13 +387,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
                                 put4(d + q, 0.f, 0.f, 0.f, 0.f, false);
                         }
                 }
-                if (p.row_sums && what < 2 && n == 0 && part == 0) {
-                    uint32_t v[16];
-                    tmem_ld16(t0 + (uint32_t)BN, v);
-                    tmem_wait();
-                    pin(v);
-                    if (f < p.F && (some || !add)) put1(sums + f, some ? __uint_as_float(v[0]) : 0.f, add);
-                }
                 if (sums && what == 2 && m == 0 && quarter == 0) {  // every row holds the sums: lane 0 writes
 #pragma unroll 1
                     for (int c = cp; c < cp + C::kPart; c += 16) {
@@ -422,77 +403,93 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
             } else if constexpr (C::kIsUp) {
 #pragma unroll 1
                 for (int c = cp; c < cp + C::kPart; c += 16) {
-                    uint32_t vg[16], vu[16], w[8];
-                    tmem_ld16(t0 + (uint32_t)c, vg);
-                    tmem_ld16(t0 + (uint32_t)(128 + c), vu);
+                    uint32_t vg[2][8], vu[2][8];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        tmem_ld_frag(t0 + ((uint32_t)(q * 16) << 16) + (uint32_t)c, vg[q]);
+                        tmem_ld_frag(t0 + ((uint32_t)(q * 16) << 16) + (uint32_t)(128 + c), vu[q]);
+                    }
+                    const int c2 = c + 2 * (lane & 3);
+                    float bg[4], bu[4], sg[4], su[4];
+                    two_pairs(bg, v0 + c2);
+                    two_pairs(bu, v1 + c2);
+                    if constexpr (C::kQ8) {
+                        two_pairs(sg, s0 + c2);
+                        two_pairs(su, s1 + c2);
+                    }
+                    tmem_wait();
+                    // this lane's row of the four 8 x 8 matrices of 16 rows x 16 columns
+                    const uint32_t at = smem_u32(tile_s + (c / 64) * kBox) +
+                                        swizzled(quarter * 32 + (lane & 15), (c % 64) / 8 + (lane >> 4));
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        pin(vg[q]);
+                        pin(vu[q]);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            float h[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int k = (j >> 2) * 2 + e;
+                                const float a = __uint_as_float(vg[q][j + e]), b = __uint_as_float(vu[q][j + e]);
+                                if constexpr (C::kQ8) {
+                                    const float x = xs[2 * q + ((j >> 1) & 1)];
+                                    h[e] = Act<ACT>::hidden(fmaf(a, x * sg[k], bg[k]), fmaf(b, x * su[k], bu[k]));
+                                } else {
+                                    h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, bg[k]),
+                                                            fmaf(b, Act<ACT>::kUp, bu[k]));
+                                }
+                            }
+                            w[j / 2] = pack_bf16(h[0], h[1]);
+                        }
+                        store_frags(at + (uint32_t)(q * 16 * 128), w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else if constexpr (KIND == kHidden) {
+                float cs[8] = {};
+                const int t2 = cp + 2 * (lane & 3);
+                float bg[4], bu[4];
+                two_pairs(bg, v0 + t2);
+                two_pairs(bu, v1 + t2);
+                // this lane's row of the four 8 x 8 matrices of 16 rows x 16 columns
+                const uint32_t at0 = smem_u32(tile_s) + swizzled(quarter * 32 + (lane & 15), cp / 8 + (lane >> 4));
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {  // 16 of the warp's rows
+                    uint32_t vg[8], vu[8], vd[8], w[3][4];
+                    const uint32_t tq = t0 + ((uint32_t)(q * 16) << 16) + (uint32_t)cp;
+                    tmem_ld_frag(tq, vg);
+                    tmem_ld_frag(tq + 64, vu);
+                    tmem_ld_frag(tq + 128, vd);
                     tmem_wait();
                     pin(vg);
                     pin(vu);
+                    pin(vd);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        float bg[4], bu[4], sg[4], su[4], h[4];
-                        four(bg, v0 + c + j);
-                        four(bu, v1 + c + j);
-                        if constexpr (C::kQ8) {
-                            four(sg, s0 + c + j);
-                            four(su, s1 + c + j);
+                    for (int j = 0; j < 8; j += 2) {
+                        float h[2], dg[2], du[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int c = (j >> 2) * 2 + e;
+                            const float b = __uint_as_float(vu[j + e]) + bu[c], dh = __uint_as_float(vd[j + e]);
+                            float slope;
+                            const float act = Act<ACT>::fast(__uint_as_float(vg[j + e]) + bg[c], &slope);
+                            h[e] = act * b;
+                            dg[e] = dh * b * slope;
+                            du[e] = dh * act;
+                            cs[c] += dg[e];
+                            cs[4 + c] += du[e];
                         }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = __uint_as_float(vg[j + e]), b = __uint_as_float(vu[j + e]);
-                            if constexpr (C::kQ8)
-                                h[e] = Act<ACT>::hidden(fmaf(a, xs * sg[e], bg[e]), fmaf(b, xs * su[e], bu[e]));
-                            else
-                                h[e] = Act<ACT>::hidden(fmaf(a, Act<ACT>::kGate, bg[e]), fmaf(b, Act<ACT>::kUp, bu[e]));
-                        }
-                        w[j / 2] = pack_bf16(h[0], h[1]);
-                        w[j / 2 + 1] = pack_bf16(h[2], h[3]);
+                        w[0][j / 2] = pack_bf16(h[0], h[1]);
+                        w[1][j / 2] = pack_bf16(dg[0], dg[1]);
+                        w[2][j / 2] = pack_bf16(du[0], du[1]);
                     }
-                    uint8_t *sb = tile_s + (c / 64) * kBox;
-                    const int u = (c % 64) / 8;
-                    *reinterpret_cast<uint4 *>(sb + swizzled(r, u)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(sb + swizzled(r, u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+                    for (int o = 0; o < 3; ++o)
+                        store_frags(at0 + (uint32_t)(o * kBox + q * 16 * 128), w[o][0], w[o][1], w[o][2], w[o][3]);
                 }
-            } else if constexpr (KIND == kHidden) {
-                uint32_t vg[16], vu[16], vd[16];
-                tmem_ld16(t0 + (uint32_t)cp, vg);
-                tmem_ld16(t0 + (uint32_t)(64 + cp), vu);
-                tmem_ld16(t0 + (uint32_t)(128 + cp), vd);
-                tmem_wait();
-                pin(vg);
-                pin(vu);
-                pin(vd);
-                uint32_t wo[3][8];
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    float bg[4], bu[4], h[4], dg[4], du[4];
-                    four(bg, v0 + cp + j);
-                    four(bu, v1 + cp + j);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float b = __uint_as_float(vu[j + e]) + bu[e], dh = __uint_as_float(vd[j + e]);
-                        float slope;
-                        const float act = Act<ACT>::fast(__uint_as_float(vg[j + e]) + bg[e], &slope);
-                        h[e] = act * b;
-                        dg[e] = dh * b * slope;
-                        du[e] = dh * act;
-                    }
-                    if (p.sums)
-                        add_column_sums(p.sums + (size_t)(blockIdx.x * 4 + quarter) * 2 * p.F, dg, du, c0 + cp + j, p.F, lane);
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        wo[0][(j + e) / 2] = pack_bf16(h[e], h[e + 1]);
-                        wo[1][(j + e) / 2] = pack_bf16(dg[e], dg[e + 1]);
-                        wo[2][(j + e) / 2] = pack_bf16(du[e], du[e + 1]);
-                    }
-                }
-#pragma unroll
-                for (int o = 0; o < 3; ++o) {
-                    const uint32_t(&w)[8] = wo[o];
-                    uint8_t *sb = tile_s + o * kBox;
-                    *reinterpret_cast<uint4 *>(sb + swizzled(r, cp / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(sb + swizzled(r, cp / 8 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
-                }
+                if (p.sums)
+                    add_column_sums(p.sums + (size_t)(blockIdx.x * 4 + quarter) * 2 * p.F, cs, c0 + cp, p.F, lane);
             } else {
 #pragma unroll 1
                 for (int c = cp; c < cp + C::kPart; c += 16) {
@@ -571,39 +568,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_ffn(c
 
 // ---------------------------------------------------------------- host side
 
-// Pairs that run at once on the current device for this kernel.
-template <typename K>
-pmha_status configure(K kern, int smem, int *pairs)
-{
-    static std::mutex mu;
-    static std::map<std::pair<int, void *>, int> known;
-    int dev = 0;
-    PMHA_CUDA_TRY(cudaGetDevice(&dev));
-    std::lock_guard<std::mutex> lk(mu);
-    const auto it = known.find({dev, (void *)kern});
-    if (it != known.end()) {
-        *pairs = it->second;
-        return PMHA_OK;
-    }
-    PMHA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 2;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    PMHA_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
-    n = std::max(1, std::min(n, num_sms() / 2));
-    known[{dev, (void *)kern}] = n;
-    *pairs = n;
-    return PMHA_OK;
-}
-
 template <int KIND, int BN, int ACT>
 pmha_status launch(Params &p, const char *stage, cudaStream_t s)
 {
@@ -612,7 +576,8 @@ pmha_status launch(Params &p, const char *stage, cudaStream_t s)
     if (!p.err) return PMHA_ERR_CUDA;
     int pairs = 0;
     auto kern = k_ffn<KIND, BN, ACT>;
-    const pmha_status st = configure(kern, C::kSmem, &pairs);
+    static std::atomic<int> known[kKnownDevices];
+    const pmha_status st = pairs_at_once(kern, kThreads, C::kSmem, known, &pairs);
     if (st != PMHA_OK) return st;
     StageTimer timer(stage, s);
     return launch_overlapping(kern, dim3(2u * (unsigned)std::min(pairs, p.n_tiles)), kThreads, C::kSmem, s, p);
@@ -749,7 +714,6 @@ pmha_status ffn_tc_dw(const FfnTc &f, const FfnDwArgs &a, cudaStream_t s)
     p.kb = (int)ceil_div(a.M, 64);
     p.part = a.part;
     p.sums = a.sums;
-    p.row_sums = a.sums && a.row_sums;
     p.accumulate = a.accumulate;
     if (!make_tile_map(&p.a0, a.dg, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.a1, a.du, a.M, f.F, f.F, 2, 64) ||
         !make_tile_map(&p.a2, a.h, a.M, f.F, f.F, 2, 64) || !make_tile_map(&p.b0, a.x, a.M, f.E, f.E, 2, 64) ||

@@ -5,6 +5,8 @@
 // the products; its barriers count the copies and arrivals of both.
 #pragma once
 
+#include <atomic>
+
 #include "tc_util.cuh"
 
 namespace pmha {
@@ -128,6 +130,18 @@ __host__ __device__ constexpr uint32_t idesc_of(bool q8, bool mn_major, int m, i
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// 16 accumulator columns of this warp's 32 rows
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_store_tile(const CUtensorMap *map, uint32_t src, int x, int y)
 {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -137,21 +151,9 @@ __device__ __forceinline__ void tma_store_tile(const CUtensorMap *map, uint32_t 
 }
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// named barrier 1 + g over 128 threads, returning whether any of them passed `pred`
-__device__ __forceinline__ bool group_sync_or(int g, bool pred)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)pred), "r"(1 + g)
-        : "memory");
-    return r != 0;
-}
+// named barrier 1 + g over 128 threads
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
@@ -159,9 +161,38 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&h);
 }
-// Sums of eight values over the warp's 32 lanes; lane l returns that of value
-// (l / 4) % 8.
-__device__ __forceinline__ float sum8_over_lanes(float (&v)[8], int lane)
+// 16 rows (taddr's lane and on) x 16 accumulator columns, eight values a lane,
+// spread like the result of a warp's matrix product: with g = lane / 4, t = lane % 4,
+// r[4 c + 2 h + e] is row g + 8 h, column 8 c + 2 t + e. A lane so holds four
+// columns of several rows: column sums are mostly its own additions, and it
+// needs four columns' biases instead of sixteen.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values in that layout (two columns a register)
+// to shared memory; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_frags(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+// The values of columns 2 t, 2 t + 1, 8 + 2 t, 9 + 2 t; p is at the first.
+__device__ __forceinline__ void two_pairs(float (&f)[4], const float *p)
+{
+    const float2 a = *reinterpret_cast<const float2 *>(p), b = *reinterpret_cast<const float2 *>(p + 8);
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+// Adds the sums over a warp's rows of 16 columns' dg and du (float32, before
+// their rounding: the bias gradients) to this warp's row of partial sums, [2][F]
+// from `sums`, columns col .. col + 15. v: the lane's own sums, dg's columns
+// 8 c + 2 t + e at v[2 c + e], du's four further. One warp owns each value, so the
+// additions' order is fixed, and they need no read.
+__device__ __forceinline__ void add_column_sums(float *sums, float (&v)[8], int col, int F, int lane)
 {
 #pragma unroll
     for (int h = 4, o = 16; h > 0; h >>= 1, o >>= 1)
@@ -171,19 +202,9 @@ __device__ __forceinline__ float sum8_over_lanes(float (&v)[8], int lane)
             const float keep = up ? v[i + h] : v[i], send = up ? v[i] : v[i + h];
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
-    float s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 2);
-    return s + __shfl_xor_sync(0xffffffffu, s, 1);
-}
-// Adds the column sums over a warp's 32 rows of four columns' dg and du (float32, before their rounding: the bias
-// gradients) to this warp's row of partial sums, [2][F] from `sums`. One warp owns each value, so the additions' order
-// is fixed, and they need no read.
-__device__ __forceinline__ void add_column_sums(float *sums, const float (&dg)[4], const float (&du)[4], int col, int F, int lane)
-{
-    float v[8] = {dg[0], dg[1], dg[2], dg[3], du[0], du[1], du[2], du[3]};
-    const float s = sum8_over_lanes(v, lane);
-    const int i = (lane >> 2) & 7, c = col + (i & 3);
-    if ((lane & 3) == 0 && c < F)
-        asm volatile("red.global.add.f32 [%0], %1;" ::"l"(sums + (size_t)(i >> 2) * F + c), "f"(s) : "memory");
+    const int i = lane >> 2, c = col + ((i >> 1) & 1) * 8 + 2 * (lane & 3) + (i & 1);
+    if (c < F)
+        asm volatile("red.global.add.f32 [%0], %1;" ::"l"(sums + (i >= 4 ? (size_t)F : 0) + c), "f"(v[0]) : "memory");
 }
 
 // 16-byte unit u (0..7) of row r of a 128-byte-wide tile with 128-byte swizzle
@@ -206,6 +227,36 @@ pmha_status launch_overlapping(void (*kern)(P), dim3 grid, int threads, int smem
     cfg.numAttrs = 1;
     PMHA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p));
     count_launch();
+    return PMHA_OK;
+}
+
+// Pairs of `threads`-thread CTAs with `smem` bytes that run at once on the
+// current device, and the kernel's permission to use that much shared memory.
+// `known` holds the answer for the first devices; two threads that ask at once
+// both find it.
+constexpr int kKnownDevices = 64;
+template <typename P>
+pmha_status pairs_at_once(void (*kern)(P), int threads, int smem, std::atomic<int> (&known)[kKnownDevices], int *pairs)
+{
+    int dev = 0;
+    PMHA_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < kKnownDevices && (*pairs = known[dev].load(std::memory_order_acquire)) > 0) return PMHA_OK;
+    PMHA_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    PMHA_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
+    const int most = num_sms() / 2;
+    *pairs = n < 1 ? 1 : n < most ? n : most;
+    if (dev < kKnownDevices) known[dev].store(*pairs, std::memory_order_release);
     return PMHA_OK;
 }
 

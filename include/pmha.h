@@ -27,9 +27,13 @@
  *    unless stated. Every call returns a pmha_status; on failure
  *    pmha_last_error() gives a message for the calling thread. A failing call
  *    writes nothing to its outputs unless it says otherwise.
- *  - Nothing in this library waits on another CTA or launch inside a kernel;
- *    the only bounded device-side waits are the tensor-core GEMM's pipeline
- *    barriers, which give up with PMHA_ERR_TIMEOUT (see pmha_device_status).
+ *  - No kernel waits on another launch, and none on another CTA but the
+ *    tensor-core kernels of the gated block, whose CTAs work in clusters of
+ *    two (which the GPU starts together). Every device-side wait is on a
+ *    pipeline barrier and bounded: it gives up with PMHA_ERR_TIMEOUT (see
+ *    pmha_device_status).
+ *  - A workspace holds intermediate values of one call. Calls, or replays of
+ *    captured graphs, that may run at the same time need one each.
  */
 #ifndef PMHA_H
 #define PMHA_H
@@ -343,7 +347,8 @@ pmha_status pmha_graph_export_by_source(const pmha_graph *graph, int32_t *src_ro
  *          float32), whatever the order of its sums, for rows whose
  *          squares are not below float32's normal numbers. A row with an
  *          infinity or a NaN gets a NaN scale and NaN bytes.
- * Statistics are float32; a row whose squares leave float32 is scaled first. Asynchronous; needs no workspace.
+ * Statistics are float32; a row whose squares leave float32 is scaled first.
+ * Needs no workspace.
  * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_CUDA.
  */
 pmha_status pmha_rms_norm(pmha_dtype dtype, int64_t rows, int64_t width, const void *x, const void *residual,
@@ -393,9 +398,12 @@ typedef struct {
  *  out          device (rows, E).
  *  workspace    pmha_ffn_forward_workspace_size() bytes, 256-byte aligned
  *               (0 bytes, and workspace may be NULL, for some sizes; the
- *               size function returns SIZE_MAX for invalid arguments).
- * Sums are float32. A bf16 block rounds the hidden row act(.) * (.) to bf16
- * between its products, a float32 block keeps float32.
+ *               size function returns SIZE_MAX for invalid arguments). The
+ *               size never shrinks as rows grow: one for the largest batch
+ *               serves every smaller one. So for the backward pass.
+ * Sums are float32. A bf16 block of more than 64 tokens rounds the hidden row
+ * act(.) * (.) to bf16 between its products (what the tensor cores take); for
+ * fewer tokens, and in a float32 block, it stays float32.
  * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
  */
 size_t pmha_ffn_forward_workspace_size(const pmha_ffn_params *params, int64_t rows);
@@ -429,13 +437,15 @@ pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha
  *  dx      device (rows, E) in dtype, or NULL.
  *  grads   parameter gradients in dtype, any member NULL to skip it, NULL
  *          skips all; written, not accumulated. The sums are float32, in a
- *          fixed order (deterministic), and rounded to dtype once: a bf16
- *          block's products take the hidden gradients rounded to bf16, so
- *          float32 results would carry no more.
+ *          fixed order (deterministic), and rounded to dtype once. A bf16
+ *          block with many rows (rows * E * F above 2^21 and rows * E above 2^11) rounds
+ *          the hidden values and their gradients to bf16 for the products
+ *          that take them, not for the biases' sums; one with few keeps
+ *          them float32.
  *  workspace  pmha_ffn_backward_workspace_size() bytes, 256-byte aligned
- *          (SIZE_MAX when the arguments are invalid). Its size does not grow
- *          with rows past some tens of MB: rows are taken in blocks whose
- *          hidden gradients stay in L2.
+ *          (SIZE_MAX when the arguments are invalid). It holds the hidden
+ *          values and gradients of at most 2 GiB's worth of rows, which are
+ *          taken in blocks: past that its size does not grow with rows.
  * Errors as pmha_ffn_forward.
  */
 typedef struct {

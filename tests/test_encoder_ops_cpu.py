@@ -192,3 +192,14 @@ def test_quantize_rows():
     # half a step of 4 significant bits, below 2^-6 half a step of 2^-9
     back = q.float() * s[:, None]
     assert bool(((back - w).abs() <= 2.0 ** -4 * w.abs() + 2.0 ** -10 * s[:, None]).all())
+
+
+@pytest.mark.parametrize("E,F", [(1, 1), (5, 7), (64, 72), (256, 1024), (1032, 200)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_a_workspace_for_many_rows_serves_fewer(lib, E, F, dtype):
+    rows = sorted({1, 2, 16, 63, 64, 65, 100, 256, 257, 1000, 2047, 2048, 2049, 100_000, 1_000_000,
+                   *(max(1, n // (E * F) + d) for n in (2048 * F, 1 << 21) for d in (-1, 0, 1))})
+    b = ctypes.byref(ffn(E=E, F=F, dtype=dtype))
+    for size in (lib.pmha_ffn_forward_workspace_size, lib.pmha_ffn_backward_workspace_size):
+        n = [size(b, r) for r in rows]
+        assert n == sorted(n)

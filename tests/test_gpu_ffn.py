@@ -73,7 +73,7 @@ def test_forward_f32(rows, E, F):
     check_forward(rows, E, F, F32, act="gelu")
 
 
-# past the small problems that run in float32: both ways of the bias sums, fused or not, padded widths, K tails
+# past the small problems that run in float32: fused or not, padded widths, K tails
 BIG = [(40000, 64, 64), (30000, 136, 264), (9000, 320, 72), (5000, 192, 520), (12001, 256, 600), (20011, 100, 171),
        (3000, 328, 1032)]
 
@@ -92,7 +92,7 @@ def test_backward_f32(rows, E, F):
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_more_rows_than_a_block(dtype):
-    # hidden rows past the block of rows that stays in L2: several rounds, sums carried on
+    # many rows of a wide block (test_gpu_ffn_precision.py has those of several blocks of rows)
     check_forward(9000 if dtype == BF16 else 5000, 32, 4096, dtype)
     check_backward(4500, 32, 4096, dtype)
 
