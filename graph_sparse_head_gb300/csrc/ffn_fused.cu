@@ -3,7 +3,7 @@
 // its tokens stay in shared memory while the hidden width passes in chunks of
 // 64 columns, whose weights stream through two rings of TMA stages.
 //
-//   forward, chunk c:   S = x [Wg_c | Wu_c]^T           tensor memory, two or three buffers
+//   forward, chunk c:   S = x [Wg_c | Wu_c]^T           tensor memory, two buffers
 //                       h = act(S_g + bg) * (S_u + bu)   -> shared memory, bf16
 //                       Y += h Wd_c^T                    tensor memory
 //   after the last:     y = Y + bd + residual
@@ -17,19 +17,23 @@
 // read once. The warps are specialised: warp 0 copies, warp 1 of the even CTA
 // issues the products, sixteen warps turn S into hidden values, and four drain
 // the row block's result while the next block's chunks go on. The issuer runs S
-// as many chunks ahead as there are buffers, across row blocks: S(0) S(1) S(2) |
-// Y(0) S(3) | Y(1) S(4) ... A chunk's time is that of a loop, S -> epilogue -> Y
-// and the next S of the buffer, over the buffers; what was measured on the way
-// (cycles a chunk of 64 columns, embed_dim 128, where the products take 770):
+// two chunks ahead, across row blocks: S(0) S(1) | S(2) Y(0) | S(3) Y(1) ... A
+// chunk's time is that of a loop, S -> epilogue -> Y and the next S of the
+// buffer, over the buffers; what was measured on the way (cycles a chunk of 64
+// columns, embed_dim 128, where the products take 770):
 // waits with cluster-scope acquires and one wait and commit for each stage
 // 3,100; one commit a step, waits for what is long loaded taken first, the
 // issuing warp converged (uniform addresses) and the epilogue rolled, so that
 // the warps share the instruction cache, 2,000; sixteen epilogue warps instead
 // of eight 1,440 to 1,640; the result through TMA instead of 32-byte accesses (a
-// warp's 32 rows cost the memory pipe 32 cycles an instruction) and a third
-// S buffer about 1,350, of which two special-function results a value take 1,024.
-// 320,000 rows of embed_dim 128, 512 hidden: forward 125 us (126 GFLOP: 1.01
-// PFLOP/s, 53 % of cuBLAS bf16), backward 246 of the 443 us of its pass.
+// warp's 32 rows cost the memory pipe 32 cycles an instruction) 1,350; the
+// accumulators read as fragments (fewer bias loads), a second accumulator of the
+// result instead of a third of S (with one the next row block's first Y waits
+// for the drain) and a third Y stage 1,200. Slower were: reads of the next eight
+// columns under this eight's arithmetic, the wait for the staged tile after the
+// arithmetic (both some 5 %), and Y before S (10 %).
+// 320,000 rows of embed_dim 128, 512 hidden: forward 109 us (126 GFLOP: 1.15
+// PFLOP/s, 61 % of cuBLAS bf16), backward 250 of the 440 us of its pass.
 //
 // Every wait is bounded; after an expired one the waits return at once, the
 // loops run out, and pmha_device_status reports PMHA_ERR_TIMEOUT.
@@ -52,14 +56,14 @@ template <int EB, bool BWD, bool Q8>
 struct Cfg {
     static constexpr int KB = Q8 ? (EB + 1) / 2 : EB;
     static constexpr bool kOut = !BWD || EB <= 2;               // the kernel forms y, or dx
-    static constexpr int SB = !BWD && EB <= 2 ? 3 : 2;          // S buffers in tensor memory
+    static constexpr int SB = 2;                                // S buffers in tensor memory
     static constexpr int kX = (BWD ? 2 : 1) * KB * kBox;        // x (and dy) of a row block
     static constexpr int kSBlock = BWD ? 12288 : 8192;          // 64 rows of Wg or Wu (and 32 of Wd^T), one K block
     static constexpr int SG = BWD ? 1 : !Q8 && EB == 4 ? 2 : KB;        // K blocks of a stage of the S ring
     static constexpr int kSSlot = SG * kSBlock;
     static constexpr int kYSlot = kOut ? EB * (BWD ? 8192 : 4096) : 0;  // half of the output columns of a chunk
-    static constexpr int kNY = !kOut ? 0 : SB == 3 ? 3 : 2;
-    static constexpr int kMaxHidden = !BWD && !Q8 && EB == 2 ? 1024 : 2048;  // bias (and scale) columns held
+    static constexpr int kNY = !kOut ? 0 : !BWD && EB <= 2 ? 3 : 2;
+    static constexpr int kMaxHidden = 2048;                     // bias (and scale) columns held
     static constexpr int kStaged = BWD ? 3 * kBox : kBox;       // dg, du and h, or h
     static constexpr int kStages = BWD ? 1 : SB;
     static constexpr int kOT = BWD ? 1 : 2;                     // tiles of 64 result columns
@@ -718,8 +722,7 @@ pmha_status launch_width(pmha_act act, Params &p, const char *stage, cudaStream_
 
 bool ffn_fused_supported(int64_t E, int64_t F, bool backward, bool q8)
 {
-    const bool two = E > 64 && E <= 128 && !backward && !q8;
-    return E <= 256 && F <= (two ? Cfg<2, false, false>::kMaxHidden : Cfg<1, false, false>::kMaxHidden);
+    return E <= 256 && F <= Cfg<1, false, false>::kMaxHidden;
 }
 bool ffn_fused_dx(int64_t E) { return E <= 128; }
 

@@ -27,10 +27,9 @@ __device__ __forceinline__ float rcp(float x)
 // The fast forms take the gate and the other factor times constants (kGate,
 // kUp) that the caller folds into scales and biases: with the gate times
 // -log2(e) the exponential needs no product of its own, and -ln(2) on the other
-// side undoes it. Two special-function results a value (16 a clock and SM: 128 x
-// 64 values take 1,024 clocks) and seven other instructions, which is what
-// decides a chunk's time; packed float32 pairs and one reciprocal for two
-// values were measured slower (register moves: 15 instructions a value).
+// side undoes it: two special-function results and seven other instructions a
+// value. Packed float32 pairs and one reciprocal for two values were measured
+// slower (register moves: 15 instructions a value).
 template <int ACT>
 struct Act;
 
