@@ -23,7 +23,18 @@ namespace pmha {
 namespace {
 
 constexpr int64_t kBlock = (int64_t)2 << 30;   // bytes of hidden values (h, or h, dg and du) of a block of rows
-constexpr int64_t kFusedRows = 2048;    // rows from which the forward pass runs as one kernel
+// Rows from which the forward pass runs as one kernel, whose pairs of SMs take
+// 256 rows each through the whole hidden width, while the two products deal
+// tiles of that width out too. Measured (us, one kernel / two): 64 x 256 at 100
+// rows 6.9 / 8.6, 128 x 512 at 2,000 rows 11.0 / 10.3 and at 10,000 11.4 / 13.4,
+// 128 x 1,024 at 4,096 16.3 / 13.1 and at 10,000 16.9 / 17.5, 256 x 1,024 at
+// 10,000 22.8 / 21.2 and at 19,000 23.9 / 27.0, 256 x 2,048 at 10,000 37.3 / 31.4 and
+// at 19,000 38.7 / 47.9.
+int64_t fused_rows(int64_t E, int64_t F)
+{
+    if (E * F <= 1 << 14) return 1;
+    return std::min<int64_t>(16384, F * (E > 128 ? 12 : 8));
+}
 // rows * E * F up to which a bf16 block's backward pass runs on float32 copies
 // and the CUDA cores, without the rounding of the hidden gradients to bf16,
 // which few values do not average out. Both wait for launches there: 64 x 128 at
@@ -342,7 +353,7 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
     l.small = bf16 && !backward && ffn_small_supported(p->embed_dim, rows, q8);
     if (l.small) l.E2 = p->embed_dim, l.F2 = p->hidden_dim;
     l.padded = l.E2 != p->embed_dim || l.F2 != p->hidden_dim;
-    l.fused = bf16 && ffn_fused_supported(l.E2, l.F2, backward, q8) && (backward || rows >= kFusedRows);
+    l.fused = bf16 && !l.small && ffn_fused_supported(l.E2, l.F2) && (backward || rows >= fused_rows(l.E2, l.F2));
     const int64_t per_row = l.F2 * (int64_t)es * (backward ? 3 : 1);
     // a whole number of times 256 rows for each pair of SMs, where there are that many
     const int64_t wave = 256 * (int64_t)(num_sms() / 2);
@@ -396,13 +407,14 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
 // sizes its workspace once can run every smaller batch in it. The paths for
 // fewer rows may take more than the one for many (float32 hidden rows of a few
 // tokens, the float32 backward pass of small problems, hidden rows in memory
-// below kFusedRows); within a path the size grows with the rows.
+// below fused_rows()); within a path the size grows with the rows.
 size_t most_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
 {
     if (!rows) return 0;
     const int64_t few = std::max(kFewWork / p->hidden_dim, kFewOut) / p->embed_dim;
     size_t n = 0;
-    for (const int64_t r : {rows, backward ? few : kSmallRows, kFusedRows - 1})
+    const int64_t tiled = fused_rows(round8(p->embed_dim), round8(p->hidden_dim)) - 1;
+    for (const int64_t r : {rows, backward ? few : kSmallRows, tiled})
         if (r > 0 && r <= rows) n = std::max(n, plan_of(p, r, backward, q8).total);
     return n;
 }

@@ -720,7 +720,7 @@ pmha_status launch_width(pmha_act act, Params &p, const char *stage, cudaStream_
 
 }  // namespace
 
-bool ffn_fused_supported(int64_t E, int64_t F, bool backward, bool q8)
+bool ffn_fused_supported(int64_t E, int64_t F)
 {
     return E <= 256 && F <= Cfg<1, false, false>::kMaxHidden;
 }

@@ -27,7 +27,7 @@ pmha_status ffn_tc_up(const FfnTc &f, const FfnUpArgs &a, cudaStream_t s);
 pmha_status ffn_tc_down(const FfnTc &f, const void *h, const void *wd, const void *residual, int64_t M, void *out,
                         cudaStream_t s);
 // The whole forward in one kernel, the hidden rows on the chip (ffn_fused.cu).
-bool ffn_fused_supported(int64_t E, int64_t F, bool backward, bool q8);
+bool ffn_fused_supported(int64_t E, int64_t F);
 pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
                               cudaStream_t s);
 // The same for a few tokens, on the CUDA cores (ffn_small.cu); any widths.

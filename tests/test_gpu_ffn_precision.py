@@ -5,6 +5,7 @@ import torch
 
 import graph_sparse_head_gb300 as pmha
 from tests import _encoder_ref as ref
+from tests import test_gpu_ffn as plain
 from tests.test_gpu_ffn import BF16, DEV, F32, block, make
 
 pytestmark = pytest.mark.gpu
@@ -145,3 +146,23 @@ def test_captured_and_replayed(rows, E, F):
         w = pmha.pmha_ffn_backward(p, a, b)
         assert all(torch.equal(g[n], w[n]) for n in w)
     pmha.pmha_device_status()
+
+
+# the kernel that keeps the hidden rows on the chip, at every embed_dim it has, with ragged ends and short and long
+# hidden widths (it runs from some rows on: fewer for narrow blocks), each with a second round of row blocks
+CHIP = [(70, 64, 128), (300, 40, 264), (5000, 128, 264), (16500, 72, 2048), (41000, 128, 136), (4000, 192, 264),
+        (20001, 136, 1032), (4100, 256, 320), (16400, 256, 2048), (25000, 200, 72)]
+
+
+@pytest.mark.parametrize("rows,E,F", CHIP)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_forward_on_the_chip(rows, E, F, act):
+    plain.check_forward(rows, E, F, BF16, bias=True, act=act, residual=rows % 2 == 0)
+    plain.check_forward(rows, E, F, BF16, bias=False, act=act, residual=rows % 2 == 1)
+
+
+@pytest.mark.parametrize("rows,E,F", [(70, 64, 128), (5000, 128, 264), (16500, 80, 2048), (4000, 192, 264),
+                                      (20001, 144, 1032), (41000, 256, 72)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_quantized_on_the_chip(rows, E, F, act):
+    plain.test_forward_quantized(rows, E, F, act)
