@@ -78,14 +78,15 @@ __global__ void __launch_bounds__(256) k_widen(Widen w)
         for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < w.n[a]; i += (int64_t)gridDim.x * 256)
             w.out[a][i] = __bfloat162float(w.in[a][i]);
 }
-// out = the sum of `parts` float32 arrays, n apart, as bf16
-__global__ void __launch_bounds__(256) k_narrow(const float *in, int64_t n, int parts, __nv_bfloat16 *out)
+// out = the sum of `parts` float32 arrays, n apart
+template <typename T>
+__global__ void __launch_bounds__(256) k_narrow(const float *in, int64_t n, int parts, T *out)
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         float v = 0.f;
 #pragma unroll 4
         for (int k = 0; k < parts; ++k) v += in[k * n + i];
-        out[i] = __float2bfloat16_rn(v);
+        out[i] = from_f<T>(v);
     }
 }
 
@@ -350,7 +351,7 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
     const size_t es = bf16 ? 2 : 4;
     l.E2 = bf16 ? round8(p->embed_dim) : p->embed_dim;
     l.F2 = bf16 ? round8(p->hidden_dim) : p->hidden_dim;
-    l.small = bf16 && !backward && ffn_small_supported(p->embed_dim, rows, q8);
+    l.small = !backward && ffn_small_supported(p->embed_dim, rows, q8 ? 1 : (int)es);
     if (l.small) l.E2 = p->embed_dim, l.F2 = p->hidden_dim;
     l.padded = l.E2 != p->embed_dim || l.F2 != p->hidden_dim;
     l.fused = bf16 && !l.small && ffn_fused_supported(l.E2, l.F2) && (backward || rows >= fused_rows(l.E2, l.F2));
@@ -372,7 +373,7 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
         l.bg = take(l.F2), l.bu = take(l.F2), l.bd = take(l.E2);
         l.x = take(l.R * l.E2), l.dy = take(l.R * l.E2), l.out = take(l.R * l.E2);
     }
-    if (backward || !l.fused) l.h = take(l.R * l.F2 * (l.small ? 2 : 1));  // float32 for a few tokens
+    if (backward || !l.fused) l.h = take(l.R * l.F2 * (l.small && bf16 ? 2 : 1));  // float32 for a few tokens
     if (backward) {
         l.dg = take(l.R * l.F2), l.du = take(l.R * l.F2);
         if (bf16) l.wgt = take(l.E2 * l.F2), l.wut = take(l.E2 * l.F2), l.wdt = take(l.E2 * l.F2);
@@ -390,11 +391,13 @@ Plan plan_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
         l.sums = o;
         l.sum_rows = bf16 ? ffn_hidden_parts(block, l.F2) : 0;
         o += align256((size_t)l.sum_rows * (size_t)(2 * l.F2) * 4);
+        l.dx_parts = 1;
+        if (!bf16) {  // dx in parts, of at most a tile of 64 x 32 for each SM
+            l.dx_parts = ffn_f32_dx_parts(l.E2, l.F2, block);
+            l.f_dx = take(std::max<int64_t>(l.few ? l.R * l.E2 : 0, (int64_t)num_sms() * 64 * 32));
+        }
         if (l.few) {
             l.f_x = take(l.R * l.E2), l.f_dy = take(l.R * l.E2);
-            // dx in parts, of at most a tile of 64 x 32 for each SM
-            l.dx_parts = ffn_f32_dx_parts(l.E2, l.F2, block);
-            l.f_dx = take(std::max<int64_t>(l.R * l.E2, (int64_t)num_sms() * 64 * 32));
             for (size_t &w : l.f_w) w = take(l.E2 * l.F2);
             for (size_t &w : l.f_b) w = take(l.F2);
         }
@@ -414,7 +417,7 @@ size_t most_of(const pmha_ffn_params *p, int64_t rows, bool backward, bool q8)
     const int64_t few = std::max(kFewWork / p->hidden_dim, kFewOut) / p->embed_dim;
     size_t n = 0;
     const int64_t tiled = fused_rows(round8(p->embed_dim), round8(p->hidden_dim)) - 1;
-    for (const int64_t r : {rows, backward ? few : kSmallRows, tiled})
+    for (const int64_t r : {rows, backward ? few : 1, tiled})
         if (r > 0 && r <= rows) n = std::max(n, plan_of(p, r, backward, q8).total);
     return n;
 }
@@ -508,7 +511,7 @@ pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_qu
         const char *xr = (const char *)x + (size_t)(r * E) * (q8 ? 1 : es);
         const char *rr = residual ? (const char *)residual + (size_t)(r * E) * es : nullptr;
         char *yr = (char *)out + (size_t)(r * E) * es;
-        if (p->dtype == PMHA_F32) {
+        if (p->dtype == PMHA_F32 && !l.small) {
             FfnF32Args a = {};
             a.x = (const float *)xr, a.wg = (const float *)p->wg, a.wu = (const float *)p->wu;
             a.wd = (const float *)p->wd, a.bg = (const float *)p->bg, a.bu = (const float *)p->bu;
@@ -535,7 +538,7 @@ pmha_status forward(const char *who, const pmha_ffn_params *p, const pmha_ffn_qu
         up.M = M;
         up.h = ws + l.h;
         if (l.small) {
-            PMHA_TRY(ffn_small_forward(tc, up, q.wd, rp, yp, s));
+            PMHA_TRY(ffn_small_forward(tc, p->dtype == PMHA_F32, up, q.wd, rp, yp, s));
         } else if (l.fused) {
             PMHA_TRY(ffn_fused_forward(tc, up, q.wd, rp, yp, s));
         } else {
@@ -691,7 +694,6 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
             for (int i = 0; i < (first ? 7 : 2); ++i)
                 if (in[i]) w.in[i] = (const __nv_bfloat16 *)in[i], w.out[i] = (float *)(ws + at[i]), w.n[i] = n[i];
             xr = ws + l.f_x, dyr = ws + l.f_dy;
-            if (dx) dxr = ws + l.f_dx;
             StageTimer timer("ffn_widen", s);
             k_widen<<<grid_of(std::max(E * F, M * E)), 256, 0, s>>>(w);
             PMHA_TRY(launched());
@@ -719,13 +721,15 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 PMHA_TRY(ffn_tc_dw(tc, d, s));
             }
         } else {
+            const bool sum_dx = dx && (l.few || l.dx_parts > 1);
+            if (sum_dx) dxr = ws + l.f_dx;
             FfnF32Args a = {};
             a.x = (const float *)xr, a.dy = (const float *)dyr, a.wg = (const float *)q.wg;
             a.wu = (const float *)q.wu, a.wd = (const float *)q.wd, a.bg = (const float *)q.bg;
             a.bu = (const float *)q.bu, a.h = (float *)(ws + l.h), a.dg = (float *)(ws + l.dg);
             a.du = (float *)(ws + l.du), a.out = (float *)dxr, a.M = M, a.E = E, a.F = F;
             PMHA_TRY(ffn_f32_hidden(p->act, a, true, s));
-            if (dx) PMHA_TRY(ffn_f32_dx(a, l.few ? l.dx_parts : 1, s));
+            if (dx) PMHA_TRY(ffn_f32_dx(a, l.dx_parts, s));
             if (any_w) PMHA_TRY(ffn_f32_dw(a, part, l.splits, !first, s));
             if (any_b) {
                 Sums c = {};
@@ -738,9 +742,11 @@ pmha_status pmha_ffn_backward(const pmha_ffn_params *params, const void *x, cons
                 k_colsum<<<dim3((unsigned)ceil_div(std::max(E, F), 32), (unsigned)l.sum_parts, 3), 256, 0, s>>>(c);
                 PMHA_TRY(launched());
             }
-            if (l.few && dx) {
-                StageTimer timer("ffn_narrow", s);
-                k_narrow<<<grid_of(M * E), 256, 0, s>>>((const float *)dxr, M * E, l.dx_parts, (__nv_bfloat16 *)dx_out);
+            if (sum_dx) {
+                StageTimer timer("ffn_dx_sum", s);
+                const float *in = (const float *)dxr;
+                if (l.few) k_narrow<<<grid_of(M * E), 256, 0, s>>>(in, M * E, l.dx_parts, (__nv_bfloat16 *)dx_out);
+                else k_narrow<<<grid_of(M * E), 256, 0, s>>>(in, M * E, l.dx_parts, (float *)dx_out);
                 PMHA_TRY(launched());
             }
         }

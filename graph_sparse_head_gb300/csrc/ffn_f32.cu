@@ -331,7 +331,7 @@ pmha_status ffn_f32_down(const FfnF32Args &a, cudaStream_t s)
 
 int ffn_f32_dx_parts(int64_t E, int64_t F, int64_t rows)
 {
-    // pieces of 64 hidden columns or more, until every SM has a tile of 64 x 32
+    // pieces of 64 hidden columns or more, until every SM has a tile of 64 x 32 (512 x 1,024, 2 rows: 73 -> 14 us)
     return (int)std::max<int64_t>(1, std::min(ceil_div(F, 64), num_sms() / (ceil_div(rows, 64) * ceil_div(E, 32))));
 }
 

@@ -30,11 +30,10 @@ pmha_status ffn_tc_down(const FfnTc &f, const void *h, const void *wd, const voi
 bool ffn_fused_supported(int64_t E, int64_t F);
 pmha_status ffn_fused_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
                               cudaStream_t s);
-// The same for a few tokens, on the CUDA cores (ffn_small.cu); any widths.
-constexpr int64_t kSmallRows = 64;
-bool ffn_small_supported(int64_t E, int64_t M, bool q8);
-pmha_status ffn_small_forward(const FfnTc &f, const FfnUpArgs &a, const void *wd, const void *residual, void *out,
-                              cudaStream_t s);
+// The same for a few tokens, on the CUDA cores (ffn_small.cu); any widths, float32 too.
+bool ffn_small_supported(int64_t E, int64_t M, int token_bytes);
+pmha_status ffn_small_forward(const FfnTc &f, bool f32, const FfnUpArgs &a, const void *wd, const void *residual,
+                              void *out, cudaStream_t s);
 // h, dg, du (M, F): the hidden row and the gradients of gate and up, from x,
 // dout and wd_t (F, E) = Wd transposed
 struct FfnHiddenArgs {

@@ -6,6 +6,8 @@
 // second comes up and loads its weights while the first one runs.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "ffn_internal.h"
 #include "ffn_math.cuh"
 #include "tc_pair.cuh"
@@ -17,41 +19,52 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr unsigned kFull = 0xffffffffu;
 
+// Type of the tokens and of the gate and up weights (E4M3 ones have scales); the rest of a block is float32 or bf16.
+enum Kind { kBf16, kE4m3, kF32 };
+template <int KIND>
+constexpr int kBytesOf = KIND == kF32 ? 4 : KIND == kE4m3 ? 1 : 2;
+
 struct SmallArgs {
     const void *x, *wg, *wu;
     const float *xs, *gs, *us;
-    const __nv_bfloat16 *wd, *bg, *bu, *bd, *res;
+    const void *wd, *bg, *bu, *bd, *res;  // float32 or bf16
     float *h;
-    __nv_bfloat16 *out;
+    void *out;
     int M, E, F;
 };
 constexpr int kTokens = 16;  // of a block; blockIdx.y counts the blocks of tokens
 
-// This block's tokens of the arguments.
-__device__ __forceinline__ SmallArgs tokens_of(SmallArgs a, int bytes)
+// This block's tokens of the arguments; `bytes` of a token's value, es of a result's.
+__device__ __forceinline__ SmallArgs tokens_of(SmallArgs a, int bytes, int es)
 {
     const int m0 = blockIdx.y * kTokens;
     a.x = (const uint8_t *)a.x + (size_t)m0 * a.E * bytes;
     if (a.xs) a.xs += m0;
-    if (a.res) a.res += (size_t)m0 * a.E;
+    if (a.res) a.res = (const uint8_t *)a.res + (size_t)m0 * a.E * es;
     a.h += (size_t)m0 * a.F;
-    a.out += (size_t)m0 * a.E;
+    a.out = (uint8_t *)a.out + (size_t)m0 * a.E * es;
     a.M = min(kTokens, a.M - m0);
     return a;
 }
+__device__ __forceinline__ float value_at(const void *p, size_t i, bool f32)
+{
+    return f32 ? ((const float *)p)[i] : __bfloat162float(((const __nv_bfloat16 *)p)[i]);
+}
 
-// V consecutive values as float: 16 bytes of bf16 (V = 8) or E4M3 (V = 16), or one value
-template <bool Q8, int V>
+// V consecutive values as float: 16 bytes of float32 (V = 4), bf16 (8) or E4M3 (16), or one value
+template <int KIND, int V>
 __device__ __forceinline__ void widen(const void *p, float (&f)[V])
 {
     if constexpr (V == 1) {
-        f[0] = __bfloat162float(*(const __nv_bfloat16 *)p);
+        f[0] = value_at(p, 0, KIND == kF32);
     } else {
         const uint4 raw = *reinterpret_cast<const uint4 *>(p);
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (Q8) {
+            if constexpr (KIND == kF32) {
+                f[i] = __uint_as_float(w[i]);
+            } else if constexpr (KIND == kE4m3) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> (16 * k)), __NV_E4M3);
@@ -74,11 +87,12 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-template <bool Q8, int V, int MB, int ACT>
+template <int KIND, int V, int MB, int ACT>
 __global__ void __launch_bounds__(kThreads) k_small_up(SmallArgs all)
 {
-    constexpr int kBytes = Q8 ? 1 : 2;
-    const SmallArgs a = tokens_of(all, kBytes);
+    constexpr int kBytes = kBytesOf<KIND>;
+    constexpr bool kIsF32 = KIND == kF32;
+    const SmallArgs a = tokens_of(all, kBytes, kIsF32 ? 4 : 2);
     extern __shared__ __align__(16) uint8_t x_s[];  // M rows
     tcu::grid_dependents_may_start();
     const int lane = threadIdx.x & 31, f = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -86,7 +100,8 @@ __global__ void __launch_bounds__(kThreads) k_small_up(SmallArgs all)
         for (int i = threadIdx.x * 16; i < a.M * a.E * kBytes; i += kThreads * 16)
             *reinterpret_cast<uint4 *>(x_s + i) = *reinterpret_cast<const uint4 *>((const uint8_t *)a.x + i);
     } else {
-        for (int i = threadIdx.x; i < a.M * a.E; i += kThreads) ((uint16_t *)x_s)[i] = ((const uint16_t *)a.x)[i];
+        using Word = std::conditional_t<kIsF32, uint32_t, uint16_t>;
+        for (int i = threadIdx.x; i < a.M * a.E; i += kThreads) ((Word *)x_s)[i] = ((const Word *)a.x)[i];
     }
     __syncthreads();
     if (f >= a.F) return;
@@ -97,12 +112,12 @@ __global__ void __launch_bounds__(kThreads) k_small_up(SmallArgs all)
 #pragma unroll 2
     for (int c = lane * V; c < a.E; c += 32 * V) {
         float eg[V], eu[V], ex[V];
-        widen<Q8, V>(wg + (size_t)c * kBytes, eg);
-        widen<Q8, V>(wu + (size_t)c * kBytes, eu);
+        widen<KIND, V>(wg + (size_t)c * kBytes, eg);
+        widen<KIND, V>(wu + (size_t)c * kBytes, eu);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             if (m >= a.M) break;
-            widen<Q8, V>(x_s + ((size_t)m * a.E + c) * kBytes, ex);
+            widen<KIND, V>(x_s + ((size_t)m * a.E + c) * kBytes, ex);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 g[m] = fmaf(eg[i], ex[i], g[m]);
@@ -117,28 +132,30 @@ __global__ void __launch_bounds__(kThreads) k_small_up(SmallArgs all)
         if (lane == m) mg = sg, mu = su;
     }
     if (lane >= a.M) return;
-    if constexpr (Q8) {
+    if constexpr (KIND == kE4m3) {
         const float xs = a.xs[lane];
         mg *= xs * a.gs[f];
         mu *= xs * a.us[f];
     }
-    if (a.bg) mg += __bfloat162float(a.bg[f]);
-    if (a.bu) mu += __bfloat162float(a.bu[f]);
-    a.h[(size_t)lane * a.F + f] = Act<ACT>::hidden(mg * Act<ACT>::kGate, mu * Act<ACT>::kUp);
+    if (a.bg) mg += value_at(a.bg, f, kIsF32);
+    if (a.bu) mu += value_at(a.bu, f, kIsF32);
+    a.h[(size_t)lane * a.F + f] =
+        kIsF32 ? Act<ACT>::exact(mg) * mu : Act<ACT>::hidden(mg * Act<ACT>::kGate, mu * Act<ACT>::kUp);
 }
 
-template <int V, int MB>
+template <bool F32, int V, int MB>
 __global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs all)
 {
-    const SmallArgs a = tokens_of(all, 2);
+    constexpr int KIND = F32 ? kF32 : kBf16, kBytes = F32 ? 4 : 2;
+    const SmallArgs a = tokens_of(all, kBytes, kBytes);
     constexpr int kAhead = 4;  // weight pieces loaded before the hidden rows are there
     const int lane = threadIdx.x & 31, e = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const __nv_bfloat16 *wd = a.wd + (size_t)min(e, a.E - 1) * a.F;
+    const uint8_t *wd = (const uint8_t *)a.wd + (size_t)min(e, a.E - 1) * a.F * kBytes;
     float w[kAhead][V];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
         const int c = (j * 32 + lane) * V;
-        if (c < a.F) widen<false, V>(wd + c, w[j]);
+        if (c < a.F) widen<KIND, V>(wd + (size_t)c * kBytes, w[j]);
     }
     tcu::grid_wait();  // the weights come from before the launch that this one overlaps
     if (e >= a.E) return;
@@ -151,11 +168,12 @@ __global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs all)
             if (m >= a.M) break;
             const float *h = a.h + (size_t)m * a.F + c;
             float hv[V];
-            if constexpr (V == 8) {
-                *reinterpret_cast<float4 *>(hv) = *reinterpret_cast<const float4 *>(h);
-                *reinterpret_cast<float4 *>(hv + 4) = *reinterpret_cast<const float4 *>(h + 4);
-            } else {
+            if constexpr (V == 1) {
                 hv[0] = h[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; i += 4)
+                    *reinterpret_cast<float4 *>(hv + i) = *reinterpret_cast<const float4 *>(h + i);
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) y[m] = fmaf(wv[i], hv[i], y[m]);
@@ -167,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs all)
         if (c < a.F) add(w[j], c);
     }
     for (int c = (kAhead * 32 + lane) * V; c < a.F; c += 32 * V) {
-        widen<false, V>(wd + c, w[0]);
+        widen<KIND, V>(wd + (size_t)c * kBytes, w[0]);
         add(w[0], c);
     }
     float mine = 0.f;
@@ -177,59 +195,67 @@ __global__ void __launch_bounds__(kThreads) k_small_down(SmallArgs all)
         if (lane == m) mine = s;
     }
     if (lane >= a.M) return;
-    if (a.bd) mine += __bfloat162float(a.bd[e]);
-    if (a.res) mine += __bfloat162float(a.res[(size_t)lane * a.E + e]);
-    a.out[(size_t)lane * a.E + e] = __float2bfloat16_rn(mine);
+    const size_t at = (size_t)lane * a.E + e;
+    if (a.bd) mine += value_at(a.bd, e, F32);
+    if (a.res) mine += value_at(a.res, at, F32);
+    if constexpr (F32) ((float *)a.out)[at] = mine;
+    else ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(mine);
 }
 
-template <bool Q8, int V, int MB>
+template <int KIND, int V, int MB>
 pmha_status launch_up(pmha_act act, const SmallArgs &a, cudaStream_t s)
 {
     const dim3 grid((unsigned)((a.F + kWarps - 1) / kWarps), (unsigned)((a.M + kTokens - 1) / kTokens));
-    const size_t smem = (size_t)std::min(a.M, kTokens) * a.E * (Q8 ? 1 : 2);
-    StageTimer timer(Q8 ? "ffn_up_quantized" : "ffn_up", s);
-    if (act == PMHA_ACT_SILU) k_small_up<Q8, V, MB, PMHA_ACT_SILU><<<grid, kThreads, smem, s>>>(a);
-    else k_small_up<Q8, V, MB, PMHA_ACT_GELU><<<grid, kThreads, smem, s>>>(a);
+    const size_t smem = (size_t)std::min(a.M, kTokens) * a.E * kBytesOf<KIND>;
+    StageTimer timer(KIND == kE4m3 ? "ffn_up_quantized" : "ffn_up", s);
+    if (act == PMHA_ACT_SILU) k_small_up<KIND, V, MB, PMHA_ACT_SILU><<<grid, kThreads, smem, s>>>(a);
+    else k_small_up<KIND, V, MB, PMHA_ACT_GELU><<<grid, kThreads, smem, s>>>(a);
     count_launch();
     PMHA_CUDA_TRY(cudaGetLastError());
     return PMHA_OK;
 }
 
 template <int MB>
-pmha_status launch(pmha_act act, const SmallArgs &a, cudaStream_t s)
+pmha_status launch(pmha_act act, const SmallArgs &a, bool f32, cudaStream_t s)
 {
     pmha_status st;
-    if (a.xs) st = launch_up<true, 16, MB>(act, a, s);
-    else if (a.E % 8 == 0) st = launch_up<false, 8, MB>(act, a, s);
-    else st = launch_up<false, 1, MB>(act, a, s);
+    if (a.xs) st = launch_up<kE4m3, 16, MB>(act, a, s);
+    else if (f32) st = a.E % 4 == 0 ? launch_up<kF32, 4, MB>(act, a, s) : launch_up<kF32, 1, MB>(act, a, s);
+    else st = a.E % 8 == 0 ? launch_up<kBf16, 8, MB>(act, a, s) : launch_up<kBf16, 1, MB>(act, a, s);
     if (st != PMHA_OK) return st;
     StageTimer timer("ffn_down", s);
     const dim3 grid((unsigned)((a.E + kWarps - 1) / kWarps), (unsigned)((a.M + kTokens - 1) / kTokens));
-    return a.F % 8 == 0 ? tcu::launch_overlapping(k_small_down<8, MB>, grid, kThreads, 0, s, a)
-                        : tcu::launch_overlapping(k_small_down<1, MB>, grid, kThreads, 0, s, a);
+    if (f32)
+        return a.F % 4 == 0 ? tcu::launch_overlapping(k_small_down<true, 4, MB>, grid, kThreads, 0, s, a)
+                            : tcu::launch_overlapping(k_small_down<true, 1, MB>, grid, kThreads, 0, s, a);
+    return a.F % 8 == 0 ? tcu::launch_overlapping(k_small_down<false, 8, MB>, grid, kThreads, 0, s, a)
+                        : tcu::launch_overlapping(k_small_down<false, 1, MB>, grid, kThreads, 0, s, a);
 }
 
 }  // namespace
 
-// Up to 64 tokens, 16 of whose rows fit in 48 KB of shared memory. One token
-// through width 256, hidden 1,024: 6.2 us against 17 of the tensor-core kernels,
-// whose tiles hold 256 tokens.
-bool ffn_small_supported(int64_t E, int64_t M, bool q8)
+// Up to 4 tokens, of float32 8, and up to 64 where all their values are 2,048 at
+// most (whose hidden rows better stay float32). Against the other kernels, whose
+// tiles hold 64 or 256 tokens (us): bf16, 256 x 1,024, 1 token 4.2 / 13.2, 4 tokens
+// 7.7 / 13.2, 8 tokens 13.4 / 13.2; 512 x 2,048, 4 tokens 12 / 19, 8 tokens 24 / 19;
+// 64 x 256, 32 tokens 8.9 / 6.7. Float32, 1,024 x 4,096, 1 token 9.9 / 164, 8 tokens
+// 82 / 162, 16 tokens 159 / 159. 16 rows have to fit in 48 KB of shared memory.
+bool ffn_small_supported(int64_t E, int64_t M, int token_bytes)
 {
-    return M <= kSmallRows && std::min<int64_t>(M, kTokens) * E * (q8 ? 1 : 2) <= 48 * 1024;
+    if (std::min<int64_t>(M, kTokens) * E * token_bytes > 48 * 1024) return false;
+    return M <= (token_bytes == 4 ? 8 : 4) || (token_bytes < 4 && M <= 64 && M * E <= 2048);
 }
 
-pmha_status ffn_small_forward(const FfnTc &f, const FfnUpArgs &u, const void *wd, const void *residual, void *out,
-                              cudaStream_t s)
+pmha_status ffn_small_forward(const FfnTc &f, bool f32, const FfnUpArgs &u, const void *wd, const void *residual,
+                              void *out, cudaStream_t s)
 {
     SmallArgs a = {};
     a.x = u.x, a.wg = u.wg, a.wu = u.wu, a.xs = u.x_scale, a.gs = u.wg_scale, a.us = u.wu_scale;
-    a.wd = (const __nv_bfloat16 *)wd, a.res = (const __nv_bfloat16 *)residual;
-    a.bg = (const __nv_bfloat16 *)f.bg, a.bu = (const __nv_bfloat16 *)f.bu, a.bd = (const __nv_bfloat16 *)f.bd;
-    a.h = (float *)u.h, a.out = (__nv_bfloat16 *)out;
+    a.wd = wd, a.res = residual, a.bg = f.bg, a.bu = f.bu, a.bd = f.bd;
+    a.h = (float *)u.h, a.out = out;
     a.M = (int)u.M, a.E = (int)f.E, a.F = (int)f.F;
-    if (a.M == 1) return launch<1>(f.act, a, s);
-    return a.M <= 4 ? launch<4>(f.act, a, s) : launch<16>(f.act, a, s);
+    if (a.M == 1) return launch<1>(f.act, a, f32, s);
+    return a.M <= 4 ? launch<4>(f.act, a, f32, s) : launch<16>(f.act, a, f32, s);
 }
 
 }  // namespace pmha

@@ -401,9 +401,9 @@ typedef struct {
  *               size function returns SIZE_MAX for invalid arguments). The
  *               size never shrinks as rows grow: one for the largest batch
  *               serves every smaller one. So for the backward pass.
- * Sums are float32. A bf16 block of more than 64 tokens rounds the hidden row
- * act(.) * (.) to bf16 between its products (what the tensor cores take); for
- * fewer tokens, and in a float32 block, it stays float32.
+ * Sums are float32. A bf16 block rounds the hidden row act(.) * (.) to bf16
+ * between its products (what the tensor cores take), except for a few tokens
+ * (up to 4, or rows * E up to 2^11); in a float32 block it stays float32.
  * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
  */
 size_t pmha_ffn_forward_workspace_size(const pmha_ffn_params *params, int64_t rows);
