@@ -35,13 +35,18 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kSmall = 9.094947e-13f, kBig = 1.0995116e12f;  // 2^-40, 2^40
 constexpr float kUp = 1.2089258e24f, kDown = 8.2718061e-25f;   // 2^80, 2^-80
 
-struct Table {
-    const void *g[kBatch];
-    void *out[kBatch];
-    uint32_t first[kBatch + 1];  // first chunk of each tensor
-    uint32_t last_n[kBatch];     // values of its last chunk; top bit: bf16
+template <int N>
+struct TableOf {
+    const void *g[N];
+    void *out[N];
+    uint32_t first[N + 1];  // first chunk of each tensor
+    uint32_t last_n[N];     // values of its last chunk; top bit: bf16
     int n;
 };
+using Table = TableOf<kBatch>;
+// Tensors of a short table, whose launches carry 0.8 KB of parameters instead of
+// 12: 16 tensors 18.5 -> 16.7 us.
+constexpr int kShort = 32;
 
 struct Sums {
     float mid, big, small;
@@ -61,7 +66,8 @@ __device__ __forceinline__ void add_square(Sums &s, float g)
 }
 
 // chunk -> tensor: the last i with first[i] <= c
-__device__ __forceinline__ int tensor_of(const Table &t, uint32_t c)
+template <int N>
+__device__ __forceinline__ int tensor_of(const TableOf<N> &t, uint32_t c)
 {
     int lo = 0, hi = t.n;
     while (hi - lo > 1) {
@@ -158,7 +164,8 @@ __device__ __forceinline__ uint32_t run_start(uint32_t chunks, uint32_t block)
     return (uint32_t)((uint64_t)chunks * block / gridDim.x);
 }
 
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_grad_squares(const __grid_constant__ Table t, double *part)
+template <int N>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_grad_squares(const __grid_constant__ TableOf<N> t, double *part)
 {
     __shared__ double sh[kThreads / 32];
     const uint32_t chunks = t.first[t.n], last = run_start(chunks, blockIdx.x + 1);
@@ -181,8 +188,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_grad_squares(const _
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
+template <int N>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-    k_grad_scale(const __grid_constant__ Table t, const double *__restrict__ part, int n_part, float max_norm,
+    k_grad_scale(const __grid_constant__ TableOf<N> t, const double *__restrict__ part, int n_part, float max_norm,
                  float *norm_out)
 {
     __shared__ double sh[kThreads / 32];
@@ -218,6 +226,17 @@ size_t part_bytes(int64_t n_tensors)
 {
     // batches are cut by tensors and by chunks (32-bit), so a call may take a few more than n / kBatch
     return (size_t)((n_tensors + kBatch - 1) / kBatch + 1) * kMaxBlocks * sizeof(double);
+}
+
+TableOf<kShort> shortened(const Table &t)
+{
+    TableOf<kShort> s = {};
+    s.n = t.n;
+    std::copy_n(t.g, t.n, s.g);
+    std::copy_n(t.out, t.n, s.out);
+    std::copy_n(t.first, t.n + 1, s.first);
+    std::copy_n(t.last_n, t.n, s.last_n);
+    return s;
 }
 
 struct Range {
@@ -333,7 +352,8 @@ pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, voi
                 return PMHA_ERR_INVALID_ARG;
             }
             StageTimer timer("grad_squares", cs);
-            k_grad_squares<<<grid, kThreads, 0, cs>>>(t, part + n_part);
+            if (t.n <= kShort) k_grad_squares<<<grid, kThreads, 0, cs>>>(shortened(t), part + n_part);
+            else k_grad_squares<<<grid, kThreads, 0, cs>>>(t, part + n_part);
             count_launch();
             PMHA_CUDA_TRY(cudaGetLastError());
             n_part += grid;
@@ -346,7 +366,9 @@ pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, voi
             else i = n_tensors;  // the only table is still here
             const int grid = std::max(1, std::min<int>((int)t.first[t.n], max_grid));
             StageTimer timer("grad_scale", cs);
-            k_grad_scale<<<grid, kThreads, 0, cs>>>(t, part, n_part, max_norm, first ? norm : nullptr);
+            float *const norm_out = first ? norm : nullptr;
+            if (t.n <= kShort) k_grad_scale<<<grid, kThreads, 0, cs>>>(shortened(t), part, n_part, max_norm, norm_out);
+            else k_grad_scale<<<grid, kThreads, 0, cs>>>(t, part, n_part, max_norm, norm_out);
             count_launch();
             PMHA_CUDA_TRY(cudaGetLastError());
             first = false;
