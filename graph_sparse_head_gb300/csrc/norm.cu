@@ -555,6 +555,8 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
             if (a.dx && live && c < a.width) store<T, VEC>((T *)a.dx + base + c, o.v);
         }
     }
+    // the last steps' copies (zeros past the rows) land before the block's shared memory can go to another
+    if constexpr (kRing > 0) asm volatile("cp.async.wait_all;" ::: "memory");
     if (!a.part) return;
     // the warp's row groups, then the warps one after the other
 #pragma unroll
