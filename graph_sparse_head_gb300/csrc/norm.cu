@@ -24,10 +24,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kScaleMin = 5.42101086e-20f;  // 2^-64
-// A row whose squares' sum leaves float32 is taken again as s 2^-64 (exact),
-// with eps 2^-128: the norm does not change.
-constexpr float kDown = 5.42101086e-20f;
+// A row whose squares' sum leaves float32 is taken again times the power of two
+// that brings its largest magnitude into [2, 4) (exact but for values 2^-120 of
+// it), with eps times its square: the norm does not change, and no sum of up to 2^24 squares
+// overflows. A fixed factor would not do: 2^-64, taken before, left rows from 2^128 / sqrt(width) infinite.
 constexpr float kMostSquares = 3.0e38f;
+__device__ __forceinline__ float down_scale(float most)
+{
+    const uint32_t e = __float_as_uint(most) >> 23;  // exponent + 127
+    return e >= 128 && e < 255 ? __uint_as_float((255 - e) << 23) : 1.f;  // 1 for infinities and NaN too
+}
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
@@ -235,15 +241,30 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
             if (live && c < a.width) store<T, VEC>((T *)a.sum + base + c, v[j].v);
         }
     }
+    float sc = 1.f;  // v holds the row times this
+    auto scale_rows = [&](bool over) {
+        float most = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) most = fmaxf(most, fabsf(to_f<T>(v[j].v[i])));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+        const float by = over ? down_scale(most) : 1.f;
+        sc *= by;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j].v[i] = from_f<T>(to_f<T>(v[j].v[i]) * by);
+    };
     if (a.out) {
-        float sc = 1.f;
         auto squares = [&]() {
             float ss = 0.f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float f = to_f<T>(v[j].v[i]) * sc;
+                    const float f = to_f<T>(v[j].v[i]);
                     ss = fmaf(f, f, ss);
                 }
 #pragma unroll
@@ -252,10 +273,10 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
         };
         float ss = squares();
         if (__any_sync(kFull, ss > kMostSquares)) {
-            sc = ss > kMostSquares ? kDown : 1.f;
+            scale_rows(ss > kMostSquares);
             ss = squares();
         }
-        const float r = rsqrtf(ss / (float)a.width + a.eps * sc * sc) * sc;
+        const float r = rsqrtf(ss / (float)a.width + a.eps * sc * sc);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + l) * VEC;
@@ -267,14 +288,13 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
     }
     if constexpr (Q8) {
         Two ss, am;
-        float sc = 1.f;
         auto stats = [&]() {
             ss = am = Two{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float f = to_f<T>(v[j].v[i]) * sc;
+                    const float f = to_f<T>(v[j].v[i]);
                     square_into<kExact>(ss, f);
                     take_max<kExact>(am, abs_mul<kExact>(f, to_f<T>(wv[j].v[i])));
                 }
@@ -286,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
         };
         stats();
         if (__any_sync(kFull, !(ss.hi <= kMostSquares))) {
-            sc = ss.hi <= kMostSquares ? 1.f : kDown;
+            scale_rows(!(ss.hi <= kMostSquares));
             stats();
         }
         const Quant z = quant(ss, am, a.inv_width, a.eps * sc * sc);
@@ -298,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
             alignas(8) uint8_t b[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                b[i] = to_e4m3(quant_value<kExact>(to_f<T>(v[j].v[i]) * sc, to_f<T>(wv[j].v[i]), z.c));
+                b[i] = to_e4m3(quant_value<kExact>(to_f<T>(v[j].v[i]), to_f<T>(wv[j].v[i]), z.c));
             *reinterpret_cast<typename Bytes<VEC>::type *>(a.q + base + c) =
                 *reinterpret_cast<typename Bytes<VEC>::type *>(b);
         }
@@ -314,6 +334,19 @@ __device__ __forceinline__ float block_sum(float v, float *sh)
     v = 0.f;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
+    __syncthreads();
+    return v;
+}
+
+__device__ __forceinline__ float block_max(float v, float *sh)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) v = fmaxf(v, sh[i]);
     __syncthreads();
     return v;
 }
@@ -367,7 +400,14 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
     };
     stats(a.sum != nullptr);
     if (!(ss <= kMostSquares)) {  // the same in every thread
-        sc = kDown;
+        float most = 0.f;
+        for (int c = threadIdx.x * VEC; c < a.width; c += kThreads * VEC) {
+            Vals<T, VEC> v;
+            kept(c, v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) most = fmaxf(most, fabsf(to_f<T>(v.v[i])));
+        }
+        sc = down_scale(block_max(most, sh));
         stats(false);
     }
     Quant z;
@@ -390,14 +430,14 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
         z = quant(s2, am, a.inv_width, a.eps * sc * sc);
         if (threadIdx.x == 0) a.scale[row] = z.scale;
     }
-    const float r = rsqrtf(ss / (float)a.width + a.eps * sc * sc) * sc;
+    const float r = rsqrtf(ss / (float)a.width + a.eps * sc * sc);
     for (int c = threadIdx.x * VEC; c < a.width; c += kThreads * VEC) {
         Vals<T, VEC> v, wv, y;
         kept(c, v);
         weight(c, wv);
         if (a.out) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) y.v[i] = from_f<T>(to_f<T>(v.v[i]) * r * to_f<T>(wv.v[i]));
+            for (int i = 0; i < VEC; ++i) y.v[i] = from_f<T>(to_f<T>(v.v[i]) * sc * r * to_f<T>(wv.v[i]));
             store<T, VEC>((T *)a.out + base + c, y.v);
         }
         if constexpr (Q8) {
@@ -532,7 +572,14 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
         stats();
         float sc = 1.f;
         if (__any_sync(kFull, ss > kMostSquares)) {
-            sc = ss > kMostSquares ? kDown : 1.f;
+            float most = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) most = fmaxf(most, fabsf(f[j][i]));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+            sc = ss > kMostSquares ? down_scale(most) : 1.f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -610,7 +657,14 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd_wide(NormBwdArgs a)
         };
         stats();
         if (ss > kMostSquares) {  // the same in every thread
-            sc = kDown;
+            float most = 0.f;
+            for (int c = threadIdx.x * VEC; c < a.width; c += kThreads * VEC) {
+                Vals<T, VEC> v;
+                load<T, VEC>(x + base + c, v.v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) most = fmaxf(most, fabsf(to_f<T>(v.v[i])));
+            }
+            sc = down_scale(block_max(most, sh));
             stats();
         }
         const float r = rsqrtf(ss / (float)a.width + a.eps * sc * sc);
