@@ -571,7 +571,9 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
             }
         stats();
         float sc = 1.f;
-        if (__any_sync(kFull, ss > kMostSquares)) {
+        // the sum of a s is of s as it is, too: s of 2^58 and a of 2^64 are ordinary numbers
+        const bool over = ss > kMostSquares || !(fabsf(as) <= kMostSquares);
+        if (__any_sync(kFull, over)) {
             float most = 0.f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
                 for (int i = 0; i < VEC; ++i) most = fmaxf(most, fabsf(f[j][i]));
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-            sc = ss > kMostSquares ? down_scale(most) : 1.f;
+            sc = over ? down_scale(most) : 1.f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd_wide(NormBwdArgs a)
             as = block_sum(as, sh);
         };
         stats();
-        if (ss > kMostSquares) {  // the same in every thread
+        if (ss > kMostSquares || !(fabsf(as) <= kMostSquares)) {  // the same in every thread
             float most = 0.f;
             for (int c = threadIdx.x * VEC; c < a.width; c += kThreads * VEC) {
                 Vals<T, VEC> v;

@@ -65,3 +65,22 @@ def test_backward(width, dtype):
         tol = 4 * ref.stat_tol(width) * mag + ref.half_ulp(dtype) * dx.abs() + torch.finfo(dtype).smallest_normal
         ref.assert_within("dx", got["dx"], dx, 1.01 * tol)
         ref.assert_within("dweight", got["dweight"], dw, 1.01 * (40 * 2.0 ** -24 + ref.stat_tol(width)) * dw_mag)
+
+
+@DTYPES
+@pytest.mark.parametrize("width", WIDTHS)
+def test_backward_of_large_rows_and_large_gradients(width, dtype):
+    # x = 2^58 and dout = 2^64 are ordinary numbers whose products' sum is not: dx is some 2^6
+    g = torch.Generator().manual_seed(width)
+    u = 0.5 + 0.5 * torch.rand(5, width, generator=g)
+    w = 1 + 0.2 * torch.randn(width, generator=g)
+    sizes = torch.tensor([2.0 ** 58, 2.0 ** 62, 1.0, 2.0 ** -20, 2.0 ** 100])[:, None]
+    x, w = (sizes * u).to(dtype).to(DEV), w.to(dtype).to(DEV)
+    dy = (2.0 ** 64 * (0.5 + 0.5 * torch.rand(5, width, generator=g))).to(dtype).to(DEV)  # of one sign: nothing cancels
+    ds = torch.randn(5, width, generator=g).to(dtype).to(DEV)
+    for dsum in (None, ds):
+        got = pmha.pmha_rms_norm_backward(x, w, ref.EPS, dy, dsum=dsum)
+        dx, mag, dw, dw_mag = ref.norm_backward(x, w, dy, dsum)
+        tol = 4 * ref.stat_tol(width) * mag + ref.half_ulp(dtype) * dx.abs() + torch.finfo(dtype).smallest_normal
+        ref.assert_within("dx", got["dx"], dx, 1.01 * tol)
+        ref.assert_within("dweight", got["dweight"], dw, 1.01 * (40 * 2.0 ** -24 + ref.stat_tol(width)) * dw_mag)
