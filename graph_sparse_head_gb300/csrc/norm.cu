@@ -305,8 +305,9 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
             }
         };
         stats();
-        if (__any_sync(kFull, !(ss.hi <= kMostSquares))) {
-            scale_rows(!(ss.hi <= kMostSquares));
+        const bool over = !(ss.hi <= kMostSquares && am.hi <= kMostSquares);  // squares, or products with the weight
+        if (__any_sync(kFull, over)) {
+            scale_rows(over);
             stats();
         }
         const Quant z = quant(ss, am, a.inv_width, a.eps * sc * sc);
@@ -397,9 +398,27 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
             }
         }
         ss = block_sum(ss, sh);
+        if constexpr (Q8) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                s2 = add(s2, Two{__shfl_xor_sync(kFull, s2.hi, o), __shfl_xor_sync(kFull, s2.lo, o)});
+                take_max<kExact>(am, Two{__shfl_xor_sync(kFull, am.hi, o), __shfl_xor_sync(kFull, am.lo, o)});
+            }
+            if ((threadIdx.x & 31) == 0) {
+                sh2[threadIdx.x >> 5] = s2;
+                shm[threadIdx.x >> 5] = am;
+            }
+            __syncthreads();
+            s2 = am = Two{0.f, 0.f};
+            for (int i = 0; i < kThreads / 32; ++i) {
+                s2 = add(s2, sh2[i]);
+                take_max<kExact>(am, shm[i]);
+            }
+            __syncthreads();  // read before a second pass writes there
+        }
     };
     stats(a.sum != nullptr);
-    if (!(ss <= kMostSquares)) {  // the same in every thread
+    if (!(ss <= kMostSquares && am.hi <= kMostSquares)) {  // the same in every thread
         float most = 0.f;
         for (int c = threadIdx.x * VEC; c < a.width; c += kThreads * VEC) {
             Vals<T, VEC> v;
@@ -412,21 +431,6 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
     }
     Quant z;
     if constexpr (Q8) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            s2 = add(s2, Two{__shfl_xor_sync(kFull, s2.hi, o), __shfl_xor_sync(kFull, s2.lo, o)});
-            take_max<kExact>(am, Two{__shfl_xor_sync(kFull, am.hi, o), __shfl_xor_sync(kFull, am.lo, o)});
-        }
-        if ((threadIdx.x & 31) == 0) {
-            sh2[threadIdx.x >> 5] = s2;
-            shm[threadIdx.x >> 5] = am;
-        }
-        __syncthreads();
-        s2 = am = Two{0.f, 0.f};
-        for (int i = 0; i < kThreads / 32; ++i) {
-            s2 = add(s2, sh2[i]);
-            take_max<kExact>(am, shm[i]);
-        }
         z = quant(s2, am, a.inv_width, a.eps * sc * sc);
         if (threadIdx.x == 0) a.scale[row] = z.scale;
     }

@@ -84,3 +84,18 @@ def test_backward_of_large_rows_and_large_gradients(width, dtype):
         tol = 4 * ref.stat_tol(width) * mag + ref.half_ulp(dtype) * dx.abs() + torch.finfo(dtype).smallest_normal
         ref.assert_within("dx", got["dx"], dx, 1.01 * tol)
         ref.assert_within("dweight", got["dweight"], dw, 1.01 * (40 * 2.0 ** -24 + ref.stat_tol(width)) * dw_mag)
+
+
+@DTYPES
+@pytest.mark.parametrize("width", WIDTHS)
+def test_quantized_rows_times_large_weights(width, dtype):
+    # rows of 2^58 whose squares are float32 numbers, weights of 2^72: their products are not, the norm's values are
+    g = torch.Generator().manual_seed(width)
+    u = 0.5 + 0.5 * torch.rand(4, width, generator=g)
+    x = (torch.tensor([2.0 ** 55, 1.0, 2.0 ** 58, 2.0 ** 100])[:, None] * u).to(dtype).to(DEV)
+    w = (2.0 ** 72 * torch.randn(width, generator=g)).to(dtype).to(DEV)
+    q, scale, _ = pmha.pmha_rms_norm_quantized(x, w, ref.EPS)
+    y, _ = ref.norm(x, w, eps=float(torch.tensor(ref.EPS, dtype=torch.float32)))
+    rq, rscale = ref.quantized(y)
+    assert torch.equal(scale, rscale)
+    assert torch.equal(q.double(), rq)
