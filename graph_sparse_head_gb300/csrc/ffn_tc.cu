@@ -688,12 +688,19 @@ int64_t ffn_hidden_parts(int64_t M, int64_t F)
     return 8 * std::min<int64_t>(num_sms() / 2, ceil_div(M, 256) * ceil_div(F, 64));
 }
 
+// Rows of one accumulator of the weights' products, 16 an addition. The tensor core cuts its sums instead of rounding
+// them: measured, an addition takes some 2^-22.3 of a running sum of one sign, 4,096 of them 4e-4 in all, a fifth of what rounding
+// to bf16 may take. Without a limit the chains of narrow blocks had 52,000 (20,000,000 rows, hidden width 16: 5e-3).
+constexpr int64_t kChain = 65536;
+
 int ffn_dw_splits(int64_t E, int64_t F, int64_t rows)
 {
-    // as many pieces of the row range as fill the pairs, each of at least 4 blocks of 64 rows
+    // As many pieces of the row range as fill the pairs, each of at least 4 blocks of 64 rows; and so many times as
+    // many that a piece has kChain rows at most.
     const int64_t tiles = 3 * ceil_div(F, 256) * ceil_div(E, wide_tiles(E) ? 256 : 128);
     const int64_t pairs = num_sms() / 2;
-    return (int)std::max<int64_t>(1, std::min(pairs / tiles, ceil_div(rows, 256)));
+    const int64_t fill = std::max<int64_t>(1, std::min(pairs / tiles, ceil_div(rows, 256)));
+    return (int)(fill * ceil_div(std::max<int64_t>(rows, 1), fill * kChain));
 }
 
 pmha_status ffn_tc_dw(const FfnTc &f, const FfnDwArgs &a, cudaStream_t s)

@@ -110,3 +110,28 @@ def test_layer_gradients_in_norm(n, nnz, B, E, H, F, dt):
     for name, v in leaf.items():
         if name != "bk":  # zero in exact arithmetic
             assert rel(grads["dx" if name == "x" else "d" + name], v.grad) <= bar, name
+
+
+def test_weight_gradients_of_one_sign():
+    # Sums over many rows of a narrow block, all terms positive: cut at each of 4,096 additions by up to 2^-22 of the
+    # running sum (two bits below float32's) they are off by 2^-11 at most, to one side. The gradients of a row of the
+    # weights are all alike here, so that their roundings to bf16 may go one way too: 2^-9.
+    rows, E, F = 20_000_000, 64, 16
+    g = torch.Generator(device=DEV).manual_seed(4)
+
+    def r(*shape):
+        return torch.rand(*shape, generator=g, device=DEV)
+
+    p = pmha.FfnParams(*((t / E * 2).to(BF16) for t in (r(F, E), r(F, E))), (r(E, F) / F).to(BF16))
+    x, dy = (0.5 + r(rows, E)).to(BF16), (0.5 + r(rows, E)).to(BF16)
+    got = pmha.pmha_ffn_backward(p, x, dy, input_grads=False)
+    pmha.pmha_device_status()
+    want = {}
+    for at in range(0, rows, 200_000):
+        for n, (v, _) in block(p).backward(x[at:at + 200_000], dy[at:at + 200_000]).items():
+            if n in ("dwg", "dwu", "dwd"):
+                want[n] = want.get(n, 0) + v
+    for n, v in want.items():
+        assert bool((v > 0).all())
+        off = float((got[n].double() / v - 1).mean())
+        assert abs(off) <= 2.0 ** -11 + 2.0 ** -9, (n, off)
