@@ -811,14 +811,17 @@ void dispatch_wide(pmha_dtype dt, int vec, F f)
     else f(Tag<float, 1, 1, 32>());
 }
 
-// Blocks of the backward pass: four a SM keep its memory pipe full, more where a block would take more than kSteps
-// steps; each writes one partial row.
+// Blocks of the backward pass, each of which writes one partial row: four a SM keep its memory pipe full, more where a
+// block would take more than kSteps steps. Blocks that take one wide row at a time come in whole fives a SM, which are
+// resident (100,000 x 2,048: 677 us, with four a SM 715, with just as many as kSteps needs 782); for the others
+// just as many is faster (1,280,000 x 256: 382 us, 405 in threes a SM, of which those are resident).
 int64_t bwd_blocks(pmha_dtype dt, int64_t rows, int64_t width)
 {
     const Shape s = shape_of(dt, width);
-    const int64_t per = s.lpr ? (int64_t)(kThreads / 32) * (32 / s.lpr) : 1;
-    const int64_t steps = (rows + per - 1) / per;
-    return std::max({(int64_t)1, std::min<int64_t>(steps, (int64_t)num_sms() * 4), (steps + kSteps - 1) / kSteps});
+    const int64_t per = s.lpr ? (int64_t)(kThreads / 32) * (32 / s.lpr) : 1, steps = (rows + per - 1) / per;
+    const int64_t full = (int64_t)num_sms() * (s.lpr ? 4 : 5);
+    const int64_t least = s.lpr ? (steps + kSteps - 1) / kSteps : (steps + full * kSteps - 1) / (full * kSteps) * full;
+    return std::max<int64_t>(1, std::min(steps, std::max(full, least)));
 }
 
 }  // namespace
