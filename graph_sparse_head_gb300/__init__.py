@@ -889,6 +889,8 @@ class PackedEncoderLayer:
                  eps: float = 1e-6):
         if graph.query_features != graph.key_features:
             raise ValueError("an encoder layer needs a graph with query_features == key_features")
+        if not isinstance(block, FfnParams):
+            raise TypeError("block must be FfnParams (the layer has a backward pass; a block in 8 bits is called beside it)")
         E = attention.embed_dim
         for n, t in (("norm1", norm1), ("norm2", norm2)):
             _like(n, t, (E,), attention.dtype, attention.wq.get_device())
