@@ -29,6 +29,9 @@ constexpr float kScaleMin = 5.42101086e-20f;  // 2^-64
 // it), with eps times its square: the norm does not change, and no sum of up to 2^24 squares
 // overflows. A fixed factor would not do: 2^-64, taken before, left rows from 2^128 / sqrt(width) infinite.
 constexpr float kMostSquares = 3.0e38f;
+// The 8-bit output's statistics are pairs of floats, and the second float of 1 / (mean square) is a normal
+// number up to 2^102: its rows are scaled from 2^96 on.
+constexpr float kMostPairs = 7.9228163e28f;
 __device__ __forceinline__ float down_scale(float most)
 {
     const uint32_t e = __float_as_uint(most) >> 23;  // exponent + 127
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
             }
         };
         stats();
-        const bool over = !(ss.hi <= kMostSquares && am.hi <= kMostSquares);  // squares, or products with the weight
+        const bool over = !(ss.hi <= kMostPairs && am.hi <= kMostSquares);  // squares, or products with the weight
         if (__any_sync(kFull, over)) {
             scale_rows(over);
             stats();
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
         }
     };
     stats(a.sum != nullptr);
-    if (!(ss <= kMostSquares && am.hi <= kMostSquares)) {  // the same in every thread
+    if (!(ss <= (Q8 ? kMostPairs : kMostSquares) && am.hi <= kMostSquares)) {  // the same in every thread
         float most = 0.f;
         for (int c = threadIdx.x * VEC; c < a.width; c += kThreads * VEC) {
             Vals<T, VEC> v;

@@ -99,3 +99,18 @@ def test_quantized_rows_times_large_weights(width, dtype):
     rq, rscale = ref.quantized(y)
     assert torch.equal(scale, rscale)
     assert torch.equal(q.double(), rq)
+
+
+@DTYPES
+@pytest.mark.parametrize("width", [7, 64, 256, 1500])
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** 40, 2.0 ** 52, 2.0 ** 58, 2.0 ** 62])
+def test_quantized_keeps_its_pairs_of_floats(width, dtype, size):
+    # the inverse of a large mean square has a second float below the normal numbers: over 20,000 rows some scales show it
+    g = torch.Generator(device=DEV).manual_seed(width)
+    x = (size * torch.randn(20_000, width, generator=g, device=DEV)).to(dtype)
+    w = (1 + 0.2 * torch.randn(width, generator=g, device=DEV)).to(dtype)
+    q, scale, _ = pmha.pmha_rms_norm_quantized(x, w, ref.EPS)
+    y, _ = ref.norm(x, w, eps=float(torch.tensor(ref.EPS, dtype=torch.float32)))
+    rq, rscale = ref.quantized(y)
+    assert torch.equal(scale, rscale)
+    assert torch.equal(q.double(), rq)
