@@ -565,7 +565,7 @@ def pmha_rms_norm_quantized(x: torch.Tensor, weight: torch.Tensor | None, eps: f
                             residual: torch.Tensor | None = None, stream=None):
     """pmha_rms_norm with its output in 8 bits: (q, scale, s) with q in
     float8_e4m3fn, scale (...,) float32, norm ~ q * scale[..., None]; every q is
-    the formula's value rounded once. What pmha_ffn_forward_quantized takes."""
+    the formula's value, computed to some 46 bits and rounded once. What pmha_ffn_forward_quantized takes."""
     shape, rows, width, dev = _rows_of("x", x)
     dtype = x.dtype
     w = _like("weight", weight, (width,), dtype, dev)

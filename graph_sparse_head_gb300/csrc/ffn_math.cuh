@@ -68,7 +68,8 @@ struct Act<PMHA_ACT_GELU> {
     static __device__ __forceinline__ float exact(float g) { return g * (0.5f * erfcf(-0.70710678f * g)); }
     static constexpr float kGate = 1.f, kUp = 1.f;
     // Phi(-z) for z = min(|g|, 64) (0 from 14 on), by the rational form 7.1.26 of Abramowitz
-    // and Stegun for erfc(z / sqrt(2)) (error below 1.5e-7): a polynomial in
+    // and Stegun for erfc(z / sqrt(2)) (error below 1.5e-7; relative to the tail 0.16 % at z = 5, where it is 3e-7, and
+    // 2 % at 10): a polynomial in
     // t = 1 / (1 + p z) times e = exp(-g^2 / 2), which the slope needs as well.
     static __device__ __forceinline__ float lower(float g, float z, float *e)
     {

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm_bwd(NormBwdArgs a)
     Vals<T, VEC> v[NV], g[NV], s[NV];
     // Rows of 16-byte pieces come through a ring of kRing rows a warp, each lane
     // copying and reading its own pieces (no barrier): what is in flight does
-    // not take registers, and 200 KB an SM of it keep memory busy. Others are
+    // not take registers, and 150 KB an SM of it keep memory busy. Others are
     // loaded when they are needed.
     constexpr int kRing = kRingOf<T, VEC, NV>;
     uint8_t *ring = (uint8_t *)shw + ((a.width * 4 + 15) & ~15) + threadIdx.x * 16;

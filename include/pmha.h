@@ -27,11 +27,15 @@
  *    unless stated. Every call returns a pmha_status; on failure
  *    pmha_last_error() gives a message for the calling thread. A failing call
  *    writes nothing to its outputs unless it says otherwise.
- *  - No kernel waits on another launch, and none on another CTA but the
- *    tensor-core kernels of the gated block, whose CTAs work in clusters of
- *    two (which the GPU starts together). Every device-side wait is on a
- *    pipeline barrier and bounded: it gives up with PMHA_ERR_TIMEOUT (see
- *    pmha_device_status).
+ *  - No kernel waits on another CTA but the tensor-core kernels of the gated
+ *    block, whose CTAs work in clusters of two (which the GPU starts together).
+ *    Every wait on a pipeline barrier is bounded: it gives up with
+ *    PMHA_ERR_TIMEOUT (see pmha_device_status).
+ *  - The gated block's kernels may come up before the launch ahead of them on
+ *    their stream has ended (programmatic dependent launches). They wait for
+ *    its end before they read what it writes, or write. That wait, the
+ *    meeting of a cluster's two CTAs and the allocation of tensor memory are
+ *    the GPU's own: they have no limit, and end with the work before them.
  *  - A workspace holds intermediate values of one call. Calls, or replays of
  *    captured graphs, that may run at the same time need one each.
  */
@@ -342,12 +346,16 @@ pmha_status pmha_graph_export_by_source(const pmha_graph *graph, int32_t *src_ro
  *          float format E4M3 and device (rows) float32. A row's scale is
  *          max|y| / 448, at least 2^-64, with y the row of the norm in exact
  *          arithmetic, and out_q is y / scale rounded to the nearest E4M3
- *          value (ties to even): y ~ out_q * scale. The values are those of
- *          the formula in exact arithmetic (scale and eps rounded to
- *          float32), whatever the order of its sums, for rows whose
- *          squares are not below float32's normal numbers. A row with an
- *          infinity or a NaN gets a NaN scale and NaN bytes.
- * Statistics are float32; a row whose squares leave float32 is scaled first.
+ *          value (ties to even): y ~ out_q * scale. Statistics and products
+ *          are pairs of floats here, some 46 bits, before the one rounding
+ *          to scale or byte: for rows whose squares are not below float32's
+ *          normal numbers the values are those of the formula in exact
+ *          arithmetic (scale and eps rounded to float32), but for the last
+ *          bit of about one scale in 10^7. A row with an infinity or a NaN
+ *          gets a NaN scale and NaN bytes.
+ * Statistics of out are float32. A row whose squares (for out_q, or its products
+ * with the weight) leave float32 is scaled by a power of two first: rows up to
+ * the largest finite values are normalised.
  * Needs no workspace.
  * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_CUDA.
  */
@@ -364,7 +372,9 @@ pmha_status pmha_rms_norm(pmha_dtype dtype, int64_t rows, int64_t width, const v
  *        residual stream), added to dx.
  *  dx    device (rows, width) or NULL: the gradient of x, and of the residual.
  *  dweight  device float32 (width) or NULL: summed over the rows in a fixed
- *        order (deterministic).
+ *        order (deterministic), in float32 over up to 128 terms and as pairs of
+ *        floats from there: the error does not grow with the rows.
+ * A row whose squares or products dout weight x leave float32 is scaled first.
  *  workspace  pmha_rms_norm_backward_workspace_size() bytes, 256-byte aligned
  *        (0 when the arguments are invalid).
  * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
@@ -402,8 +412,10 @@ typedef struct {
  *               size never shrinks as rows grow: one for the largest batch
  *               serves every smaller one. So for the backward pass.
  * Sums are float32. A bf16 block rounds the hidden row act(.) * (.) to bf16
- * between its products (what the tensor cores take), except for a few tokens
- * (up to 4, or rows * E up to 2^11); in a float32 block it stays float32.
+ * between its products (what the tensor cores take), except for a few tokens:
+ * up to 4, or up to 64 with rows * E up to 2^11, where those tokens (16 of
+ * them, if there are more) fill at most 48 KB. In a float32 block it stays
+ * float32.
  * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
  */
 size_t pmha_ffn_forward_workspace_size(const pmha_ffn_params *params, int64_t rows);
@@ -444,8 +456,9 @@ pmha_status pmha_ffn_forward_quantized(const pmha_ffn_params *params, const pmha
  *          them float32.
  *  workspace  pmha_ffn_backward_workspace_size() bytes, 256-byte aligned
  *          (SIZE_MAX when the arguments are invalid). It holds the hidden
- *          values and gradients of at most 2 GiB's worth of rows, which are
- *          taken in blocks: past that its size does not grow with rows.
+ *          values and gradients of at most 2 GiB's worth of rows, or of 256
+ *          rows where these have more; rows are taken in such blocks, and past one
+ *          block the size does not grow with them.
  * Errors as pmha_ffn_forward.
  */
 typedef struct {
