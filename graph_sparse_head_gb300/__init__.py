@@ -442,7 +442,7 @@ def pmha_profile_enable(on: bool = True) -> None:
 
 def pmha_profile_read() -> dict:
     """{stage: (launches, total_ms)} since the last read."""
-    n_max = 32
+    n_max = 256  # the library has some 50 stages
     names = ctypes.create_string_buffer(32 * n_max)
     launches = (ctypes.c_int64 * n_max)()
     totals = (ctypes.c_double * n_max)()

@@ -497,8 +497,8 @@ pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, voi
 const char *pmha_last_error(void);
 
 /*
- * Stage timing. With pmha_profile_enable(1), pmha_forward / pmha_edge_weights
- * record a CUDA event pair around each kernel launch on the caller's stream.
+ * Stage timing. With pmha_profile_enable(1), the calls record a CUDA event pair
+ * around each of their launches on the caller's stream.
  * pmha_profile_read() synchronizes those events and returns, per stage, the
  * number of launches and their total device time in milliseconds, then clears
  * the records. names receives up to max_stages NUL-terminated names of at
