@@ -14,8 +14,11 @@ mixes go through out_proj.
 
 Around it stands the rest of an encoder and of its training step: the norm of
 the residual sum (pmha_rms_norm), the gated feed-forward block (pmha_ffn_*),
-their gradients, clipping by the global norm (pmha_clip_grad_norm), and
-PackedEncoderLayer, which runs them together with the layer.
+their gradients, clipping by the global norm (pmha_clip_grad_norm), the join
+of a block with the residual stream (pmha_join: norms on both sides, gate,
+residual scale), tensors kept in 8 bits for the backward pass
+(pmha_checkpoint), and PackedEncoderLayer, which runs them together with the
+layer.
 """
 from __future__ import annotations
 
@@ -45,6 +48,8 @@ __all__ = [
     "pmha_ffn_forward", "pmha_ffn_forward_quantized", "pmha_ffn_backward",
     "pmha_ffn_forward_workspace_size", "pmha_ffn_forward_quantized_workspace_size",
     "pmha_ffn_backward_workspace_size", "pmha_clip_grad_norm",
+    "JoinParams", "Checkpoint", "pmha_join", "pmha_join_checkpointed", "pmha_join_backward",
+    "pmha_join_backward_workspace_size", "pmha_checkpoint", "pmha_checkpoint_restore",
 ]
 
 WMODES = {"none": PMHA_WEIGHTS_NONE, "avg": PMHA_WEIGHTS_AVG, "per_head": PMHA_WEIGHTS_PER_HEAD}
@@ -872,6 +877,212 @@ def pmha_ffn_backward(params: FfnParams, x: torch.Tensor, dout: torch.Tensor, in
     if st:
         _lib.check(st, "pmha_ffn_backward")
     return out
+
+
+# ---------------------------------------------------------------- joins with the residual stream, 8-bit checkpoints
+@dataclasses.dataclass
+class Checkpoint:
+    """A tensor (..., width) kept in 8 bits between the forward and the backward pass: codes int8 of its shape and one
+    bfloat16 scale for every 32 values of a row, (..., ceil(width / 32)); value ~ code * scale. dtype: what it was."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    dtype: torch.dtype
+
+    @property
+    def shape(self) -> torch.Size:
+        return self.codes.shape
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.scale.numel()
+
+    @staticmethod
+    def _empty(shape, dtype, device) -> "Checkpoint":
+        return Checkpoint(torch.empty(shape, dtype=torch.int8, device=device),
+                          torch.empty((*shape[:-1], (shape[-1] + 31) // 32), dtype=torch.bfloat16, device=device), dtype)
+
+    def _struct(self):
+        return _lib.PmhaKept(self.codes.data_ptr(), self.scale.data_ptr())
+
+
+def _kept_like(name, k, shape, dtype, index):
+    """The struct of a Checkpoint of a tensor of this shape, type and device."""
+    if k.dtype is not dtype:
+        raise ValueError(f"{name} was kept from {k.dtype}, the call runs in {dtype}")
+    if _like(name + ".codes", k.codes, shape, torch.int8, index) is None \
+            or _like(name + ".scale", k.scale, (*shape[:-1], (shape[-1] + 31) // 32), torch.bfloat16, index) is None:
+        raise ValueError(f"{name} lacks its codes or scales")
+    return k._struct()
+
+
+def pmha_checkpoint(x: torch.Tensor, stream=None) -> Checkpoint:
+    """Keeps x (..., width) in 8 bits: groups of 32 values along the last axis, scale max|group| / 127 rounded up to
+    bfloat16, each code the nearest integer to value / scale (off by half a scale at most)."""
+    shape, rows, width, dev = _rows_of("x", x)
+    with _on(dev, stream):
+        k = Checkpoint._empty(shape, x.dtype, x.device)
+        st = _library().pmha_checkpoint(_DTYPES[x.dtype], rows, width, x.data_ptr(), ctypes.byref(k._struct()),
+                                        _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_checkpoint")
+    return k
+
+
+def pmha_checkpoint_restore(kept: Checkpoint, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """code * scale in the type that the tensor had."""
+    shape, dtype = _shape_of("kept", kept)
+    dev = kept.codes.get_device()
+    k = _kept_like("kept", kept, shape, dtype, dev)
+    o = _like("out", out, shape, dtype, dev)
+    width = shape[-1]
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=kept.codes.device)
+            o = out.data_ptr()
+        st = _library().pmha_checkpoint_restore(_DTYPES[dtype], kept.codes.numel() // width if width else 0, width,
+                                                ctypes.byref(k), o, _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_checkpoint_restore")
+    return out
+
+
+def _shape_of(name, x):
+    """(shape, dtype) of a tensor or Checkpoint."""
+    if isinstance(x, Checkpoint):
+        if not isinstance(x.codes, _T) or not x.codes.is_cuda or not x.codes.dim() or x.dtype not in _DTYPES:
+            raise ValueError(f"{name} must keep a CUDA tensor (..., width) of float32 or bfloat16")
+        return x.codes.shape, x.dtype
+    shape, _, _, _ = _rows_of(name, x)
+    return shape, x.dtype
+
+
+@dataclasses.dataclass
+class JoinParams:
+    """How a block's output joins the residual stream:
+
+        z = norm(branch) * post;  sum = residual_scale * residual + gate * z;  out = norm(sum) * pre
+
+    post (E,): weight of the norm after the block (None: no such norm). gate: (E,), a learned one, or (G, E), row i of
+    the M rows takes gate row i / (M / G), for example one a sample (None: 1). pre (E,): weight of the norm before the
+    next block (None: no such norm). All float32 or all bfloat16 on one CUDA device."""
+    pre: torch.Tensor | None = None
+    post: torch.Tensor | None = None
+    gate: torch.Tensor | None = None
+    residual_scale: float = 1.0
+    eps: float = 1e-6
+
+    def _struct(self, dtype, width, rows, index):
+        gates = 0
+        if self.gate is not None:
+            if not isinstance(self.gate, _T) or self.gate.dim() not in (1, 2):
+                raise ValueError(f"gate must be ({width},) or (G, {width})")
+            gates = 1 if self.gate.dim() == 1 else self.gate.shape[0]
+        shape = (gates, width) if gates and self.gate.dim() == 2 else (width,)
+        return _lib.PmhaJoinParams(_DTYPES[dtype], width, _like("post", self.post, (width,), dtype, index),
+                                   _like("gate", self.gate, shape, dtype, index), gates, self.residual_scale,
+                                   _like("pre", self.pre, (width,), dtype, index), self.eps)
+
+
+def _join_inputs(params, branch, residual):
+    """(struct, shape, dtype, rows, device index, the four pointers of branch and residual)"""
+    shape, dtype = _shape_of("residual", residual)
+    dev = (residual.codes if isinstance(residual, Checkpoint) else residual).get_device()
+    width = shape[-1]
+    rows = (residual.codes if isinstance(residual, Checkpoint) else residual).numel() // width if width else 0
+    p = params._struct(dtype, width, rows, dev)
+    ptrs = []
+    for name, t in (("branch", branch), ("residual", residual)):
+        if isinstance(t, Checkpoint):
+            ptrs += [None, ctypes.byref(_kept_like(name, t, shape, dtype, dev))]
+        else:
+            ptrs += [_like(name, t, shape, dtype, dev), None]
+    return p, shape, dtype, rows, dev, ptrs
+
+
+def _join(params, branch, residual, keep_branch, keep_residual, stream):
+    p, shape, dtype, rows, dev, ptrs = _join_inputs(params, branch, residual)
+    device = (residual.codes if isinstance(residual, Checkpoint) else residual).device
+    kept = [None, None]
+    with _on(dev, stream):
+        s = torch.empty(shape, dtype=dtype, device=device)
+        out = None if params.pre is None else torch.empty(shape, dtype=dtype, device=device)
+        for i, wanted in enumerate((keep_branch, keep_residual)):
+            if wanted:
+                kept[i] = Checkpoint._empty(shape, dtype, device)
+        st = _library().pmha_join(ctypes.byref(p), rows, *ptrs, s.data_ptr(), _ptr(out),
+                                  *(None if k is None else ctypes.byref(k._struct()) for k in kept),
+                                  _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_join")
+    return s, out, kept[0], kept[1]
+
+
+def pmha_join(params: JoinParams, branch, residual, stream=None):
+    """(sum, out) of JoinParams' formulas; sum is rounded to the type and out is the norm of that (None without pre).
+    branch and residual: tensors of one shape (..., E), or Checkpoints of such, whose values then are code * scale.
+    branch None: nothing is added (without post and gate)."""
+    return _join(params, branch, residual, False, False, stream)[:2]
+
+
+def pmha_join_checkpointed(params: JoinParams, branch: torch.Tensor, residual, keep_branch: bool = True,
+                           keep_residual: bool = True, stream=None):
+    """pmha_join that keeps its tensors in 8 bits as it reads them: (sum, out, branch's Checkpoint, residual's), None for
+    one that is not kept."""
+    if keep_branch and not isinstance(branch, _T) or keep_residual and not isinstance(residual, _T):
+        raise TypeError("only a tensor can be kept: the other is a Checkpoint already, or missing")
+    return _join(params, branch, residual, keep_branch, keep_residual, stream)
+
+
+def pmha_join_backward_workspace_size(params: JoinParams, x: torch.Tensor) -> int:
+    """Bytes of pmha_join_backward's workspace for tokens like x (its sum or dsum)."""
+    shape, rows, width, dev = _rows_of("x", x)
+    p = params._struct(x.dtype, width, rows, dev)
+    return _join_size(p, rows)
+
+
+def _join_size(p, rows) -> int:
+    need = _library().pmha_join_backward_workspace_size(ctypes.byref(p), rows)
+    if need == _NO_SIZE:
+        message = (_lib.load().pmha_last_error() or b"").decode()
+        raise PmhaError(5 if "too many" in message else 1, "pmha_join_backward", message)
+    return need
+
+
+def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dout: torch.Tensor | None,
+                       dsum: torch.Tensor | None = None, input_grads: bool = True, param_grads: bool = True,
+                       workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of pmha_join: {"dbranch", "dresidual", "dpre", "dpost", "dgate"}, the first two in the type of the tokens,
+    the others in float32 (None for parameters that are not there). branch: the tensor or its Checkpoint (None where
+    there is neither post nor gate); sum: what the forward pass returned (None without pre); dout: the gradient of
+    out (None without pre); dsum: the gradient of sum from its other uses. Without post, gate and residual scale
+    dbranch and dresidual are one tensor."""
+    like = dsum if dout is None else dout
+    if like is None:
+        raise ValueError("dout or dsum is needed")
+    shape, rows, width, dev = _rows_of("dsum" if dout is None else "dout", like)
+    dtype = like.dtype
+    p = params._struct(dtype, width, rows, dev)
+    s = _like("sum", sum, shape, dtype, dev)
+    dy, ds = _like("dout", dout, shape, dtype, dev), _like("dsum", dsum, shape, dtype, dev)
+    if isinstance(branch, Checkpoint):
+        b, bk = None, ctypes.byref(_kept_like("branch", branch, shape, dtype, dev))
+    else:
+        b, bk = _like("branch", branch, shape, dtype, dev), None
+    lib = _library()
+    wanted = param_grads and (params.pre is not None or params.post is not None or params.gate is not None)
+    need = _join_size(p, rows) if wanted else 0
+    alone = params.post is None and params.gate is None and params.residual_scale == 1.0
+    with _on(dev, stream):
+        dr = torch.empty_like(like) if input_grads else None
+        db = dr if alone or not input_grads else torch.empty_like(like)
+        grads = [None if not param_grads or t is None else torch.empty(t.shape, dtype=torch.float32, device=like.device)
+                 for t in (params.post, params.gate, params.pre)]
+        wp, wn, keep = _scratch(like, need, workspace)
+        st = lib.pmha_join_backward(ctypes.byref(p), rows, b, bk, s, dy, ds, None if alone else _ptr(db), _ptr(dr),
+                                    *map(_ptr, grads), wp, wn, _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_join_backward")
+    return {"dbranch": db, "dresidual": dr, "dpre": grads[2], "dpost": grads[0], "dgate": grads[1]}
 
 
 class PackedEncoderLayer:

@@ -47,11 +47,22 @@ class PmhaFfnGrads(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("wg", "wu", "wd", "bg", "bu", "bd")]
 
 
+class PmhaKept(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scale", _vp)]
+
+
+class PmhaJoinParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("width", _i64), ("post", _vp), ("gate", _vp), ("gates", _i64),
+                ("residual_scale", ctypes.c_float), ("pre", _vp), ("eps", ctypes.c_float)]
+
+
 _P = ctypes.POINTER(PmhaParams)
 _F = ctypes.POINTER(PmhaFfnParams)
 _FQ = ctypes.POINTER(PmhaFfnQuantized)
 _FG = ctypes.POINTER(PmhaFfnGrads)
 _G = ctypes.POINTER(PmhaGrads)
+_K = ctypes.POINTER(PmhaKept)
+_J = ctypes.POINTER(PmhaJoinParams)
 _I64P = ctypes.POINTER(ctypes.c_int64)
 
 SIGNATURES = {
@@ -86,6 +97,11 @@ SIGNATURES = {
     "pmha_ffn_forward_quantized": (ctypes.c_int, [_F, _FQ, _vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
     "pmha_ffn_backward_workspace_size": (_sz, [_F, _i64]),
     "pmha_ffn_backward": (ctypes.c_int, [_F, _vp, _vp, _i64, _vp, _FG, _vp, _sz, _vp]),
+    "pmha_checkpoint": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _vp, _K, _vp]),
+    "pmha_checkpoint_restore": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _K, _vp, _vp]),
+    "pmha_join": (ctypes.c_int, [_J, _i64, _vp, _K, _vp, _K, _vp, _vp, _K, _K, _vp]),
+    "pmha_join_backward_workspace_size": (_sz, [_J, _i64]),
+    "pmha_join_backward": (ctypes.c_int, [_J, _i64, _vp, _K, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "pmha_clip_grad_norm_workspace_size": (_sz, [_i64]),
     "pmha_clip_grad_norm": (ctypes.c_int, [_i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }

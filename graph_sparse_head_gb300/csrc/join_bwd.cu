@@ -1,0 +1,480 @@
+// Backward pass of the join (join.cu has the formulas).
+#include "join.cuh"
+
+namespace pmha {
+namespace {
+
+// ---------------------------------------------------------------- backward
+struct JoinBwdArgs {
+    Source branch;
+    const void *sum, *dy, *ds;  // dy null: no norm after the join
+    const void *post, *gate, *pre;
+    void *dbranch, *dres;
+    float *part_pre, *part_branch;  // (grid, width) partial sums of dn s r and of D branch r_b, or null
+    long long rows, per_gate;       // rows that share a gate (all, without one)
+    int blocks_per_gate;            // blocks that share them
+    int width;
+    float alpha, eps;
+};
+
+// Steps of a block: so many terms of a sum over rows at most are added in
+// float32 one after the other; the blocks' partial rows are added as pairs of floats.
+constexpr int kSteps = 128;
+
+// A team (join.cuh) walks rows of one gate and keeps its columns' two sums over rows in
+// registers; a block adds its teams' through shared memory and writes one partial row of each.
+template <typename T, int VEC, int NV, int LPR, bool KEPT>
+__global__ void __launch_bounds__(kThreads) k_join_bwd(JoinBwdArgs a)
+{
+    extern __shared__ float shw[];  // width values
+    __shared__ TeamSums sh;
+    constexpr int kRows = kThreads / LPR, N = NV * VEC;  // rows of a block's step
+    constexpr int kPerWarp = LPR < 32 ? 32 / LPR : 1;
+    const int l = threadIdx.x % LPR;
+    int turn = 0;
+    const long long gate = blockIdx.x / a.blocks_per_gate;
+    const long long begin = gate * a.per_gate, end = begin + a.per_gate;
+    const long long step = (long long)a.blocks_per_gate * kRows;
+    const float inv_width = 1.f / (float)a.width;
+    Vals<T, VEC> wpre[NV], wpost[NV], wgate[NV];
+    float q[N], pb[N];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * LPR + l) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            wpre[j].v[i] = wpost[j].v[i] = wgate[j].v[i] = from_f<T>(1.f);
+            q[j * VEC + i] = pb[j * VEC + i] = 0.f;
+        }
+        if (c < a.width) {
+            if (a.pre) load<T, VEC>((const T *)a.pre + c, wpre[j].v);
+            if (a.post) load<T, VEC>((const T *)a.post + c, wpost[j].v);
+            if (a.gate) load<T, VEC>((const T *)a.gate + gate * a.width + c, wgate[j].v);
+        }
+    }
+    const bool with_branch = a.branch.any();
+    // a warp's threads walk together: row0 is the first of its rows
+    for (long long row0 = begin + (long long)(blockIdx.x % a.blocks_per_gate) * kRows +
+                          (int)threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
+         row0 < end; row0 += step) {
+        const long long row = row0 + (LPR < 32 ? (int)(threadIdx.x & 31) / LPR : 0), base = row * a.width;
+        const bool live = row < end;
+        float D[N], f[N], b[N];
+        Vals<T, VEC> g[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + l) * VEC;
+            float (&Dj)[VEC] = *reinterpret_cast<float (*)[VEC]>(D + j * VEC);
+            float (&fj)[VEC] = *reinterpret_cast<float (*)[VEC]>(f + j * VEC);
+            float (&bj)[VEC] = *reinterpret_cast<float (*)[VEC]>(b + j * VEC);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                Dj[i] = fj[i] = bj[i] = 0.f;
+                g[j].v[i] = from_f<T>(0.f);
+            }
+            if (live && c < a.width) {
+                if (a.ds) load_row<T, VEC>(a.ds, base + c, Dj);
+                if (a.dy) {
+                    load<T, VEC>((const T *)a.dy + base + c, g[j].v);
+                    load_row<T, VEC>(a.sum, base + c, fj);
+                }
+                if constexpr (KEPT) load_kept<VEC>(a.branch.k, row, c, a.width, bj);
+                else if (with_branch) load_row<T, VEC>(a.branch.p, base + c, bj);
+            }
+        }
+        if (a.dy) {
+            float sc, as = 0.f;
+            const float r = row_root<N, LPR>(f, a.width, a.eps, &sc, sh, turn);  // of f as it is now, times sc
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    f[j * VEC + i] *= r;
+                    as = fmaf(to_f<T>(g[j].v[i]) * to_f<T>(wpre[j].v[i]), f[j * VEC + i], as);
+                }
+            const float k = team_sum<LPR>(as, sh, turn) * inv_width, rd = r * sc;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float gi = to_f<T>(g[j].v[i]), u = f[j * VEC + i];
+                    q[j * VEC + i] = fmaf(gi, u, q[j * VEC + i]);
+                    D[j * VEC + i] = fmaf(rd, fmaf(-u, k, gi * to_f<T>(wpre[j].v[i])), D[j * VEC + i]);
+                }
+        }
+        if (a.dres) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * LPR + l) * VEC;
+                if (!(live && c < a.width)) continue;
+                Vals<T, VEC> o;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o.v[i] = from_f<T>(a.alpha * D[j * VEC + i]);
+                store<T, VEC>((T *)a.dres + base + c, o.v);
+            }
+        }
+        float rb = 1.f, scb = 1.f;
+        if (a.post) {
+            rb = row_root<N, LPR>(b, a.width, a.eps, &scb, sh, turn);
+#pragma unroll
+            for (int i = 0; i < N; ++i) b[i] *= rb;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) pb[i] = fmaf(D[i], b[i], pb[i]);
+        if (!a.dbranch) continue;
+        float bs = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                D[j * VEC + i] *= to_f<T>(wgate[j].v[i]) * to_f<T>(wpost[j].v[i]);
+                bs = fmaf(D[j * VEC + i], b[j * VEC + i], bs);
+            }
+        if (a.post) {
+            const float k = team_sum<LPR>(bs, sh, turn) * inv_width, rd = rb * scb;
+#pragma unroll
+            for (int i = 0; i < N; ++i) D[i] = rd * fmaf(-b[i], k, D[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + l) * VEC;
+            if (!(live && c < a.width)) continue;
+            Vals<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.v[i] = from_f<T>(D[j * VEC + i]);
+            store<T, VEC>((T *)a.dbranch + base + c, o.v);
+        }
+    }
+    // a warp's rows, then the warps (or teams of warps) one after the other
+    constexpr int kTeam = LPR < 32 ? 32 : LPR;
+    const int team = threadIdx.x / kTeam;
+    __syncthreads();
+    auto put = [&](float (&v)[N], float *part) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int o = LPR; o < 32; o <<= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+        for (int t = 0; t < kThreads / kTeam; ++t) {
+            if (team == t && (int)threadIdx.x % kTeam < LPR) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = (j * LPR + l) * VEC;
+                    if (c < a.width)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) shw[c + i] = t ? shw[c + i] + v[j * VEC + i] : v[j * VEC + i];
+                }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.width; c += kThreads) part[(long long)blockIdx.x * a.width + c] = shw[c];
+        __syncthreads();
+    };
+    if (a.part_pre) put(q, a.part_pre);
+    if (a.part_branch) put(pb, a.part_branch);
+}
+
+// Wide rows: a block walks the rows of its gate's part; the partial sums live in its rows of part_pre and part_branch
+// (each column belongs to one thread).
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) k_join_bwd_wide(JoinBwdArgs a)
+{
+    __shared__ float sh[kThreads / 32];
+    const int first = (int)threadIdx.x * VEC, stride = kThreads * VEC;
+    const long long gate = blockIdx.x / a.blocks_per_gate;
+    const long long begin = gate * a.per_gate, end = begin + a.per_gate;
+    const long long row_first = begin + blockIdx.x % a.blocks_per_gate;
+    const float inv_width = 1.f / (float)a.width;
+    float *pq = a.part_pre ? a.part_pre + (long long)blockIdx.x * a.width : nullptr;
+    float *pp = a.part_branch ? a.part_branch + (long long)blockIdx.x * a.width : nullptr;
+    for (long long row = row_first; row < end; row += a.blocks_per_gate) {
+        const long long base = row * a.width;
+        auto square_sum = [&](const Source &s) {
+            return [&, s](float sc) {
+                float ss = 0.f;
+                for (int c = first; c < a.width; c += stride) {
+                    float v[VEC];
+                    load_source<T, VEC>(s, row, c, a.width, v);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) ss = fmaf(v[i] * sc, v[i] * sc, ss);
+                }
+                return ss;
+            };
+        };
+        auto largest = [&](const Source &s) {
+            return [&, s]() {
+                float m = 0.f;
+                for (int c = first; c < a.width; c += stride) {
+                    float v[VEC];
+                    load_source<T, VEC>(s, row, c, a.width, v);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(v[i]));
+                }
+                return m;
+            };
+        };
+        float r = 0.f, sc = 1.f, k = 0.f, rb = 1.f, scb = 1.f;
+        if (a.dy) {
+            const Source s = {a.sum, {nullptr, nullptr}};
+            r = block_root(sh, a.width, a.eps, &sc, square_sum(s), largest(s));
+            float as = 0.f;
+            for (int c = first; c < a.width; c += stride) {
+                float f[VEC], g[VEC], w[VEC];
+                load_row<T, VEC>(a.sum, base + c, f);
+                load_row<T, VEC>(a.dy, base + c, g);
+                load_row<T, VEC>(a.pre, c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) as = fmaf(g[i] * w[i], f[i] * sc * r, as);
+            }
+            k = block_sum(as, sh) * inv_width;
+        }
+        if (a.post) rb = block_root(sh, a.width, a.eps, &scb, square_sum(a.branch), largest(a.branch));
+        // the columns at c: D, and the branch times its 1 / rms
+        auto columns = [&](int c, float (&D)[VEC], float (&b)[VEC], float (&gu)[VEC]) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) D[i] = b[i] = gu[i] = 0.f;
+            if (a.ds) load_row<T, VEC>(a.ds, base + c, D);
+            if (a.dy) {
+                float f[VEC], g[VEC], w[VEC];
+                load_row<T, VEC>(a.sum, base + c, f);
+                load_row<T, VEC>(a.dy, base + c, g);
+                load_row<T, VEC>(a.pre, c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float u = f[i] * sc * r;
+                    gu[i] = g[i] * u;
+                    D[i] = fmaf(r * sc, fmaf(-u, k, g[i] * w[i]), D[i]);
+                }
+            }
+            if (a.branch.any()) {
+                load_source<T, VEC>(a.branch, row, c, a.width, b);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) b[i] = a.post ? b[i] * scb * rb : b[i];
+            }
+        };
+        auto through = [&](int c, float (&w)[VEC]) {  // gate post
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = 1.f;
+            if (a.gate) load_row<T, VEC>(a.gate, gate * a.width + c, w);
+            if (a.post) {
+                float p[VEC];
+                load_row<T, VEC>(a.post, c, p);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) w[i] *= p[i];
+            }
+        };
+        float kb = 0.f;
+        if (a.post && a.dbranch) {
+            float bs = 0.f;
+            for (int c = first; c < a.width; c += stride) {
+                float D[VEC], b[VEC], w[VEC], gu[VEC];
+                columns(c, D, b, gu);
+                through(c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) bs = fmaf(D[i] * w[i], b[i], bs);
+            }
+            kb = block_sum(bs, sh) * inv_width;
+        }
+        for (int c = first; c < a.width; c += stride) {
+            float D[VEC], b[VEC], w[VEC], gu[VEC];
+            Vals<T, VEC> o;
+            columns(c, D, b, gu);
+            if (pq) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) pq[c + i] = row == row_first ? gu[i] : pq[c + i] + gu[i];
+            }
+            if (pp) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) pp[c + i] = row == row_first ? D[i] * b[i] : fmaf(D[i], b[i], pp[c + i]);
+            }
+            if (a.dres) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o.v[i] = from_f<T>(a.alpha * D[i]);
+                store<T, VEC>((T *)a.dres + base + c, o.v);
+            }
+            if (a.dbranch) {
+                through(c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    o.v[i] = from_f<T>(a.post ? rb * scb * fmaf(-b[i], kb, D[i] * w[i]) : D[i] * w[i]);
+                store<T, VEC>((T *)a.dbranch + base + c, o.v);
+            }
+        }
+    }
+}
+
+struct JoinSumArgs {
+    const float *part_pre, *part_branch;
+    const void *post, *gate;
+    float *dpre, *dpost, *dgate;  // null: not wanted
+    long long gates;              // rows of dgate
+    int blocks_per_gate, width, tiles;
+};
+// One block: eight columns of one output row (dpre, dpost, or a row of dgate), 32
+// threads a column in a fixed order, as pairs.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_join_sums(JoinSumArgs a)
+{
+    __shared__ Two sh[32][8];
+    const int c8 = threadIdx.x & 7, c = (int)(blockIdx.x % a.tiles) * 8 + c8, t = threadIdx.x >> 3;
+    long long what = blockIdx.x / a.tiles;
+    if (!a.dpre) ++what;
+    if (!a.dpost && what > 0) ++what;
+    const long long gate = what - 2;
+    const float *part = what == 0 ? a.part_pre : a.part_branch;
+    const long long n = what < 2 ? a.gates * a.blocks_per_gate : a.blocks_per_gate;
+    const long long at = what < 2 ? 0 : gate * a.blocks_per_gate;
+    const bool weighted = what == 1 && a.gate;
+    Two s = {0.f, 0.f};
+    if (c < a.width) {
+#pragma unroll 4
+        for (long long i = t; i < n; i += 32) {
+            const float v = part[(at + i) * a.width + c];
+            if (weighted) {
+                const float g = to_f<T>(((const T *)a.gate)[i / a.blocks_per_gate * a.width + c]);
+                const float p = __fmul_rn(v, g);
+                s = add(s, Two{p, __fmaf_rn(v, g, -p)});
+            } else {
+                s = add(s, Two{v, 0.f});
+            }
+        }
+    }
+    sh[t][c8] = s;
+    __syncthreads();
+    if (t == 0 && c < a.width) {
+        for (int i = 1; i < 32; ++i) s = add(s, sh[i][c8]);
+        const float v = s.hi + s.lo;
+        if (what == 0) a.dpre[c] = v;
+        else if (what == 1) a.dpost[c] = v;
+        else a.dgate[gate * a.width + c] = a.post ? v * to_f<T>(((const T *)a.post)[c]) : v;
+    }
+}
+
+pmha_status check_join_backward(const pmha_join_params *p, int64_t rows)
+{
+    pmha_status st = check_join("pmha_join_backward", p, rows);
+    if (st != PMHA_OK) return st;
+    if ((p->gates + 2) * ((p->width + 7) / 8) > ((int64_t)1 << 31) - 1) {  // blocks of one launch
+        set_error("pmha_join_backward: %lld gates of width %lld are too many", (long long)p->gates, (long long)p->width);
+        return PMHA_ERR_UNSUPPORTED;
+    }
+    return PMHA_OK;
+}
+
+// Blocks that share the rows of a gate, each of which writes a partial row: together at most about four a SM, more where
+// a block would take more than kSteps steps.
+int64_t bwd_blocks(pmha_dtype dt, int64_t per_gate, int64_t gates, int64_t width)
+{
+    const Shape s = join_shape(dt, width);
+    const int64_t per = s.lpr ? kThreads / s.lpr : 1, steps = (per_gate + per - 1) / per;
+    const int64_t full = std::max<int64_t>(1, (int64_t)num_sms() * 4 / gates);
+    return std::max<int64_t>(1, std::min(steps, std::max(full, (steps + kSteps - 1) / kSteps)));
+}
+
+}  // namespace
+}  // namespace pmha
+
+using namespace pmha;
+
+extern "C" {
+
+size_t pmha_join_backward_workspace_size(const pmha_join_params *params, int64_t rows)
+{
+    if (check_join_backward(params, rows) != PMHA_OK) return SIZE_MAX;
+    if (rows == 0) return 0;
+    const int64_t gates = params->gate ? params->gates : 1;
+    const size_t one = (size_t)(bwd_blocks(params->dtype, rows / gates, gates, params->width) * gates) *
+                       (size_t)params->width * 4;
+    return 2 * ((one + 255) & ~(size_t)255);
+}
+
+pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, const void *branch,
+                               const pmha_kept *branch_kept, const void *sum, const void *dout, const void *dsum,
+                               void *dbranch, void *dresidual, float *dpost, float *dgate, float *dpre, void *workspace,
+                               size_t workspace_bytes, pmha_stream stream)
+{
+    pmha_status st = check_join_backward(params, rows);
+    if (st != PMHA_OK) return st;
+    const pmha_join_params &p = *params;
+    cudaStream_t cs = (cudaStream_t)stream;
+    const int64_t w = p.width, gates = p.gate ? p.gates : 1;
+    if (!aligned(dpost, 16) || !aligned(dgate, 16) || !aligned(dpre, 16) || (dpost && !p.post) || (dgate && !p.gate) ||
+        (dpre && !p.pre)) {
+        set_error("pmha_join_backward: dpost, dgate or dpre is not 16-byte aligned, or has no parameter");
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (rows == 0) {
+        if (dpost) PMHA_CUDA_TRY(cudaMemsetAsync(dpost, 0, (size_t)w * 4, cs));
+        if (dgate) PMHA_CUDA_TRY(cudaMemsetAsync(dgate, 0, (size_t)(w * gates) * 4, cs));
+        if (dpre) PMHA_CUDA_TRY(cudaMemsetAsync(dpre, 0, (size_t)w * 4, cs));
+        return PMHA_OK;
+    }
+    const bool need_branch = (p.post && dbranch) || dpost || dgate;
+    if ((branch && branch_kept) || (need_branch && !branch && !branch_kept) || (dout != nullptr) != (p.pre != nullptr) ||
+        (dout && !sum) || (!dout && !dsum)) {
+        set_error("pmha_join_backward: needs one form of the branch (with post or a gate's gradient), dout and sum just if "
+                  "pre is set, and dout or dsum");
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (!aligned(branch, 16) || !whole(branch_kept) || !aligned(sum, 16) || !aligned(dout, 16) || !aligned(dsum, 16) ||
+        !aligned(dbranch, 16) || !aligned(dresidual, 16)) {
+        set_error("pmha_join_backward: a pointer is not 16-byte aligned, or the kept branch lacks its codes or scales");
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const size_t nb = (size_t)(rows * w) * bytes_of(p.dtype), wb = (size_t)w * bytes_of(p.dtype), fb = (size_t)w * 4;
+    const Span ins[] = {{branch, nb}, codes_of(branch_kept, rows, w), scales_of(branch_kept, rows, w), {sum, nb},
+                        {dout, nb}, {dsum, nb}, {p.post, wb}, {p.pre, wb}, {p.gate, wb * (size_t)p.gates}};
+    const Span outs[] = {{dbranch, nb}, {dresidual, nb}, {dpost, fb}, {dgate, fb * (size_t)gates}, {dpre, fb}};
+    if (any_overlap(ins, outs)) {
+        set_error("pmha_join_backward: an output overlaps an input or another output");
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (!dbranch && !dresidual && !dpost && !dgate && !dpre) return PMHA_OK;
+    const bool sums = dpost || dgate || dpre;
+    const size_t need = pmha_join_backward_workspace_size(params, rows);
+    if (sums && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))) {
+        set_error("pmha_join_backward: workspace needs %zu bytes, 256-byte aligned (got %zu at %p)", need, workspace_bytes,
+                  workspace);
+        return PMHA_ERR_WORKSPACE;
+    }
+    const int64_t per_gate = rows / gates, blocks = bwd_blocks(p.dtype, per_gate, gates, w);
+    float *part_pre = dpre ? (float *)workspace : nullptr;
+    float *part_branch = dpost || dgate ? (float *)((uint8_t *)workspace + need / 2) : nullptr;
+    Source b = source(branch, branch_kept);
+    if (!need_branch) b = Source{nullptr, {nullptr, nullptr}};
+    JoinBwdArgs a{b, sum, dout, dsum, p.post, p.gate, p.pre, dbranch, dresidual, part_pre, part_branch, rows, per_gate,
+                  (int)blocks, (int)w, p.residual_scale, p.eps};
+    if (!need_branch) a.post = nullptr;
+    const Shape s = join_shape(p.dtype, w);
+    const unsigned grid = (unsigned)(blocks * gates);
+    {
+        StageTimer timer(branch_kept ? "join_backward_kept" : "join_backward", cs);
+        if (s.lpr)
+            join_dispatch(p.dtype, s, [&](auto t) {
+                using G = decltype(t);
+                using T = typename G::type;
+                if (b.k.codes) k_join_bwd<T, G::vec, G::nv, G::lpr, true><<<grid, kThreads, (size_t)w * 4, cs>>>(a);
+                else k_join_bwd<T, G::vec, G::nv, G::lpr, false><<<grid, kThreads, (size_t)w * 4, cs>>>(a);
+            });
+        else
+            dispatch_wide(p.dtype, s.vec, [&](auto t) {
+                using G = decltype(t);
+                k_join_bwd_wide<typename G::type, G::vec><<<grid, kThreads, 0, cs>>>(a);
+            });
+    }
+    count_launch();
+    PMHA_CUDA_TRY(cudaGetLastError());
+    if (sums) {
+        StageTimer timer("join_sums", cs);
+        const int tiles = (int)((w + 7) / 8);
+        const int64_t outs_n = (dpre ? 1 : 0) + (dpost ? 1 : 0) + (dgate ? gates : 0);
+        JoinSumArgs q{part_pre, part_branch, p.post, p.gate, dpre, dpost, dgate, gates, (int)blocks, (int)w, tiles};
+        const unsigned n = (unsigned)(outs_n * tiles);
+        if (p.dtype == PMHA_BF16) k_join_sums<__nv_bfloat16><<<n, kThreads, 0, cs>>>(q);
+        else k_join_sums<float><<<n, kThreads, 0, cs>>>(q);
+        count_launch();
+        PMHA_CUDA_TRY(cudaGetLastError());
+    }
+    return PMHA_OK;
+}
+
+}  // extern "C"

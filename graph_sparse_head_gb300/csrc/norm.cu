@@ -12,88 +12,26 @@
 // bf16 with a residual: 320,000 x 128 in 50.5 us, 6.5 TB/s (96 % of a copy). The
 // 8-bit output is bound by its some 30 instructions a value: 64,000 x 128 in 17 us.
 #include <cuda_fp8.h>
-#include <math.h>
 
 #include <algorithm>
 
-#include "pmha_internal.h"
+#include "rows.cuh"
 
 namespace pmha {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr unsigned kFull = 0xffffffffu;
 constexpr float kScaleMin = 5.42101086e-20f;  // 2^-64
-// A row whose squares' sum leaves float32 is taken again times the power of two
-// that brings its largest magnitude into [2, 4) (exact but for values 2^-120 of
-// it), with eps times its square: the norm does not change, and no sum of up to 2^24 squares
-// overflows. A fixed factor would not do: 2^-64, taken before, left rows from 2^128 / sqrt(width) infinite.
-constexpr float kMostSquares = 3.0e38f;
 // The 8-bit output's statistics are pairs of floats, and the second float of 1 / (mean square) is a normal
 // number up to 2^102: its rows are scaled from 2^96 on.
 constexpr float kMostPairs = 7.9228163e28f;
-__device__ __forceinline__ float down_scale(float most)
-{
-    const uint32_t e = __float_as_uint(most) >> 23;  // exponent + 127
-    return e >= 128 && e < 255 ? __uint_as_float((255 - e) << 23) : 1.f;  // 1 for infinities and NaN too
-}
-
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-// VEC consecutive values as one load or store (16, 4 or 2 bytes).
-template <typename T, int VEC> struct Pack;
-template <> struct Pack<float, 4> { using type = uint4; };
-template <> struct Pack<float, 1> { using type = uint32_t; };
-template <> struct Pack<__nv_bfloat16, 8> { using type = uint4; };
-template <> struct Pack<__nv_bfloat16, 2> { using type = uint32_t; };
-template <> struct Pack<__nv_bfloat16, 1> { using type = uint16_t; };
-// VEC bytes
-template <int VEC> struct Bytes;
-template <> struct Bytes<8> { using type = uint2; };
-template <> struct Bytes<4> { using type = uint32_t; };
-template <> struct Bytes<2> { using type = uint16_t; };
-template <> struct Bytes<1> { using type = uint8_t; };
-
-template <typename T, int VEC>
-__device__ __forceinline__ void load(const T *p, T (&v)[VEC])
-{
-    *reinterpret_cast<typename Pack<T, VEC>::type *>(v) = *reinterpret_cast<const typename Pack<T, VEC>::type *>(p);
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store(T *p, const T (&v)[VEC])
-{
-    *reinterpret_cast<typename Pack<T, VEC>::type *>(p) = *reinterpret_cast<const typename Pack<T, VEC>::type *>(v);
-}
-template <typename T, int VEC> struct alignas(sizeof(typename Pack<T, VEC>::type)) Vals {
-    T v[VEC];
-};
-
 // ---------------------------------------------------------------- pairs of floats
 // An unevaluated sum hi + lo (about 46 bits), for the 8-bit output: a value
 // next to a border of the E4M3 grid must fall where exact arithmetic puts it,
 // and 32-bit sums and products would move about 5 values in a million.
-struct Two {
-    float hi, lo;
-};
-__device__ __forceinline__ Two two_sum(float a, float b)
-{
-    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
-}
 __device__ __forceinline__ Two two_mul(float a, float b)
 {
     const float p = __fmul_rn(a, b);
     return {p, __fmaf_rn(a, b, -p)};
-}
-__device__ __forceinline__ Two add(Two a, Two b)
-{
-    const Two s = two_sum(a.hi, b.hi);
-    return {s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
 }
 __device__ __forceinline__ float rcp(float x)
 {
@@ -329,32 +267,6 @@ __global__ void __launch_bounds__(kThreads) k_rms_norm(NormArgs a)
     }
 }
 
-__device__ __forceinline__ float block_sum(float v, float *sh)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v += sh[i];
-    __syncthreads();
-    return v;
-}
-
-__device__ __forceinline__ float block_max(float v, float *sh)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v = fmaxf(v, sh[i]);
-    __syncthreads();
-    return v;
-}
-
 // Rows of more than 1024 values: one block a row.
 template <typename T, int VEC, bool Q8>
 __global__ void __launch_bounds__(kThreads) k_rms_norm_wide(NormArgs a)
@@ -465,13 +377,6 @@ struct NormBwdArgs {
     float eps;
 };
 
-// 16 bytes from global to shared memory, or zeros
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
 template <typename T, int VEC, int NV>
 constexpr int kRingOf = VEC * sizeof(T) == 16 && NV <= 2 ? 4 / NV : 0;
 
@@ -722,98 +627,6 @@ __global__ void __launch_bounds__(kThreads) k_sum_rows(const float *__restrict__
 }
 
 // ---------------------------------------------------------------- host side
-bool overlap(const void *a, size_t an, const void *b, size_t bn)
-{
-    if (!a || !b || !an || !bn) return false;
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + bn && y < x + an;
-}
-bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-size_t bytes_of(pmha_dtype dt) { return dt == PMHA_BF16 ? 2 : 4; }
-
-pmha_status check_rows(const char *who, pmha_dtype dt, int64_t rows, int64_t width)
-{
-    if (dt != PMHA_F32 && dt != PMHA_BF16) {
-        set_error("%s: dtype %d is neither PMHA_F32 nor PMHA_BF16", who, (int)dt);
-        return PMHA_ERR_INVALID_ARG;
-    }
-    if (rows < 0 || width < 1 || width > ((int64_t)1 << 24) || rows > ((int64_t)1 << 31) - 1 ||
-        rows * width > (int64_t)1 << 46) {
-        set_error("%s: rows %lld must be 0 .. 2^31 - 1, width %lld 1 .. 2^24, and their product at most 2^46", who,
-                  (long long)rows, (long long)width);
-        return PMHA_ERR_INVALID_ARG;
-    }
-    return PMHA_OK;
-}
-
-// The kernel shape of a width: values a piece, pieces a lane, lanes a row; 0 lanes: one block a row.
-struct Shape {
-    int vec, nv, lpr;
-};
-Shape shape_of(pmha_dtype dt, int64_t width)
-{
-    const int v = dt == PMHA_BF16 ? 8 : 4;
-    const int vec = width % v == 0 ? v : (dt == PMHA_BF16 && width % 2 == 0 ? 2 : 1);
-    if (width > 1024) return {vec, 0, 0};
-    const int64_t pieces = width / vec;
-    if (vec == v) {
-        if (pieces <= 8) return {vec, 1, 8};
-        if (pieces <= 16) return {vec, 1, 16};
-        if (pieces <= 32) return {vec, 1, 32};
-        if (pieces <= 64) return {vec, 2, 32};
-        if (pieces <= 128) return {vec, 4, 32};
-        return {vec, 8, 32};
-    }
-    return pieces <= 256 / vec ? Shape{vec, 8 / vec, 32} : Shape{vec, 32 / vec, 32};
-}
-
-// F(type tag, vec, nv, lpr) for every shape that shape_of gives.
-template <typename T, int V, int N, int L> struct Tag {
-    using type = T;
-    static constexpr int vec = V, nv = N, lpr = L;
-};
-template <typename F>
-void dispatch(pmha_dtype dt, Shape s, F f)
-{
-    using B = __nv_bfloat16;
-    if (dt == PMHA_BF16) {
-        if (s.vec == 8) {
-            if (s.lpr == 8) f(Tag<B, 8, 1, 8>());
-            else if (s.lpr == 16) f(Tag<B, 8, 1, 16>());
-            else if (s.nv == 1) f(Tag<B, 8, 1, 32>());
-            else if (s.nv == 2) f(Tag<B, 8, 2, 32>());
-            else f(Tag<B, 8, 4, 32>());
-        } else if (s.vec == 2) {
-            if (s.nv == 4) f(Tag<B, 2, 4, 32>());
-            else f(Tag<B, 2, 16, 32>());
-        } else {
-            if (s.nv == 8) f(Tag<B, 1, 8, 32>());
-            else f(Tag<B, 1, 32, 32>());
-        }
-    } else if (s.vec == 4) {
-        if (s.lpr == 8) f(Tag<float, 4, 1, 8>());
-        else if (s.lpr == 16) f(Tag<float, 4, 1, 16>());
-        else if (s.nv == 1) f(Tag<float, 4, 1, 32>());
-        else if (s.nv == 2) f(Tag<float, 4, 2, 32>());
-        else if (s.nv == 4) f(Tag<float, 4, 4, 32>());
-        else f(Tag<float, 4, 8, 32>());
-    } else {
-        if (s.nv == 8) f(Tag<float, 1, 8, 32>());
-        else f(Tag<float, 1, 32, 32>());
-    }
-}
-template <typename F>
-void dispatch_wide(pmha_dtype dt, int vec, F f)
-{
-    using B = __nv_bfloat16;
-    if (dt == PMHA_BF16) {
-        if (vec == 8) f(Tag<B, 8, 1, 32>());
-        else if (vec == 2) f(Tag<B, 2, 1, 32>());
-        else f(Tag<B, 1, 1, 32>());
-    } else if (vec == 4) f(Tag<float, 4, 1, 32>());
-    else f(Tag<float, 1, 1, 32>());
-}
-
 // Blocks of the backward pass, each of which writes one partial row: four a SM keep its memory pipe full, more where a
 // block would take more than kSteps steps. Blocks that take one wide row at a time come in whole fives a SM, which are
 // resident (100,000 x 2,048: 677 us, with four a SM 715, with just as many as kSteps needs 782); for the others

@@ -493,6 +493,95 @@ pmha_status pmha_clip_grad_norm(int64_t n_tensors, const void *const *grads, voi
                                 const pmha_dtype *dtype, float max_norm, float *norm, void *workspace,
                                 size_t workspace_bytes, pmha_stream stream);
 
+/* ------------------------------------------------------------------------
+ * The join of a block's output with the residual stream, for stacks whose
+ * blocks are normalised on both sides, gated, or added to a scaled residual;
+ * and the tensors that a training step keeps in 8 bits between its passes.
+ */
+
+/*
+ * A tensor of `rows` rows kept in 8 bits, as groups of 32 values along each row
+ * (the last group of a row may be shorter):
+ *  codes  device int8 (rows, width);
+ *  scale  device bfloat16 (rows, ceil(width / 32)): max|group| / 127 rounded up,
+ *         at least 2^-100; a code is value / scale to the nearest integer (ties
+ *         to even, as in exact arithmetic). value ~ code * scale.
+ * A group with an infinity or a NaN gets a NaN scale. Both 16-byte aligned.
+ */
+typedef struct {
+    void *codes;
+    void *scale;
+} pmha_kept;
+
+/*
+ * pmha_checkpoint - keeps x (rows, width) of `dtype` in 8 bits.
+ * pmha_checkpoint_restore - code * scale rounded to `dtype`.
+ * rows may be 0. Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_CUDA.
+ */
+pmha_status pmha_checkpoint(pmha_dtype dtype, int64_t rows, int64_t width, const void *x, const pmha_kept *kept,
+                            pmha_stream stream);
+pmha_status pmha_checkpoint_restore(pmha_dtype dtype, int64_t rows, int64_t width, const pmha_kept *kept, void *out,
+                                    pmha_stream stream);
+
+/* Device pointers in `dtype`, 16-byte aligned. */
+typedef struct {
+    pmha_dtype dtype;
+    int64_t width;
+    const void *post;      /* (width) weight of the norm after the block; NULL: no such norm */
+    const void *gate;      /* (gates, width) or NULL: none */
+    int64_t gates;         /* 0 without a gate; row i takes gate row i / (rows / gates), so gates divides rows */
+    float residual_scale;  /* finite */
+    const void *pre;       /* (width) weight of the norm before the next block; NULL: no such norm */
+    float eps;             /* of both norms: finite, at least 1e-30 */
+} pmha_join_params;
+
+/*
+ * pmha_join - for each row
+ *   z   = branch / sqrt(mean(branch^2) + eps) * post   (without post: branch)
+ *   sum = residual_scale * residual + gate * z, rounded to dtype
+ *   out = sum / sqrt(mean(sum^2) + eps) * pre          (of the rounded sum)
+ *  branch    device (rows, width), the block's output, or branch_kept in its
+ *            place (its values then are code * scale, not rounded). Neither:
+ *            z = 0, without post and gate.
+ *  residual  device (rows, width), or residual_kept in its place.
+ *  sum       device (rows, width).
+ *  out       device (rows, width) just if pre is set, else NULL.
+ *  keep_branch, keep_residual  NULL, or where branch / residual (given in
+ *            dtype) are kept in 8 bits on the way, as pmha_checkpoint does.
+ * Arithmetic is float32 up to the one rounding of sum and of out; rows whose
+ * squares leave float32 are scaled by a power of two first, as in pmha_rms_norm.
+ * Needs no workspace. Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_CUDA.
+ */
+pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *branch, const pmha_kept *branch_kept,
+                      const void *residual, const pmha_kept *residual_kept, void *sum, void *out,
+                      const pmha_kept *keep_branch, const pmha_kept *keep_residual, pmha_stream stream);
+
+/*
+ * pmha_join_backward - gradients of pmha_join.
+ *  branch, branch_kept  the block's output in either form; needed for dpost,
+ *          dgate, and dbranch with post.
+ *  sum     device (rows, width), the kept sum; needed with pre.
+ *  dout    dLoss/d(out), just if pre is set.
+ *  dsum    dLoss/d(sum) from its other uses (the residual stream), or NULL;
+ *          one of dout and dsum is needed.
+ *  dbranch, dresidual  device (rows, width) in dtype, or NULL.
+ *  dpost (width), dgate (gates, width), dpre (width)  device float32, or NULL;
+ *          each only with its parameter. Sums over rows run in a fixed order
+ *          (deterministic), in float32 over up to 128 terms and as pairs of
+ *          floats from there.
+ *  workspace  pmha_join_backward_workspace_size() bytes, 256-byte aligned
+ *          (SIZE_MAX when the arguments are invalid); not needed without
+ *          dpost, dgate and dpre.
+ * rows = 0 writes zeros to dpost, dgate and dpre.
+ * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_UNSUPPORTED ((gates + 2) *
+ * ceil(width / 8) above 2^31 - 1), PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
+ */
+size_t pmha_join_backward_workspace_size(const pmha_join_params *params, int64_t rows);
+pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, const void *branch,
+                               const pmha_kept *branch_kept, const void *sum, const void *dout, const void *dsum,
+                               void *dbranch, void *dresidual, float *dpost, float *dgate, float *dpre, void *workspace,
+                               size_t workspace_bytes, pmha_stream stream);
+
 /* Message describing the last failure of a call made by this thread ("" if none). */
 const char *pmha_last_error(void);
 
