@@ -17,8 +17,9 @@ the residual sum (pmha_rms_norm), the gated feed-forward block (pmha_ffn_*),
 their gradients, clipping by the global norm (pmha_clip_grad_norm), the join
 of a block with the residual stream (pmha_join: norms on both sides, gate,
 residual scale), tensors kept in 8 bits for the backward pass
-(pmha_checkpoint), and PackedEncoderLayer, which runs them together with the
-layer.
+(pmha_checkpoint), products and the gated block in microscaled 4-bit floating
+point (pmha_mx_*, pmha_ffn_forward_mx), and PackedEncoderLayer, which runs them
+together with the layer.
 """
 from __future__ import annotations
 
@@ -26,6 +27,7 @@ import contextlib
 import ctypes
 import dataclasses
 import itertools
+import math
 import operator
 import struct
 
@@ -50,6 +52,8 @@ __all__ = [
     "pmha_ffn_backward_workspace_size", "pmha_clip_grad_norm",
     "JoinParams", "Checkpoint", "pmha_join", "pmha_join_checkpointed", "pmha_join_backward",
     "pmha_join_backward_workspace_size", "pmha_checkpoint", "pmha_checkpoint_restore",
+    "MxTensor", "FfnMxParams", "pmha_mx_quantize", "pmha_mx_linear", "pmha_ffn_forward_mx",
+    "pmha_ffn_forward_mx_workspace_size",
 ]
 
 WMODES = {"none": PMHA_WEIGHTS_NONE, "avg": PMHA_WEIGHTS_AVG, "per_head": PMHA_WEIGHTS_PER_HEAD}
@@ -1083,6 +1087,169 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
     if st:
         _lib.check(st, "pmha_join_backward")
     return {"dbranch": db, "dresidual": dr, "dpre": grads[2], "dpost": grads[0], "dgate": grads[1]}
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floating point
+@dataclasses.dataclass
+class MxTensor:
+    """A tensor (..., width) in microscaled 4 bits, as a matrix of its rows: E2M1 values in blocks of 32 along the row,
+    each block times a power of two. codes uint8 (rows, ceil(width / 32) * 16), two a byte, the lower column in the low
+    half; scale uint8 (row tiles, block tiles, 512), tiles of 128 rows by 4 blocks, byte b for 2^(b - 127), row r and
+    block k of a tile at 16 (r % 32) + 4 (r / 32) + k. shape: the tensor's."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    shape: tuple
+
+    def __post_init__(self):
+        self.shape = torch.Size(self.shape)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scale.numel()
+
+    @staticmethod
+    def _sizes(shape):
+        """(rows, width, shape of codes, shape of scale)"""
+        width = shape[-1] if len(shape) else 0
+        if not width:
+            raise ValueError("an MxTensor has rows of one value at least")
+        rows, blocks = math.prod(shape[:-1]), (width + 31) // 32
+        return rows, width, (rows, blocks * 16), ((rows + 127) // 128, (blocks + 3) // 4, 512)
+
+    def _struct(self, name, index=None):
+        """(struct, rows, width, device index); index: the device it has to be on."""
+        rows, width, codes, scale = self._sizes(self.shape)
+        if index is None:
+            if not isinstance(self.codes, _T) or not self.codes.is_cuda:
+                raise ValueError(f"{name} must hold CUDA tensors")
+            index = self.codes.get_device()
+        c = _like(name + ".codes", self.codes, codes, torch.uint8, index)
+        s = _like(name + ".scale", self.scale, scale, torch.uint8, index)
+        if c is None or s is None:
+            raise ValueError(f"{name} lacks its codes or scales")
+        return _lib.PmhaMx(c, s), rows, width, index
+
+    def values(self) -> torch.Tensor:
+        """The values that it stands for, in float64 (values near float32's end can round to 2^128). Torch operations, for
+        inspection: not for a hot path."""
+        rows, width, _, _ = self._sizes(self.shape)
+        grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=self.codes.device)
+        v = torch.cat((grid, -grid))[torch.stack((self.codes & 15, self.codes >> 4), -1).long()].view(rows, -1, 32)
+        t = self.scale.view(*self.scale.shape[:2], 32, 4, 4).permute(0, 3, 2, 1, 4)
+        t = t.reshape(self.scale.shape[0] * 128, self.scale.shape[1] * 4)[:rows, :v.shape[1]].long()
+        s = torch.where(t == 255, math.nan, ((t - 127 + 1023) << 52).view(torch.float64))
+        return (v * s[..., None]).view(rows, -1)[:, :width].reshape(self.shape)
+
+
+def pmha_mx_quantize(x: torch.Tensor, stream=None) -> MxTensor:
+    """x (..., width), float32 or bfloat16, in microscaled 4 bits: a block's scale is the least power of two with
+    max|block| <= 6 * scale, each value the nearest E2M1 value times that (ties to the even code). For tokens and, once,
+    for weights."""
+    shape, rows, width, dev = _rows_of("x", x)
+    _, _, codes, scale = MxTensor._sizes(shape)
+    with _on(dev, stream):
+        q = MxTensor(torch.empty(codes, dtype=torch.uint8, device=x.device),
+                     torch.empty(scale, dtype=torch.uint8, device=x.device), shape)
+        st = _library().pmha_mx_quantize(_DTYPES[x.dtype], rows, width, x.data_ptr(),
+                                         ctypes.byref(_lib.PmhaMx(q.codes.data_ptr(), q.scale.data_ptr())),
+                                         _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_mx_quantize")
+    return q
+
+
+def _mx_tokens(name, x):
+    if not isinstance(x, MxTensor):
+        raise TypeError(f"{name} must be an MxTensor (pmha_mx_quantize makes one)")
+    return x._struct(name)
+
+
+def pmha_mx_linear(x: MxTensor, weight: MxTensor, bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x weight^T + bias + residual in bfloat16, for x (..., width) and weight (outputs, width) in microscaled 4 bits;
+    sums are float32."""
+    xs, rows, width, dev = _mx_tokens("x", x)
+    if not isinstance(weight, MxTensor) or len(weight.shape) != 2 or weight.shape[1] != width:
+        raise ValueError(f"weight must be an MxTensor (outputs, {width})")
+    ws, N, _, _ = weight._struct("weight", dev)
+    bf16, shape = torch.bfloat16, (*x.shape[:-1], N)
+    b = _like("bias", bias, (N,), bf16, dev)
+    r = _like("residual", residual, shape, bf16, dev)
+    o = _like("out", out, shape, bf16, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=bf16, device=x.codes.device)
+            o = out.data_ptr()
+        st = _library().pmha_mx_linear(rows, width, N, ctypes.byref(xs), ctypes.byref(ws), b, r, o, _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_mx_linear")
+    return out
+
+
+@dataclasses.dataclass
+class FfnMxParams:
+    """A gated block whose weights, wg and wu (F, E) and wd (E, F), are in microscaled 4 bits; biases bfloat16 or None."""
+    wg: MxTensor
+    wu: MxTensor
+    wd: MxTensor
+    bg: torch.Tensor | None = None
+    bu: torch.Tensor | None = None
+    bd: torch.Tensor | None = None
+    act: str = "silu"
+
+    def _structs(self):
+        """(pmha_ffn_params, pmha_ffn_mx, device index)"""
+        if not all(isinstance(w, MxTensor) for w in (self.wg, self.wu, self.wd)):
+            raise TypeError("wg, wu and wd must be MxTensors")
+        wd, E, F, dev = self.wd._struct("wd")
+        wg, *gs, _ = self.wg._struct("wg", dev)
+        wu, *us, _ = self.wu._struct("wu", dev)
+        if gs != [F, E] or us != [F, E]:
+            raise ValueError(f"wg and wu must be ({F}, {E}) beside wd ({E}, {F})")
+        act = ACTS.get(self.act)
+        if act is None:
+            raise ValueError(f"act must be one of {sorted(ACTS)}")
+        t = torch.bfloat16
+        p = _lib.PmhaFfnParams(E, F, PMHA_BF16, act, None, None, None, _like("bg", self.bg, (F,), t, dev),
+                               _like("bu", self.bu, (F,), t, dev), _like("bd", self.bd, (E,), t, dev))
+        return p, _lib.PmhaFfnMx(wg, wu, wd), dev
+
+    @staticmethod
+    def from_params(params: FfnParams) -> "FfnMxParams":
+        """The block with its weights quantized, once, when a model is loaded. Its biases become bfloat16."""
+        def b(t):
+            return None if t is None else t.bfloat16()
+        return FfnMxParams(*(pmha_mx_quantize(w) for w in (params.wg, params.wu, params.wd)), b(params.bg), b(params.bu),
+                           b(params.bd), params.act)
+
+
+def pmha_ffn_forward_mx_workspace_size(params: FfnMxParams, rows: int) -> int:
+    return _ffn_size(_library().pmha_ffn_forward_mx_workspace_size, params._structs()[0], int(rows), "pmha_ffn_forward_mx")
+
+
+def pmha_ffn_forward_mx(params: FfnMxParams, x: MxTensor, residual: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The gated block on tokens x (..., E) in microscaled 4 bits, plus the residual, in bfloat16; the hidden rows are
+    rounded to 4 bits between its products."""
+    p, w, dev = params._structs()
+    xs, rows, width, xdev = _mx_tokens("x", x)
+    if width != p.embed_dim or xdev != dev:
+        raise ValueError(f"x must be (..., {p.embed_dim}) on cuda:{dev}")
+    bf16 = torch.bfloat16
+    r = _like("residual", residual, x.shape, bf16, dev)
+    o = _like("out", out, x.shape, bf16, dev)
+    lib = _library()
+    need = _ffn_size(lib.pmha_ffn_forward_mx_workspace_size, p, rows, "pmha_ffn_forward_mx")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=bf16, device=x.codes.device)
+            o = out.data_ptr()
+        wp, wn, keep = _scratch(x.codes, need, workspace)
+        st = lib.pmha_ffn_forward_mx(ctypes.byref(p), ctypes.byref(w), ctypes.byref(xs), r, rows, o, wp, wn,
+                                     _stream_of(dev, stream))
+    if st:
+        _lib.check(st, "pmha_ffn_forward_mx")
+    return out
 
 
 class PackedEncoderLayer:

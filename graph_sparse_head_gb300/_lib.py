@@ -56,6 +56,14 @@ class PmhaJoinParams(ctypes.Structure):
                 ("residual_scale", ctypes.c_float), ("pre", _vp), ("eps", ctypes.c_float)]
 
 
+class PmhaMx(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scale", _vp)]
+
+
+class PmhaFfnMx(ctypes.Structure):
+    _fields_ = [("wg", PmhaMx), ("wu", PmhaMx), ("wd", PmhaMx)]
+
+
 _P = ctypes.POINTER(PmhaParams)
 _F = ctypes.POINTER(PmhaFfnParams)
 _FQ = ctypes.POINTER(PmhaFfnQuantized)
@@ -63,6 +71,8 @@ _FG = ctypes.POINTER(PmhaFfnGrads)
 _G = ctypes.POINTER(PmhaGrads)
 _K = ctypes.POINTER(PmhaKept)
 _J = ctypes.POINTER(PmhaJoinParams)
+_M = ctypes.POINTER(PmhaMx)
+_FM = ctypes.POINTER(PmhaFfnMx)
 _I64P = ctypes.POINTER(ctypes.c_int64)
 
 SIGNATURES = {
@@ -102,6 +112,12 @@ SIGNATURES = {
     "pmha_join": (ctypes.c_int, [_J, _i64, _vp, _K, _vp, _K, _vp, _vp, _K, _K, _vp]),
     "pmha_join_backward_workspace_size": (_sz, [_J, _i64]),
     "pmha_join_backward": (ctypes.c_int, [_J, _i64, _vp, _K, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "pmha_mx_code_bytes": (_sz, [_i64, _i64]),
+    "pmha_mx_scale_bytes": (_sz, [_i64, _i64]),
+    "pmha_mx_quantize": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _vp, _M, _vp]),
+    "pmha_mx_linear": (ctypes.c_int, [_i64, _i64, _i64, _M, _M, _vp, _vp, _vp, _vp]),
+    "pmha_ffn_forward_mx_workspace_size": (_sz, [_F, _i64]),
+    "pmha_ffn_forward_mx": (ctypes.c_int, [_F, _FM, _M, _vp, _i64, _vp, _vp, _sz, _vp]),
     "pmha_clip_grad_norm_workspace_size": (_sz, [_i64]),
     "pmha_clip_grad_norm": (ctypes.c_int, [_i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }

@@ -1,0 +1,443 @@
+// Microscaled 4-bit floating point (mx.cuh): quantisation, products for a few
+// tokens, argument checks and the order of launches of the linear product and the gated block.
+//
+//   linear  y = x W^T + bias + residual
+//   block   h = act(x Wg^T + bg) * (x Wu^T + bu), rounded to 4 bits;  y = h Wd^T + bd + residual
+//
+// Sums are float32 (products of two E2M1 values are exact in any of the forms), outputs bf16.
+#include <math.h>
+
+#include <algorithm>
+
+#include "ffn_math.cuh"
+#include "mx.cuh"
+#include "rows.cuh"
+#include "tc_pair.cuh"
+
+namespace pmha {
+namespace {
+
+// ---------------------------------------------------------------- quantisation
+// A lane takes VEC values of a block, 32 / VEC lanes a block. Blocks past the row's last up to a multiple of four, and
+// rows past the last up to a multiple of 128, get zero scales. Bound by memory.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long rows, int width, uint8_t *codes,
+                                                          uint8_t *scale)
+{
+    constexpr int kLanes = 32 / VEC;
+    tcu::grid_dependents_may_start();
+    const int blocks = (width + 31) / 32, padded = (blocks + 3) & ~3;
+    const long long n = ((rows + 127) & ~127ll) * padded, step = (long long)gridDim.x * kThreads / kLanes;
+    const int l = threadIdx.x % kLanes;
+    const long long lead = ((long long)blockIdx.x * kThreads + threadIdx.x / 32 * 32) / kLanes;
+    for (long long g0 = lead; g0 < n; g0 += step) {  // whole warps walk
+        const long long g = g0 + (threadIdx.x % 32) / kLanes;
+        const long long row = g / padded;
+        const int k = (int)(g - row * padded), c = k * 32 + l * VEC;
+        const bool block = g < n && row < rows && k < blocks, in = block && c < width;
+        Vals<T, VEC> v;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(0.f);
+        if (in) load<T, VEC>(x + row * width + c, v.v);
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) most = max(most, abs_bits(to_f<T>(v.v[i])));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+        const uint32_t byte = mx_scale_byte(most);
+        const bool fine = byte < 255u;
+        const float inv = fine ? mx_inverse(byte) : 0.f;
+        uint8_t *dst = codes + row * (blocks * 16ll) + k * 16;
+        if constexpr (VEC == 8) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w |= mx_byte(to_f<T>(v.v[2 * i]) * inv, to_f<T>(v.v[2 * i + 1]) * inv) << (8 * i);
+            if (block) *reinterpret_cast<uint32_t *>(dst + l * 4) = fine ? w : 0u;
+        } else if constexpr (VEC == 4) {
+            const uint32_t w = mx_byte(to_f<T>(v.v[0]) * inv, to_f<T>(v.v[1]) * inv) |
+                               mx_byte(to_f<T>(v.v[2]) * inv, to_f<T>(v.v[3]) * inv) << 8;
+            if (block) *reinterpret_cast<uint16_t *>(dst + l * 2) = fine ? (uint16_t)w : (uint16_t)0;
+        } else if constexpr (VEC == 2) {
+            const uint32_t w = mx_byte(to_f<T>(v.v[0]) * inv, to_f<T>(v.v[1]) * inv);
+            if (block) dst[l] = fine ? (uint8_t)w : (uint8_t)0;
+        } else {
+            const float f = to_f<T>(v.v[0]) * inv, next = __shfl_down_sync(kFull, f, 1);
+            const uint32_t w = mx_byte(f, next);
+            if (block && l % 2 == 0) dst[l / 2] = fine ? (uint8_t)w : (uint8_t)0;
+        }
+        if (l == 0 && g < n)
+            scale[((row >> 7) * (padded / 4) + (k >> 2)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (k & 3)] =
+                block ? (uint8_t)byte : (uint8_t)0;
+    }
+}
+
+// ---------------------------------------------------------------- a few tokens
+// The weights are read once, by every SM, and multiplied on the CUDA cores. A lane takes a block of 32 weights (16
+// bytes), LPR lanes an output column. The tokens lie in shared memory as the E2M1 values themselves in fp16, 80 bytes a
+// block with its scale behind them (a stride that spreads eight lanes' 16-byte reads over all banks). Eight products of
+// E2M1 values are at most 288 and multiples of 1/4: their sums are exact in fp16. What bounds it is latency.
+constexpr int kCell = 80;
+
+struct MxSmallArgs {
+    const uint8_t *x, *xs;   // tokens in 4 bits, or null
+    const float *h;          // tokens in float32, rounded to 4 bits here
+    const uint8_t *w0, *s0, *w1, *s1;
+    const __nv_bfloat16 *b0, *b1, *res;
+    float *h_out;            // gated
+    __nv_bfloat16 *out;
+    int M, N, K;
+};
+
+__device__ __forceinline__ size_t scale_at(long long row, int k, int tiles)
+{
+    return (size_t)((row >> 7) * tiles + (k >> 2)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (k & 3);
+}
+__device__ __forceinline__ __half2 two_of(uint32_t byte)
+{
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
+    return *reinterpret_cast<const __half2 *>(&h);
+}
+__device__ __forceinline__ void widen16(uint4 raw, __half2 (&v)[16])
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = two_of((w[i >> 2] >> (8 * (i & 3))) & 0xffu);
+}
+// 32 products of a block, without the scales
+__device__ __forceinline__ float block_dot(const __half2 (&w)[16], const uint8_t *cell)
+{
+    float s = 0.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        __half2 acc = __float2half2_rn(0.f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(cell + 32 * half + 16 * j);
+            const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc = __hfma2(w[8 * half + 4 * j + i], *reinterpret_cast<const __half2 *>(&x[i]), acc);
+        }
+        const float2 f = __half22float2(acc);
+        s += f.x + f.y;
+    }
+    return s;
+}
+
+template <bool GATED, int ACT, int MB, int LPR>
+__global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
+{
+    extern __shared__ __align__(16) uint8_t cells[];  // [M][blocks]
+    const int blocks = (a.K + 31) / 32, tiles = (blocks + 3) / 4;
+    const int l = threadIdx.x % LPR, n = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const bool live = n < a.N;
+    const size_t wrow = (size_t)min(n, a.N - 1) * blocks * 16;
+    // The launch before this one may be what writes the weights, but for the block's down product: the up product is
+    // before that, and lets it start only when all that came before itself is done.
+    uint4 first = make_uint4(0, 0, 0, 0);
+    if (a.h && l < blocks) first = *reinterpret_cast<const uint4 *>(a.w0 + wrow + l * 16);
+    tcu::grid_wait();
+    tcu::grid_dependents_may_start();
+    if (a.x) {
+        for (int i = threadIdx.x; i < a.M * blocks; i += kThreads) {
+            const int m = i / blocks, k = i - m * blocks;
+            __half2 v[16];
+            widen16(*reinterpret_cast<const uint4 *>(a.x + (size_t)i * 16), v);
+            uint8_t *cell = cells + i * kCell;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(cell + 16 * j) = *reinterpret_cast<uint4 *>(&v[4 * j]);
+            *reinterpret_cast<float *>(cell + 64) = mx_scale_value(a.xs[scale_at(m, k, tiles)]);
+        }
+    } else {
+        // eight lanes a block; whole warps walk
+        for (int i0 = threadIdx.x / 32 * 4; i0 < a.M * blocks; i0 += kThreads / 8) {
+            const int i = i0 + (threadIdx.x & 31) / 8, q = threadIdx.x % 8;
+            const int m = i / blocks, k = i - m * blocks;
+            float f[4];
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = k * 32 + q * 4 + e;
+                f[e] = i < a.M * blocks && c < a.K ? a.h[(size_t)m * a.K + c] : 0.f;
+                most = max(most, abs_bits(f[e]));
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+            if (i >= a.M * blocks) continue;
+            const uint32_t byte = mx_scale_byte(most);
+            const float inv = byte < 255u ? mx_inverse(byte) : 0.f;
+            __half2 v[2] = {two_of(mx_byte(f[0] * inv, f[1] * inv)), two_of(mx_byte(f[2] * inv, f[3] * inv))};
+            uint8_t *cell = cells + i * kCell;
+            *reinterpret_cast<uint2 *>(cell + 8 * q) = *reinterpret_cast<uint2 *>(v);
+            if (q == 0) *reinterpret_cast<float *>(cell + 64) = mx_scale_value(byte);
+        }
+    }
+    __syncthreads();
+    float y0[MB], y1[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) y0[m] = y1[m] = 0.f;
+    for (int k = l; k < blocks; k += LPR) {
+        __half2 w0[16], w1[16];
+        widen16(k == l && a.h ? first : *reinterpret_cast<const uint4 *>(a.w0 + wrow + k * 16), w0);
+        if constexpr (GATED) widen16(*reinterpret_cast<const uint4 *>(a.w1 + wrow + k * 16), w1);
+        const size_t at = scale_at(min(n, a.N - 1), k, tiles);
+        const float s0 = mx_scale_value(a.s0[at]), s1 = GATED ? mx_scale_value(a.s1[at]) : 0.f;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            if (m >= a.M) break;
+            const uint8_t *cell = cells + (m * blocks + k) * kCell;
+            const float sx = *reinterpret_cast<const float *>(cell + 64);
+            y0[m] = fmaf(block_dot(w0, cell) * s0, sx, y0[m]);
+            if constexpr (GATED) y1[m] = fmaf(block_dot(w1, cell) * s1, sx, y1[m]);
+        }
+    }
+    float m0 = 0.f, m1 = 0.f;  // of token l
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+            y0[m] += __shfl_xor_sync(kFull, y0[m], o);
+            if constexpr (GATED) y1[m] += __shfl_xor_sync(kFull, y1[m], o);
+        }
+        if (l == m) m0 = y0[m], m1 = y1[m];
+    }
+    if (!live || l >= a.M) return;
+    if (a.b0) m0 += __bfloat162float(a.b0[n]);
+    const size_t at = (size_t)l * a.N + n;
+    if constexpr (GATED) {
+        if (a.b1) m1 += __bfloat162float(a.b1[n]);
+        a.h_out[at] = Act<ACT>::hidden(m0 * Act<ACT>::kGate, m1 * Act<ACT>::kUp);
+    } else {
+        if (a.res) m0 += __bfloat162float(a.res[at]);
+        a.out[at] = __float2bfloat16_rn(m0);
+    }
+}
+
+constexpr int kFewTokens = 8;
+constexpr size_t kFewBytes = 48 * 1024;
+bool few(int64_t M, int64_t K) { return M <= kFewTokens && (size_t)(M * mx_blocks(K)) * kCell <= kFewBytes; }
+
+template <bool GATED, int ACT, int MB, int LPR>
+pmha_status launch_small(const MxSmallArgs &a, cudaStream_t s)
+{
+    const int per = kThreads / LPR;
+    return tcu::launch_overlapping(k_mx_small<GATED, ACT, MB, LPR>, dim3((unsigned)((a.N + per - 1) / per)), kThreads,
+                                   (int)((size_t)a.M * mx_blocks(a.K) * kCell), s, a);
+}
+// LPR lanes have a block each at least
+template <bool GATED, int ACT, int MB>
+pmha_status by_lanes(const MxSmallArgs &a, cudaStream_t s)
+{
+    const int64_t blocks = mx_blocks(a.K);
+    if (blocks <= 8) return launch_small<GATED, ACT, MB, 8>(a, s);
+    if (blocks <= 16) return launch_small<GATED, ACT, MB, 16>(a, s);
+    return launch_small<GATED, ACT, MB, 32>(a, s);
+}
+template <bool GATED, int ACT>
+pmha_status small(const MxSmallArgs &a, const char *stage, cudaStream_t s)
+{
+    StageTimer timer(stage, s);
+    if (a.M == 1) return by_lanes<GATED, ACT, 1>(a, s);
+    return a.M <= 4 ? by_lanes<GATED, ACT, 4>(a, s) : by_lanes<GATED, ACT, kFewTokens>(a, s);
+}
+
+// ---------------------------------------------------------------- checks
+pmha_status check_mx(const char *who, const char *name, const pmha_mx *m)
+{
+    if (m && m->codes && m->scale && aligned(m->codes, 16) && aligned(m->scale, 16)) return PMHA_OK;
+    set_error("%s: %s lacks its codes or scales, or they are not 16-byte aligned", who, name);
+    return PMHA_ERR_INVALID_ARG;
+}
+pmha_status check_sizes(const char *who, int64_t rows, int64_t width, int64_t outputs)
+{
+    if (rows < 0 || rows > ((int64_t)1 << 31) - 1 || width < 1 || width > ((int64_t)1 << 20) || outputs < 1 ||
+        outputs > ((int64_t)1 << 20) || width * outputs > (int64_t)1 << 34 ||
+        rows * std::max(width, outputs) > (int64_t)1 << 40) {
+        set_error("%s: rows %lld must be 0 .. 2^31 - 1, widths %lld and %lld 1 .. 2^20, their product at most 2^34, rows "
+                  "times the wider at most 2^40",
+                  who, (long long)rows, (long long)width, (long long)outputs);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    return PMHA_OK;
+}
+Mx mx_of(const pmha_mx &m) { return Mx{(const uint8_t *)m.codes, (const uint8_t *)m.scale}; }
+struct Span {
+    const void *p;
+    size_t n;
+};
+template <int N>
+bool overlaps_any(const void *p, size_t n, const Span (&in)[N])
+{
+    for (int i = 0; i < N; ++i)
+        if (overlap(p, n, in[i].p, in[i].n)) return true;
+    return false;
+}
+
+pmha_status linear(const MxLinear &a, const char *stage, cudaStream_t s)
+{
+    if (!few(a.M, a.K)) return mx_tc_linear(a, stage, s);
+    MxSmallArgs q = {};
+    q.x = a.x.codes, q.xs = a.x.scale, q.w0 = a.w.codes, q.s0 = a.w.scale;
+    q.b0 = (const __nv_bfloat16 *)a.bias, q.res = (const __nv_bfloat16 *)a.residual, q.out = (__nv_bfloat16 *)a.out;
+    q.M = (int)a.M, q.N = (int)a.N, q.K = (int)a.K;
+    return small<false, 0>(q, stage, s);
+}
+
+pmha_status check_ffn_mx(const char *who, const pmha_ffn_params *p, int64_t rows)
+{
+    if (!p || p->dtype != PMHA_BF16 || (p->act != PMHA_ACT_SILU && p->act != PMHA_ACT_GELU)) {
+        set_error("%s: params is NULL, its dtype is not PMHA_BF16 or its act is unknown", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    return check_sizes(who, rows, p->embed_dim, p->hidden_dim);
+}
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+// Hidden rows in 4 bits, or those of a few tokens in float32
+size_t hidden_bytes(const pmha_ffn_params *p, int64_t rows)
+{
+    const size_t small = (size_t)std::min<int64_t>(rows, kFewTokens) * (size_t)p->hidden_dim * 4;
+    if (few(rows, p->embed_dim) && few(rows, p->hidden_dim)) return round256(small);
+    return std::max(round256(small),
+                    round256(mx_code_bytes(rows, p->hidden_dim)) + round256(mx_scale_bytes(rows, p->hidden_dim)));
+}
+
+}  // namespace
+}  // namespace pmha
+
+using namespace pmha;
+
+extern "C" {
+
+size_t pmha_mx_code_bytes(int64_t rows, int64_t width)
+{
+    return check_sizes("pmha_mx_code_bytes", rows, width, 1) == PMHA_OK ? mx_code_bytes(rows, width) : SIZE_MAX;
+}
+size_t pmha_mx_scale_bytes(int64_t rows, int64_t width)
+{
+    return check_sizes("pmha_mx_scale_bytes", rows, width, 1) == PMHA_OK ? mx_scale_bytes(rows, width) : SIZE_MAX;
+}
+
+pmha_status pmha_mx_quantize(pmha_dtype dtype, int64_t rows, int64_t width, const void *x, const pmha_mx *out,
+                             pmha_stream stream)
+{
+    const char *who = "pmha_mx_quantize";
+    pmha_status st = check_rows(who, dtype, rows, width);
+    if (st == PMHA_OK) st = check_sizes(who, rows, width, 1);
+    if (st != PMHA_OK || rows == 0) return st;
+    if ((st = check_mx(who, "out", out)) != PMHA_OK) return st;
+    if (!x || !aligned(x, 16)) {
+        set_error("%s: x is NULL or not 16-byte aligned", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const size_t nb = (size_t)(rows * width) * bytes_of(dtype), cb = mx_code_bytes(rows, width), sb = mx_scale_bytes(rows, width);
+    if (overlap(out->codes, cb, x, nb) || overlap(out->scale, sb, x, nb) || overlap(out->codes, cb, out->scale, sb)) {
+        set_error("%s: an output overlaps an input or another output", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    cudaStream_t cs = (cudaStream_t)stream;
+    {
+        StageTimer timer("mx_quantize", cs);
+        dispatch_wide(dtype, shape_of(dtype, width).vec, [&](auto t) {
+            using G = decltype(t);
+            const int64_t lanes = ((rows + 127) & ~(int64_t)127) * ((mx_blocks(width) + 3) & ~(int64_t)3) * (32 / G::vec);
+            const unsigned grid = (unsigned)std::min<int64_t>((lanes + kThreads - 1) / kThreads, (int64_t)num_sms() * 8);
+            k_mx_quantize<typename G::type, G::vec><<<grid, kThreads, 0, cs>>>(
+                (const typename G::type *)x, rows, (int)width, (uint8_t *)out->codes, (uint8_t *)out->scale);
+        });
+    }
+    count_launch();
+    PMHA_CUDA_TRY(cudaGetLastError());
+    return PMHA_OK;
+}
+
+pmha_status pmha_mx_linear(int64_t rows, int64_t width, int64_t outputs, const pmha_mx *x, const pmha_mx *weight,
+                           const void *bias, const void *residual, void *out, pmha_stream stream)
+{
+    const char *who = "pmha_mx_linear";
+    pmha_status st = check_sizes(who, rows, width, outputs);
+    if (st != PMHA_OK || rows == 0) return st;
+    if ((st = check_mx(who, "x", x)) != PMHA_OK || (st = check_mx(who, "weight", weight)) != PMHA_OK) return st;
+    if (!out || !aligned(out, 16) || !aligned(residual, 16) || !aligned(bias, 2)) {
+        set_error("%s: out is NULL, out or residual is not 16-byte aligned, or bias not to its elements", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const size_t ob = (size_t)(rows * outputs) * 2;
+    const Span ins[] = {{x->codes, mx_code_bytes(rows, width)}, {x->scale, mx_scale_bytes(rows, width)},
+                        {weight->codes, mx_code_bytes(outputs, width)}, {weight->scale, mx_scale_bytes(outputs, width)},
+                        {bias, (size_t)outputs * 2}, {residual, ob}};
+    if (overlaps_any(out, ob, ins)) {
+        set_error("%s: an output overlaps an input or another output", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    return linear(MxLinear{mx_of(*x), mx_of(*weight), bias, residual, out, rows, outputs, width}, "mx_linear",
+                  (cudaStream_t)stream);
+}
+
+size_t pmha_ffn_forward_mx_workspace_size(const pmha_ffn_params *params, int64_t rows)
+{
+    if (check_ffn_mx("pmha_ffn_forward_mx", params, rows) != PMHA_OK) return SIZE_MAX;
+    return rows ? hidden_bytes(params, rows) : 0;
+}
+
+pmha_status pmha_ffn_forward_mx(const pmha_ffn_params *params, const pmha_ffn_mx *weights, const pmha_mx *x,
+                                const void *residual, int64_t rows, void *out, void *workspace, size_t workspace_bytes,
+                                pmha_stream stream)
+{
+    const char *who = "pmha_ffn_forward_mx";
+    pmha_status st = check_ffn_mx(who, params, rows);
+    if (st != PMHA_OK || rows == 0) return st;
+    const int64_t E = params->embed_dim, F = params->hidden_dim;
+    if (!weights) {
+        set_error("%s: weights is NULL", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if ((st = check_mx(who, "x", x)) != PMHA_OK || (st = check_mx(who, "wg", &weights->wg)) != PMHA_OK ||
+        (st = check_mx(who, "wu", &weights->wu)) != PMHA_OK || (st = check_mx(who, "wd", &weights->wd)) != PMHA_OK)
+        return st;
+    if (!out || !aligned(out, 16) || !aligned(residual, 16) || !aligned(params->bg, 2) || !aligned(params->bu, 2) ||
+        !aligned(params->bd, 2)) {
+        set_error("%s: out is NULL, out or residual is not 16-byte aligned, or a bias not to its elements", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    const size_t ob = (size_t)(rows * E) * 2, need = hidden_bytes(params, rows);
+    const size_t wc = mx_code_bytes(F, E), wsc = mx_scale_bytes(F, E);
+    const Span ins[] = {{x->codes, mx_code_bytes(rows, E)}, {x->scale, mx_scale_bytes(rows, E)},
+                        {weights->wg.codes, wc}, {weights->wg.scale, wsc}, {weights->wu.codes, wc}, {weights->wu.scale, wsc},
+                        {weights->wd.codes, mx_code_bytes(E, F)}, {weights->wd.scale, mx_scale_bytes(E, F)},
+                        {params->bg, (size_t)F * 2}, {params->bu, (size_t)F * 2}, {params->bd, (size_t)E * 2}, {residual, ob},
+                        {workspace, need}};
+    if (overlaps_any(out, ob, ins)) {
+        set_error("%s: an output overlaps an input or the workspace", who);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) {
+        set_error("%s: workspace needs %zu bytes, 256-byte aligned (got %zu at %p)", who, need, workspace_bytes, workspace);
+        return PMHA_ERR_WORKSPACE;
+    }
+    cudaStream_t s = (cudaStream_t)stream;
+    if (few(rows, E) && few(rows, F)) {
+        MxSmallArgs a = {};
+        a.x = (const uint8_t *)x->codes, a.xs = (const uint8_t *)x->scale;
+        a.w0 = (const uint8_t *)weights->wg.codes, a.s0 = (const uint8_t *)weights->wg.scale;
+        a.w1 = (const uint8_t *)weights->wu.codes, a.s1 = (const uint8_t *)weights->wu.scale;
+        a.b0 = (const __nv_bfloat16 *)params->bg, a.b1 = (const __nv_bfloat16 *)params->bu;
+        a.h_out = (float *)workspace;
+        a.M = (int)rows, a.N = (int)F, a.K = (int)E;
+        st = params->act == PMHA_ACT_SILU ? small<true, PMHA_ACT_SILU>(a, "ffn_up_mx", s)
+                                          : small<true, PMHA_ACT_GELU>(a, "ffn_up_mx", s);
+        if (st != PMHA_OK) return st;
+        MxSmallArgs d = {};
+        d.h = (const float *)workspace;
+        d.w0 = (const uint8_t *)weights->wd.codes, d.s0 = (const uint8_t *)weights->wd.scale;
+        d.b0 = (const __nv_bfloat16 *)params->bd, d.res = (const __nv_bfloat16 *)residual, d.out = (__nv_bfloat16 *)out;
+        d.M = (int)rows, d.N = (int)E, d.K = (int)F;
+        return small<false, 0>(d, "ffn_down_mx", s);
+    }
+    uint8_t *hc = (uint8_t *)workspace, *hs = hc + round256(mx_code_bytes(rows, F));
+    st = mx_tc_gated(MxGated{mx_of(*x), mx_of(weights->wg), mx_of(weights->wu), params->bg, params->bu, hc, hs, rows, F, E,
+                             params->act},
+                     s);
+    if (st != PMHA_OK) return st;
+    return mx_tc_linear(MxLinear{Mx{hc, hs}, mx_of(weights->wd), params->bd, residual, out, rows, E, F}, "ffn_down_mx", s);
+}
+
+}  // extern "C"

@@ -1,0 +1,464 @@
+// Products of matrices in microscaled 4 bits (mx.cuh) on the tensor cores (sm_103a), one kernel shape for two:
+//
+//   linear  y = x W^T + bias + residual                          tile 256 tokens x 256 outputs, bf16
+//   gated   h = act(x Wg^T + bg) * (x Wu^T + bu), in 4 bits      tile 256 tokens x 128 hidden, gate and up side by side
+//
+// Two CTAs form a pair (tc_pair.cuh). Each has 18 warps: warp 0 copies stages of
+// 256 columns of codes (128 bytes a row, two values a byte) and the scale tiles that belong to them by TMA, warp
+// 1 of the even CTA copies the scale tiles to tensor memory (tcgen05.cp, into both CTAs) and issues tcgen05.mma
+// kind::mxf4, whose scaling by block is the hardware's; sixteen warps turn accumulators into outputs. Accumulators of 256
+// columns and the scales of four stages fill tensor memory, so there is one set: each epilogue thread takes all of its
+// accumulators into registers (64) and hands the set back at once, the next tile's products run under its arithmetic.
+//
+// Ragged sizes need no code of their own: TMA fills rows and columns past a
+// tensor's end with zeros (codes and scale tiles) and does not store them. Only
+// outputs whose rows are no multiples of 16 bytes go through plain loads and stores.
+//
+// Every mbarrier wait is bounded (tc_util.cuh); on expiry the pair gives up,
+// waits for its copies and products, frees its tensor memory and returns, and
+// pmha_device_status reports PMHA_ERR_TIMEOUT.
+#include <algorithm>
+
+#include "ffn_math.cuh"
+#include "mx.cuh"
+#include "tc_pair.cuh"
+
+namespace pmha {
+namespace {
+using namespace tcu;
+
+constexpr int kThreads = 64 + 512;
+constexpr int kBox = 128 * 128;       // bytes of a tile of 128 rows of 128 bytes
+constexpr int kSfA = 2 * 512;         // scale tiles of a stage: 128 rows x 256 columns
+constexpr int kSfB = 4 * 512;         // 256 rows x 256 columns
+constexpr int kStage = 2 * kBox + kSfA + kSfB;
+constexpr int kStages = 4;
+constexpr int kTile = 4 * kBox;       // 128 x 256 bf16; gated: 128 x 64 bytes and 512 scales
+constexpr int kVec = 256 * 4;
+constexpr int kBars = 256;
+constexpr int kSmem = 1024 + kStages * kStage + kTile + kVec + kBars;
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+static_assert(kStage % 1024 == 0, "swizzled tiles lie on 1024 bytes");
+constexpr int kTmemCols = 512;        // 256 accumulator columns, 24 scale columns a stage
+constexpr int kScaleCol = 256;
+
+struct Params {
+    CUtensorMap a, b0, b1, sa, sb0, sb1, out, res, h;
+    int M, N;               // tokens, outputs (gated: hidden width)
+    int n_tiles, tiles_n, kb;
+    const __nv_bfloat16 *bias0, *bias1;
+    const __nv_bfloat16 *res_p;  // plain: row-wise outputs without TMA
+    __nv_bfloat16 *out_p;
+    uint8_t *h_scale;
+    int h_tiles;            // scale tiles of a row block of h
+    int has_res, plain;
+    int *err;
+};
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// A scale tile of 32 rows of 16 bytes, 8-row groups 128 bytes apart, without swizzle
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
+}
+// to 4 columns of tensor memory, the same 32 lanes for each of the four warps, in both CTAs from their own shared memory
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// kind::mxf4: A and B E2M1 (1 at bits 7-9 and 10-12), 256 x 256 (N >> 3 at bits 17-22, M >> 7 at bits 27-28), E8M0
+// scales (bit 23); sf: which of a column's byte pairs holds the scales, 0 or 2 (bits 4-5 for B, 29-30 for A).
+__host__ __device__ constexpr uint32_t idesc_mx(uint32_t sf)
+{
+    return (sf << 4) | (1u << 7) | (1u << 10) | (32u << 17) | (1u << 23) | (2u << 27) | (sf << 29);
+}
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void team_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+
+template <bool GATED, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(const __grid_constant__ Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *tile_s = smem + kStages * kStage;
+    float *vec_s = (float *)(tile_s + kTile);                   // 256 biases: of outputs, or 128 of gate and of up
+    uint64_t *full = (uint64_t *)((uint8_t *)vec_s + kVec);     // [kStages], counted in the even CTA
+    uint64_t *empty = full + kStages;                           // [kStages], in each CTA
+    uint64_t *acc_full = empty + kStages;                       // in each CTA
+    uint64_t *acc_empty = acc_full + 1;                         // counted in the even CTA
+    uint64_t *mma_done = acc_empty + 1;
+    uint64_t *res_full = mma_done + 1;
+    uint32_t *tmem_holder = (uint32_t *)(res_full + 1);
+    volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
+    volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    constexpr int kCols = GATED ? 128 : 256;  // output columns of a tile
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(acc_full), 1);
+        mbar_init(smem_u32(acc_empty), 2);  // the epilogue of either CTA
+        mbar_init(smem_u32(mma_done), 1);
+        mbar_init(smem_u32(res_full), 1);
+        *abort_flag = 0;
+        *armed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), kTmemCols);
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    grid_dependency_wait();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp == 0) {
+        // ---------------- TMA producer of this CTA
+        const bool one = elect_one();
+        uint32_t made = 0;
+        for (int tile = pair; tile < p.n_tiles && !*abort_flag; tile += n_pairs) {
+            const int m = tile / p.tiles_n, n = tile % p.tiles_n;
+            const int rows = m * 2 + (int)rank;  // block of 128 tokens
+            for (int kb = 0; kb < p.kb; ++kb, ++made) {
+                const int stage = (int)(made % kStages);
+                if (!wait_bar(smem_u32(&empty[stage]), ((made / kStages) & 1u) ^ 1u, abort_flag, p.err)) break;
+                if (!one) continue;
+                const uint32_t fb = map_rank(smem_u32(&full[stage]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * kStage);
+                *armed = made + 1;
+                const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + kBox, ssb = ssa + kSfA;
+                tma_load_2d_pair(sa, &p.a, kb * 128, rows * 128, fb);
+                if constexpr (GATED) tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * 128, n * 128, fb);
+                else tma_load_2d_pair(sb, &p.b0, kb * 128, n * 256 + (int)rank * 128, fb);
+                tma_load_3d_pair(ssa, &p.sa, 0, kb * 2, rows, fb);
+                // the scales of all 256 columns, in both CTAs
+                tma_load_3d_pair(ssb, &p.sb0, 0, kb * 2, GATED ? n : n * 2, fb);
+                tma_load_3d_pair(ssb + 1024, GATED ? &p.sb1 : &p.sb0, 0, kb * 2, GATED ? n : n * 2 + 1, fb);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ---------------- issuer of the pair: the whole warp walks, one lane issues
+            const bool one = elect_one();
+            uint32_t used = 0, i = 0;
+            bool ok = true;
+            for (int tile = pair; tile < p.n_tiles && ok; tile += n_pairs, ++i) {
+                if (!wait_bar(smem_u32(acc_empty), (i & 1u) ^ 1u, abort_flag, p.err)) break;
+                tc_fence_after();
+                for (int kb = 0; kb < p.kb; ++kb, ++used) {
+                    const int stage = (int)(used % kStages);
+                    ok = wait_bar(smem_u32(&full[stage]), (used / kStages) & 1u, abort_flag, p.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + kBox, ssb = ssa + kSfA;
+                    if (one) {
+                        // scale columns of this stage: 2 x 4 of the tokens, then 2 x 8 of the weights (128 columns
+                        // of K, then 256 rows)
+                        const uint32_t ca = tmem + (uint32_t)(kScaleCol + 24 * stage), cb = ca + 8;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            copy_scales(ca + 4 * h, scale_desc(ssa + 512 * h));
+                            copy_scales(cb + 8 * h, scale_desc(ssb + 512 * h));
+                            copy_scales(cb + 8 * h + 4, scale_desc(ssb + 1024 + 512 * h));
+                        }
+                        const uint64_t da = smem_desc(sa), db = smem_desc(sb);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // 64 values = 32 bytes along K = 2 in the address field
+                            mma_mx(tmem, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), k & 1 ? idesc_mx(2) : idesc_mx(0),
+                                   ca + 4 * (k >> 1), cb + 8 * (k >> 1), kb > 0 || k > 0 ? 1u : 0u);
+                        mma_commit_pair(smem_u32(&empty[stage]));
+                    }
+                    __syncwarp();
+                }
+                if (one && ok) mma_commit_pair(smem_u32(acc_full));
+                __syncwarp();
+            }
+            if (one) mma_commit_pair(smem_u32(mma_done));
+            __syncwarp();
+            int dummy = 0;
+            mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
+        }
+    } else {
+        // ---------------- epilogue: four groups of four warps, each a quarter of a tile's columns
+        const int et = threadIdx.x - 64, quarter = warp & 3, part = et >> 7;
+        const bool lead = et == 0;
+        const int r = quarter * 32 + lane;  // row within this CTA's 128
+        uint32_t i = 0;
+        for (int tile = pair; tile < p.n_tiles; tile += n_pairs, ++i) {
+            const int m = tile / p.tiles_n, n = tile % p.tiles_n;
+            const int row0 = m * 256 + (int)rank * 128, c0 = n * kCols;
+            // biases of the tile's columns, and the residual's tile, under the products
+            constexpr float kg = GATED ? Act<ACT>::kGate : 1.f, ku = GATED ? Act<ACT>::kUp : 1.f;
+            if (et < 256) {
+                const int c = c0 + (GATED ? et & 127 : et);
+                const bool up = GATED && et >= 128;
+                const __nv_bfloat16 *b = up ? p.bias1 : p.bias0;
+                vec_s[et] = b && c < p.N ? (up ? ku : kg) * __bfloat162float(b[c]) : 0.f;
+            }
+            if (lead) store_wait_read();  // the last tile's store has read the tile
+            if (!GATED && p.has_res) {
+                if (p.plain) {
+                    team_sync();
+                    // a warp a row, the row's values side by side
+                    for (int q = warp - 2; q < 128 && row0 + q < p.M; q += 16)
+                        for (int c = lane; c < 256 && c0 + c < p.N; c += 32)
+                            *(__nv_bfloat16 *)(tile_s + (c >> 6) * kBox + swizzled(q, (c & 63) >> 3) + (c & 7) * 2) =
+                                p.res_p[(size_t)(row0 + q) * p.N + c0 + c];
+                } else if (lead) {
+                    uint32_t bytes = 0;
+                    for (int j = 0; j < 4; ++j) bytes += row0 < p.M && c0 + j * 64 < p.N ? kBox : 0;
+                    if (bytes) mbar_arrive_expect_tx(smem_u32(res_full), bytes);
+                    else mbar_arrive(smem_u32(res_full));
+                    for (int j = 0; j < 4; ++j)
+                        if (row0 < p.M && c0 + j * 64 < p.N)
+                            tma_load_2d(smem_u32(tile_s + j * kBox), &p.res, c0 + j * 64, row0, smem_u32(res_full));
+                }
+            }
+            team_sync();
+            // after an expired wait the waits return at once and the loop runs out
+            wait_bar(smem_u32(acc_full), i & 1u, abort_flag, p.err);
+            tc_fence_after();
+            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16);
+            uint32_t v[2][32];  // gated: gate and up of 32 hidden columns; else 64 outputs
+            tmem_ld32_nowait(t0 + (uint32_t)(GATED ? part * 32 : part * 64), v[0]);
+            tmem_ld32_nowait(t0 + (uint32_t)(GATED ? 128 + part * 32 : part * 64 + 32), v[1]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            pin(v[0]);
+            pin(v[1]);
+            tc_fence_before();
+            team_sync();
+            if (lead) mbar_arrive_cluster(map_rank(smem_u32(acc_empty), 0));
+            if constexpr (GATED) {
+                float h[32];
+                uint32_t most = 0;
+                const float *bg = vec_s + part * 32, *bu = bg + 128;
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 g = *reinterpret_cast<const float4 *>(bg + c), u = *reinterpret_cast<const float4 *>(bu + c);
+                    const float gf[4] = {g.x, g.y, g.z, g.w}, uf[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h[c + e] = Act<ACT>::hidden(fmaf(__uint_as_float(v[0][c + e]), kg, gf[e]),
+                                                    fmaf(__uint_as_float(v[1][c + e]), ku, uf[e]));
+                        most = max(most, abs_bits(h[c + e]));
+                    }
+                }
+                const uint32_t byte = mx_scale_byte(most);
+                const float inv = byte < 255u ? mx_inverse(byte) : 0.f;
+                uint32_t w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    w[c] = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[c] |= mx_byte(h[8 * c + 2 * e] * inv, h[8 * c + 2 * e + 1] * inv) << (8 * e);
+                    if (byte == 255u) w[c] = 0;
+                }
+                *reinterpret_cast<uint4 *>(tile_s + r * 64 + part * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                tile_s[128 * 64 + 16 * lane + 4 * quarter + part] = (uint8_t)byte;
+            } else {
+                if (p.has_res && !p.plain) wait_bar(smem_u32(res_full), i & 1u, abort_flag, p.err);
+                uint8_t *box = tile_s + part * kBox;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    uint4 *at = reinterpret_cast<uint4 *>(box + swizzled(r, u));
+                    uint32_t rw[4] = {0, 0, 0, 0};
+                    if (p.has_res) {
+                        const uint4 q = *at;
+                        rw[0] = q.x, rw[1] = q.y, rw[2] = q.z, rw[3] = q.w;
+                    }
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = 8 * u + 2 * e;
+                        const float2 b = *reinterpret_cast<const float2 *>(vec_s + part * 64 + c);
+                        w[e] = pack_bf16(__uint_as_float(v[c >> 5][c & 31]) + b.x + __uint_as_float(rw[e] << 16),
+                                         __uint_as_float(v[c >> 5][(c & 31) + 1]) + b.y + __uint_as_float(rw[e] & 0xffff0000u));
+                    }
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            fence_async_shared();
+            team_sync();
+            if constexpr (GATED) {
+                if (lead) {
+                    if (row0 < p.M) {
+                        tma_store_tile(&p.h, smem_u32(tile_s), n * 64, row0);
+                        uint8_t *dst = p.h_scale + ((size_t)(row0 / 128) * p.h_tiles + n) * 512;
+                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], 512;" ::"l"(dst),
+                                     "r"(smem_u32(tile_s + 128 * 64))
+                                     : "memory");
+                    }
+                    store_commit();
+                }
+            } else if (p.plain) {
+                for (int q = warp - 2; q < 128 && row0 + q < p.M; q += 16)
+                    for (int c = lane; c < 256 && c0 + c < p.N; c += 32)
+                        p.out_p[(size_t)(row0 + q) * p.N + c0 + c] =
+                            *(const __nv_bfloat16 *)(tile_s + (c >> 6) * kBox + swizzled(q, (c & 63) >> 3) + (c & 7) * 2);
+                team_sync();  // read before the next tile's residual comes
+            } else if (lead) {
+                for (int j = 0; j < 4; ++j)
+                    if (row0 < p.M && c0 + j * 64 < p.N)
+                        tma_store_tile(&p.out, smem_u32(tile_s + j * kBox), c0 + j * 64, row0);
+                store_commit();
+            }
+        }
+        if (lead) {
+            store_wait_all();  // shared memory outlives its stores, and after an expired wait the residual's copy
+            int dummy = 0;
+            if (*abort_flag && p.has_res && !p.plain && i)
+                mbar_wait(smem_u32(res_full), (i - 1) & 1u, (volatile int *)&dummy, p.err);
+        }
+    }
+
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // every product has run before either CTA goes; after an expired wait the counted copies land first
+        int dummy = 0;
+        mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
+        if (*abort_flag && rank == 0)
+            for (uint32_t i = *armed > kStages ? *armed - kStages : 0; i < *armed; ++i)
+                mbar_wait(smem_u32(&full[i % kStages]), (i / kStages) & 1u, (volatile int *)&dummy, p.err);
+    }
+    __syncthreads();
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free_pair(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- host side
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Codes as rows of bytes, boxes of 128 bytes x 128 rows; scale tiles as (row block, tile, 128 words), boxes of two tiles
+bool maps_of(CUtensorMap *codes, CUtensorMap *scale, const Mx &m, int64_t rows, int64_t width)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || !make_tile_map(codes, m.codes, rows, mx_pitch(width), mx_pitch(width), 1, 128)) return false;
+    const cuuint64_t tiles = (cuuint64_t)ceil_div(mx_blocks(width), 4);
+    cuuint64_t dims[3] = {128, tiles, (cuuint64_t)ceil_div(rows, 128)};
+    cuuint64_t strides[2] = {512, 512 * tiles};
+    cuuint32_t box[3] = {128, 2, 1}, estr[3] = {1, 1, 1};
+    return fn(scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(m.scale), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool GATED, int ACT>
+pmha_status launch(Params &p, const char *stage, cudaStream_t s)
+{
+    p.err = device_error_word();
+    if (!p.err) return PMHA_ERR_CUDA;
+    int pairs = 0;
+    auto kern = k_mx<GATED, ACT>;
+    static std::atomic<int> known[kKnownDevices];
+    const pmha_status st = pairs_at_once(kern, kThreads, kSmem, known, &pairs);
+    if (st != PMHA_OK) return st;
+    StageTimer timer(stage, s);
+    return launch_overlapping(kern, dim3(2u * (unsigned)std::min(pairs, p.n_tiles)), kThreads, kSmem, s, p);
+}
+
+pmha_status map_failed(const char *what)
+{
+    set_error("%s: cuTensorMapEncodeTiled failed", what);
+    return PMHA_ERR_CUDA;
+}
+
+pmha_status tiles_of(Params &p, int64_t M, int64_t N, int64_t K, int cols, const char *stage)
+{
+    p.M = (int)M, p.N = (int)N;
+    p.tiles_n = (int)ceil_div(N, cols);
+    p.kb = (int)ceil_div(K, 256);
+    const int64_t tiles = ceil_div(M, 256) * p.tiles_n;
+    if (tiles > 0x3fffffff) {
+        set_error("%s: %lld tiles exceed the 32-bit tile index", stage, (long long)tiles);
+        return PMHA_ERR_INVALID_ARG;
+    }
+    p.n_tiles = (int)tiles;
+    return PMHA_OK;
+}
+
+}  // namespace
+
+pmha_status mx_tc_linear(const MxLinear &a, const char *stage, cudaStream_t s)
+{
+    Params p = {};
+    const pmha_status st = tiles_of(p, a.M, a.N, a.K, 256, stage);
+    if (st != PMHA_OK) return st;
+    p.bias0 = (const __nv_bfloat16 *)a.bias;
+    p.has_res = a.residual != nullptr;
+    p.plain = a.N % 8 != 0;
+    p.res_p = (const __nv_bfloat16 *)a.residual;
+    p.out_p = (__nv_bfloat16 *)a.out;
+    if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.w, a.N, a.K) ||
+        (!p.plain && (!make_tile_map(&p.out, a.out, a.M, a.N, a.N, 2, 128) ||
+                      (a.residual && !make_tile_map(&p.res, a.residual, a.M, a.N, a.N, 2, 128)))))
+        return map_failed(stage);
+    return launch<false, 0>(p, stage, s);
+}
+
+pmha_status mx_tc_gated(const MxGated &a, cudaStream_t s)
+{
+    Params p = {};
+    const char *stage = "ffn_up_mx";
+    const pmha_status st = tiles_of(p, a.M, a.F, a.K, 128, stage);
+    if (st != PMHA_OK) return st;
+    p.bias0 = (const __nv_bfloat16 *)a.bg;
+    p.bias1 = (const __nv_bfloat16 *)a.bu;
+    p.h_scale = a.h_scale;
+    p.h_tiles = (int)ceil_div(mx_blocks(a.F), 4);
+    EncodeTiledFn fn = encode_fn();
+    cuuint64_t dims[2] = {(cuuint64_t)mx_pitch(a.F), (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)mx_pitch(a.F)};
+    cuuint32_t box[2] = {64, 128}, estr[2] = {1, 1};
+    if (!fn || !maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.wg, a.F, a.K) ||
+        !maps_of(&p.b1, &p.sb1, a.wu, a.F, a.K) ||
+        fn(&p.h, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.h_codes, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return map_failed(stage);
+    return a.act == PMHA_ACT_SILU ? launch<true, PMHA_ACT_SILU>(p, stage, s) : launch<true, PMHA_ACT_GELU>(p, stage, s);
+}
+
+}  // namespace pmha

@@ -582,6 +582,76 @@ pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, con
                                void *dbranch, void *dresidual, float *dpost, float *dgate, float *dpre, void *workspace,
                                size_t workspace_bytes, pmha_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (the OCP MX format MXFP4): serving from
+ * tokens and weights of E2M1 values (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their
+ * negatives) that share a power of two in blocks of 32 along each row.
+ */
+
+/*
+ * A matrix of `rows` rows of `width` values, 16-byte aligned device pointers:
+ *  codes  rows of ceil(width / 32) * 16 bytes, two codes a byte, the lower
+ *         column in the low half (sign in bit 3), zeros past the width;
+ *         pmha_mx_code_bytes().
+ *  scale  a byte b for each block of a row, 2^(b - 127) (255: NaN), in tiles of
+ *         128 rows by 4 blocks, 512 bytes each: tile (row / 128, block / 4) at
+ *         512 ((row / 128) * ceil(blocks / 4) + block / 4), in it the byte of
+ *         row r = row % 128 and block k = block % 4 at 16 (r % 32) + 4 (r / 32) + k.
+ *         Every tile is whole, with zeros past the rows and blocks;
+ *         pmha_mx_scale_bytes().
+ */
+typedef struct {
+    const void *codes;
+    const void *scale;
+} pmha_mx;
+/* Sizes of the two arrays; SIZE_MAX for sizes out of range. */
+size_t pmha_mx_code_bytes(int64_t rows, int64_t width);
+size_t pmha_mx_scale_bytes(int64_t rows, int64_t width);
+
+/*
+ * pmha_mx_quantize - x (rows, width) of `dtype` in 4 bits, into out's arrays,
+ * which are written whole. A block's scale is the least power of two 2^e with
+ * max|block| <= 6 * 2^e, at least 2^-127; a code is the value / 2^e rounded to
+ * the nearest E2M1 value, ties to the even code: as in exact arithmetic. A
+ * block with an infinity or a NaN gets the NaN scale.
+ * Sizes: rows 0 .. 2^31 - 1, width 1 .. 2^20, rows * width up to 2^40.
+ * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_CUDA.
+ */
+pmha_status pmha_mx_quantize(pmha_dtype dtype, int64_t rows, int64_t width, const void *x, const pmha_mx *out,
+                             pmha_stream stream);
+
+/*
+ * pmha_mx_linear - out = x weight^T + bias + residual, for x (rows, width) and
+ * weight (outputs, width) in 4 bits.
+ *  bias      device bf16 (outputs) or NULL.
+ *  residual  device bf16 (rows, outputs) or NULL.
+ *  out       device bf16 (rows, outputs).
+ * Sums are float32, rounded once. Any sizes; outputs a multiple of 8 are stored
+ * and their residual is read in tiles, others value by value.
+ * Needs no workspace. Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_CUDA.
+ */
+pmha_status pmha_mx_linear(int64_t rows, int64_t width, int64_t outputs, const pmha_mx *x, const pmha_mx *weight,
+                           const void *bias, const void *residual, void *out, pmha_stream stream);
+
+/* Weights of a gated block in 4 bits: wg, wu (F, E), wd (E, F). */
+typedef struct {
+    pmha_mx wg, wu, wd;
+} pmha_ffn_mx;
+
+/*
+ * pmha_ffn_forward_mx - pmha_ffn_forward for tokens x (rows, E) and all three
+ * weights in 4 bits. The hidden rows act(.) * (.), float32, are rounded to 4
+ * bits as pmha_mx_quantize does; biases, residual and out are bf16
+ * (params->dtype must be PMHA_BF16; params->wg, wu and wd are not read).
+ *  workspace  pmha_ffn_forward_mx_workspace_size() bytes, 256-byte aligned (SIZE_MAX
+ *             for invalid arguments). It holds the hidden rows and grows with them.
+ * Errors: PMHA_ERR_INVALID_ARG, PMHA_ERR_WORKSPACE, PMHA_ERR_CUDA.
+ */
+size_t pmha_ffn_forward_mx_workspace_size(const pmha_ffn_params *params, int64_t rows);
+pmha_status pmha_ffn_forward_mx(const pmha_ffn_params *params, const pmha_ffn_mx *weights, const pmha_mx *x,
+                                const void *residual, int64_t rows, void *out, void *workspace, size_t workspace_bytes,
+                                pmha_stream stream);
+
 /* Message describing the last failure of a call made by this thread ("" if none). */
 const char *pmha_last_error(void);
 
