@@ -901,9 +901,10 @@ class Checkpoint:
         return self.codes.numel() + 2 * self.scale.numel()
 
     @staticmethod
-    def _empty(shape, dtype, device) -> "Checkpoint":
-        return Checkpoint(torch.empty(shape, dtype=torch.int8, device=device),
-                          torch.empty((*shape[:-1], (shape[-1] + 31) // 32), dtype=torch.bfloat16, device=device), dtype)
+    def _empty(x) -> "Checkpoint":
+        *rows, width = x.shape
+        return Checkpoint(torch.empty_like(x, dtype=torch.int8),
+                          torch.empty((*rows, (width + 31) // 32), dtype=torch.bfloat16, device=x.device), x.dtype)
 
     def _struct(self):
         return _lib.PmhaKept(self.codes.data_ptr(), self.scale.data_ptr())
@@ -924,7 +925,7 @@ def pmha_checkpoint(x: torch.Tensor, stream=None) -> Checkpoint:
     bfloat16, each code the nearest integer to value / scale (off by half a scale at most)."""
     shape, rows, width, dev = _rows_of("x", x)
     with _on(dev, stream):
-        k = Checkpoint._empty(shape, x.dtype, x.device)
+        k = Checkpoint._empty(x)
         st = _library().pmha_checkpoint(_DTYPES[x.dtype], rows, width, x.data_ptr(), ctypes.byref(k._struct()),
                                         _stream_of(dev, stream))
     if st:
@@ -975,50 +976,45 @@ class JoinParams:
     residual_scale: float = 1.0
     eps: float = 1e-6
 
-    def _struct(self, dtype, width, rows, index):
-        gates = 0
-        if self.gate is not None:
-            if not isinstance(self.gate, _T) or self.gate.dim() not in (1, 2):
+    def _struct(self, dtype, width, index):
+        gates, gate, one = 0, self.gate, (width,)
+        if gate is not None:
+            if not isinstance(gate, _T) or gate.dim() not in (1, 2):
                 raise ValueError(f"gate must be ({width},) or (G, {width})")
-            gates = 1 if self.gate.dim() == 1 else self.gate.shape[0]
-        shape = (gates, width) if gates and self.gate.dim() == 2 else (width,)
-        return _lib.PmhaJoinParams(_DTYPES[dtype], width, _like("post", self.post, (width,), dtype, index),
-                                   _like("gate", self.gate, shape, dtype, index), gates, self.residual_scale,
-                                   _like("pre", self.pre, (width,), dtype, index), self.eps)
-
-
-def _join_inputs(params, branch, residual):
-    """(struct, shape, dtype, rows, device index, the four pointers of branch and residual)"""
-    shape, dtype = _shape_of("residual", residual)
-    dev = (residual.codes if isinstance(residual, Checkpoint) else residual).get_device()
-    width = shape[-1]
-    rows = (residual.codes if isinstance(residual, Checkpoint) else residual).numel() // width if width else 0
-    p = params._struct(dtype, width, rows, dev)
-    ptrs = []
-    for name, t in (("branch", branch), ("residual", residual)):
-        if isinstance(t, Checkpoint):
-            ptrs += [None, ctypes.byref(_kept_like(name, t, shape, dtype, dev))]
-        else:
-            ptrs += [_like(name, t, shape, dtype, dev), None]
-    return p, shape, dtype, rows, dev, ptrs
+            gates = 1 if gate.dim() == 1 else gate.shape[0]
+            gate = _like("gate", gate, one if gate.dim() == 1 else (gates, width), dtype, index)
+        return _lib.PmhaJoinParams(_DTYPES[dtype], width, _like("post", self.post, one, dtype, index), gate, gates,
+                                   self.residual_scale, _like("pre", self.pre, one, dtype, index), self.eps)
 
 
 def _join(params, branch, residual, keep_branch, keep_residual, stream):
-    p, shape, dtype, rows, dev, ptrs = _join_inputs(params, branch, residual)
-    device = (residual.codes if isinstance(residual, Checkpoint) else residual).device
-    kept = [None, None]
+    x = residual.codes if type(residual) is Checkpoint else residual
+    shape, dtype = _shape_of("residual", residual)
+    dev = x.get_device()
+    width = shape[-1]
+    p = params._struct(dtype, width, dev)
+    b = r = bk = rk = kb = kr = None
+    if type(branch) is Checkpoint:
+        bk = ctypes.byref(_kept_like("branch", branch, shape, dtype, dev))
+    else:
+        b = _like("branch", branch, shape, dtype, dev)
+    if x is residual:
+        r = x.data_ptr()
+    else:
+        rk = ctypes.byref(_kept_like("residual", residual, shape, dtype, dev))
     with _on(dev, stream):
-        s = torch.empty(shape, dtype=dtype, device=device)
-        out = None if params.pre is None else torch.empty(shape, dtype=dtype, device=device)
-        for i, wanted in enumerate((keep_branch, keep_residual)):
-            if wanted:
-                kept[i] = Checkpoint._empty(shape, dtype, device)
-        st = _library().pmha_join(ctypes.byref(p), rows, *ptrs, s.data_ptr(), _ptr(out),
-                                  *(None if k is None else ctypes.byref(k._struct()) for k in kept),
-                                  _stream_of(dev, stream))
+        s = torch.empty_like(x, dtype=dtype)
+        out = None if params.pre is None else torch.empty_like(s)
+        if keep_branch:
+            kb = Checkpoint._empty(branch)
+        if keep_residual:
+            kr = Checkpoint._empty(x)
+        st = _library().pmha_join(ctypes.byref(p), x.numel() // width if width else 0, b, bk, r, rk, s.data_ptr(),
+                                  None if out is None else out.data_ptr(), None if kb is None else ctypes.byref(kb._struct()),
+                                  None if kr is None else ctypes.byref(kr._struct()), _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_join")
-    return s, out, kept[0], kept[1]
+    return s, out, kb, kr
 
 
 def pmha_join(params: JoinParams, branch, residual, stream=None):
@@ -1040,7 +1036,7 @@ def pmha_join_checkpointed(params: JoinParams, branch: torch.Tensor, residual, k
 def pmha_join_backward_workspace_size(params: JoinParams, x: torch.Tensor) -> int:
     """Bytes of pmha_join_backward's workspace for tokens like x (its sum or dsum)."""
     shape, rows, width, dev = _rows_of("x", x)
-    p = params._struct(x.dtype, width, rows, dev)
+    p = params._struct(x.dtype, width, dev)
     return _join_size(p, rows)
 
 
@@ -1065,7 +1061,7 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
         raise ValueError("dout or dsum is needed")
     shape, rows, width, dev = _rows_of("dsum" if dout is None else "dout", like)
     dtype = like.dtype
-    p = params._struct(dtype, width, rows, dev)
+    p = params._struct(dtype, width, dev)
     s = _like("sum", sum, shape, dtype, dev)
     dy, ds = _like("dout", dout, shape, dtype, dev), _like("dsum", dsum, shape, dtype, dev)
     if isinstance(branch, Checkpoint):
@@ -1079,29 +1075,42 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
     with _on(dev, stream):
         dr = torch.empty_like(like) if input_grads else None
         db = dr if alone or not input_grads else torch.empty_like(like)
-        grads = [None if not param_grads or t is None else torch.empty(t.shape, dtype=torch.float32, device=like.device)
-                 for t in (params.post, params.gate, params.pre)]
+        dpost = dgate = dpre = None
+        if wanted:
+            f32 = torch.float32
+            dpost = None if params.post is None else torch.empty_like(params.post, dtype=f32)
+            dgate = None if params.gate is None else torch.empty_like(params.gate, dtype=f32)
+            dpre = None if params.pre is None else torch.empty_like(params.pre, dtype=f32)
         wp, wn, keep = _scratch(like, need, workspace)
         st = lib.pmha_join_backward(ctypes.byref(p), rows, b, bk, s, dy, ds, None if alone else _ptr(db), _ptr(dr),
-                                    *map(_ptr, grads), wp, wn, _stream_of(dev, stream))
+                                    _ptr(dpost), _ptr(dgate), _ptr(dpre), wp, wn, _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_join_backward")
-    return {"dbranch": db, "dresidual": dr, "dpre": grads[2], "dpost": grads[0], "dgate": grads[1]}
+    return {"dbranch": db, "dresidual": dr, "dpre": dpre, "dpost": dpost, "dgate": dgate}
 
 
 # ---------------------------------------------------------------- microscaled 4-bit floating point
-@dataclasses.dataclass
 class MxTensor:
     """A tensor (..., width) in microscaled 4 bits, as a matrix of its rows: E2M1 values in blocks of 32 along the row,
     each block times a power of two. codes uint8 (rows, ceil(width / 32) * 16), two a byte, the lower column in the low
     half; scale uint8 (row tiles, block tiles, 512), tiles of 128 rows by 4 blocks, byte b for 2^(b - 127), row r and
-    block k of a tile at 16 (r % 32) + 4 (r / 32) + k. shape: the tensor's."""
-    codes: torch.Tensor
-    scale: torch.Tensor
-    shape: tuple
+    block k of a tile at 16 (r % 32) + 4 (r / 32) + k. shape: the tensor's. Checked when it is made; its parts are not
+    exchanged afterwards."""
+    __slots__ = ("_codes", "_scale", "_shape", "_rows", "_width", "_index")
 
-    def __post_init__(self):
-        self.shape = torch.Size(self.shape)
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, shape):
+        shape = torch.Size(shape)
+        rows, width, c, s = MxTensor._sizes(shape)
+        if not isinstance(codes, _T) or not codes.is_cuda:
+            raise ValueError("codes and scale must be CUDA tensors")
+        index, u8 = codes.get_device(), torch.uint8
+        if _like("codes", codes, c, u8, index) is None or _like("scale", scale, s, u8, index) is None:
+            raise ValueError("codes or scale is missing")
+        self._codes, self._scale, self._shape, self._rows, self._width, self._index = codes, scale, shape, rows, width, index
+
+    codes = property(lambda self: self._codes)
+    scale = property(lambda self: self._scale)
+    shape = property(lambda self: self._shape)
 
     @property
     def nbytes(self) -> int:
@@ -1116,18 +1125,19 @@ class MxTensor:
         rows, blocks = math.prod(shape[:-1]), (width + 31) // 32
         return rows, width, (rows, blocks * 16), ((rows + 127) // 128, (blocks + 3) // 4, 512)
 
-    def _struct(self, name, index=None):
-        """(struct, rows, width, device index); index: the device it has to be on."""
-        rows, width, codes, scale = self._sizes(self.shape)
-        if index is None:
-            if not isinstance(self.codes, _T) or not self.codes.is_cuda:
-                raise ValueError(f"{name} must hold CUDA tensors")
-            index = self.codes.get_device()
-        c = _like(name + ".codes", self.codes, codes, torch.uint8, index)
-        s = _like(name + ".scale", self.scale, scale, torch.uint8, index)
-        if c is None or s is None:
-            raise ValueError(f"{name} lacks its codes or scales")
-        return _lib.PmhaMx(c, s), rows, width, index
+    @staticmethod
+    def _empty(x) -> "MxTensor":
+        """For a tensor like x, to be written."""
+        q = object.__new__(MxTensor)
+        shape = x.shape
+        rows, width, codes, scale = MxTensor._sizes(shape)
+        u8 = torch.uint8
+        q._codes, q._scale = torch.empty(codes, dtype=u8, device=x.device), torch.empty(scale, dtype=u8, device=x.device)
+        q._shape, q._rows, q._width, q._index = shape, rows, width, x.get_device()
+        return q
+
+    def _struct(self):
+        return _lib.PmhaMx(self._codes.data_ptr(), self._scale.data_ptr())
 
     def values(self) -> torch.Tensor:
         """The values that it stands for, in float64 (values near float32's end can round to 2^128). Torch operations, for
@@ -1145,42 +1155,35 @@ def pmha_mx_quantize(x: torch.Tensor, stream=None) -> MxTensor:
     """x (..., width), float32 or bfloat16, in microscaled 4 bits: a block's scale is the least power of two with
     max|block| <= 6 * scale, each value the nearest E2M1 value times that (ties to the even code). For tokens and, once,
     for weights."""
-    shape, rows, width, dev = _rows_of("x", x)
-    _, _, codes, scale = MxTensor._sizes(shape)
+    _, rows, width, dev = _rows_of("x", x)
     with _on(dev, stream):
-        q = MxTensor(torch.empty(codes, dtype=torch.uint8, device=x.device),
-                     torch.empty(scale, dtype=torch.uint8, device=x.device), shape)
-        st = _library().pmha_mx_quantize(_DTYPES[x.dtype], rows, width, x.data_ptr(),
-                                         ctypes.byref(_lib.PmhaMx(q.codes.data_ptr(), q.scale.data_ptr())),
+        q = MxTensor._empty(x)
+        st = _library().pmha_mx_quantize(_DTYPES[x.dtype], rows, width, x.data_ptr(), ctypes.byref(q._struct()),
                                          _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_mx_quantize")
     return q
 
 
-def _mx_tokens(name, x):
-    if not isinstance(x, MxTensor):
-        raise TypeError(f"{name} must be an MxTensor (pmha_mx_quantize makes one)")
-    return x._struct(name)
-
-
 def pmha_mx_linear(x: MxTensor, weight: MxTensor, bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x weight^T + bias + residual in bfloat16, for x (..., width) and weight (outputs, width) in microscaled 4 bits;
     sums are float32."""
-    xs, rows, width, dev = _mx_tokens("x", x)
-    if not isinstance(weight, MxTensor) or len(weight.shape) != 2 or weight.shape[1] != width:
-        raise ValueError(f"weight must be an MxTensor (outputs, {width})")
-    ws, N, _, _ = weight._struct("weight", dev)
-    bf16, shape = torch.bfloat16, (*x.shape[:-1], N)
+    if type(x) is not MxTensor or type(weight) is not MxTensor:
+        raise TypeError("x and weight must be MxTensors (pmha_mx_quantize makes them)")
+    width, dev, N = x._width, x._index, weight._rows
+    if len(weight._shape) != 2 or weight._width != width or weight._index != dev:
+        raise ValueError(f"weight must be an MxTensor (outputs, {width}) on cuda:{dev}")
+    bf16, shape = torch.bfloat16, (*x._shape[:-1], N)
     b = _like("bias", bias, (N,), bf16, dev)
     r = _like("residual", residual, shape, bf16, dev)
     o = _like("out", out, shape, bf16, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=bf16, device=x.codes.device)
+            out = torch.empty(shape, dtype=bf16, device=x._codes.device)
             o = out.data_ptr()
-        st = _library().pmha_mx_linear(rows, width, N, ctypes.byref(xs), ctypes.byref(ws), b, r, o, _stream_of(dev, stream))
+        st = _library().pmha_mx_linear(x._rows, width, N, ctypes.byref(x._struct()), ctypes.byref(weight._struct()), b, r, o,
+                                       _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_mx_linear")
     return out
@@ -1199,20 +1202,19 @@ class FfnMxParams:
 
     def _structs(self):
         """(pmha_ffn_params, pmha_ffn_mx, device index)"""
-        if not all(isinstance(w, MxTensor) for w in (self.wg, self.wu, self.wd)):
+        wg, wu, wd = self.wg, self.wu, self.wd
+        if not type(wg) is type(wu) is type(wd) is MxTensor:
             raise TypeError("wg, wu and wd must be MxTensors")
-        wd, E, F, dev = self.wd._struct("wd")
-        wg, *gs, _ = self.wg._struct("wg", dev)
-        wu, *us, _ = self.wu._struct("wu", dev)
-        if gs != [F, E] or us != [F, E]:
-            raise ValueError(f"wg and wu must be ({F}, {E}) beside wd ({E}, {F})")
+        E, F, dev = wd._rows, wd._width, wd._index
+        if wd._shape != (E, F) or wg._shape != (F, E) or wu._shape != (F, E) or wg._index != dev or wu._index != dev:
+            raise ValueError(f"wg and wu must be (F, E) beside wd (E, F), on one device: {wg._shape}, {wu._shape}, {wd._shape}")
         act = ACTS.get(self.act)
         if act is None:
             raise ValueError(f"act must be one of {sorted(ACTS)}")
         t = torch.bfloat16
         p = _lib.PmhaFfnParams(E, F, PMHA_BF16, act, None, None, None, _like("bg", self.bg, (F,), t, dev),
                                _like("bu", self.bu, (F,), t, dev), _like("bd", self.bd, (E,), t, dev))
-        return p, _lib.PmhaFfnMx(wg, wu, wd), dev
+        return p, _lib.PmhaFfnMx(wg._struct(), wu._struct(), wd._struct()), dev
 
     @staticmethod
     def from_params(params: FfnParams) -> "FfnMxParams":
@@ -1232,20 +1234,23 @@ def pmha_ffn_forward_mx(params: FfnMxParams, x: MxTensor, residual: torch.Tensor
     """The gated block on tokens x (..., E) in microscaled 4 bits, plus the residual, in bfloat16; the hidden rows are
     rounded to 4 bits between its products."""
     p, w, dev = params._structs()
-    xs, rows, width, xdev = _mx_tokens("x", x)
-    if width != p.embed_dim or xdev != dev:
+    if type(x) is not MxTensor:
+        raise TypeError("x must be an MxTensor (pmha_mx_quantize makes one)")
+    if x._width != p.embed_dim or x._index != dev:
         raise ValueError(f"x must be (..., {p.embed_dim}) on cuda:{dev}")
-    bf16 = torch.bfloat16
-    r = _like("residual", residual, x.shape, bf16, dev)
-    o = _like("out", out, x.shape, bf16, dev)
-    lib = _library()
-    need = _ffn_size(lib.pmha_ffn_forward_mx_workspace_size, p, rows, "pmha_ffn_forward_mx")
+    bf16, shape, rows = torch.bfloat16, x._shape, x._rows
+    r = _like("residual", residual, shape, bf16, dev)
+    o = _like("out", out, shape, bf16, dev)
+    lib, pp = _library(), ctypes.byref(p)
+    need = lib.pmha_ffn_forward_mx_workspace_size(pp, rows)
+    if need == _NO_SIZE:
+        need = _ffn_size(lib.pmha_ffn_forward_mx_workspace_size, p, rows, "pmha_ffn_forward_mx")  # raises
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(x.shape, dtype=bf16, device=x.codes.device)
+            out = torch.empty(shape, dtype=bf16, device=x._codes.device)
             o = out.data_ptr()
-        wp, wn, keep = _scratch(x.codes, need, workspace)
-        st = lib.pmha_ffn_forward_mx(ctypes.byref(p), ctypes.byref(w), ctypes.byref(xs), r, rows, o, wp, wn,
+        wp, wn, keep = _scratch(x._codes, need, workspace)
+        st = lib.pmha_ffn_forward_mx(pp, ctypes.byref(w), ctypes.byref(x._struct()), r, rows, o, wp, wn,
                                      _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_ffn_forward_mx")

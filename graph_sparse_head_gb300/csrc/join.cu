@@ -29,92 +29,186 @@ struct JoinArgs {
     float alpha, eps;
 };
 
-// LPR threads share a row; thread l of them holds pieces l, l + LPR, ... of VEC values, NV of them.
+constexpr int kResident = 3;  // blocks of an SM
+// Rows of 16-byte pieces come through a ring of kRing steps, each thread copying and reading its own pieces (no
+// barrier): what is in flight does not take registers. Others are loaded a step ahead.
+template <typename T, int VEC, int NV>
+constexpr int kRingOf = VEC * sizeof(T) == 16 ? 4 / NV : 0;
+constexpr int kSlotBytes = 2 * 16 * kThreads;  // branch and residual of one piece
+template <typename T, int VEC, int NV>
+constexpr size_t kRingBytes = (size_t)kRingOf<T, VEC, NV> * NV * kSlotBytes;
+
+// Teams of LPR threads (join.cuh) walk rows; thread l of a team holds pieces l, l + LPR, ... of VEC values, NV of them,
+// of a row, and of the weights.
 template <typename T, int VEC, int NV, int LPR, bool KEPT>
-__global__ void __launch_bounds__(kThreads) k_join(JoinArgs a)
+__global__ void __launch_bounds__(kThreads, 3) k_join(JoinArgs a)
 {
+    extern __shared__ __align__(16) uint8_t ring_s[];
     __shared__ TeamSums sh;
+    constexpr int kRows = kThreads / LPR;  // rows of a block's step
+    constexpr int kRing = kRingOf<T, VEC, NV>;
     int turn = 0;
     const int l = threadIdx.x % LPR;
-    const long long row = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-    const bool live = row < a.rows;
-    const long long base = row * a.width;
-    float b[NV * VEC], x[NV * VEC];
+    const long long step = (long long)gridDim.x * kRows;
+    const int groups = (a.width + kGroup - 1) / kGroup;
+    Vals<T, VEC> wpost[NV], wpre[NV], wgate[NV];  // the gate of the next row, if rows have different ones
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * LPR + l) * VEC;
-        float (&bj)[VEC] = *reinterpret_cast<float (*)[VEC]>(b + j * VEC);
-        float (&xj)[VEC] = *reinterpret_cast<float (*)[VEC]>(x + j * VEC);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) bj[i] = xj[i] = 0.f;
-        if (live && c < a.width) {
-            if constexpr (KEPT) {
-                if (a.branch.any()) load_source<T, VEC>(a.branch, row, c, a.width, bj);
-                load_source<T, VEC>(a.res, row, c, a.width, xj);
-            } else {
-                if (a.branch.p) load_row<T, VEC>(a.branch.p, base + c, bj);
-                load_row<T, VEC>(a.res.p, base + c, xj);
-            }
+        for (int i = 0; i < VEC; ++i) wpost[j].v[i] = wpre[j].v[i] = wgate[j].v[i] = from_f<T>(1.f);
+        if (c < a.width) {
+            if (a.post) load<T, VEC>((const T *)a.post + c, wpost[j].v);
+            if (a.out) load<T, VEC>((const T *)a.pre + c, wpre[j].v);
         }
     }
-    if constexpr (KEPT) {
-        auto keep_row = [&](const KeptOut &k, float *f) {
+    float sb[NV] = {}, sx[NV] = {};  // scales of kept values, of the next row
+    const bool own_gate = a.gate && a.per_gate < a.rows;
+    auto fetch_gate = [&](long long row) {
+        const long long at = own_gate ? (long long)((unsigned)row / (unsigned)a.per_gate) * a.width : 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + l) * VEC;
+            if (row < a.rows && c < a.width) load<T, VEC>((const T *)a.gate + at + c, wgate[j].v);
+        }
+    };
+    auto fetch_scales = [&](long long row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + l) * VEC;
+            if (!(row < a.rows && c < a.width)) continue;
+            if (a.branch.k.codes) sb[j] = __bfloat162float(a.branch.k.scale[row * groups + c / kGroup]);
+            if (a.res.k.codes) sx[j] = __bfloat162float(a.res.k.scale[row * groups + c / kGroup]);
+        }
+    };
+    uint8_t *ring = ring_s + threadIdx.x * 16;
+    using Codes = typename Bytes<VEC>::type;
+    union Piece {
+        Vals<T, VEC> v;
+        Codes codes;
+        uint32_t zero[(sizeof(Vals<T, VEC>) + 3) / 4];
+        __device__ __forceinline__ Piece() : zero{} {}
+    };
+    Piece nb[kRing ? 1 : NV], nx[kRing ? 1 : NV];  // the next row's, without a ring
+    auto fetch = [&](long long row, int slot) {
+        if constexpr (kRing > 0) {
+            const long long base = row * a.width;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = (j * LPR + l) * VEC;
-                T v[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) v[i] = from_f<T>(f[j * VEC + i]);  // exact: values of the type
-                keep<T, VEC>(k, row, c, a.width, live && c < a.width, v);
+                const bool in = row < a.rows && c < a.width;
+                const long long at = in ? base + c : 0;
+                uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
+                if (a.branch.p) copy16(p, (const T *)a.branch.p + at, in);
+                else if (KEPT && a.branch.k.codes) copy_codes<VEC>(p, a.branch.k.codes + at, in);
+                if (!KEPT || a.res.p) copy16(p + 16 * kThreads, (const T *)a.res.p + at, in);
+                else copy_codes<VEC>(p + 16 * kThreads, a.res.k.codes + at, in);
             }
-        };
-        if (a.keep_branch.codes) keep_row(a.keep_branch, b);
-        if (a.keep_res.codes) keep_row(a.keep_res, x);
-    }
-    float rb = 1.f;
-    if (a.post) {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
+            const long long base = row * a.width;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * LPR + l) * VEC;
+                nb[j] = nx[j] = Piece{};
+                if (!(row < a.rows && c < a.width)) continue;
+                if (a.branch.p) load<T, VEC>((const T *)a.branch.p + base + c, nb[j].v.v);
+                else if (KEPT && a.branch.k.codes) nb[j].codes = *reinterpret_cast<const Codes *>(a.branch.k.codes + base + c);
+                if (!KEPT || a.res.p) load<T, VEC>((const T *)a.res.p + base + c, nx[j].v.v);
+                else nx[j].codes = *reinterpret_cast<const Codes *>(a.res.k.codes + base + c);
+            }
+        }
+    };
+    // VEC values of a source, which lie at `p` in one form or the other; zeros where there is none
+    auto values = [&](const Source &s, const void *p, float scale, float *f) {
+        float (&v)[VEC] = *reinterpret_cast<float (*)[VEC]>(f);
+        if (s.p) load_row<T, VEC>(p, 0, v);
+        else if (KEPT && s.k.codes) unkeep<VEC>(*reinterpret_cast<const Codes *>(p), scale, v);
+    };
+    // a warp's threads walk together: row0 is the first of its rows
+    constexpr int kPerWarp = LPR < 32 ? 32 / LPR : 1;
+    const int sub = LPR < 32 ? (int)(threadIdx.x & 31) / LPR : 0;
+    const long long row_first = (long long)blockIdx.x * kRows + (int)threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
+    if constexpr (kRing > 0)
+        for (int i = 0; i < kRing - 1; ++i) fetch(row_first + i * step + sub, i);
+    else fetch(row_first + sub, 0);
+    if (a.gate) fetch_gate(row_first + sub);
+    if constexpr (KEPT) fetch_scales(row_first + sub);
+    int slot = 0;
+    for (long long row0 = row_first; row0 < a.rows; row0 += step) {
+        const long long row = row0 + sub, base = row * a.width;
+        const bool live = row < a.rows;
+        if constexpr (kRing > 0) {
+            fetch(row + (kRing - 1) * step, slot ? slot - 1 : kRing - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        }
+        float b[NV * VEC], x[NV * VEC];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + l) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) b[j * VEC + i] = x[j * VEC + i] = 0.f;
+            if constexpr (kRing > 0) {
+                const uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
+                values(a.branch, p, sb[j], b + j * VEC);
+                values(a.res, p + 16 * kThreads, sx[j], x + j * VEC);
+            } else if (live && c < a.width) {
+                values(a.branch, &nb[j], sb[j], b + j * VEC);
+                values(a.res, &nx[j], sx[j], x + j * VEC);
+            }
+        }
+        if constexpr (kRing > 0) slot = slot + 1 == kRing ? 0 : slot + 1;
+        else fetch(row + step, 0);
+        if constexpr (KEPT) {
+            fetch_scales(row + step);
+            auto keep_row = [&](const KeptOut &k, float *f) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = (j * LPR + l) * VEC;
+                    T v[VEC];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) v[i] = from_f<T>(f[j * VEC + i]);  // exact: values of the type
+                    keep<T, VEC>(KeptOut{k.codes + base + c, k.scale + row * groups + c / kGroup}, c % kGroup == 0, live && c < a.width, v);
+                }
+            };
+            if (a.keep_branch.codes) keep_row(a.keep_branch, b);
+            if (a.keep_res.codes) keep_row(a.keep_res, x);
+        }
+        // sum: of the weights' product first, exact in bf16, so that branch, weights and root meet in one more product and
+        // the addition: sums rounded to bf16 seldom fall to the other side of what exact arithmetic gives
+        float rb = 1.f;
+        if (a.post) {
+            float sc;
+            rb = row_root<NV * VEC, LPR>(b, a.width, a.eps, &sc, sh, turn);  // of b sc, which is what b holds now
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + l) * VEC;
+            Vals<T, VEC> s;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float z = b[j * VEC + i] * (to_f<T>(wpost[j].v[i]) * to_f<T>(wgate[j].v[i]));
+                s.v[i] = from_f<T>(fmaf(z, rb, a.alpha * x[j * VEC + i]));
+                x[j * VEC + i] = to_f<T>(s.v[i]);
+            }
+            if (live && c < a.width) store<T, VEC>((T *)a.sum + base + c, s.v);
+        }
+        if (own_gate) fetch_gate(row + step);
+        if (!a.out) continue;
         float sc;
-        rb = row_root<NV * VEC, LPR>(b, a.width, a.eps, &sc, sh, turn);  // of b sc, which is what b holds now
-    }
-    const long long gate_at = a.gate && live ? row / a.per_gate * a.width : 0;
+        const float r = row_root<NV * VEC, LPR>(x, a.width, a.eps, &sc, sh, turn);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * LPR + l) * VEC;
-        const bool in = live && c < a.width;
-        Vals<T, VEC> s;
-        if (a.post && in) {
-            float w[VEC];
-            load_row<T, VEC>(a.post, c, w);
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + l) * VEC;
+            if (!(live && c < a.width)) continue;
+            Vals<T, VEC> y;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) b[j * VEC + i] *= rb * w[i];
+            for (int i = 0; i < VEC; ++i) y.v[i] = from_f<T>(x[j * VEC + i] * r * to_f<T>(wpre[j].v[i]));
+            store<T, VEC>((T *)a.out + base + c, y.v);
         }
-        if (a.gate && in) {
-            float w[VEC];
-            load_row<T, VEC>(a.gate, gate_at + c, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) b[j * VEC + i] *= w[i];
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            s.v[i] = from_f<T>(fmaf(a.alpha, x[j * VEC + i], b[j * VEC + i]));
-            x[j * VEC + i] = to_f<T>(s.v[i]);
-        }
-        if (in) store<T, VEC>((T *)a.sum + base + c, s.v);
     }
-    if (!a.out) return;
-    float sc;
-    const float r = row_root<NV * VEC, LPR>(x, a.width, a.eps, &sc, sh, turn);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * LPR + l) * VEC;
-        if (!(live && c < a.width)) continue;
-        float w[VEC];
-        load_row<T, VEC>(a.pre, c, w);
-        Vals<T, VEC> y;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) y.v[i] = from_f<T>(x[j * VEC + i] * r * w[i]);
-        store<T, VEC>((T *)a.out + base + c, y.v);
-    }
+    // the last steps' copies (zeros past the rows) land before the block's shared memory can go to another
+    if constexpr (kRing > 0) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Rows of more than 2048 values: one block a row, which reads its inputs again from L1 / L2 for each step.
@@ -133,7 +227,8 @@ __global__ void __launch_bounds__(kThreads) k_join_wide(JoinArgs a)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(0.f);
             if (c < a.width) load<T, VEC>((const T *)p + base + c, v.v);
-            keep<T, VEC>(k, row, c, a.width, c < a.width, v.v);
+            keep<T, VEC>(KeptOut{k.codes + base + c, k.scale + row * groups_of(a.width) + c / kGroup}, c % kGroup == 0,
+                         c < a.width, v.v);
         }
     };
     if (a.keep_branch.codes) keep_row(a.keep_branch, a.branch.p);
@@ -169,20 +264,21 @@ __global__ void __launch_bounds__(kThreads) k_join_wide(JoinArgs a)
         for (int i = 0; i < VEC; ++i) b[i] = 0.f;
         if (a.branch.any()) load_source<T, VEC>(a.branch, row, c, a.width, b);
         load_source<T, VEC>(a.res, row, c, a.width, x);
-        if (a.post) {
-            load_row<T, VEC>(a.post, c, w);
+        if (a.post) load_row<T, VEC>(a.post, c, w);
+        else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) b[i] = b[i] * scb * (rb * w[i]);
+            for (int i = 0; i < VEC; ++i) w[i] = 1.f;
         }
         if (a.gate) {
-            load_row<T, VEC>(a.gate, gate_at + c, w);
+            float g[VEC];
+            load_row<T, VEC>(a.gate, gate_at + c, g);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) b[i] *= w[i];
+            for (int i = 0; i < VEC; ++i) w[i] *= g[i];
         }
         Vals<T, VEC> s;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            s.v[i] = from_f<T>(fmaf(a.alpha, x[i], b[i]));
+            s.v[i] = from_f<T>(fmaf(b[i] * scb * w[i], rb, a.alpha * x[i]));
             const float f = to_f<T>(s.v[i]);
             ss = fmaf(f, f, ss);
             most = fmaxf(most, fabsf(f));
@@ -216,44 +312,68 @@ __global__ void __launch_bounds__(kThreads) k_join_wide(JoinArgs a)
 }
 
 // ---------------------------------------------------------------- 8-bit tensors on their own
-// A lane takes VEC values of a group; a warp 32 / (32 / VEC) groups at a time.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) k_keep(const T *x, long long rows, int width, KeptOut k)
+// A lane takes VEC values of a group, 32 / VEC lanes a group; each thread has kAhead groups' values loaded before it uses
+// the first. A tensor whose rows are whole groups is one long row here (`groups` 0: no division by a row's groups).
+constexpr int kAhead = 4;
+struct Place {
+    long long at, group;  // of the values, of the scale
+    bool in;
+};
+template <int VEC>
+__device__ __forceinline__ Place place_of(long long g, long long n, unsigned groups, int width)
 {
-    constexpr int kLanes = kGroup / VEC;
-    const int groups = (width + kGroup - 1) / kGroup;
-    const long long n = rows * groups, step = (long long)gridDim.x * kThreads / kLanes;
-    const int l = threadIdx.x % kLanes;
+    const int l = (int)(threadIdx.x % (kGroup / VEC)) * VEC;
+    if (!groups) return {g * kGroup + l, g, g < n};
+    const long long row = n >> 32 ? g / groups : (long long)((unsigned)g / groups);
+    const int c = (int)(g - row * groups) * kGroup + l;
+    return {row * width + c, g, g < n && c < width};
+}
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) k_keep(const T *x, long long n, unsigned groups, int width, KeptOut k)
+{
+    constexpr int kPer = 32 / (kGroup / VEC);  // groups of a warp
+    const long long step = (long long)gridDim.x * (kThreads / 32) * kPer;
     // whole warps walk: a warp's groups are consecutive
-    const long long lead = ((long long)blockIdx.x * kThreads + threadIdx.x / 32 * 32) / kLanes;
-    for (long long g0 = lead; g0 < n; g0 += step) {
-        const long long g = g0 + (threadIdx.x % 32) / kLanes;
-        const long long row = g / groups;
-        const int c = (int)(g - row * groups) * kGroup + l * VEC;
-        const bool in = g < n && c < width;
-        Vals<T, VEC> v;
+    for (long long g0 = ((long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kPer; g0 < n; g0 += kAhead * step) {
+        Vals<T, VEC> v[kAhead];
+        Place p[kAhead];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(0.f);
-        if (in) load<T, VEC>(x + row * width + c, v.v);
-        keep<T, VEC>(k, row, c, width, in, v.v);
+        for (int i = 0; i < kAhead; ++i) {
+            p[i] = place_of<VEC>(g0 + i * step + (threadIdx.x % 32) / (kGroup / VEC), n, groups, width);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[i].v[e] = from_f<T>(0.f);
+            if (p[i].in) load<T, VEC>(x + p[i].at, v[i].v);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            keep<T, VEC>(KeptOut{k.codes + p[i].at, k.scale + p[i].group}, threadIdx.x % (kGroup / VEC) == 0, p[i].in, v[i].v);
     }
 }
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) k_unkeep(Kept k, long long rows, int width, T *out)
+__global__ void __launch_bounds__(kThreads) k_unkeep(Kept k, long long n, unsigned groups, int width, T *out)
 {
-    constexpr int kLanes = kGroup / VEC;
-    const int groups = (width + kGroup - 1) / kGroup;
-    const long long n = rows * groups, step = (long long)gridDim.x * kThreads / kLanes;
-    for (long long g = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes; g < n; g += step) {
-        const long long row = g / groups;
-        const int c = (int)(g - row * groups) * kGroup + (int)(threadIdx.x % kLanes) * VEC;
-        if (c >= width) continue;
-        float f[VEC];
-        load_kept<VEC>(k, row, c, width, f);
-        Vals<T, VEC> v;
+    const long long step = (long long)gridDim.x * kThreads / (kGroup / VEC);
+    for (long long g0 = ((long long)blockIdx.x * kThreads + threadIdx.x) / (kGroup / VEC); g0 < n; g0 += kAhead * step) {
+        typename Bytes<VEC>::type c[kAhead];
+        float scale[kAhead];
+        Place p[kAhead];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(f[i]);
-        store<T, VEC>(out + row * width + c, v.v);
+        for (int i = 0; i < kAhead; ++i) {
+            p[i] = place_of<VEC>(g0 + i * step, n, groups, width);
+            if (!p[i].in) continue;
+            c[i] = *reinterpret_cast<const typename Bytes<VEC>::type *>(k.codes + p[i].at);
+            scale[i] = __bfloat162float(k.scale[p[i].group]);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (!p[i].in) continue;
+            float f[VEC];
+            unkeep<VEC>(c[i], scale[i], f);
+            Vals<T, VEC> v;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v.v[e] = from_f<T>(f[e]);
+            store<T, VEC>(out + p[i].at, v.v);
+        }
     }
 }
 
@@ -305,11 +425,13 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
         StageTimer timer(kept ? "join_kept" : "join", cs);
         if (s.lpr) {
             const int64_t per = kThreads / s.lpr;
-            const unsigned grid = (unsigned)((rows + per - 1) / per);
+            const unsigned grid = (unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)num_sms() * kResident);
             join_dispatch(p.dtype, s, [&](auto t) {
                 using G = decltype(t);
-                if (kept) k_join<typename G::type, G::vec, G::nv, G::lpr, true><<<grid, kThreads, 0, cs>>>(a);
-                else k_join<typename G::type, G::vec, G::nv, G::lpr, false><<<grid, kThreads, 0, cs>>>(a);
+                constexpr size_t smem = kRingBytes<typename G::type, G::vec, G::nv>;
+                static_assert(smem <= 48 * 1024, "what a launch may have without asking");
+                if (kept) k_join<typename G::type, G::vec, G::nv, G::lpr, true><<<grid, kThreads, smem, cs>>>(a);
+                else k_join<typename G::type, G::vec, G::nv, G::lpr, false><<<grid, kThreads, smem, cs>>>(a);
             });
         } else {
             dispatch_wide(p.dtype, s.vec, [&](auto t) {
@@ -323,6 +445,13 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
     return PMHA_OK;
 }
 
+static unsigned kept_groups(int64_t width) { return width % kGroup ? (unsigned)groups_of(width) : 0u; }
+// Every thread its kAhead groups once, or as many blocks as are resident
+static unsigned kept_grid(int64_t n, int vec)
+{
+    const int64_t threads = (n * (kGroup / vec) + kAhead - 1) / kAhead;
+    return (unsigned)std::min<int64_t>((threads + kThreads - 1) / kThreads, (int64_t)num_sms() * 8);
+}
 static pmha_status check_kept(const char *who, pmha_dtype dtype, int64_t rows, int64_t width, const void *x,
                               const pmha_kept *kept)
 {
@@ -351,10 +480,9 @@ pmha_status pmha_checkpoint(pmha_dtype dtype, int64_t rows, int64_t width, const
         StageTimer timer("checkpoint", cs);
         dispatch_wide(dtype, shape_of(dtype, width).vec, [&](auto t) {
             using G = decltype(t);
-            const int64_t lanes = rows * groups_of(width) * (kGroup / G::vec);
-            const unsigned grid = (unsigned)std::min<int64_t>((lanes + kThreads - 1) / kThreads, (int64_t)num_sms() * 8);
-            k_keep<typename G::type, G::vec>
-                <<<grid, kThreads, 0, cs>>>((const typename G::type *)x, rows, (int)width, kept_out(kept));
+            const int64_t n = rows * groups_of(width);
+            k_keep<typename G::type, G::vec><<<kept_grid(n, G::vec), kThreads, 0, cs>>>(
+                (const typename G::type *)x, n, kept_groups(width), (int)width, kept_out(kept));
         });
     }
     count_launch();
@@ -372,10 +500,9 @@ pmha_status pmha_checkpoint_restore(pmha_dtype dtype, int64_t rows, int64_t widt
         StageTimer timer("checkpoint_restore", cs);
         dispatch_wide(dtype, shape_of(dtype, width).vec, [&](auto t) {
             using G = decltype(t);
-            const int64_t lanes = rows * groups_of(width) * (kGroup / G::vec);
-            const unsigned grid = (unsigned)std::min<int64_t>((lanes + kThreads - 1) / kThreads, (int64_t)num_sms() * 8);
-            k_unkeep<typename G::type, G::vec><<<grid, kThreads, 0, cs>>>(source(nullptr, kept).k, rows, (int)width,
-                                                                          (typename G::type *)out);
+            const int64_t n = rows * groups_of(width);
+            k_unkeep<typename G::type, G::vec><<<kept_grid(n, G::vec), kThreads, 0, cs>>>(
+                source(nullptr, kept).k, n, kept_groups(width), (int)width, (typename G::type *)out);
         });
     }
     count_launch();

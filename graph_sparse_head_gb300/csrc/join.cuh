@@ -8,6 +8,8 @@
 namespace pmha {
 namespace {
 
+__host__ __device__ inline int64_t groups_of(int64_t width) { return (width + kGroup - 1) / kGroup; }
+
 // A tensor of the layer type, or one kept in 8 bits (codes set), or none.
 struct Source {
     const void *p;
@@ -35,63 +37,101 @@ __device__ __forceinline__ void load_row(const void *p, long long at, float (&v)
     for (int i = 0; i < VEC; ++i) v[i] = to_f<T>(t.v[i]);
 }
 
+// 8 bytes from global to shared memory, or zeros
+__device__ __forceinline__ void copy8(void *dst, const void *src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 8 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 4 : 0)
+                 : "memory");
+}
+
+// VEC codes
+template <int VEC>
+__device__ __forceinline__ void copy_codes(void *dst, const int8_t *src, bool in)
+{
+    static_assert(VEC == 8 || VEC == 4, "of a piece of 16 bytes");
+    if constexpr (VEC == 8) copy8(dst, src, in);
+    else copy4(dst, src, in);
+}
+
 // A row is shared by LPR threads ("a team"), lanes of one warp or whole warps of
 // a block, each with some eight values in registers. Sums over a team of warps go through
-// shared memory: a warp writes to one of two places in turn, so that one barrier a sum is enough
+// shared memory: a warp writes to one of two places in turn, so that one barrier for up to three sums is enough
 // (who writes to a place again has passed the barrier behind which all have read it).
 struct TeamSums {
-    float v[2][kThreads / 32];
+    float v[2][3][kThreads / 32];
 };
-template <int LPR, bool MAX>
-__device__ __forceinline__ float team_reduce(float v, TeamSums &sh, int &turn)
+template <int LPR, bool MAX, int K>
+__device__ __forceinline__ void team_reduce(float (&v)[K], TeamSums &sh, int &turn)
 {
+    static_assert(K <= 3, "places in TeamSums");
     constexpr int kLanes = LPR < 32 ? LPR : 32;
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-        const float t = __shfl_xor_sync(kFull, v, o);
-        v = MAX ? fmaxf(v, t) : v + t;
-    }
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float t = __shfl_xor_sync(kFull, v[k], o);
+            v[k] = MAX ? fmaxf(v[k], t) : v[k] + t;
+        }
     if constexpr (LPR > 32) {
         constexpr int kWarps = LPR / 32;
         const int warp = threadIdx.x >> 5, first = warp / kWarps * kWarps;
-        if ((threadIdx.x & 31) == 0) sh.v[turn][warp] = v;
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) sh.v[turn][k][warp] = v[k];
+        }
         if constexpr (LPR == kThreads) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / LPR), "n"(LPR) : "memory");
-        v = sh.v[turn][first];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) v = MAX ? fmaxf(v, sh.v[turn][first + i]) : v + sh.v[turn][first + i];
+        for (int k = 0; k < K; ++k) {
+            v[k] = sh.v[turn][k][first];
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i)
+                v[k] = MAX ? fmaxf(v[k], sh.v[turn][k][first + i]) : v[k] + sh.v[turn][k][first + i];
+        }
         turn ^= 1;
     }
-    return v;
 }
-template <int LPR>
-__device__ __forceinline__ float team_sum(float v, TeamSums &sh, int &turn)
+template <int N>
+__device__ __forceinline__ float squares_of(const float (&f)[N])
 {
-    return team_reduce<LPR, false>(v, sh, turn);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss = fmaf(f[i], f[i], ss);
+    return ss;
+}
+// The power of two that a team's row is scaled by, in place, where `over`.
+template <int N, int LPR>
+__device__ __forceinline__ float scale_row(float (&f)[N], bool over, TeamSums &sh, int &turn)
+{
+    float most[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) most[0] = fmaxf(most[0], fabsf(f[i]));
+    team_reduce<LPR, true>(most, sh, turn);
+    const float sc = over ? down_scale(most[0]) : 1.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] *= sc;
+    return sc;
 }
 // The row's 1 / rms; a row whose squares leave float32 is scaled in place by *sc first.
 template <int N, int LPR>
 __device__ __forceinline__ float row_root(float (&f)[N], int width, float eps, float *sc, TeamSums &sh, int &turn)
 {
-    auto squares = [&]() {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) ss = fmaf(f[i], f[i], ss);
-        return team_sum<LPR>(ss, sh, turn);
-    };
-    float ss = squares();
+    float ss[1] = {squares_of(f)};
+    team_reduce<LPR, false>(ss, sh, turn);
     *sc = 1.f;
-    if (__any_sync(kFull, ss > kMostSquares)) {  // a team of warps comes here together: they have one row
-        float most = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(f[i]));
-        most = team_reduce<LPR, true>(most, sh, turn);
-        if (ss > kMostSquares) *sc = down_scale(most);
-#pragma unroll
-        for (int i = 0; i < N; ++i) f[i] *= *sc;
-        ss = squares();
+    if (__any_sync(kFull, ss[0] > kMostSquares)) {  // a team of warps comes here together: they have one row
+        *sc = scale_row<N, LPR>(f, ss[0] > kMostSquares, sh, turn);
+        ss[0] = squares_of(f);
+        team_reduce<LPR, false>(ss, sh, turn);
     }
-    return rsqrtf(ss / (float)width + eps * *sc * *sc);
+    return rsqrtf(ss[0] / (float)width + eps * *sc * *sc);
 }
 
 // The kernel shape of a width up to 2048: values a piece, pieces a thread, threads a row; 0 threads: one block walks the
@@ -169,7 +209,6 @@ inline bool any_overlap(const Span (&in)[NI], const Span (&out)[NO])
     }
     return false;
 }
-inline int64_t groups_of(int64_t width) { return (width + kGroup - 1) / kGroup; }
 inline Span codes_of(const pmha_kept *k, int64_t rows, int64_t width)
 {
     return k ? Span{k->codes, (size_t)(rows * width)} : Span{nullptr, 0};

@@ -21,21 +21,31 @@ struct JoinBwdArgs {
 // float32 one after the other; the blocks' partial rows are added as pairs of floats.
 constexpr int kSteps = 128;
 
+// Rows of 16-byte pieces come through a ring of kRing steps, each thread copying and reading its own pieces (no
+// barrier): what is in flight does not take registers. Others are loaded when they are needed.
+template <typename T, int VEC, int NV>
+constexpr int kRingOf = VEC * sizeof(T) == 16 ? 4 / NV : 0;
+constexpr int kSlotBytes = 4 * 16 * kThreads;  // dout, sum, dsum and branch of one piece
+template <typename T, int VEC, int NV>
+constexpr size_t kRingBytes = (size_t)kRingOf<T, VEC, NV> * NV * kSlotBytes;
+
 // A team (join.cuh) walks rows of one gate and keeps its columns' two sums over rows in
 // registers; a block adds its teams' through shared memory and writes one partial row of each.
 template <typename T, int VEC, int NV, int LPR, bool KEPT>
-__global__ void __launch_bounds__(kThreads) k_join_bwd(JoinBwdArgs a)
+__global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
 {
-    extern __shared__ float shw[];  // width values
+    extern __shared__ __align__(16) float shw[];  // the ring, then width values
     __shared__ TeamSums sh;
     constexpr int kRows = kThreads / LPR, N = NV * VEC;  // rows of a block's step
     constexpr int kPerWarp = LPR < 32 ? 32 / LPR : 1;
+    constexpr int kRing = kRingOf<T, VEC, NV>;
     const int l = threadIdx.x % LPR;
     int turn = 0;
     const long long gate = blockIdx.x / a.blocks_per_gate;
     const long long begin = gate * a.per_gate, end = begin + a.per_gate;
     const long long step = (long long)a.blocks_per_gate * kRows;
     const float inv_width = 1.f / (float)a.width;
+    const int groups = (a.width + kGroup - 1) / kGroup;
     Vals<T, VEC> wpre[NV], wpost[NV], wgate[NV];
     float q[N], pb[N];
 #pragma unroll
@@ -52,15 +62,57 @@ __global__ void __launch_bounds__(kThreads) k_join_bwd(JoinBwdArgs a)
             if (a.gate) load<T, VEC>((const T *)a.gate + gate * a.width + c, wgate[j].v);
         }
     }
-    const bool with_branch = a.branch.any();
+    uint8_t *ring = (uint8_t *)shw + threadIdx.x * 16;
+    float scale[NV] = {};  // of the kept branch's values, loaded a step ahead
+    auto fetch_scale = [&](long long row) {
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * LPR + l) * VEC;
+                if (row < end && c < a.width) scale[j] = __bfloat162float(a.branch.k.scale[row * groups + c / kGroup]);
+            }
+        }
+    };
+    auto fetch = [&](long long row, int slot) {
+        if constexpr (kRing > 0) {
+            const long long base = row * a.width;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * LPR + l) * VEC;
+                const bool in = row < end && c < a.width;
+                const long long at = in ? base + c : 0;
+                uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
+                if (a.dy) {
+                    copy16(p, (const T *)a.dy + at, in);
+                    copy16(p + 16 * kThreads, (const T *)a.sum + at, in);
+                }
+                if (a.ds) copy16(p + 32 * kThreads, (const T *)a.ds + at, in);
+                if constexpr (KEPT) {
+                    copy_codes<VEC>(p + 48 * kThreads, a.branch.k.codes + at, in);
+                } else if (a.branch.p) {
+                    copy16(p + 48 * kThreads, (const T *)a.branch.p + at, in);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
     // a warp's threads walk together: row0 is the first of its rows
-    for (long long row0 = begin + (long long)(blockIdx.x % a.blocks_per_gate) * kRows +
-                          (int)threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
-         row0 < end; row0 += step) {
-        const long long row = row0 + (LPR < 32 ? (int)(threadIdx.x & 31) / LPR : 0), base = row * a.width;
+    const int sub = LPR < 32 ? (int)(threadIdx.x & 31) / LPR : 0;
+    const long long row_first = begin + (long long)(blockIdx.x % a.blocks_per_gate) * kRows +
+                                (int)threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
+    if constexpr (kRing > 0)
+        for (int i = 0; i < kRing - 1; ++i) fetch(row_first + i * step + sub, i);
+    fetch_scale(row_first + sub);
+    int slot = 0;
+    for (long long row0 = row_first; row0 < end; row0 += step) {
+        const long long row = row0 + sub, base = row * a.width;
         const bool live = row < end;
-        float D[N], f[N], b[N];
+        float D[N], f[N], b[N], da[N];
         Vals<T, VEC> g[NV];
+        if constexpr (kRing > 0) {
+            fetch(row + (kRing - 1) * step, slot ? slot - 1 : kRing - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + l) * VEC;
@@ -72,34 +124,61 @@ __global__ void __launch_bounds__(kThreads) k_join_bwd(JoinBwdArgs a)
                 Dj[i] = fj[i] = bj[i] = 0.f;
                 g[j].v[i] = from_f<T>(0.f);
             }
-            if (live && c < a.width) {
-                if (a.ds) load_row<T, VEC>(a.ds, base + c, Dj);
+            if constexpr (kRing > 0) {
+                const uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
+                if (a.dy) {
+                    load<T, VEC>((const T *)p, g[j].v);
+                    load_row<T, VEC>(p + 16 * kThreads, 0, fj);
+                }
+                if (a.ds) load_row<T, VEC>(p + 32 * kThreads, 0, Dj);
+                if constexpr (KEPT)
+                    unkeep<VEC>(*reinterpret_cast<const typename Bytes<VEC>::type *>(p + 48 * kThreads), scale[j], bj);
+                else if (a.branch.p) load_row<T, VEC>(p + 48 * kThreads, 0, bj);
+            } else if (live && c < a.width) {
                 if (a.dy) {
                     load<T, VEC>((const T *)a.dy + base + c, g[j].v);
                     load_row<T, VEC>(a.sum, base + c, fj);
                 }
-                if constexpr (KEPT) load_kept<VEC>(a.branch.k, row, c, a.width, bj);
-                else if (with_branch) load_row<T, VEC>(a.branch.p, base + c, bj);
+                if (a.ds) load_row<T, VEC>(a.ds, base + c, Dj);
+                if constexpr (KEPT)
+                    unkeep<VEC>(*reinterpret_cast<const typename Bytes<VEC>::type *>(a.branch.k.codes + base + c), scale[j], bj);
+                else if (a.branch.p) load_row<T, VEC>(a.branch.p, base + c, bj);
             }
         }
+        fetch_scale(row + step);
+        if constexpr (kRing > 0) slot = slot + 1 == kRing ? 0 : slot + 1;
+        // the squares' sums of sum and branch and the sum of dout pre sum, together
+        float sc = 1.f, scb = 1.f;
+        float t[3];
+        auto stats = [&]() {
+            t[0] = squares_of(f);
+            t[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) t[1] = fmaf(da[i], f[i], t[1]);
+            t[2] = a.post ? squares_of(b) : 0.f;
+            team_reduce<LPR, false>(t, sh, turn);
+        };
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) da[j * VEC + i] = to_f<T>(g[j].v[i]) * to_f<T>(wpre[j].v[i]);
+        stats();
+        const bool over = t[0] > kMostSquares || !(fabsf(t[1]) <= kMostSquares), overb = t[2] > kMostSquares;
+        if (__any_sync(kFull, over || overb)) {  // a team of warps comes here together: they have one row
+            sc = scale_row<N, LPR>(f, over, sh, turn);
+            scb = scale_row<N, LPR>(b, overb, sh, turn);
+            stats();
+        }
         if (a.dy) {
-            float sc, as = 0.f;
-            const float r = row_root<N, LPR>(f, a.width, a.eps, &sc, sh, turn);  // of f as it is now, times sc
+            const float r = rsqrtf(t[0] * inv_width + a.eps * sc * sc);  // of sum sc
+            const float k = t[1] * inv_width * r * r, rd = r * sc;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    f[j * VEC + i] *= r;
-                    as = fmaf(to_f<T>(g[j].v[i]) * to_f<T>(wpre[j].v[i]), f[j * VEC + i], as);
-                }
-            const float k = team_sum<LPR>(as, sh, turn) * inv_width, rd = r * sc;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float gi = to_f<T>(g[j].v[i]), u = f[j * VEC + i];
-                    q[j * VEC + i] = fmaf(gi, u, q[j * VEC + i]);
-                    D[j * VEC + i] = fmaf(rd, fmaf(-u, k, gi * to_f<T>(wpre[j].v[i])), D[j * VEC + i]);
+                    const int n = j * VEC + i;
+                    q[n] = fmaf(to_f<T>(g[j].v[i]), f[n] * r, q[n]);
+                    D[n] = fmaf(rd, fmaf(-f[n], k, da[n]), D[n]);
                 }
         }
         if (a.dres) {
@@ -113,25 +192,26 @@ __global__ void __launch_bounds__(kThreads) k_join_bwd(JoinBwdArgs a)
                 store<T, VEC>((T *)a.dres + base + c, o.v);
             }
         }
-        float rb = 1.f, scb = 1.f;
+        float rb = 1.f;
         if (a.post) {
-            rb = row_root<N, LPR>(b, a.width, a.eps, &scb, sh, turn);
+            rb = rsqrtf(t[2] * inv_width + a.eps * scb * scb);
 #pragma unroll
             for (int i = 0; i < N; ++i) b[i] *= rb;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) pb[i] = fmaf(D[i], b[i], pb[i]);
         if (!a.dbranch) continue;
-        float bs = 0.f;
+        float bs[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 D[j * VEC + i] *= to_f<T>(wgate[j].v[i]) * to_f<T>(wpost[j].v[i]);
-                bs = fmaf(D[j * VEC + i], b[j * VEC + i], bs);
+                bs[0] = fmaf(D[j * VEC + i], b[j * VEC + i], bs[0]);
             }
         if (a.post) {
-            const float k = team_sum<LPR>(bs, sh, turn) * inv_width, rd = rb * scb;
+            team_reduce<LPR, false>(bs, sh, turn);
+            const float k = bs[0] * inv_width, rd = rb * scb;
 #pragma unroll
             for (int i = 0; i < N; ++i) D[i] = rd * fmaf(-b[i], k, D[i]);
         }
@@ -145,6 +225,8 @@ __global__ void __launch_bounds__(kThreads) k_join_bwd(JoinBwdArgs a)
             store<T, VEC>((T *)a.dbranch + base + c, o.v);
         }
     }
+    // the last steps' copies (zeros past the rows) land before the block's shared memory is used for other things
+    if constexpr (kRing > 0) asm volatile("cp.async.wait_all;" ::: "memory");
     // a warp's rows, then the warps (or teams of warps) one after the other
     constexpr int kTeam = LPR < 32 ? 32 : LPR;
     const int team = threadIdx.x / kTeam;
@@ -360,14 +442,14 @@ pmha_status check_join_backward(const pmha_join_params *p, int64_t rows)
     return PMHA_OK;
 }
 
-// Blocks that share the rows of a gate, each of which writes a partial row: together at most about four a SM, more where
-// a block would take more than kSteps steps.
+// Blocks that share the rows of a gate, each of which writes a partial row: all gates' together about two a SM, which are
+// resident, or as many times that as no block takes more than kSteps steps.
 int64_t bwd_blocks(pmha_dtype dt, int64_t per_gate, int64_t gates, int64_t width)
 {
     const Shape s = join_shape(dt, width);
     const int64_t per = s.lpr ? kThreads / s.lpr : 1, steps = (per_gate + per - 1) / per;
-    const int64_t full = std::max<int64_t>(1, (int64_t)num_sms() * 4 / gates);
-    return std::max<int64_t>(1, std::min(steps, std::max(full, (steps + kSteps - 1) / kSteps)));
+    const int64_t full = std::max<int64_t>(1, (int64_t)num_sms() * (s.lpr ? 2 : 4) / gates);
+    return std::min(steps, full * ((steps + full * kSteps - 1) / (full * kSteps)));
 }
 
 }  // namespace
@@ -446,14 +528,19 @@ pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, con
     if (!need_branch) a.post = nullptr;
     const Shape s = join_shape(p.dtype, w);
     const unsigned grid = (unsigned)(blocks * gates);
+    cudaError_t attr = cudaSuccess;
     {
         StageTimer timer(branch_kept ? "join_backward_kept" : "join_backward", cs);
         if (s.lpr)
             join_dispatch(p.dtype, s, [&](auto t) {
                 using G = decltype(t);
                 using T = typename G::type;
-                if (b.k.codes) k_join_bwd<T, G::vec, G::nv, G::lpr, true><<<grid, kThreads, (size_t)w * 4, cs>>>(a);
-                else k_join_bwd<T, G::vec, G::nv, G::lpr, false><<<grid, kThreads, (size_t)w * 4, cs>>>(a);
+                // the ring, and in its place at the end the block's sums
+                const size_t smem = std::max((size_t)w * 4, kRingBytes<T, G::vec, G::nv>);
+                auto kern = b.k.codes ? k_join_bwd<T, G::vec, G::nv, G::lpr, true> : k_join_bwd<T, G::vec, G::nv, G::lpr, false>;
+                attr = smem > 48 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                        : cudaSuccess;
+                if (attr == cudaSuccess) kern<<<grid, kThreads, smem, cs>>>(a);
             });
         else
             dispatch_wide(p.dtype, s.vec, [&](auto t) {
@@ -461,6 +548,7 @@ pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, con
                 k_join_bwd_wide<typename G::type, G::vec><<<grid, kThreads, 0, cs>>>(a);
             });
     }
+    PMHA_CUDA_TRY(attr);
     count_launch();
     PMHA_CUDA_TRY(cudaGetLastError());
     if (sums) {

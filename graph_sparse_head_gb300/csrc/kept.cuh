@@ -26,31 +26,48 @@ struct KeptOut {
     __nv_bfloat16 *scale;
 };
 
-// The scale of a group from the bits of its largest magnitude (compared as integers, infinities and NaN come last).
-__device__ __forceinline__ float kept_scale(uint32_t most)
+// The scale of a group from the bits of its largest magnitude (compared as integers, infinities and NaN come last): the
+// least bfloat16 c with 127 c >= max (127 c is exact in float32), found beside an approximate quotient.
+__device__ __forceinline__ float kept_scale(uint32_t bits)
 {
-    if (most >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-    const float up = __fdiv_ru(__uint_as_float(most), 127.f);
-    const uint32_t b = (__float_as_uint(up) + 0xffffu) & 0xffff0000u;  // up again: that of the exact quotient
-    return fmaxf(__uint_as_float(b), kKeptLeast);
+    if (bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+    const float most = __uint_as_float(bits);
+    uint32_t c = (__float_as_uint(most * (1.f / 127.f)) + 0xffffu) & 0xffff0000u;
+    if (c > __float_as_uint(kKeptLeast)) {  // normal numbers, and their neighbours below
+        if (127.f * __uint_as_float(c) < most) c += 0x10000u;
+        else if (127.f * __uint_as_float(c - 0x10000u) >= most) c -= 0x10000u;
+    }
+    return fmaxf(__uint_as_float(c), kKeptLeast);
 }
-// v / scale to the nearest integer, in the low byte. A bfloat16 v and scale: the quotient is at least 2^-10 away from a
-// half unless it is one, and a product with the reciprocal is within 2^-17 of it, so that rounding it to a grid of 2^-11
-// first gives back the halves. A float32 v: the rounded quotient is a half only if the exact one is (the half times the
-// scale has 16 bits, v is then at least its last bit away).
+__device__ __forceinline__ float kept_inverse(float scale)  // within 2^-22
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(scale));
+    return y;
+}
+// v / scale to the nearest integer, in the low byte, ties to even. A bfloat16 v and scale: the quotient is at least 2^-10
+// away from a half unless it is one, and its product with the inverse is within 2^-15 of it, so that rounding it to a grid of
+// 2^-11 first gives back the halves. A float32 v: the remainder of the product's nearest integer q is exact (both v and
+// q scale are multiples of its last bit) and says whether the neighbour is nearer, or as near and even.
 template <typename T>
 __device__ __forceinline__ uint32_t kept_code(float v, float scale, float inv)
 {
-    float y;
-    if constexpr (sizeof(T) == 2) y = __fsub_rn(__fmaf_rn(v, inv, 6144.f), 6144.f);
-    else y = __fdiv_rn(v, scale);
-    return __float_as_uint(__fadd_rn(y, 12582912.f)) & 0xffu;  // 1.5 * 2^23
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+    if constexpr (sizeof(T) == 2) {
+        const float y = __fsub_rn(__fmaf_rn(v, inv, 6144.f), 6144.f);
+        return __float_as_uint(__fadd_rn(y, kRound)) & 0xffu;
+    } else {
+        const float m = __fmaf_rn(v, inv, kRound), q = __fsub_rn(m, kRound);
+        const float e = __fmaf_rn(-q, scale, v), half = 0.5f * scale;
+        const bool move = fabsf(e) > half || (fabsf(e) == half && (__float_as_uint(m) & 1u));
+        return (__float_as_uint(m) + (move ? (e > 0.f ? 1u : 0xffffffffu) : 0u)) & 0xffu;
+    }
 }
 
-// Keeps VEC values at column c of a row whose group's other values lie in the neighbouring lanes; every lane of the warp
-// comes here, those past the width with zeros and in == false.
+// Keeps VEC values of a group whose others lie in the neighbouring lanes, at these places; `first`: the group's first
+// lane. Every lane of the warp comes here, those past the width with zeros and in == false.
 template <typename T, int VEC>
-__device__ __forceinline__ void keep(const KeptOut &k, long long row, int c, int width, bool in, const T (&v)[VEC])
+__device__ __forceinline__ void keep(const KeptOut &at, bool first, bool in, const T (&v)[VEC])
 {
     constexpr int kLanes = kGroup / VEC;
     uint32_t most = 0;
@@ -60,13 +77,13 @@ __device__ __forceinline__ void keep(const KeptOut &k, long long row, int c, int
     for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
     const float scale = kept_scale(most);
     const bool fine = most < 0x7f800000u;
-    const float inv = __fdiv_rn(1.f, scale);
+    const float inv = kept_inverse(scale);
     alignas(8) uint8_t b[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) b[i] = fine ? (uint8_t)kept_code<T>(to_f<T>(v[i]), scale, inv) : (uint8_t)0;
     if (!in) return;
-    *reinterpret_cast<typename Bytes<VEC>::type *>(k.codes + row * width + c) = *reinterpret_cast<typename Bytes<VEC>::type *>(b);
-    if (c % kGroup == 0) k.scale[row * ((width + kGroup - 1) / kGroup) + c / kGroup] = __float2bfloat16_rn(scale);
+    *reinterpret_cast<typename Bytes<VEC>::type *>(at.codes) = *reinterpret_cast<typename Bytes<VEC>::type *>(b);
+    if (first) *at.scale = __float2bfloat16_rn(scale);
 }
 // VEC kept values, in float32
 template <int VEC>

@@ -18,57 +18,70 @@ namespace pmha {
 namespace {
 
 // ---------------------------------------------------------------- quantisation
-// A lane takes VEC values of a block, 32 / VEC lanes a block. Blocks past the row's last up to a multiple of four, and
-// rows past the last up to a multiple of 128, get zero scales. Bound by memory.
+// A block of threads takes a scale tile, 128 rows by 128 columns: a lane VEC values, 32 / VEC lanes a block of 32. Some
+// rows' values are loaded before the first of them is used; the scales are gathered in shared memory and written as one
+// piece, zeros for blocks and rows that are not there. Bound by memory.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long rows, int width, uint8_t *codes,
+__global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long rows, int width, int tiles, uint8_t *codes,
                                                           uint8_t *scale)
 {
-    constexpr int kLanes = 32 / VEC;
+    constexpr int kLanes = 32 / VEC, kRow = 4 * kLanes, kRows = kThreads / kRow;  // lanes of a row, rows of a pass
+    constexpr int kAhead = 128 / kRows < 8 ? 128 / kRows : 8;
+    __shared__ __align__(16) uint8_t bytes[512];
     tcu::grid_dependents_may_start();
-    const int blocks = (width + 31) / 32, padded = (blocks + 3) & ~3;
-    const long long n = ((rows + 127) & ~127ll) * padded, step = (long long)gridDim.x * kThreads / kLanes;
-    const int l = threadIdx.x % kLanes;
-    const long long lead = ((long long)blockIdx.x * kThreads + threadIdx.x / 32 * 32) / kLanes;
-    for (long long g0 = lead; g0 < n; g0 += step) {  // whole warps walk
-        const long long g = g0 + (threadIdx.x % 32) / kLanes;
-        const long long row = g / padded;
-        const int k = (int)(g - row * padded), c = k * 32 + l * VEC;
-        const bool block = g < n && row < rows && k < blocks, in = block && c < width;
-        Vals<T, VEC> v;
+    const long long row0 = (long long)(blockIdx.x / (unsigned)tiles) * 128;
+    const int tile = (int)(blockIdx.x % (unsigned)tiles), l = threadIdx.x % kLanes, k = threadIdx.x % kRow / kLanes;
+    const int blocks = (width + 31) / 32, c = tile * 128 + k * 32 + l * VEC;
+    const bool block = tile * 4 + k < blocks;
+    for (int i = threadIdx.x; i < 128; i += kThreads) ((uint32_t *)bytes)[i] = 0;
+    __syncthreads();
+    const int r_end = (int)min(128ll, rows - row0);
+    for (int r0 = threadIdx.x / 32 * 32 / kRow; r0 < r_end; r0 += kAhead * kRows) {  // whole warps walk
+        Vals<T, VEC> v[kAhead];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(0.f);
-        if (in) load<T, VEC>(x + row * width + c, v.v);
-        uint32_t most = 0;
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = (int)threadIdx.x / kRow + (r0 - (int)(threadIdx.x / 32 * 32 / kRow)) + i * kRows;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) most = max(most, abs_bits(to_f<T>(v.v[i])));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
-        const uint32_t byte = mx_scale_byte(most);
-        const bool fine = byte < 255u;
-        const float inv = fine ? mx_inverse(byte) : 0.f;
-        uint8_t *dst = codes + row * (blocks * 16ll) + k * 16;
-        if constexpr (VEC == 8) {
-            uint32_t w = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w |= mx_byte(to_f<T>(v.v[2 * i]) * inv, to_f<T>(v.v[2 * i + 1]) * inv) << (8 * i);
-            if (block) *reinterpret_cast<uint32_t *>(dst + l * 4) = fine ? w : 0u;
-        } else if constexpr (VEC == 4) {
-            const uint32_t w = mx_byte(to_f<T>(v.v[0]) * inv, to_f<T>(v.v[1]) * inv) |
-                               mx_byte(to_f<T>(v.v[2]) * inv, to_f<T>(v.v[3]) * inv) << 8;
-            if (block) *reinterpret_cast<uint16_t *>(dst + l * 2) = fine ? (uint16_t)w : (uint16_t)0;
-        } else if constexpr (VEC == 2) {
-            const uint32_t w = mx_byte(to_f<T>(v.v[0]) * inv, to_f<T>(v.v[1]) * inv);
-            if (block) dst[l] = fine ? (uint8_t)w : (uint8_t)0;
-        } else {
-            const float f = to_f<T>(v.v[0]) * inv, next = __shfl_down_sync(kFull, f, 1);
-            const uint32_t w = mx_byte(f, next);
-            if (block && l % 2 == 0) dst[l / 2] = fine ? (uint8_t)w : (uint8_t)0;
+            for (int e = 0; e < VEC; ++e) v[i].v[e] = from_f<T>(0.f);
+            if (r < r_end && c < width) load<T, VEC>(x + (row0 + r) * width + c, v[i].v);
         }
-        if (l == 0 && g < n)
-            scale[((row >> 7) * (padded / 4) + (k >> 2)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (k & 3)] =
-                block ? (uint8_t)byte : (uint8_t)0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = (int)threadIdx.x / kRow + (r0 - (int)(threadIdx.x / 32 * 32 / kRow)) + i * kRows;
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) most = max(most, abs_bits(to_f<T>(v[i].v[e])));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+            const uint32_t byte = mx_scale_byte(most);
+            const bool fine = byte < 255u, in = block && r < r_end;
+            const float inv = fine ? mx_inverse(byte) : 0.f;
+            uint8_t *dst = codes + ((row0 + r) * blocks + tile * 4 + k) * 16;
+            if constexpr (VEC == 8) {
+                uint32_t w = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w |= mx_byte(to_f<T>(v[i].v[2 * e]) * inv, to_f<T>(v[i].v[2 * e + 1]) * inv) << (8 * e);
+                if (in) *reinterpret_cast<uint32_t *>(dst + l * 4) = fine ? w : 0u;
+            } else if constexpr (VEC == 4) {
+                const uint32_t w = mx_byte(to_f<T>(v[i].v[0]) * inv, to_f<T>(v[i].v[1]) * inv) |
+                                   mx_byte(to_f<T>(v[i].v[2]) * inv, to_f<T>(v[i].v[3]) * inv) << 8;
+                if (in) *reinterpret_cast<uint16_t *>(dst + l * 2) = fine ? (uint16_t)w : (uint16_t)0;
+            } else if constexpr (VEC == 2) {
+                const uint32_t w = mx_byte(to_f<T>(v[i].v[0]) * inv, to_f<T>(v[i].v[1]) * inv);
+                if (in) dst[l] = fine ? (uint8_t)w : (uint8_t)0;
+            } else {
+                const float f = to_f<T>(v[i].v[0]) * inv, next = __shfl_down_sync(kFull, f, 1);
+                const uint32_t w = mx_byte(f, next);
+                if (in && l % 2 == 0) dst[l / 2] = fine ? (uint8_t)w : (uint8_t)0;
+            }
+            if (l == 0 && in) bytes[(r & 31) * 16 + (r >> 5) * 4 + k] = (uint8_t)byte;
+        }
     }
+    __syncthreads();
+    if (threadIdx.x < 32)
+        *reinterpret_cast<uint4 *>(scale + (size_t)blockIdx.x * 512 + threadIdx.x * 16) =
+            *reinterpret_cast<const uint4 *>(bytes + threadIdx.x * 16);
 }
 
 // ---------------------------------------------------------------- a few tokens
@@ -338,10 +351,9 @@ pmha_status pmha_mx_quantize(pmha_dtype dtype, int64_t rows, int64_t width, cons
         StageTimer timer("mx_quantize", cs);
         dispatch_wide(dtype, shape_of(dtype, width).vec, [&](auto t) {
             using G = decltype(t);
-            const int64_t lanes = ((rows + 127) & ~(int64_t)127) * ((mx_blocks(width) + 3) & ~(int64_t)3) * (32 / G::vec);
-            const unsigned grid = (unsigned)std::min<int64_t>((lanes + kThreads - 1) / kThreads, (int64_t)num_sms() * 8);
-            k_mx_quantize<typename G::type, G::vec><<<grid, kThreads, 0, cs>>>(
-                (const typename G::type *)x, rows, (int)width, (uint8_t *)out->codes, (uint8_t *)out->scale);
+            const int64_t tiles = (mx_blocks(width) + 3) / 4;
+            k_mx_quantize<typename G::type, G::vec><<<(unsigned)((rows + 127) / 128 * tiles), kThreads, 0, cs>>>(
+                (const typename G::type *)x, rows, (int)width, (int)tiles, (uint8_t *)out->codes, (uint8_t *)out->scale);
         });
     }
     count_launch();

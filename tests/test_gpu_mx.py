@@ -56,6 +56,15 @@ def test_borders_ties_and_extremes(dtype):
     assert torch.equal(q.values(), ref.values(x)) and torch.equal(q.codes, codes)
 
 
+def test_values_of_a_matrix_by_hand():
+    codes = torch.zeros(1, 16, dtype=torch.uint8, device=DEV)
+    codes[0, :4] = torch.tensor([0x21, 0x43, 0x65, 0x8F], dtype=torch.uint8)
+    scale = torch.zeros(1, 1, 512, dtype=torch.uint8, device=DEV)
+    scale[0, 0, 0] = 128
+    v = pmha.MxTensor(codes, scale, (1, 8)).values()
+    assert v.tolist() == [[1.0, 2.0, 3.0, 4.0, 6.0, 8.0, -12.0, 0.0]]
+
+
 def test_blocks_that_are_not_finite():
     x = normal(5, 130, 96)
     x[3, 40], x[129, 0], x[64, 95] = float("nan"), float("inf"), float("-inf")
@@ -255,9 +264,11 @@ def test_refusals():
     with pytest.raises(TypeError, match="MxTensor"):
         pmha.pmha_mx_linear(x, w)
     with pytest.raises(ValueError, match="codes"):
-        pmha.pmha_mx_linear(pmha.MxTensor(q.codes, q.scale, (5, 64)), w)
+        pmha.MxTensor(q.codes, q.scale, (5, 64))
     with pytest.raises(ValueError, match="scale"):
-        pmha.pmha_mx_linear(pmha.MxTensor(q.codes, q.scale[:, :, :256], (4, 64)), w)
+        pmha.MxTensor(q.codes, q.scale[:, :, :256], (4, 64))
+    with pytest.raises(AttributeError):
+        q.codes = w.codes
     with pytest.raises(ValueError, match="bias"):
         pmha.pmha_mx_linear(q, w, bias=normal(3, 32, dtype=torch.float32))
     with pytest.raises(ValueError, match="beside"):
