@@ -29,6 +29,11 @@ struct JoinArgs {
     float alpha, eps;
 };
 
+// A block takes a few steps of rows, so that blocks are dealt out as others leave, where memory bounds the call: 320,000 x
+// 128 took 50 us with 4 steps, 51 with 16, and 57 with all rows dealt to resident blocks beforehand (SMs do not get at
+// memory alike). One step where there are fewer blocks otherwise than are resident. Calls with kept tensors are bound by
+// instructions, and a block's start costs some: 62 us with rows dealt out beforehand, 74 with 8 steps.
+constexpr int kFewSteps = 4;
 constexpr int kResident = 3;  // blocks of an SM
 // Rows of 16-byte pieces come through a ring of kRing steps, each thread copying and reading its own pieces (no
 // barrier): what is in flight does not take registers. Others are loaded a step ahead.
@@ -39,175 +44,209 @@ template <typename T, int VEC, int NV>
 constexpr size_t kRingBytes = (size_t)kRingOf<T, VEC, NV> * NV * kSlotBytes;
 
 // Teams of LPR threads (join.cuh) walk rows; thread l of a team holds pieces l, l + LPR, ... of VEC values, NV of them,
-// of a row, and of the weights.
-template <typename T, int VEC, int NV, int LPR, bool KEPT>
-__global__ void __launch_bounds__(kThreads, 3) k_join(JoinArgs a)
+// of a row, and of the weights. Instructions count here: with 275 of them for 8 values a lane the 20,000-node graph took
+// 57 us and the warps were issuing in three cycles of four, so addresses are one running offset, and copies are skipped
+// rather than zero-filled: lanes past the width find zeros in their places, which nothing overwrites, and teams past the
+// last row find what was there before, and store nothing.
+template <typename T, int VEC, int NV, int LPR, bool KEPT, int kSteps>
+__global__ void __launch_bounds__(kThreads, kResident) k_join(JoinArgs a)
 {
     extern __shared__ __align__(16) uint8_t ring_s[];
     __shared__ TeamSums sh;
-    constexpr int kRows = kThreads / LPR;  // rows of a block's step
+    using Codes = typename Bytes<VEC>::type;
+    using V = Vals<T, VEC>;
+    constexpr int kRows = kThreads / LPR, N = NV * VEC;  // rows of a block's step, values of a thread
     constexpr int kRing = kRingOf<T, VEC, NV>;
+    constexpr int kPiece = LPR * VEC;                    // from one piece of a thread to the next
     int turn = 0;
     const int l = threadIdx.x % LPR;
-    const long long step = (long long)gridDim.x * kRows;
-    const int groups = (a.width + kGroup - 1) / kGroup;
-    Vals<T, VEC> wpost[NV], wpre[NV], wgate[NV];  // the gate of the next row, if rows have different ones
+    // a few steps of consecutive rows, or rows from all over
+    const unsigned step = KEPT ? gridDim.x * kRows : kRows;
+    const unsigned begin = blockIdx.x * (KEPT ? kRows : kRows * kSteps);
+    const unsigned rows = KEPT ? (unsigned)a.rows : min((unsigned)a.rows, begin + kRows * kSteps);
+    const long long stride = (long long)step * a.width;
+    const float inv_width = 1.f / (float)a.width;
+    // a warp's threads walk together: row0 is the first of its rows
+    constexpr int kPerWarp = LPR < 32 ? 32 / LPR : 1;
+    const unsigned sub = LPR < 32 ? (threadIdx.x & 31) / LPR : 0;
+    const unsigned row_first = begin + threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
+    bool col[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) col[j] = l * VEC + j * kPiece < a.width;
+    V wpost[NV], wpre[NV], wgate[NV];  // the gate of the next row, if rows have different ones
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * LPR + l) * VEC;
+        const int c = l * VEC + j * kPiece;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) wpost[j].v[i] = wpre[j].v[i] = wgate[j].v[i] = from_f<T>(1.f);
-        if (c < a.width) {
+        if (col[j]) {
             if (a.post) load<T, VEC>((const T *)a.post + c, wpost[j].v);
             if (a.out) load<T, VEC>((const T *)a.pre + c, wpre[j].v);
         }
     }
-    float sb[NV] = {}, sx[NV] = {};  // scales of kept values, of the next row
     const bool own_gate = a.gate && a.per_gate < a.rows;
-    auto fetch_gate = [&](long long row) {
-        const long long at = own_gate ? (long long)((unsigned)row / (unsigned)a.per_gate) * a.width : 0;
+    auto fetch_gate = [&](unsigned row) {
+        if (row >= rows) return;
+        const long long at = own_gate ? (long long)(row / (unsigned)a.per_gate) * a.width : 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (col[j]) load<T, VEC>((const T *)a.gate + at + l * VEC + j * kPiece, wgate[j].v);
+    };
+    float wz[N];  // post times gate of the row at hand: exact in bf16
+    auto times_gate = [&]() {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + l) * VEC;
-            if (row < a.rows && c < a.width) load<T, VEC>((const T *)a.gate + at + c, wgate[j].v);
-        }
-    };
-    auto fetch_scales = [&](long long row) {
+            float g[VEC];
+            widen<T, VEC>(wpost[j], wz + j * VEC);
+            widen<T, VEC>(wgate[j], g);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + l) * VEC;
-            if (!(row < a.rows && c < a.width)) continue;
-            if (a.branch.k.codes) sb[j] = __bfloat162float(a.branch.k.scale[row * groups + c / kGroup]);
-            if (a.res.k.codes) sx[j] = __bfloat162float(a.res.k.scale[row * groups + c / kGroup]);
+            for (int i = 0; i < VEC; ++i) wz[j * VEC + i] *= g[i];
         }
     };
+    // kept values' scales, of the next row
+    const int groups = (a.width + kGroup - 1) / kGroup;
+    float sb[NV] = {}, sx[NV] = {};
+    auto fetch_scales = [&](unsigned row, long long at) {
+        if constexpr (KEPT) {
+            if (row >= rows) return;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (!col[j]) continue;
+                const long long s = at + j * (kPiece / kGroup);
+                if (a.branch.k.codes) sb[j] = __bfloat162float(a.branch.k.scale[s]);
+                if (a.res.k.codes) sx[j] = __bfloat162float(a.res.k.scale[s]);
+            }
+        }
+    };
+    // the row's offset, and its scales'; those of the row to fetch lie ahead by a fixed distance
+    long long at = (long long)(row_first + sub) * a.width + l * VEC;
+    long long sat = (long long)(row_first + sub) * groups + l * VEC / kGroup;
+    V nb[kRing ? 1 : NV] = {}, nx[kRing ? 1 : NV] = {};  // the next row's, without a ring
+    Codes cb[kRing ? 1 : NV] = {}, cx[kRing ? 1 : NV] = {};
     uint8_t *ring = ring_s + threadIdx.x * 16;
-    using Codes = typename Bytes<VEC>::type;
-    union Piece {
-        Vals<T, VEC> v;
-        Codes codes;
-        uint32_t zero[(sizeof(Vals<T, VEC>) + 3) / 4];
-        __device__ __forceinline__ Piece() : zero{} {}
-    };
-    Piece nb[kRing ? 1 : NV], nx[kRing ? 1 : NV];  // the next row's, without a ring
-    auto fetch = [&](long long row, int slot) {
-        if constexpr (kRing > 0) {
-            const long long base = row * a.width;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    auto fetch = [&](unsigned row, long long from, int slot) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * LPR + l) * VEC;
-                const bool in = row < a.rows && c < a.width;
-                const long long at = in ? base + c : 0;
-                uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
-                if (a.branch.p) copy16(p, (const T *)a.branch.p + at, in);
-                else if (KEPT && a.branch.k.codes) copy_codes<VEC>(p, a.branch.k.codes + at, in);
-                if (!KEPT || a.res.p) copy16(p + 16 * kThreads, (const T *)a.res.p + at, in);
-                else copy_codes<VEC>(p + 16 * kThreads, a.res.k.codes + at, in);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        } else {
-            const long long base = row * a.width;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * LPR + l) * VEC;
-                nb[j] = nx[j] = Piece{};
-                if (!(row < a.rows && c < a.width)) continue;
-                if (a.branch.p) load<T, VEC>((const T *)a.branch.p + base + c, nb[j].v.v);
-                else if (KEPT && a.branch.k.codes) nb[j].codes = *reinterpret_cast<const Codes *>(a.branch.k.codes + base + c);
-                if (!KEPT || a.res.p) load<T, VEC>((const T *)a.res.p + base + c, nx[j].v.v);
-                else nx[j].codes = *reinterpret_cast<const Codes *>(a.res.k.codes + base + c);
+        for (int j = 0; j < NV; ++j) {
+            if (row >= rows || !col[j]) continue;
+            const long long e = from + j * kPiece;
+            if constexpr (kRing > 0) {
+                const uint32_t dst = ring_at + (slot * NV + j) * kSlotBytes;
+                if (a.branch.p) ring_copy(dst, (const T *)a.branch.p + e);
+                else if (KEPT && a.branch.k.codes) ring_codes<VEC>(dst, a.branch.k.codes + e);
+                if (!KEPT || a.res.p) ring_copy(dst + 16 * kThreads, (const T *)a.res.p + e);
+                else ring_codes<VEC>(dst + 16 * kThreads, a.res.k.codes + e);
+            } else {
+                if (a.branch.p) load<T, VEC>((const T *)a.branch.p + e, nb[j].v);
+                else if (KEPT && a.branch.k.codes) cb[j] = *reinterpret_cast<const Codes *>(a.branch.k.codes + e);
+                if (!KEPT || a.res.p) load<T, VEC>((const T *)a.res.p + e, nx[j].v);
+                else cx[j] = *reinterpret_cast<const Codes *>(a.res.k.codes + e);
             }
         }
+        if constexpr (kRing > 0) asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // VEC values of a source, which lie at `p` in one form or the other; zeros where there is none
-    auto values = [&](const Source &s, const void *p, float scale, float *f) {
-        float (&v)[VEC] = *reinterpret_cast<float (*)[VEC]>(f);
-        if (s.p) load_row<T, VEC>(p, 0, v);
-        else if (KEPT && s.k.codes) unkeep<VEC>(*reinterpret_cast<const Codes *>(p), scale, v);
-    };
-    // a warp's threads walk together: row0 is the first of its rows
-    constexpr int kPerWarp = LPR < 32 ? 32 / LPR : 1;
-    const int sub = LPR < 32 ? (int)(threadIdx.x & 31) / LPR : 0;
-    const long long row_first = (long long)blockIdx.x * kRows + (int)threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
-    if constexpr (kRing > 0)
-        for (int i = 0; i < kRing - 1; ++i) fetch(row_first + i * step + sub, i);
-    else fetch(row_first + sub, 0);
+    if constexpr (kRing > 0) {
+#pragma unroll
+        for (int i = 0; i < kRing * NV; ++i)
+            if (!col[i % NV] || row_first + sub >= rows)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    *reinterpret_cast<uint4 *>(ring + i * kSlotBytes + k * 16 * kThreads) = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kRing - 1; ++i) fetch(row_first + sub + i * step, at + i * stride, i);
+    } else {
+        fetch(row_first + sub, at, 0);
+    }
     if (a.gate) fetch_gate(row_first + sub);
-    if constexpr (KEPT) fetch_scales(row_first + sub);
+    times_gate();
+    if (own_gate) fetch_gate(row_first + sub + step);
+    fetch_scales(row_first + sub, sat);
     int slot = 0;
-    for (long long row0 = row_first; row0 < a.rows; row0 += step) {
-        const long long row = row0 + sub, base = row * a.width;
-        const bool live = row < a.rows;
+    for (unsigned row0 = row_first; row0 < rows; row0 += step, at += stride, sat += (long long)step * groups) {
+        const unsigned row = row0 + sub;
+        const bool live = row < rows;
         if constexpr (kRing > 0) {
-            fetch(row + (kRing - 1) * step, slot ? slot - 1 : kRing - 1);
+            fetch(row + (kRing - 1) * step, at + (kRing - 1) * stride, slot ? slot - 1 : kRing - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
         }
-        float b[NV * VEC], x[NV * VEC];
+        float b[N], x[N];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + l) * VEC;
+            const uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
+            auto piece = [&](const V *next, int k) {
+                if constexpr (kRing > 0) return *reinterpret_cast<const V *>(p + k * 16 * kThreads);
+                else return next[j];
+            };
+            auto codes = [&](const Codes *next, int k) {
+                if constexpr (kRing > 0) return *reinterpret_cast<const Codes *>(p + k * 16 * kThreads);
+                else return next[j];
+            };
+            float (&bj)[VEC] = *reinterpret_cast<float (*)[VEC]>(b + j * VEC);
+            float (&xj)[VEC] = *reinterpret_cast<float (*)[VEC]>(x + j * VEC);
+            if (a.branch.p) {
+                const V v = piece(nb, 0);
+                widen<T, VEC>(v, bj);
+                if constexpr (KEPT)
+                    if (a.keep_branch.codes) {
+                        const long long e = at + j * kPiece;
+                        keep<T, VEC>(KeptOut{a.keep_branch.codes + e, a.keep_branch.scale + sat + j * (kPiece / kGroup)},
+                                     l * VEC % kGroup == 0, live && col[j], v);
+                    }
+            } else if (KEPT && a.branch.k.codes) {
+                unkeep<VEC>(codes(cb, 0), sb[j], bj);
+            } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) b[j * VEC + i] = x[j * VEC + i] = 0.f;
-            if constexpr (kRing > 0) {
-                const uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
-                values(a.branch, p, sb[j], b + j * VEC);
-                values(a.res, p + 16 * kThreads, sx[j], x + j * VEC);
-            } else if (live && c < a.width) {
-                values(a.branch, &nb[j], sb[j], b + j * VEC);
-                values(a.res, &nx[j], sx[j], x + j * VEC);
+                for (int i = 0; i < VEC; ++i) bj[i] = 0.f;
+            }
+            if (!KEPT || a.res.p) {
+                const V v = piece(nx, 1);
+                widen<T, VEC>(v, xj);
+                if constexpr (KEPT)
+                    if (a.keep_res.codes) {
+                        const long long e = at + j * kPiece;
+                        keep<T, VEC>(KeptOut{a.keep_res.codes + e, a.keep_res.scale + sat + j * (kPiece / kGroup)},
+                                     l * VEC % kGroup == 0, live && col[j], v);
+                    }
+            } else {
+                unkeep<VEC>(codes(cx, 1), sx[j], xj);
             }
         }
         if constexpr (kRing > 0) slot = slot + 1 == kRing ? 0 : slot + 1;
-        else fetch(row + step, 0);
-        if constexpr (KEPT) {
-            fetch_scales(row + step);
-            auto keep_row = [&](const KeptOut &k, float *f) {
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int c = (j * LPR + l) * VEC;
-                    T v[VEC];
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) v[i] = from_f<T>(f[j * VEC + i]);  // exact: values of the type
-                    keep<T, VEC>(KeptOut{k.codes + base + c, k.scale + row * groups + c / kGroup}, c % kGroup == 0, live && c < a.width, v);
-                }
-            };
-            if (a.keep_branch.codes) keep_row(a.keep_branch, b);
-            if (a.keep_res.codes) keep_row(a.keep_res, x);
-        }
-        // sum: of the weights' product first, exact in bf16, so that branch, weights and root meet in one more product and
-        // the addition: sums rounded to bf16 seldom fall to the other side of what exact arithmetic gives
+        else fetch(row + step, at + stride, 0);
+        fetch_scales(row + step, sat + (long long)step * groups);
+        // sum: of the weights' product first, so that branch, weights and root meet in one more product and the addition:
+        // sums rounded to bf16 seldom fall to the other side of what exact arithmetic gives
         float rb = 1.f;
         if (a.post) {
             float sc;
-            rb = row_root<NV * VEC, LPR>(b, a.width, a.eps, &sc, sh, turn);  // of b sc, which is what b holds now
+            rb = row_root<N, LPR>(b, inv_width, a.eps, &sc, sh, turn);  // of b sc, which is what b holds now
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + l) * VEC;
-            Vals<T, VEC> s;
+            float (&xj)[VEC] = *reinterpret_cast<float (*)[VEC]>(x + j * VEC);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float z = b[j * VEC + i] * (to_f<T>(wpost[j].v[i]) * to_f<T>(wgate[j].v[i]));
-                s.v[i] = from_f<T>(fmaf(z, rb, a.alpha * x[j * VEC + i]));
-                x[j * VEC + i] = to_f<T>(s.v[i]);
-            }
-            if (live && c < a.width) store<T, VEC>((T *)a.sum + base + c, s.v);
+            for (int i = 0; i < VEC; ++i) xj[i] = fmaf(b[j * VEC + i] * wz[j * VEC + i], rb, a.alpha * xj[i]);
+            const V s = rounded<T, VEC>(xj);
+            if (live && col[j]) store<T, VEC>((T *)a.sum + at + j * kPiece, s.v);
         }
-        if (own_gate) fetch_gate(row + step);
+        if (own_gate) {
+            times_gate();
+            fetch_gate(row + 2 * step);
+        }
         if (!a.out) continue;
         float sc;
-        const float r = row_root<NV * VEC, LPR>(x, a.width, a.eps, &sc, sh, turn);
+        const float r = row_root<N, LPR>(x, inv_width, a.eps, &sc, sh, turn);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + l) * VEC;
-            if (!(live && c < a.width)) continue;
-            Vals<T, VEC> y;
+            float (&xj)[VEC] = *reinterpret_cast<float (*)[VEC]>(x + j * VEC);
+            float w[VEC];
+            widen<T, VEC>(wpre[j], w);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) y.v[i] = from_f<T>(x[j * VEC + i] * r * to_f<T>(wpre[j].v[i]));
-            store<T, VEC>((T *)a.out + base + c, y.v);
+            for (int i = 0; i < VEC; ++i) xj[i] *= r * w[i];
+            const V y = rounded<T, VEC>(xj);
+            if (live && col[j]) store<T, VEC>((T *)a.out + at + j * kPiece, y.v);
         }
     }
-    // the last steps' copies (zeros past the rows) land before the block's shared memory can go to another
+    // the last copies land before the block's shared memory can go to another
     if constexpr (kRing > 0) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
@@ -228,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) k_join_wide(JoinArgs a)
             for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(0.f);
             if (c < a.width) load<T, VEC>((const T *)p + base + c, v.v);
             keep<T, VEC>(KeptOut{k.codes + base + c, k.scale + row * groups_of(a.width) + c / kGroup}, c % kGroup == 0,
-                         c < a.width, v.v);
+                         c < a.width, v);
         }
     };
     if (a.keep_branch.codes) keep_row(a.keep_branch, a.branch.p);
@@ -346,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) k_keep(const T *x, long long n, unsi
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            keep<T, VEC>(KeptOut{k.codes + p[i].at, k.scale + p[i].group}, threadIdx.x % (kGroup / VEC) == 0, p[i].in, v[i].v);
+            keep<T, VEC>(KeptOut{k.codes + p[i].at, k.scale + p[i].group}, threadIdx.x % (kGroup / VEC) == 0, p[i].in, v[i]);
     }
 }
 template <typename T, int VEC>
@@ -425,13 +464,16 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
         StageTimer timer(kept ? "join_kept" : "join", cs);
         if (s.lpr) {
             const int64_t per = kThreads / s.lpr;
-            const unsigned grid = (unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)num_sms() * kResident);
+            const int64_t steps = (rows + per - 1) / per, all = (int64_t)num_sms() * kResident;
+            const bool few = steps < all * kFewSteps;
             join_dispatch(p.dtype, s, [&](auto t) {
                 using G = decltype(t);
-                constexpr size_t smem = kRingBytes<typename G::type, G::vec, G::nv>;
+                using T = typename G::type;
+                constexpr size_t smem = kRingBytes<T, G::vec, G::nv>;
                 static_assert(smem <= 48 * 1024, "what a launch may have without asking");
-                if (kept) k_join<typename G::type, G::vec, G::nv, G::lpr, true><<<grid, kThreads, smem, cs>>>(a);
-                else k_join<typename G::type, G::vec, G::nv, G::lpr, false><<<grid, kThreads, smem, cs>>>(a);
+                if (kept) k_join<T, G::vec, G::nv, G::lpr, true, 1><<<(unsigned)std::min(steps, all), kThreads, smem, cs>>>(a);
+                else if (few) k_join<T, G::vec, G::nv, G::lpr, false, 1><<<(unsigned)steps, kThreads, smem, cs>>>(a);
+                else k_join<T, G::vec, G::nv, G::lpr, false, kFewSteps><<<(unsigned)((steps + kFewSteps - 1) / kFewSteps), kThreads, smem, cs>>>(a);
             });
         } else {
             dispatch_wide(p.dtype, s.vec, [&](auto t) {

@@ -37,27 +37,53 @@ __device__ __forceinline__ void load_row(const void *p, long long at, float (&v)
     for (int i = 0; i < VEC; ++i) v[i] = to_f<T>(t.v[i]);
 }
 
-// 8 bytes from global to shared memory, or zeros
-__device__ __forceinline__ void copy8(void *dst, const void *src, bool in)
+// VEC values rounded to the type, two to an instruction in bf16; v holds them as rounded afterwards
+template <typename T, int VEC>
+__device__ __forceinline__ Vals<T, VEC> rounded(float (&v)[VEC])
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(in ? 8 : 0)
-                 : "memory");
+    Vals<T, VEC> r;
+    if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(r.v);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[i], v[i + 1]);
+            w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+            v[i] = __uint_as_float(w[i / 2] << 16);
+            v[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            r.v[i] = from_f<T>(v[i]);
+            v[i] = to_f<T>(r.v[i]);
+        }
+    }
+    return r;
 }
-__device__ __forceinline__ void copy4(void *dst, const void *src, bool in)
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(const Vals<T, VEC> &r, float *v)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(in ? 4 : 0)
-                 : "memory");
+    if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(r.v);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            v[i] = __uint_as_float(w[i / 2] << 16);
+            v[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = to_f<T>(r.v[i]);
+    }
 }
-
-// VEC codes
+// 16 bytes of values, or their codes, into the ring
+__device__ __forceinline__ void ring_copy(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int VEC>
-__device__ __forceinline__ void copy_codes(void *dst, const int8_t *src, bool in)
+__device__ __forceinline__ void ring_codes(uint32_t dst, const int8_t *src)
 {
-    static_assert(VEC == 8 || VEC == 4, "of a piece of 16 bytes");
-    if constexpr (VEC == 8) copy8(dst, src, in);
-    else copy4(dst, src, in);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(VEC == 8 ? 8 : 4) : "memory");
 }
 
 // A row is shared by LPR threads ("a team"), lanes of one warp or whole warps of
@@ -121,7 +147,7 @@ __device__ __forceinline__ float scale_row(float (&f)[N], bool over, TeamSums &s
 }
 // The row's 1 / rms; a row whose squares leave float32 is scaled in place by *sc first.
 template <int N, int LPR>
-__device__ __forceinline__ float row_root(float (&f)[N], int width, float eps, float *sc, TeamSums &sh, int &turn)
+__device__ __forceinline__ float row_root(float (&f)[N], float inv_width, float eps, float *sc, TeamSums &sh, int &turn)
 {
     float ss[1] = {squares_of(f)};
     team_reduce<LPR, false>(ss, sh, turn);
@@ -131,7 +157,7 @@ __device__ __forceinline__ float row_root(float (&f)[N], int width, float eps, f
         ss[0] = squares_of(f);
         team_reduce<LPR, false>(ss, sh, turn);
     }
-    return rsqrtf(ss[0] / (float)width + eps * *sc * *sc);
+    return rsqrtf(fmaf(ss[0], inv_width, eps * *sc * *sc));
 }
 
 // The kernel shape of a width up to 2048: values a piece, pieces a thread, threads a row; 0 threads: one block walks the

@@ -1,5 +1,6 @@
 // Backward pass of the join (join.cu has the formulas).
 #include "join.cuh"
+#include "tc_pair.cuh"
 
 namespace pmha {
 namespace {
@@ -21,8 +22,7 @@ struct JoinBwdArgs {
 // float32 one after the other; the blocks' partial rows are added as pairs of floats.
 constexpr int kSteps = 128;
 
-// Rows of 16-byte pieces come through a ring of kRing steps, each thread copying and reading its own pieces (no
-// barrier): what is in flight does not take registers. Others are loaded when they are needed.
+// Rows of 16-byte pieces come through a ring as in the forward pass; others are loaded when they are needed.
 template <typename T, int VEC, int NV>
 constexpr int kRingOf = VEC * sizeof(T) == 16 ? 4 / NV : 0;
 constexpr int kSlotBytes = 4 * 16 * kThreads;  // dout, sum, dsum and branch of one piece
@@ -30,122 +30,145 @@ template <typename T, int VEC, int NV>
 constexpr size_t kRingBytes = (size_t)kRingOf<T, VEC, NV> * NV * kSlotBytes;
 
 // A team (join.cuh) walks rows of one gate and keeps its columns' two sums over rows in
-// registers; a block adds its teams' through shared memory and writes one partial row of each.
+// registers; a block adds its teams' through shared memory and writes one partial row of each. As in the forward pass,
+// addresses are one running offset and copies are skipped where there is nothing to copy.
 template <typename T, int VEC, int NV, int LPR, bool KEPT>
 __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
 {
     extern __shared__ __align__(16) float shw[];  // the ring, then width values
     __shared__ TeamSums sh;
-    constexpr int kRows = kThreads / LPR, N = NV * VEC;  // rows of a block's step
+    using Codes = typename Bytes<VEC>::type;
+    using V = Vals<T, VEC>;
+    constexpr int kRows = kThreads / LPR, N = NV * VEC;  // rows of a block's step, values of a thread
     constexpr int kPerWarp = LPR < 32 ? 32 / LPR : 1;
     constexpr int kRing = kRingOf<T, VEC, NV>;
+    constexpr int kPiece = LPR * VEC;                    // from one piece of a thread to the next
     const int l = threadIdx.x % LPR;
     int turn = 0;
-    const long long gate = blockIdx.x / a.blocks_per_gate;
-    const long long begin = gate * a.per_gate, end = begin + a.per_gate;
-    const long long step = (long long)a.blocks_per_gate * kRows;
+    tcu::grid_dependents_may_start();  // the few blocks of the sums come up and wait
+    const unsigned gate = blockIdx.x / (unsigned)a.blocks_per_gate;
+    const unsigned end = (gate + 1) * (unsigned)a.per_gate, step = (unsigned)a.blocks_per_gate * kRows;
+    const long long stride = (long long)step * a.width;
     const float inv_width = 1.f / (float)a.width;
     const int groups = (a.width + kGroup - 1) / kGroup;
-    Vals<T, VEC> wpre[NV], wpost[NV], wgate[NV];
-    float q[N], pb[N];
+    bool col[NV];
+    V wpre[NV];
+    float wz[N], q[N], pb[N];  // post times gate; sums of dout sum r and of D branch r_b
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * LPR + l) * VEC;
+        const int c = l * VEC + j * kPiece;
+        col[j] = c < a.width;
+        V post, gt;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            wpre[j].v[i] = wpost[j].v[i] = wgate[j].v[i] = from_f<T>(1.f);
+            wpre[j].v[i] = post.v[i] = gt.v[i] = from_f<T>(1.f);
             q[j * VEC + i] = pb[j * VEC + i] = 0.f;
         }
-        if (c < a.width) {
+        if (col[j]) {
             if (a.pre) load<T, VEC>((const T *)a.pre + c, wpre[j].v);
-            if (a.post) load<T, VEC>((const T *)a.post + c, wpost[j].v);
-            if (a.gate) load<T, VEC>((const T *)a.gate + gate * a.width + c, wgate[j].v);
+            if (a.post) load<T, VEC>((const T *)a.post + c, post.v);
+            if (a.gate) load<T, VEC>((const T *)a.gate + (long long)gate * a.width + c, gt.v);
         }
+        float g[VEC];
+        widen<T, VEC>(post, wz + j * VEC);
+        widen<T, VEC>(gt, g);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) wz[j * VEC + i] *= g[i];
     }
-    uint8_t *ring = (uint8_t *)shw + threadIdx.x * 16;
-    float scale[NV] = {};  // of the kept branch's values, loaded a step ahead
-    auto fetch_scale = [&](long long row) {
-        if constexpr (KEPT) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * LPR + l) * VEC;
-                if (row < end && c < a.width) scale[j] = __bfloat162float(a.branch.k.scale[row * groups + c / kGroup]);
-            }
-        }
-    };
-    auto fetch = [&](long long row, int slot) {
-        if constexpr (kRing > 0) {
-            const long long base = row * a.width;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * LPR + l) * VEC;
-                const bool in = row < end && c < a.width;
-                const long long at = in ? base + c : 0;
-                uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
-                if (a.dy) {
-                    copy16(p, (const T *)a.dy + at, in);
-                    copy16(p + 16 * kThreads, (const T *)a.sum + at, in);
-                }
-                if (a.ds) copy16(p + 32 * kThreads, (const T *)a.ds + at, in);
-                if constexpr (KEPT) {
-                    copy_codes<VEC>(p + 48 * kThreads, a.branch.k.codes + at, in);
-                } else if (a.branch.p) {
-                    copy16(p + 48 * kThreads, (const T *)a.branch.p + at, in);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-    };
     // a warp's threads walk together: row0 is the first of its rows
-    const int sub = LPR < 32 ? (int)(threadIdx.x & 31) / LPR : 0;
-    const long long row_first = begin + (long long)(blockIdx.x % a.blocks_per_gate) * kRows +
-                                (int)threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
-    if constexpr (kRing > 0)
-        for (int i = 0; i < kRing - 1; ++i) fetch(row_first + i * step + sub, i);
-    fetch_scale(row_first + sub);
+    const unsigned sub = LPR < 32 ? (threadIdx.x & 31) / LPR : 0;
+    const unsigned row_first = gate * (unsigned)a.per_gate + blockIdx.x % (unsigned)a.blocks_per_gate * kRows +
+                               threadIdx.x / (LPR < 32 ? 32 : LPR) * kPerWarp;
+    long long at = (long long)(row_first + sub) * a.width + l * VEC;
+    long long sat = (long long)(row_first + sub) * groups + l * VEC / kGroup;
+    uint8_t *ring = (uint8_t *)shw + threadIdx.x * 16;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    float scale[NV] = {};  // of the kept branch's values, loaded a step ahead
+    auto fetch_scale = [&](unsigned row, long long from) {
+        if constexpr (KEPT) {
+            if (row >= end) return;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (col[j]) scale[j] = __bfloat162float(a.branch.k.scale[from + j * (kPiece / kGroup)]);
+        }
+    };
+    auto fetch = [&](unsigned row, long long from, int slot) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (row >= end || !col[j]) continue;
+            const long long e = from + j * kPiece;
+            const uint32_t dst = ring_at + (slot * NV + j) * kSlotBytes;
+            if (a.dy) {
+                ring_copy(dst, (const T *)a.dy + e);
+                ring_copy(dst + 16 * kThreads, (const T *)a.sum + e);
+            }
+            if (a.ds) ring_copy(dst + 32 * kThreads, (const T *)a.ds + e);
+            if constexpr (KEPT && kRing > 0) ring_codes<VEC>(dst + 48 * kThreads, a.branch.k.codes + e);
+            else if (a.branch.p) ring_copy(dst + 48 * kThreads, (const T *)a.branch.p + e);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (kRing > 0) {
+#pragma unroll
+        for (int i = 0; i < kRing * NV; ++i)
+            if (!col[i % NV])
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4 *>(ring + i * kSlotBytes + k * 16 * kThreads) = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kRing - 1; ++i) fetch(row_first + sub + i * step, at + i * stride, i);
+    }
+    fetch_scale(row_first + sub, sat);
     int slot = 0;
-    for (long long row0 = row_first; row0 < end; row0 += step) {
-        const long long row = row0 + sub, base = row * a.width;
+    for (unsigned row0 = row_first; row0 < end; row0 += step, at += stride, sat += (long long)step * groups) {
+        const unsigned row = row0 + sub;
         const bool live = row < end;
-        float D[N], f[N], b[N], da[N];
-        Vals<T, VEC> g[NV];
+        float D[N], f[N], b[N], g[N], da[N];
         if constexpr (kRing > 0) {
-            fetch(row + (kRing - 1) * step, slot ? slot - 1 : kRing - 1);
+            fetch(row + (kRing - 1) * step, at + (kRing - 1) * stride, slot ? slot - 1 : kRing - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        }
+        // without a ring: all loads first
+        V raw[kRing ? 1 : 4][kRing ? 1 : NV] = {};
+        Codes codes[kRing ? 1 : NV] = {};
+        if constexpr (kRing == 0) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const long long e = at + j * kPiece;
+                const bool in = live && col[j];
+                if (in && a.dy) load<T, VEC>((const T *)a.dy + e, raw[0][j].v);
+                if (in && a.dy) load<T, VEC>((const T *)a.sum + e, raw[1][j].v);
+                if (in && a.ds) load<T, VEC>((const T *)a.ds + e, raw[2][j].v);
+                if constexpr (KEPT) {
+                    if (in) codes[j] = *reinterpret_cast<const Codes *>(a.branch.k.codes + e);
+                } else if (in && a.branch.p) {
+                    load<T, VEC>((const T *)a.branch.p + e, raw[3][j].v);
+                }
+            }
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + l) * VEC;
-            float (&Dj)[VEC] = *reinterpret_cast<float (*)[VEC]>(D + j * VEC);
-            float (&fj)[VEC] = *reinterpret_cast<float (*)[VEC]>(f + j * VEC);
+            const uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
             float (&bj)[VEC] = *reinterpret_cast<float (*)[VEC]>(b + j * VEC);
+            if constexpr (kRing == 0) {
+                widen<T, VEC>(raw[0][j], g + j * VEC);
+                widen<T, VEC>(raw[1][j], f + j * VEC);
+                widen<T, VEC>(raw[2][j], D + j * VEC);
+                if constexpr (KEPT) unkeep<VEC>(codes[j], scale[j], bj);
+                else widen<T, VEC>(raw[3][j], bj);
+            } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                Dj[i] = fj[i] = bj[i] = 0.f;
-                g[j].v[i] = from_f<T>(0.f);
-            }
-            if constexpr (kRing > 0) {
-                const uint8_t *p = ring + (slot * NV + j) * kSlotBytes;
+                for (int i = 0; i < VEC; ++i) D[j * VEC + i] = f[j * VEC + i] = g[j * VEC + i] = bj[i] = 0.f;
+                if (!live) continue;  // zeros for the sums; past the width the ring holds them
                 if (a.dy) {
-                    load<T, VEC>((const T *)p, g[j].v);
-                    load_row<T, VEC>(p + 16 * kThreads, 0, fj);
+                    widen<T, VEC>(*(const V *)p, g + j * VEC);
+                    widen<T, VEC>(*(const V *)(p + 16 * kThreads), f + j * VEC);
                 }
-                if (a.ds) load_row<T, VEC>(p + 32 * kThreads, 0, Dj);
-                if constexpr (KEPT)
-                    unkeep<VEC>(*reinterpret_cast<const typename Bytes<VEC>::type *>(p + 48 * kThreads), scale[j], bj);
-                else if (a.branch.p) load_row<T, VEC>(p + 48 * kThreads, 0, bj);
-            } else if (live && c < a.width) {
-                if (a.dy) {
-                    load<T, VEC>((const T *)a.dy + base + c, g[j].v);
-                    load_row<T, VEC>(a.sum, base + c, fj);
-                }
-                if (a.ds) load_row<T, VEC>(a.ds, base + c, Dj);
-                if constexpr (KEPT)
-                    unkeep<VEC>(*reinterpret_cast<const typename Bytes<VEC>::type *>(a.branch.k.codes + base + c), scale[j], bj);
-                else if (a.branch.p) load_row<T, VEC>(a.branch.p, base + c, bj);
+                if (a.ds) widen<T, VEC>(*(const V *)(p + 32 * kThreads), D + j * VEC);
+                if constexpr (KEPT) unkeep<VEC>(*(const Codes *)(p + 48 * kThreads), scale[j], bj);
+                else if (a.branch.p) widen<T, VEC>(*(const V *)(p + 48 * kThreads), bj);
             }
         }
-        fetch_scale(row + step);
+        fetch_scale(row + step, sat + (long long)step * groups);
         if constexpr (kRing > 0) slot = slot + 1 == kRing ? 0 : slot + 1;
         // the squares' sums of sum and branch and the sum of dout pre sum, together
         float sc = 1.f, scb = 1.f;
@@ -159,9 +182,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
             team_reduce<LPR, false>(t, sh, turn);
         };
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            float w[VEC];
+            widen<T, VEC>(wpre[j], w);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) da[j * VEC + i] = to_f<T>(g[j].v[i]) * to_f<T>(wpre[j].v[i]);
+            for (int i = 0; i < VEC; ++i) da[j * VEC + i] = g[j * VEC + i] * w[i];
+        }
         stats();
         const bool over = t[0] > kMostSquares || !(fabsf(t[1]) <= kMostSquares), overb = t[2] > kMostSquares;
         if (__any_sync(kFull, over || overb)) {  // a team of warps comes here together: they have one row
@@ -170,86 +196,72 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
             stats();
         }
         if (a.dy) {
-            const float r = rsqrtf(t[0] * inv_width + a.eps * sc * sc);  // of sum sc
+            const float r = rsqrtf(fmaf(t[0], inv_width, a.eps * sc * sc));  // of sum sc
             const float k = t[1] * inv_width * r * r, rd = r * sc;
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int n = j * VEC + i;
-                    q[n] = fmaf(to_f<T>(g[j].v[i]), f[n] * r, q[n]);
-                    D[n] = fmaf(rd, fmaf(-f[n], k, da[n]), D[n]);
-                }
-        }
-        if (a.dres) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * LPR + l) * VEC;
-                if (!(live && c < a.width)) continue;
-                Vals<T, VEC> o;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o.v[i] = from_f<T>(a.alpha * D[j * VEC + i]);
-                store<T, VEC>((T *)a.dres + base + c, o.v);
+            for (int n = 0; n < N; ++n) {
+                q[n] = fmaf(g[n], f[n] * r, q[n]);
+                D[n] = fmaf(rd, fmaf(-f[n], k, da[n]), D[n]);
             }
         }
         float rb = 1.f;
         if (a.post) {
-            rb = rsqrtf(t[2] * inv_width + a.eps * scb * scb);
+            rb = rsqrtf(fmaf(t[2], inv_width, a.eps * scb * scb));
 #pragma unroll
             for (int i = 0; i < N; ++i) b[i] *= rb;
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) pb[i] = fmaf(D[i], b[i], pb[i]);
-        if (!a.dbranch) continue;
         float bs[1] = {0.f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int n = 0; n < N; ++n) {
+            pb[n] = fmaf(D[n], b[n], pb[n]);
+            da[n] = D[n] * wz[n];
+            bs[0] = fmaf(da[n], b[n], bs[0]);
+            D[n] *= a.alpha;
+        }
+        if (a.dres) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                D[j * VEC + i] *= to_f<T>(wgate[j].v[i]) * to_f<T>(wpost[j].v[i]);
-                bs[0] = fmaf(D[j * VEC + i], b[j * VEC + i], bs[0]);
+            for (int j = 0; j < NV; ++j) {
+                const V o = rounded<T, VEC>(*reinterpret_cast<float (*)[VEC]>(D + j * VEC));
+                if (live && col[j]) store<T, VEC>((T *)a.dres + at + j * kPiece, o.v);
             }
+        }
+        if (!a.dbranch) continue;
         if (a.post) {
             team_reduce<LPR, false>(bs, sh, turn);
             const float k = bs[0] * inv_width, rd = rb * scb;
 #pragma unroll
-            for (int i = 0; i < N; ++i) D[i] = rd * fmaf(-b[i], k, D[i]);
+            for (int i = 0; i < N; ++i) da[i] = rd * fmaf(-b[i], k, da[i]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + l) * VEC;
-            if (!(live && c < a.width)) continue;
-            Vals<T, VEC> o;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o.v[i] = from_f<T>(D[j * VEC + i]);
-            store<T, VEC>((T *)a.dbranch + base + c, o.v);
+            const V o = rounded<T, VEC>(*reinterpret_cast<float (*)[VEC]>(da + j * VEC));
+            if (live && col[j]) store<T, VEC>((T *)a.dbranch + at + j * kPiece, o.v);
         }
     }
-    // the last steps' copies (zeros past the rows) land before the block's shared memory is used for other things
+    // the last copies land before the block's shared memory is used for other things
     if constexpr (kRing > 0) asm volatile("cp.async.wait_all;" ::: "memory");
-    // a warp's rows, then the warps (or teams of warps) one after the other
-    constexpr int kTeam = LPR < 32 ? 32 : LPR;
+    // a warp's rows, then the warps (or teams of warps) in order, all at once through shared memory
+    constexpr int kTeam = LPR < 32 ? 32 : LPR, kTeams = kThreads / kTeam;
     const int team = threadIdx.x / kTeam;
-    __syncthreads();
     auto put = [&](float (&v)[N], float *part) {
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int o = LPR; o < 32; o <<= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
-        for (int t = 0; t < kThreads / kTeam; ++t) {
-            if (team == t && (int)threadIdx.x % kTeam < LPR) {
+        if ((int)threadIdx.x % kTeam < LPR)
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int c = (j * LPR + l) * VEC;
-                    if (c < a.width)
+            for (int j = 0; j < NV; ++j)
+                if (col[j])
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) shw[c + i] = t ? shw[c + i] + v[j * VEC + i] : v[j * VEC + i];
-                }
-            }
-            __syncthreads();
-        }
-        for (int c = threadIdx.x; c < a.width; c += kThreads) part[(long long)blockIdx.x * a.width + c] = shw[c];
+                    for (int i = 0; i < VEC; ++i) shw[team * a.width + l * VEC + j * kPiece + i] = v[j * VEC + i];
         __syncthreads();
+        for (int c = threadIdx.x; c < a.width; c += kThreads) {
+            float t = shw[c];
+#pragma unroll
+            for (int i = 1; i < kTeams; ++i) t += shw[i * a.width + c];
+            part[(long long)blockIdx.x * a.width + c] = t;
+        }
     };
     if (a.part_pre) put(q, a.part_pre);
     if (a.part_branch) put(pb, a.part_branch);
@@ -396,20 +408,21 @@ struct JoinSumArgs {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_join_sums(JoinSumArgs a)
 {
-    __shared__ Two sh[32][8];
+    __shared__ Two sh[kThreads / 32][8];
+    tcu::grid_wait();
     const int c8 = threadIdx.x & 7, c = (int)(blockIdx.x % a.tiles) * 8 + c8, t = threadIdx.x >> 3;
     long long what = blockIdx.x / a.tiles;
     if (!a.dpre) ++what;
     if (!a.dpost && what > 0) ++what;
     const long long gate = what - 2;
     const float *part = what == 0 ? a.part_pre : a.part_branch;
-    const long long n = what < 2 ? a.gates * a.blocks_per_gate : a.blocks_per_gate;
+    const int n = what < 2 ? (int)a.gates * a.blocks_per_gate : a.blocks_per_gate;
     const long long at = what < 2 ? 0 : gate * a.blocks_per_gate;
     const bool weighted = what == 1 && a.gate;
     Two s = {0.f, 0.f};
     if (c < a.width) {
 #pragma unroll 4
-        for (long long i = t; i < n; i += 32) {
+        for (int i = t; i < n; i += 32) {
             const float v = part[(at + i) * a.width + c];
             if (weighted) {
                 const float g = to_f<T>(((const T *)a.gate)[i / a.blocks_per_gate * a.width + c]);
@@ -420,10 +433,14 @@ __global__ void __launch_bounds__(kThreads) k_join_sums(JoinSumArgs a)
             }
         }
     }
-    sh[t][c8] = s;
+    // four of a warp's threads share a column, then the eight warps in order
+    s = add(s, Two{__shfl_xor_sync(kFull, s.hi, 8), __shfl_xor_sync(kFull, s.lo, 8)});
+    s = add(s, Two{__shfl_xor_sync(kFull, s.hi, 16), __shfl_xor_sync(kFull, s.lo, 16)});
+    if ((threadIdx.x & 31) < 8) sh[threadIdx.x >> 5][c8] = s;
     __syncthreads();
     if (t == 0 && c < a.width) {
-        for (int i = 1; i < 32; ++i) s = add(s, sh[i][c8]);
+#pragma unroll
+        for (int i = 1; i < kThreads / 32; ++i) s = add(s, sh[i][c8]);
         const float v = s.hi + s.lo;
         if (what == 0) a.dpre[c] = v;
         else if (what == 1) a.dpost[c] = v;
@@ -535,8 +552,8 @@ pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, con
             join_dispatch(p.dtype, s, [&](auto t) {
                 using G = decltype(t);
                 using T = typename G::type;
-                // the ring, and in its place at the end the block's sums
-                const size_t smem = std::max((size_t)w * 4, kRingBytes<T, G::vec, G::nv>);
+                // the ring, and in its place at the end the teams' sums
+                const size_t smem = std::max((size_t)w * 4 * (kThreads / std::max(G::lpr, 32)), kRingBytes<T, G::vec, G::nv>);
                 auto kern = b.k.codes ? k_join_bwd<T, G::vec, G::nv, G::lpr, true> : k_join_bwd<T, G::vec, G::nv, G::lpr, false>;
                 attr = smem > 48 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                                         : cudaSuccess;
@@ -557,10 +574,9 @@ pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, con
         const int64_t outs_n = (dpre ? 1 : 0) + (dpost ? 1 : 0) + (dgate ? gates : 0);
         JoinSumArgs q{part_pre, part_branch, p.post, p.gate, dpre, dpost, dgate, gates, (int)blocks, (int)w, tiles};
         const unsigned n = (unsigned)(outs_n * tiles);
-        if (p.dtype == PMHA_BF16) k_join_sums<__nv_bfloat16><<<n, kThreads, 0, cs>>>(q);
-        else k_join_sums<float><<<n, kThreads, 0, cs>>>(q);
-        count_launch();
-        PMHA_CUDA_TRY(cudaGetLastError());
+        st = p.dtype == PMHA_BF16 ? tcu::launch_overlapping(k_join_sums<__nv_bfloat16>, dim3(n), kThreads, 0, cs, q)
+                                  : tcu::launch_overlapping(k_join_sums<float>, dim3(n), kThreads, 0, cs, q);
+        if (st != PMHA_OK) return st;
     }
     return PMHA_OK;
 }

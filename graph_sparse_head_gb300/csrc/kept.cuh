@@ -48,51 +48,50 @@ __device__ __forceinline__ float kept_inverse(float scale)  // within 2^-22
 // v / scale to the nearest integer, in the low byte, ties to even. A bfloat16 v and scale: the quotient is at least 2^-10
 // away from a half unless it is one, and its product with the inverse is within 2^-15 of it, so that rounding it to a grid of
 // 2^-11 first gives back the halves. A float32 v: the remainder of the product's nearest integer q is exact (both v and
-// q scale are multiples of its last bit) and says whether the neighbour is nearer, or as near and even.
+// q scale are multiples of its last bit) and says whether the neighbour is nearer, or as near and even. (Of a group with
+// an infinity or a NaN any code will do: its scale is NaN.)
 template <typename T>
 __device__ __forceinline__ uint32_t kept_code(float v, float scale, float inv)
 {
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23
     if constexpr (sizeof(T) == 2) {
-        const float y = __fsub_rn(__fmaf_rn(v, inv, 6144.f), 6144.f);
-        return __float_as_uint(__fadd_rn(y, kRound)) & 0xffu;
+        // 6144 off before the last addition: a multiple of the grid and of 256
+        return __float_as_uint(__fadd_rn(__fmaf_rn(v, inv, 6144.f), kRound));
     } else {
         const float m = __fmaf_rn(v, inv, kRound), q = __fsub_rn(m, kRound);
         const float e = __fmaf_rn(-q, scale, v), half = 0.5f * scale;
         const bool move = fabsf(e) > half || (fabsf(e) == half && (__float_as_uint(m) & 1u));
-        return (__float_as_uint(m) + (move ? (e > 0.f ? 1u : 0xffffffffu) : 0u)) & 0xffu;
+        return __float_as_uint(m) + (move ? (e > 0.f ? 1u : 0xffffffffu) : 0u);
     }
 }
 
 // Keeps VEC values of a group whose others lie in the neighbouring lanes, at these places; `first`: the group's first
 // lane. Every lane of the warp comes here, those past the width with zeros and in == false.
 template <typename T, int VEC>
-__device__ __forceinline__ void keep(const KeptOut &at, bool first, bool in, const T (&v)[VEC])
+__device__ __forceinline__ void keep(const KeptOut &at, bool first, bool in, const Vals<T, VEC> &v)
 {
-    constexpr int kLanes = kGroup / VEC;
-    uint32_t most = 0;
+    uint32_t most = most_bits<T, VEC>(v);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) most = max(most, __float_as_uint(to_f<T>(v[i])) & 0x7fffffffu);
+    for (int o = kGroup / VEC / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+    const float scale = kept_scale(most), inv = kept_inverse(scale);
+    uint32_t w[VEC];
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
-    const float scale = kept_scale(most);
-    const bool fine = most < 0x7f800000u;
-    const float inv = kept_inverse(scale);
-    alignas(8) uint8_t b[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) b[i] = fine ? (uint8_t)kept_code<T>(to_f<T>(v[i]), scale, inv) : (uint8_t)0;
+    for (int i = 0; i < VEC; ++i) w[i] = kept_code<T>(to_f<T>(v.v[i]), scale, inv);
     if (!in) return;
-    *reinterpret_cast<typename Bytes<VEC>::type *>(at.codes) = *reinterpret_cast<typename Bytes<VEC>::type *>(b);
+    *reinterpret_cast<typename Bytes<VEC>::type *>(at.codes) = low_bytes<VEC>(w);
     if (first) *at.scale = __float2bfloat16_rn(scale);
 }
-// VEC kept values, in float32
+// VEC kept values, in float32: a byte b ^ 0x80 in the last place of 2^23 is 2^23 + 128 + b
 template <int VEC>
 __device__ __forceinline__ void unkeep(const typename Bytes<VEC>::type &codes, float scale, float (&v)[VEC])
 {
-    alignas(8) int8_t b[VEC];
-    *reinterpret_cast<typename Bytes<VEC>::type *>(b) = codes;
+    uint32_t w[(VEC + 3) / 4] = {};
+    *reinterpret_cast<typename Bytes<VEC>::type *>(w) = codes;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = (float)b[i] * scale;
+    for (int i = 0; i < VEC; ++i) {
+        const uint32_t b = __byte_perm(w[i / 4] ^ 0x80808080u, 0x4b000000u, 0x7540 + (i & 3));
+        v[i] = __fsub_rn(__uint_as_float(b), 8388736.f) * scale;
+    }
 }
 template <int VEC>
 __device__ __forceinline__ void load_kept(const Kept &k, long long row, int c, int width, float (&v)[VEC])

@@ -48,32 +48,30 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long 
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int r = (int)threadIdx.x / kRow + (r0 - (int)(threadIdx.x / 32 * 32 / kRow)) + i * kRows;
-            uint32_t most = 0;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) most = max(most, abs_bits(to_f<T>(v[i].v[e])));
+            uint32_t most = most_bits<T, VEC>(v[i]);
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
             const uint32_t byte = mx_scale_byte(most);
-            const bool fine = byte < 255u, in = block && r < r_end;
-            const float inv = fine ? mx_inverse(byte) : 0.f;
+            const bool in = block && r < r_end;
+            const float inv = mx_inverse(byte);
             uint8_t *dst = codes + ((row0 + r) * blocks + tile * 4 + k) * 16;
             if constexpr (VEC == 8) {
                 uint32_t w = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     w |= mx_byte(to_f<T>(v[i].v[2 * e]) * inv, to_f<T>(v[i].v[2 * e + 1]) * inv) << (8 * e);
-                if (in) *reinterpret_cast<uint32_t *>(dst + l * 4) = fine ? w : 0u;
+                if (in) *reinterpret_cast<uint32_t *>(dst + l * 4) = w;
             } else if constexpr (VEC == 4) {
                 const uint32_t w = mx_byte(to_f<T>(v[i].v[0]) * inv, to_f<T>(v[i].v[1]) * inv) |
                                    mx_byte(to_f<T>(v[i].v[2]) * inv, to_f<T>(v[i].v[3]) * inv) << 8;
-                if (in) *reinterpret_cast<uint16_t *>(dst + l * 2) = fine ? (uint16_t)w : (uint16_t)0;
+                if (in) *reinterpret_cast<uint16_t *>(dst + l * 2) = (uint16_t)w;
             } else if constexpr (VEC == 2) {
                 const uint32_t w = mx_byte(to_f<T>(v[i].v[0]) * inv, to_f<T>(v[i].v[1]) * inv);
-                if (in) dst[l] = fine ? (uint8_t)w : (uint8_t)0;
+                if (in) dst[l] = (uint8_t)w;
             } else {
                 const float f = to_f<T>(v[i].v[0]) * inv, next = __shfl_down_sync(kFull, f, 1);
                 const uint32_t w = mx_byte(f, next);
-                if (in && l % 2 == 0) dst[l / 2] = fine ? (uint8_t)w : (uint8_t)0;
+                if (in && l % 2 == 0) dst[l / 2] = (uint8_t)w;
             }
             if (l == 0 && in) bytes[(r & 31) * 16 + (r >> 5) * 4 + k] = (uint8_t)byte;
         }
@@ -177,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
             for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
             if (i >= a.M * blocks) continue;
             const uint32_t byte = mx_scale_byte(most);
-            const float inv = byte < 255u ? mx_inverse(byte) : 0.f;
+            const float inv = mx_inverse(byte);
             __half2 v[2] = {two_of(mx_byte(f[0] * inv, f[1] * inv)), two_of(mx_byte(f[2] * inv, f[3] * inv))};
             uint8_t *cell = cells + i * kCell;
             *reinterpret_cast<uint2 *>(cell + 8 * q) = *reinterpret_cast<uint2 *>(v);

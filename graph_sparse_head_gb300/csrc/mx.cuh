@@ -54,8 +54,8 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t most)
     const int b = e - ((most & 0x7fffffu) <= 0x400000u ? 2 : 1);  // 6 2^e = 1.5 2^(e + 2)
     return e >= 255 ? 255u : (uint32_t)max(b, 0);
 }
-// 2^(127 - byte), for bytes up to 253
-__device__ __forceinline__ float mx_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^(127 - byte), for bytes up to 253; 0 for 255 (of a block whose scale is NaN the codes are zeros)
+__device__ __forceinline__ float mx_inverse(uint32_t byte) { return __uint_as_float((uint32_t)max(254 - (int)byte, 0) << 23); }
 // 2^(byte - 127), NaN for 255
 __device__ __forceinline__ float mx_scale_value(uint32_t byte)
 {

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                     }
                 }
                 const uint32_t byte = mx_scale_byte(most);
-                const float inv = byte < 255u ? mx_inverse(byte) : 0.f;
+                const float inv = mx_inverse(byte);
                 uint32_t w[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -293,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         w[c] |= mx_byte(h[8 * c + 2 * e] * inv, h[8 * c + 2 * e + 1] * inv) << (8 * e);
-                    if (byte == 255u) w[c] = 0;
                 }
                 *reinterpret_cast<uint4 *>(tile_s + r * 64 + part * 16) = make_uint4(w[0], w[1], w[2], w[3]);
                 tile_s[128 * 64 + 16 * lane + 4 * quarter + part] = (uint8_t)byte;

@@ -58,6 +58,35 @@ template <typename T, int VEC> struct alignas(sizeof(typename Pack<T, VEC>::type
     T v[VEC];
 };
 
+// The bits, as float32, of the largest magnitude of some values; compared as integers, so that infinities and NaN come last.
+template <typename T, int VEC>
+__device__ __forceinline__ uint32_t most_bits(const Vals<T, VEC> &v)
+{
+    uint32_t most = 0;
+    if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(v.v);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) most = __vmaxu2(most, w[i] & 0x7fff7fffu);
+        return max(most & 0xffff0000u, most << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) most = max(most, __float_as_uint(to_f<T>(v.v[i])) & 0x7fffffffu);
+        return most;
+    }
+}
+// The low bytes of VEC words
+template <int VEC>
+__device__ __forceinline__ typename Bytes<VEC>::type low_bytes(const uint32_t (&w)[VEC])
+{
+    if constexpr (VEC == 1) return (uint8_t)w[0];
+    else if constexpr (VEC == 2) return (uint16_t)__byte_perm(w[0], w[1], 0x0040);
+    else {
+        const uint32_t a = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+        if constexpr (VEC == 4) return a;
+        else return make_uint2(a, __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
+    }
+}
+
 // An unevaluated sum hi + lo (about 46 bits).
 struct Two {
     float hi, lo;
