@@ -9,6 +9,9 @@
 // kind::mxf4, whose scaling by block is the hardware's; sixteen warps turn accumulators into outputs. Accumulators of 256
 // columns and the scales of four stages fill tensor memory, so there is one set: each epilogue thread takes all of its
 // accumulators into registers (64) and hands the set back at once, the next tile's products run under its arithmetic.
+// Epilogue warps go their own ways: each has its 32 rows' share of the columns, its own piece of shared memory, its own
+// copies of the residual and of the result, and no barrier with the others. (With a barrier for all sixteen around each
+// step 320,000 x 128 x 512 gated took 152 us.)
 //
 // Ragged sizes need no code of their own: TMA fills rows and columns past a
 // tensor's end with zeros (codes and scale tiles) and does not store them. Only
@@ -33,9 +36,10 @@ constexpr int kSfA = 2 * 512;         // scale tiles of a stage: 128 rows x 256 
 constexpr int kSfB = 4 * 512;         // 256 rows x 256 columns
 constexpr int kStage = 2 * kBox + kSfA + kSfB;
 constexpr int kStages = 4;
-constexpr int kTile = 4 * kBox;       // 128 x 256 bf16; gated: 128 x 64 bytes and 512 scales
-constexpr int kVec = 256 * 4;
-constexpr int kBars = 256;
+constexpr int kTile = 4 * kBox;       // 128 x 256 bf16, a piece of 32 x 64 for each epilogue warp
+constexpr int kPiece = kTile / 16;
+constexpr int kVec = 16 * 64 * 4;     // a warp's biases: of 64 outputs, or 32 of gate and of up
+constexpr int kBars = 512;
 constexpr int kSmem = 1024 + kStages * kStage + kTile + kVec + kBars;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 static_assert(kStage % 1024 == 0, "swizzled tiles lie on 1024 bytes");
@@ -43,14 +47,15 @@ constexpr int kTmemCols = 512;        // 256 accumulator columns, 24 scale colum
 constexpr int kScaleCol = 256;
 
 struct Params {
-    CUtensorMap a, b0, b1, sa, sb0, sb1, out, res, h;
+    CUtensorMap a, b0, b1, sa, sb0, sb1, out, res;
     int M, N;               // tokens, outputs (gated: hidden width)
     int n_tiles, tiles_n, kb;
     const __nv_bfloat16 *bias0, *bias1;
     const __nv_bfloat16 *res_p;  // plain: row-wise outputs without TMA
     __nv_bfloat16 *out_p;
-    uint8_t *h_scale;
-    int h_tiles;            // scale tiles of a row block of h
+    uint8_t *h_codes, *h_scale;
+    long long h_pitch;
+    int h_blocks, h_tiles;  // blocks of a row of h, scale tiles of a row block
     int has_res, plain;
     int *err;
 };
@@ -109,7 +114,27 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N])
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-__device__ __forceinline__ void team_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+// The larger magnitude, NaN before all
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
+}
+// Eight values as codes, the first in the lowest half byte
+__device__ __forceinline__ uint32_t mx_word(const float (&f)[8])
+{
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return w;
+}
 
 template <bool GATED, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(const __grid_constant__ Params p)
@@ -117,14 +142,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *tile_s = smem + kStages * kStage;
-    float *vec_s = (float *)(tile_s + kTile);                   // 256 biases: of outputs, or 128 of gate and of up
+    float *vec_s = (float *)(tile_s + kTile);
     uint64_t *full = (uint64_t *)((uint8_t *)vec_s + kVec);     // [kStages], counted in the even CTA
     uint64_t *empty = full + kStages;                           // [kStages], in each CTA
     uint64_t *acc_full = empty + kStages;                       // in each CTA
     uint64_t *acc_empty = acc_full + 1;                         // counted in the even CTA
     uint64_t *mma_done = acc_empty + 1;
-    uint64_t *res_full = mma_done + 1;
-    uint32_t *tmem_holder = (uint32_t *)(res_full + 1);
+    uint64_t *res_full = mma_done + 1;                          // [16], of the epilogue warps
+    uint32_t *tmem_holder = (uint32_t *)(res_full + 16);
     volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
     volatile uint32_t *armed = (volatile uint32_t *)(tmem_holder + 2);  // copies counted
 
@@ -139,9 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             mbar_init(smem_u32(&empty[s]), 1);
         }
         mbar_init(smem_u32(acc_full), 1);
-        mbar_init(smem_u32(acc_empty), 2);  // the epilogue of either CTA
+        mbar_init(smem_u32(acc_empty), 32);  // the epilogue warps of both CTAs
         mbar_init(smem_u32(mma_done), 1);
-        mbar_init(smem_u32(res_full), 1);
+        for (int w = 0; w < 16; ++w) mbar_init(smem_u32(&res_full[w]), 1);
         *abort_flag = 0;
         *armed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -220,136 +245,152 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
     } else {
-        // ---------------- epilogue: four groups of four warps, each a quarter of a tile's columns
-        const int et = threadIdx.x - 64, quarter = warp & 3, part = et >> 7;
-        const bool lead = et == 0;
-        const int r = quarter * 32 + lane;  // row within this CTA's 128
+        // ---------------- epilogue: a warp 32 rows and a quarter of a tile's columns
+        const int w = warp - 2, quarter = warp & 3, part = w >> 2;
+        const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(GATED ? part * 32 : part * 64);
+        const uint32_t empty_bar = map_rank(smem_u32(acc_empty), 0);
+        float *bias = vec_s + w * 64;
+        uint8_t *piece = tile_s + w * kPiece;
+        constexpr float kg = GATED ? Act<ACT>::kGate : 1.f, ku = GATED ? Act<ACT>::kUp : 1.f;
+        auto rows_of = [&](int tile) { return tile / p.tiles_n * 256 + (int)rank * 128 + quarter * 32; };
+        auto column_of = [&](int tile) { return tile % p.tiles_n * kCols + part * (GATED ? 32 : 64); };
+        auto fetch_residual = [&](int tile) {
+            if (GATED || !p.has_res || p.plain || lane) return;
+            const int row = rows_of(tile), c = column_of(tile);
+            if (row < p.M && c < p.N) {
+                mbar_arrive_expect_tx(smem_u32(&res_full[w]), kPiece);
+                tma_load_2d(smem_u32(piece), &p.res, c, row, smem_u32(&res_full[w]));
+            } else {
+                mbar_arrive(smem_u32(&res_full[w]));
+            }
+        };
+        // biases of the next tile: this lane's columns
+        float b0 = 0.f, b1 = 0.f;
+        auto fetch_bias = [&](int tile) {
+            const int c = column_of(tile) + lane, c2 = GATED ? c : c + 32;
+            const __nv_bfloat16 *second = GATED ? p.bias1 : p.bias0;
+            b0 = p.bias0 && c < p.N ? kg * __bfloat162float(p.bias0[c]) : 0.f;
+            b1 = second && c2 < p.N ? ku * __bfloat162float(second[c2]) : 0.f;
+        };
         uint32_t i = 0;
+        if (pair < p.n_tiles) {
+            fetch_residual(pair);
+            fetch_bias(pair);
+        }
         for (int tile = pair; tile < p.n_tiles; tile += n_pairs, ++i) {
-            const int m = tile / p.tiles_n, n = tile % p.tiles_n;
-            const int row0 = m * 256 + (int)rank * 128, c0 = n * kCols;
-            // biases of the tile's columns, and the residual's tile, under the products
-            constexpr float kg = GATED ? Act<ACT>::kGate : 1.f, ku = GATED ? Act<ACT>::kUp : 1.f;
-            if (et < 256) {
-                const int c = c0 + (GATED ? et & 127 : et);
-                const bool up = GATED && et >= 128;
-                const __nv_bfloat16 *b = up ? p.bias1 : p.bias0;
-                vec_s[et] = b && c < p.N ? (up ? ku : kg) * __bfloat162float(b[c]) : 0.f;
-            }
-            if (lead) store_wait_read();  // the last tile's store has read the tile
-            if (!GATED && p.has_res) {
-                if (p.plain) {
-                    team_sync();
-                    // a warp a row, the row's values side by side
-                    for (int q = warp - 2; q < 128 && row0 + q < p.M; q += 16)
-                        for (int c = lane; c < 256 && c0 + c < p.N; c += 32)
-                            *(__nv_bfloat16 *)(tile_s + (c >> 6) * kBox + swizzled(q, (c & 63) >> 3) + (c & 7) * 2) =
-                                p.res_p[(size_t)(row0 + q) * p.N + c0 + c];
-                } else if (lead) {
-                    uint32_t bytes = 0;
-                    for (int j = 0; j < 4; ++j) bytes += row0 < p.M && c0 + j * 64 < p.N ? kBox : 0;
-                    if (bytes) mbar_arrive_expect_tx(smem_u32(res_full), bytes);
-                    else mbar_arrive(smem_u32(res_full));
-                    for (int j = 0; j < 4; ++j)
-                        if (row0 < p.M && c0 + j * 64 < p.N)
-                            tma_load_2d(smem_u32(tile_s + j * kBox), &p.res, c0 + j * 64, row0, smem_u32(res_full));
-                }
-            }
-            team_sync();
+            const int row0 = rows_of(tile), c0 = column_of(tile);
+            __syncwarp();
+            bias[lane] = b0;
+            bias[32 + lane] = b1;
+            __syncwarp();
+            if (tile + n_pairs < p.n_tiles) fetch_bias(tile + n_pairs);
             // after an expired wait the waits return at once and the loop runs out
             wait_bar(smem_u32(acc_full), i & 1u, abort_flag, p.err);
             tc_fence_after();
-            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16);
+            __syncwarp();
             uint32_t v[2][32];  // gated: gate and up of 32 hidden columns; else 64 outputs
-            tmem_ld32_nowait(t0 + (uint32_t)(GATED ? part * 32 : part * 64), v[0]);
-            tmem_ld32_nowait(t0 + (uint32_t)(GATED ? 128 + part * 32 : part * 64 + 32), v[1]);
+            tmem_ld32_nowait(t0, v[0]);
+            tmem_ld32_nowait(t0 + (GATED ? 128u : 32u), v[1]);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
             pin(v[0]);
             pin(v[1]);
             tc_fence_before();
-            team_sync();
-            if (lead) mbar_arrive_cluster(map_rank(smem_u32(acc_empty), 0));
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_bar);
             if constexpr (GATED) {
-                float h[32];
-                uint32_t most = 0;
-                const float *bg = vec_s + part * 32, *bu = bg + 128;
+                float most = 0.f;
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
-                    const float4 g = *reinterpret_cast<const float4 *>(bg + c), u = *reinterpret_cast<const float4 *>(bu + c);
+                    const float4 g = *reinterpret_cast<const float4 *>(bias + c), u = *reinterpret_cast<const float4 *>(bias + 32 + c);
                     const float gf[4] = {g.x, g.y, g.z, g.w}, uf[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        h[c + e] = Act<ACT>::hidden(fmaf(__uint_as_float(v[0][c + e]), kg, gf[e]),
-                                                    fmaf(__uint_as_float(v[1][c + e]), ku, uf[e]));
-                        most = max(most, abs_bits(h[c + e]));
+                        const float h = Act<ACT>::hidden(fmaf(__uint_as_float(v[0][c + e]), kg, gf[e]),
+                                                         fmaf(__uint_as_float(v[1][c + e]), ku, uf[e]));
+                        most = max_nan(most, h);
+                        v[0][c + e] = __float_as_uint(h);
                     }
                 }
-                const uint32_t byte = mx_scale_byte(most);
+                const uint32_t byte = mx_scale_byte(abs_bits(most));
                 const float inv = mx_inverse(byte);
-                uint32_t w[4];
+                uint32_t code[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    w[c] = 0;
+                    float f[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[c] |= mx_byte(h[8 * c + 2 * e] * inv, h[8 * c + 2 * e + 1] * inv) << (8 * e);
+                    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[0][8 * c + e]) * inv;
+                    code[c] = mx_word(f);
                 }
-                *reinterpret_cast<uint4 *>(tile_s + r * 64 + part * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                tile_s[128 * 64 + 16 * lane + 4 * quarter + part] = (uint8_t)byte;
+                // Straight to memory: 16 bytes of a row each, which meet those of the neighbouring blocks in L2. Blocks
+                // past the last have a place in the scale tile, where they put the scale of zeros.
+                const int row = row0 + lane, block = c0 / 32;
+                if (row < p.M) {
+                    if (block < p.h_blocks)
+                        *reinterpret_cast<uint4 *>(p.h_codes + row * p.h_pitch + block * 16) =
+                            make_uint4(code[0], code[1], code[2], code[3]);
+                    p.h_scale[((size_t)(row0 >> 7) * p.h_tiles + (block >> 2)) * 512 + 16 * lane + 4 * quarter + part] =
+                        (uint8_t)byte;
+                }
             } else {
-                if (p.has_res && !p.plain) wait_bar(smem_u32(res_full), i & 1u, abort_flag, p.err);
-                uint8_t *box = tile_s + part * kBox;
+                if (p.plain) {
+                    if (p.has_res) {
+                        for (int q = 0; q < 32 && row0 + q < p.M; ++q)
+                            for (int c = lane; c < 64 && c0 + c < p.N; c += 32)
+                                *(__nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2) =
+                                    p.res_p[(size_t)(row0 + q) * p.N + c0 + c];
+                        __syncwarp();
+                    }
+                } else if (p.has_res) {
+                    wait_bar(smem_u32(&res_full[w]), i & 1u, abort_flag, p.err);
+                } else {
+                    if (lane == 0) store_wait_read();  // the last tile's store has read the piece
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    uint4 *at = reinterpret_cast<uint4 *>(box + swizzled(r, u));
+                    uint4 *at = reinterpret_cast<uint4 *>(piece + swizzled(lane, u));
                     uint32_t rw[4] = {0, 0, 0, 0};
                     if (p.has_res) {
                         const uint4 q = *at;
                         rw[0] = q.x, rw[1] = q.y, rw[2] = q.z, rw[3] = q.w;
                     }
-                    uint32_t w[4];
+                    uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int c = 8 * u + 2 * e;
-                        const float2 b = *reinterpret_cast<const float2 *>(vec_s + part * 64 + c);
-                        w[e] = pack_bf16(__uint_as_float(v[c >> 5][c & 31]) + b.x + __uint_as_float(rw[e] << 16),
+                        const float2 b = *reinterpret_cast<const float2 *>(bias + c);
+                        o[e] = pack_bf16(__uint_as_float(v[c >> 5][c & 31]) + b.x + __uint_as_float(rw[e] << 16),
                                          __uint_as_float(v[c >> 5][(c & 31) + 1]) + b.y + __uint_as_float(rw[e] & 0xffff0000u));
                     }
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    *at = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-            }
-            fence_async_shared();
-            team_sync();
-            if constexpr (GATED) {
-                if (lead) {
-                    if (row0 < p.M) {
-                        tma_store_tile(&p.h, smem_u32(tile_s), n * 64, row0);
-                        uint8_t *dst = p.h_scale + ((size_t)(row0 / 128) * p.h_tiles + n) * 512;
-                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], 512;" ::"l"(dst),
-                                     "r"(smem_u32(tile_s + 128 * 64))
-                                     : "memory");
+                if (p.plain) {
+                    __syncwarp();
+                    for (int q = 0; q < 32 && row0 + q < p.M; ++q)
+                        for (int c = lane; c < 64 && c0 + c < p.N; c += 32)
+                            p.out_p[(size_t)(row0 + q) * p.N + c0 + c] =
+                                *(const __nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2);
+                } else {
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row0 < p.M && c0 < p.N) tma_store_tile(&p.out, smem_u32(piece), c0, row0);
+                        store_commit();
+                        if (p.has_res && tile + n_pairs < p.n_tiles) {
+                            store_wait_read();
+                            fetch_residual(tile + n_pairs);
+                        }
                     }
-                    store_commit();
                 }
-            } else if (p.plain) {
-                for (int q = warp - 2; q < 128 && row0 + q < p.M; q += 16)
-                    for (int c = lane; c < 256 && c0 + c < p.N; c += 32)
-                        p.out_p[(size_t)(row0 + q) * p.N + c0 + c] =
-                            *(const __nv_bfloat16 *)(tile_s + (c >> 6) * kBox + swizzled(q, (c & 63) >> 3) + (c & 7) * 2);
-                team_sync();  // read before the next tile's residual comes
-            } else if (lead) {
-                for (int j = 0; j < 4; ++j)
-                    if (row0 < p.M && c0 + j * 64 < p.N)
-                        tma_store_tile(&p.out, smem_u32(tile_s + j * kBox), c0 + j * 64, row0);
-                store_commit();
             }
         }
-        if (lead) {
-            store_wait_all();  // shared memory outlives its stores, and after an expired wait the residual's copy
+        if (!GATED && lane == 0) {
+            store_wait_all();  // shared memory outlives its stores, and after an expired wait the residual's copies
             int dummy = 0;
             if (*abort_flag && p.has_res && !p.plain && i)
-                mbar_wait(smem_u32(res_full), (i - 1) & 1u, (volatile int *)&dummy, p.err);
+                mbar_wait(smem_u32(&res_full[w]), (i - 1) & 1u, (volatile int *)&dummy, p.err);
         }
+        __syncwarp();
     }
 
     __syncthreads();
@@ -433,8 +474,8 @@ pmha_status mx_tc_linear(const MxLinear &a, const char *stage, cudaStream_t s)
     p.res_p = (const __nv_bfloat16 *)a.residual;
     p.out_p = (__nv_bfloat16 *)a.out;
     if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.w, a.N, a.K) ||
-        (!p.plain && (!make_tile_map(&p.out, a.out, a.M, a.N, a.N, 2, 128) ||
-                      (a.residual && !make_tile_map(&p.res, a.residual, a.M, a.N, a.N, 2, 128)))))
+        (!p.plain && (!make_tile_map(&p.out, a.out, a.M, a.N, a.N, 2, 32) ||
+                      (a.residual && !make_tile_map(&p.res, a.residual, a.M, a.N, a.N, 2, 32)))))
         return map_failed(stage);
     return launch<false, 0>(p, stage, s);
 }
@@ -447,15 +488,13 @@ pmha_status mx_tc_gated(const MxGated &a, cudaStream_t s)
     if (st != PMHA_OK) return st;
     p.bias0 = (const __nv_bfloat16 *)a.bg;
     p.bias1 = (const __nv_bfloat16 *)a.bu;
+    p.h_codes = a.h_codes;
     p.h_scale = a.h_scale;
+    p.h_pitch = mx_pitch(a.F);
+    p.h_blocks = (int)mx_blocks(a.F);
     p.h_tiles = (int)ceil_div(mx_blocks(a.F), 4);
-    EncodeTiledFn fn = encode_fn();
-    cuuint64_t dims[2] = {(cuuint64_t)mx_pitch(a.F), (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)mx_pitch(a.F)};
-    cuuint32_t box[2] = {64, 128}, estr[2] = {1, 1};
-    if (!fn || !maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.wg, a.F, a.K) ||
-        !maps_of(&p.b1, &p.sb1, a.wu, a.F, a.K) ||
-        fn(&p.h, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.h_codes, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.wg, a.F, a.K) ||
+        !maps_of(&p.b1, &p.sb1, a.wu, a.F, a.K))
         return map_failed(stage);
     return a.act == PMHA_ACT_SILU ? launch<true, PMHA_ACT_SILU>(p, stage, s) : launch<true, PMHA_ACT_GELU>(p, stage, s);
 }
