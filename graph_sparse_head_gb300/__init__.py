@@ -26,6 +26,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import functools
 import itertools
 import math
 import operator
@@ -50,7 +51,7 @@ __all__ = [
     "pmha_ffn_forward", "pmha_ffn_forward_quantized", "pmha_ffn_backward",
     "pmha_ffn_forward_workspace_size", "pmha_ffn_forward_quantized_workspace_size",
     "pmha_ffn_backward_workspace_size", "pmha_clip_grad_norm",
-    "JoinParams", "Checkpoint", "pmha_join", "pmha_join_checkpointed", "pmha_join_backward",
+    "JoinParams", "Checkpoint", "LayerCheckpoint", "pmha_join", "pmha_join_checkpointed", "pmha_join_backward",
     "pmha_join_backward_workspace_size", "pmha_checkpoint", "pmha_checkpoint_restore",
     "MxTensor", "FfnMxParams", "pmha_mx_quantize", "pmha_mx_linear", "pmha_ffn_forward_mx",
     "pmha_ffn_forward_mx_workspace_size",
@@ -884,39 +885,97 @@ def pmha_ffn_backward(params: FfnParams, x: torch.Tensor, dout: torch.Tensor, in
 
 
 # ---------------------------------------------------------------- joins with the residual stream, 8-bit checkpoints
-@dataclasses.dataclass
-class Checkpoint:
-    """A tensor (..., width) kept in 8 bits between the forward and the backward pass: codes int8 of its shape and one
-    bfloat16 scale for every 32 values of a row, (..., ceil(width / 32)); value ~ code * scale. dtype: what it was."""
-    codes: torch.Tensor
-    scale: torch.Tensor
-    dtype: torch.dtype
+class _Buffer:
+    """What Checkpoint and MxTensor have in common: two arrays, codes and scales, given as tensors or lying in one
+    allocation of which tensors are made when they are asked for (an allocation and a view take as long as a launch)."""
+    __slots__ = ("_codes", "_scale", "_buffer", "_at", "_pointers", "_shape", "_index")
 
     @property
-    def shape(self) -> torch.Size:
-        return self.codes.shape
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n, shape, dtype = self._code_layout()
+            self._codes = self._buffer[:n].view(dtype).view(shape)
+        return self._codes
+
+    @property
+    def scale(self) -> torch.Tensor:
+        if self._scale is None:
+            n, shape, dtype = self._scale_layout()
+            self._scale = self._buffer[self._at:self._at + n].view(dtype).view(shape)
+        return self._scale
+
+    shape = property(lambda self: self._shape)
+
+    @property
+    def device(self) -> torch.device:
+        return (self._codes if self._buffer is None else self._buffer).device
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + 2 * self.scale.numel()
+        return self._code_layout()[0] + self._scale_layout()[0]
+
+    def _allocate(self, x):
+        n = self._code_layout()[0]
+        self._at = (n + 255) & ~255
+        self._buffer = b = torch.empty(self._at + self._scale_layout()[0], dtype=torch.uint8, device=x.device)
+        p = b.data_ptr()
+        self._codes = self._scale = None
+        self._pointers = p, p + self._at
+
+    def _given(self, codes, scale):
+        """Takes tensors, which must be of the layouts."""
+        if not isinstance(codes, _T) or not codes.is_cuda:
+            raise ValueError("codes and scale must be CUDA tensors")
+        self._index = codes.get_device()
+        for name, t, (_, shape, dtype) in (("codes", codes, self._code_layout()), ("scale", scale, self._scale_layout())):
+            if _like(name, t, torch.Size(shape), dtype, self._index) is None:
+                raise ValueError(f"{name} is missing")
+        self._codes, self._scale, self._buffer = codes, scale, None
+        self._pointers = codes.data_ptr(), scale.data_ptr()
+
+
+class Checkpoint(_Buffer):
+    """A tensor (..., width) kept in 8 bits between the forward and the backward pass: codes int8 of its shape and one
+    bfloat16 scale for every 32 values of a row, (..., ceil(width / 32)); value ~ code * scale. dtype: what it was.
+    Checked when it is made; its parts are not exchanged afterwards."""
+    __slots__ = ("_dtype",)
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype):
+        if dtype not in _DTYPES:
+            raise ValueError("a Checkpoint is of float32 or bfloat16")
+        if not isinstance(codes, _T) or not codes.dim():
+            raise ValueError("codes must be a CUDA tensor (..., width)")
+        self._shape, self._dtype = codes.shape, dtype
+        self._given(codes, scale)
+
+    dtype = property(lambda self: self._dtype)
+
+    def _code_layout(self):
+        return self._shape.numel(), self._shape, torch.int8
+
+    def _scale_layout(self):
+        *rows, width = self._shape
+        groups = (width + 31) // 32
+        return 2 * math.prod(rows) * groups, (*rows, groups), torch.bfloat16
 
     @staticmethod
     def _empty(x) -> "Checkpoint":
-        *rows, width = x.shape
-        return Checkpoint(torch.empty_like(x, dtype=torch.int8),
-                          torch.empty((*rows, (width + 31) // 32), dtype=torch.bfloat16, device=x.device), x.dtype)
+        """For a tensor like x, to be written."""
+        k = object.__new__(Checkpoint)
+        k._shape, k._dtype, k._index = x.shape, x.dtype, x.get_device()
+        k._allocate(x)
+        return k
 
     def _struct(self):
-        return _lib.PmhaKept(self.codes.data_ptr(), self.scale.data_ptr())
+        return _lib.PmhaKept(*self._pointers)
 
 
 def _kept_like(name, k, shape, dtype, index):
     """The struct of a Checkpoint of a tensor of this shape, type and device."""
-    if k.dtype is not dtype:
+    if k._dtype is not dtype:
         raise ValueError(f"{name} was kept from {k.dtype}, the call runs in {dtype}")
-    if _like(name + ".codes", k.codes, shape, torch.int8, index) is None \
-            or _like(name + ".scale", k.scale, (*shape[:-1], (shape[-1] + 31) // 32), torch.bfloat16, index) is None:
-        raise ValueError(f"{name} lacks its codes or scales")
+    if k._shape != shape or k._index != index:
+        raise ValueError(f"{name} must be of {tuple(shape)} on cuda:{index}")
     return k._struct()
 
 
@@ -935,30 +994,20 @@ def pmha_checkpoint(x: torch.Tensor, stream=None) -> Checkpoint:
 
 def pmha_checkpoint_restore(kept: Checkpoint, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """code * scale in the type that the tensor had."""
-    shape, dtype = _shape_of("kept", kept)
-    dev = kept.codes.get_device()
-    k = _kept_like("kept", kept, shape, dtype, dev)
+    if type(kept) is not Checkpoint:
+        raise TypeError("kept must be a Checkpoint (pmha_checkpoint makes one)")
+    shape, dtype, dev = kept._shape, kept._dtype, kept._index
     o = _like("out", out, shape, dtype, dev)
     width = shape[-1]
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=kept.codes.device)
+            out = torch.empty(shape, dtype=dtype, device=kept.device)
             o = out.data_ptr()
-        st = _library().pmha_checkpoint_restore(_DTYPES[dtype], kept.codes.numel() // width if width else 0, width,
-                                                ctypes.byref(k), o, _stream_of(dev, stream))
+        st = _library().pmha_checkpoint_restore(_DTYPES[dtype], shape.numel() // width if width else 0, width,
+                                                ctypes.byref(kept._struct()), o, _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_checkpoint_restore")
     return out
-
-
-def _shape_of(name, x):
-    """(shape, dtype) of a tensor or Checkpoint."""
-    if isinstance(x, Checkpoint):
-        if not isinstance(x.codes, _T) or not x.codes.is_cuda or not x.codes.dim() or x.dtype not in _DTYPES:
-            raise ValueError(f"{name} must keep a CUDA tensor (..., width) of float32 or bfloat16")
-        return x.codes.shape, x.dtype
-    shape, _, _, _ = _rows_of(name, x)
-    return shape, x.dtype
 
 
 @dataclasses.dataclass
@@ -988,29 +1037,30 @@ class JoinParams:
 
 
 def _join(params, branch, residual, keep_branch, keep_residual, stream):
-    x = residual.codes if type(residual) is Checkpoint else residual
-    shape, dtype = _shape_of("residual", residual)
-    dev = x.get_device()
-    width = shape[-1]
-    p = params._struct(dtype, width, dev)
     b = r = bk = rk = kb = kr = None
+    if type(residual) is Checkpoint:
+        shape, dtype, dev = residual._shape, residual._dtype, residual._index
+        rows, width = shape.numel(), shape[-1]
+        rows = rows // width if width else 0
+        rk = ctypes.byref(residual._struct())
+    else:
+        shape, rows, width, dev = _rows_of("residual", residual)
+        dtype = residual.dtype
+        r = residual.data_ptr()
+    p = params._struct(dtype, width, dev)
     if type(branch) is Checkpoint:
         bk = ctypes.byref(_kept_like("branch", branch, shape, dtype, dev))
     else:
         b = _like("branch", branch, shape, dtype, dev)
-    if x is residual:
-        r = x.data_ptr()
-    else:
-        rk = ctypes.byref(_kept_like("residual", residual, shape, dtype, dev))
     with _on(dev, stream):
-        s = torch.empty_like(x, dtype=dtype)
+        s = torch.empty(shape, dtype=dtype, device=residual.device) if r is None else torch.empty_like(residual)
         out = None if params.pre is None else torch.empty_like(s)
         if keep_branch:
             kb = Checkpoint._empty(branch)
         if keep_residual:
-            kr = Checkpoint._empty(x)
-        st = _library().pmha_join(ctypes.byref(p), x.numel() // width if width else 0, b, bk, r, rk, s.data_ptr(),
-                                  None if out is None else out.data_ptr(), None if kb is None else ctypes.byref(kb._struct()),
+            kr = Checkpoint._empty(residual)
+        st = _library().pmha_join(ctypes.byref(p), rows, b, bk, r, rk, s.data_ptr(), None if out is None else out.data_ptr(),
+                                  None if kb is None else ctypes.byref(kb._struct()),
                                   None if kr is None else ctypes.byref(kr._struct()), _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_join")
@@ -1064,7 +1114,7 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
     p = params._struct(dtype, width, dev)
     s = _like("sum", sum, shape, dtype, dev)
     dy, ds = _like("dout", dout, shape, dtype, dev), _like("dsum", dsum, shape, dtype, dev)
-    if isinstance(branch, Checkpoint):
+    if type(branch) is Checkpoint:
         b, bk = None, ctypes.byref(_kept_like("branch", branch, shape, dtype, dev))
     else:
         b, bk = _like("branch", branch, shape, dtype, dev), None
@@ -1077,10 +1127,14 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
         db = dr if alone or not input_grads else torch.empty_like(like)
         dpost = dgate = dpre = None
         if wanted:
-            f32 = torch.float32
-            dpost = None if params.post is None else torch.empty_like(params.post, dtype=f32)
-            dgate = None if params.gate is None else torch.empty_like(params.gate, dtype=f32)
-            dpre = None if params.pre is None else torch.empty_like(params.pre, dtype=f32)
+            f32, post, gate, pre = torch.float32, params.post, params.gate, params.pre
+            if post is not None and gate is not None and pre is not None and gate.shape == pre.shape and not width & 3:
+                # one allocation for three rows of whole 16 bytes
+                dpost, dgate, dpre = torch.empty((3, width), dtype=f32, device=like.device).unbind()
+            else:
+                dpost = None if post is None else torch.empty_like(post, dtype=f32)
+                dgate = None if gate is None else torch.empty_like(gate, dtype=f32)
+                dpre = None if pre is None else torch.empty_like(pre, dtype=f32)
         wp, wn, keep = _scratch(like, need, workspace)
         st = lib.pmha_join_backward(ctypes.byref(p), rows, b, bk, s, dy, ds, None if alone else _ptr(db), _ptr(dr),
                                     _ptr(dpost), _ptr(dgate), _ptr(dpre), wp, wn, _stream_of(dev, stream))
@@ -1090,59 +1144,49 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
 
 
 # ---------------------------------------------------------------- microscaled 4-bit floating point
-class MxTensor:
+class MxTensor(_Buffer):
     """A tensor (..., width) in microscaled 4 bits, as a matrix of its rows: E2M1 values in blocks of 32 along the row,
     each block times a power of two. codes uint8 (rows, ceil(width / 32) * 16), two a byte, the lower column in the low
     half; scale uint8 (row tiles, block tiles, 512), tiles of 128 rows by 4 blocks, byte b for 2^(b - 127), row r and
     block k of a tile at 16 (r % 32) + 4 (r / 32) + k. shape: the tensor's. Checked when it is made; its parts are not
     exchanged afterwards."""
-    __slots__ = ("_codes", "_scale", "_shape", "_rows", "_width", "_index")
+    __slots__ = ("_rows", "_width")
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, shape):
-        shape = torch.Size(shape)
-        rows, width, c, s = MxTensor._sizes(shape)
-        if not isinstance(codes, _T) or not codes.is_cuda:
-            raise ValueError("codes and scale must be CUDA tensors")
-        index, u8 = codes.get_device(), torch.uint8
-        if _like("codes", codes, c, u8, index) is None or _like("scale", scale, s, u8, index) is None:
-            raise ValueError("codes or scale is missing")
-        self._codes, self._scale, self._shape, self._rows, self._width, self._index = codes, scale, shape, rows, width, index
+        self._of(torch.Size(shape))
+        self._given(codes, scale)
 
-    codes = property(lambda self: self._codes)
-    scale = property(lambda self: self._scale)
-    shape = property(lambda self: self._shape)
-
-    @property
-    def nbytes(self) -> int:
-        return self.codes.numel() + self.scale.numel()
-
-    @staticmethod
-    def _sizes(shape):
-        """(rows, width, shape of codes, shape of scale)"""
-        width = shape[-1] if len(shape) else 0
+    def _of(self, shape):
+        self._shape = shape
+        self._width = width = shape[-1] if len(shape) else 0
         if not width:
             raise ValueError("an MxTensor has rows of one value at least")
-        rows, blocks = math.prod(shape[:-1]), (width + 31) // 32
-        return rows, width, (rows, blocks * 16), ((rows + 127) // 128, (blocks + 3) // 4, 512)
+        self._rows = shape.numel() // width
+
+    def _code_layout(self):
+        n = (self._width + 31) // 32 * 16
+        return self._rows * n, (self._rows, n), torch.uint8
+
+    def _scale_layout(self):
+        shape = (self._rows + 127) // 128, (self._width + 127) // 128, 512
+        return shape[0] * shape[1] * 512, shape, torch.uint8
 
     @staticmethod
     def _empty(x) -> "MxTensor":
         """For a tensor like x, to be written."""
         q = object.__new__(MxTensor)
-        shape = x.shape
-        rows, width, codes, scale = MxTensor._sizes(shape)
-        u8 = torch.uint8
-        q._codes, q._scale = torch.empty(codes, dtype=u8, device=x.device), torch.empty(scale, dtype=u8, device=x.device)
-        q._shape, q._rows, q._width, q._index = shape, rows, width, x.get_device()
+        q._of(x.shape)
+        q._index = x.get_device()
+        q._allocate(x)
         return q
 
     def _struct(self):
-        return _lib.PmhaMx(self._codes.data_ptr(), self._scale.data_ptr())
+        return _lib.PmhaMx(*self._pointers)
 
     def values(self) -> torch.Tensor:
         """The values that it stands for, in float64 (values near float32's end can round to 2^128). Torch operations, for
         inspection: not for a hot path."""
-        rows, width, _, _ = self._sizes(self.shape)
+        rows, width = self._rows, self._width
         grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=self.codes.device)
         v = torch.cat((grid, -grid))[torch.stack((self.codes & 15, self.codes >> 4), -1).long()].view(rows, -1, 32)
         t = self.scale.view(*self.scale.shape[:2], 32, 4, 4).permute(0, 3, 2, 1, 4)
@@ -1180,7 +1224,7 @@ def pmha_mx_linear(x: MxTensor, weight: MxTensor, bias: torch.Tensor | None = No
     o = _like("out", out, shape, bf16, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=bf16, device=x._codes.device)
+            out = torch.empty(shape, dtype=bf16, device=x.device)
             o = out.data_ptr()
         st = _library().pmha_mx_linear(x._rows, width, N, ctypes.byref(x._struct()), ctypes.byref(weight._struct()), b, r, o,
                                        _stream_of(dev, stream))
@@ -1247,9 +1291,9 @@ def pmha_ffn_forward_mx(params: FfnMxParams, x: MxTensor, residual: torch.Tensor
         need = _ffn_size(lib.pmha_ffn_forward_mx_workspace_size, p, rows, "pmha_ffn_forward_mx")  # raises
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=bf16, device=x._codes.device)
+            out = torch.empty(shape, dtype=bf16, device=x.device)
             o = out.data_ptr()
-        wp, wn, keep = _scratch(x._codes, need, workspace)
+        wp, wn, keep = _scratch(x, need, workspace)
         st = lib.pmha_ffn_forward_mx(pp, ctypes.byref(w), ctypes.byref(x._struct()), r, rows, o, wp, wn,
                                      _stream_of(dev, stream))
     if st:
@@ -1257,54 +1301,152 @@ def pmha_ffn_forward_mx(params: FfnMxParams, x: MxTensor, residual: torch.Tensor
     return out
 
 
+@dataclasses.dataclass
+class LayerCheckpoint:
+    """What a layer's backward pass needs of its forward pass, in 8 bits: the layer's input, the attention's output,
+    the block's output where its join needs it, and the mask."""
+    x: Checkpoint
+    attention: Checkpoint
+    block: Checkpoint | None
+    key_padding_mask: torch.Tensor | None
+
+    @property
+    def nbytes(self) -> int:
+        return sum(k.nbytes for k in (self.x, self.attention, self.block) if k is not None)
+
+
 class PackedEncoderLayer:
-    """One pre-norm encoder layer around the packed attention, on tokens
-    x (B, n, E) of one graph with query_features == key_features:
+    """One encoder layer around the packed attention, on tokens x (B, n, E) of one graph with
+    query_features == key_features:
 
         a = attention(norm1(x));  s = x + a;  y = s + block(norm2(s))
 
-    ``layer(x)`` runs it (residual and norm2 in one pass over the tokens);
-    ``layer.backward(x, dy)`` returns the gradients of x and of every parameter
-    for dy = dLoss/dy, recomputing the forward pass; ``layer.clip_grads`` scales
-    them by their global norm."""
+    or, with norms after the blocks, gates (learned (E,), or one a sample, (B, E)) and a scaled residual stream,
+
+        s = residual_scale x + gate1 norm(a; post1);  y = residual_scale s + gate2 norm(block(norm2(s)); post2)
+
+    ``layer(x)`` runs it (the joins with the residual stream in one pass over the tokens each); ``layer.backward(x, dy)``
+    returns the gradients of x and of every parameter for dy = dLoss/dy, recomputing the forward pass;
+    ``y, kept = layer.forward_checkpointed(x)`` and ``layer.backward_checkpointed(kept, dy)`` do the same from blocks'
+    outputs kept in 8 bits, without running the attention and the block forward again; ``layer.serve(x, block)`` runs it
+    with a block in 8 or 4 bits; ``layer.clip_grads`` scales the gradients by their global norm."""
 
     def __init__(self, graph: Graph, attention: Params, norm1: torch.Tensor, norm2: torch.Tensor, block: FfnParams,
-                 eps: float = 1e-6):
+                 eps: float = 1e-6, post1: torch.Tensor | None = None, gate1: torch.Tensor | None = None,
+                 post2: torch.Tensor | None = None, gate2: torch.Tensor | None = None, residual_scale: float = 1.0):
         if graph.query_features != graph.key_features:
             raise ValueError("an encoder layer needs a graph with query_features == key_features")
         if not isinstance(block, FfnParams):
             raise TypeError("block must be FfnParams (the layer has a backward pass; a block in 8 bits is called beside it)")
         E = attention.embed_dim
-        for n, t in (("norm1", norm1), ("norm2", norm2)):
-            _like(n, t, (E,), attention.dtype, attention.wq.get_device())
+        dev = attention.wq.get_device()
+        for n, t in (("norm1", norm1), ("norm2", norm2), ("post1", post1), ("post2", post2)):
+            _like(n, t, (E,), attention.dtype, dev)
         if block.wd.dtype != attention.dtype or block.wd.shape[0] != E:
             raise ValueError(f"the block must have width {E} and type {attention.dtype}")
         block.as_struct()  # checks its tensors
         self.graph, self.attention, self.block = graph, attention, block
         self.norm1, self.norm2, self.eps = norm1, norm2, float(eps)
+        self.join1 = JoinParams(norm2, post1, gate1, float(residual_scale), self.eps)
+        self.join2 = JoinParams(None, post2, gate2, float(residual_scale), self.eps)
+        for j in (self.join1, self.join2):
+            j._struct(attention.dtype, E, dev)  # checks its tensors
 
-    def _attend(self, x, key_padding_mask):
+    @staticmethod
+    def _plain(join: JoinParams) -> bool:
+        """An addition: what the norm and the block do on their way."""
+        return join.post is None and join.gate is None and join.residual_scale == 1.0
+
+    def _attention(self, x, key_padding_mask):
         n1, _ = pmha_rms_norm(x, self.norm1, self.eps)
         a, _ = pmha_forward(self.graph, self.attention, n1, n1, n1, key_padding_mask=key_padding_mask)
-        n2, s = pmha_rms_norm(a, self.norm2, self.eps, residual=x)
-        return n1, s, n2
+        return n1, a
+
+    def _attend(self, x, key_padding_mask):
+        n1, a = self._attention(x, key_padding_mask)
+        if self._plain(self.join1):
+            n2, s = pmha_rms_norm(a, self.norm2, self.eps, residual=x)
+        else:
+            s, n2 = pmha_join(self.join1, a, x)
+        return n1, a, s, n2
 
     def __call__(self, x: torch.Tensor, key_padding_mask: torch.Tensor | None = None) -> torch.Tensor:
-        _, s, n2 = self._attend(x, key_padding_mask)
-        return pmha_ffn_forward(self.block, n2, residual=s)
+        _, _, s, n2 = self._attend(x, key_padding_mask)
+        if self._plain(self.join2):
+            return pmha_ffn_forward(self.block, n2, residual=s)
+        return pmha_join(self.join2, pmha_ffn_forward(self.block, n2), s)[0]
+
+    def serve(self, x: torch.Tensor, block: FfnQuantizedParams | FfnMxParams,
+              key_padding_mask: torch.Tensor | None = None) -> torch.Tensor:
+        """The layer with a block of 8-bit or 4-bit weights, its tokens quantized on the way (bfloat16 layers)."""
+        if type(block) is FfnQuantizedParams:
+            if self._plain(self.join1):
+                _, a = self._attention(x, key_padding_mask)
+                q, scale, s = pmha_rms_norm_quantized(a, self.norm2, self.eps, residual=x)
+            else:
+                s = self._attend(x, key_padding_mask)[2]
+                q, scale, _ = pmha_rms_norm_quantized(s, self.norm2, self.eps)
+            forward = functools.partial(pmha_ffn_forward_quantized, block, q, scale)
+        elif type(block) is FfnMxParams:
+            _, _, s, n2 = self._attend(x, key_padding_mask)
+            forward = functools.partial(pmha_ffn_forward_mx, block, pmha_mx_quantize(n2))
+        else:
+            raise TypeError("block must be FfnQuantizedParams or FfnMxParams")
+        if self._plain(self.join2):
+            return forward(residual=s)
+        return pmha_join(self.join2, forward(), s)[0]
 
     def backward(self, x: torch.Tensor, dy: torch.Tensor, key_padding_mask: torch.Tensor | None = None) -> dict:
         """{"dx", "dnorm1", "dnorm2", and the keys of pmha_backward's and
-        pmha_ffn_backward's parameter gradients}."""
-        n1, s, n2 = self._attend(x, key_padding_mask)
-        gb = pmha_ffn_backward(self.block, n2, dy)
-        g2 = pmha_rms_norm_backward(s, self.norm2, self.eps, gb.pop("dx"), dsum=dy)
-        ds = g2["dx"]  # of x and of the attention's output
-        ga = pmha_backward(self.graph, self.attention, n1, n1, n1, ds, key_padding_mask=key_padding_mask)
+        pmha_ffn_backward's parameter gradients; "dpost1", "dgate1", "dpost2", "dgate2" of those the layer has}."""
+        n1, a, s, n2 = self._attend(x, key_padding_mask)
+        f = None if self._plain(self.join2) else pmha_ffn_forward(self.block, n2)
+        return self._backward(x, n1, a, s, n2, f, dy, key_padding_mask)
+
+    def forward_checkpointed(self, x: torch.Tensor, key_padding_mask: torch.Tensor | None = None):
+        """(y, LayerCheckpoint): layer(x), and what backward_checkpointed takes in x's place."""
+        _, a = self._attention(x, key_padding_mask)
+        s, n2, a8, x8 = pmha_join_checkpointed(self.join1, a, x)
+        f8 = None
+        if self._plain(self.join2):
+            y = pmha_ffn_forward(self.block, n2, residual=s)
+        else:
+            y, _, f8, _ = pmha_join_checkpointed(self.join2, pmha_ffn_forward(self.block, n2), s, keep_residual=False)
+        return y, LayerCheckpoint(x8, a8, f8, key_padding_mask)
+
+    def backward_checkpointed(self, kept: LayerCheckpoint, dy: torch.Tensor) -> dict:
+        """backward()'s gradients, of the layer at the kept values of its input and its blocks' outputs."""
+        s, n2 = pmha_join(self.join1, kept.attention, kept.x)
+        x, n1 = pmha_join(JoinParams(pre=self.norm1, eps=self.eps), None, kept.x)
+        return self._backward(x, n1, kept.attention, s, n2, kept.block, dy, kept.key_padding_mask)
+
+    def _backward(self, x, n1, a, s, n2, f, dy, key_padding_mask):
+        extra = {}
+
+        def parameters(join, g, i):
+            for n in ("post", "gate"):
+                if getattr(join, n) is not None:
+                    extra[f"d{n}{i}"] = g["d" + n]
+
+        df = ds = dy  # of the block's output, and of s by its way past the block
+        if not self._plain(self.join2):
+            g = pmha_join_backward(self.join2, f, None, None, dy)
+            df, ds = g["dbranch"], g["dresidual"]
+            parameters(self.join2, g, 2)
+        gb = pmha_ffn_backward(self.block, n2, df)
+        if self._plain(self.join1):
+            g2 = pmha_rms_norm_backward(s, self.norm2, self.eps, gb.pop("dx"), dsum=ds)
+            da = dx = g2["dx"]  # of x and of the attention's output
+            dnorm2 = g2["dweight"]
+        else:
+            g = pmha_join_backward(self.join1, a, s, gb.pop("dx"), ds)
+            da, dx, dnorm2 = g["dbranch"], g["dresidual"], g["dpre"]
+            parameters(self.join1, g, 1)
+        ga = pmha_backward(self.graph, self.attention, n1, n1, n1, da, key_padding_mask=key_padding_mask)
         dn1 = ga.pop("dquery")  # one tensor: the sum over the three roles
         del ga["dkey"], ga["dvalue"]
-        g1 = pmha_rms_norm_backward(x, self.norm1, self.eps, dn1, dsum=ds)
-        return {"dx": g1["dx"], "dnorm1": g1["dweight"], "dnorm2": g2["dweight"], **ga, **gb}
+        g1 = pmha_rms_norm_backward(x, self.norm1, self.eps, dn1, dsum=dx)
+        return {"dx": g1["dx"], "dnorm1": g1["dweight"], "dnorm2": dnorm2, **extra, **ga, **gb}
 
     @staticmethod
     def clip_grads(grads: dict, max_norm: float) -> torch.Tensor:

@@ -35,14 +35,20 @@ constexpr int kBox = 128 * 128;       // bytes of a tile of 128 rows of 128 byte
 constexpr int kSfA = 2 * 512;         // scale tiles of a stage: 128 rows x 256 columns
 constexpr int kSfB = 4 * 512;         // 256 rows x 256 columns
 constexpr int kStage = 2 * kBox + kSfA + kSfB;
-constexpr int kStages = 4;
-constexpr int kTile = 4 * kBox;       // 128 x 256 bf16, a piece of 32 x 64 for each epilogue warp
-constexpr int kPiece = kTile / 16;
-constexpr int kVec = 16 * 64 * 4;     // a warp's biases: of 64 outputs, or 32 of gate and of up
-constexpr int kBars = 512;
-constexpr int kSmem = 1024 + kStages * kStage + kTile + kVec + kBars;
-static_assert(kSmem <= 232448, "shared memory of one CTA");
 static_assert(kStage % 1024 == 0, "swizzled tiles lie on 1024 bytes");
+// Six stages instead of four in the linear kernel, its outputs straight from registers to make room, gave 8,192 x 4,096 x
+// 4,096 50.0 us for 50.9, and 85 for 58 with a residual: not kept.
+enum Kind { kTiles, kGated };
+constexpr int kPiece = 32 * 128;      // 32 x 64 bf16 of an epilogue warp
+template <int KIND>
+struct Cfg {
+    static constexpr int kStages = KIND == kTiles ? 4 : 6;
+    static constexpr int kTile = KIND == kTiles ? 16 * kPiece : 0;
+    static constexpr int kVec = 16 * 64 * 4;  // a warp's biases: of 64 outputs, or 32 of gate and of up
+    static constexpr int kBars = 512;
+    static constexpr int kSmem = 1024 + kStages * kStage + kTile + kVec + kBars;
+    static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
 constexpr int kTmemCols = 512;        // 256 accumulator columns, 24 scale columns a stage
 constexpr int kScaleCol = 256;
 
@@ -114,12 +120,63 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N])
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-// The larger magnitude, NaN before all
-__device__ __forceinline__ float max_nan(float a, float b)
+// The largest magnitude, NaN before all
+__device__ __forceinline__ float max_nan(float a, float b, float c)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
     return r;
+}
+// Two float32 values in a register pair, one instruction for both: accumulators come from tensor memory in pairs, and
+// with 15 instructions a hidden value the gated kernel's schedulers were the bound.
+struct Pair {
+    uint64_t v;
+    __device__ __forceinline__ Pair() {}
+    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+// Act<ACT>::hidden of two gates and ups (times kGate and kUp, as there)
+template <int ACT>
+__device__ __forceinline__ Pair hidden2(Pair g, Pair u)
+{
+    float g0, g1;
+    g.get(g0, g1);
+    if constexpr (ACT == PMHA_ACT_SILU) {
+        float d0, d1;
+        add2(Pair(ex2(g0), ex2(g1)), Pair(1.f, 1.f)).get(d0, d1);
+        return mul2(mul2(g, Pair(rcp(d0), rcp(d1))), u);
+    } else {
+        const float z0 = fminf(fabsf(g0), 64.f), z1 = fminf(fabsf(g1), 64.f);
+        const Pair z(z0, z1);
+        float t0, t1, e0, e1;
+        fma2(z, Pair(0.3275911f * 0.70710678f, 0.3275911f * 0.70710678f), Pair(1.f, 1.f)).get(t0, t1);
+        const Pair t(rcp(t0), rcp(t1));
+        mul2(mul2(g, g), Pair(-0.72134752f, -0.72134752f)).get(e0, e1);
+        Pair q = fma2(t, Pair(0.5f * 1.061405429f, 0.5f * 1.061405429f), Pair(-0.5f * 1.453152027f, -0.5f * 1.453152027f));
+        q = fma2(t, q, Pair(0.5f * 1.421413741f, 0.5f * 1.421413741f));
+        q = fma2(t, q, Pair(-0.5f * 0.284496736f, -0.5f * 0.284496736f));
+        q = fma2(t, q, Pair(0.5f * 0.254829592f, 0.5f * 0.254829592f));
+        q = mul2(mul2(q, t), Pair(ex2(e0), ex2(e1)));
+        return mul2(fma2(Pair(-z0, -z1), q, Pair(fmaxf(g0, 0.f), fmaxf(g1, 0.f))), u);
+    }
 }
 // Eight values as codes, the first in the lowest half byte
 __device__ __forceinline__ uint32_t mx_word(const float (&f)[8])
@@ -136,14 +193,17 @@ __device__ __forceinline__ uint32_t mx_word(const float (&f)[8])
     return w;
 }
 
-template <bool GATED, int ACT>
+template <int KIND, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(const __grid_constant__ Params p)
 {
+    using C = Cfg<KIND>;
+    constexpr bool GATED = KIND == kGated;
+    constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *tile_s = smem + kStages * kStage;
-    float *vec_s = (float *)(tile_s + kTile);
-    uint64_t *full = (uint64_t *)((uint8_t *)vec_s + kVec);     // [kStages], counted in the even CTA
+    float *vec_s = (float *)(tile_s + C::kTile);
+    uint64_t *full = (uint64_t *)((uint8_t *)vec_s + C::kVec);     // [kStages], counted in the even CTA
     uint64_t *empty = full + kStages;                           // [kStages], in each CTA
     uint64_t *acc_full = empty + kStages;                       // in each CTA
     uint64_t *acc_empty = acc_full + 1;                         // counted in the even CTA
@@ -255,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
         auto rows_of = [&](int tile) { return tile / p.tiles_n * 256 + (int)rank * 128 + quarter * 32; };
         auto column_of = [&](int tile) { return tile % p.tiles_n * kCols + part * (GATED ? 32 : 64); };
         auto fetch_residual = [&](int tile) {
-            if (GATED || !p.has_res || p.plain || lane) return;
+            if (KIND != kTiles || !p.has_res || p.plain || lane) return;
             const int row = rows_of(tile), c = column_of(tile);
             if (row < p.M && c < p.N) {
                 mbar_arrive_expect_tx(smem_u32(&res_full[w]), kPiece);
@@ -297,18 +357,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(empty_bar);
+            // eight outputs: accumulators 8 u and on, biases, and the residual's values
+            auto sums = [&](int u, const uint32_t (&rw)[4]) {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 8 * u + 2 * e;
+                    const float2 b = *reinterpret_cast<const float2 *>(bias + c);
+                    o[e] = pack_bf16(__uint_as_float(v[c >> 5][c & 31]) + b.x + __uint_as_float(rw[e] << 16),
+                                     __uint_as_float(v[c >> 5][(c & 31) + 1]) + b.y + __uint_as_float(rw[e] & 0xffff0000u));
+                }
+                return make_uint4(o[0], o[1], o[2], o[3]);
+            };
             if constexpr (GATED) {
                 float most = 0.f;
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
                     const float4 g = *reinterpret_cast<const float4 *>(bias + c), u = *reinterpret_cast<const float4 *>(bias + 32 + c);
-                    const float gf[4] = {g.x, g.y, g.z, g.w}, uf[4] = {u.x, u.y, u.z, u.w};
+                    const Pair gb[2] = {Pair(g.x, g.y), Pair(g.z, g.w)}, ub[2] = {Pair(u.x, u.y), Pair(u.z, u.w)};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float h = Act<ACT>::hidden(fmaf(__uint_as_float(v[0][c + e]), kg, gf[e]),
-                                                         fmaf(__uint_as_float(v[1][c + e]), ku, uf[e]));
-                        most = max_nan(most, h);
-                        v[0][c + e] = __float_as_uint(h);
+                    for (int e = 0; e < 4; e += 2) {
+                        const Pair gate = fma2(Pair(__uint_as_float(v[0][c + e]), __uint_as_float(v[0][c + e + 1])), Pair(kg, kg), gb[e / 2]);
+                        const Pair up = fma2(Pair(__uint_as_float(v[1][c + e]), __uint_as_float(v[1][c + e + 1])), Pair(ku, ku), ub[e / 2]);
+                        float h0, h1;
+                        hidden2<ACT>(gate, up).get(h0, h1);
+                        most = max_nan(most, h0, h1);
+                        v[0][c + e] = __float_as_uint(h0);
+                        v[0][c + e + 1] = __float_as_uint(h1);
                     }
                 }
                 const uint32_t byte = mx_scale_byte(abs_bits(most));
@@ -318,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                 for (int c = 0; c < 4; ++c) {
                     float f[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[0][8 * c + e]) * inv;
+                    for (int e = 0; e < 8; e += 2)
+                        mul2(Pair(__uint_as_float(v[0][8 * c + e]), __uint_as_float(v[0][8 * c + e + 1])), Pair(inv, inv)).get(f[e], f[e + 1]);
                     code[c] = mx_word(f);
                 }
                 // Straight to memory: 16 bytes of a row each, which meet those of the neighbouring blocks in L2. Blocks
@@ -354,15 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                         const uint4 q = *at;
                         rw[0] = q.x, rw[1] = q.y, rw[2] = q.z, rw[3] = q.w;
                     }
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = 8 * u + 2 * e;
-                        const float2 b = *reinterpret_cast<const float2 *>(bias + c);
-                        o[e] = pack_bf16(__uint_as_float(v[c >> 5][c & 31]) + b.x + __uint_as_float(rw[e] << 16),
-                                         __uint_as_float(v[c >> 5][(c & 31) + 1]) + b.y + __uint_as_float(rw[e] & 0xffff0000u));
-                    }
-                    *at = make_uint4(o[0], o[1], o[2], o[3]);
+                    *at = sums(u, rw);
                 }
                 if (p.plain) {
                     __syncwarp();
@@ -384,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                 }
             }
         }
-        if (!GATED && lane == 0) {
+        if (KIND == kTiles && lane == 0) {
             store_wait_all();  // shared memory outlives its stores, and after an expired wait the residual's copies
             int dummy = 0;
             if (*abort_flag && p.has_res && !p.plain && i)
@@ -427,13 +495,14 @@ bool maps_of(CUtensorMap *codes, CUtensorMap *scale, const Mx &m, int64_t rows, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool GATED, int ACT>
+template <int KIND, int ACT>
 pmha_status launch(Params &p, const char *stage, cudaStream_t s)
 {
+    constexpr int kSmem = Cfg<KIND>::kSmem;
     p.err = device_error_word();
     if (!p.err) return PMHA_ERR_CUDA;
     int pairs = 0;
-    auto kern = k_mx<GATED, ACT>;
+    auto kern = k_mx<KIND, ACT>;
     static std::atomic<int> known[kKnownDevices];
     const pmha_status st = pairs_at_once(kern, kThreads, kSmem, known, &pairs);
     if (st != PMHA_OK) return st;
@@ -477,7 +546,7 @@ pmha_status mx_tc_linear(const MxLinear &a, const char *stage, cudaStream_t s)
         (!p.plain && (!make_tile_map(&p.out, a.out, a.M, a.N, a.N, 2, 32) ||
                       (a.residual && !make_tile_map(&p.res, a.residual, a.M, a.N, a.N, 2, 32)))))
         return map_failed(stage);
-    return launch<false, 0>(p, stage, s);
+    return launch<kTiles, 0>(p, stage, s);
 }
 
 pmha_status mx_tc_gated(const MxGated &a, cudaStream_t s)
@@ -496,7 +565,7 @@ pmha_status mx_tc_gated(const MxGated &a, cudaStream_t s)
     if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.wg, a.F, a.K) ||
         !maps_of(&p.b1, &p.sb1, a.wu, a.F, a.K))
         return map_failed(stage);
-    return a.act == PMHA_ACT_SILU ? launch<true, PMHA_ACT_SILU>(p, stage, s) : launch<true, PMHA_ACT_GELU>(p, stage, s);
+    return a.act == PMHA_ACT_SILU ? launch<kGated, PMHA_ACT_SILU>(p, stage, s) : launch<kGated, PMHA_ACT_GELU>(p, stage, s);
 }
 
 }  // namespace pmha

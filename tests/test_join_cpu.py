@@ -126,7 +126,7 @@ def test_binding_refuses_host_tensors():
     x = torch.zeros(4, 64)
     for call in (lambda: pmha.pmha_checkpoint(x), lambda: pmha.pmha_join(pmha.JoinParams(), x, x),
                  lambda: pmha.pmha_join_backward(pmha.JoinParams(), x, None, None, x),
-                 lambda: pmha.pmha_checkpoint_restore(pmha.Checkpoint(x, x, torch.float32))):
+                 lambda: pmha.Checkpoint(x, x, torch.float32)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
     with pytest.raises(ValueError, match="dout or dsum"):

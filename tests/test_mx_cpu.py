@@ -99,6 +99,8 @@ def test_binding_refuses_host_tensors():
         pmha.pmha_mx_linear(x, x)
     with pytest.raises(TypeError, match="MxTensor"):
         pmha.pmha_ffn_forward_mx(pmha.FfnMxParams(x, x, x), x)
+    with pytest.raises(TypeError, match="Checkpoint"):
+        pmha.pmha_checkpoint_restore(x)
     for shape in ((), (4, 0)):
         with pytest.raises(ValueError, match="one value"):
             pmha.MxTensor(x, x, shape)
