@@ -1127,14 +1127,10 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
         db = dr if alone or not input_grads else torch.empty_like(like)
         dpost = dgate = dpre = None
         if wanted:
-            f32, post, gate, pre = torch.float32, params.post, params.gate, params.pre
-            if post is not None and gate is not None and pre is not None and gate.shape == pre.shape and not width & 3:
-                # one allocation for three rows of whole 16 bytes
-                dpost, dgate, dpre = torch.empty((3, width), dtype=f32, device=like.device).unbind()
-            else:
-                dpost = None if post is None else torch.empty_like(post, dtype=f32)
-                dgate = None if gate is None else torch.empty_like(gate, dtype=f32)
-                dpre = None if pre is None else torch.empty_like(pre, dtype=f32)
+            f32 = torch.float32
+            dpost = None if params.post is None else torch.empty_like(params.post, dtype=f32)
+            dgate = None if params.gate is None else torch.empty_like(params.gate, dtype=f32)
+            dpre = None if params.pre is None else torch.empty_like(params.pre, dtype=f32)
         wp, wn, keep = _scratch(like, need, workspace)
         st = lib.pmha_join_backward(ctypes.byref(p), rows, b, bk, s, dy, ds, None if alone else _ptr(db), _ptr(dr),
                                     _ptr(dpost), _ptr(dgate), _ptr(dpre), wp, wn, _stream_of(dev, stream))

@@ -352,22 +352,24 @@ __global__ void __launch_bounds__(kThreads) k_join_wide(JoinArgs a)
 
 // ---------------------------------------------------------------- 8-bit tensors on their own
 // A lane takes VEC values of a group, 32 / VEC lanes a group; each thread has kAhead groups' values loaded before it uses
-// the first. A tensor whose rows are whole groups is one long row here (`groups` 0: no division by a row's groups).
+// the first. A tensor whose rows are whole groups is one long row here (`groups` 0: no division by a row's groups). Where
+// rows do not lie on 16-byte boundaries a lane's values are still next to one another, and go one by one: with one value a
+// lane every lane does a whole group's sums, 100,000 x 171 took 52 us.
 constexpr int kAhead = 4;
 struct Place {
     long long at, group;  // of the values, of the scale
-    bool in;
+    int left;             // values from there to the end of the row, 0 past the last group
 };
 template <int VEC>
 __device__ __forceinline__ Place place_of(long long g, long long n, unsigned groups, int width)
 {
     const int l = (int)(threadIdx.x % (kGroup / VEC)) * VEC;
-    if (!groups) return {g * kGroup + l, g, g < n};
+    if (!groups) return {g * kGroup + l, g, g < n ? VEC : 0};
     const long long row = n >> 32 ? g / groups : (long long)((unsigned)g / groups);
     const int c = (int)(g - row * groups) * kGroup + l;
-    return {row * width + c, g, g < n && c < width};
+    return {row * width + c, g, g < n ? max(width - c, 0) : 0};
 }
-template <typename T, int VEC>
+template <typename T, int VEC, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_keep(const T *x, long long n, unsigned groups, int width, KeptOut k)
 {
     constexpr int kPer = 32 / (kGroup / VEC);  // groups of a warp
@@ -381,13 +383,26 @@ __global__ void __launch_bounds__(kThreads) k_keep(const T *x, long long n, unsi
             p[i] = place_of<VEC>(g0 + i * step + (threadIdx.x % 32) / (kGroup / VEC), n, groups, width);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[i].v[e] = from_f<T>(0.f);
-            if (p[i].in) load<T, VEC>(x + p[i].at, v[i].v);
+            if (p[i].left) load_some<T, VEC, ALIGNED>(x + p[i].at, p[i].left, v[i]);
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            keep<T, VEC>(KeptOut{k.codes + p[i].at, k.scale + p[i].group}, threadIdx.x % (kGroup / VEC) == 0, p[i].in, v[i]);
+        for (int i = 0; i < kAhead; ++i) {
+            const bool first = threadIdx.x % (kGroup / VEC) == 0;
+            if constexpr (ALIGNED) {
+                keep<T, VEC>(KeptOut{k.codes + p[i].at, k.scale + p[i].group}, first, p[i].left > 0, v[i]);
+            } else {
+                uint32_t w[VEC];
+                const float scale = kept_codes<T, VEC>(v[i], w);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (e < p[i].left) k.codes[p[i].at + e] = (int8_t)w[e];
+                if (first && p[i].left) k.scale[p[i].group] = __float2bfloat16_rn(scale);
+            }
+        }
     }
 }
+// Back to values: without sums to share a lane takes as many as one access holds (at odd widths one; eight of them one by
+// one: 100,000 x 171 43 us instead of 33, its stores lie apart).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_unkeep(Kept k, long long n, unsigned groups, int width, T *out)
 {
@@ -399,21 +414,42 @@ __global__ void __launch_bounds__(kThreads) k_unkeep(Kept k, long long n, unsign
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             p[i] = place_of<VEC>(g0 + i * step, n, groups, width);
-            if (!p[i].in) continue;
+            if (!p[i].left) continue;
             c[i] = *reinterpret_cast<const typename Bytes<VEC>::type *>(k.codes + p[i].at);
             scale[i] = __bfloat162float(k.scale[p[i].group]);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (!p[i].in) continue;
+            if (!p[i].left) continue;
             float f[VEC];
             unkeep<VEC>(c[i], scale[i], f);
-            Vals<T, VEC> v;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) v.v[e] = from_f<T>(f[e]);
+            const Vals<T, VEC> v = rounded<T, VEC>(f);
             store<T, VEC>(out + p[i].at, v.v);
         }
     }
+}
+
+// ---------------------------------------------------------------- host side
+unsigned kept_groups(int64_t width) { return width % kGroup ? (unsigned)groups_of(width) : 0u; }
+// Every thread its kAhead groups once, or as many blocks as are resident
+unsigned kept_grid(int64_t n, int vec)
+{
+    const int64_t threads = (n * (kGroup / vec) + kAhead - 1) / kAhead;
+    return (unsigned)std::min<int64_t>((threads + kThreads - 1) / kThreads, (int64_t)num_sms() * 8);
+}
+pmha_status launch_keep(pmha_dtype dtype, int64_t rows, int64_t width, const void *x, const KeptOut &k, cudaStream_t cs)
+{
+    StageTimer timer("checkpoint", cs);
+    const int64_t n = rows * groups_of(width);
+    auto launch = [&](auto kern, auto *p, int vec) {
+        kern<<<kept_grid(n, vec), kThreads, 0, cs>>>(p, n, kept_groups(width), (int)width, k);
+    };
+    using B = __nv_bfloat16;
+    if (dtype == PMHA_BF16) launch(width % 8 == 0 ? k_keep<B, 8, true> : k_keep<B, 8, false>, (const B *)x, 8);
+    else launch(width % 4 == 0 ? k_keep<float, 4, true> : k_keep<float, 4, false>, (const float *)x, 4);
+    count_launch();
+    PMHA_CUDA_TRY(cudaGetLastError());
+    return PMHA_OK;
 }
 
 }  // namespace
@@ -457,9 +493,16 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
     JoinArgs a{source(branch, branch_kept), source(residual, residual_kept), p.post, p.gate, p.pre, sum, out,
                kept_out(keep_branch), kept_out(keep_residual), rows, p.gate ? rows / p.gates : rows, (int)w,
                p.residual_scale, p.eps};
-    const bool kept = branch_kept || residual_kept || keep_branch || keep_residual;
     const Shape s = join_shape(p.dtype, w);
     cudaStream_t cs = (cudaStream_t)stream;
+    if (s.vec < 4) {
+        // With one or two values a lane the codes cost more on the way than a pass of their own: 100,000 x 171 150 us with
+        // the branch's, without them 52.
+        if (keep_branch && (st = launch_keep(p.dtype, rows, w, branch, a.keep_branch, cs)) != PMHA_OK) return st;
+        if (keep_residual && (st = launch_keep(p.dtype, rows, w, residual, a.keep_res, cs)) != PMHA_OK) return st;
+        a.keep_branch = a.keep_res = KeptOut{nullptr, nullptr};
+    }
+    const bool kept = branch_kept || residual_kept || a.keep_branch.codes || a.keep_res.codes;
     {
         StageTimer timer(kept ? "join_kept" : "join", cs);
         if (s.lpr) {
@@ -487,13 +530,6 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
     return PMHA_OK;
 }
 
-static unsigned kept_groups(int64_t width) { return width % kGroup ? (unsigned)groups_of(width) : 0u; }
-// Every thread its kAhead groups once, or as many blocks as are resident
-static unsigned kept_grid(int64_t n, int vec)
-{
-    const int64_t threads = (n * (kGroup / vec) + kAhead - 1) / kAhead;
-    return (unsigned)std::min<int64_t>((threads + kThreads - 1) / kThreads, (int64_t)num_sms() * 8);
-}
 static pmha_status check_kept(const char *who, pmha_dtype dtype, int64_t rows, int64_t width, const void *x,
                               const pmha_kept *kept)
 {
@@ -517,19 +553,7 @@ pmha_status pmha_checkpoint(pmha_dtype dtype, int64_t rows, int64_t width, const
 {
     pmha_status st = check_kept("pmha_checkpoint", dtype, rows, width, x, kept);
     if (st != PMHA_OK || rows == 0) return st;
-    cudaStream_t cs = (cudaStream_t)stream;
-    {
-        StageTimer timer("checkpoint", cs);
-        dispatch_wide(dtype, shape_of(dtype, width).vec, [&](auto t) {
-            using G = decltype(t);
-            const int64_t n = rows * groups_of(width);
-            k_keep<typename G::type, G::vec><<<kept_grid(n, G::vec), kThreads, 0, cs>>>(
-                (const typename G::type *)x, n, kept_groups(width), (int)width, kept_out(kept));
-        });
-    }
-    count_launch();
-    PMHA_CUDA_TRY(cudaGetLastError());
-    return PMHA_OK;
+    return launch_keep(dtype, rows, width, x, kept_out(kept), (cudaStream_t)stream);
 }
 
 pmha_status pmha_checkpoint_restore(pmha_dtype dtype, int64_t rows, int64_t width, const pmha_kept *kept, void *out,

@@ -65,18 +65,25 @@ __device__ __forceinline__ uint32_t kept_code(float v, float scale, float inv)
     }
 }
 
-// Keeps VEC values of a group whose others lie in the neighbouring lanes, at these places; `first`: the group's first
-// lane. Every lane of the warp comes here, those past the width with zeros and in == false.
+// The codes of VEC values of a group whose others lie in the neighbouring lanes, in the low bytes, and the group's scale;
+// every lane of the warp comes here, those without a value with zeros.
 template <typename T, int VEC>
-__device__ __forceinline__ void keep(const KeptOut &at, bool first, bool in, const Vals<T, VEC> &v)
+__device__ __forceinline__ float kept_codes(const Vals<T, VEC> &v, uint32_t (&w)[VEC])
 {
     uint32_t most = most_bits<T, VEC>(v);
 #pragma unroll
     for (int o = kGroup / VEC / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
     const float scale = kept_scale(most), inv = kept_inverse(scale);
-    uint32_t w[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) w[i] = kept_code<T>(to_f<T>(v.v[i]), scale, inv);
+    return scale;
+}
+// Keeps them at these places; `first`: the group's first lane, which writes the scale.
+template <typename T, int VEC>
+__device__ __forceinline__ void keep(const KeptOut &at, bool first, bool in, const Vals<T, VEC> &v)
+{
+    uint32_t w[VEC];
+    const float scale = kept_codes<T, VEC>(v, w);
     if (!in) return;
     *reinterpret_cast<typename Bytes<VEC>::type *>(at.codes) = low_bytes<VEC>(w);
     if (first) *at.scale = __float2bfloat16_rn(scale);

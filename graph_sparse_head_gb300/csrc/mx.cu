@@ -20,13 +20,15 @@ namespace {
 // ---------------------------------------------------------------- quantisation
 // A block of threads takes a scale tile, 128 rows by 128 columns: a lane VEC values, 32 / VEC lanes a block of 32. Some
 // rows' values are loaded before the first of them is used; the scales are gathered in shared memory and written as one
-// piece, zeros for blocks and rows that are not there. Bound by memory.
-template <typename T, int VEC>
+// piece, zeros for blocks and rows that are not there. Where rows do not lie on 16-byte boundaries a lane's values go one by
+// one, but stay next to one another: one value a lane made every lane do a whole block's sums (100,000 x 171 62 us).
+// Bound by memory: 320,000 x 128 bf16 in 20 us, 5.0 TB/s.
+template <typename T, int VEC, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long rows, int width, int tiles, uint8_t *codes,
                                                           uint8_t *scale)
 {
     constexpr int kLanes = 32 / VEC, kRow = 4 * kLanes, kRows = kThreads / kRow;  // lanes of a row, rows of a pass
-    constexpr int kAhead = 128 / kRows < 8 ? 128 / kRows : 8;
+    constexpr int kAhead = ALIGNED ? 8 : 4;
     __shared__ __align__(16) uint8_t bytes[512];
     tcu::grid_dependents_may_start();
     const long long row0 = (long long)(blockIdx.x / (unsigned)tiles) * 128;
@@ -35,45 +37,34 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long 
     const bool block = tile * 4 + k < blocks;
     for (int i = threadIdx.x; i < 128; i += kThreads) ((uint32_t *)bytes)[i] = 0;
     __syncthreads();
-    const int r_end = (int)min(128ll, rows - row0);
-    for (int r0 = threadIdx.x / 32 * 32 / kRow; r0 < r_end; r0 += kAhead * kRows) {  // whole warps walk
+    const int r_end = (int)min(128ll, rows - row0), r_first = (int)threadIdx.x / kRow;
+    const int r_warp = (int)(threadIdx.x / 32 * 32) / kRow;  // whole warps walk
+    for (int p0 = 0; p0 + r_warp < r_end; p0 += kAhead * kRows) {
         Vals<T, VEC> v[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int r = (int)threadIdx.x / kRow + (r0 - (int)(threadIdx.x / 32 * 32 / kRow)) + i * kRows;
+            const int r = p0 + i * kRows + r_first;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[i].v[e] = from_f<T>(0.f);
-            if (r < r_end && c < width) load<T, VEC>(x + (row0 + r) * width + c, v[i].v);
+            if (r < r_end && c < width) load_some<T, VEC, ALIGNED>(x + (row0 + r) * width + c, width - c, v[i]);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int r = (int)threadIdx.x / kRow + (r0 - (int)(threadIdx.x / 32 * 32 / kRow)) + i * kRows;
+            const int r = p0 + i * kRows + r_first;
             uint32_t most = most_bits<T, VEC>(v[i]);
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
             const uint32_t byte = mx_scale_byte(most);
-            const bool in = block && r < r_end;
             const float inv = mx_inverse(byte);
-            uint8_t *dst = codes + ((row0 + r) * blocks + tile * 4 + k) * 16;
-            if constexpr (VEC == 8) {
-                uint32_t w = 0;
+            if (!(block && r < r_end)) continue;
+            uint32_t w = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w |= mx_byte(to_f<T>(v[i].v[2 * e]) * inv, to_f<T>(v[i].v[2 * e + 1]) * inv) << (8 * e);
-                if (in) *reinterpret_cast<uint32_t *>(dst + l * 4) = w;
-            } else if constexpr (VEC == 4) {
-                const uint32_t w = mx_byte(to_f<T>(v[i].v[0]) * inv, to_f<T>(v[i].v[1]) * inv) |
-                                   mx_byte(to_f<T>(v[i].v[2]) * inv, to_f<T>(v[i].v[3]) * inv) << 8;
-                if (in) *reinterpret_cast<uint16_t *>(dst + l * 2) = (uint16_t)w;
-            } else if constexpr (VEC == 2) {
-                const uint32_t w = mx_byte(to_f<T>(v[i].v[0]) * inv, to_f<T>(v[i].v[1]) * inv);
-                if (in) dst[l] = (uint8_t)w;
-            } else {
-                const float f = to_f<T>(v[i].v[0]) * inv, next = __shfl_down_sync(kFull, f, 1);
-                const uint32_t w = mx_byte(f, next);
-                if (in && l % 2 == 0) dst[l / 2] = (uint8_t)w;
-            }
-            if (l == 0 && in) bytes[(r & 31) * 16 + (r >> 5) * 4 + k] = (uint8_t)byte;
+            for (int e = 0; e < VEC / 2; ++e)
+                w |= mx_byte(to_f<T>(v[i].v[2 * e]) * inv, to_f<T>(v[i].v[2 * e + 1]) * inv) << (8 * e);
+            uint8_t *dst = codes + ((row0 + r) * blocks + tile * 4 + k) * 16 + l * (VEC / 2);
+            if constexpr (VEC == 8) *reinterpret_cast<uint32_t *>(dst) = w;
+            else *reinterpret_cast<uint16_t *>(dst) = (uint16_t)w;
+            if (l == 0) bytes[(r & 31) * 16 + (r >> 5) * 4 + k] = (uint8_t)byte;
         }
     }
     __syncthreads();
@@ -347,12 +338,16 @@ pmha_status pmha_mx_quantize(pmha_dtype dtype, int64_t rows, int64_t width, cons
     cudaStream_t cs = (cudaStream_t)stream;
     {
         StageTimer timer("mx_quantize", cs);
-        dispatch_wide(dtype, shape_of(dtype, width).vec, [&](auto t) {
-            using G = decltype(t);
-            const int64_t tiles = (mx_blocks(width) + 3) / 4;
-            k_mx_quantize<typename G::type, G::vec><<<(unsigned)((rows + 127) / 128 * tiles), kThreads, 0, cs>>>(
-                (const typename G::type *)x, rows, (int)width, (int)tiles, (uint8_t *)out->codes, (uint8_t *)out->scale);
-        });
+        const int64_t tiles = (mx_blocks(width) + 3) / 4;
+        const unsigned grid = (unsigned)((rows + 127) / 128 * tiles);
+        auto launch = [&](auto kern, auto *p) {
+            kern<<<grid, kThreads, 0, cs>>>(p, rows, (int)width, (int)tiles, (uint8_t *)out->codes, (uint8_t *)out->scale);
+        };
+        using B = __nv_bfloat16;
+        if (dtype == PMHA_BF16)
+            launch(width % 8 == 0 ? k_mx_quantize<B, 8, true> : k_mx_quantize<B, 8, false>, (const B *)x);
+        else
+            launch(width % 4 == 0 ? k_mx_quantize<float, 4, true> : k_mx_quantize<float, 4, false>, (const float *)x);
     }
     count_launch();
     PMHA_CUDA_TRY(cudaGetLastError());

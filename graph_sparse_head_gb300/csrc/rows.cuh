@@ -74,6 +74,20 @@ __device__ __forceinline__ uint32_t most_bits(const Vals<T, VEC> &v)
         return most;
     }
 }
+// VEC consecutive values of a row that need not lie on a boundary: one by one, those past the row's end zeros (left alone).
+// The same cache line serves a lane's values and its neighbours'.
+template <typename T, int VEC, bool ALIGNED>
+__device__ __forceinline__ void load_some(const T *p, int left, Vals<T, VEC> &v)
+{
+    if constexpr (ALIGNED) {
+        load<T, VEC>(p, v.v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < left) v.v[i] = p[i];
+    }
+}
+
 // The low bytes of VEC words
 template <int VEC>
 __device__ __forceinline__ typename Bytes<VEC>::type low_bytes(const uint32_t (&w)[VEC])
