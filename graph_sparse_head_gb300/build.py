@@ -22,7 +22,7 @@ SOURCES = ["api.cu", "csr.cu", "gemm_simt.cu", "gemm_tc.cu", "edge_attn.cu", "ed
            "dense_attn.cu", "backward.cu", "bwd_ring.cu", "noalloc.cu", "heavy.cu", "norm.cu", "join.cu", "join_bwd.cu", "clip.cu", "ffn.cu", "ffn_tc.cu", "ffn_fused.cu", "ffn_f32.cu", "ffn_small.cu", "mx.cu", "mx_tc.cu"]
 HEADERS = [os.path.join(CSRC, "pmha_internal.h"), os.path.join(CSRC, "edge_stream.cuh"), os.path.join(CSRC, "edge_ring.cuh"), os.path.join(CSRC, "edge_out.cuh"), os.path.join(CSRC, "bwd_stream.cuh"),
            os.path.join(CSRC, "tc_util.cuh"), os.path.join(CSRC, "tc_pair.cuh"),
-           os.path.join(CSRC, "rows.cuh"), os.path.join(CSRC, "kept.cuh"), os.path.join(CSRC, "join.cuh"), os.path.join(CSRC, "mx.cuh"), os.path.join(CSRC, "ffn_internal.h"), os.path.join(CSRC, "ffn_math.cuh"),
+           os.path.join(CSRC, "rows.cuh"), os.path.join(CSRC, "kept.cuh"), os.path.join(CSRC, "join.cuh"), os.path.join(CSRC, "mx.cuh"), os.path.join(CSRC, "pair.cuh"), os.path.join(CSRC, "ffn_internal.h"), os.path.join(CSRC, "ffn_math.cuh"),
            os.path.join(ROOT, "include", "pmha.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -1,5 +1,6 @@
 // Backward pass of the join (join.cu has the formulas).
 #include "join.cuh"
+#include "pair.cuh"
 #include "tc_pair.cuh"
 
 namespace pmha {
@@ -52,29 +53,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
     const float inv_width = 1.f / (float)a.width;
     const int groups = (a.width + kGroup - 1) / kGroup;
     bool col[NV];
-    V wpre[NV];
-    float wz[N], q[N], pb[N];  // post times gate; sums of dout sum r and of D branch r_b
+    Values<N> wp, wz, q, pb;  // pre; post times gate; sums of dout sum r and of D branch r_b
+    float wf[2][N];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = l * VEC + j * kPiece;
         col[j] = c < a.width;
-        V post, gt;
+        V pre, post, gt;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            wpre[j].v[i] = post.v[i] = gt.v[i] = from_f<T>(1.f);
-            q[j * VEC + i] = pb[j * VEC + i] = 0.f;
-        }
+        for (int i = 0; i < VEC; ++i) pre.v[i] = post.v[i] = gt.v[i] = from_f<T>(1.f);
         if (col[j]) {
-            if (a.pre) load<T, VEC>((const T *)a.pre + c, wpre[j].v);
+            if (a.pre) load<T, VEC>((const T *)a.pre + c, pre.v);
             if (a.post) load<T, VEC>((const T *)a.post + c, post.v);
             if (a.gate) load<T, VEC>((const T *)a.gate + (long long)gate * a.width + c, gt.v);
         }
         float g[VEC];
-        widen<T, VEC>(post, wz + j * VEC);
+        widen<T, VEC>(pre, wf[0] + j * VEC);
+        widen<T, VEC>(post, wf[1] + j * VEC);
         widen<T, VEC>(gt, g);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) wz[j * VEC + i] *= g[i];
+        for (int i = 0; i < VEC; ++i) wf[1][j * VEC + i] *= g[i];
     }
+    wp = Values<N>(wf[0]);
+    wz = Values<N>(wf[1]);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) q.p[i] = pb.p[i] = Pair(0.f, 0.f);
     // a warp's threads walk together: row0 is the first of its rows
     const unsigned sub = LPR < 32 ? (threadIdx.x & 31) / LPR : 0;
     const unsigned row_first = gate * (unsigned)a.per_gate + blockIdx.x % (unsigned)a.blocks_per_gate * kRows +
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
     for (unsigned row0 = row_first; row0 < end; row0 += step, at += stride, sat += (long long)step * groups) {
         const unsigned row = row0 + sub;
         const bool live = row < end;
-        float D[N], f[N], b[N], g[N], da[N];
+        float D[N], f[N], b[N], g[N];
         if constexpr (kRing > 0) {
             fetch(row + (kRing - 1) * step, at + (kRing - 1) * stride, slot ? slot - 1 : kRing - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
@@ -173,21 +176,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
         // the squares' sums of sum and branch and the sum of dout pre sum, together
         float sc = 1.f, scb = 1.f;
         float t[3];
+        Values<N> vf, vb, vd(D);
+        const Values<N> vg(g), va = times(vg, wp);
         auto stats = [&]() {
-            t[0] = squares_of(f);
-            t[1] = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) t[1] = fmaf(da[i], f[i], t[1]);
-            t[2] = a.post ? squares_of(b) : 0.f;
+            vf = Values<N>(f);
+            vb = Values<N>(b);
+            t[0] = Values<N>::dot(vf, vf);
+            t[1] = Values<N>::dot(va, vf);
+            t[2] = a.post ? Values<N>::dot(vb, vb) : 0.f;
             team_reduce<LPR, false>(t, sh, turn);
         };
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float w[VEC];
-            widen<T, VEC>(wpre[j], w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) da[j * VEC + i] = g[j * VEC + i] * w[i];
-        }
         stats();
         const bool over = t[0] > kMostSquares || !(fabsf(t[1]) <= kMostSquares), overb = t[2] > kMostSquares;
         if (__any_sync(kFull, over || overb)) {  // a team of warps comes here together: they have one row
@@ -198,27 +196,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
         if (a.dy) {
             const float r = rsqrtf(fmaf(t[0], inv_width, a.eps * sc * sc));  // of sum sc
             const float k = t[1] * inv_width * r * r, rd = r * sc;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                q[n] = fmaf(g[n], f[n] * r, q[n]);
-                D[n] = fmaf(rd, fmaf(-f[n], k, da[n]), D[n]);
-            }
+            q = times_plus(vg, times(vf, r), q);
+            vd = times_plus(times_plus(vf, -k, va), rd, vd);
         }
         float rb = 1.f;
         if (a.post) {
             rb = rsqrtf(fmaf(t[2], inv_width, a.eps * scb * scb));
-#pragma unroll
-            for (int i = 0; i < N; ++i) b[i] *= rb;
+            vb = times(vb, rb);
         }
-        float bs[1] = {0.f};
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            pb[n] = fmaf(D[n], b[n], pb[n]);
-            da[n] = D[n] * wz[n];
-            bs[0] = fmaf(da[n], b[n], bs[0]);
-            D[n] *= a.alpha;
-        }
+        pb = times_plus(vd, vb, pb);
+        Values<N> vz = times(vd, wz);
         if (a.dres) {
+            times(vd, a.alpha).get(D);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const V o = rounded<T, VEC>(*reinterpret_cast<float (*)[VEC]>(D + j * VEC));
@@ -227,14 +216,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
         }
         if (!a.dbranch) continue;
         if (a.post) {
+            float bs[1] = {Values<N>::dot(vz, vb)};
             team_reduce<LPR, false>(bs, sh, turn);
-            const float k = bs[0] * inv_width, rd = rb * scb;
-#pragma unroll
-            for (int i = 0; i < N; ++i) da[i] = rd * fmaf(-b[i], k, da[i]);
+            vz = times(times_plus(vb, -bs[0] * inv_width, vz), rb * scb);
         }
+        vz.get(D);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const V o = rounded<T, VEC>(*reinterpret_cast<float (*)[VEC]>(da + j * VEC));
+            const V o = rounded<T, VEC>(*reinterpret_cast<float (*)[VEC]>(D + j * VEC));
             if (live && col[j]) store<T, VEC>((T *)a.dbranch + at + j * kPiece, o.v);
         }
     }
@@ -243,7 +232,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
     // a warp's rows, then the warps (or teams of warps) in order, all at once through shared memory
     constexpr int kTeam = LPR < 32 ? 32 : LPR, kTeams = kThreads / kTeam;
     const int team = threadIdx.x / kTeam;
-    auto put = [&](float (&v)[N], float *part) {
+    auto put = [&](const Values<N> &sums, float *part) {
+        float v[N];
+        sums.get(v);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i)

@@ -9,6 +9,7 @@
 // an E4M3 value by 0.025. Codes are those of exact arithmetic, ties to even.
 #pragma once
 
+#include "pair.cuh"
 #include "rows.cuh"
 
 namespace pmha {
@@ -97,7 +98,15 @@ __device__ __forceinline__ void unkeep(const typename Bytes<VEC>::type &codes, f
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const uint32_t b = __byte_perm(w[i / 4] ^ 0x80808080u, 0x4b000000u, 0x7540 + (i & 3));
-        v[i] = __fsub_rn(__uint_as_float(b), 8388736.f) * scale;
+        v[i] = __uint_as_float(b);
+    }
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2)
+            mul2(add2(Pair(v[i], v[i + 1]), Pair(-8388736.f, -8388736.f)), Pair(scale, scale)).get(v[i], v[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = __fsub_rn(v[i], 8388736.f) * scale;
     }
 }
 template <int VEC>

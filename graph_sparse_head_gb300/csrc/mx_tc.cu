@@ -24,6 +24,7 @@
 
 #include "ffn_math.cuh"
 #include "mx.cuh"
+#include "pair.cuh"
 #include "tc_pair.cuh"
 
 namespace pmha {
@@ -127,33 +128,8 @@ __device__ __forceinline__ float max_nan(float a, float b, float c)
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
     return r;
 }
-// Two float32 values in a register pair, one instruction for both: accumulators come from tensor memory in pairs, and
-// with 15 instructions a hidden value the gated kernel's schedulers were the bound.
-struct Pair {
-    uint64_t v;
-    __device__ __forceinline__ Pair() {}
-    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ __forceinline__ void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
-{
-    Pair d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return d;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b)
-{
-    Pair d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b)
-{
-    Pair d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-// Act<ACT>::hidden of two gates and ups (times kGate and kUp, as there)
+// Act<ACT>::hidden of two gates and ups (times kGate and kUp, as there). Accumulators come from tensor memory in register
+// pairs; with 15 instructions a hidden value the gated kernel's schedulers were the bound.
 template <int ACT>
 __device__ __forceinline__ Pair hidden2(Pair g, Pair u)
 {
