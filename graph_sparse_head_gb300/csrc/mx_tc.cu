@@ -56,7 +56,7 @@ constexpr int kScaleCol = 256;
 struct Params {
     CUtensorMap a, b0, b1, sa, sb0, sb1, out, res;
     int M, N;               // tokens, outputs (gated: hidden width)
-    int n_tiles, tiles_n, kb;
+    int n_tiles, tiles_n, kb, k64;  // K blocks of 256 columns, products of 64
     const __nv_bfloat16 *bias0, *bias1;
     const __nv_bfloat16 *res_p;  // plain: row-wise outputs without TMA
     __nv_bfloat16 *out_p;
@@ -253,21 +253,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + kBox, ssb = ssa + kSfA;
+                    const int steps = min(4, p.k64 - 4 * kb);  // products of 64 columns, up to the width's end
                     if (one) {
                         // scale columns of this stage: 2 x 4 of the tokens, then 2 x 8 of the weights (128 columns
                         // of K, then 256 rows)
                         const uint32_t ca = tmem + (uint32_t)(kScaleCol + 24 * stage), cb = ca + 8;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            copy_scales(ca + 4 * h, scale_desc(ssa + 512 * h));
-                            copy_scales(cb + 8 * h, scale_desc(ssb + 512 * h));
-                            copy_scales(cb + 8 * h + 4, scale_desc(ssb + 1024 + 512 * h));
-                        }
                         const uint64_t da = smem_desc(sa), db = smem_desc(sb);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 64 values = 32 bytes along K = 2 in the address field
+                        for (int k = 0; k < 4; ++k) {  // 64 values = 32 bytes along K = 2 in the address field
+                            if (k >= steps) break;
+                            if (k % 2 == 0) {
+                                const int h = k / 2;
+                                copy_scales(ca + 4 * h, scale_desc(ssa + 512 * h));
+                                copy_scales(cb + 8 * h, scale_desc(ssb + 512 * h));
+                                copy_scales(cb + 8 * h + 4, scale_desc(ssb + 1024 + 512 * h));
+                            }
                             mma_mx(tmem, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), k & 1 ? idesc_mx(2) : idesc_mx(0),
                                    ca + 4 * (k >> 1), cb + 8 * (k >> 1), kb > 0 || k > 0 ? 1u : 0u);
+                        }
                         mma_commit_pair(smem_u32(&empty[stage]));
                     }
                     __syncwarp();
@@ -497,6 +500,7 @@ pmha_status tiles_of(Params &p, int64_t M, int64_t N, int64_t K, int cols, const
     p.M = (int)M, p.N = (int)N;
     p.tiles_n = (int)ceil_div(N, cols);
     p.kb = (int)ceil_div(K, 256);
+    p.k64 = (int)ceil_div(K, 64);
     const int64_t tiles = ceil_div(M, 256) * p.tiles_n;
     if (tiles > 0x3fffffff) {
         set_error("%s: %lld tiles exceed the 32-bit tile index", stage, (long long)tiles);
