@@ -516,7 +516,9 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
                 static_assert(smem <= 48 * 1024, "what a launch may have without asking");
                 if (kept) k_join<T, G::vec, G::nv, G::lpr, true, 1><<<(unsigned)std::min(steps, all), kThreads, smem, cs>>>(a);
                 else if (few) k_join<T, G::vec, G::nv, G::lpr, false, 1><<<(unsigned)steps, kThreads, smem, cs>>>(a);
-                else k_join<T, G::vec, G::nv, G::lpr, false, kFewSteps><<<(unsigned)((steps + kFewSteps - 1) / kFewSteps), kThreads, smem, cs>>>(a);
+                else
+                    k_join<T, G::vec, G::nv, G::lpr, false, kFewSteps>
+                        <<<(unsigned)((steps + kFewSteps - 1) / kFewSteps), kThreads, smem, cs>>>(a);
             });
         } else {
             dispatch_wide(p.dtype, s.vec, [&](auto t) {

@@ -1,17 +1,20 @@
 // Products of matrices in microscaled 4 bits (mx.cuh) on the tensor cores (sm_103a), one kernel shape for two:
 //
 //   linear  y = x W^T + bias + residual                          tile 256 tokens x 256 outputs, bf16
-//   gated   h = act(x Wg^T + bg) * (x Wu^T + bu), in 4 bits      tile 256 tokens x 128 hidden, gate and up side by side
+//   gated   h = act(x Wg^T + bg) * (x Wu^T + bu), in 4 bits      tile 256 tokens x 64 hidden, gate and up side by side
 //
 // Two CTAs form a pair (tc_pair.cuh). Each has 18 warps: warp 0 copies stages of
 // 256 columns of codes (128 bytes a row, two values a byte) and the scale tiles that belong to them by TMA, warp
 // 1 of the even CTA copies the scale tiles to tensor memory (tcgen05.cp, into both CTAs) and issues tcgen05.mma
-// kind::mxf4, whose scaling by block is the hardware's; sixteen warps turn accumulators into outputs. Accumulators of 256
-// columns and the scales of four stages fill tensor memory, so there is one set: each epilogue thread takes all of its
-// accumulators into registers (64) and hands the set back at once, the next tile's products run under its arithmetic.
+// kind::mxf4, whose scaling by block is the hardware's; sixteen warps turn accumulators into outputs. Linear: 256
+// accumulator columns and the scales of four stages fill tensor memory, there is one set; an epilogue thread takes all of its
+// accumulators into registers (64) and hands the set back at once, so that the next products run under its arithmetic. Gated:
+// three sets of 64 gates and 64 ups, and two teams of eight warps that take the tiles in turn, one team's waits under the
+// other's special functions, 16 columns' accumulators on their way while 16 are used (320,000 x 128 x 512 in 98 us; with one
+// set of 128 + 128, one team and all accumulators in registers at once 112).
 // Epilogue warps go their own ways: each has its 32 rows' share of the columns, its own piece of shared memory, its own
 // copies of the residual and of the result, and no barrier with the others. (With a barrier for all sixteen around each
-// step 320,000 x 128 x 512 gated took 152 us.)
+// step the same took 152 us.)
 //
 // Ragged sizes need no code of their own: TMA fills rows and columns past a
 // tensor's end with zeros (codes and scale tiles) and does not store them. Only
@@ -34,24 +37,33 @@ using namespace tcu;
 constexpr int kThreads = 64 + 512;
 constexpr int kBox = 128 * 128;       // bytes of a tile of 128 rows of 128 bytes
 constexpr int kSfA = 2 * 512;         // scale tiles of a stage: 128 rows x 256 columns
-constexpr int kSfB = 4 * 512;         // 256 rows x 256 columns
-constexpr int kStage = 2 * kBox + kSfA + kSfB;
-static_assert(kStage % 1024 == 0, "swizzled tiles lie on 1024 bytes");
-// Six stages instead of four in the linear kernel, its outputs straight from registers to make room, gave 8,192 x 4,096 x
-// 4,096 50.0 us for 50.9, and 85 for 58 with a residual: not kept.
+constexpr int kSfB = 4 * 512;         // 256 rows x 256 columns, or 128 each of gate and up
+// Not kept in the linear kernel: six stages instead of four, its outputs straight from registers to make room (8,192 x
+// 4,096 x 4,096 50.0 us for 50.9, with a residual 85 for 58); two stages and two output pieces a warp for rows of up to 512
+// columns (320,000 x 128 -> 384 with a residual 101 us for 105, without one 60 for 58).
 enum Kind { kTiles, kGated };
 constexpr int kPiece = 32 * 128;      // 32 x 64 bf16 of an epilogue warp
 template <int KIND>
 struct Cfg {
-    static constexpr int kStages = KIND == kTiles ? 4 : 6;
+    static constexpr bool kGate = KIND == kGated;
+    static constexpr int kCols = kGate ? 64 : 256;      // output columns of a tile: N of a product
+    static constexpr int kOps = kGate ? 2 : 1;          // products side by side
+    static constexpr int kRowsB = kCols / 2;            // weight rows that a CTA brings to a product
+    static constexpr int kB = kOps * kRowsB * 128;
+    static constexpr int kStage = kBox + kB + kSfA + kSfB;
+    static_assert(kStage % 1024 == 0, "swizzled tiles lie on 1024 bytes");
+    static constexpr int kAccs = kGate ? 3 : 1, kAccCols = kOps * kCols;
+    static constexpr int kTeams = kGate ? 2 : 1;        // of epilogue warps, which take tiles in turn
+    static constexpr int kStages = kGate ? 5 : 4;
+    static constexpr int kScaleCol = kAccs * kAccCols;  // then 24 scale columns a stage
+    static_assert(kScaleCol + 24 * kStages <= 512, "tensor memory");
     static constexpr int kTile = KIND == kTiles ? 16 * kPiece : 0;
     static constexpr int kVec = 16 * 64 * 4;  // a warp's biases: of 64 outputs, or 32 of gate and of up
     static constexpr int kBars = 512;
     static constexpr int kSmem = 1024 + kStages * kStage + kTile + kVec + kBars;
     static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
-constexpr int kTmemCols = 512;        // 256 accumulator columns, 24 scale columns a stage
-constexpr int kScaleCol = 256;
+constexpr int kTmemCols = 512;
 
 struct Params {
     CUtensorMap a, b0, b1, sa, sb0, sb1, out, res;
@@ -95,11 +107,11 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
 }
-// kind::mxf4: A and B E2M1 (1 at bits 7-9 and 10-12), 256 x 256 (N >> 3 at bits 17-22, M >> 7 at bits 27-28), E8M0
+// kind::mxf4: A and B E2M1 (1 at bits 7-9 and 10-12), 256 x N (N >> 3 at bits 17-22, M >> 7 at bits 27-28), E8M0
 // scales (bit 23); sf: which of a column's byte pairs holds the scales, 0 or 2 (bits 4-5 for B, 29-30 for A).
-__host__ __device__ constexpr uint32_t idesc_mx(uint32_t sf)
+__host__ __device__ constexpr uint32_t idesc_mx(uint32_t n, uint32_t sf)
 {
-    return (sf << 4) | (1u << 7) | (1u << 10) | (32u << 17) | (1u << 23) | (2u << 27) | (sf << 29);
+    return (sf << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | (2u << 27) | (sf << 29);
 }
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -174,16 +186,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
 {
     using C = Cfg<KIND>;
     constexpr bool GATED = KIND == kGated;
-    constexpr int kStages = C::kStages;
+    constexpr int kStages = C::kStages, kStage = C::kStage, kCols = C::kCols, kAccs = C::kAccs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *tile_s = smem + kStages * kStage;
     float *vec_s = (float *)(tile_s + C::kTile);
     uint64_t *full = (uint64_t *)((uint8_t *)vec_s + C::kVec);     // [kStages], counted in the even CTA
     uint64_t *empty = full + kStages;                           // [kStages], in each CTA
-    uint64_t *acc_full = empty + kStages;                       // in each CTA
-    uint64_t *acc_empty = acc_full + 1;                         // counted in the even CTA
-    uint64_t *mma_done = acc_empty + 1;
+    uint64_t *acc_full = empty + kStages;                       // [kAccs], in each CTA
+    uint64_t *acc_empty = acc_full + kAccs;                     // [kAccs], counted in the even CTA
+    uint64_t *mma_done = acc_empty + kAccs;
     uint64_t *res_full = mma_done + 1;                          // [16], of the epilogue warps
     uint32_t *tmem_holder = (uint32_t *)(res_full + 16);
     volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
@@ -192,15 +204,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-    constexpr int kCols = GATED ? 128 : 256;  // output columns of a tile
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        mbar_init(smem_u32(acc_full), 1);
-        mbar_init(smem_u32(acc_empty), 32);  // the epilogue warps of both CTAs
+        for (int i = 0; i < kAccs; ++i) {
+            mbar_init(smem_u32(&acc_full[i]), 1);
+            mbar_init(smem_u32(&acc_empty[i]), 32 / C::kTeams);  // a team's warps of both CTAs
+        }
         mbar_init(smem_u32(mma_done), 1);
         for (int w = 0; w < 16; ++w) mbar_init(smem_u32(&res_full[w]), 1);
         *abort_flag = 0;
@@ -228,14 +241,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                 const uint32_t fb = map_rank(smem_u32(&full[stage]), 0);
                 if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * kStage);
                 *armed = made + 1;
-                const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + kBox, ssb = ssa + kSfA;
+                const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + C::kB, ssb = ssa + kSfA;
                 tma_load_2d_pair(sa, &p.a, kb * 128, rows * 128, fb);
-                if constexpr (GATED) tma_load_2d_pair(sb, rank ? &p.b1 : &p.b0, kb * 128, n * 128, fb);
-                else tma_load_2d_pair(sb, &p.b0, kb * 128, n * 256 + (int)rank * 128, fb);
+                const int row = n * kCols + (int)rank * C::kRowsB;
+                tma_load_2d_pair(sb, &p.b0, kb * 128, row, fb);
+                if constexpr (GATED) tma_load_2d_pair(sb + C::kRowsB * 128, &p.b1, kb * 128, row, fb);
                 tma_load_3d_pair(ssa, &p.sa, 0, kb * 2, rows, fb);
-                // the scales of all 256 columns, in both CTAs
-                tma_load_3d_pair(ssb, &p.sb0, 0, kb * 2, GATED ? n : n * 2, fb);
-                tma_load_3d_pair(ssb + 1024, GATED ? &p.sb1 : &p.sb0, 0, kb * 2, GATED ? n : n * 2 + 1, fb);
+                // the scales of all columns, in both CTAs: two tiles of the weights', or the tiles of gate and of up in
+                // which the 64 columns lie
+                tma_load_3d_pair(ssb, &p.sb0, 0, kb * 2, GATED ? n / 2 : n * 2, fb);
+                tma_load_3d_pair(ssb + 1024, GATED ? &p.sb1 : &p.sb0, 0, kb * 2, GATED ? n / 2 : n * 2 + 1, fb);
             }
         }
     } else if (warp == 1) {
@@ -245,19 +260,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             uint32_t used = 0, i = 0;
             bool ok = true;
             for (int tile = pair; tile < p.n_tiles && ok; tile += n_pairs, ++i) {
-                if (!wait_bar(smem_u32(acc_empty), (i & 1u) ^ 1u, abort_flag, p.err)) break;
+                const int acc = (int)(i % kAccs);
+                if (!wait_bar(smem_u32(&acc_empty[acc]), ((i / kAccs) & 1u) ^ 1u, abort_flag, p.err)) break;
                 tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * C::kAccCols);
+                // of a scale tile's four columns of 32 rows, the first of this tile's
+                const uint32_t half = GATED ? 2u * ((uint32_t)(tile % p.tiles_n) & 1u) : 0u;
                 for (int kb = 0; kb < p.kb; ++kb, ++used) {
                     const int stage = (int)(used % kStages);
                     ok = wait_bar(smem_u32(&full[stage]), (used / kStages) & 1u, abort_flag, p.err);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + kBox, ssb = ssa + kSfA;
+                    const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + C::kB, ssb = ssa + kSfA;
                     const int steps = min(4, p.k64 - 4 * kb);  // products of 64 columns, up to the width's end
                     if (one) {
                         // scale columns of this stage: 2 x 4 of the tokens, then 2 x 8 of the weights (128 columns
-                        // of K, then 256 rows)
-                        const uint32_t ca = tmem + (uint32_t)(kScaleCol + 24 * stage), cb = ca + 8;
+                        // of K, then 256 rows, or 128 of gate and of up)
+                        const uint32_t ca = tmem + (uint32_t)(C::kScaleCol + 24 * stage), cb = ca + 8;
                         const uint64_t da = smem_desc(sa), db = smem_desc(sb);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {  // 64 values = 32 bytes along K = 2 in the address field
@@ -268,14 +287,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                                 copy_scales(cb + 8 * h, scale_desc(ssb + 512 * h));
                                 copy_scales(cb + 8 * h + 4, scale_desc(ssb + 1024 + 512 * h));
                             }
-                            mma_mx(tmem, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), k & 1 ? idesc_mx(2) : idesc_mx(0),
-                                   ca + 4 * (k >> 1), cb + 8 * (k >> 1), kb > 0 || k > 0 ? 1u : 0u);
+#pragma unroll
+                            for (int o = 0; o < C::kOps; ++o)
+                                mma_mx(d + o * kCols, da + (uint64_t)(2 * k), db + (uint64_t)(o * C::kRowsB * 8 + 2 * k),
+                                       k & 1 ? idesc_mx(kCols, 2) : idesc_mx(kCols, 0), ca + 4 * (k >> 1),
+                                       cb + 8 * (k >> 1) + 4 * o + half, kb > 0 || k > 0 ? 1u : 0u);
                         }
                         mma_commit_pair(smem_u32(&empty[stage]));
                     }
                     __syncwarp();
                 }
-                if (one && ok) mma_commit_pair(smem_u32(acc_full));
+                if (one && ok) mma_commit_pair(smem_u32(&acc_full[acc]));
                 __syncwarp();
             }
             if (one) mma_commit_pair(smem_u32(mma_done));
@@ -284,10 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
     } else {
-        // ---------------- epilogue: a warp 32 rows and a quarter of a tile's columns
-        const int w = warp - 2, quarter = warp & 3, part = w >> 2;
+        // ---------------- epilogue: a warp 32 rows and 64 accumulator columns of a tile, of which teams take turns
+        const int w = warp - 2, quarter = warp & 3, team = GATED ? w >> 3 : 0, part = (w >> 2) & (GATED ? 1 : 3);
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(GATED ? part * 32 : part * 64);
         const uint32_t empty_bar = map_rank(smem_u32(acc_empty), 0);
+        const int first = pair + team * n_pairs, next = C::kTeams * n_pairs;
         float *bias = vec_s + w * 64;
         uint8_t *piece = tile_s + w * kPiece;
         constexpr float kg = GATED ? Act<ACT>::kGate : 1.f, ku = GATED ? Act<ACT>::kUp : 1.f;
@@ -311,31 +334,34 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             b0 = p.bias0 && c < p.N ? kg * __bfloat162float(p.bias0[c]) : 0.f;
             b1 = second && c2 < p.N ? ku * __bfloat162float(second[c2]) : 0.f;
         };
-        uint32_t i = 0;
-        if (pair < p.n_tiles) {
-            fetch_residual(pair);
-            fetch_bias(pair);
+        uint32_t i = (uint32_t)team;
+        if (first < p.n_tiles) {
+            fetch_residual(first);
+            fetch_bias(first);
         }
-        for (int tile = pair; tile < p.n_tiles; tile += n_pairs, ++i) {
+        for (int tile = first; tile < p.n_tiles; tile += next, i += C::kTeams) {
+            const int acc = (int)(i % kAccs);
             const int row0 = rows_of(tile), c0 = column_of(tile);
             __syncwarp();
             bias[lane] = b0;
             bias[32 + lane] = b1;
             __syncwarp();
-            if (tile + n_pairs < p.n_tiles) fetch_bias(tile + n_pairs);
+            if (tile + next < p.n_tiles) fetch_bias(tile + next);
             // after an expired wait the waits return at once and the loop runs out
-            wait_bar(smem_u32(acc_full), i & 1u, abort_flag, p.err);
+            wait_bar(smem_u32(&acc_full[acc]), (i / kAccs) & 1u, abort_flag, p.err);
             tc_fence_after();
             __syncwarp();
-            uint32_t v[2][32];  // gated: gate and up of 32 hidden columns; else 64 outputs
-            tmem_ld32_nowait(t0, v[0]);
-            tmem_ld32_nowait(t0 + (GATED ? 128u : 32u), v[1]);
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-            pin(v[0]);
-            pin(v[1]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty_bar);
+            uint32_t v[2][32];  // 64 outputs
+            if constexpr (!GATED) {
+                tmem_ld32_nowait(t0 + (uint32_t)(acc * C::kAccCols), v[0]);
+                tmem_ld32_nowait(t0 + (uint32_t)(acc * C::kAccCols + 32), v[1]);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                pin(v[0]);
+                pin(v[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(empty_bar + 8u * (uint32_t)acc);
+            }
             // eight outputs: accumulators 8 u and on, biases, and the residual's values
             auto sums = [&](int u, const uint32_t (&rw)[4]) {
                 uint32_t o[4];
@@ -349,20 +375,43 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                 return make_uint4(o[0], o[1], o[2], o[3]);
             };
             if constexpr (GATED) {
+                // gate and up of 32 hidden columns, CH at a time: the next ones come from tensor memory meanwhile
+                constexpr int CH = 16;
+                const uint32_t tg = t0 + (uint32_t)(acc * C::kAccCols), tu = tg + (uint32_t)kCols;
+                uint32_t g[2][CH], u[2][CH];
                 float most = 0.f;
+                tmem_ld16(tg, g[0]);
+                tmem_ld16(tu, u[0]);
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 g = *reinterpret_cast<const float4 *>(bias + c), u = *reinterpret_cast<const float4 *>(bias + 32 + c);
-                    const Pair gb[2] = {Pair(g.x, g.y), Pair(g.z, g.w)}, ub[2] = {Pair(u.x, u.y), Pair(u.z, u.w)};
+                for (int q = 0; q < 32 / CH; ++q) {
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    pin(g[q & 1]);
+                    pin(u[q & 1]);
+                    if (q + 1 < 32 / CH) {
+                        tmem_ld16(tg + CH * (q + 1), g[(q + 1) & 1]);
+                        tmem_ld16(tu + CH * (q + 1), u[(q + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(empty_bar + 8u * (uint32_t)acc);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const Pair gate = fma2(Pair(__uint_as_float(v[0][c + e]), __uint_as_float(v[0][c + e + 1])), Pair(kg, kg), gb[e / 2]);
-                        const Pair up = fma2(Pair(__uint_as_float(v[1][c + e]), __uint_as_float(v[1][c + e + 1])), Pair(ku, ku), ub[e / 2]);
-                        float h0, h1;
-                        hidden2<ACT>(gate, up).get(h0, h1);
-                        most = max_nan(most, h0, h1);
-                        v[0][c + e] = __float_as_uint(h0);
-                        v[0][c + e + 1] = __float_as_uint(h1);
+                    for (int c = 0; c < CH; c += 4) {
+                        const float4 gb4 = *reinterpret_cast<const float4 *>(bias + q * CH + c);
+                        const float4 ub4 = *reinterpret_cast<const float4 *>(bias + 32 + q * CH + c);
+                        const Pair gb[2] = {Pair(gb4.x, gb4.y), Pair(gb4.z, gb4.w)};
+                        const Pair ub[2] = {Pair(ub4.x, ub4.y), Pair(ub4.z, ub4.w)};
+                        auto two = [](const uint32_t *r) { return Pair(__uint_as_float(r[0]), __uint_as_float(r[1])); };
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const Pair gate = fma2(two(&g[q & 1][c + e]), Pair(kg, kg), gb[e / 2]);
+                            const Pair up = fma2(two(&u[q & 1][c + e]), Pair(ku, ku), ub[e / 2]);
+                            float h0, h1;
+                            hidden2<ACT>(gate, up).get(h0, h1);
+                            most = max_nan(most, h0, h1);
+                            v[0][q * CH + c + e] = __float_as_uint(h0);
+                            v[0][q * CH + c + e + 1] = __float_as_uint(h1);
+                        }
                     }
                 }
                 const uint32_t byte = mx_scale_byte(abs_bits(most));
@@ -373,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                     float f[8];
 #pragma unroll
                     for (int e = 0; e < 8; e += 2)
-                        mul2(Pair(__uint_as_float(v[0][8 * c + e]), __uint_as_float(v[0][8 * c + e + 1])), Pair(inv, inv)).get(f[e], f[e + 1]);
+                        mul2(Pair(__uint_as_float(v[0][8 * c + e]), __uint_as_float(v[0][8 * c + e + 1])), Pair(inv, inv))
+                            .get(f[e], f[e + 1]);
                     code[c] = mx_word(f);
                 }
                 // Straight to memory: 16 bytes of a row each, which meet those of the neighbouring blocks in L2. Blocks
@@ -383,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                     if (block < p.h_blocks)
                         *reinterpret_cast<uint4 *>(p.h_codes + row * p.h_pitch + block * 16) =
                             make_uint4(code[0], code[1], code[2], code[3]);
-                    p.h_scale[((size_t)(row0 >> 7) * p.h_tiles + (block >> 2)) * 512 + 16 * lane + 4 * quarter + part] =
+                    p.h_scale[((size_t)(row0 >> 7) * p.h_tiles + (block >> 2)) * 512 + 16 * lane + 4 * quarter + (block & 3)] =
                         (uint8_t)byte;
                 }
             } else {
@@ -423,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                     if (lane == 0) {
                         if (row0 < p.M && c0 < p.N) tma_store_tile(&p.out, smem_u32(piece), c0, row0);
                         store_commit();
-                        if (p.has_res && tile + n_pairs < p.n_tiles) {
+                        if (p.has_res && tile + next < p.n_tiles) {
                             store_wait_read();
-                            fetch_residual(tile + n_pairs);
+                            fetch_residual(tile + next);
                         }
                     }
                 }
@@ -460,11 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
 // ---------------------------------------------------------------- host side
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Codes as rows of bytes, boxes of 128 bytes x 128 rows; scale tiles as (row block, tile, 128 words), boxes of two tiles
-bool maps_of(CUtensorMap *codes, CUtensorMap *scale, const Mx &m, int64_t rows, int64_t width)
+// Codes as rows of bytes, boxes of 128 bytes x box_rows; scale tiles as (row block, tile, 128 words), boxes of two tiles
+bool maps_of(CUtensorMap *codes, CUtensorMap *scale, const Mx &m, int64_t rows, int64_t width, uint32_t box_rows = 128)
 {
     EncodeTiledFn fn = encode_fn();
-    if (!fn || !make_tile_map(codes, m.codes, rows, mx_pitch(width), mx_pitch(width), 1, 128)) return false;
+    if (!fn || !make_tile_map(codes, m.codes, rows, mx_pitch(width), mx_pitch(width), 1, box_rows)) return false;
     const cuuint64_t tiles = (cuuint64_t)ceil_div(mx_blocks(width), 4);
     cuuint64_t dims[3] = {128, tiles, (cuuint64_t)ceil_div(rows, 128)};
     cuuint64_t strides[2] = {512, 512 * tiles};
@@ -533,7 +583,7 @@ pmha_status mx_tc_gated(const MxGated &a, cudaStream_t s)
 {
     Params p = {};
     const char *stage = "ffn_up_mx";
-    const pmha_status st = tiles_of(p, a.M, a.F, a.K, 128, stage);
+    const pmha_status st = tiles_of(p, a.M, a.F, a.K, 64, stage);
     if (st != PMHA_OK) return st;
     p.bias0 = (const __nv_bfloat16 *)a.bg;
     p.bias1 = (const __nv_bfloat16 *)a.bu;
@@ -542,8 +592,11 @@ pmha_status mx_tc_gated(const MxGated &a, cudaStream_t s)
     p.h_pitch = mx_pitch(a.F);
     p.h_blocks = (int)mx_blocks(a.F);
     p.h_tiles = (int)ceil_div(mx_blocks(a.F), 4);
-    if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.wg, a.F, a.K) ||
-        !maps_of(&p.b1, &p.sb1, a.wu, a.F, a.K))
+    p.tiles_n = 2 * p.h_tiles;  // whole scale tiles of h, to their zeros past the last block
+    p.n_tiles = (int)(ceil_div(a.M, 256) * p.tiles_n);
+    constexpr uint32_t kBoxRows = Cfg<kGated>::kRowsB;
+    if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.wg, a.F, a.K, kBoxRows) ||
+        !maps_of(&p.b1, &p.sb1, a.wu, a.F, a.K, kBoxRows))
         return map_failed(stage);
     return a.act == PMHA_ACT_SILU ? launch<kGated, PMHA_ACT_SILU>(p, stage, s) : launch<kGated, PMHA_ACT_GELU>(p, stage, s);
 }
