@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(kThreads, kResident) k_join(JoinArgs a)
             for (int i = 0; i < VEC; ++i) wz[j * VEC + i] *= g[i];
         }
     };
-    // kept values' scales, of the next row
+    // kept values' scales, of the next row, as they were loaded: widened there they would be waited for there
     const int groups = (a.width + kGroup - 1) / kGroup;
-    float sb[NV] = {}, sx[NV] = {};
+    __nv_bfloat16 sb[NV] = {}, sx[NV] = {};
     auto fetch_scales = [&](unsigned row, long long at) {
         if constexpr (KEPT) {
             if (row >= rows) return;
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_join(JoinArgs a)
             for (int j = 0; j < NV; ++j) {
                 if (!col[j]) continue;
                 const long long s = at + j * (kPiece / kGroup);
-                if (a.branch.k.codes) sb[j] = __bfloat162float(a.branch.k.scale[s]);
-                if (a.res.k.codes) sx[j] = __bfloat162float(a.res.k.scale[s]);
+                if (a.branch.k.codes) sb[j] = a.branch.k.scale[s];
+                if (a.res.k.codes) sx[j] = a.res.k.scale[s];
             }
         }
     };
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_join(JoinArgs a)
                                      l * VEC % kGroup == 0, live && col[j], v);
                     }
             } else if (KEPT && a.branch.k.codes) {
-                unkeep<VEC>(codes(cb, 0), sb[j], bj);
+                unkeep<VEC>(codes(cb, 0), __bfloat162float(sb[j]), bj);
             } else {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) bj[i] = 0.f;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_join(JoinArgs a)
                                      l * VEC % kGroup == 0, live && col[j], v);
                     }
             } else {
-                unkeep<VEC>(codes(cx, 1), sx[j], xj);
+                unkeep<VEC>(codes(cx, 1), __bfloat162float(sx[j]), xj);
             }
         }
         if constexpr (kRing > 0) slot = slot + 1 == kRing ? 0 : slot + 1;

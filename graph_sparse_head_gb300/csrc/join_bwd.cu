@@ -86,13 +86,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
     long long sat = (long long)(row_first + sub) * groups + l * VEC / kGroup;
     uint8_t *ring = (uint8_t *)shw + threadIdx.x * 16;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-    float scale[NV] = {};  // of the kept branch's values, loaded a step ahead
+    // of the kept branch's values, loaded a step ahead, and as they were loaded: widened there they would be waited for there
+    __nv_bfloat16 scale[NV] = {};
     auto fetch_scale = [&](unsigned row, long long from) {
         if constexpr (KEPT) {
             if (row >= end) return;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                if (col[j]) scale[j] = __bfloat162float(a.branch.k.scale[from + j * (kPiece / kGroup)]);
+                if (col[j]) scale[j] = a.branch.k.scale[from + j * (kPiece / kGroup)];
         }
     };
     auto fetch = [&](unsigned row, long long from, int slot) {
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
                 widen<T, VEC>(raw[0][j], g + j * VEC);
                 widen<T, VEC>(raw[1][j], f + j * VEC);
                 widen<T, VEC>(raw[2][j], D + j * VEC);
-                if constexpr (KEPT) unkeep<VEC>(codes[j], scale[j], bj);
+                if constexpr (KEPT) unkeep<VEC>(codes[j], __bfloat162float(scale[j]), bj);
                 else widen<T, VEC>(raw[3][j], bj);
             } else {
 #pragma unroll
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
                     widen<T, VEC>(*(const V *)(p + 16 * kThreads), f + j * VEC);
                 }
                 if (a.ds) widen<T, VEC>(*(const V *)(p + 32 * kThreads), D + j * VEC);
-                if constexpr (KEPT) unkeep<VEC>(*(const Codes *)(p + 48 * kThreads), scale[j], bj);
+                if constexpr (KEPT) unkeep<VEC>(*(const Codes *)(p + 48 * kThreads), __bfloat162float(scale[j]), bj);
                 else if (a.branch.p) widen<T, VEC>(*(const V *)(p + 48 * kThreads), bj);
             }
         }
