@@ -125,7 +125,7 @@ __device__ __forceinline__ float block_dot(const __half2 (&w)[16], const uint8_t
     return s;
 }
 
-template <bool GATED, int ACT, int MB, int LPR>
+template <bool GATED, int ACT, int MB, int LPR, int AHEAD>
 __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
 {
     extern __shared__ __align__(16) uint8_t cells[];  // [M][blocks]
@@ -150,46 +150,82 @@ __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
             *reinterpret_cast<float *>(cell + 64) = mx_scale_value(a.xs[scale_at(m, k, tiles)]);
         }
     } else {
-        // eight lanes a block; whole warps walk
-        for (int i0 = threadIdx.x / 32 * 4; i0 < a.M * blocks; i0 += kThreads / 8) {
-            const int i = i0 + (threadIdx.x & 31) / 8, q = threadIdx.x % 8;
-            const int m = i / blocks, k = i - m * blocks;
-            float f[4];
-            uint32_t most = 0;
+        // eight lanes a block, four values a lane; whole warps walk, with kAhead blocks' values under way
+        constexpr int kAhead = 4, kStep = kThreads / 8;
+        const int all = a.M * blocks, q = threadIdx.x % 8;
+        const bool whole = a.K % 32 == 0;  // rows are whole blocks, one after the other
+        for (int i0 = threadIdx.x / 32 * 4; i0 < all; i0 += kAhead * kStep) {
+            float4 f[kAhead];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = k * 32 + q * 4 + e;
-                f[e] = i < a.M * blocks && c < a.K ? a.h[(size_t)m * a.K + c] : 0.f;
-                most = max(most, abs_bits(f[e]));
+            for (int e = 0; e < kAhead; ++e) {
+                const int i = i0 + e * kStep + (threadIdx.x & 31) / 8;
+                f[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i >= all) continue;
+                if (whole) {
+                    f[e] = *reinterpret_cast<const float4 *>(a.h + (size_t)i * 32 + q * 4);
+                } else {
+                    const int m = i / blocks, c = (i - m * blocks) * 32 + q * 4;
+                    const float *h = a.h + (size_t)m * a.K + c;
+                    if (c < a.K) f[e].x = h[0];
+                    if (c + 1 < a.K) f[e].y = h[1];
+                    if (c + 2 < a.K) f[e].z = h[2];
+                    if (c + 3 < a.K) f[e].w = h[3];
+                }
             }
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
-            if (i >= a.M * blocks) continue;
-            const uint32_t byte = mx_scale_byte(most);
-            const float inv = mx_inverse(byte);
-            __half2 v[2] = {two_of(mx_byte(f[0] * inv, f[1] * inv)), two_of(mx_byte(f[2] * inv, f[3] * inv))};
-            uint8_t *cell = cells + i * kCell;
-            *reinterpret_cast<uint2 *>(cell + 8 * q) = *reinterpret_cast<uint2 *>(v);
-            if (q == 0) *reinterpret_cast<float *>(cell + 64) = mx_scale_value(byte);
+            for (int e = 0; e < kAhead; ++e) {
+                const int i = i0 + e * kStep + (threadIdx.x & 31) / 8;
+                uint32_t most = max(max(abs_bits(f[e].x), abs_bits(f[e].y)), max(abs_bits(f[e].z), abs_bits(f[e].w)));
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+                if (i >= all) continue;
+                const uint32_t byte = mx_scale_byte(most);
+                const float inv = mx_inverse(byte);
+                __half2 v[2] = {two_of(mx_byte(f[e].x * inv, f[e].y * inv)), two_of(mx_byte(f[e].z * inv, f[e].w * inv))};
+                uint8_t *cell = cells + i * kCell;
+                *reinterpret_cast<uint2 *>(cell + 8 * q) = *reinterpret_cast<uint2 *>(v);
+                if (q == 0) *reinterpret_cast<float *>(cell + 64) = mx_scale_value(byte);
+            }
         }
     }
     __syncthreads();
     float y0[MB], y1[MB];
 #pragma unroll
     for (int m = 0; m < MB; ++m) y0[m] = y1[m] = 0.f;
-    for (int k = l; k < blocks; k += LPR) {
-        __half2 w0[16], w1[16];
-        widen16(k == l && a.h ? first : *reinterpret_cast<const uint4 *>(a.w0 + wrow + k * 16), w0);
-        if constexpr (GATED) widen16(*reinterpret_cast<const uint4 *>(a.w1 + wrow + k * 16), w1);
-        const size_t at = scale_at(min(n, a.N - 1), k, tiles);
-        const float s0 = mx_scale_value(a.s0[at]), s1 = GATED ? mx_scale_value(a.s1[at]) : 0.f;
+    // AHEAD blocks' weights under way
+    for (int k0 = l; k0 < blocks; k0 += AHEAD * LPR) {
+        uint4 r0[AHEAD], r1[AHEAD];
+        uint32_t b0[AHEAD], b1[AHEAD];
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            if (m >= a.M) break;
-            const uint8_t *cell = cells + (m * blocks + k) * kCell;
-            const float sx = *reinterpret_cast<const float *>(cell + 64);
-            y0[m] = fmaf(block_dot(w0, cell) * s0, sx, y0[m]);
-            if constexpr (GATED) y1[m] = fmaf(block_dot(w1, cell) * s1, sx, y1[m]);
+        for (int e = 0; e < AHEAD; ++e) {
+            const int k = k0 + e * LPR;
+            r0[e] = r1[e] = make_uint4(0, 0, 0, 0);
+            b0[e] = b1[e] = 0;
+            if (k >= blocks) continue;
+            const size_t at = scale_at(min(n, a.N - 1), k, tiles);
+            r0[e] = e == 0 && k0 == l && a.h ? first : *reinterpret_cast<const uint4 *>(a.w0 + wrow + k * 16);
+            b0[e] = a.s0[at];
+            if constexpr (GATED) {
+                r1[e] = *reinterpret_cast<const uint4 *>(a.w1 + wrow + k * 16);
+                b1[e] = a.s1[at];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            const int k = k0 + e * LPR;
+            if (k >= blocks) break;
+            __half2 w0[16], w1[16];
+            widen16(r0[e], w0);
+            if constexpr (GATED) widen16(r1[e], w1);
+            const float s0 = mx_scale_value(b0[e]), s1 = mx_scale_value(b1[e]);
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                if (m >= a.M) break;
+                const uint8_t *cell = cells + (m * blocks + k) * kCell;
+                const float sx = *reinterpret_cast<const float *>(cell + 64);
+                y0[m] = fmaf(block_dot(w0, cell) * s0, sx, y0[m]);
+                if constexpr (GATED) y1[m] = fmaf(block_dot(w1, cell) * s1, sx, y1[m]);
+            }
         }
     }
     float m0 = 0.f, m1 = 0.f;  // of token l
@@ -214,25 +250,34 @@ __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
     }
 }
 
+// Up to 8 tokens whose cells fill at most 48 KB. Against the tensor cores, whose tiles hold 256 tokens (us, here / there):
+// linear 512 -> 2,048, 1 token 1.8 / 4.7, 8 tokens 2.6 / 4.7; 1,024 -> 4,096, 1 token 2.3 / 5.3, 6 tokens 4.8 / 5.4, 8
+// tokens 5.5 / 5.3; 4,096 -> 1,024, 4 tokens 3.8 / 8.4.
 constexpr int kFewTokens = 8;
 constexpr size_t kFewBytes = 48 * 1024;
 bool few(int64_t M, int64_t K) { return M <= kFewTokens && (size_t)(M * mx_blocks(K)) * kCell <= kFewBytes; }
+// A block's, where the hidden values are 12,288 at most: every thread block of the down product rounds all of them. 256 x
+// 1,024, 8 tokens 6.7 / 8.4; 512 x 2,048, 6 tokens 8.9 / 10.0, 8 tokens 13.2 / 10.1; 1,024 x 4,096, 2 tokens 9.1 / 13.4, 4
+// tokens 13.2 / 13.4.
+bool few_block(int64_t M, int64_t E, int64_t F) { return few(M, E) && few(M, F) && M * F <= 12288; }
 
-template <bool GATED, int ACT, int MB, int LPR>
+template <bool GATED, int ACT, int MB, int LPR, int AHEAD>
 pmha_status launch_small(const MxSmallArgs &a, cudaStream_t s)
 {
     const int per = kThreads / LPR;
-    return tcu::launch_overlapping(k_mx_small<GATED, ACT, MB, LPR>, dim3((unsigned)((a.N + per - 1) / per)), kThreads,
+    return tcu::launch_overlapping(k_mx_small<GATED, ACT, MB, LPR, AHEAD>, dim3((unsigned)((a.N + per - 1) / per)), kThreads,
                                    (int)((size_t)a.M * mx_blocks(a.K) * kCell), s, a);
 }
-// LPR lanes have a block each at least
+// As many lanes an output as blocks, up to a warp; longer rows have several blocks' weights under way (4,096 -> 1,024, 1
+// token 2.4 us, one at a time 3.1; rows of one block a lane lose by it: 1,024 -> 4,096, 4 tokens 4.6 for 3.7).
 template <bool GATED, int ACT, int MB>
 pmha_status by_lanes(const MxSmallArgs &a, cudaStream_t s)
 {
     const int64_t blocks = mx_blocks(a.K);
-    if (blocks <= 8) return launch_small<GATED, ACT, MB, 8>(a, s);
-    if (blocks <= 16) return launch_small<GATED, ACT, MB, 16>(a, s);
-    return launch_small<GATED, ACT, MB, 32>(a, s);
+    if (blocks <= 8) return launch_small<GATED, ACT, MB, 8, 1>(a, s);
+    if (blocks <= 16) return launch_small<GATED, ACT, MB, 16, 1>(a, s);
+    if (blocks <= 32) return launch_small<GATED, ACT, MB, 32, 1>(a, s);
+    return launch_small<GATED, ACT, MB, 32, GATED ? 2 : 4>(a, s);
 }
 template <bool GATED, int ACT>
 pmha_status small(const MxSmallArgs &a, const char *stage, cudaStream_t s)
@@ -297,7 +342,7 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t hidden_bytes(const pmha_ffn_params *p, int64_t rows)
 {
     const size_t small = (size_t)std::min<int64_t>(rows, kFewTokens) * (size_t)p->hidden_dim * 4;
-    if (few(rows, p->embed_dim) && few(rows, p->hidden_dim)) return round256(small);
+    if (few_block(rows, p->embed_dim, p->hidden_dim)) return round256(small);
     return std::max(round256(small),
                     round256(mx_code_bytes(rows, p->hidden_dim)) + round256(mx_scale_bytes(rows, p->hidden_dim)));
 }
@@ -419,7 +464,7 @@ pmha_status pmha_ffn_forward_mx(const pmha_ffn_params *params, const pmha_ffn_mx
         return PMHA_ERR_WORKSPACE;
     }
     cudaStream_t s = (cudaStream_t)stream;
-    if (few(rows, E) && few(rows, F)) {
+    if (few_block(rows, E, F)) {
         MxSmallArgs a = {};
         a.x = (const uint8_t *)x->codes, a.xs = (const uint8_t *)x->scale;
         a.w0 = (const uint8_t *)weights->wg.codes, a.s0 = (const uint8_t *)weights->wg.scale;
