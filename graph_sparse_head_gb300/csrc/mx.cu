@@ -222,9 +222,10 @@ __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
             for (int m = 0; m < MB; ++m) {
                 if (m >= a.M) break;
                 const uint8_t *cell = cells + (m * blocks + k) * kCell;
+                // the scales' product first: far scales that cancel leave no room for an infinity between
                 const float sx = *reinterpret_cast<const float *>(cell + 64);
-                y0[m] = fmaf(block_dot(w0, cell) * s0, sx, y0[m]);
-                if constexpr (GATED) y1[m] = fmaf(block_dot(w1, cell) * s1, sx, y1[m]);
+                y0[m] = fmaf(block_dot(w0, cell), s0 * sx, y0[m]);
+                if constexpr (GATED) y1[m] = fmaf(block_dot(w1, cell), s1 * sx, y1[m]);
             }
         }
     }

@@ -108,6 +108,17 @@ def test_linear(rows, width, outputs, extra):
     check_linear(ref.values(x), ref.values(w), bias, residual, got)
 
 
+@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("ex,ew", [(119, -119), (-119, 119), (60, 50), (-60, -50), (124, -20)])
+def test_linear_of_far_scales(rows, ex, ew):
+    """Scales near the ends of their range whose products are ordinary numbers."""
+    width, outputs = 96, 40
+    x = (normal(10, rows, width, dtype=torch.float32).clamp(-3, 3).double() * 2.0 ** ex).float()
+    w = (normal(20, outputs, width, dtype=torch.float32).clamp(-3, 3).double() * 2.0 ** ew).float()
+    got = pmha.pmha_mx_linear(pmha.pmha_mx_quantize(x), pmha.pmha_mx_quantize(w))
+    check_linear(ref.values(x), ref.values(w), None, None, got)
+
+
 def test_linear_places_every_row_column_and_scale():
     """Integers small enough for exact sums, scales of every block their own: the result is exact."""
     rows, width, outputs = 391, 800, 520
