@@ -252,14 +252,15 @@ __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
 }
 
 // Up to 8 tokens whose cells fill at most 48 KB. Against the tensor cores, whose tiles hold 256 tokens (us, here / there):
-// linear 512 -> 2,048, 1 token 1.8 / 4.7, 8 tokens 2.6 / 4.7; 1,024 -> 4,096, 1 token 2.3 / 5.3, 6 tokens 4.8 / 5.4, 8
-// tokens 5.5 / 5.3; 4,096 -> 1,024, 4 tokens 3.8 / 8.4.
+// linear 512 -> 2,048, 1 token 1.7 / 3.6, 8 tokens 2.6 / 3.7; 2,048 -> 512, 8 tokens 3.8 / 4.9; 4,096 -> 1,024, 4 tokens 3.8 /
+// 6.9. The CUDA cores' time grows with tokens x outputs, the tensor cores' with the width alone: 1,024 -> 4,096, 4 tokens 3.7
+// / 4.8, 6 tokens 4.8 / 4.7, 8 tokens 5.5 / 4.7.
 constexpr int kFewTokens = 8;
 constexpr size_t kFewBytes = 48 * 1024;
 bool few(int64_t M, int64_t K) { return M <= kFewTokens && (size_t)(M * mx_blocks(K)) * kCell <= kFewBytes; }
+bool few_linear(int64_t M, int64_t N, int64_t K) { return few(M, K) && M * N * K <= (1 << 24) + 8192 * K; }
 // A block's, where the hidden values are 12,288 at most: every thread block of the down product rounds all of them. 256 x
-// 1,024, 8 tokens 6.7 / 8.4; 512 x 2,048, 6 tokens 8.9 / 10.0, 8 tokens 13.2 / 10.1; 1,024 x 4,096, 2 tokens 9.1 / 13.4, 4
-// tokens 13.2 / 13.4.
+// 1,024, 8 tokens 6.9 / 7.5; 512 x 2,048, 4 tokens 6.3 / 8.8, 6 tokens 8.8 / 8.9; 1,024 x 4,096, 2 tokens 9.2 / 12.0.
 bool few_block(int64_t M, int64_t E, int64_t F) { return few(M, E) && few(M, F) && M * F <= 12288; }
 
 template <bool GATED, int ACT, int MB, int LPR, int AHEAD>
@@ -322,7 +323,7 @@ bool overlaps_any(const void *p, size_t n, const Span (&in)[N])
 
 pmha_status linear(const MxLinear &a, const char *stage, cudaStream_t s)
 {
-    if (!few(a.M, a.K)) return mx_tc_linear(a, stage, s);
+    if (!few_linear(a.M, a.N, a.K)) return mx_tc_linear(a, stage, s);
     MxSmallArgs q = {};
     q.x = a.x.codes, q.xs = a.x.scale, q.w0 = a.w.codes, q.s0 = a.w.scale;
     q.b0 = (const __nv_bfloat16 *)a.bias, q.res = (const __nv_bfloat16 *)a.residual, q.out = (__nv_bfloat16 *)a.out;

@@ -1,6 +1,6 @@
 // Products of matrices in microscaled 4 bits (mx.cuh) on the tensor cores (sm_103a), one kernel shape for two:
 //
-//   linear  y = x W^T + bias + residual                          tile 256 tokens x 256 outputs, bf16
+//   linear  y = x W^T + bias + residual                          tile 256 tokens x 256 or 128 outputs, bf16
 //   gated   h = act(x Wg^T + bg) * (x Wu^T + bu), in 4 bits      tile 256 tokens x 64 hidden, gate and up side by side
 //
 // Two CTAs form a pair (tc_pair.cuh). Each has 18 warps: warp 0 copies stages of
@@ -8,10 +8,11 @@
 // 1 of the even CTA copies the scale tiles to tensor memory (tcgen05.cp, into both CTAs) and issues tcgen05.mma
 // kind::mxf4, whose scaling by block is the hardware's; sixteen warps turn accumulators into outputs. Linear: 256
 // accumulator columns and the scales of four stages fill tensor memory, there is one set; an epilogue thread takes all of its
-// accumulators into registers (64) and hands the set back at once, so that the next products run under its arithmetic. Gated:
-// three sets of 64 gates and 64 ups, and two teams of eight warps that take the tiles in turn, one team's waits under the
-// other's special functions, 16 columns' accumulators on their way while 16 are used (320,000 x 128 x 512 in 98 us; with one
-// set of 128 + 128, one team and all accumulators in registers at once 112).
+// accumulators into registers (64) and hands the set back at once, so that the next products run under its arithmetic. With
+// 128 columns there are three sets, and two teams of eight warps that take the tiles in turn. Gated: three sets of 64 gates
+// and 64 ups and two teams, one team's waits under the other's special functions, 16 columns' accumulators on their way while
+// 16 are used (320,000 x 128 x 512 in 98 us; with one set of 128 + 128, one team and all accumulators in registers at once
+// 112).
 // Epilogue warps go their own ways: each has its 32 rows' share of the columns, its own piece of shared memory, its own
 // copies of the residual and of the result, and no barrier with the others. (With a barrier for all sixteen around each
 // step the same took 152 us.)
@@ -37,27 +38,27 @@ using namespace tcu;
 constexpr int kThreads = 64 + 512;
 constexpr int kBox = 128 * 128;       // bytes of a tile of 128 rows of 128 bytes
 constexpr int kSfA = 2 * 512;         // scale tiles of a stage: 128 rows x 256 columns
-constexpr int kSfB = 4 * 512;         // 256 rows x 256 columns, or 128 each of gate and up
 // Not kept in the linear kernel: six stages instead of four, its outputs straight from registers to make room (8,192 x
 // 4,096 x 4,096 50.0 us for 50.9, with a residual 85 for 58); two stages and two output pieces a warp for rows of up to 512
 // columns (320,000 x 128 -> 384 with a residual 101 us for 105, without one 60 for 58).
-enum Kind { kTiles, kGated };
+enum Kind { kTiles, kNarrow, kGated };
 constexpr int kPiece = 32 * 128;      // 32 x 64 bf16 of an epilogue warp
 template <int KIND>
 struct Cfg {
     static constexpr bool kGate = KIND == kGated;
-    static constexpr int kCols = kGate ? 64 : 256;      // output columns of a tile: N of a product
+    static constexpr int kCols = kGate ? 64 : KIND == kNarrow ? 128 : 256;  // output columns of a tile: N of a product
     static constexpr int kOps = kGate ? 2 : 1;          // products side by side
     static constexpr int kRowsB = kCols / 2;            // weight rows that a CTA brings to a product
     static constexpr int kB = kOps * kRowsB * 128;
-    static constexpr int kStage = kBox + kB + kSfA + kSfB;
+    static constexpr int kSfTiles = KIND == kNarrow ? 1 : 2;  // of 128 rows of weights (one each of gate and up)
+    static constexpr int kStage = kBox + kB + kSfA + 1024 * kSfTiles;
     static_assert(kStage % 1024 == 0, "swizzled tiles lie on 1024 bytes");
-    static constexpr int kAccs = kGate ? 3 : 1, kAccCols = kOps * kCols;
-    static constexpr int kTeams = kGate ? 2 : 1;        // of epilogue warps, which take tiles in turn
-    static constexpr int kStages = kGate ? 5 : 4;
+    static constexpr int kAccs = KIND == kTiles ? 1 : 3, kAccCols = kOps * kCols;
+    static constexpr int kTeams = KIND == kTiles ? 1 : 2;        // of epilogue warps, which take tiles in turn
+    static constexpr int kStages = KIND == kTiles ? 4 : 5;
     static constexpr int kScaleCol = kAccs * kAccCols;  // then 24 scale columns a stage
     static_assert(kScaleCol + 24 * kStages <= 512, "tensor memory");
-    static constexpr int kTile = KIND == kTiles ? 16 * kPiece : 0;
+    static constexpr int kTile = kGate ? 0 : 16 * kPiece;
     static constexpr int kVec = 16 * 64 * 4;  // a warp's biases: of 64 outputs, or 32 of gate and of up
     static constexpr int kBars = 512;
     static constexpr int kSmem = 1024 + kStages * kStage + kTile + kVec + kBars;
@@ -75,7 +76,7 @@ struct Params {
     uint8_t *h_codes, *h_scale;
     long long h_pitch;
     int h_blocks, h_tiles;  // blocks of a row of h, scale tiles of a row block
-    int has_res, plain;
+    int has_res;
     int *err;
 };
 
@@ -181,11 +182,12 @@ __device__ __forceinline__ uint32_t mx_word(const float (&f)[8])
     return w;
 }
 
-template <int KIND, int ACT>
+// VARIANT: gated, the activation; else whether outputs go through plain loads and stores (which cost registers)
+template <int KIND, int VARIANT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(const __grid_constant__ Params p)
 {
     using C = Cfg<KIND>;
-    constexpr bool GATED = KIND == kGated;
+    constexpr bool GATED = KIND == kGated, kPlain = !GATED && VARIANT;
     constexpr int kStages = C::kStages, kStage = C::kStage, kCols = C::kCols, kAccs = C::kAccs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -249,8 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                 tma_load_3d_pair(ssa, &p.sa, 0, kb * 2, rows, fb);
                 // the scales of all columns, in both CTAs: two tiles of the weights', or the tiles of gate and of up in
                 // which the 64 columns lie
-                tma_load_3d_pair(ssb, &p.sb0, 0, kb * 2, GATED ? n / 2 : n * 2, fb);
-                tma_load_3d_pair(ssb + 1024, GATED ? &p.sb1 : &p.sb0, 0, kb * 2, GATED ? n / 2 : n * 2 + 1, fb);
+                tma_load_3d_pair(ssb, &p.sb0, 0, kb * 2, GATED ? n / 2 : n * C::kSfTiles, fb);
+                if constexpr (C::kSfTiles == 2)
+                    tma_load_3d_pair(ssb + 1024, GATED ? &p.sb1 : &p.sb0, 0, kb * 2, GATED ? n / 2 : n * 2 + 1, fb);
             }
         }
     } else if (warp == 1) {
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                                 const int h = k / 2;
                                 copy_scales(ca + 4 * h, scale_desc(ssa + 512 * h));
                                 copy_scales(cb + 8 * h, scale_desc(ssb + 512 * h));
-                                copy_scales(cb + 8 * h + 4, scale_desc(ssb + 1024 + 512 * h));
+                                if constexpr (C::kSfTiles == 2) copy_scales(cb + 8 * h + 4, scale_desc(ssb + 1024 + 512 * h));
                             }
 #pragma unroll
                             for (int o = 0; o < C::kOps; ++o)
@@ -307,17 +310,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
         }
     } else {
         // ---------------- epilogue: a warp 32 rows and 64 accumulator columns of a tile, of which teams take turns
-        const int w = warp - 2, quarter = warp & 3, team = GATED ? w >> 3 : 0, part = (w >> 2) & (GATED ? 1 : 3);
+        const int w = warp - 2, quarter = warp & 3, team = C::kTeams == 2 ? w >> 3 : 0;
+        const int part = (w >> 2) & (C::kTeams == 2 ? 1 : 3);
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(GATED ? part * 32 : part * 64);
         const uint32_t empty_bar = map_rank(smem_u32(acc_empty), 0);
         const int first = pair + team * n_pairs, next = C::kTeams * n_pairs;
         float *bias = vec_s + w * 64;
         uint8_t *piece = tile_s + w * kPiece;
-        constexpr float kg = GATED ? Act<ACT>::kGate : 1.f, ku = GATED ? Act<ACT>::kUp : 1.f;
+        constexpr float kg = GATED ? Act<VARIANT>::kGate : 1.f, ku = GATED ? Act<VARIANT>::kUp : 1.f;
         auto rows_of = [&](int tile) { return tile / p.tiles_n * 256 + (int)rank * 128 + quarter * 32; };
         auto column_of = [&](int tile) { return tile % p.tiles_n * kCols + part * (GATED ? 32 : 64); };
         auto fetch_residual = [&](int tile) {
-            if (KIND != kTiles || !p.has_res || p.plain || lane) return;
+            if (GATED || kPlain || !p.has_res || lane) return;
             const int row = rows_of(tile), c = column_of(tile);
             if (row < p.M && c < p.N) {
                 mbar_arrive_expect_tx(smem_u32(&res_full[w]), kPiece);
@@ -334,9 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             b0 = p.bias0 && c < p.N ? kg * __bfloat162float(p.bias0[c]) : 0.f;
             b1 = second && c2 < p.N ? ku * __bfloat162float(second[c2]) : 0.f;
         };
-        uint32_t i = (uint32_t)team;
+        uint32_t i = (uint32_t)team, fetched = 0;  // tiles of all teams, residual copies of this warp
         if (first < p.n_tiles) {
             fetch_residual(first);
+            fetched = 1;
             fetch_bias(first);
         }
         for (int tile = first; tile < p.n_tiles; tile += next, i += C::kTeams) {
@@ -351,26 +356,29 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
             wait_bar(smem_u32(&acc_full[acc]), (i / kAccs) & 1u, abort_flag, p.err);
             tc_fence_after();
             __syncwarp();
-            uint32_t v[2][32];  // 64 outputs
-            if constexpr (!GATED) {
+            uint32_t v[2][KIND == kNarrow ? 16 : 32];  // 64 outputs (narrow: 16 and the next 16; gated: 32)
+            auto hand_back = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(empty_bar + 8u * (uint32_t)acc);
+            };
+            if constexpr (KIND == kNarrow) tmem_ld16(t0 + (uint32_t)(acc * C::kAccCols), v[0]);
+            if constexpr (KIND == kTiles) {
                 tmem_ld32_nowait(t0 + (uint32_t)(acc * C::kAccCols), v[0]);
                 tmem_ld32_nowait(t0 + (uint32_t)(acc * C::kAccCols + 32), v[1]);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                 pin(v[0]);
                 pin(v[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(empty_bar + 8u * (uint32_t)acc);
+                hand_back();
             }
-            // eight outputs: accumulators 8 u and on, biases, and the residual's values
-            auto sums = [&](int u, const uint32_t (&rw)[4]) {
+            // outputs 8 u and on: eight accumulators, biases, and the residual's values
+            auto sums = [&](int u, const uint32_t *acc8, const uint32_t (&rw)[4]) {
                 uint32_t o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int c = 8 * u + 2 * e;
-                    const float2 b = *reinterpret_cast<const float2 *>(bias + c);
-                    o[e] = pack_bf16(__uint_as_float(v[c >> 5][c & 31]) + b.x + __uint_as_float(rw[e] << 16),
-                                     __uint_as_float(v[c >> 5][(c & 31) + 1]) + b.y + __uint_as_float(rw[e] & 0xffff0000u));
+                    const float2 b = *reinterpret_cast<const float2 *>(bias + 8 * u + 2 * e);
+                    o[e] = pack_bf16(__uint_as_float(acc8[2 * e]) + b.x + __uint_as_float(rw[e] << 16),
+                                     __uint_as_float(acc8[2 * e + 1]) + b.y + __uint_as_float(rw[e] & 0xffff0000u));
                 }
                 return make_uint4(o[0], o[1], o[2], o[3]);
             };
@@ -391,9 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                         tmem_ld16(tg + CH * (q + 1), g[(q + 1) & 1]);
                         tmem_ld16(tu + CH * (q + 1), u[(q + 1) & 1]);
                     } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(empty_bar + 8u * (uint32_t)acc);
+                        hand_back();
                     }
 #pragma unroll
                     for (int c = 0; c < CH; c += 4) {
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                             const Pair gate = fma2(two(&g[q & 1][c + e]), Pair(kg, kg), gb[e / 2]);
                             const Pair up = fma2(two(&u[q & 1][c + e]), Pair(ku, ku), ub[e / 2]);
                             float h0, h1;
-                            hidden2<ACT>(gate, up).get(h0, h1);
+                            hidden2<VARIANT>(gate, up).get(h0, h1);
                             most = max_nan(most, h0, h1);
                             v[0][q * CH + c + e] = __float_as_uint(h0);
                             v[0][q * CH + c + e + 1] = __float_as_uint(h1);
@@ -437,16 +443,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                         (uint8_t)byte;
                 }
             } else {
-                if (p.plain) {
+                bool ok = true;
+                // plain rows: a lane a column, of eight rows at a time
+                auto by_rows = [&](auto load, auto store) {
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = lane + 32 * h;
+                        if (c0 + c >= p.N) return;
+                        for (int q0 = 0; q0 < 32; q0 += 8) {
+                            __nv_bfloat16 x[8];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (row0 + q0 + q < p.M) x[q] = load(q0 + q, c, (size_t)(row0 + q0 + q) * p.N + c0 + c);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (row0 + q0 + q < p.M) store(q0 + q, c, (size_t)(row0 + q0 + q) * p.N + c0 + c, x[q]);
+                        }
+                    }
+                };
+                if constexpr (kPlain) {
                     if (p.has_res) {
-                        for (int q = 0; q < 32 && row0 + q < p.M; ++q)
-                            for (int c = lane; c < 64 && c0 + c < p.N; c += 32)
-                                *(__nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2) =
-                                    p.res_p[(size_t)(row0 + q) * p.N + c0 + c];
+                        by_rows([&](int q, int c, size_t at) { return p.res_p[at]; },
+                                [&](int q, int c, size_t at, __nv_bfloat16 x) {
+                                    *(__nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2) = x;
+                                });
                         __syncwarp();
                     }
                 } else if (p.has_res) {
-                    wait_bar(smem_u32(&res_full[w]), i & 1u, abort_flag, p.err);
+                    ok = wait_bar(smem_u32(&res_full[w]), (i / C::kTeams) & 1u, abort_flag, p.err);
                 } else {
                     if (lane == 0) store_wait_read();  // the last tile's store has read the piece
                     __syncwarp();
@@ -454,38 +477,54 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     uint4 *at = reinterpret_cast<uint4 *>(piece + swizzled(lane, u));
+                    const uint32_t *acc8;
+                    if constexpr (KIND == kNarrow) {
+                        const int q = u / 2;
+                        if (u % 2 == 0) {
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                            pin(v[q & 1]);
+                            if (q < 3)
+                                tmem_ld16(t0 + (uint32_t)(acc * C::kAccCols + 16 * (q + 1)), v[(q + 1) & 1]);
+                            else
+                                hand_back();
+                        }
+                        acc8 = &v[q & 1][8 * (u % 2)];
+                    } else {
+                        acc8 = &v[u / 4][8 * (u % 4)];
+                    }
                     uint32_t rw[4] = {0, 0, 0, 0};
                     if (p.has_res) {
                         const uint4 q = *at;
                         rw[0] = q.x, rw[1] = q.y, rw[2] = q.z, rw[3] = q.w;
                     }
-                    *at = sums(u, rw);
+                    *at = sums(u, acc8, rw);
                 }
-                if (p.plain) {
+                if constexpr (kPlain) {
                     __syncwarp();
-                    for (int q = 0; q < 32 && row0 + q < p.M; ++q)
-                        for (int c = lane; c < 64 && c0 + c < p.N; c += 32)
-                            p.out_p[(size_t)(row0 + q) * p.N + c0 + c] =
-                                *(const __nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2);
+                    by_rows([&](int q, int c, size_t at) {
+                                return *(const __nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2);
+                            },
+                            [&](int q, int c, size_t at, __nv_bfloat16 x) { p.out_p[at] = x; });
                 } else {
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
                         if (row0 < p.M && c0 < p.N) tma_store_tile(&p.out, smem_u32(piece), c0, row0);
                         store_commit();
-                        if (p.has_res && tile + next < p.n_tiles) {
+                        if (p.has_res && ok && tile + next < p.n_tiles) {
                             store_wait_read();
                             fetch_residual(tile + next);
+                            ++fetched;
                         }
                     }
                 }
             }
         }
-        if (KIND == kTiles && lane == 0) {
+        if (!GATED && lane == 0) {
             store_wait_all();  // shared memory outlives its stores, and after an expired wait the residual's copies
             int dummy = 0;
-            if (*abort_flag && p.has_res && !p.plain && i)
-                mbar_wait(smem_u32(&res_full[w]), (i - 1) & 1u, (volatile int *)&dummy, p.err);
+            if (*abort_flag && p.has_res && !kPlain && fetched)
+                mbar_wait(smem_u32(&res_full[w]), (fetched - 1) & 1u, (volatile int *)&dummy, p.err);
         }
         __syncwarp();
     }
@@ -524,14 +563,14 @@ bool maps_of(CUtensorMap *codes, CUtensorMap *scale, const Mx &m, int64_t rows, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND, int ACT>
+template <int KIND, int VARIANT>
 pmha_status launch(Params &p, const char *stage, cudaStream_t s)
 {
     constexpr int kSmem = Cfg<KIND>::kSmem;
     p.err = device_error_word();
     if (!p.err) return PMHA_ERR_CUDA;
     int pairs = 0;
-    auto kern = k_mx<KIND, ACT>;
+    auto kern = k_mx<KIND, VARIANT>;
     static std::atomic<int> known[kKnownDevices];
     const pmha_status st = pairs_at_once(kern, kThreads, kSmem, known, &pairs);
     if (st != PMHA_OK) return st;
@@ -560,23 +599,36 @@ pmha_status tiles_of(Params &p, int64_t M, int64_t N, int64_t K, int cols, const
     return PMHA_OK;
 }
 
+// Tiles of 128 outputs instead of 256? Short products are bound by their outputs, which two teams of epilogue warps on
+// narrow tiles take without waiting for each other: 128 -> 384 at 320,000 tokens 45 us for 58, with a residual 81 for 105;
+// 512 -> 128 28 for 33, with a residual 39 for 47; 32,000 x 1,024 -> 1,024 with a residual 28.6 for 31.8. Long ones are bound
+// by the products, of which a narrow tile's take 0.6 of a wide one's time (8,192 x 4,096 -> 4,096 62 us for 51): there, the
+// fewer rounds of tiles by that weight (300 x 4,096 -> 1,024 7.4 for 9.6; 8,192 x 4,096 -> 512 12.2 for 10.7).
+bool narrow_tiles(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t pairs = std::max(1, num_sms() / 2), rows = ceil_div(M, 256);
+    auto rounds = [&](int64_t cols) { return ceil_div(rows * ceil_div(N, cols), pairs); };
+    return K <= 1024 || 5 * rounds(128) < 8 * rounds(256);
+}
+
 }  // namespace
 
 pmha_status mx_tc_linear(const MxLinear &a, const char *stage, cudaStream_t s)
 {
     Params p = {};
-    const pmha_status st = tiles_of(p, a.M, a.N, a.K, 256, stage);
+    const bool narrow = narrow_tiles(a.M, a.N, a.K), plain = a.N % 8 != 0;
+    const pmha_status st = tiles_of(p, a.M, a.N, a.K, narrow ? 128 : 256, stage);
     if (st != PMHA_OK) return st;
     p.bias0 = (const __nv_bfloat16 *)a.bias;
     p.has_res = a.residual != nullptr;
-    p.plain = a.N % 8 != 0;
     p.res_p = (const __nv_bfloat16 *)a.residual;
     p.out_p = (__nv_bfloat16 *)a.out;
-    if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.w, a.N, a.K) ||
-        (!p.plain && (!make_tile_map(&p.out, a.out, a.M, a.N, a.N, 2, 32) ||
+    if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.w, a.N, a.K, narrow ? 64 : 128) ||
+        (!plain && (!make_tile_map(&p.out, a.out, a.M, a.N, a.N, 2, 32) ||
                       (a.residual && !make_tile_map(&p.res, a.residual, a.M, a.N, a.N, 2, 32)))))
         return map_failed(stage);
-    return launch<kTiles, 0>(p, stage, s);
+    if (narrow) return plain ? launch<kNarrow, 1>(p, stage, s) : launch<kNarrow, 0>(p, stage, s);
+    return plain ? launch<kTiles, 1>(p, stage, s) : launch<kTiles, 0>(p, stage, s);
 }
 
 pmha_status mx_tc_gated(const MxGated &a, cudaStream_t s)

@@ -96,7 +96,8 @@ def check_linear(x, w, bias, residual, got):
     (1, 1, 1), (1, 32, 8), (1, 256, 1024), (1, 512, 2048), (1, 4096, 100), (2, 33, 17), (3, 171, 40), (4, 1000, 96), (8, 64, 24),
     (8, 2400, 64), (5, 4096, 72), (9, 32, 8), (9, 64, 16), (16, 128, 128), (100, 256, 256), (128, 200, 264), (129, 300, 7),
     (200, 100, 513), (256, 512, 512), (300, 257, 384), (511, 1025, 130), (1000, 2048, 1000), (77, 40, 1), (2000, 128, 24),
-    (20_000, 256, 300)])
+    (20_000, 256, 300), (20_000, 64, 301), (6, 1024, 4096), (7, 1024, 4096), (8000, 1100, 511), (9000, 1030, 1280),
+    (9000, 1030, 1281)])
 @pytest.mark.parametrize("extra", [False, True])
 def test_linear(rows, width, outputs, extra):
     x, w = tokens(10, rows, width), normal(20, outputs, width, s=width ** -0.5)
