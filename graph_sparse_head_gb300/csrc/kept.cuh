@@ -75,8 +75,18 @@ __device__ __forceinline__ float kept_codes(const Vals<T, VEC> &v, uint32_t (&w)
 #pragma unroll
     for (int o = kGroup / VEC / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
     const float scale = kept_scale(most), inv = kept_inverse(scale);
+    if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {  // kept_code of two values an instruction
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] = kept_code<T>(to_f<T>(v.v[i]), scale, inv);
+        for (int i = 0; i < VEC; i += 2) {
+            float a, b;
+            add2(fma2(Pair(to_f<T>(v.v[i]), to_f<T>(v.v[i + 1])), Pair(inv, inv), Pair(6144.f, 6144.f)),
+                 Pair(12582912.f, 12582912.f)).get(a, b);
+            w[i] = __float_as_uint(a), w[i + 1] = __float_as_uint(b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = kept_code<T>(to_f<T>(v.v[i]), scale, inv);
+    }
     return scale;
 }
 // Keeps them at these places; `first`: the group's first lane, which writes the scale.

@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t most)
     const int b = e - ((most & 0x7fffffu) <= 0x400000u ? 2 : 1);  // 6 2^e = 1.5 2^(e + 2)
     return e >= 255 ? 255u : (uint32_t)max(b, 0);
 }
-// 2^(127 - byte), for bytes up to 253; 0 for 255 (of a block whose scale is NaN the codes are zeros)
+// 2^(127 - byte), for bytes up to 253; 0 for 255 (of a block whose scale is NaN any code will do)
 __device__ __forceinline__ float mx_inverse(uint32_t byte) { return __uint_as_float((uint32_t)max(254 - (int)byte, 0) << 23); }
 // 2^(byte - 127), NaN for 255
 __device__ __forceinline__ float mx_scale_value(uint32_t byte)
@@ -65,6 +65,20 @@ __device__ __forceinline__ float mx_scale_value(uint32_t byte)
 __device__ __forceinline__ uint32_t mx_byte(float low, float high)
 {
     return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(low, high), __NV_E2M1, cudaRoundNearest);
+}
+// Eight values as codes, the first in the lowest half byte
+__device__ __forceinline__ uint32_t mx_word(const float *f)
+{
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return w;
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 

@@ -167,21 +167,6 @@ __device__ __forceinline__ Pair hidden2(Pair g, Pair u)
         return mul2(fma2(Pair(-z0, -z1), q, Pair(fmaxf(g0, 0.f), fmaxf(g1, 0.f))), u);
     }
 }
-// Eight values as codes, the first in the lowest half byte
-__device__ __forceinline__ uint32_t mx_word(const float (&f)[8])
-{
-    uint32_t w;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(w)
-        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
-    return w;
-}
-
 // VARIANT: gated, the activation; else whether outputs go through plain loads and stores (which cost registers)
 template <int KIND, int VARIANT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(const __grid_constant__ Params p)

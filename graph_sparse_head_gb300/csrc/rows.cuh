@@ -30,8 +30,13 @@ template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// VEC consecutive values as one load or store (16, 4 or 2 bytes).
+// VEC consecutive values as one load or store (16, 4 or 2 bytes), or as two of 16.
+struct alignas(16) TwoPieces {
+    uint4 a, b;
+};
 template <typename T, int VEC> struct Pack;
+template <> struct Pack<float, 8> { using type = TwoPieces; };
+template <> struct Pack<__nv_bfloat16, 16> { using type = TwoPieces; };
 template <> struct Pack<float, 4> { using type = uint4; };
 template <> struct Pack<float, 1> { using type = uint32_t; };
 template <> struct Pack<__nv_bfloat16, 8> { using type = uint4; };
@@ -39,6 +44,7 @@ template <> struct Pack<__nv_bfloat16, 2> { using type = uint32_t; };
 template <> struct Pack<__nv_bfloat16, 1> { using type = uint16_t; };
 // VEC bytes
 template <int VEC> struct Bytes;
+template <> struct Bytes<16> { using type = uint4; };
 template <> struct Bytes<8> { using type = uint2; };
 template <> struct Bytes<4> { using type = uint32_t; };
 template <> struct Bytes<2> { using type = uint16_t; };
@@ -54,7 +60,7 @@ __device__ __forceinline__ void store(T *p, const T (&v)[VEC])
 {
     *reinterpret_cast<typename Pack<T, VEC>::type *>(p) = *reinterpret_cast<const typename Pack<T, VEC>::type *>(v);
 }
-template <typename T, int VEC> struct alignas(sizeof(typename Pack<T, VEC>::type)) Vals {
+template <typename T, int VEC> struct alignas(alignof(typename Pack<T, VEC>::type)) Vals {
     T v[VEC];
 };
 
@@ -95,9 +101,12 @@ __device__ __forceinline__ typename Bytes<VEC>::type low_bytes(const uint32_t (&
     if constexpr (VEC == 1) return (uint8_t)w[0];
     else if constexpr (VEC == 2) return (uint16_t)__byte_perm(w[0], w[1], 0x0040);
     else {
-        const uint32_t a = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
-        if constexpr (VEC == 4) return a;
-        else return make_uint2(a, __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
+        auto four = [&](int i) {
+            return __byte_perm(__byte_perm(w[i], w[i + 1], 0x0040), __byte_perm(w[i + 2], w[i + 3], 0x0040), 0x5410);
+        };
+        if constexpr (VEC == 4) return four(0);
+        else if constexpr (VEC == 8) return make_uint2(four(0), four(4));
+        else return make_uint4(four(0), four(4), four(8), four(12));
     }
 }
 

@@ -131,7 +131,8 @@ def test_large_and_zero_rows(width, dt):
 # ---------------------------------------------------------------- 8 bits
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,width", [(1, 1), (3, 2), (5, 31), (4, 32), (7, 33), (9, 40), (33, 128), (2, 171), (11, 1000),
-                                        (3, 2049), (1, 70_000), (5000, 24)])
+                                        (3, 2049), (1, 70_000), (5000, 24), (4001, 171), (1001, 7), (300, 33), (600, 6), (100, 3),
+                                        (64, 48)])
 def test_checkpoint_codes_are_those_of_exact_arithmetic(rows, width, dt):
     x = normal(20, rows, width, s=3.0, dtype=TYPES[dt])
     x = x * torch.exp2(torch.randint(-8, 9, (rows, 1), device=DEV)).to(x.dtype)
