@@ -42,7 +42,6 @@ constexpr int kSfA = 2 * 512;         // scale tiles of a stage: 128 rows x 256 
 // 4,096 x 4,096 50.0 us for 50.9, with a residual 85 for 58); two stages and two output pieces a warp for rows of up to 512
 // columns (320,000 x 128 -> 384 with a residual 101 us for 105, without one 60 for 58).
 enum Kind { kTiles, kNarrow, kGated };
-constexpr int kPiece = 32 * 128;      // 32 x 64 bf16 of an epilogue warp
 template <int KIND>
 struct Cfg {
     static constexpr bool kGate = KIND == kGated;
@@ -55,9 +54,11 @@ struct Cfg {
     static_assert(kStage % 1024 == 0, "swizzled tiles lie on 1024 bytes");
     static constexpr int kAccs = KIND == kTiles ? 1 : 3, kAccCols = kOps * kCols;
     static constexpr int kTeams = KIND == kTiles ? 1 : 2;        // of epilogue warps, which take tiles in turn
-    static constexpr int kStages = KIND == kTiles ? 4 : 5;
+    static constexpr int kStages = 5;
     static constexpr int kScaleCol = kAccs * kAccCols;  // then 24 scale columns a stage
     static_assert(kScaleCol + 24 * kStages <= 512, "tensor memory");
+    // An epilogue warp's 32 x 64 outputs leave in one piece of shared memory or in two
+    static constexpr int kPieceCols = KIND == kTiles ? 32 : 64, kPiece = 32 * kPieceCols * 2;
     static constexpr int kTile = kGate ? 0 : 16 * kPiece;
     static constexpr int kVec = 16 * 64 * 4;  // a warp's biases: of 64 outputs, or 32 of gate and of up
     static constexpr int kBars = 512;
@@ -301,15 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
         const uint32_t empty_bar = map_rank(smem_u32(acc_empty), 0);
         const int first = pair + team * n_pairs, next = C::kTeams * n_pairs;
         float *bias = vec_s + w * 64;
-        uint8_t *piece = tile_s + w * kPiece;
+        auto in_piece = [](int r, int u) {  // 16 bytes u of row r, as TMA places them (128- or 64-byte rows)
+            return C::kPieceCols == 64 ? swizzled(r, u) : (uint32_t)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+        };
+        uint8_t *piece = tile_s + w * C::kPiece;
         constexpr float kg = GATED ? Act<VARIANT>::kGate : 1.f, ku = GATED ? Act<VARIANT>::kUp : 1.f;
         auto rows_of = [&](int tile) { return tile / p.tiles_n * 256 + (int)rank * 128 + quarter * 32; };
         auto column_of = [&](int tile) { return tile % p.tiles_n * kCols + part * (GATED ? 32 : 64); };
-        auto fetch_residual = [&](int tile) {
+        auto fetch_residual = [&](int tile, int half) {
             if (GATED || kPlain || !p.has_res || lane) return;
-            const int row = rows_of(tile), c = column_of(tile);
+            const int row = rows_of(tile), c = column_of(tile) + half * C::kPieceCols;
             if (row < p.M && c < p.N) {
-                mbar_arrive_expect_tx(smem_u32(&res_full[w]), kPiece);
+                mbar_arrive_expect_tx(smem_u32(&res_full[w]), C::kPiece);
                 tma_load_2d(smem_u32(piece), &p.res, c, row, smem_u32(&res_full[w]));
             } else {
                 mbar_arrive(smem_u32(&res_full[w]));
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
         };
         uint32_t i = (uint32_t)team, fetched = 0;  // tiles of all teams, residual copies of this warp
         if (first < p.n_tiles) {
-            fetch_residual(first);
+            fetch_residual(first, 0);
             fetched = 1;
             fetch_bias(first);
         }
@@ -428,78 +432,83 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                         (uint8_t)byte;
                 }
             } else {
+                constexpr int kHalves = 64 / C::kPieceCols;
                 bool ok = true;
                 // plain rows: a lane a column, of eight rows at a time
-                auto by_rows = [&](auto load, auto store) {
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = lane + 32 * h;
-                        if (c0 + c >= p.N) return;
+                auto by_rows = [&](int first_col, auto load, auto store) {
+                    for (int h = 0; h < C::kPieceCols / 32; ++h) {
+                        const int c = lane + 32 * h, col = first_col + c;
+                        if (col >= p.N) return;
                         for (int q0 = 0; q0 < 32; q0 += 8) {
                             __nv_bfloat16 x[8];
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
-                                if (row0 + q0 + q < p.M) x[q] = load(q0 + q, c, (size_t)(row0 + q0 + q) * p.N + c0 + c);
+                                if (row0 + q0 + q < p.M) x[q] = load(q0 + q, c, (size_t)(row0 + q0 + q) * p.N + col);
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
-                                if (row0 + q0 + q < p.M) store(q0 + q, c, (size_t)(row0 + q0 + q) * p.N + c0 + c, x[q]);
+                                if (row0 + q0 + q < p.M) store(q0 + q, c, (size_t)(row0 + q0 + q) * p.N + col, x[q]);
                         }
                     }
                 };
-                if constexpr (kPlain) {
-                    if (p.has_res) {
-                        by_rows([&](int q, int c, size_t at) { return p.res_p[at]; },
-                                [&](int q, int c, size_t at, __nv_bfloat16 x) {
-                                    *(__nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2) = x;
-                                });
+                auto value = [&](int q, int c) { return (__nv_bfloat16 *)(piece + in_piece(q, c >> 3) + (c & 7) * 2); };
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half) {
+                    const int col = c0 + half * C::kPieceCols;
+                    if constexpr (kPlain) {
+                        __syncwarp();
+                        if (p.has_res) {
+                            by_rows(col, [&](int q, int c, size_t at) { return p.res_p[at]; },
+                                    [&](int q, int c, size_t at, __nv_bfloat16 x) { *value(q, c) = x; });
+                            __syncwarp();
+                        }
+                    } else if (p.has_res) {
+                        ok = ok && wait_bar(smem_u32(&res_full[w]), (i / C::kTeams * kHalves + half) & 1u, abort_flag, p.err);
+                    } else {
+                        if (lane == 0) store_wait_read();  // the last store has read the piece
                         __syncwarp();
                     }
-                } else if (p.has_res) {
-                    ok = wait_bar(smem_u32(&res_full[w]), (i / C::kTeams) & 1u, abort_flag, p.err);
-                } else {
-                    if (lane == 0) store_wait_read();  // the last tile's store has read the piece
-                    __syncwarp();
-                }
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    uint4 *at = reinterpret_cast<uint4 *>(piece + swizzled(lane, u));
-                    const uint32_t *acc8;
-                    if constexpr (KIND == kNarrow) {
-                        const int q = u / 2;
-                        if (u % 2 == 0) {
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                            pin(v[q & 1]);
-                            if (q < 3)
-                                tmem_ld16(t0 + (uint32_t)(acc * C::kAccCols + 16 * (q + 1)), v[(q + 1) & 1]);
-                            else
-                                hand_back();
+                    for (int x = 0; x < C::kPieceCols / 8; ++x) {
+                        const int u = half * (C::kPieceCols / 8) + x;
+                        uint4 *at = reinterpret_cast<uint4 *>(piece + in_piece(lane, x));
+                        const uint32_t *acc8;
+                        if constexpr (KIND == kNarrow) {
+                            const int q = u / 2;
+                            if (u % 2 == 0) {
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                                pin(v[q & 1]);
+                                if (q < 3)
+                                    tmem_ld16(t0 + (uint32_t)(acc * C::kAccCols + 16 * (q + 1)), v[(q + 1) & 1]);
+                                else
+                                    hand_back();
+                            }
+                            acc8 = &v[q & 1][8 * (u % 2)];
+                        } else {
+                            acc8 = &v[u / 4][8 * (u % 4)];
                         }
-                        acc8 = &v[q & 1][8 * (u % 2)];
+                        uint32_t rw[4] = {0, 0, 0, 0};
+                        if (p.has_res) {
+                            const uint4 q = *at;
+                            rw[0] = q.x, rw[1] = q.y, rw[2] = q.z, rw[3] = q.w;
+                        }
+                        *at = sums(u, acc8, rw);
+                    }
+                    if constexpr (kPlain) {
+                        __syncwarp();
+                        by_rows(col, [&](int q, int c, size_t at) { return *value(q, c); },
+                                [&](int q, int c, size_t at, __nv_bfloat16 x) { p.out_p[at] = x; });
                     } else {
-                        acc8 = &v[u / 4][8 * (u % 4)];
-                    }
-                    uint32_t rw[4] = {0, 0, 0, 0};
-                    if (p.has_res) {
-                        const uint4 q = *at;
-                        rw[0] = q.x, rw[1] = q.y, rw[2] = q.z, rw[3] = q.w;
-                    }
-                    *at = sums(u, acc8, rw);
-                }
-                if constexpr (kPlain) {
-                    __syncwarp();
-                    by_rows([&](int q, int c, size_t at) {
-                                return *(const __nv_bfloat16 *)(piece + swizzled(q, c >> 3) + (c & 7) * 2);
-                            },
-                            [&](int q, int c, size_t at, __nv_bfloat16 x) { p.out_p[at] = x; });
-                } else {
-                    fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (row0 < p.M && c0 < p.N) tma_store_tile(&p.out, smem_u32(piece), c0, row0);
-                        store_commit();
-                        if (p.has_res && ok && tile + next < p.n_tiles) {
-                            store_wait_read();
-                            fetch_residual(tile + next);
-                            ++fetched;
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (row0 < p.M && col < p.N) tma_store_tile(&p.out, smem_u32(piece), col, row0);
+                            store_commit();
+                            const bool last = half + 1 == kHalves;
+                            if (p.has_res && ok && (!last || tile + next < p.n_tiles)) {
+                                store_wait_read();
+                                fetch_residual(last ? tile + next : tile, last ? 0 : half + 1);
+                                ++fetched;
+                            }
                         }
                     }
                 }
@@ -546,6 +555,18 @@ bool maps_of(CUtensorMap *codes, CUtensorMap *scale, const Mx &m, int64_t rows, 
     return fn(scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(m.scale), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// (rows, cols) bf16 in boxes of 32 rows x piece_cols, as the epilogue warps' pieces
+bool map_of_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int piece_cols)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(cols * 2)};
+    cuuint32_t box[2] = {(cuuint32_t)piece_cols, 32}, estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, piece_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KIND, int VARIANT>
@@ -604,13 +625,14 @@ pmha_status mx_tc_linear(const MxLinear &a, const char *stage, cudaStream_t s)
     const bool narrow = narrow_tiles(a.M, a.N, a.K), plain = a.N % 8 != 0;
     const pmha_status st = tiles_of(p, a.M, a.N, a.K, narrow ? 128 : 256, stage);
     if (st != PMHA_OK) return st;
+    const int piece = narrow ? Cfg<kNarrow>::kPieceCols : Cfg<kTiles>::kPieceCols;
     p.bias0 = (const __nv_bfloat16 *)a.bias;
     p.has_res = a.residual != nullptr;
     p.res_p = (const __nv_bfloat16 *)a.residual;
     p.out_p = (__nv_bfloat16 *)a.out;
     if (!maps_of(&p.a, &p.sa, a.x, a.M, a.K) || !maps_of(&p.b0, &p.sb0, a.w, a.N, a.K, narrow ? 64 : 128) ||
-        (!plain && (!make_tile_map(&p.out, a.out, a.M, a.N, a.N, 2, 32) ||
-                      (a.residual && !make_tile_map(&p.res, a.residual, a.M, a.N, a.N, 2, 32)))))
+        (!plain && (!map_of_rows(&p.out, a.out, a.M, a.N, piece) ||
+                    (a.residual && !map_of_rows(&p.res, a.residual, a.M, a.N, piece)))))
         return map_failed(stage);
     if (narrow) return plain ? launch<kNarrow, 1>(p, stage, s) : launch<kNarrow, 0>(p, stage, s);
     return plain ? launch<kTiles, 1>(p, stage, s) : launch<kTiles, 0>(p, stage, s);
