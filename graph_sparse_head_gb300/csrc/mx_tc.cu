@@ -244,37 +244,37 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
         }
     } else if (warp == 1) {
         if (rank == 0) {
-            // ---------------- issuer of the pair: the whole warp walks, one lane issues
-            const bool one = elect_one();
-            uint32_t used = 0, i = 0;
-            bool ok = true;
-            for (int tile = pair; tile < p.n_tiles && ok; tile += n_pairs, ++i) {
-                const int acc = (int)(i % kAccs);
-                if (!wait_bar(smem_u32(&acc_empty[acc]), ((i / kAccs) & 1u) ^ 1u, abort_flag, p.err)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * C::kAccCols);
-                // of a scale tile's four columns of 32 rows, the first of this tile's
-                const uint32_t half = GATED ? 2u * ((uint32_t)(tile % p.tiles_n) & 1u) : 0u;
-                for (int kb = 0; kb < p.kb; ++kb, ++used) {
-                    const int stage = (int)(used % kStages);
-                    ok = wait_bar(smem_u32(&full[stage]), (used / kStages) & 1u, abort_flag, p.err);
-                    if (!ok) break;
+            // ---------------- issuer of the pair: one lane, which waits and issues by itself
+            if (elect_one()) {
+                uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 1;
+                const uint32_t base = smem_u32(smem);
+                const uint64_t a_first = smem_desc(base), b_first = smem_desc(base + kBox);
+                const uint64_t sa_first = scale_desc(base + kBox + C::kB), sb_first = scale_desc(base + kBox + C::kB + kSfA);
+                bool ok = true;
+                for (int tile = pair; tile < p.n_tiles && ok; tile += n_pairs) {
+                    if (!wait_bar(smem_u32(&acc_empty[acc]), acc_phase, abort_flag, p.err)) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBox, ssa = sb + C::kB, ssb = ssa + kSfA;
-                    const int steps = min(4, p.k64 - 4 * kb);  // products of 64 columns, up to the width's end
-                    if (one) {
-                        // scale columns of this stage: 2 x 4 of the tokens, then 2 x 8 of the weights (128 columns
-                        // of K, then 256 rows, or 128 of gate and of up)
-                        const uint32_t ca = tmem + (uint32_t)(C::kScaleCol + 24 * stage), cb = ca + 8;
-                        const uint64_t da = smem_desc(sa), db = smem_desc(sb);
+                    const uint32_t d = tmem + acc * C::kAccCols;
+                    // of a scale tile's four columns of 32 rows, the first of this tile's
+                    const uint32_t half = GATED ? 2u * ((uint32_t)(tile % p.tiles_n) & 1u) : 0u;
+                    for (int kb = 0; kb < p.kb; ++kb) {
+                        ok = wait_bar(smem_u32(&full[stage]), phase, abort_flag, p.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int steps = p.k64 - 4 * kb;  // products of 64 columns left, up to the width's end
+                        // scale columns of this stage: 2 x 4 of the tokens, then 2 x 8 of the weights (128 columns of K,
+                        // then 256 rows, or 128 of gate and of up)
+                        const uint32_t ca = tmem + C::kScaleCol + 24 * stage, cb = ca + 8;
+                        const uint64_t at = (uint64_t)(stage * (kStage / 16));  // of the address field, 16 bytes each
+                        const uint64_t da = a_first + at, db = b_first + at, dsa = sa_first + at, dsb = sb_first + at;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {  // 64 values = 32 bytes along K = 2 in the address field
                             if (k >= steps) break;
                             if (k % 2 == 0) {
                                 const int h = k / 2;
-                                copy_scales(ca + 4 * h, scale_desc(ssa + 512 * h));
-                                copy_scales(cb + 8 * h, scale_desc(ssb + 512 * h));
-                                if constexpr (C::kSfTiles == 2) copy_scales(cb + 8 * h + 4, scale_desc(ssb + 1024 + 512 * h));
+                                copy_scales(ca + 4 * h, dsa + 32 * h);
+                                copy_scales(cb + 8 * h, dsb + 32 * h);
+                                if constexpr (C::kSfTiles == 2) copy_scales(cb + 8 * h + 4, dsb + 64 + 32 * h);
                             }
 #pragma unroll
                             for (int o = 0; o < C::kOps; ++o)
@@ -283,16 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                                        cb + 8 * (k >> 1) + 4 * o + half, kb > 0 || k > 0 ? 1u : 0u);
                         }
                         mma_commit_pair(smem_u32(&empty[stage]));
+                        if (++stage == kStages) stage = 0, phase ^= 1u;
                     }
-                    __syncwarp();
+                    if (ok) mma_commit_pair(smem_u32(&acc_full[acc]));
+                    if (++acc == kAccs) acc = 0, acc_phase ^= 1u;
                 }
-                if (one && ok) mma_commit_pair(smem_u32(&acc_full[acc]));
-                __syncwarp();
+                mma_commit_pair(smem_u32(mma_done));
+                int dummy = 0;
+                mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
             }
-            if (one) mma_commit_pair(smem_u32(mma_done));
             __syncwarp();
-            int dummy = 0;
-            mbar_wait(smem_u32(mma_done), 0, (volatile int *)&dummy, p.err);
         }
     } else {
         // ---------------- epilogue: a warp 32 rows and 64 accumulator columns of a tile, of which teams take turns
