@@ -32,7 +32,10 @@ constexpr size_t kRingBytes = (size_t)kRingOf<T, VEC, NV> * NV * kSlotBytes;
 
 // A team (join.cuh) walks rows of one gate and keeps its columns' two sums over rows in
 // registers; a block adds its teams' through shared memory and writes one partial row of each. As in the forward pass,
-// addresses are one running offset and copies are skipped where there is nothing to copy.
+// addresses are one running offset and copies are skipped where there is nothing to copy. Bound by memory where rows are many:
+// 1,280,000 x 256 bf16 601 us, 96 % of the copy rate; 320,000 x 128 88 us, 83 of them without the sums over rows; from 8
+// bits 80. 114 registers, two blocks an SM: the sums' and the weights' columns stay in them (three blocks an SM with the
+// weights in shared memory spilled, 95 us).
 template <typename T, int VEC, int NV, int LPR, bool KEPT>
 __global__ void __launch_bounds__(kThreads, 2) k_join_bwd(JoinBwdArgs a)
 {

@@ -4,15 +4,16 @@
 //   gated   h = act(x Wg^T + bg) * (x Wu^T + bu), in 4 bits      tile 256 tokens x 64 hidden, gate and up side by side
 //
 // Two CTAs form a pair (tc_pair.cuh). Each has 18 warps: warp 0 copies stages of
-// 256 columns of codes (128 bytes a row, two values a byte) and the scale tiles that belong to them by TMA, warp
+// 256 columns of codes (128 bytes a row, two values a byte) and the scale tiles that belong to them by TMA, a lane of warp
 // 1 of the even CTA copies the scale tiles to tensor memory (tcgen05.cp, into both CTAs) and issues tcgen05.mma
-// kind::mxf4, whose scaling by block is the hardware's; sixteen warps turn accumulators into outputs. Linear: 256
-// accumulator columns and the scales of four stages fill tensor memory, there is one set; an epilogue thread takes all of its
-// accumulators into registers (64) and hands the set back at once, so that the next products run under its arithmetic. With
-// 128 columns there are three sets, and two teams of eight warps that take the tiles in turn. Gated: three sets of 64 gates
-// and 64 ups and two teams, one team's waits under the other's special functions, 16 columns' accumulators on their way while
-// 16 are used (320,000 x 128 x 512 in 98 us; with one set of 128 + 128, one team and all accumulators in registers at once
-// 112).
+// kind::mxf4, whose scaling by block is the hardware's; sixteen warps turn accumulators into outputs.
+// Linear, 256 outputs: accumulators and the scales of the stages leave no room for a second set in tensor memory; an
+// epilogue thread takes all of its accumulators into registers (64) and hands the set back at once, so that the next
+// products run under its arithmetic (8,192 x 4,096 -> 4,096 in 45.5 us, 6.0 PFLOP/s). 128 outputs: three sets, and two teams
+// of eight warps that take the tiles in turn (320,000 x 128 -> 384 in 44 us, 88 % of the copy rate, with a residual 81,
+// 94 %). Gated: three sets of 64 gates and 64 ups and two teams, one team's waits under the other's special functions, 16
+// columns' accumulators on their way while 16 are used (320,000 x 128 x 512 in 98 us; with one set of 128 + 128, one team
+// and all accumulators in registers at once 112).
 // Epilogue warps go their own ways: each has its 32 rows' share of the columns, its own piece of shared memory, its own
 // copies of the residual and of the result, and no barrier with the others. (With a barrier for all sixteen around each
 // step the same took 152 us.)
@@ -38,9 +39,8 @@ using namespace tcu;
 constexpr int kThreads = 64 + 512;
 constexpr int kBox = 128 * 128;       // bytes of a tile of 128 rows of 128 bytes
 constexpr int kSfA = 2 * 512;         // scale tiles of a stage: 128 rows x 256 columns
-// Not kept in the linear kernel: six stages instead of four, its outputs straight from registers to make room (8,192 x
-// 4,096 x 4,096 50.0 us for 50.9, with a residual 85 for 58); two stages and two output pieces a warp for rows of up to 512
-// columns (320,000 x 128 -> 384 with a residual 101 us for 105, without one 60 for 58).
+// Not kept for tiles of 256 outputs: four stages, with output pieces of 64 columns (8,192 x 4,096 -> 4,096 51.5 us for 45.5);
+// six, with outputs straight from registers to make room (50.0, with a residual 85 for 51).
 enum Kind { kTiles, kNarrow, kGated };
 template <int KIND>
 struct Cfg {
