@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) k_join_sums(JoinSumArgs a)
         for (int i = t; i < n; i += 32) {
             const float v = part[(at + i) * a.width + c];
             if (weighted) {
-                const float g = to_f<T>(((const T *)a.gate)[i / a.blocks_per_gate * a.width + c]);
+                const float g = to_f<T>(((const T *)a.gate)[(long long)(i / a.blocks_per_gate) * a.width + c]);
                 const float p = __fmul_rn(v, g);
                 s = add(s, Two{p, __fmaf_rn(v, g, -p)});
             } else {

@@ -19,10 +19,11 @@ namespace pmha {
 namespace {
 
 // ---------------------------------------------------------------- quantisation
-// A block of threads takes a scale tile, 128 rows by 128 columns: a lane VEC values, 32 / VEC lanes a block of 32, two 16-byte
-// loads a lane where the width allows (one: 320,000 x 128 bf16 20 us, bound by instructions). Some rows' values are loaded before the first of them is used; the scales are gathered in shared memory and written as one
-// piece, zeros for blocks and rows that are not there. Where rows do not lie on 16-byte boundaries a lane's values go one by
-// one, but stay next to one another: one value a lane made every lane do a whole block's sums (100,000 x 171 62 us).
+// A block of threads takes a scale tile, 128 rows by 128 columns: a lane VEC values, 32 / VEC lanes a block of 32, two
+// 16-byte loads a lane where the width allows (one: 320,000 x 128 bf16 20 us, bound by instructions). Some rows' values are
+// loaded before the first of them is used; the scales are gathered in shared memory and written as one piece, zeros for
+// blocks and rows that are not there. Where rows do not lie on 16-byte boundaries a lane's values go one by one, but stay
+// next to one another: one value a lane made every lane do a whole block's sums (100,000 x 171 62 us for 16).
 // Bound by memory: 320,000 x 128 bf16 in 15.3 us, the copy rate.
 template <typename T, int VEC, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long rows, int width, int tiles, uint8_t *codes,
@@ -49,7 +50,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T *x, long long 
             const int r = p0 + i * kRows + r_first;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[i].v[e] = from_f<T>(0.f);
-            if (r < r_end && c < width) load_some<T, VEC, ALIGNED>(x_first + (size_t)(unsigned)r * (unsigned)width, width - c, v[i]);
+            if (r < r_end && c < width)
+                load_some<T, VEC, ALIGNED>(x_first + (size_t)(unsigned)r * (unsigned)width, width - c, v[i]);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {

@@ -43,6 +43,28 @@ def test_join_and_checkpoints(rows, width):
     assert torch.equal(back[-1000:], pmha.pmha_checkpoint_restore(kept1))
 
 
+def test_gates_of_every_row():
+    """More than 2^31 gate values: dpost sums over all of them."""
+    rows, width = 16_800_000, 128
+    assert rows * width > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(9)
+    post = (1 + 0.1 * torch.randn(width, generator=g, device=DEV)).to(BF16)
+    gate, branch, ds = big(1, rows, width), big(2, rows, width), big(3, rows, width)
+    gate[-1000:] *= 8  # their part is no small one
+    got = pmha.pmha_join_backward(pmha.JoinParams(post=post, gate=gate), branch, None, None, ds, input_grads=False)
+    want, mag = (torch.zeros(width, dtype=torch.float64, device=DEV) for _ in range(2))
+    for at in range(0, rows, 400_000):
+        b = branch[at:at + 400_000].double()
+        t = gate[at:at + 400_000].double() * ds[at:at + 400_000].double() * b * (b.square().mean(-1, True) + 1e-6).rsqrt()
+        want += t.sum(0)
+        mag += t.abs().sum(0)
+    # a root within 2^-21 and two products, each rounded, a row; sums as pairs
+    assert bool(((got["dpost"].double() - want).abs() <= 2.0 ** -20 * mag + 2.0 ** -23 * want.abs()).all())
+    b = branch[-5:].double()
+    r = ds[-5:].double() * b * (b.square().mean(-1, True) + 1e-6).rsqrt() * post.double()
+    assert bool(((got["dgate"][-5:].double() - r).abs() <= 2.0 ** -20 * r.abs()).all())
+
+
 def test_quantize_linear_and_block():
     rows, width, outputs = 34_000_000, 64, 72
     assert rows * width > 2 ** 31 and rows * outputs > 2 ** 31
