@@ -250,6 +250,40 @@ def test_batches_capture_streams_and_workspace():
     assert pmha.pmha_ffn_forward_mx(params, none).shape == (0, 100, E)
 
 
+def test_calls_at_once():
+    """Products, blocks and joins on three streams at the same time, some of them captured: the results of each alone."""
+    E, F = 256, 1024
+    block = pmha.FfnParams(normal(20, F, E, s=E ** -0.5), normal(21, F, E, s=E ** -0.5), normal(22, E, F, s=F ** -0.5))
+    params = pmha.FfnMxParams.from_params(block)
+    w = pmha.pmha_mx_quantize(normal(23, 1280, 1030, s=0.03))
+    join = pmha.JoinParams(pre=normal(1, E), post=normal(2, E), gate=normal(3, 8, E))
+    x, y = normal(10, 4000, E), normal(11, 6000, 1030)
+
+    def step():
+        s, n, kept, _ = pmha.pmha_join_checkpointed(join, x, x, keep_residual=False)
+        g = pmha.pmha_join_backward(join, kept, s, n, x)
+        f = pmha.pmha_ffn_forward_mx(params, pmha.pmha_mx_quantize(n), residual=s)
+        return [f, g["dbranch"], g["dgate"], g["dpost"], pmha.pmha_mx_linear(pmha.pmha_mx_quantize(y), w)]
+
+    want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        graph.replay()
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(step())
+    torch.cuda.synchronize()
+    pmha.pmha_device_status()
+    for out in (captured, *got):
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_weights_written_by_the_launch_before():
     """Quantisation of the weights right in front of the products that read them, many times over: no product starts early."""
     E, F = 256, 1024
