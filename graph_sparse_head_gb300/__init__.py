@@ -888,7 +888,7 @@ def pmha_ffn_backward(params: FfnParams, x: torch.Tensor, dout: torch.Tensor, in
 class _Buffer:
     """What Checkpoint and MxTensor have in common: two arrays, codes and scales, given as tensors or lying in one
     allocation of which tensors are made when they are asked for (an allocation and a view take as long as a launch)."""
-    __slots__ = ("_codes", "_scale", "_buffer", "_at", "_pointers", "_shape", "_index")
+    __slots__ = ("_codes", "_scale", "_buffer", "_at", "_c", "_ref", "_shape", "_index")
 
     @property
     def codes(self) -> torch.Tensor:
@@ -920,7 +920,7 @@ class _Buffer:
         self._buffer = b = torch.empty(self._at + self._scale_layout()[0], dtype=torch.uint8, device=x.device)
         p = b.data_ptr()
         self._codes = self._scale = None
-        self._pointers = p, p + self._at
+        self._point(p, p + self._at)
 
     def _given(self, codes, scale):
         """Takes tensors, which must be of the layouts."""
@@ -931,7 +931,12 @@ class _Buffer:
             if _like(name, t, torch.Size(shape), dtype, self._index) is None:
                 raise ValueError(f"{name} is missing")
         self._codes, self._scale, self._buffer = codes, scale, None
-        self._pointers = codes.data_ptr(), scale.data_ptr()
+        self._point(codes.data_ptr(), scale.data_ptr())
+
+    def _point(self, codes, scale):
+        """The C struct of the arrays, which stay where they are, and a reference to it."""
+        self._c = c = self._STRUCT(codes, scale)
+        self._ref = ctypes.byref(c)
 
 
 class Checkpoint(_Buffer):
@@ -939,6 +944,7 @@ class Checkpoint(_Buffer):
     bfloat16 scale for every 32 values of a row, (..., ceil(width / 32)); value ~ code * scale. dtype: what it was.
     Checked when it is made; its parts are not exchanged afterwards."""
     __slots__ = ("_dtype",)
+    _STRUCT = _lib.PmhaKept
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype):
         if dtype not in _DTYPES:
@@ -947,6 +953,9 @@ class Checkpoint(_Buffer):
             raise ValueError("codes must be a CUDA tensor (..., width)")
         self._shape, self._dtype = codes.shape, dtype
         self._given(codes, scale)
+
+    def __reduce__(self):  # copies and pickles have arrays, and pointers, of their own
+        return Checkpoint, (self.codes, self.scale, self._dtype)
 
     dtype = property(lambda self: self._dtype)
 
@@ -966,17 +975,14 @@ class Checkpoint(_Buffer):
         k._allocate(x)
         return k
 
-    def _struct(self):
-        return _lib.PmhaKept(*self._pointers)
-
 
 def _kept_like(name, k, shape, dtype, index):
-    """The struct of a Checkpoint of a tensor of this shape, type and device."""
+    """The C argument of a Checkpoint of a tensor of this shape, type and device."""
     if k._dtype is not dtype:
         raise ValueError(f"{name} was kept from {k.dtype}, the call runs in {dtype}")
     if k._shape != shape or k._index != index:
         raise ValueError(f"{name} must be of {tuple(shape)} on cuda:{index}")
-    return k._struct()
+    return k._ref
 
 
 def pmha_checkpoint(x: torch.Tensor, stream=None) -> Checkpoint:
@@ -985,7 +991,7 @@ def pmha_checkpoint(x: torch.Tensor, stream=None) -> Checkpoint:
     shape, rows, width, dev = _rows_of("x", x)
     with _on(dev, stream):
         k = Checkpoint._empty(x)
-        st = _library().pmha_checkpoint(_DTYPES[x.dtype], rows, width, x.data_ptr(), ctypes.byref(k._struct()),
+        st = _library().pmha_checkpoint(_DTYPES[x.dtype], rows, width, x.data_ptr(), k._ref,
                                         _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_checkpoint")
@@ -1004,7 +1010,7 @@ def pmha_checkpoint_restore(kept: Checkpoint, out: torch.Tensor | None = None, s
             out = torch.empty(shape, dtype=dtype, device=kept.device)
             o = out.data_ptr()
         st = _library().pmha_checkpoint_restore(_DTYPES[dtype], shape.numel() // width if width else 0, width,
-                                                ctypes.byref(kept._struct()), o, _stream_of(dev, stream))
+                                                kept._ref, o, _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_checkpoint_restore")
     return out
@@ -1042,14 +1048,14 @@ def _join(params, branch, residual, keep_branch, keep_residual, stream):
         shape, dtype, dev = residual._shape, residual._dtype, residual._index
         rows, width = shape.numel(), shape[-1]
         rows = rows // width if width else 0
-        rk = ctypes.byref(residual._struct())
+        rk = residual._ref
     else:
         shape, rows, width, dev = _rows_of("residual", residual)
         dtype = residual.dtype
         r = residual.data_ptr()
     p = params._struct(dtype, width, dev)
     if type(branch) is Checkpoint:
-        bk = ctypes.byref(_kept_like("branch", branch, shape, dtype, dev))
+        bk = _kept_like("branch", branch, shape, dtype, dev)
     else:
         b = _like("branch", branch, shape, dtype, dev)
     with _on(dev, stream):
@@ -1060,8 +1066,8 @@ def _join(params, branch, residual, keep_branch, keep_residual, stream):
         if keep_residual:
             kr = Checkpoint._empty(residual)
         st = _library().pmha_join(ctypes.byref(p), rows, b, bk, r, rk, s.data_ptr(), None if out is None else out.data_ptr(),
-                                  None if kb is None else ctypes.byref(kb._struct()),
-                                  None if kr is None else ctypes.byref(kr._struct()), _stream_of(dev, stream))
+                                  None if kb is None else kb._ref,
+                                  None if kr is None else kr._ref, _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_join")
     return s, out, kb, kr
@@ -1115,7 +1121,7 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
     s = _like("sum", sum, shape, dtype, dev)
     dy, ds = _like("dout", dout, shape, dtype, dev), _like("dsum", dsum, shape, dtype, dev)
     if type(branch) is Checkpoint:
-        b, bk = None, ctypes.byref(_kept_like("branch", branch, shape, dtype, dev))
+        b, bk = None, _kept_like("branch", branch, shape, dtype, dev)
     else:
         b, bk = _like("branch", branch, shape, dtype, dev), None
     lib = _library()
@@ -1147,10 +1153,14 @@ class MxTensor(_Buffer):
     block k of a tile at 16 (r % 32) + 4 (r / 32) + k. shape: the tensor's. Checked when it is made; its parts are not
     exchanged afterwards."""
     __slots__ = ("_rows", "_width")
+    _STRUCT = _lib.PmhaMx
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, shape):
         self._of(torch.Size(shape))
         self._given(codes, scale)
+
+    def __reduce__(self):
+        return MxTensor, (self.codes, self.scale, tuple(self._shape))
 
     def _of(self, shape):
         self._shape = shape
@@ -1176,9 +1186,6 @@ class MxTensor(_Buffer):
         q._allocate(x)
         return q
 
-    def _struct(self):
-        return _lib.PmhaMx(*self._pointers)
-
     def values(self) -> torch.Tensor:
         """The values that it stands for, in float64 (values near float32's end can round to 2^128). Torch operations, for
         inspection: not for a hot path."""
@@ -1198,7 +1205,7 @@ def pmha_mx_quantize(x: torch.Tensor, stream=None) -> MxTensor:
     _, rows, width, dev = _rows_of("x", x)
     with _on(dev, stream):
         q = MxTensor._empty(x)
-        st = _library().pmha_mx_quantize(_DTYPES[x.dtype], rows, width, x.data_ptr(), ctypes.byref(q._struct()),
+        st = _library().pmha_mx_quantize(_DTYPES[x.dtype], rows, width, x.data_ptr(), q._ref,
                                          _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_mx_quantize")
@@ -1222,7 +1229,7 @@ def pmha_mx_linear(x: MxTensor, weight: MxTensor, bias: torch.Tensor | None = No
         if out is None:
             out = torch.empty(shape, dtype=bf16, device=x.device)
             o = out.data_ptr()
-        st = _library().pmha_mx_linear(x._rows, width, N, ctypes.byref(x._struct()), ctypes.byref(weight._struct()), b, r, o,
+        st = _library().pmha_mx_linear(x._rows, width, N, x._ref, weight._ref, b, r, o,
                                        _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_mx_linear")
@@ -1246,7 +1253,8 @@ class FfnMxParams:
         if not type(wg) is type(wu) is type(wd) is MxTensor:
             raise TypeError("wg, wu and wd must be MxTensors")
         E, F, dev = wd._rows, wd._width, wd._index
-        if wd._shape != (E, F) or wg._shape != (F, E) or wu._shape != (F, E) or wg._index != dev or wu._index != dev:
+        if not (wg._rows == wu._rows == F and wg._width == wu._width == E and wg._index == wu._index == dev) \
+                or not len(wd._shape) == len(wg._shape) == len(wu._shape) == 2:
             raise ValueError(f"wg and wu must be (F, E) beside wd (E, F), on one device: {wg._shape}, {wu._shape}, {wd._shape}")
         act = ACTS.get(self.act)
         if act is None:
@@ -1254,7 +1262,7 @@ class FfnMxParams:
         t = torch.bfloat16
         p = _lib.PmhaFfnParams(E, F, PMHA_BF16, act, None, None, None, _like("bg", self.bg, (F,), t, dev),
                                _like("bu", self.bu, (F,), t, dev), _like("bd", self.bd, (E,), t, dev))
-        return p, _lib.PmhaFfnMx(wg._struct(), wu._struct(), wd._struct()), dev
+        return p, _lib.PmhaFfnMx(wg._c, wu._c, wd._c), dev
 
     @staticmethod
     def from_params(params: FfnParams) -> "FfnMxParams":
@@ -1290,7 +1298,7 @@ def pmha_ffn_forward_mx(params: FfnMxParams, x: MxTensor, residual: torch.Tensor
             out = torch.empty(shape, dtype=bf16, device=x.device)
             o = out.data_ptr()
         wp, wn, keep = _scratch(x, need, workspace)
-        st = lib.pmha_ffn_forward_mx(pp, ctypes.byref(w), ctypes.byref(x._struct()), r, rows, o, wp, wn,
+        st = lib.pmha_ffn_forward_mx(pp, ctypes.byref(w), x._ref, r, rows, o, wp, wn,
                                      _stream_of(dev, stream))
     if st:
         _lib.check(st, "pmha_ffn_forward_mx")

@@ -1,4 +1,7 @@
 """Microscaled 4-bit floating point: quantisation, the linear product and the gated block, against 64-bit forms."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -300,6 +303,27 @@ def test_weights_written_by_the_launch_before():
         y = pmha.pmha_ffn_forward_mx(p, x)
         z = pmha.pmha_mx_linear(x, pmha.pmha_mx_quantize(sets[i % 2][0]))
         assert torch.equal(y, want[i % 2][0]) and torch.equal(z, want[i % 2][1]), i
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_copies_stand_for_the_same_values(how):
+    """A copy has arrays of its own (copy: the same ones), which the calls read after the original is gone."""
+    make = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda t: pickle.loads(pickle.dumps(t))}[how]
+    x, w = normal(1, 40, 96), normal(2, 24, 96)
+    q, k = pmha.pmha_mx_quantize(w), pmha.pmha_checkpoint(x)
+    want = pmha.pmha_mx_linear(pmha.pmha_mx_quantize(x), q), pmha.pmha_checkpoint_restore(k)
+    block = make(pmha.FfnMxParams(q, q, pmha.pmha_mx_quantize(normal(3, 96, 24))))
+    assert torch.equal(block.wg.values(), q.values())
+    q2, k2 = make(q), make(k)
+    if how != "copy":
+        q.codes.fill_(0x11), k.codes.zero_()
+    del q, k
+    assert q2.shape == w.shape and k2.dtype == BF16
+    got = pmha.pmha_mx_linear(pmha.pmha_mx_quantize(x), q2), pmha.pmha_checkpoint_restore(k2)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    if how != "copy":
+        pmha.pmha_device_status()
+        assert torch.equal(block.wg.values(), q2.values())
 
 
 def test_refusals():
