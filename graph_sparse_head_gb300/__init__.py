@@ -887,7 +887,8 @@ def pmha_ffn_backward(params: FfnParams, x: torch.Tensor, dout: torch.Tensor, in
 # ---------------------------------------------------------------- joins with the residual stream, 8-bit checkpoints
 class _Buffer:
     """What Checkpoint and MxTensor have in common: two arrays, codes and scales, given as tensors or lying in one
-    allocation of which tensors are made when they are asked for (an allocation and a view take as long as a launch)."""
+    allocation of which tensors are made when they are asked for (an allocation and a view take as long as a launch).
+    _c, _ref: the C struct of the arrays, which stay where they are, and a reference to it."""
     __slots__ = ("_codes", "_scale", "_buffer", "_at", "_c", "_ref", "_shape", "_index")
 
     @property
@@ -914,13 +915,13 @@ class _Buffer:
     def nbytes(self) -> int:
         return self._code_layout()[0] + self._scale_layout()[0]
 
-    def _allocate(self, x):
-        n = self._code_layout()[0]
-        self._at = (n + 255) & ~255
-        self._buffer = b = torch.empty(self._at + self._scale_layout()[0], dtype=torch.uint8, device=x.device)
+    def _allocate(self, device, code_bytes, scale_bytes):
+        self._at = at = (code_bytes + 255) & ~255
+        self._buffer = b = torch.empty(at + scale_bytes, dtype=torch.uint8, device=device)
         p = b.data_ptr()
         self._codes = self._scale = None
-        self._point(p, p + self._at)
+        self._c = c = self._STRUCT(p, p + at)
+        self._ref = ctypes.byref(c)
 
     def _given(self, codes, scale):
         """Takes tensors, which must be of the layouts."""
@@ -931,12 +932,8 @@ class _Buffer:
             if _like(name, t, torch.Size(shape), dtype, self._index) is None:
                 raise ValueError(f"{name} is missing")
         self._codes, self._scale, self._buffer = codes, scale, None
-        self._point(codes.data_ptr(), scale.data_ptr())
-
-    def _point(self, codes, scale):
-        """The C struct of the arrays, which stay where they are, and a reference to it."""
-        self._c = c = self._STRUCT(codes, scale)
-        self._ref = ctypes.byref(c)
+        self._c = self._STRUCT(codes.data_ptr(), scale.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
 
 class Checkpoint(_Buffer):
@@ -968,11 +965,11 @@ class Checkpoint(_Buffer):
         return 2 * math.prod(rows) * groups, (*rows, groups), torch.bfloat16
 
     @staticmethod
-    def _empty(x) -> "Checkpoint":
+    def _empty(x, shape, rows, width, index) -> "Checkpoint":
         """For a tensor like x, to be written."""
         k = object.__new__(Checkpoint)
-        k._shape, k._dtype, k._index = x.shape, x.dtype, x.get_device()
-        k._allocate(x)
+        k._shape, k._dtype, k._index = shape, x.dtype, index
+        k._allocate(x.device, rows * width, (width + 31) // 32 * rows * 2)
         return k
 
 
@@ -990,7 +987,7 @@ def pmha_checkpoint(x: torch.Tensor, stream=None) -> Checkpoint:
     bfloat16, each code the nearest integer to value / scale (off by half a scale at most)."""
     shape, rows, width, dev = _rows_of("x", x)
     with _on(dev, stream):
-        k = Checkpoint._empty(x)
+        k = Checkpoint._empty(x, shape, rows, width, dev)
         st = _library().pmha_checkpoint(_DTYPES[x.dtype], rows, width, x.data_ptr(), k._ref,
                                         _stream_of(dev, stream))
     if st:
@@ -1062,9 +1059,9 @@ def _join(params, branch, residual, keep_branch, keep_residual, stream):
         s = torch.empty(shape, dtype=dtype, device=residual.device) if r is None else torch.empty_like(residual)
         out = None if params.pre is None else torch.empty_like(s)
         if keep_branch:
-            kb = Checkpoint._empty(branch)
+            kb = Checkpoint._empty(branch, shape, rows, width, dev)
         if keep_residual:
-            kr = Checkpoint._empty(residual)
+            kr = Checkpoint._empty(residual, shape, rows, width, dev)
         st = _library().pmha_join(ctypes.byref(p), rows, b, bk, r, rk, s.data_ptr(), None if out is None else out.data_ptr(),
                                   None if kb is None else kb._ref,
                                   None if kr is None else kr._ref, _stream_of(dev, stream))
@@ -1178,12 +1175,13 @@ class MxTensor(_Buffer):
         return shape[0] * shape[1] * 512, shape, torch.uint8
 
     @staticmethod
-    def _empty(x) -> "MxTensor":
+    def _empty(x, shape, rows, width, index) -> "MxTensor":
         """For a tensor like x, to be written."""
+        if not width:
+            raise ValueError("an MxTensor has rows of one value at least")
         q = object.__new__(MxTensor)
-        q._of(x.shape)
-        q._index = x.get_device()
-        q._allocate(x)
+        q._shape, q._rows, q._width, q._index = shape, rows, width, index
+        q._allocate(x.device, (width + 31) // 32 * rows * 16, (rows + 127) // 128 * ((width + 127) // 128) * 512)
         return q
 
     def values(self) -> torch.Tensor:
@@ -1202,9 +1200,9 @@ def pmha_mx_quantize(x: torch.Tensor, stream=None) -> MxTensor:
     """x (..., width), float32 or bfloat16, in microscaled 4 bits: a block's scale is the least power of two with
     max|block| <= 6 * scale, each value the nearest E2M1 value times that (ties to the even code). For tokens and, once,
     for weights."""
-    _, rows, width, dev = _rows_of("x", x)
+    shape, rows, width, dev = _rows_of("x", x)
     with _on(dev, stream):
-        q = MxTensor._empty(x)
+        q = MxTensor._empty(x, shape, rows, width, dev)
         st = _library().pmha_mx_quantize(_DTYPES[x.dtype], rows, width, x.data_ptr(), q._ref,
                                          _stream_of(dev, stream))
     if st:
