@@ -127,10 +127,8 @@ __device__ __forceinline__ void team_reduce(float (&v)[K], TeamSums &sh, int &tu
 template <int N>
 __device__ __forceinline__ float squares_of(const float (&f)[N])
 {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) ss = fmaf(f[i], f[i], ss);
-    return ss;
+    const Values<N> v(f);
+    return Values<N>::dot(v, v);
 }
 // The power of two that a team's row is scaled by, in place, where `over`.
 template <int N, int LPR>
