@@ -411,16 +411,17 @@ __global__ void __launch_bounds__(kThreads) k_join_sums(JoinSumArgs a)
     if (!a.dpost && what > 0) ++what;
     const long long gate = what - 2;
     const float *part = what == 0 ? a.part_pre : a.part_branch;
-    const int n = what < 2 ? (int)a.gates * a.blocks_per_gate : a.blocks_per_gate;
+    // up to 2^31 - 3 partial rows: an int would wrap behind the last of them
+    const unsigned n = what < 2 ? (unsigned)a.gates * (unsigned)a.blocks_per_gate : (unsigned)a.blocks_per_gate;
     const long long at = what < 2 ? 0 : gate * a.blocks_per_gate;
     const bool weighted = what == 1 && a.gate;
     Two s = {0.f, 0.f};
     if (c < a.width) {
 #pragma unroll 4
-        for (int i = t; i < n; i += 32) {
+        for (unsigned i = t; i < n; i += 32) {
             const float v = part[(at + i) * a.width + c];
             if (weighted) {
-                const float g = to_f<T>(((const T *)a.gate)[(long long)(i / a.blocks_per_gate) * a.width + c]);
+                const float g = to_f<T>(((const T *)a.gate)[(long long)(i / (unsigned)a.blocks_per_gate) * a.width + c]);
                 const float p = __fmul_rn(v, g);
                 s = add(s, Two{p, __fmaf_rn(v, g, -p)});
             } else {
