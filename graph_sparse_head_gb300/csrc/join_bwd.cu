@@ -398,6 +398,9 @@ struct JoinSumArgs {
     long long gates;              // rows of dgate
     int blocks_per_gate, width, tiles;
 };
+// Terms added to a pair before its parts are set apart again. The low part takes what the high part's rounding leaves: left to
+// itself it loses bits as it grows (2^20 terms of 0.7 a thread were 6e-5 off), and from 2^25 terms on neither part moves.
+constexpr unsigned kPlain = 16;
 // One block: eight columns of one output row (dpre, dpost, or a row of dgate), 32
 // threads a column in a fixed order, as pairs.
 template <typename T>
@@ -417,16 +420,20 @@ __global__ void __launch_bounds__(kThreads) k_join_sums(JoinSumArgs a)
     const bool weighted = what == 1 && a.gate;
     Two s = {0.f, 0.f};
     if (c < a.width) {
+        for (unsigned i = t; i < n;) {
+            const unsigned stop = min(n, i + 32 * kPlain);
 #pragma unroll 4
-        for (unsigned i = t; i < n; i += 32) {
-            const float v = part[(at + i) * a.width + c];
-            if (weighted) {
-                const float g = to_f<T>(((const T *)a.gate)[(long long)(i / (unsigned)a.blocks_per_gate) * a.width + c]);
-                const float p = __fmul_rn(v, g);
-                s = add(s, Two{p, __fmaf_rn(v, g, -p)});
-            } else {
-                s = add(s, Two{v, 0.f});
+            for (; i < stop; i += 32) {
+                const float v = part[(at + i) * a.width + c];
+                if (weighted) {
+                    const float g = to_f<T>(((const T *)a.gate)[(long long)(i / (unsigned)a.blocks_per_gate) * a.width + c]);
+                    const float p = __fmul_rn(v, g);
+                    s = add(s, Two{p, __fmaf_rn(v, g, -p)});
+                } else {
+                    s = add(s, Two{v, 0.f});
+                }
             }
+            s = two_sum(s.hi, s.lo);
         }
     }
     // four of a warp's threads share a column, then the eight warps in order

@@ -30,3 +30,16 @@ def test_a_gate_for_each_of_almost_2_31_rows():
     # a root within 2^-21 and its product
     assert abs(float(dpost[0].double()) - want) <= 2.0 ** -20 * want
     assert bool((dpost[1:] == 0).all())
+
+
+def test_sums_of_many_like_rows():
+    """2^24 partial rows of the same values: what the pairs' low parts lose must not grow with the rows."""
+    rows, width = 2 ** 24 + 5, 8
+    x = torch.tensor([1.0, 2.5, -0.75, 3.0, 0.25, -1.5, 2.0, 0.5], dtype=torch.bfloat16, device=DEV).repeat(rows, 1)
+    ones = torch.ones(width, dtype=torch.bfloat16, device=DEV)
+    p = pmha.JoinParams(post=ones, gate=torch.full_like(x, 1.0))
+    got = pmha.pmha_join_backward(p, x, None, None, torch.ones_like(x), input_grads=False)
+    each = got["dgate"].double()  # with a gate a row and ones for post: the partial rows themselves
+    assert bool((each == each[0]).all())
+    want = rows * each[0]
+    assert bool(((got["dpost"].double() - want).abs() <= 2.0 ** -23 * want.abs()).all())
