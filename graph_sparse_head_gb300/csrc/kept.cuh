@@ -34,7 +34,7 @@ __device__ __forceinline__ float kept_scale(uint32_t bits)
     if (bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
     const float most = __uint_as_float(bits);
     uint32_t c = (__float_as_uint(most * (1.f / 127.f)) + 0xffffu) & 0xffff0000u;
-    if (c > __float_as_uint(kKeptLeast)) {  // normal numbers, and their neighbours below
+    if (c >= __float_as_uint(kKeptLeast)) {  // normal numbers, and their neighbours below
         if (127.f * __uint_as_float(c) < most) c += 0x10000u;
         else if (127.f * __uint_as_float(c - 0x10000u) >= most) c -= 0x10000u;
     }
