@@ -1028,13 +1028,17 @@ class JoinParams:
     residual_scale: float = 1.0
     eps: float = 1e-6
 
-    def _struct(self, dtype, width, index):
+    def _struct(self, dtype, width, index, rows=0):
         gates, gate, one = 0, self.gate, (width,)
         if gate is not None:
             if not isinstance(gate, _T) or gate.dim() not in (1, 2):
                 raise ValueError(f"gate must be ({width},) or (G, {width})")
             gates = 1 if gate.dim() == 1 else gate.shape[0]
             gate = _like("gate", gate, one if gate.dim() == 1 else (gates, width), dtype, index)
+            if not gates:  # to the library no gate at all: right without tokens only
+                if rows:
+                    raise ValueError(f"gate has no rows, the tokens have {rows}")
+                gate = None
         return _lib.PmhaJoinParams(_DTYPES[dtype], width, _like("post", self.post, one, dtype, index), gate, gates,
                                    self.residual_scale, _like("pre", self.pre, one, dtype, index), self.eps)
 
@@ -1050,7 +1054,7 @@ def _join(params, branch, residual, keep_branch, keep_residual, stream):
         shape, rows, width, dev = _rows_of("residual", residual)
         dtype = residual.dtype
         r = residual.data_ptr()
-    p = params._struct(dtype, width, dev)
+    p = params._struct(dtype, width, dev, rows)
     if type(branch) is Checkpoint:
         bk = _kept_like("branch", branch, shape, dtype, dev)
     else:
@@ -1089,7 +1093,7 @@ def pmha_join_checkpointed(params: JoinParams, branch: torch.Tensor, residual, k
 def pmha_join_backward_workspace_size(params: JoinParams, x: torch.Tensor) -> int:
     """Bytes of pmha_join_backward's workspace for tokens like x (its sum or dsum)."""
     shape, rows, width, dev = _rows_of("x", x)
-    p = params._struct(x.dtype, width, dev)
+    p = params._struct(x.dtype, width, dev, rows)
     return _join_size(p, rows)
 
 
@@ -1114,7 +1118,7 @@ def pmha_join_backward(params: JoinParams, branch, sum: torch.Tensor | None, dou
         raise ValueError("dout or dsum is needed")
     shape, rows, width, dev = _rows_of("dsum" if dout is None else "dout", like)
     dtype = like.dtype
-    p = params._struct(dtype, width, dev)
+    p = params._struct(dtype, width, dev, rows)
     s = _like("sum", sum, shape, dtype, dev)
     dy, ds = _like("dout", dout, shape, dtype, dev), _like("dsum", dsum, shape, dtype, dev)
     if type(branch) is Checkpoint:
