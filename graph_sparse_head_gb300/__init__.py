@@ -1327,7 +1327,8 @@ class PackedEncoderLayer:
 
         a = attention(norm1(x));  s = x + a;  y = s + block(norm2(s))
 
-    or, with norms after the blocks, gates (learned (E,), or one a sample, (B, E)) and a scaled residual stream,
+    or, with norms after the blocks, gates (learned (E,), or one a sample, (B, E), for batches of B only) and a scaled
+    residual stream,
 
         s = residual_scale x + gate1 norm(a; post1);  y = residual_scale s + gate2 norm(block(norm2(s)); post2)
 
@@ -1363,7 +1364,20 @@ class PackedEncoderLayer:
         """An addition: what the norm and the block do on their way."""
         return join.post is None and join.gate is None and join.residual_scale == 1.0
 
+    def _check_gates(self, shape):
+        """Gates of samples belong to this batch. Their rows only have to divide the tokens for a join, which would give a
+        sample another's gate (and refuses those that do not divide them)."""
+        if len(shape) != 3 or not shape[0]:
+            return  # the attention refuses it, or there is no sample
+        batch, n, _ = shape
+        for name, join in (("gate1", self.join1), ("gate2", self.join2)):
+            gate = join.gate
+            if gate is not None and gate.dim() == 2 and gate.shape[0] not in (1, batch) and \
+                    not batch * n % (gate.shape[0] or 1):
+                raise ValueError(f"{name} is of {gate.shape[0]} samples, the tokens of {batch}")
+
     def _attention(self, x, key_padding_mask):
+        self._check_gates(getattr(x, "shape", ()))
         n1, _ = pmha_rms_norm(x, self.norm1, self.eps)
         a, _ = pmha_forward(self.graph, self.attention, n1, n1, n1, key_padding_mask=key_padding_mask)
         return n1, a
@@ -1422,6 +1436,7 @@ class PackedEncoderLayer:
 
     def backward_checkpointed(self, kept: LayerCheckpoint, dy: torch.Tensor) -> dict:
         """backward()'s gradients, of the layer at the kept values of its input and its blocks' outputs."""
+        self._check_gates(kept.x.shape)
         s, n2 = pmha_join(self.join1, kept.attention, kept.x)
         x, n1 = pmha_join(JoinParams(pre=self.norm1, eps=self.eps), None, kept.x)
         return self._backward(x, n1, kept.attention, s, n2, kept.block, dy, kept.key_padding_mask)
