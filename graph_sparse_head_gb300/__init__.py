@@ -1364,6 +1364,11 @@ class PackedEncoderLayer:
         """An addition: what the norm and the block do on their way."""
         return join.post is None and join.gate is None and join.residual_scale == 1.0
 
+    @staticmethod
+    def _reads_branch(join: JoinParams) -> bool:
+        """Whether the join's backward pass needs the block's output (of a norm after the block or of a gate)."""
+        return join.post is not None or join.gate is not None
+
     def _check_gates(self, shape):
         """Gates of samples belong to this batch. Their rows only have to divide the tokens for a join, which would give a
         sample another's gate (and refuses those that do not divide them)."""
@@ -1420,7 +1425,7 @@ class PackedEncoderLayer:
         """{"dx", "dnorm1", "dnorm2", and the keys of pmha_backward's and
         pmha_ffn_backward's parameter gradients; "dpost1", "dgate1", "dpost2", "dgate2" of those the layer has}."""
         n1, a, s, n2 = self._attend(x, key_padding_mask)
-        f = None if self._plain(self.join2) else pmha_ffn_forward(self.block, n2)
+        f = pmha_ffn_forward(self.block, n2) if self._reads_branch(self.join2) else None
         return self._backward(x, n1, a, s, n2, f, dy, key_padding_mask)
 
     def forward_checkpointed(self, x: torch.Tensor, key_padding_mask: torch.Tensor | None = None):
@@ -1431,7 +1436,8 @@ class PackedEncoderLayer:
         if self._plain(self.join2):
             y = pmha_ffn_forward(self.block, n2, residual=s)
         else:
-            y, _, f8, _ = pmha_join_checkpointed(self.join2, pmha_ffn_forward(self.block, n2), s, keep_residual=False)
+            y, _, f8, _ = pmha_join_checkpointed(self.join2, pmha_ffn_forward(self.block, n2), s,
+                                                 keep_branch=self._reads_branch(self.join2), keep_residual=False)
         return y, LayerCheckpoint(x8, a8, f8, key_padding_mask)
 
     def backward_checkpointed(self, kept: LayerCheckpoint, dy: torch.Tensor) -> dict:
