@@ -1405,11 +1405,11 @@ class PackedEncoderLayer:
               key_padding_mask: torch.Tensor | None = None) -> torch.Tensor:
         """The layer with a block of 8-bit or 4-bit weights, its tokens quantized on the way (bfloat16 layers)."""
         if type(block) is FfnQuantizedParams:
+            _, a = self._attention(x, key_padding_mask)
             if self._plain(self.join1):
-                _, a = self._attention(x, key_padding_mask)
                 q, scale, s = pmha_rms_norm_quantized(a, self.norm2, self.eps, residual=x)
-            else:
-                s = self._attend(x, key_padding_mask)[2]
+            else:  # the sum alone: the norm to 8 bits follows
+                s, _ = pmha_join(dataclasses.replace(self.join1, pre=None), a, x)
                 q, scale, _ = pmha_rms_norm_quantized(s, self.norm2, self.eps)
             forward = functools.partial(pmha_ffn_forward_quantized, block, q, scale)
         elif type(block) is FfnMxParams:

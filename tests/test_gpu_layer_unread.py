@@ -41,3 +41,24 @@ def test_a_step_from_checkpoints_with_norm_or_gate_alone_keeps_the_block():
     for post, gates in ((True, 0), (False, 1)):
         _, kept = joined(base, 5, post, gates, 1.0).forward_checkpointed(x)
         assert kept.block is not None
+
+
+def test_serving_in_8_bits_normalises_a_join_once(monkeypatch):
+    """The 8-bit norm takes the join's sum: the join itself leaves its norm out."""
+    base, x, _, _ = make(100, 800, 2, 128, 8, 256, "bf16", seed=5)
+    layer = joined(base, 9, True, 1)
+    block = pmha.FfnQuantizedParams.from_params(base.block)
+    n1, _ = pmha.pmha_rms_norm(x, layer.norm1, layer.eps)
+    a, _ = pmha.pmha_forward(layer.graph, layer.attention, n1, n1, n1)
+    s, _ = pmha.pmha_join(layer.join1, a, x)
+    q, scale, _ = pmha.pmha_rms_norm_quantized(s, layer.norm2, layer.eps)
+    want = pmha.pmha_join(layer.join2, pmha.pmha_ffn_forward_quantized(block, q, scale), s)[0]
+    join, seen = pmha.pmha_join, []
+
+    def spy(params, *args, **kw):
+        seen.append(params.pre is None)
+        return join(params, *args, **kw)
+
+    monkeypatch.setattr(pmha, "pmha_join", spy)
+    assert torch.equal(layer.serve(x, block), want)
+    assert seen == [True, True]
