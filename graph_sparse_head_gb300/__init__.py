@@ -1192,12 +1192,14 @@ class MxTensor(_Buffer):
         """The values that it stands for, in float64 (values near float32's end can round to 2^128). Torch operations, for
         inspection: not for a hot path."""
         rows, width = self._rows, self._width
+        blocks = (width + 31) // 32
         grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=self.codes.device)
-        v = torch.cat((grid, -grid))[torch.stack((self.codes & 15, self.codes >> 4), -1).long()].view(rows, -1, 32)
-        t = self.scale.view(*self.scale.shape[:2], 32, 4, 4).permute(0, 3, 2, 1, 4)
-        t = t.reshape(self.scale.shape[0] * 128, self.scale.shape[1] * 4)[:rows, :v.shape[1]].long()
+        v = torch.cat((grid, -grid))[torch.stack((self.codes & 15, self.codes >> 4), -1).long()].view(rows, blocks, 32)
+        tiles = self.scale.shape[:2]
+        t = self.scale.view(*tiles, 32, 4, 4).permute(0, 3, 2, 1, 4)
+        t = t.reshape(tiles[0] * 128, tiles[1] * 4)[:rows, :blocks].long()
         s = torch.where(t == 255, math.nan, ((t - 127 + 1023) << 52).view(torch.float64))
-        return (v * s[..., None]).view(rows, -1)[:, :width].reshape(self.shape)
+        return (v * s[..., None]).view(rows, blocks * 32)[:, :width].reshape(self.shape)
 
 
 def pmha_mx_quantize(x: torch.Tensor, stream=None) -> MxTensor:
