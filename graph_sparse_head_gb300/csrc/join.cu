@@ -23,7 +23,7 @@ struct JoinArgs {
     Source branch, res;
     const void *post, *gate, *pre;
     void *sum, *out;
-    KeptOut keep_branch, keep_res;
+    KeptOut keep_branch, keep_res;  // at widths of whole 16-byte pieces only
     long long rows, per_gate;  // rows that share a gate
     int width;
     float alpha, eps;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_join(JoinArgs a)
             if (a.branch.p) {
                 const V v = piece(nb, 0);
                 widen<T, VEC>(v, bj);
-                if constexpr (KEPT)
+                if constexpr (KEPT && VEC >= 4)
                     if (a.keep_branch.codes) {
                         const long long e = at + j * kPiece;
                         keep<T, VEC>(KeptOut{a.keep_branch.codes + e, a.keep_branch.scale + sat + j * (kPiece / kGroup)},
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_join(JoinArgs a)
             if (!KEPT || a.res.p) {
                 const V v = piece(nx, 1);
                 widen<T, VEC>(v, xj);
-                if constexpr (KEPT)
+                if constexpr (KEPT && VEC >= 4)
                     if (a.keep_res.codes) {
                         const long long e = at + j * kPiece;
                         keep<T, VEC>(KeptOut{a.keep_res.codes + e, a.keep_res.scale + sat + j * (kPiece / kGroup)},
@@ -256,22 +256,24 @@ __global__ void __launch_bounds__(kThreads) k_join_wide(JoinArgs a)
 {
     __shared__ float sh[kThreads / 32];
     const long long row = blockIdx.x, base = row * a.width;
-    const int lane = threadIdx.x & 31;
     const int first = (int)threadIdx.x * VEC, stride = kThreads * VEC;
-    // whole warps walk here: a group's values lie in neighbouring lanes
-    auto keep_row = [&](const KeptOut &k, const void *p) {
-        for (int c0 = first - lane * VEC; c0 < a.width; c0 += stride) {
-            const int c = c0 + lane * VEC;
-            Vals<T, VEC> v;
+    if constexpr (VEC >= 4) {
+        // whole warps walk here: a group's values lie in neighbouring lanes
+        auto keep_row = [&](const KeptOut &k, const void *p) {
+            const int lane = threadIdx.x & 31;
+            for (int c0 = first - lane * VEC; c0 < a.width; c0 += stride) {
+                const int c = c0 + lane * VEC;
+                Vals<T, VEC> v;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(0.f);
-            if (c < a.width) load<T, VEC>((const T *)p + base + c, v.v);
-            keep<T, VEC>(KeptOut{k.codes + base + c, k.scale + row * groups_of(a.width) + c / kGroup}, c % kGroup == 0,
-                         c < a.width, v);
-        }
-    };
-    if (a.keep_branch.codes) keep_row(a.keep_branch, a.branch.p);
-    if (a.keep_res.codes) keep_row(a.keep_res, a.res.p);
+                for (int i = 0; i < VEC; ++i) v.v[i] = from_f<T>(0.f);
+                if (c < a.width) load<T, VEC>((const T *)p + base + c, v.v);
+                keep<T, VEC>(KeptOut{k.codes + base + c, k.scale + row * groups_of(a.width) + c / kGroup}, c % kGroup == 0,
+                             c < a.width, v);
+            }
+        };
+        if (a.keep_branch.codes) keep_row(a.keep_branch, a.branch.p);
+        if (a.keep_res.codes) keep_row(a.keep_res, a.res.p);
+    }
     float rb = 1.f, scb = 1.f;
     if (a.post)
         rb = block_root(sh, a.width, a.eps, &scb,
@@ -543,7 +545,7 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
     cudaStream_t cs = (cudaStream_t)stream;
     if (s.vec < 4) {
         // With one or two values a lane the codes cost more on the way than a pass of their own: 100,000 x 171 150 us with
-        // the branch's, without them 52.
+        // the branch's, without them 45 and 21 for the pass. The kernels have no such form.
         if (keep_branch && (st = launch_keep(p.dtype, rows, w, branch, a.keep_branch, cs)) != PMHA_OK) return st;
         if (keep_residual && (st = launch_keep(p.dtype, rows, w, residual, a.keep_res, cs)) != PMHA_OK) return st;
         a.keep_branch = a.keep_res = KeptOut{nullptr, nullptr};

@@ -13,7 +13,7 @@ struct JoinBwdArgs {
     const void *post, *gate, *pre;
     void *dbranch, *dres;
     float *part_pre, *part_branch;  // (grid, width) partial sums of dn s r and of D branch r_b, or null
-    long long rows, per_gate;       // rows that share a gate (all, without one)
+    long long per_gate;             // rows that share a gate (all, without one)
     int blocks_per_gate;            // blocks that share them
     int width;
     float alpha, eps;
@@ -543,7 +543,7 @@ pmha_status pmha_join_backward(const pmha_join_params *params, int64_t rows, con
     float *part_branch = dpost || dgate ? (float *)((uint8_t *)workspace + need / 2) : nullptr;
     Source b = source(branch, branch_kept);
     if (!need_branch) b = Source{nullptr, {nullptr, nullptr}};
-    JoinBwdArgs a{b, sum, dout, dsum, p.post, p.gate, p.pre, dbranch, dresidual, part_pre, part_branch, rows, per_gate,
+    JoinBwdArgs a{b, sum, dout, dsum, p.post, p.gate, p.pre, dbranch, dresidual, part_pre, part_branch, per_gate,
                   (int)blocks, (int)w, p.residual_scale, p.eps};
     if (!need_branch) a.post = nullptr;
     const Shape s = join_shape(p.dtype, w);

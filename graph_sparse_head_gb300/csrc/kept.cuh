@@ -46,24 +46,25 @@ __device__ __forceinline__ float kept_inverse(float scale)  // within 2^-22
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(scale));
     return y;
 }
-// v / scale to the nearest integer, in the low byte, ties to even. A bfloat16 v and scale: the quotient is at least 2^-10
-// away from a half unless it is one, and its product with the inverse is within 2^-15 of it, so that rounding it to a grid of
-// 2^-11 first gives back the halves. A float32 v: the remainder of the product's nearest integer q is exact (both v and
-// q scale are multiples of its last bit) and says whether the neighbour is nearer, or as near and even. (Of a group with
-// an infinity or a NaN any code will do: its scale is NaN.)
-template <typename T>
+// v / scale to the nearest integer, in the low byte, ties to even. A bfloat16 v and scale, two values at once: the quotient is
+// at least 2^-10 away from a half unless it is one, and its product with the inverse is within 2^-15 of it, so that rounding it
+// to a grid of 2^-11 first (6144 off: a multiple of the grid and of 256) gives back the halves. (Of a group with an infinity or
+// a NaN any code will do: its scale is NaN.)
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+__device__ __forceinline__ void kept_code2(float v0, float v1, float inv, uint32_t &c0, uint32_t &c1)
+{
+    float a, b;
+    add2(fma2(Pair(v0, v1), Pair(inv, inv), Pair(6144.f, 6144.f)), Pair(kRound, kRound)).get(a, b);
+    c0 = __float_as_uint(a), c1 = __float_as_uint(b);
+}
+// A float32 v: the remainder of the product's nearest integer q is exact (both v and q scale are multiples of its last bit)
+// and says whether the neighbour is nearer, or as near and even.
 __device__ __forceinline__ uint32_t kept_code(float v, float scale, float inv)
 {
-    constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-    if constexpr (sizeof(T) == 2) {
-        // 6144 off before the last addition: a multiple of the grid and of 256
-        return __float_as_uint(__fadd_rn(__fmaf_rn(v, inv, 6144.f), kRound));
-    } else {
-        const float m = __fmaf_rn(v, inv, kRound), q = __fsub_rn(m, kRound);
-        const float e = __fmaf_rn(-q, scale, v), half = 0.5f * scale;
-        const bool move = fabsf(e) > half || (fabsf(e) == half && (__float_as_uint(m) & 1u));
-        return __float_as_uint(m) + (move ? (e > 0.f ? 1u : 0xffffffffu) : 0u);
-    }
+    const float m = __fmaf_rn(v, inv, kRound), q = __fsub_rn(m, kRound);
+    const float e = __fmaf_rn(-q, scale, v), half = 0.5f * scale;
+    const bool move = fabsf(e) > half || (fabsf(e) == half && (__float_as_uint(m) & 1u));
+    return __float_as_uint(m) + (move ? (e > 0.f ? 1u : 0xffffffffu) : 0u);
 }
 
 // The codes of VEC values of a group whose others lie in the neighbouring lanes, in the low bytes, and the group's scale;
@@ -75,17 +76,14 @@ __device__ __forceinline__ float kept_codes(const Vals<T, VEC> &v, uint32_t (&w)
 #pragma unroll
     for (int o = kGroup / VEC / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
     const float scale = kept_scale(most), inv = kept_inverse(scale);
-    if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {  // kept_code of two values an instruction
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) {
-            float a, b;
-            add2(fma2(Pair(to_f<T>(v.v[i]), to_f<T>(v.v[i + 1])), Pair(inv, inv), Pair(6144.f, 6144.f)),
-                 Pair(12582912.f, 12582912.f)).get(a, b);
-            w[i] = __float_as_uint(a), w[i + 1] = __float_as_uint(b);
+    for (int i = 0; i < VEC; i += 2) {
+        if constexpr (sizeof(T) == 2) {
+            kept_code2(to_f<T>(v.v[i]), to_f<T>(v.v[i + 1]), inv, w[i], w[i + 1]);
+        } else {
+            w[i] = kept_code(v.v[i], scale, inv);
+            w[i + 1] = kept_code(v.v[i + 1], scale, inv);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = kept_code<T>(to_f<T>(v.v[i]), scale, inv);
     }
     return scale;
 }

@@ -98,16 +98,12 @@ __device__ __forceinline__ void load_some(const T *p, int left, Vals<T, VEC> &v)
 template <int VEC>
 __device__ __forceinline__ typename Bytes<VEC>::type low_bytes(const uint32_t (&w)[VEC])
 {
-    if constexpr (VEC == 1) return (uint8_t)w[0];
-    else if constexpr (VEC == 2) return (uint16_t)__byte_perm(w[0], w[1], 0x0040);
-    else {
-        auto four = [&](int i) {
-            return __byte_perm(__byte_perm(w[i], w[i + 1], 0x0040), __byte_perm(w[i + 2], w[i + 3], 0x0040), 0x5410);
-        };
-        if constexpr (VEC == 4) return four(0);
-        else if constexpr (VEC == 8) return make_uint2(four(0), four(4));
-        else return make_uint4(four(0), four(4), four(8), four(12));
-    }
+    auto four = [&](int i) {
+        return __byte_perm(__byte_perm(w[i], w[i + 1], 0x0040), __byte_perm(w[i + 2], w[i + 3], 0x0040), 0x5410);
+    };
+    if constexpr (VEC == 4) return four(0);
+    else if constexpr (VEC == 8) return make_uint2(four(0), four(4));
+    else return make_uint4(four(0), four(4), four(8), four(12));
 }
 
 // An unevaluated sum hi + lo (about 46 bits).
