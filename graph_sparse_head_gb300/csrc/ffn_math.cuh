@@ -6,6 +6,7 @@
 
 #include <math.h>
 
+#include "pair.cuh"
 #include "pmha_internal.h"
 
 namespace pmha {
@@ -28,8 +29,9 @@ __device__ __forceinline__ float rcp(float x)
 // kUp) that the caller folds into scales and biases: with the gate times
 // -log2(e) the exponential needs no product of its own, and -ln(2) on the other
 // side undoes it: two special-function results and seven other instructions a
-// value. Packed float32 pairs and one reciprocal for two values were measured
-// slower (register moves: 15 instructions a value).
+// value. In the bf16 kernels packed float32 pairs and one reciprocal for two values were
+// measured slower (register moves: 15 instructions a value); the 4-bit kernel, whose accumulators come from tensor memory
+// in register pairs, takes hidden2.
 template <int ACT>
 struct Act;
 
@@ -47,6 +49,13 @@ struct Act<PMHA_ACT_SILU> {
     static __device__ __forceinline__ float hidden(float gate, float up)
     {
         return gate * rcp(1.f + ex2(gate)) * up;
+    }
+    static __device__ __forceinline__ Pair hidden2(Pair gate, Pair up)
+    {
+        float g0, g1, d0, d1;
+        gate.get(g0, g1);
+        add2(Pair(ex2(g0), ex2(g1)), Pair(1.f, 1.f)).get(d0, d1);
+        return mul2(mul2(gate, Pair(rcp(d0), rcp(d1))), up);
     }
     // act(g) and its slope, from the plain gate
     static __device__ __forceinline__ float fast(float g, float *slope)
@@ -71,15 +80,30 @@ struct Act<PMHA_ACT_GELU> {
     // and Stegun for erfc(z / sqrt(2)) (error below 1.5e-7; relative to the tail 0.16 % at z = 5, where it is 3e-7, and
     // 2 % at 10): a polynomial in
     // t = 1 / (1 + p z) times e = exp(-g^2 / 2), which the slope needs as well.
+    static constexpr float kP = 0.3275911f * 0.70710678f, kE = -0.72134752f;  // of z in t; -log2(e) / 2
+    static constexpr float kA1 = 0.5f * 0.254829592f, kA2 = -0.5f * 0.284496736f, kA3 = 0.5f * 1.421413741f,
+                           kA4 = -0.5f * 1.453152027f, kA5 = 0.5f * 1.061405429f;
     static __device__ __forceinline__ float lower(float g, float z, float *e)
     {
-        const float t = rcp(fmaf(z, 0.3275911f * 0.70710678f, 1.f));
-        *e = ex2(g * g * -0.72134752f);
-        float q = fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f);
-        q = fmaf(t, q, 0.5f * 1.421413741f);
-        q = fmaf(t, q, -0.5f * 0.284496736f);
-        q = fmaf(t, q, 0.5f * 0.254829592f);
+        const float t = rcp(fmaf(z, kP, 1.f));
+        *e = ex2(g * g * kE);
+        float q = fmaf(t, kA5, kA4);
+        q = fmaf(t, q, kA3);
+        q = fmaf(t, q, kA2);
+        q = fmaf(t, q, kA1);
         return q * t * *e;
+    }
+    static __device__ __forceinline__ Pair lower2(Pair g, Pair z)
+    {
+        float t0, t1, e0, e1;
+        fma2(z, Pair(kP, kP), Pair(1.f, 1.f)).get(t0, t1);
+        const Pair t(rcp(t0), rcp(t1));
+        mul2(mul2(g, g), Pair(kE, kE)).get(e0, e1);
+        Pair q = fma2(t, Pair(kA5, kA5), Pair(kA4, kA4));
+        q = fma2(t, q, Pair(kA3, kA3));
+        q = fma2(t, q, Pair(kA2, kA2));
+        q = fma2(t, q, Pair(kA1, kA1));
+        return mul2(mul2(q, t), Pair(ex2(e0), ex2(e1)));
     }
     // g Phi(g) = max(g, 0) - |g| Phi(-|g|)
     static __device__ __forceinline__ float hidden(float gate, float up)
@@ -87,6 +111,13 @@ struct Act<PMHA_ACT_GELU> {
         float e;
         const float z = fminf(fabsf(gate), 64.f);
         return fmaf(-z, lower(gate, z, &e), fmaxf(gate, 0.f)) * up;
+    }
+    static __device__ __forceinline__ Pair hidden2(Pair gate, Pair up)
+    {
+        float g0, g1;
+        gate.get(g0, g1);
+        const float z0 = fminf(fabsf(g0), 64.f), z1 = fminf(fabsf(g1), 64.f);
+        return mul2(fma2(Pair(-z0, -z1), lower2(gate, Pair(z0, z1)), Pair(fmaxf(g0, 0.f), fmaxf(g1, 0.f))), up);
     }
     static __device__ __forceinline__ float fast(float g, float *slope)
     {

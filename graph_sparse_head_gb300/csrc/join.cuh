@@ -217,22 +217,6 @@ __device__ __forceinline__ float block_root(float *sh, int width, float eps, flo
 }
 
 // ---------------------------------------------------------------- host side
-struct Span {
-    const void *p;
-    size_t n;
-};
-// Whether an output overlaps an input or another output.
-template <int NI, int NO>
-inline bool any_overlap(const Span (&in)[NI], const Span (&out)[NO])
-{
-    for (int o = 0; o < NO; ++o) {
-        for (int i = 0; i < NI; ++i)
-            if (overlap(out[o].p, out[o].n, in[i].p, in[i].n)) return true;
-        for (int i = 0; i < o; ++i)
-            if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return true;
-    }
-    return false;
-}
 inline Span codes_of(const pmha_kept *k, int64_t rows, int64_t width)
 {
     return k ? Span{k->codes, (size_t)(rows * width)} : Span{nullptr, 0};

@@ -315,18 +315,6 @@ pmha_status check_sizes(const char *who, int64_t rows, int64_t width, int64_t ou
     return PMHA_OK;
 }
 Mx mx_of(const pmha_mx &m) { return Mx{(const uint8_t *)m.codes, (const uint8_t *)m.scale}; }
-struct Span {
-    const void *p;
-    size_t n;
-};
-template <int N>
-bool overlaps_any(const void *p, size_t n, const Span (&in)[N])
-{
-    for (int i = 0; i < N; ++i)
-        if (overlap(p, n, in[i].p, in[i].n)) return true;
-    return false;
-}
-
 pmha_status linear(const MxLinear &a, const char *stage, cudaStream_t s)
 {
     if (!few_linear(a.M, a.N, a.K)) return mx_tc_linear(a, stage, s);
@@ -384,7 +372,8 @@ pmha_status pmha_mx_quantize(pmha_dtype dtype, int64_t rows, int64_t width, cons
         return PMHA_ERR_INVALID_ARG;
     }
     const size_t nb = (size_t)(rows * width) * bytes_of(dtype), cb = mx_code_bytes(rows, width), sb = mx_scale_bytes(rows, width);
-    if (overlap(out->codes, cb, x, nb) || overlap(out->scale, sb, x, nb) || overlap(out->codes, cb, out->scale, sb)) {
+    const Span ins[] = {{x, nb}}, outs[] = {{out->codes, cb}, {out->scale, sb}};
+    if (any_overlap(ins, outs)) {
         set_error("%s: an output overlaps an input or another output", who);
         return PMHA_ERR_INVALID_ARG;
     }
@@ -425,7 +414,8 @@ pmha_status pmha_mx_linear(int64_t rows, int64_t width, int64_t outputs, const p
     const Span ins[] = {{x->codes, mx_code_bytes(rows, width)}, {x->scale, mx_scale_bytes(rows, width)},
                         {weight->codes, mx_code_bytes(outputs, width)}, {weight->scale, mx_scale_bytes(outputs, width)},
                         {bias, (size_t)outputs * 2}, {residual, ob}};
-    if (overlaps_any(out, ob, ins)) {
+    const Span outs[] = {{out, ob}};
+    if (any_overlap(ins, outs)) {
         set_error("%s: an output overlaps an input or another output", who);
         return PMHA_ERR_INVALID_ARG;
     }
@@ -466,7 +456,8 @@ pmha_status pmha_ffn_forward_mx(const pmha_ffn_params *params, const pmha_ffn_mx
                         {weights->wd.codes, mx_code_bytes(E, F)}, {weights->wd.scale, mx_scale_bytes(E, F)},
                         {params->bg, (size_t)F * 2}, {params->bu, (size_t)F * 2}, {params->bd, (size_t)E * 2}, {residual, ob},
                         {workspace, need}};
-    if (overlaps_any(out, ob, ins)) {
+    const Span outs[] = {{out, ob}};
+    if (any_overlap(ins, outs)) {
         set_error("%s: an output overlaps an input or the workspace", who);
         return PMHA_ERR_INVALID_ARG;
     }

@@ -142,32 +142,6 @@ __device__ __forceinline__ float max_nan(float a, float b, float c)
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
     return r;
 }
-// Act<ACT>::hidden of two gates and ups (times kGate and kUp, as there). Accumulators come from tensor memory in register
-// pairs; with 15 instructions a hidden value the gated kernel's schedulers were the bound.
-template <int ACT>
-__device__ __forceinline__ Pair hidden2(Pair g, Pair u)
-{
-    float g0, g1;
-    g.get(g0, g1);
-    if constexpr (ACT == PMHA_ACT_SILU) {
-        float d0, d1;
-        add2(Pair(ex2(g0), ex2(g1)), Pair(1.f, 1.f)).get(d0, d1);
-        return mul2(mul2(g, Pair(rcp(d0), rcp(d1))), u);
-    } else {
-        const float z0 = fminf(fabsf(g0), 64.f), z1 = fminf(fabsf(g1), 64.f);
-        const Pair z(z0, z1);
-        float t0, t1, e0, e1;
-        fma2(z, Pair(0.3275911f * 0.70710678f, 0.3275911f * 0.70710678f), Pair(1.f, 1.f)).get(t0, t1);
-        const Pair t(rcp(t0), rcp(t1));
-        mul2(mul2(g, g), Pair(-0.72134752f, -0.72134752f)).get(e0, e1);
-        Pair q = fma2(t, Pair(0.5f * 1.061405429f, 0.5f * 1.061405429f), Pair(-0.5f * 1.453152027f, -0.5f * 1.453152027f));
-        q = fma2(t, q, Pair(0.5f * 1.421413741f, 0.5f * 1.421413741f));
-        q = fma2(t, q, Pair(-0.5f * 0.284496736f, -0.5f * 0.284496736f));
-        q = fma2(t, q, Pair(0.5f * 0.254829592f, 0.5f * 0.254829592f));
-        q = mul2(mul2(q, t), Pair(ex2(e0), ex2(e1)));
-        return mul2(fma2(Pair(-z0, -z1), q, Pair(fmaxf(g0, 0.f), fmaxf(g1, 0.f))), u);
-    }
-}
 // VARIANT: gated, the activation; else whether outputs go through plain loads and stores (which cost registers)
 template <int KIND, int VARIANT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(const __grid_constant__ Params p)
@@ -402,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_mx(co
                             const Pair gate = fma2(two(&g[q & 1][c + e]), Pair(kg, kg), gb[e / 2]);
                             const Pair up = fma2(two(&u[q & 1][c + e]), Pair(ku, ku), ub[e / 2]);
                             float h0, h1;
-                            hidden2<VARIANT>(gate, up).get(h0, h1);
+                            Act<VARIANT>::hidden2(gate, up).get(h0, h1);
                             most = max_nan(most, h0, h1);
                             v[0][q * CH + c + e] = __float_as_uint(h0);
                             v[0][q * CH + c + e + 1] = __float_as_uint(h1);

@@ -160,6 +160,22 @@ inline bool overlap(const void *a, size_t an, const void *b, size_t bn)
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return x < y + bn && y < x + an;
 }
+struct Span {
+    const void *p;
+    size_t n;
+};
+// Whether an output overlaps an input or another output.
+template <int NI, int NO>
+inline bool any_overlap(const Span (&in)[NI], const Span (&out)[NO])
+{
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            if (overlap(out[o].p, out[o].n, in[i].p, in[i].n)) return true;
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return true;
+    }
+    return false;
+}
 inline bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 inline size_t bytes_of(pmha_dtype dt) { return dt == PMHA_BF16 ? 2 : 4; }
 
