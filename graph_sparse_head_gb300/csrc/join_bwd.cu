@@ -19,8 +19,8 @@ struct JoinBwdArgs {
     float alpha, eps;
 };
 
-// Steps of a block: so many terms of a sum over rows at most are added in
-// float32 one after the other; the blocks' partial rows are added as pairs of floats.
+// Steps of a block: so many rows at most does a team add in float32 one after the other. A block's teams (32 at most) follow in
+// float32, by shuffles and then eight in order; blocks' partial rows are added as pairs of floats.
 constexpr int kSteps = 128;
 
 // Rows of 16-byte pieces come through a ring as in the forward pass; others are loaded when they are needed.

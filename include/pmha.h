@@ -567,8 +567,9 @@ pmha_status pmha_join(const pmha_join_params *params, int64_t rows, const void *
  *  dbranch, dresidual  device (rows, width) in dtype, or NULL.
  *  dpost (width), dgate (gates, width), dpre (width)  device float32, or NULL;
  *          each only with its parameter. Sums over rows run in a fixed order
- *          (deterministic), in float32 over up to 128 terms and as pairs of
- *          floats from there.
+ *          (deterministic): in float32 up to 128 rows one after the other, and
+ *          the up to 32 such sums of a thread block (a short tree, then eight in
+ *          order); from block to block as pairs of floats.
  *  workspace  pmha_join_backward_workspace_size() bytes, 256-byte aligned
  *          (SIZE_MAX when the arguments are invalid); not needed without
  *          dpost, dgate and dpre.
