@@ -131,6 +131,16 @@ __device__ __forceinline__ float block_dot(const __half2 (&w)[16], const uint8_t
     return s;
 }
 
+// y + dot s t for scales s and t: times the smaller one first, which is exact (dot is 0 or 1/4 to 1152, s and t powers of two
+// from 2^-127 on), so that neither far scales that cancel nor two large ones beside a small dot or 0 leave float32 between
+__device__ __forceinline__ float plus_scaled(float y, float dot, float s, float t)
+{
+    float lo, hi;  // NaN where either is
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(s), "f"(t));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(s), "f"(t));
+    return fmaf(dot * lo, hi, y);
+}
+
 template <bool GATED, int ACT, int MB, int LPR, int AHEAD>
 __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
 {
@@ -228,10 +238,9 @@ __global__ void __launch_bounds__(kThreads) k_mx_small(MxSmallArgs a)
             for (int m = 0; m < MB; ++m) {
                 if (m >= a.M) break;
                 const uint8_t *cell = cells + (m * blocks + k) * kCell;
-                // the scales' product first: far scales that cancel leave no room for an infinity between
                 const float sx = *reinterpret_cast<const float *>(cell + 64);
-                y0[m] = fmaf(block_dot(w0, cell), s0 * sx, y0[m]);
-                if constexpr (GATED) y1[m] = fmaf(block_dot(w1, cell), s1 * sx, y1[m]);
+                y0[m] = plus_scaled(y0[m], block_dot(w0, cell), s0, sx);
+                if constexpr (GATED) y1[m] = plus_scaled(y1[m], block_dot(w1, cell), s1, sx);
             }
         }
     }
