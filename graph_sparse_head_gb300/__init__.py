@@ -1312,7 +1312,7 @@ def pmha_ffn_forward_mx(params: FfnMxParams, x: MxTensor, residual: torch.Tensor
 @dataclasses.dataclass
 class LayerCheckpoint:
     """What a layer's backward pass needs of its forward pass, in 8 bits: the layer's input, the attention's output,
-    the block's output where its join needs it, and the mask."""
+    the block's output where its join needs it (a norm or a gate after the block), and a copy of the mask."""
     x: Checkpoint
     attention: Checkpoint
     block: Checkpoint | None
@@ -1440,7 +1440,8 @@ class PackedEncoderLayer:
         else:
             y, _, f8, _ = pmha_join_checkpointed(self.join2, pmha_ffn_forward(self.block, n2), s,
                                                  keep_branch=self._reads_branch(self.join2), keep_residual=False)
-        return y, LayerCheckpoint(x8, a8, f8, key_padding_mask)
+        # a copy, as x's is: the caller's mask may take the next batch's before this one's backward pass
+        return y, LayerCheckpoint(x8, a8, f8, None if key_padding_mask is None else key_padding_mask.clone())
 
     def backward_checkpointed(self, kept: LayerCheckpoint, dy: torch.Tensor) -> dict:
         """backward()'s gradients, of the layer at the kept values of its input and its blocks' outputs."""
